@@ -51,7 +51,7 @@ typedef enum pkv_dtype { PKV_F32 = 0, PKV_F16 = 1, PKV_BF16 = 2 } pkv_dtype;
 #define PKV_DEVERR_SLOT     0x2u  /* a slot at or past num_blocks * block_size */
 #define PKV_DEVERR_CONTEXT  0x4u  /* context_len < 0, > max_blocks_per_seq * B or > max_context_len */
 #define PKV_DEVERR_TIMEOUT  0x8u  /* a copy pipeline wait ran out of time (about 2 s) */
-#define PKV_DEVERR_POSITION 0x10u /* slot mapping: position past the table row, or bad sequence index */
+#define PKV_DEVERR_POSITION 0x10u /* position past the table row or the rotation table, bad sequence index or query start */
 #define PKV_DEVERR_PAIR     0x20u /* copy_blocks: a src or dst outside [0, num_blocks) */
 #define PKV_DEVERR_PREFIX   0x40u /* cascade decode: a sequence's prefix blocks differ from sequence 0's */
 
@@ -426,6 +426,117 @@ pkv_status pkv_free_sequences(const pkv_block_allocator* alloc, int32_t block_si
                               int32_t* block_tables, int32_t max_blocks_per_seq,
                               const int32_t* seqs, const int32_t* lens, int32_t num_seqs,
                               void* stream);
+
+/*
+ * One ragged step from the request lengths alone: request s holds past_lens[s]
+ * cached tokens and brings new_lens[s] (any number, one for a decoding request,
+ * none for one that waits); the step's tokens are packed request by request.  In
+ * one launch: the blocks the new tokens need go from the free stack into the
+ * tables, and every token gets its request, position and slot ("What Is vLLM",
+ * section "How does PagedAttention work?": blocks are allocated on demand;
+ * "Serving models with vLLM", section "How it works: continuous batching").
+ *   past_lens, new_lens  int32 [num_seqs]
+ *   max_tokens      rows of the token arrays; the entries past the step's last
+ *                   token are set to -1 (room for a captured step)
+ *   free_count_out  where the free count left over goes; NULL: alloc->free_count
+ *                   itself.  Another word leaves the count as it was, so a caller
+ *                   can drop the step and build another over it.
+ *   query_start     int32 [num_seqs + 1], output: first token of each request, and the end
+ *   context_lens    int32 [num_seqs], output: past + new; 0 for a request not served
+ *   positions, token_seq  int32 [max_tokens], slot_mapping int64 [max_tokens], outputs:
+ *                   position, request and slot of each token; position and slot are -1
+ *                   for the tokens of a request that is not served
+ *   seq_status      int32 [num_seqs], output: 0 served; 1 out of free blocks; 2 lengths
+ *                   invalid, past the table row or past max_tokens; 3 the partly filled
+ *                   last block has other references (copy it first: pkv_copy_blocks, or
+ *                   let pkv_allocate_for_append grow that request).  Nothing is allocated
+ *                   for a request that is not served.
+ * Free blocks go to the requests in order: request s is served when the blocks
+ * needed by requests 0 .. s together are free (or it needs none), and fresh blocks
+ * are taken from the top of the stack in request and position order, so the same
+ * state gives the same ids.  Each fresh block has one reference.  Table rows of
+ * different requests must be distinct memory.  Device errors: the tokens exceed
+ * max_tokens (PKV_DEVERR_POSITION); a block id outside [0, num_blocks) in the table
+ * entry that receives tokens or on the free stack (PKV_DEVERR_BLOCK_ID).
+ */
+pkv_status pkv_build_batch(const pkv_block_allocator* alloc, int32_t block_size,
+                           int32_t* block_tables, int32_t max_blocks_per_seq,
+                           const int32_t* past_lens, const int32_t* new_lens, int32_t num_seqs,
+                           int32_t max_tokens, int32_t* free_count_out, int32_t* query_start,
+                           int32_t* context_lens, int32_t* positions, int32_t* token_seq,
+                           int64_t* slot_mapping, int32_t* seq_status, void* stream);
+
+/*
+ * Queries and keys of new tokens, as the projections leave them, made ready in
+ * one pass: the norm of each head, the rotation by position, and the keys and
+ * values into their cache slots ("vLLM in Production", section "PagedAttention -
+ * Virtual Memory for the KV Cache").  For each head row x of q and k, in 32 bits:
+ *   y = x / sqrt(mean(x^2) + eps) * weight          (no weight: y = x)
+ *   (a, b) becomes (a cos - b sin, b cos + a sin)   for each pair of the first
+ *                                                   rotary_dim elements
+ * then one rounding to the pool's type; q goes to q_out, k to its slot of the K
+ * pool, v as it is to its slot of the V pool.
+ *   q [T][num_q_heads][D], k, v [T][num_kv_heads][D] in the pool's type; token t's
+ *                 heads start q_stride (k_stride, v_stride) elements after token
+ *                 t - 1's and are packed, so all three may be views of one packed
+ *                 projection output.  Strides are multiples of 16 bytes.
+ *   q_weight, k_weight  [D] in the pool's type, either or both NULL for no norm
+ *   cos_sin       float [max_position][rotary_dim]: a position's rotary_dim / 2
+ *                 cosines, then its sines; NULL with rotary_dim 0 for no rotation
+ *   rotary_dim    a multiple of 16, at most D; the elements past it are not rotated
+ *   interleaved   0: element i pairs with i + rotary_dim / 2; otherwise 2 i with 2 i + 1
+ *   positions     int32 [T]; negative: the row holds no token and nothing is written
+ *   slot_mapping  int64 [T]; negative: k and v of that token are not written
+ *   q_out         [T][num_q_heads][D]; may be q itself when q_stride = num_q_heads * D,
+ *                 but must not overlap the inputs in another way
+ * All pointers but positions and slot_mapping 16-byte aligned.  Slots within one call
+ * must be distinct.  A position at or past max_position skips its token and sets
+ * PKV_DEVERR_POSITION; a slot past the pool skips its k and v and sets PKV_DEVERR_SLOT.
+ */
+pkv_status pkv_qk_norm_rope_write(const pkv_pool* pool, const void* q, int64_t q_stride,
+                                  const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                                  int32_t num_tokens, int32_t num_q_heads, const void* q_weight,
+                                  const void* k_weight, float eps, const float* cos_sin,
+                                  int32_t max_position, int32_t rotary_dim, int32_t interleaved,
+                                  const int32_t* positions, const int64_t* slot_mapping,
+                                  void* q_out, void* stream);
+
+/*
+ * Causal attention of a ragged batch of new tokens over the paged cache, each
+ * request with its own number of queries: whole prompts, parts of prompts and
+ * decoding requests together ("Serving models with vLLM", section "How it works:
+ * continuous batching": chunked prefill).  Request s has the n_s = query_start[s+1]
+ * - query_start[s] query rows from query_start[s] on, for its last n_s positions,
+ * whose K and V are already in the cache; its query j gives
+ *   out[t][h] = softmax(scale * q[t][h] . K_s[0..c_j)^T) V_s[0..c_j),
+ *   c_j = context_lens[s] - n_s + 1 + j     (a row with c_j <= 0 is zero).
+ *   q             [num_tokens][num_q_heads][head_dim], pool type, 16-byte aligned
+ *   query_start   int32 [num_seqs + 1], ascending within [0, num_tokens]
+ *   context_lens  int32 [num_seqs], each counting the request's new tokens
+ *   max_context_len  host-side upper bound of context_lens
+ *   out           [num_tokens][num_q_heads][head_dim] of out_dtype (PKV_F32 or the pool
+ *                 type), 16-byte aligned; rows outside every request are left as they were
+ *   workspace     pkv_chunk_workspace_bytes(...) bytes, always required; its contents need
+ *                 no clearing.  Calls that may run at the same time need one each.
+ * Cached rows at and past a request's context may hold anything; those below it must be
+ * finite.  Any group size num_q_heads / num_kv_heads up to 128.  The probabilities enter
+ * the product with V rounded to the pool's type when the output has that type, and with
+ * about twice its precision when the output is fp32.  fp16 / bf16 pools of fewer than 2^31
+ * (block, kv head, position) rows (else PKV_ERR_UNSUPPORTED).  Device errors: query_start
+ * not ascending within [0, num_tokens] (PKV_DEVERR_POSITION, nothing is computed); a
+ * context_lens entry negative or past the table row or max_context_len
+ * (PKV_DEVERR_CONTEXT, cut to that range); a table entry outside the pool
+ * (PKV_DEVERR_BLOCK_ID, its positions count as zeros).
+ */
+size_t pkv_chunk_workspace_bytes(const pkv_pool* pool, int32_t num_tokens, int32_t num_seqs,
+                                 int32_t num_q_heads, int32_t max_context_len);
+pkv_status pkv_paged_attention_chunk(const pkv_pool* pool, const void* q, int32_t num_tokens,
+                                     int32_t num_q_heads, const int32_t* query_start,
+                                     int32_t num_seqs, const int32_t* block_tables,
+                                     int32_t max_blocks_per_seq, const int32_t* context_lens,
+                                     int32_t max_context_len, float scale, void* out,
+                                     int32_t out_dtype, void* workspace, size_t workspace_bytes,
+                                     void* stream);
 
 /*
  * Synchronises stream, then reads and clears the current device's error word

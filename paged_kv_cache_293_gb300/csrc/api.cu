@@ -829,6 +829,229 @@ pkv_status pkv_free_sequences(const pkv_block_allocator* alloc, int32_t block_si
                : PKV_ERR_CUDA;
 }
 
+pkv_status pkv_build_batch(const pkv_block_allocator* alloc, int32_t block_size,
+                           int32_t* block_tables, int32_t max_blocks_per_seq,
+                           const int32_t* past_lens, const int32_t* new_lens, int32_t num_seqs,
+                           int32_t max_tokens, int32_t* free_count_out, int32_t* query_start,
+                           int32_t* context_lens, int32_t* positions, int32_t* token_seq,
+                           int64_t* slot_mapping, int32_t* seq_status, void* stream) {
+    if (!allocator_ok(alloc) || block_size <= 0 || max_blocks_per_seq <= 0 || num_seqs < 0 ||
+        max_tokens < 0)
+        return PKV_ERR_INVALID;
+    if (!query_start) return PKV_ERR_INVALID;
+    if (num_seqs > 0 && (!block_tables || !past_lens || !new_lens || !context_lens || !seq_status))
+        return PKV_ERR_INVALID;
+    if (max_tokens > 0 && (!positions || !token_seq || !slot_mapping)) return PKV_ERR_INVALID;
+    pkv::BatchParams p{};
+    pkv_status st = error_word(&p.err);
+    if (st != PKV_OK) return st;
+    p.alloc = allocator_state(alloc);
+    p.block_size = block_size;
+    p.block_tables = block_tables;
+    p.max_blocks_per_seq = max_blocks_per_seq;
+    p.past_lens = past_lens;
+    p.new_lens = new_lens;
+    p.num_seqs = num_seqs;
+    p.max_tokens = max_tokens;
+    p.free_count_out = free_count_out ? free_count_out : alloc->free_count;
+    p.query_start = query_start;
+    p.context_lens = context_lens;
+    p.positions = positions;
+    p.token_seq = token_seq;
+    p.slot_mapping = slot_mapping;
+    p.seq_status = seq_status;
+    return pkv::launch_build_batch(p, static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? PKV_OK
+               : PKV_ERR_CUDA;
+}
+
+pkv_status pkv_qk_norm_rope_write(const pkv_pool* pool, const void* q, int64_t q_stride,
+                                  const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                                  int32_t num_tokens, int32_t num_q_heads, const void* q_weight,
+                                  const void* k_weight, float eps, const float* cos_sin,
+                                  int32_t max_position, int32_t rotary_dim, int32_t interleaved,
+                                  const int32_t* positions, const int64_t* slot_mapping,
+                                  void* q_out, void* stream) {
+    pkv_status st = check_pool(pool);
+    if (st != PKV_OK) return st;
+    if (num_tokens < 0 || num_q_heads <= 0 || rotary_dim < 0 || rotary_dim > pool->head_dim)
+        return PKV_ERR_INVALID;
+    if (!std::isfinite(eps) || eps < 0.f) return PKV_ERR_INVALID;
+    if ((rotary_dim > 0) != (cos_sin != nullptr) || (rotary_dim > 0 && max_position <= 0))
+        return PKV_ERR_INVALID;
+    if (rotary_dim % 16 != 0) return PKV_ERR_UNSUPPORTED;
+    if (num_q_heads > INT32_MAX - 2 * (int64_t)pool->num_kv_heads) return PKV_ERR_UNSUPPORTED;
+    if (num_tokens == 0) return PKV_OK;
+    if (!q || !k || !v || !q_out || !positions || !slot_mapping) return PKV_ERR_INVALID;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out) ||
+        !aligned16(q_weight) || !aligned16(k_weight) || !aligned16(cos_sin))
+        return PKV_ERR_INVALID;
+    // a row of heads is packed; rows may be further apart, by whole 16-byte vectors
+    const int64_t vec = pool->dtype == PKV_F32 ? 4 : 8, D = pool->head_dim;
+    const int64_t need_q = num_q_heads * D, need_kv = pool->num_kv_heads * D;
+    if (q_stride % vec != 0 || k_stride % vec != 0 || v_stride % vec != 0) return PKV_ERR_INVALID;
+    if (num_tokens > 1 && (q_stride < need_q || k_stride < need_kv || v_stride < need_kv))
+        return PKV_ERR_INVALID;
+    pkv::RopeParams p{};
+    st = error_word(&p.err);
+    if (st != PKV_OK) return st;
+    p.q = q;
+    p.k = k;
+    p.v = v;
+    p.q_stride = q_stride;
+    p.k_stride = k_stride;
+    p.v_stride = v_stride;
+    p.num_tokens = num_tokens;
+    p.num_q_heads = num_q_heads;
+    p.q_weight = q_weight;
+    p.k_weight = k_weight;
+    p.eps = eps;
+    p.cos_sin = cos_sin;
+    p.max_position = max_position;
+    p.rotary_dim = rotary_dim;
+    p.interleaved = interleaved != 0;
+    p.positions = positions;
+    p.slot_mapping = slot_mapping;
+    p.q_out = q_out;
+    p.k_pool = pool->k;
+    p.v_pool = pool->v;
+    p.num_blocks = pool->num_blocks;
+    p.block_size = pool->block_size;
+    p.num_kv_heads = pool->num_kv_heads;
+    p.head_dim = pool->head_dim;
+    return pkv::launch_rope_write(p, pool->dtype, static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? PKV_OK
+               : PKV_ERR_CUDA;
+}
+
+namespace {
+
+// Sizes of a chunk attention call and where its workspace's parts lie.
+struct ChunkShape {
+    int64_t tiles, pieces, cut_pieces, partial_rows;
+    size_t tile_start, tile, piece, merge, m, l, o, bytes;
+};
+
+ChunkShape chunk_shape(const pkv_pool* pool, int32_t T, int32_t S, int32_t Hq, int32_t max_ctx) {
+    const int64_t Hkv = pool->num_kv_heads, G = Hq / Hkv, sms = sm_count();
+    const int64_t QT = 2 * (128 / G);  // queries per tile
+    ChunkShape c{};
+    c.tiles = std::min<int64_t>(T, T / QT + S);
+    const bool cuts = (max_ctx + (int64_t)pkv::CHUNK_TILE - 1) / pkv::CHUNK_TILE >= pkv::CHUNK_SPLIT_MIN;
+    c.cut_pieces = cuts ? std::min<int64_t>(8 * sms, c.tiles * Hkv * 32) : 0;
+    c.partial_rows = cuts ? std::min<int64_t>(3 * sms * 256, (int64_t)T * Hq * 32) : 0;
+    c.pieces = c.tiles * Hkv + c.cut_pieces;
+    size_t at = 128;  // header
+    auto take = [&at](size_t bytes) {
+        const size_t here = at;
+        at = (at + bytes + 127) & ~size_t(127);
+        return here;
+    };
+    c.tile_start = take(((size_t)S + 1) * 4);
+    c.tile = take((size_t)c.tiles * sizeof(int4));
+    c.piece = take((size_t)c.pieces * sizeof(pkv::ChunkPiece));
+    c.merge = take((size_t)(c.cut_pieces / 2) * sizeof(pkv::ChunkMerge));
+    c.m = take((size_t)c.partial_rows * 4);
+    c.l = take((size_t)c.partial_rows * 4);
+    c.o = take((size_t)c.partial_rows * pool->head_dim * 4);
+    c.bytes = at;
+    return c;
+}
+
+}  // namespace
+
+size_t pkv_chunk_workspace_bytes(const pkv_pool* pool, int32_t num_tokens, int32_t num_seqs,
+                                 int32_t num_q_heads, int32_t max_context_len) {
+    if (!pool || pool->num_kv_heads <= 0 || pool->head_dim <= 0 || num_tokens < 0 || num_seqs < 0 ||
+        num_q_heads <= 0 || max_context_len < 0 || num_q_heads % pool->num_kv_heads != 0 ||
+        num_q_heads / pool->num_kv_heads > 128)
+        return 0;
+    return chunk_shape(pool, num_tokens, num_seqs, num_q_heads, max_context_len).bytes;
+}
+
+pkv_status pkv_paged_attention_chunk(const pkv_pool* pool, const void* q, int32_t num_tokens,
+                                     int32_t num_q_heads, const int32_t* query_start,
+                                     int32_t num_seqs, const int32_t* block_tables,
+                                     int32_t max_blocks_per_seq, const int32_t* context_lens,
+                                     int32_t max_context_len, float scale, void* out,
+                                     int32_t out_dtype, void* workspace, size_t workspace_bytes,
+                                     void* stream) {
+    pkv_status st = check_pool(pool);
+    if (st != PKV_OK) return st;
+    if (num_tokens < 0 || num_seqs < 0 || num_q_heads <= 0 || max_blocks_per_seq <= 0 ||
+        max_context_len < 0 || num_q_heads % pool->num_kv_heads != 0 || !std::isfinite(scale))
+        return PKV_ERR_INVALID;
+    if (out_dtype != PKV_F32 && out_dtype != pool->dtype) return PKV_ERR_UNSUPPORTED;
+    const int32_t G = num_q_heads / pool->num_kv_heads;
+    if (pool->dtype == PKV_F32 || G > 128) return PKV_ERR_UNSUPPORTED;
+    if ((int64_t)pool->num_blocks * pool->num_kv_heads * pool->block_size >= (1ll << 31))
+        return PKV_ERR_UNSUPPORTED;  // tensor-copy rows are int32
+    const ChunkShape c = chunk_shape(pool, num_tokens, num_seqs, num_q_heads, max_context_len);
+    if (c.pieces > INT32_MAX) return PKV_ERR_UNSUPPORTED;
+    if (num_tokens == 0 || num_seqs == 0) return PKV_OK;
+    if (!q || !query_start || !block_tables || !context_lens || !out || !aligned16(q) || !aligned16(out))
+        return PKV_ERR_INVALID;
+    if (!workspace || !aligned16(workspace) || workspace_bytes < c.bytes) return PKV_ERR_WORKSPACE;
+    unsigned int* err = nullptr;
+    st = error_word(&err);
+    if (st != PKV_OK) return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    char* ws = static_cast<char*>(workspace);
+    const int32_t sms = sm_count();
+
+    pkv::ChunkTensors x{q, pool->k, pool->v, num_tokens, (int32_t)std::min<int64_t>(c.pieces, sms)};
+    pkv::ChunkPlanParams pl{};
+    pl.query_start = query_start;
+    pl.context_lens = context_lens;
+    pl.num_seqs = num_seqs;
+    pl.num_tokens = num_tokens;
+    pl.max_blocks_per_seq = max_blocks_per_seq;
+    pl.block_size = pool->block_size;
+    pl.max_context_len = max_context_len;
+    pl.num_kv_heads = pool->num_kv_heads;
+    pl.group = G;
+    pl.num_sms = sms;
+    pl.ctas = x.ctas;
+    pl.max_partial_rows = c.partial_rows;
+    pl.max_cut_pieces = c.cut_pieces;
+    pl.header = reinterpret_cast<int32_t*>(ws);
+    pl.tile_start = reinterpret_cast<int32_t*>(ws + c.tile_start);
+    pl.tiles = reinterpret_cast<int4*>(ws + c.tile);
+    pl.pieces = reinterpret_cast<pkv::ChunkPiece*>(ws + c.piece);
+    pl.merges = reinterpret_cast<pkv::ChunkMerge*>(ws + c.merge);
+    pl.err = err;
+
+    pkv::ChunkParams p{};
+    p.num_q_heads = num_q_heads;
+    p.num_kv_heads = pool->num_kv_heads;
+    p.group = G;
+    p.head_dim = pool->head_dim;
+    p.num_blocks = pool->num_blocks;
+    p.block_size = pool->block_size;
+    p.block_tables = block_tables;
+    p.max_blocks_per_seq = max_blocks_per_seq;
+    // the kernel takes maxima before scaling, which a positive scale allows
+    p.scale_log2 = (scale == 0.f ? 1.f : std::fabs(scale)) * 1.4426950408889634f;
+    p.pre_scale = scale > 0.f ? 1.f : scale < 0.f ? -1.f : 0.f;
+    p.out = out;
+    p.out_dtype = out_dtype;
+    p.header = pl.header;
+    p.pieces = pl.pieces;
+    p.merges = pl.merges;
+    p.part_m = reinterpret_cast<float*>(ws + c.m);
+    p.part_l = reinterpret_cast<float*>(ws + c.l);
+    p.part_o = reinterpret_cast<float*>(ws + c.o);
+    p.err = err;
+    if (pkv::launch_chunk_plan(pl, s) != cudaSuccess) return PKV_ERR_CUDA;
+    const cudaError_t e = pool->dtype == PKV_F16 ? pkv::launch_chunk<__half>(p, x, s)
+                                                 : pkv::launch_chunk<__nv_bfloat16>(p, x, s);
+    if (e == cudaErrorNotSupported) return PKV_ERR_UNSUPPORTED;
+    if (e != cudaSuccess) return PKV_ERR_CUDA;
+    if (c.partial_rows == 0) return PKV_OK;
+    const int64_t merge_ctas = std::min<int64_t>(4 * (int64_t)sms, ((int64_t)num_tokens * num_q_heads + 7) / 8);
+    return pkv::launch_chunk_merge(p, (int)merge_ctas, s) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
 pkv_status pkv_get_device_error(uint32_t* flags, void* stream) {
     if (!flags) return PKV_ERR_INVALID;
     unsigned int* err = nullptr;

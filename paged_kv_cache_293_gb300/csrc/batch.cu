@@ -1,0 +1,260 @@
+// batch.cu -- one ragged step's block tables, starts, positions and slots from the request
+// lengths alone ("What Is vLLM", section "How does PagedAttention work?": blocks are
+// allocated on demand; section "What is continuous batching in vLLM?": every step carries
+// requests at different stages, so their lengths differ).
+//
+// With past_s cached and new_s arriving tokens of request s and B tokens per block,
+//   need_s = ceil((past_s + new_s) / B) - ceil(past_s / B),  upto_s = need_0 + ... + need_s,
+// a request is served when need_s = 0 or upto_s <= free: the free blocks go to the requests
+// in order, and a request's j-th fresh block is the (upto_s - need_s + j)-th from the top of
+// the free stack -- the ids a host loop popping them one by one would give, whatever order
+// the GPU works in (the growth kernel in allocator.cu pops with atomics instead).
+//
+// The traffic is a few bytes per token and block (4.4 MB = 0.65 us at the measured copy rate
+// for 4096 requests with 260,000 tokens), so launches and memory round trips bound it.  It is
+// one launch of one thread-block cluster: the scan over the requests is split over the
+// cluster's CTAs, which exchange their totals through distributed shared memory, and a
+// cluster barrier stands where a second launch would.
+#include <cooperative_groups.h>
+
+#include "pkv_common.cuh"
+
+namespace cg = cooperative_groups;
+
+namespace pkv {
+
+namespace {
+
+constexpr int BATCH_CTAS = 8;        // portable cluster size
+constexpr int BATCH_THREADS = 1024;
+constexpr int BATCH_WARPS = BATCH_THREADS / 32;
+
+struct SeqNeed {
+    int past, tokens, need, status;
+};
+
+// Lengths, blocks needed and the status that does not depend on the other requests.
+__device__ __forceinline__ SeqNeed seq_need(const BatchParams& p, int s, bool report) {
+    SeqNeed r;
+    r.past = p.past_lens[s];
+    const int nw = p.new_lens[s];
+    r.tokens = nw > 0 ? nw : 0;
+    r.need = 0;
+    r.status = 0;
+    if (r.past < 0 || nw < 0 || (long long)r.past + nw > (long long)p.max_blocks_per_seq * p.block_size) {
+        r.status = 2;
+        return r;
+    }
+    if (nw == 0) return r;
+    const int held = (r.past + p.block_size - 1) / p.block_size;
+    if (r.past % p.block_size != 0) {  // the last block held receives tokens: it must be this row's alone
+        const int b = p.block_tables[(size_t)s * p.max_blocks_per_seq + held - 1];
+        if ((unsigned)b >= (unsigned)p.alloc.num_blocks) {
+            if (report) set_error(p.err, PKV_DEVERR_BLOCK_ID);
+            r.status = 2;
+            return r;
+        }
+        if (p.alloc.refcount[b] != 1) {
+            r.status = 3;
+            return r;
+        }
+    }
+    r.need = (int)(((long long)r.past + nw + p.block_size - 1) / p.block_size) - held;
+    return r;
+}
+
+struct Pair {
+    long long tokens, need;
+};
+
+__device__ __forceinline__ Pair warp_inclusive(Pair v, int lane) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long a = __shfl_up_sync(FULL_MASK, v.tokens, o);
+        const long long b = __shfl_up_sync(FULL_MASK, v.need, o);
+        if (lane >= o) {
+            v.tokens += a;
+            v.need += b;
+        }
+    }
+    return v;
+}
+
+// Inclusive sums over the CTA's threads; `total` gets the CTA's sums.
+__device__ __forceinline__ Pair block_inclusive(Pair v, Pair* warp_sums, Pair* total) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    v = warp_inclusive(v, lane);
+    if (lane == 31) warp_sums[warp] = v;
+    __syncthreads();
+    if (warp == 0) warp_sums[lane] = warp_inclusive(warp_sums[lane], lane);
+    __syncthreads();
+    if (warp > 0) {
+        v.tokens += warp_sums[warp - 1].tokens;
+        v.need += warp_sums[warp - 1].need;
+    }
+    *total = warp_sums[BATCH_WARPS - 1];
+    __syncthreads();  // warp_sums is free again
+    return v;
+}
+
+}  // namespace
+
+__global__ void __cluster_dims__(BATCH_CTAS, 1, 1) __launch_bounds__(BATCH_THREADS)
+build_batch_kernel(const BatchParams p) {
+    static_assert(BATCH_WARPS == 32, "one lane per warp total");
+    __shared__ Pair warp_sums[BATCH_WARPS];
+    __shared__ Pair cta_total;         // read by the other CTAs of the cluster
+    __shared__ long long cta_popped;   // blocks popped up to this CTA's last served request
+    __shared__ long long upto_s[BATCH_THREADS];  // inclusive block counts of the tile's requests
+    __shared__ int first_s[BATCH_THREADS];       // first fresh logical block, -1: not served
+    cg::cluster_group cluster = cg::this_cluster();
+    const int rank = (int)cluster.block_rank(), tid = threadIdx.x;
+    const int S = p.num_seqs, M = p.max_blocks_per_seq, B = p.block_size;
+    const int per = (S + BATCH_CTAS - 1) / BATCH_CTAS;
+    const int s_lo = min(S, rank * per), s_hi = min(S, s_lo + per);
+    long long free_blocks = *p.alloc.free_count;
+    free_blocks = free_blocks < 0 ? 0 : min(free_blocks, (long long)p.alloc.num_blocks);
+
+    if (rank == 0 && tid == 0) p.query_start[0] = 0;
+
+    // ---- this CTA's totals, then the sums of the CTAs before it
+    Pair mine{0, 0}, total;
+    SeqNeed held_need{0, 0, 0, 0};
+    for (int s = s_lo + tid; s < s_hi; s += BATCH_THREADS) {
+        held_need = seq_need(p, s, true);
+        mine.tokens += held_need.tokens;
+        mine.need += held_need.need;
+    }
+    block_inclusive(mine, warp_sums, &total);
+    if (tid == 0) {
+        cta_total = total;
+        cta_popped = 0;
+    }
+    cluster.sync();  // also: every CTA has read the free count before it may be rewritten
+    Pair base{0, 0};
+    long long all_tokens = 0;
+#pragma unroll
+    for (int r = 0; r < BATCH_CTAS; ++r) {
+        const Pair* other = cluster.map_shared_rank(&cta_total, r);
+        const Pair v = *other;
+        all_tokens += v.tokens;
+        if (r < rank) {
+            base.tokens += v.tokens;
+            base.need += v.need;
+        }
+    }
+
+    // ---- requests in tiles of one per thread: starts, contexts, statuses, table entries
+    for (int s0 = s_lo; s0 < s_hi; s0 += BATCH_THREADS) {
+        const int s = s0 + tid;
+        const bool live = s < s_hi;
+        // one tile per CTA in all but the largest batches: the first pass's values serve
+        SeqNeed n{0, 0, 0, 0};
+        if (live) n = (s_hi - s_lo <= BATCH_THREADS) ? held_need : seq_need(p, s, false);
+        Pair tile;
+        Pair v = block_inclusive(Pair{n.tokens, n.need}, warp_sums, &tile);
+        v.tokens += base.tokens;
+        v.need += base.need;
+        if (live) {
+            if (v.tokens > p.max_tokens && n.tokens > 0) n.status = 2;  // its rows are not in the batch
+            if (n.status == 0 && n.need > 0 && v.need > free_blocks) n.status = 1;
+            p.query_start[s + 1] = (int)min(v.tokens, (long long)p.max_tokens);
+            p.context_lens[s] = n.status == 0 ? n.past + n.tokens : 0;
+            p.seq_status[s] = n.status;
+            if (n.status == 0 && n.need > 0) atomicMax(&cta_popped, v.need);
+        }
+        upto_s[tid] = v.need;
+        first_s[tid] = live && n.status == 0 ? (n.past + B - 1) / B : -1;
+        __syncthreads();
+        // the tile's fresh blocks, one per thread and step: the request is found by its count
+        for (long long k = tid; k < tile.need; k += BATCH_THREADS) {
+            const long long at = base.need + k;
+            if (at >= free_blocks) break;  // past the stack: its request is not served
+            int lo = 0, hi = min(BATCH_THREADS, s_hi - s0) - 1;
+            while (lo < hi) {
+                const int mid = (lo + hi) >> 1;
+                if (upto_s[mid] > at) hi = mid; else lo = mid + 1;
+            }
+            if (first_s[lo] < 0) continue;
+            const long long before = lo > 0 ? upto_s[lo - 1] : base.need;
+            const int id = p.alloc.free_ids[free_blocks - 1 - at];
+            int32_t* entry = p.block_tables + (size_t)(s0 + lo) * M + first_s[lo] + (at - before);
+            if ((unsigned)id >= (unsigned)p.alloc.num_blocks) {
+                set_error(p.err, PKV_DEVERR_BLOCK_ID);  // not a free stack: no block is taken
+                *entry = -1;
+            } else {
+                *entry = id;
+                p.alloc.refcount[id] = 1;
+            }
+        }
+        base.tokens += tile.tokens;
+        base.need += tile.need;
+        __syncthreads();
+    }
+    if (all_tokens > p.max_tokens && rank == 0 && tid == 0) set_error(p.err, PKV_DEVERR_POSITION);
+    cluster.sync();  // starts, contexts and tables of every CTA are visible
+
+    if (rank == 0 && tid == 0) {
+        long long popped = 0;
+        for (int r = 0; r < BATCH_CTAS; ++r) popped = max(popped, *cluster.map_shared_rank(&cta_popped, r));
+        *p.free_count_out = (int)(free_blocks - popped);
+    }
+
+    // ---- tokens, four in a row per thread: one search, wide stores
+    const int real = (int)min(all_tokens, (long long)p.max_tokens);
+    const bool wide = ((reinterpret_cast<uintptr_t>(p.positions) | reinterpret_cast<uintptr_t>(p.token_seq) |
+                        reinterpret_cast<uintptr_t>(p.slot_mapping)) & 15u) == 0;
+    for (long long t0 = ((long long)rank * BATCH_THREADS + tid) * 4; t0 < p.max_tokens;
+         t0 += (long long)BATCH_CTAS * BATCH_THREADS * 4) {
+        int s = -1, end = 0, next_pos = 0, ctx = 0;
+        int pos[4], seq[4];
+        long long slot[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const long long t = t0 + i;
+            pos[i] = seq[i] = -1;
+            slot[i] = -1;
+            if (t >= real) continue;
+            if (s < 0 || t >= end) {
+                int lo = s < 0 ? 0 : s + 1, hi = S - 1;  // first request ending past t
+                if (s >= 0 && p.query_start[lo + 1] > t) hi = lo;
+                while (lo < hi) {
+                    const int mid = lo + ((hi - lo) >> 1);
+                    if (p.query_start[mid + 1] > t) hi = mid; else lo = mid + 1;
+                }
+                s = lo;
+                end = p.query_start[s + 1];
+                ctx = p.context_lens[s];
+                next_pos = ctx - (end - (int)t);
+            }
+            seq[i] = s;
+            if (ctx > 0) {
+                pos[i] = next_pos;
+                const int id = p.block_tables[(size_t)s * M + next_pos / B];
+                if (id >= 0) slot[i] = (long long)id * B + next_pos % B;
+            }
+            ++next_pos;
+        }
+        if (wide && t0 + 4 <= p.max_tokens) {
+            *reinterpret_cast<int4*>(p.positions + t0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+            *reinterpret_cast<int4*>(p.token_seq + t0) = make_int4(seq[0], seq[1], seq[2], seq[3]);
+            longlong2* out = reinterpret_cast<longlong2*>(p.slot_mapping + t0);
+            out[0] = make_longlong2(slot[0], slot[1]);
+            out[1] = make_longlong2(slot[2], slot[3]);
+        } else {
+            for (int i = 0; i < 4 && t0 + i < p.max_tokens; ++i) {
+                p.positions[t0 + i] = pos[i];
+                p.token_seq[t0 + i] = seq[i];
+                p.slot_mapping[t0 + i] = slot[i];
+            }
+        }
+    }
+    cluster.sync();  // no CTA ends while CTA 0 may still read its shared memory
+}
+
+cudaError_t launch_build_batch(const BatchParams& p, cudaStream_t stream) {
+    build_batch_kernel<<<BATCH_CTAS, BATCH_THREADS, 0, stream>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace pkv

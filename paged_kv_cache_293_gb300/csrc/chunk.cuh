@@ -1,0 +1,523 @@
+// chunk.cuh -- causal attention of ragged chunks of new tokens over the paged cache, on the
+// fifth-generation tensor cores ("Serving models with vLLM", section "How it works:
+// continuous batching": chunked prefill; each request brings its own number of new tokens).
+//
+// For query j of request s (n_s queries, context c_s counting them), head h:
+//   out = softmax(scale q . K_s[0..lim)^T) V_s[0..lim),   lim = c_s - n_s + 1 + j,
+// zero when lim <= 0.  The G heads of a kv head share its K and V, so the rows of one kv
+// head are (query, head) pairs and a CTA takes two tiles of 128 of them (row r of a tile is
+// query r / G, head r % G) against the pages in steps of 128 tokens: every staged K and V
+// tile serves 256 rows.  One pass, running maximum and sum per row (one thread per row).
+//
+// A small kernel first lists the pieces of work (chunk_plan.cu): tile pair x kv head, cut
+// along the context where there would be too few of them; the CTAs of this kernel, one per
+// SM, take pieces from that list in order until it is empty.  Twelve warps, fixed roles:
+//   0-3, 4-7  softmax of tile 0 and of tile 1, and their output
+//   8         takes the next piece; tensor copies of K and V pages into a ring of stages
+//   9         one lane issues the MMAs, for both tiles in turn:
+//               S_t = Q_t . K_j^T            128 x 128 in tensor memory
+//               O_t += P_t . V_j             P_t written over S_t by the softmax
+//             so that one tile's softmax runs while the tensor cores work for the other
+//             Before a piece's last P.V the warp zeroes the V rows of the last 16-token copy
+//             past the last position the piece may see (they may hold anything; their
+//             weights are zero, and 0 * NaN is not)
+//   10        tensor copies of the query tiles
+//   11        none (fills the warpgroup)
+// The reference maximum of a row is raised only when a step's maximum exceeds it by more
+// than 8 in base 2, so O is rescaled rarely; every term of a row uses the same reference.
+// P enters its product rounded to the pool's type (relative error 2^-9 bf16, 2^-12 fp16 per
+// term at most half a step, like the output's own rounding); with a 32-bit output it enters
+// as a rounded part and the rounded remainder, in two products.
+// Every wait is bounded; a CTA that gives up sets PKV_DEVERR_TIMEOUT and returns its tensor
+// memory.
+#pragma once
+
+#include <type_traits>
+
+#include "decode_mma.cuh"
+#include "umma.cuh"
+
+namespace pkv {
+
+constexpr int CHUNK_THREADS = 384;
+constexpr float CHUNK_RESCALE_LOG2 = 8.f;
+
+template <int D>
+struct ChunkSmem {
+    static constexpr int BOXES = D / 64;                  // 128-byte columns of a row
+    static constexpr int BOX = 128 * 128;                 // one of a 128-row tile
+    static constexpr int TILE = BOXES * BOX;              // a tile of Q, K or V
+    static constexpr int STAGES = D == 128 ? 5 : 8;
+    static constexpr int Q_OFF = 0;
+    static constexpr int KV_OFF = 2 * TILE;
+    static constexpr int BAR_OFF = KV_OFF + STAGES * TILE;
+    static constexpr int NBARS = 2 * STAGES + 15;
+    static constexpr int PIECE_OFF = BAR_OFF + ((NBARS * 8 + 15) / 16) * 16;
+    static constexpr int TMEM_SLOT_OFF = PIECE_OFF + 2 * 32;
+    static constexpr int BYTES = TMEM_SLOT_OFF + 16 + 1024;  // + alignment slack
+    // tensor memory columns: S_0, S_1 (P over them), O_0, O_1
+    static constexpr uint32_t TMEM_COLS = 512;
+    static constexpr uint32_t O_COL = 256;
+    static_assert(D == 64 || D == 128, "head_dim");
+    static_assert(BYTES <= 227 * 1024, "shared memory");
+};
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int y,
+                                            int z, int w, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+        : "memory");
+}
+
+__device__ __forceinline__ uint64_t l2_evict_normal_policy() {
+    uint64_t pol;
+    asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(pol));
+    return pol;
+}
+
+template <typename T, int D, bool SPLIT_P>
+__global__ void __launch_bounds__(CHUNK_THREADS, 1)
+chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
+                       const __grid_constant__ CUtensorMap tmap_k,
+                       const __grid_constant__ CUtensorMap tmap_v, const ChunkParams p) {
+    using L = ChunkSmem<D>;
+    constexpr int NS = L::STAGES, KS = D / 16;
+    constexpr int KV_WARP = 8, MMA_WARP = 9, Q_WARP = 10, IDLE_WARP = 11;
+    constexpr int CONSUMERS = 8 + 2;  // arrivals that free a slot of the piece ring
+    constexpr uint32_t FMT = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
+    constexpr uint32_t IDESC_S = umma::idesc_f16(FMT, false, 128, CHUNK_TILE);
+    constexpr uint32_t IDESC_O = umma::idesc_f16(FMT, true, 128, D);
+
+    extern __shared__ __align__(128) unsigned char smem_raw[];
+    unsigned char* smem = reinterpret_cast<unsigned char*>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sbase = smem_addr(smem);
+    const uint32_t q_s = sbase + L::Q_OFF, ring = sbase + L::KV_OFF, bar0 = sbase + L::BAR_OFF;
+    // barriers: K / V stage landed and free; Q tile landed and free; S tile ready; P tile
+    // written; P.V done; piece published and read; every MMA done
+    auto kv_full = [&](int st) { return bar0 + 8 * st; };
+    auto kv_empty = [&](int st) { return bar0 + 8 * (NS + st); };
+    constexpr int NB = 2 * NS;
+    auto q_full = [&](int t) { return bar0 + 8 * (NB + t); };
+    auto q_empty = [&](int t) { return bar0 + 8 * (NB + 2 + t); };
+    auto s_full = [&](int t) { return bar0 + 8 * (NB + 4 + t); };
+    auto p_full = [&](int t) { return bar0 + 8 * (NB + 6 + t); };
+    auto pv_done = [&](int t) { return bar0 + 8 * (NB + 8 + t); };
+    auto piece_full = [&](int i) { return bar0 + 8 * (NB + 10 + i); };
+    auto piece_empty = [&](int i) { return bar0 + 8 * (NB + 12 + i); };
+    const uint32_t all_done = bar0 + 8 * (NB + 14);
+    ChunkPiece* pieces = reinterpret_cast<ChunkPiece*>(smem + L::PIECE_OFF);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::TMEM_SLOT_OFF);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int G = p.group, QPT = 128 / G;  // heads per kv head, queries per tile
+
+    if (threadIdx.x == 0) {
+        for (int st = 0; st < NS; ++st) {
+            mbar_init(kv_full(st), 1);
+            mbar_init(kv_empty(st), 1);
+        }
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(q_full(t), 1);
+            mbar_init(q_empty(t), 1);
+            mbar_init(s_full(t), 1);
+            mbar_init(p_full(t), 4);
+            mbar_init(pv_done(t), 1);
+            mbar_init(piece_full(t), 1);
+            mbar_init(piece_empty(t), CONSUMERS);
+        }
+        mbar_init(all_done, 1);
+        mbar_init_fence();
+    }
+    if (warp == MMA_WARP) umma::alloc(smem_addr(tmem_slot), L::TMEM_COLS);
+    umma::fence_before_sync();
+    __syncthreads();
+    umma::fence_after_sync();
+    const uint32_t tmem = *tmem_slot;
+    // the list of pieces is written by the kernel before this one in the stream
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+
+    // The i-th piece of this CTA, published by the copy warp; false when there is none left
+    // (or the wait ran out).
+    bool ok = true;
+    auto next_piece = [&](int i, ChunkPiece& pc) -> bool {
+        ok = __all_sync(FULL_MASK, mbar_wait(piece_full(i & 1), (i >> 1) & 1));
+        if (!ok) return false;
+        pc = pieces[i & 1];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(piece_empty(i & 1));
+        return pc.kv_head >= 0;
+    };
+
+    if (warp == KV_WARP) {
+        // ---- pieces, and the pages of each: K then V of every 128-token step
+        const uint64_t policy = l2_evict_normal_policy();
+        const int n_pieces = p.header[0];
+        const int B = p.block_size, Hkv = p.num_kv_heads;
+        const int far_row = p.num_blocks * Hkv * B;  // past the pools: copies bring zeros
+        // lane l copies 16-token box l % 8 of 128-byte column l / 8 of each tile
+        const int box = lane & 7, col = lane >> 3;
+        const bool copies = lane < 8 * L::BOXES;
+        uint32_t it = 0;  // stages filled so far
+        int idx = blockIdx.x;
+        for (int i = 0;; ++i) {
+            ChunkPiece pc;
+            pc.kv_head = -1;
+            if (idx < n_pieces) pc = p.pieces[idx];
+            if (i >= 2) {
+                ok = __all_sync(FULL_MASK, mbar_wait(piece_empty(i & 1), ((i >> 1) - 1) & 1));
+                if (!ok) break;
+            }
+            if (lane == 0) {
+                pieces[i & 1] = pc;
+                mbar_arrive(piece_full(i & 1));  // release: the record is visible to its waiters
+            }
+            if (pc.kv_head < 0) break;
+            int next = 0;
+            if (lane == 0) next = atomicAdd(p.header + 3, 1);
+            const int32_t* bt_row = p.block_tables + (size_t)pc.seq * p.max_blocks_per_seq;
+            const int tok_end = pc.lim0 + pc.queries - 1;
+            auto row_of = [&](int kt) -> int {  // pool row of this lane's box in step kt
+                const int t = kt * CHUNK_TILE + box * CHUNK_TOKENS;
+                if (kt >= pc.kt1 || t >= tok_end || !copies) return far_row;
+                const int phys = __ldg(bt_row + t / B);
+                if ((unsigned)phys >= (unsigned)p.num_blocks) {
+                    set_error(p.err, PKV_DEVERR_BLOCK_ID);
+                    return far_row;
+                }
+                return (phys * Hkv + pc.kv_head) * B + t % B;
+            };
+            int row = row_of(pc.kt0);
+            for (int kt = pc.kt0; kt < pc.kt1 && ok; ++kt) {
+                const int row_next = row_of(kt + 1);
+#pragma unroll
+                for (int kv = 0; kv < 2; ++kv, ++it) {
+                    const int st = it % NS;
+                    if (it >= NS) {
+                        ok = __all_sync(FULL_MASK, mbar_wait(kv_empty(st), ((it / NS) - 1) & 1));
+                        if (!ok) break;
+                    }
+                    if (lane == 0) mbar_arrive_expect_tx(kv_full(st), L::TILE);
+                    __syncwarp();
+                    if (copies)
+                        tma_load_2d(ring + st * L::TILE + col * L::BOX + box * CHUNK_TOKENS * 128,
+                                    kv == 0 ? &tmap_k : &tmap_v, col * 64, row, kv_full(st), policy);
+                }
+                row = row_next;
+            }
+            if (!ok) break;
+            idx = __shfl_sync(FULL_MASK, next, 0);
+        }
+        // the CTA must not end with copies still landing in its shared memory
+        for (uint32_t k = it > NS ? it - NS : 0; k < it; ++k) mbar_wait(kv_full(k % NS), (k / NS) & 1);
+    } else if (warp == Q_WARP) {
+        // ---- query tiles
+        int used[2] = {0, 0};
+        ChunkPiece pc;
+        for (int i = 0; next_piece(i, pc); ++i) {
+            if (pc.kt1 <= pc.kt0) continue;
+            for (int t = 0; t < (pc.queries > QPT ? 2 : 1); ++t) {
+                if (used[t] > 0) ok = __all_sync(FULL_MASK, mbar_wait(q_empty(t), (used[t] - 1) & 1));
+                if (!ok) break;
+                ++used[t];
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(q_full(t), L::BOXES * QPT * G * 128);
+                    for (int x = 0; x < L::BOXES; ++x)
+                        tma_load_4d(q_s + t * L::TILE + x * L::BOX, &tmap_q, 0, x, pc.kv_head * G,
+                                    pc.token + t * QPT, q_full(t));
+                }
+                __syncwarp();
+            }
+            if (!ok) break;
+        }
+        for (int t = 0; t < 2; ++t)
+            if (used[t] > 0) mbar_wait(q_full(t), (used[t] - 1) & 1);
+    } else if (warp == MMA_WARP) {
+        // ---- MMA issue
+        uint32_t it = 0;   // stages consumed by earlier pieces
+        int used[2] = {0, 0}, steps[2] = {0, 0};
+        auto stage_landed = [&](uint32_t k) { return mbar_wait(kv_full(k % NS), (k / NS) & 1); };
+        ChunkPiece pc;
+        for (int i = 0; next_piece(i, pc); ++i) {
+            const int n = pc.kt1 - pc.kt0;
+            if (n <= 0) continue;
+            const int tiles = pc.queries > QPT ? 2 : 1;
+            auto issue_s = [&](int t, int j) {
+                const uint32_t k_s = ring + ((it + 2 * j) % NS) * L::TILE, qt = q_s + t * L::TILE;
+#pragma unroll
+                for (int kk = 0; kk < KS; ++kk) {
+                    const uint32_t off = (kk >> 2) * L::BOX + (kk & 3) * 32;
+                    umma::mma_f16(tmem + t * CHUNK_TILE, umma::sw128_desc(qt + off, 16, 1024),
+                                  umma::sw128_desc(k_s + off, 16, 1024), IDESC_S, kk > 0 ? 1u : 0u);
+                }
+                umma::commit(s_full(t));
+                if (j == n - 1) umma::commit(q_empty(t));
+            };
+            auto issue_pv = [&](int j) -> bool {  // both tiles' P.V of step j, and S of step j + 1
+                const uint32_t kv = it + 2 * j + 1;  // V's stage; the next K's is kv + 1
+                if (!stage_landed(kv)) return false;
+                for (int t = 0; t < tiles; ++t) {
+                    if (!mbar_wait(p_full(t), steps[t] & 1)) return false;
+                    ++steps[t];
+                    umma::fence_after_sync();
+                    const uint32_t v_s = ring + (kv % NS) * L::TILE;
+                    const uint32_t p_t = tmem + t * CHUNK_TILE, o_t = tmem + L::O_COL + t * D;
+#pragma unroll
+                    for (int kk = 0; kk < CHUNK_TILE / 16; ++kk) {
+                        // V is N-major: 64-element columns BOX apart, 8-token groups 1024
+                        const uint64_t bv = umma::sw128_desc(v_s + kk * 16 * 128, L::BOX, 1024);
+                        umma::mma_f16_tmem_a(o_t, p_t + kk * 8, bv, IDESC_O, (j > 0 || kk > 0) ? 1u : 0u);
+                        if (SPLIT_P)
+                            umma::mma_f16_tmem_a(o_t, p_t + CHUNK_TILE / 2 + kk * 8, bv, IDESC_O, 1u);
+                    }
+                    umma::commit(pv_done(t));
+                    if (j + 1 < n) {  // S over the P just read: MMAs run in issue order
+                        if (t == 0 && !stage_landed(kv + 1)) return false;
+                        umma::fence_after_sync();
+                        issue_s(t, j + 1);
+                    }
+                }
+                umma::commit(kv_empty(kv % NS));
+                if (j + 1 < n) umma::commit(kv_empty((kv + 1) % NS));
+                return true;
+            };
+            if (lane == 0) {
+                ok = stage_landed(it);
+                for (int t = 0; t < tiles && ok; ++t) {
+                    ok = mbar_wait(q_full(t), used[t] & 1);
+                    ++used[t];
+                    if (!ok) break;
+                    umma::fence_after_sync();
+                    issue_s(t, 0);
+                }
+                if (ok) umma::commit(kv_empty(it % NS));
+                for (int j = 0; j < n - 1 && ok; ++j) ok = issue_pv(j);
+            }
+            ok = __shfl_sync(FULL_MASK, ok, 0);
+            if (!ok) break;
+            if (chunk_has_tail(pc)) {
+                const uint32_t k = it + 2 * n - 1;
+                ok = __all_sync(FULL_MASK, stage_landed(k));
+                if (!ok) break;
+                unsigned char* tile = smem + L::KV_OFF + (k % NS) * L::TILE;
+                const int r0 = pc.lim0 + pc.queries - 1 - (pc.kt1 - 1) * CHUNK_TILE;
+                const int rows = CHUNK_TOKENS - r0 % CHUNK_TOKENS;
+                for (int v = lane; v < rows * L::BOXES * 8; v += 32) {
+                    const int r = r0 + v / (L::BOXES * 8), c = v % (L::BOXES * 8);
+                    *reinterpret_cast<uint4*>(tile + (c / 8) * L::BOX + r * 128 + (c % 8) * 16) =
+                        make_uint4(0u, 0u, 0u, 0u);
+                }
+                umma::fence_smem_to_async();
+                __syncwarp();
+            }
+            if (lane == 0) ok = issue_pv(n - 1);
+            it += 2 * n;
+            ok = __shfl_sync(FULL_MASK, ok, 0);
+            if (!ok) break;
+        }
+        if (lane == 0) {
+            umma::commit(all_done);
+            if (!mbar_wait(all_done, 0)) ok = false;
+        }
+        __syncwarp();
+    } else if (warp != IDLE_WARP) {
+        // ---- softmax and output of tile t: this thread's row is r
+        const int t = warp >> 2, r = threadIdx.x & 127;
+        const uint32_t lane_tmem = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        const uint32_t s_t = lane_tmem + t * CHUNK_TILE, o_t = lane_tmem + L::O_COL + t * D;
+        const int jq = t * QPT + r / G, hg = r % G;  // query within the piece, head of the group
+        int steps = 0;  // S tiles taken so far: the phase of s_full and pv_done
+        ChunkPiece pc;
+        for (int i = 0; next_piece(i, pc); ++i) {
+            if (t == 1 && pc.queries <= QPT) continue;
+            const int n = pc.kt1 - pc.kt0;
+            const bool valid = r < QPT * G && jq < pc.queries;
+            const bool busy = __any_sync(FULL_MASK, valid);
+            const int lim = pc.lim0 + jq;
+            float m_ref = -INFINITY, l = 0.f;
+            for (int j = 0; j < n; ++j, ++steps) {
+                ok = __all_sync(FULL_MASK, mbar_wait(s_full(t), steps & 1));
+                if (!ok) break;
+                if (busy) {
+                    umma::fence_after_sync();
+                    float s[CHUNK_TILE];
+#pragma unroll
+                    for (int c = 0; c < CHUNK_TILE; c += 32)
+                        umma::ld32(s_t + c, *reinterpret_cast<float(*)[32]>(s + c));
+                    if (p.pre_scale != 1.f) {
+#pragma unroll
+                        for (int k = 0; k < CHUNK_TILE; ++k) s[k] *= p.pre_scale;
+                    }
+                    const int seen = lim - (pc.kt0 + j) * CHUNK_TILE;  // columns this row may see
+                    if (__any_sync(FULL_MASK, seen < CHUNK_TILE)) {
+#pragma unroll
+                        for (int k = 0; k < CHUNK_TILE; ++k)
+                            if (k >= seen) s[k] = -INFINITY;
+                    }
+                    float cm = s[0];
+#pragma unroll
+                    for (int k = 1; k < CHUNK_TILE; ++k) cm = fmaxf(cm, s[k]);
+                    cm *= p.scale_log2;
+                    const bool need = cm > m_ref + CHUNK_RESCALE_LOG2;
+                    float alpha = 1.f;
+                    if (need) {
+                        alpha = fast_exp2(m_ref - cm);
+                        m_ref = cm;
+                        l *= alpha;
+                    }
+                    const float neg = m_ref == -INFINITY ? 0.f : -m_ref;
+#pragma unroll
+                    for (int c = 0; c < CHUNK_TILE; c += 32) {
+                        uint32_t hi[16], lo[16];
+#pragma unroll
+                        for (int k = 0; k < 32; k += 2) {
+                            const float a = fast_exp2(fmaf(s[c + k], p.scale_log2, neg));
+                            const float b = fast_exp2(fmaf(s[c + k + 1], p.scale_log2, neg));
+                            l += a + b;
+                            hi[k / 2] = Mma<T>::pack(a, b);
+                            if (SPLIT_P)
+                                lo[k / 2] = Mma<T>::pack(a - Mma<T>::round_trip(a), b - Mma<T>::round_trip(b));
+                        }
+                        umma::st16(s_t + c / 2, hi);
+                        if (SPLIT_P) umma::st16(s_t + CHUNK_TILE / 2 + c / 2, lo);
+                    }
+                    // rows whose reference rose: scale their O (complete through step j - 1)
+                    if (j > 0 && __any_sync(FULL_MASK, need)) {
+                        ok = __all_sync(FULL_MASK, mbar_wait(pv_done(t), (steps - 1) & 1));
+                        if (!ok) break;
+                        umma::fence_after_sync();
+#pragma unroll
+                        for (int c = 0; c < D; c += 32) {
+                            float o[32];
+                            umma::ld32(o_t + c, o);
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) o[k] *= alpha;
+                            umma::st32(o_t + c, o);
+                        }
+                    }
+                    umma::wait_st();
+                }
+                umma::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_full(t));
+            }
+            if (!ok) break;
+            if (n > 0) {
+                ok = __all_sync(FULL_MASK, mbar_wait(pv_done(t), (steps - 1) & 1));
+                if (!ok) break;
+                umma::fence_after_sync();
+            }
+            if (busy) {
+                const long long out_row = ((long long)pc.token + jq) * p.num_q_heads + pc.kv_head * G + hg;
+                const long long part_row = (long long)pc.part_row + (t * QPT * G + r);
+                const bool direct = pc.part_row < 0;
+                const float inv = l > 0.f ? 1.f / l : 0.f;
+#pragma unroll
+                for (int c = 0; c < D; c += 32) {
+                    float o[32];
+                    if (n > 0) {
+                        umma::ld32(o_t + c, o);
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) o[k] = 0.f;
+                    }
+                    if (!valid) {
+                    } else if (direct && !SPLIT_P) {
+                        uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(p.out) + out_row * D + c);
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) o[k] = l > 0.f ? o[k] * inv : 0.f;
+#pragma unroll
+                        for (int k = 0; k < 32; k += 8)
+                            dst[k / 8] = make_uint4(Mma<T>::pack(o[k], o[k + 1]), Mma<T>::pack(o[k + 2], o[k + 3]),
+                                                    Mma<T>::pack(o[k + 4], o[k + 5]), Mma<T>::pack(o[k + 6], o[k + 7]));
+                    } else {
+                        float4* dst = reinterpret_cast<float4*>(
+                            direct ? static_cast<float*>(p.out) + out_row * D + c : p.part_o + part_row * D + c);
+                        if (direct) {
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) o[k] = l > 0.f ? o[k] * inv : 0.f;
+                        }
+#pragma unroll
+                        for (int k = 0; k < 32; k += 4) dst[k / 4] = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+                    }
+                    __syncwarp();
+                }
+                if (valid && !direct) {
+                    p.part_m[part_row] = m_ref;  // base 2
+                    p.part_l[part_row] = l;
+                }
+            }
+        }
+    }
+    if (!ok && lane == 0) set_error(p.err, PKV_DEVERR_TIMEOUT);
+
+    // tensor memory goes back only after every warp is done with it
+    umma::fence_before_sync();
+    __syncthreads();
+    if (warp == MMA_WARP) {
+        umma::fence_after_sync();
+        umma::dealloc(tmem, L::TMEM_COLS);
+    }
+}
+
+// q seen as [T][Hq][D / 64][64]: a box is the G heads of one kv head for 128 / G tokens, one
+// 128-byte column, landing as rows (token, head) of 128 bytes with the 128-byte swizzle.
+template <typename T>
+inline bool encode_query_map(CUtensorMap* map, const void* q, int T_, int Hq, int D, int G) {
+    auto enc = tensor_map_encoder();
+    if (!enc) return false;
+    const cuuint64_t dims[4] = {64, (cuuint64_t)(D / 64), (cuuint64_t)Hq, (cuuint64_t)T_};
+    const cuuint64_t strides[3] = {128, (cuuint64_t)D * 2, (cuuint64_t)Hq * D * 2};
+    const cuuint32_t box[4] = {64, 1, (cuuint32_t)G, (cuuint32_t)(128 / G)};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    return enc(map, Mma<T>::TMA_TYPE, 4, const_cast<void*>(q), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename T, int D, bool SPLIT_P>
+cudaError_t launch_chunk_tds(const ChunkParams& p, const ChunkTensors& x, cudaStream_t stream) {
+    constexpr int SMEM = ChunkSmem<D>::BYTES;
+    const long long rows = (long long)p.num_blocks * p.num_kv_heads * p.block_size;
+    CUtensorMap tq, tk, tv;
+    if (!encode_query_map<T>(&tq, x.q, x.num_tokens, p.num_q_heads, D, p.group) ||
+        !encode_pool_map<T>(&tk, x.k_pool, rows, D) || !encode_pool_map<T>(&tv, x.v_pool, rows, D))
+        return cudaErrorNotSupported;
+    auto kernel = chunk_attention_kernel<T, D, SPLIT_P>;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    static std::atomic<bool> configured[64];  // per device; setting it twice is harmless
+    if (dev >= 64 || !configured[dev].load(std::memory_order_acquire)) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+        if (e != cudaSuccess) return e;
+        if (dev < 64) configured[dev].store(true, std::memory_order_release);
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)x.ctas);
+    cfg.blockDim = dim3(CHUNK_THREADS);
+    cfg.dynamicSmemBytes = SMEM;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, tq, tk, tv, p);
+}
+
+template <typename T>
+cudaError_t launch_chunk_impl(const ChunkParams& p, const ChunkTensors& x, cudaStream_t stream) {
+    const bool f32_out = p.out_dtype == PKV_F32;
+    if (p.head_dim == 64)
+        return f32_out ? launch_chunk_tds<T, 64, true>(p, x, stream)
+                       : launch_chunk_tds<T, 64, false>(p, x, stream);
+    if (p.head_dim == 128)
+        return f32_out ? launch_chunk_tds<T, 128, true>(p, x, stream)
+                       : launch_chunk_tds<T, 128, false>(p, x, stream);
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace pkv

@@ -88,6 +88,122 @@ struct AllocatorState {
     int32_t num_blocks;
 };
 
+// One ragged step's tables, starts, positions and slots (batch.cu).
+struct BatchParams {
+    AllocatorState alloc;
+    int32_t block_size;
+    int32_t* block_tables;      // [S][M]
+    int32_t max_blocks_per_seq;
+    const int32_t* past_lens;   // [S]
+    const int32_t* new_lens;    // [S]
+    int32_t num_seqs;
+    int32_t max_tokens;
+    int32_t* free_count_out;
+    int32_t* query_start;       // [S + 1]
+    int32_t* context_lens;      // [S]
+    int32_t* positions;         // [max_tokens]
+    int32_t* token_seq;         // [max_tokens]
+    int64_t* slot_mapping;      // [max_tokens]
+    int32_t* seq_status;        // [S]
+    unsigned int* err;
+};
+
+// Norms, rotation and cache write of new tokens (rope_write.cu).
+struct RopeParams {
+    const void* q;              // token t's heads at q + t * q_stride elements, packed
+    const void* k;
+    const void* v;
+    int64_t q_stride, k_stride, v_stride;
+    int32_t num_tokens;
+    int32_t num_q_heads;
+    const void* q_weight;       // [D] or null: no norm
+    const void* k_weight;
+    float eps;
+    const float* cos_sin;       // [max_position][rotary_dim]: cosines, then sines
+    int32_t max_position;
+    int32_t rotary_dim;         // 0: no rotation
+    int32_t interleaved;
+    const int32_t* positions;   // [T]; < 0: no token in this row
+    const int64_t* slot_mapping;
+    void* q_out;                // [T][Hq][D]
+    void* k_pool;
+    void* v_pool;
+    int32_t num_blocks;
+    int32_t block_size;
+    int32_t num_kv_heads;
+    int32_t head_dim;
+    unsigned int* err;
+};
+
+// Chunk attention (chunk.cuh, chunk_plan.cu).
+constexpr int CHUNK_TILE = 128;       // cached tokens per step
+constexpr int CHUNK_SPLIT_MIN = 8;    // steps below which no context is cut
+
+// A piece of work: queries [token, token + queries) of the batch for one kv head, over the
+// steps [kt0, kt1) of the request's context.  Query j sees positions below lim0 + j.
+struct __align__(16) ChunkPiece {
+    int32_t token, kv_head, queries, lim0;
+    int32_t seq, kt0, kt1;
+    int32_t part_row;  // first row of its partial results; -1: it writes the output
+};
+
+// A cut item: `rows` (query, head) rows whose `parts` pieces left partial results, piece k's
+// at part_row + k * rows; `first` counts the rows of the cut items before it.
+struct __align__(16) ChunkMerge {
+    int32_t token, kv_head, rows, parts;
+    int32_t part_row, first, pad0, pad1;
+};
+
+// Whether the piece's last copy holds positions no query of it sees.
+__device__ __forceinline__ bool chunk_has_tail(const ChunkPiece& x) {
+    const int tok_end = x.lim0 + x.queries - 1;
+    return x.kt1 > x.kt0 && tok_end % CHUNK_TOKENS != 0 && x.kt1 * CHUNK_TILE >= tok_end;
+}
+
+struct ChunkPlanParams {
+    const int32_t* query_start;   // [S + 1]
+    const int32_t* context_lens;  // [S]
+    int32_t num_seqs, num_tokens;
+    int32_t max_blocks_per_seq, block_size, max_context_len;
+    int32_t num_kv_heads, group;
+    int32_t num_sms, ctas;
+    int64_t max_partial_rows;     // 0: no context may be cut
+    int64_t max_cut_pieces;
+    int32_t* header;              // pieces, cut items, their rows, next piece
+    int32_t* tile_start;          // [S + 1]
+    int4* tiles;                  // (request, first query, queries, limit of the first)
+    ChunkPiece* pieces;
+    ChunkMerge* merges;
+    unsigned int* err;
+};
+
+struct ChunkParams {
+    int32_t num_q_heads, num_kv_heads, group, head_dim;
+    int32_t num_blocks, block_size;
+    const int32_t* block_tables;
+    int32_t max_blocks_per_seq;
+    float scale_log2;   // |scale| * log2(e), positive
+    float pre_scale;    // 1, -1 for a negative scale, 0 for a zero one
+    void* out;          // [T][Hq][D]
+    int32_t out_dtype;
+    int32_t* header;
+    const ChunkPiece* pieces;
+    const ChunkMerge* merges;
+    float* part_m;      // base 2
+    float* part_l;
+    float* part_o;
+    unsigned int* err;
+};
+
+// What the tensor maps and the grid are made from.
+struct ChunkTensors {
+    const void* q;
+    const void* k_pool;
+    const void* v_pool;
+    int32_t num_tokens;
+    int32_t ctas;
+};
+
 // ------------------------------------------------------------------ PTX helpers
 
 __device__ __forceinline__ uint32_t smem_addr(const void* p) {
@@ -297,6 +413,12 @@ cudaError_t launch_fork_sequences(const AllocatorState& a, int32_t B, int32_t* b
 cudaError_t launch_free_sequences(const AllocatorState& a, int32_t B, int32_t* block_tables,
                                   int32_t M, const int32_t* seqs, const int32_t* lens, int32_t n,
                                   unsigned int* err, cudaStream_t stream);
+cudaError_t launch_build_batch(const BatchParams& p, cudaStream_t stream);
+cudaError_t launch_rope_write(const RopeParams& p, int32_t dtype, cudaStream_t stream);
+cudaError_t launch_chunk_plan(const ChunkPlanParams& p, cudaStream_t stream);
+template <typename T>
+cudaError_t launch_chunk(const ChunkParams& p, const ChunkTensors& x, cudaStream_t stream);
+cudaError_t launch_chunk_merge(const ChunkParams& p, int ctas, cudaStream_t stream);
 cudaError_t launch_copy_blocks(const pkv_pool& src, const pkv_pool& dst, const int32_t* pairs,
                                int32_t num_pairs, unsigned int* err, cudaStream_t stream);
 

@@ -74,6 +74,13 @@ _SIGS = {
     "pkv_allocate_for_append": (_i32, [_PA, _PP, _P, _i32, _P, _P, _i32, _P, _P]),
     "pkv_fork_sequences": (_i32, [_PA, _i32, _P, _i32, _P, _P, _i32, _P]),
     "pkv_free_sequences": (_i32, [_PA, _i32, _P, _i32, _P, _P, _i32, _P]),
+    "pkv_build_batch": (_i32, [_PA, _i32, _P, _i32, _P, _P, _i32, _i32, _P, _P, _P, _P, _P, _P, _P,
+                               _P]),
+    "pkv_qk_norm_rope_write": (_i32, [_PP, _P, _i64, _P, _i64, _P, _i64, _i32, _i32, _P, _P, _f32,
+                                      _P, _i32, _i32, _i32, _P, _P, _P, _P]),
+    "pkv_chunk_workspace_bytes": (_sz, [_PP, _i32, _i32, _i32, _i32]),
+    "pkv_paged_attention_chunk": (_i32, [_PP, _P, _i32, _i32, _P, _i32, _P, _i32, _P, _i32, _f32,
+                                         _P, _i32, _P, _sz, _P]),
     "pkv_status_str": (ctypes.c_char_p, [_i32]),
     "pkv_version": (_i32, []),
     "pkv_set_decode_engine": (_i32, [_i32]),
@@ -338,6 +345,19 @@ class BlockAllocator:
         self.refcount = torch.zeros(num_blocks, dtype=torch.int32, device=device)
         self.num_blocks = int(num_blocks)
 
+    @classmethod
+    def of_tensors(cls, free_ids, free_count, refcount):
+        """The bookkeeping over the caller's own int32 tensors."""
+        for t in (free_ids, free_count, refcount):
+            if t.dtype != torch.int32 or not t.is_contiguous():
+                raise ValueError("free_ids, free_count and refcount must be contiguous int32")
+        if free_ids.numel() != refcount.numel() or free_count.numel() != 1:
+            raise ValueError("free_ids and refcount hold one entry per block, free_count one")
+        a = cls.__new__(cls)
+        a.free_ids, a.free_count, a.refcount = free_ids, free_count, refcount
+        a.num_blocks = free_ids.numel()
+        return a
+
     def struct(self):
         return pkv_block_allocator(self.free_ids.data_ptr(), self.free_count.data_ptr(),
                                    self.refcount.data_ptr(), self.num_blocks)
@@ -374,6 +394,111 @@ def pkv_free_sequences(alloc, block_size, block_tables, seqs, lens, stream=None)
     _check(lib.pkv_free_sequences(ctypes.byref(a), int(block_size), _ptr(block_tables),
                                   block_tables.shape[1], _ptr(seqs), _ptr(lens), seqs.numel(),
                                   _stream(stream, block_tables)), "pkv_free_sequences")
+
+
+def _expect(t, name, dtype, shape):
+    """A contiguous tensor of this type and shape, or ValueError."""
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous %s tensor of shape %s" % (name, dtype, tuple(shape)))
+
+
+def _on_current_device(ref, *ts):
+    """All on ref's device, which is the current one (the library launches there)."""
+    d = ref.device
+    for t in ts:
+        if t is not None and t.device != d:
+            raise ValueError("tensors on different devices")
+    if d.type != "cuda" or d.index != torch.cuda.current_device():
+        raise ValueError("the tensors' device must be the current CUDA device")
+
+
+def pkv_build_batch(alloc, block_size, block_tables, past_lens, new_lens, query_start,
+                    context_lens, positions, token_seq, slot_mapping, seq_status,
+                    free_count_out=None, stream=None):
+    """Tables, starts, contexts, positions and slots of one ragged step, from past_lens and
+    new_lens (int32 [num_seqs]); the token arrays' length is the room for tokens."""
+    S, M = block_tables.shape
+    T = positions.numel()
+    i32 = torch.int32
+    _expect(block_tables, "block_tables", i32, (S, M))
+    for t, name, n in ((past_lens, "past_lens", S), (new_lens, "new_lens", S),
+                       (query_start, "query_start", S + 1), (context_lens, "context_lens", S),
+                       (seq_status, "seq_status", S), (positions, "positions", T),
+                       (token_seq, "token_seq", T)):
+        _expect(t, name, i32, (n,))
+    _expect(slot_mapping, "slot_mapping", torch.int64, (T,))
+    if free_count_out is not None:
+        _expect(free_count_out, "free_count_out", i32, (1,))
+    _on_current_device(block_tables, past_lens, new_lens, query_start, context_lens, positions,
+                       token_seq, slot_mapping, seq_status, free_count_out, alloc.free_ids)
+    a = alloc.struct()
+    _check(lib.pkv_build_batch(ctypes.byref(a), int(block_size), _ptr(block_tables), M,
+                               _ptr(past_lens), _ptr(new_lens), S, T, _ptr(free_count_out),
+                               _ptr(query_start), _ptr(context_lens), _ptr(positions),
+                               _ptr(token_seq), _ptr(slot_mapping), _ptr(seq_status),
+                               _stream(stream, block_tables)), "pkv_build_batch")
+
+
+def _head_rows(t, name, dtype, T, H, D):
+    """Token stride of a [T][H][D] tensor whose heads are packed."""
+    if t.dtype != dtype or t.shape != (T, H, D) or t.stride(2) != 1 or (H > 1 and t.stride(1) != D):
+        raise ValueError("%s must be a %s tensor of shape %s with packed heads" % (name, dtype, (T, H, D)))
+    return t.stride(0) if T > 1 else H * D
+
+
+def pkv_qk_norm_rope_write(q, k, v, k_pool, v_pool, positions, slot_mapping, q_out, q_weight=None,
+                           k_weight=None, eps=1e-6, cos_sin=None, interleaved=False, stream=None):
+    """Per-head norms (where a weight is given) and rotation (where cos_sin
+    [max_position][rotary_dim] is given) of q and k; q to q_out, k and v to their slots."""
+    pool = make_pool(k_pool, v_pool)
+    T, Hq, D = q.shape
+    Hkv, dt = pool.num_kv_heads, k_pool.dtype
+    if pool.head_dim != D:
+        raise ValueError("q and the pools must have the same head_dim")
+    strides = [_head_rows(t, n, dt, T, h, D) for t, n, h in ((q, "q", Hq), (k, "k", Hkv), (v, "v", Hkv))]
+    _expect(q_out, "q_out", dt, (T, Hq, D))
+    _expect(positions, "positions", torch.int32, (T,))
+    _expect(slot_mapping, "slot_mapping", torch.int64, (T,))
+    max_pos = rot = 0
+    if cos_sin is not None:
+        max_pos, rot = cos_sin.shape
+        _expect(cos_sin, "cos_sin", torch.float32, (max_pos, rot))
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None:
+            _expect(w, name, dt, (D,))
+    _on_current_device(q, k, v, k_pool, v_pool, positions, slot_mapping, q_out, q_weight, k_weight,
+                       cos_sin)
+    _check(lib.pkv_qk_norm_rope_write(
+        ctypes.byref(pool), _ptr(q), strides[0], _ptr(k), strides[1], _ptr(v), strides[2], T, Hq,
+        _ptr(q_weight), _ptr(k_weight), float(eps), _ptr(cos_sin), max_pos, rot, int(interleaved),
+        _ptr(positions), _ptr(slot_mapping), _ptr(q_out), _stream(stream, q)),
+        "pkv_qk_norm_rope_write")
+
+
+def pkv_chunk_workspace_bytes(k_pool, num_tokens, num_seqs, num_q_heads, max_context_len):
+    pool = make_pool(k_pool, k_pool)
+    return lib.pkv_chunk_workspace_bytes(ctypes.byref(pool), num_tokens, num_seqs, num_q_heads,
+                                         int(max_context_len))
+
+
+def pkv_paged_attention_chunk(q, k_pool, v_pool, query_start, block_tables, context_lens, scale,
+                              out, max_context_len, workspace, stream=None):
+    """q, out: [num_tokens][num_q_heads][head_dim], request s's rows from query_start[s] on."""
+    pool = make_pool(k_pool, v_pool)
+    T, Hq, D = q.shape
+    S, M = block_tables.shape
+    _expect(q, "q", k_pool.dtype, (T, Hq, pool.head_dim))
+    _expect(out, "out", out.dtype, (T, Hq, D))
+    _expect(query_start, "query_start", torch.int32, (S + 1,))
+    _expect(block_tables, "block_tables", torch.int32, (S, M))
+    _expect(context_lens, "context_lens", torch.int32, (S,))
+    _contig(workspace)
+    _on_current_device(q, k_pool, v_pool, query_start, block_tables, context_lens, out, workspace)
+    _check(lib.pkv_paged_attention_chunk(
+        ctypes.byref(pool), _ptr(q), T, Hq, _ptr(query_start), S, _ptr(block_tables), M,
+        _ptr(context_lens), int(max_context_len), float(scale), _ptr(out), _DTYPE[out.dtype],
+        _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream, q)),
+        "pkv_paged_attention_chunk")
 
 
 def pkv_get_device_error(stream=None, device=None):
