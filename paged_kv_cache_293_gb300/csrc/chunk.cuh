@@ -14,15 +14,14 @@
 // SM, take pieces from that list in order until it is empty.  Twelve warps, fixed roles:
 //   0-3, 4-7  softmax of tile 0 and of tile 1, and their output
 //   8         takes the next piece; tensor copies of K and V pages into a ring of stages
-//   9         one lane issues the MMAs, for both tiles in turn:
+//   9, 11     one lane each issues the MMAs of tile 0 and of tile 1:
 //               S_t = Q_t . K_j^T            128 x 128 in tensor memory
 //               O_t += P_t . V_j             P_t written over S_t by the softmax
-//             so that one tile's softmax runs while the tensor cores work for the other
+//             so that one tile's softmax runs while the tensor cores work for the other.
 //             Before a piece's last P.V the warp zeroes the V rows of the last 16-token copy
 //             past the last position the piece may see (they may hold anything; their
 //             weights are zero, and 0 * NaN is not)
 //   10        tensor copies of the query tiles
-//   11        none (fills the warpgroup)
 // The reference maximum of a row is raised only when a step's maximum exceeds it by more
 // than 8 in base 2, so O is rescaled rarely; every term of a row uses the same reference.
 // P enters its product rounded to the pool's type (relative error 2^-9 bf16, 2^-12 fp16 per
@@ -40,6 +39,9 @@
 namespace pkv {
 
 constexpr int CHUNK_THREADS = 384;
+// Registers per thread: 168 at launch; the softmax warps take what the others give back
+// (256 * 200 + 128 * 104 = 384 * 168).
+constexpr int CHUNK_REGS_SOFTMAX = 200, CHUNK_REGS_OTHERS = 104;
 constexpr float CHUNK_RESCALE_LOG2 = 8.f;
 
 template <int D>
@@ -51,7 +53,7 @@ struct ChunkSmem {
     static constexpr int Q_OFF = 0;
     static constexpr int KV_OFF = 2 * TILE;
     static constexpr int BAR_OFF = KV_OFF + STAGES * TILE;
-    static constexpr int NBARS = 2 * STAGES + 15;
+    static constexpr int NBARS = 2 * STAGES + 16;
     static constexpr int PIECE_OFF = BAR_OFF + ((NBARS * 8 + 15) / 16) * 16;
     static constexpr int TMEM_SLOT_OFF = PIECE_OFF + 2 * 32;
     static constexpr int BYTES = TMEM_SLOT_OFF + 16 + 1024;  // + alignment slack
@@ -77,6 +79,57 @@ __device__ __forceinline__ uint64_t l2_evict_normal_policy() {
     return pol;
 }
 
+// As mbar_wait, for waits that mostly end within a microsecond: reading the global timer
+// takes about that long itself, so it is first read after WAIT_TRIES tries (each of which the
+// hardware may hold for a while).  With mbar_wait's read after the first try the two tiles'
+// hand-overs took 2800 cycles per step even without any softmax work.
+constexpr int WAIT_TRIES = 256;
+__device__ __forceinline__ bool mbar_wait_short(uint32_t bar, uint32_t parity) {
+#pragma unroll 1
+    for (int i = 0; i < WAIT_TRIES; ++i)
+        if (mbar_try_wait(bar, parity)) return true;
+    return mbar_wait(bar, parity);
+}
+
+template <int N>
+__device__ __forceinline__ void regs_dec() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_inc() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// Two 32-bit values in one 64-bit register: one instruction works on both.
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+    uint64_t v;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi));
+    return v;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t v;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(v) : "l"(a), "l"(b), "l"(c));
+    return v;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t v;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
+    return v;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t v;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
+    return v;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float v;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(v) : "f"(a), "f"(b), "f"(c));
+    return v;
+}
+
 template <typename T, int D, bool SPLIT_P>
 __global__ void __launch_bounds__(CHUNK_THREADS, 1)
 chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
@@ -84,8 +137,8 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
                        const __grid_constant__ CUtensorMap tmap_v, const ChunkParams p) {
     using L = ChunkSmem<D>;
     constexpr int NS = L::STAGES, KS = D / 16;
-    constexpr int KV_WARP = 8, MMA_WARP = 9, Q_WARP = 10, IDLE_WARP = 11;
-    constexpr int CONSUMERS = 8 + 2;  // arrivals that free a slot of the piece ring
+    constexpr int KV_WARP = 8, MMA_WARP = 9, Q_WARP = 10;  // and the second tile's MMAs: 11
+    constexpr int CONSUMERS = 8 + 3;  // arrivals that free a slot of the piece ring
     constexpr uint32_t FMT = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
     constexpr uint32_t IDESC_S = umma::idesc_f16(FMT, false, 128, CHUNK_TILE);
     constexpr uint32_t IDESC_O = umma::idesc_f16(FMT, true, 128, D);
@@ -96,7 +149,7 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
     const uint32_t sbase = smem_addr(smem);
     const uint32_t q_s = sbase + L::Q_OFF, ring = sbase + L::KV_OFF, bar0 = sbase + L::BAR_OFF;
     // barriers: K / V stage landed and free; Q tile landed and free; S tile ready; P tile
-    // written; P.V done; piece published and read; every MMA done
+    // written; a piece's last P.V done; piece published and read; every MMA done
     auto kv_full = [&](int st) { return bar0 + 8 * st; };
     auto kv_empty = [&](int st) { return bar0 + 8 * (NS + st); };
     constexpr int NB = 2 * NS;
@@ -107,7 +160,7 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
     auto pv_done = [&](int t) { return bar0 + 8 * (NB + 8 + t); };
     auto piece_full = [&](int i) { return bar0 + 8 * (NB + 10 + i); };
     auto piece_empty = [&](int i) { return bar0 + 8 * (NB + 12 + i); };
-    const uint32_t all_done = bar0 + 8 * (NB + 14);
+    auto all_done = [&](int t) { return bar0 + 8 * (NB + 14 + t); };
     ChunkPiece* pieces = reinterpret_cast<ChunkPiece*>(smem + L::PIECE_OFF);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::TMEM_SLOT_OFF);
 
@@ -117,7 +170,7 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
     if (threadIdx.x == 0) {
         for (int st = 0; st < NS; ++st) {
             mbar_init(kv_full(st), 1);
-            mbar_init(kv_empty(st), 1);
+            mbar_init(kv_empty(st), 2);
         }
         for (int t = 0; t < 2; ++t) {
             mbar_init(q_full(t), 1);
@@ -125,10 +178,10 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
             mbar_init(s_full(t), 1);
             mbar_init(p_full(t), 4);
             mbar_init(pv_done(t), 1);
+            mbar_init(all_done(t), 1);
             mbar_init(piece_full(t), 1);
             mbar_init(piece_empty(t), CONSUMERS);
         }
-        mbar_init(all_done, 1);
         mbar_init_fence();
     }
     if (warp == MMA_WARP) umma::alloc(smem_addr(tmem_slot), L::TMEM_COLS);
@@ -143,7 +196,7 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
     // (or the wait ran out).
     bool ok = true;
     auto next_piece = [&](int i, ChunkPiece& pc) -> bool {
-        ok = __all_sync(FULL_MASK, mbar_wait(piece_full(i & 1), (i >> 1) & 1));
+        ok = __all_sync(FULL_MASK, mbar_wait_short(piece_full(i & 1), (i >> 1) & 1));
         if (!ok) return false;
         pc = pieces[i & 1];
         __syncwarp();
@@ -151,7 +204,10 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
         return pc.kv_head >= 0;
     };
 
+    // each role sets its registers inside its own branch: where branches meet again, the
+    // compiler would hold both to the smaller number
     if (warp == KV_WARP) {
+        regs_dec<CHUNK_REGS_OTHERS>();
         // ---- pieces, and the pages of each: K then V of every 128-token step
         const uint64_t policy = l2_evict_normal_policy();
         const int n_pieces = p.header[0];
@@ -167,7 +223,7 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
             pc.kv_head = -1;
             if (idx < n_pieces) pc = p.pieces[idx];
             if (i >= 2) {
-                ok = __all_sync(FULL_MASK, mbar_wait(piece_empty(i & 1), ((i >> 1) - 1) & 1));
+                ok = __all_sync(FULL_MASK, mbar_wait_short(piece_empty(i & 1), ((i >> 1) - 1) & 1));
                 if (!ok) break;
             }
             if (lane == 0) {
@@ -196,7 +252,7 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
                 for (int kv = 0; kv < 2; ++kv, ++it) {
                     const int st = it % NS;
                     if (it >= NS) {
-                        ok = __all_sync(FULL_MASK, mbar_wait(kv_empty(st), ((it / NS) - 1) & 1));
+                        ok = __all_sync(FULL_MASK, mbar_wait_short(kv_empty(st), ((it / NS) - 1) & 1));
                         if (!ok) break;
                     }
                     if (lane == 0) mbar_arrive_expect_tx(kv_full(st), L::TILE);
@@ -211,15 +267,16 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
             idx = __shfl_sync(FULL_MASK, next, 0);
         }
         // the CTA must not end with copies still landing in its shared memory
-        for (uint32_t k = it > NS ? it - NS : 0; k < it; ++k) mbar_wait(kv_full(k % NS), (k / NS) & 1);
+        for (uint32_t k = it > NS ? it - NS : 0; k < it; ++k) mbar_wait_short(kv_full(k % NS), (k / NS) & 1);
     } else if (warp == Q_WARP) {
+        regs_dec<CHUNK_REGS_OTHERS>();
         // ---- query tiles
         int used[2] = {0, 0};
         ChunkPiece pc;
         for (int i = 0; next_piece(i, pc); ++i) {
             if (pc.kt1 <= pc.kt0) continue;
             for (int t = 0; t < (pc.queries > QPT ? 2 : 1); ++t) {
-                if (used[t] > 0) ok = __all_sync(FULL_MASK, mbar_wait(q_empty(t), (used[t] - 1) & 1));
+                if (used[t] > 0) ok = __all_sync(FULL_MASK, mbar_wait_short(q_empty(t), (used[t] - 1) & 1));
                 if (!ok) break;
                 ++used[t];
                 if (lane == 0) {
@@ -233,75 +290,95 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
             if (!ok) break;
         }
         for (int t = 0; t < 2; ++t)
-            if (used[t] > 0) mbar_wait(q_full(t), (used[t] - 1) & 1);
-    } else if (warp == MMA_WARP) {
-        // ---- MMA issue
-        uint32_t it = 0;   // stages consumed by earlier pieces
-        int used[2] = {0, 0}, steps[2] = {0, 0};
-        auto stage_landed = [&](uint32_t k) { return mbar_wait(kv_full(k % NS), (k / NS) & 1); };
+            if (used[t] > 0) mbar_wait_short(q_full(t), (used[t] - 1) & 1);
+    } else if (warp == MMA_WARP || warp == MMA_WARP + 2) {
+        regs_dec<CHUNK_REGS_OTHERS>();
+        // ---- MMA issue for tile t.  Every stage is released by both of these warps.
+        const int t = warp == MMA_WARP ? 0 : 1;
+        const uint32_t s_t = tmem + t * CHUNK_TILE, o_t = tmem + L::O_COL + t * D;
+        const uint64_t q_desc = umma::sw128_desc(q_s + t * L::TILE, 16, 1024);
+        int st = 0, used = 0, steps = 0, all_steps = 0;  // next stage; Q tiles and P tiles taken
+        uint32_t total = 0;               // stages of all pieces so far
+        uint32_t phase = 0;               // of that stage
+        auto landed = [&] { return mbar_wait_short(kv_full(st), phase); };
+        auto advance = [&] {
+            if (++st == NS) {
+                st = 0;
+                phase ^= 1;
+            }
+        };
+        auto issue_s = [&] {  // S over the P just read: one thread's MMAs run in issue order
+            const uint64_t k_desc = umma::sw128_desc(ring + st * L::TILE, 16, 1024);
+#pragma unroll
+            for (int kk = 0; kk < KS; ++kk) {
+                const uint32_t off = ((kk >> 2) * L::BOX + (kk & 3) * 32) >> 4;  // start address field
+                umma::mma_f16(s_t, q_desc + off, k_desc + off, IDESC_S, kk > 0 ? 1u : 0u);
+            }
+            umma::commit(s_full(t));  // also says that every P.V before is done
+        };
+        auto issue_pv = [&](bool first) {
+            // V is N-major: 64-element columns BOX apart, 8-token groups 1024
+            const uint64_t v_desc = umma::sw128_desc(ring + st * L::TILE, L::BOX, 1024);
+#pragma unroll
+            for (int kk = 0; kk < CHUNK_TILE / 16; ++kk) {
+                const uint64_t bv = v_desc + (kk * 16 * 128 >> 4);
+                umma::mma_f16_tmem_a(o_t, s_t + kk * 8, bv, IDESC_O, (!first || kk > 0) ? 1u : 0u);
+                if (SPLIT_P) umma::mma_f16_tmem_a(o_t, s_t + CHUNK_TILE / 2 + kk * 8, bv, IDESC_O, 1u);
+            }
+        };
         ChunkPiece pc;
         for (int i = 0; next_piece(i, pc); ++i) {
             const int n = pc.kt1 - pc.kt0;
             if (n <= 0) continue;
-            const int tiles = pc.queries > QPT ? 2 : 1;
-            auto issue_s = [&](int t, int j) {
-                const uint32_t k_s = ring + ((it + 2 * j) % NS) * L::TILE, qt = q_s + t * L::TILE;
-#pragma unroll
-                for (int kk = 0; kk < KS; ++kk) {
-                    const uint32_t off = (kk >> 2) * L::BOX + (kk & 3) * 32;
-                    umma::mma_f16(tmem + t * CHUNK_TILE, umma::sw128_desc(qt + off, 16, 1024),
-                                  umma::sw128_desc(k_s + off, 16, 1024), IDESC_S, kk > 0 ? 1u : 0u);
+            if (t == 1 && pc.queries <= QPT) {  // no second tile: release the stages as they land
+                for (int k = 0; k < 2 * n && ok; ++k) {
+                    ok = __all_sync(FULL_MASK, landed());
+                    if (ok && lane == 0) mbar_arrive(kv_empty(st));
+                    advance();
                 }
-                umma::commit(s_full(t));
-                if (j == n - 1) umma::commit(q_empty(t));
-            };
-            auto issue_pv = [&](int j) -> bool {  // both tiles' P.V of step j, and S of step j + 1
-                const uint32_t kv = it + 2 * j + 1;  // V's stage; the next K's is kv + 1
-                if (!stage_landed(kv)) return false;
-                for (int t = 0; t < tiles; ++t) {
-                    if (!mbar_wait(p_full(t), steps[t] & 1)) return false;
-                    ++steps[t];
+                total += 2 * n;
+                if (!ok) break;
+                continue;
+            }
+            if (umma::elect_one()) {
+                ok = mbar_wait_short(q_full(t), used & 1) && landed();
+                if (ok) {
                     umma::fence_after_sync();
-                    const uint32_t v_s = ring + (kv % NS) * L::TILE;
-                    const uint32_t p_t = tmem + t * CHUNK_TILE, o_t = tmem + L::O_COL + t * D;
-#pragma unroll
-                    for (int kk = 0; kk < CHUNK_TILE / 16; ++kk) {
-                        // V is N-major: 64-element columns BOX apart, 8-token groups 1024
-                        const uint64_t bv = umma::sw128_desc(v_s + kk * 16 * 128, L::BOX, 1024);
-                        umma::mma_f16_tmem_a(o_t, p_t + kk * 8, bv, IDESC_O, (j > 0 || kk > 0) ? 1u : 0u);
-                        if (SPLIT_P)
-                            umma::mma_f16_tmem_a(o_t, p_t + CHUNK_TILE / 2 + kk * 8, bv, IDESC_O, 1u);
-                    }
-                    umma::commit(pv_done(t));
-                    if (j + 1 < n) {  // S over the P just read: MMAs run in issue order
-                        if (t == 0 && !stage_landed(kv + 1)) return false;
-                        umma::fence_after_sync();
-                        issue_s(t, j + 1);
-                    }
+                    issue_s();
+                    if (n == 1) umma::commit(q_empty(t));
+                    umma::commit(kv_empty(st));
+                    advance();
                 }
-                umma::commit(kv_empty(kv % NS));
-                if (j + 1 < n) umma::commit(kv_empty((kv + 1) % NS));
-                return true;
-            };
-            if (lane == 0) {
-                ok = stage_landed(it);
-                for (int t = 0; t < tiles && ok; ++t) {
-                    ok = mbar_wait(q_full(t), used[t] & 1);
-                    ++used[t];
+#pragma unroll 1
+                for (int j = 0; j < n - 1 && ok; ++j) {
+                    ok = landed() && mbar_wait_short(p_full(t), steps & 1);
+                    if (!ok) break;
+                    ++steps;
+                    umma::fence_after_sync();
+                    issue_pv(j == 0);
+                    const int v_st = st;
+                    advance();
+                    ok = landed();
                     if (!ok) break;
                     umma::fence_after_sync();
-                    issue_s(t, 0);
+                    issue_s();
+                    if (j == n - 2) umma::commit(q_empty(t));
+                    umma::commit(kv_empty(v_st));
+                    umma::commit(kv_empty(st));
+                    advance();
                 }
-                if (ok) umma::commit(kv_empty(it % NS));
-                for (int j = 0; j < n - 1 && ok; ++j) ok = issue_pv(j);
             }
-            ok = __shfl_sync(FULL_MASK, ok, 0);
+            ++used;
+            ok = __all_sync(FULL_MASK, ok);
             if (!ok) break;
-            if (chunk_has_tail(pc)) {
-                const uint32_t k = it + 2 * n - 1;
-                ok = __all_sync(FULL_MASK, stage_landed(k));
+            // every lane's cursor to the piece's last stage, V's
+            total += 2 * n;
+            st = (int)((total - 1) % NS);
+            phase = ((total - 1) / NS) & 1;
+            if (chunk_has_tail(pc)) {  // both warps may zero the same rows: the values agree
+                ok = __all_sync(FULL_MASK, landed());
                 if (!ok) break;
-                unsigned char* tile = smem + L::KV_OFF + (k % NS) * L::TILE;
+                unsigned char* tile = smem + L::KV_OFF + st * L::TILE;
                 const int r0 = pc.lim0 + pc.queries - 1 - (pc.kt1 - 1) * CHUNK_TILE;
                 const int rows = CHUNK_TOKENS - r0 % CHUNK_TOKENS;
                 for (int v = lane; v < rows * L::BOXES * 8; v += 32) {
@@ -312,23 +389,34 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
                 umma::fence_smem_to_async();
                 __syncwarp();
             }
-            if (lane == 0) ok = issue_pv(n - 1);
-            it += 2 * n;
-            ok = __shfl_sync(FULL_MASK, ok, 0);
+            if (umma::elect_one()) {
+                ok = landed() && mbar_wait_short(p_full(t), (all_steps + n - 1) & 1);
+                if (ok) {
+                    umma::fence_after_sync();
+                    issue_pv(n == 1);
+                    umma::commit(pv_done(t));
+                    umma::commit(kv_empty(st));
+                }
+            }
+            all_steps += n;
+            steps = all_steps;
+            advance();
+            ok = __all_sync(FULL_MASK, ok);
             if (!ok) break;
         }
-        if (lane == 0) {
-            umma::commit(all_done);
-            if (!mbar_wait(all_done, 0)) ok = false;
+        if (umma::elect_one()) {
+            umma::commit(all_done(t));
+            if (!mbar_wait_short(all_done(t), 0)) ok = false;
         }
         __syncwarp();
-    } else if (warp != IDLE_WARP) {
+    } else {
+        regs_inc<CHUNK_REGS_SOFTMAX>();
         // ---- softmax and output of tile t: this thread's row is r
         const int t = warp >> 2, r = threadIdx.x & 127;
         const uint32_t lane_tmem = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const uint32_t s_t = lane_tmem + t * CHUNK_TILE, o_t = lane_tmem + L::O_COL + t * D;
         const int jq = t * QPT + r / G, hg = r % G;  // query within the piece, head of the group
-        int steps = 0;  // S tiles taken so far: the phase of s_full and pv_done
+        int steps = 0, ends = 0;  // S tiles and last P.V's so far: the phases of s_full and pv_done
         ChunkPiece pc;
         for (int i = 0; next_piece(i, pc); ++i) {
             if (t == 1 && pc.queries <= QPT) continue;
@@ -336,46 +424,60 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
             const bool valid = r < QPT * G && jq < pc.queries;
             const bool busy = __any_sync(FULL_MASK, valid);
             const int lim = pc.lim0 + jq;
-            float m_ref = -INFINITY, l = 0.f;
+            float m_ref = -INFINITY;
+            uint64_t sum2[2] = {0, 0};  // the row's sum, in four parts
             for (int j = 0; j < n; ++j, ++steps) {
-                ok = __all_sync(FULL_MASK, mbar_wait(s_full(t), steps & 1));
+                ok = __all_sync(FULL_MASK, mbar_wait_short(s_full(t), steps & 1));
                 if (!ok) break;
                 if (busy) {
                     umma::fence_after_sync();
-                    float s[CHUNK_TILE];
+                    uint32_t raw[CHUNK_TILE];
 #pragma unroll
-                    for (int c = 0; c < CHUNK_TILE; c += 32)
-                        umma::ld32(s_t + c, *reinterpret_cast<float(*)[32]>(s + c));
+                    for (int c = 0; c < CHUNK_TILE; c += 32) umma::ld32_async(s_t + c, raw + c);
+#pragma unroll
+                    for (int c = 0; c < CHUNK_TILE; c += 32) umma::wait_ld(raw + c);
                     if (p.pre_scale != 1.f) {
 #pragma unroll
-                        for (int k = 0; k < CHUNK_TILE; ++k) s[k] *= p.pre_scale;
+                        for (int k = 0; k < CHUNK_TILE; ++k)
+                            raw[k] = __float_as_uint(__uint_as_float(raw[k]) * p.pre_scale);
                     }
                     const int seen = lim - (pc.kt0 + j) * CHUNK_TILE;  // columns this row may see
                     if (__any_sync(FULL_MASK, seen < CHUNK_TILE)) {
 #pragma unroll
                         for (int k = 0; k < CHUNK_TILE; ++k)
-                            if (k >= seen) s[k] = -INFINITY;
+                            if (k >= seen) raw[k] = 0xff800000u;  // -inf
                     }
-                    float cm = s[0];
+                    float top[4];  // four chains, three-input maxima
 #pragma unroll
-                    for (int k = 1; k < CHUNK_TILE; ++k) cm = fmaxf(cm, s[k]);
-                    cm *= p.scale_log2;
+                    for (int c = 0; c < 4; ++c) {
+                        top[c] = __uint_as_float(raw[c]);
+#pragma unroll
+                        for (int k = c + 4; k + 4 < CHUNK_TILE; k += 8)
+                            top[c] = max3(top[c], __uint_as_float(raw[k]), __uint_as_float(raw[k + 4]));
+                        top[c] = fmaxf(top[c], __uint_as_float(raw[CHUNK_TILE - 4 + c]));
+                    }
+                    const float cm = max3(top[0], top[1], fmaxf(top[2], top[3])) * p.scale_log2;
                     const bool need = cm > m_ref + CHUNK_RESCALE_LOG2;
                     float alpha = 1.f;
                     if (need) {
                         alpha = fast_exp2(m_ref - cm);
                         m_ref = cm;
-                        l *= alpha;
                     }
                     const float neg = m_ref == -INFINITY ? 0.f : -m_ref;
+                    const uint64_t scale2 = pack2(p.scale_log2, p.scale_log2), neg2 = pack2(neg, neg);
+                    sum2[0] = mul2(sum2[0], pack2(alpha, alpha));
+                    sum2[1] = mul2(sum2[1], pack2(alpha, alpha));
 #pragma unroll
                     for (int c = 0; c < CHUNK_TILE; c += 32) {
                         uint32_t hi[16], lo[16];
 #pragma unroll
                         for (int k = 0; k < 32; k += 2) {
-                            const float a = fast_exp2(fmaf(s[c + k], p.scale_log2, neg));
-                            const float b = fast_exp2(fmaf(s[c + k + 1], p.scale_log2, neg));
-                            l += a + b;
+                            float a, b;
+                            unpack2(fma2(pack2(__uint_as_float(raw[c + k]), __uint_as_float(raw[c + k + 1])),
+                                         scale2, neg2), a, b);
+                            a = fast_exp2(a);
+                            b = fast_exp2(b);
+                            sum2[(k >> 1) & 1] = add2(sum2[(k >> 1) & 1], pack2(a, b));
                             hi[k / 2] = Mma<T>::pack(a, b);
                             if (SPLIT_P)
                                 lo[k / 2] = Mma<T>::pack(a - Mma<T>::round_trip(a), b - Mma<T>::round_trip(b));
@@ -383,11 +485,9 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
                         umma::st16(s_t + c / 2, hi);
                         if (SPLIT_P) umma::st16(s_t + CHUNK_TILE / 2 + c / 2, lo);
                     }
-                    // rows whose reference rose: scale their O (complete through step j - 1)
+                    // rows whose reference rose: scale their O (complete through step j - 1: this
+                    // step's S was committed after that P.V)
                     if (j > 0 && __any_sync(FULL_MASK, need)) {
-                        ok = __all_sync(FULL_MASK, mbar_wait(pv_done(t), (steps - 1) & 1));
-                        if (!ok) break;
-                        umma::fence_after_sync();
 #pragma unroll
                         for (int c = 0; c < D; c += 32) {
                             float o[32];
@@ -405,14 +505,19 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
             }
             if (!ok) break;
             if (n > 0) {
-                ok = __all_sync(FULL_MASK, mbar_wait(pv_done(t), (steps - 1) & 1));
+                ok = __all_sync(FULL_MASK, mbar_wait_short(pv_done(t), ends & 1));
                 if (!ok) break;
+                ++ends;
                 umma::fence_after_sync();
             }
             if (busy) {
                 const long long out_row = ((long long)pc.token + jq) * p.num_q_heads + pc.kv_head * G + hg;
                 const long long part_row = (long long)pc.part_row + (t * QPT * G + r);
                 const bool direct = pc.part_row < 0;
+                float part[4];
+                unpack2(sum2[0], part[0], part[1]);
+                unpack2(sum2[1], part[2], part[3]);
+                const float l = (part[0] + part[1]) + (part[2] + part[3]);
                 const float inv = l > 0.f ? 1.f / l : 0.f;
 #pragma unroll
                 for (int c = 0; c < D; c += 32) {
