@@ -213,9 +213,7 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
         const int n_pieces = p.header[0];
         const int B = p.block_size, Hkv = p.num_kv_heads;
         const int far_row = p.num_blocks * Hkv * B;  // past the pools: copies bring zeros
-        // lane l copies 16-token box l % 8 of 128-byte column l / 8 of each tile
-        const int box = lane & 7, col = lane >> 3;
-        const bool copies = lane < 8 * L::BOXES;
+        constexpr int NBOX = CHUNK_TILE / CHUNK_TOKENS;  // 16-token copies of a step; lane b finds b's block
         uint32_t it = 0;  // stages filled so far
         int idx = blockIdx.x;
         for (int i = 0;; ++i) {
@@ -235,9 +233,9 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
             if (lane == 0) next = atomicAdd(p.header + 3, 1);
             const int32_t* bt_row = p.block_tables + (size_t)pc.seq * p.max_blocks_per_seq;
             const int tok_end = pc.lim0 + pc.queries - 1;
-            auto row_of = [&](int kt) -> int {  // pool row of this lane's box in step kt
-                const int t = kt * CHUNK_TILE + box * CHUNK_TOKENS;
-                if (kt >= pc.kt1 || t >= tok_end || !copies) return far_row;
+            auto row_of = [&](int kt) -> int {  // pool row of this lane's copy in step kt
+                const int t = kt * CHUNK_TILE + lane * CHUNK_TOKENS;
+                if (kt >= pc.kt1 || t >= tok_end || lane >= NBOX) return far_row;
                 const int phys = __ldg(bt_row + t / B);
                 if ((unsigned)phys >= (unsigned)p.num_blocks) {
                     set_error(p.err, PKV_DEVERR_BLOCK_ID);
@@ -248,6 +246,9 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
             int row = row_of(pc.kt0);
             for (int kt = pc.kt0; kt < pc.kt1 && ok; ++kt) {
                 const int row_next = row_of(kt + 1);
+                int rows[NBOX];
+#pragma unroll
+                for (int b = 0; b < NBOX; ++b) rows[b] = __shfl_sync(FULL_MASK, row, b);
 #pragma unroll
                 for (int kv = 0; kv < 2; ++kv, ++it) {
                     const int st = it % NS;
@@ -255,11 +256,26 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
                         ok = __all_sync(FULL_MASK, mbar_wait_short(kv_empty(st), ((it / NS) - 1) & 1));
                         if (!ok) break;
                     }
-                    if (lane == 0) mbar_arrive_expect_tx(kv_full(st), L::TILE);
+                    // from one elected thread: copies issued by 16 lanes at once took about
+                    // 100 cycles each, and the whole kernel the time of its copies
+                    if (umma::elect_one()) {
+                        const uint32_t full = kv_full(st), dst = ring + st * L::TILE;
+                        mbar_arrive_expect_tx(full, L::TILE);
+#pragma unroll
+                        for (int b = 0; b < NBOX; ++b) {
+                            if (kv == 0) {
+                                // K tile: 128-byte columns of 128 rows
+#pragma unroll
+                                for (int x = 0; x < L::BOXES; ++x)
+                                    tma_load_2d(dst + x * L::BOX + b * CHUNK_TOKENS * 128, &tmap_k, x * 64, rows[b],
+                                                full, policy);
+                            } else {
+                                // V tile: a copy's columns behind one another (one K step of P.V)
+                                tma_load_3d(dst + b * CHUNK_TOKENS * D * 2, &tmap_v, 0, rows[b], 0, full, policy);
+                            }
+                        }
+                    }
                     __syncwarp();
-                    if (copies)
-                        tma_load_2d(ring + st * L::TILE + col * L::BOX + box * CHUNK_TOKENS * 128,
-                                    kv == 0 ? &tmap_k : &tmap_v, col * 64, row, kv_full(st), policy);
                 }
                 row = row_next;
             }
@@ -317,11 +333,12 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
             umma::commit(s_full(t));  // also says that every P.V before is done
         };
         auto issue_pv = [&](bool first) {
-            // V is N-major: 64-element columns BOX apart, 8-token groups 1024
-            const uint64_t v_desc = umma::sw128_desc(ring + st * L::TILE, L::BOX, 1024);
+            // V is N-major: 64-element columns 2048 apart, 8-token groups 1024, and a K step
+            // is one copy's 16 tokens
+            const uint64_t v_desc = umma::sw128_desc(ring + st * L::TILE, CHUNK_TOKENS * 128, 1024);
 #pragma unroll
             for (int kk = 0; kk < CHUNK_TILE / 16; ++kk) {
-                const uint64_t bv = v_desc + (kk * 16 * 128 >> 4);
+                const uint64_t bv = v_desc + (kk * CHUNK_TOKENS * D * 2 >> 4);
                 umma::mma_f16_tmem_a(o_t, s_t + kk * 8, bv, IDESC_O, (!first || kk > 0) ? 1u : 0u);
                 if (SPLIT_P) umma::mma_f16_tmem_a(o_t, s_t + CHUNK_TILE / 2 + kk * 8, bv, IDESC_O, 1u);
             }
@@ -378,12 +395,12 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
             if (chunk_has_tail(pc)) {  // both warps may zero the same rows: the values agree
                 ok = __all_sync(FULL_MASK, landed());
                 if (!ok) break;
-                unsigned char* tile = smem + L::KV_OFF + st * L::TILE;
                 const int r0 = pc.lim0 + pc.queries - 1 - (pc.kt1 - 1) * CHUNK_TILE;
                 const int rows = CHUNK_TOKENS - r0 % CHUNK_TOKENS;
+                unsigned char* tile = smem + L::KV_OFF + st * L::TILE + r0 / CHUNK_TOKENS * (CHUNK_TOKENS * D * 2);
                 for (int v = lane; v < rows * L::BOXES * 8; v += 32) {
-                    const int r = r0 + v / (L::BOXES * 8), c = v % (L::BOXES * 8);
-                    *reinterpret_cast<uint4*>(tile + (c / 8) * L::BOX + r * 128 + (c % 8) * 16) =
+                    const int r = r0 % CHUNK_TOKENS + v / (L::BOXES * 8), c = v % (L::BOXES * 8);
+                    *reinterpret_cast<uint4*>(tile + (c / 8) * (CHUNK_TOKENS * 128) + r * 128 + (c % 8) * 16) =
                         make_uint4(0u, 0u, 0u, 0u);
                 }
                 umma::fence_smem_to_async();
@@ -588,7 +605,7 @@ cudaError_t launch_chunk_tds(const ChunkParams& p, const ChunkTensors& x, cudaSt
     const long long rows = (long long)p.num_blocks * p.num_kv_heads * p.block_size;
     CUtensorMap tq, tk, tv;
     if (!encode_query_map<T>(&tq, x.q, x.num_tokens, p.num_q_heads, D, p.group) ||
-        !encode_pool_map<T>(&tk, x.k_pool, rows, D) || !encode_pool_map<T>(&tv, x.v_pool, rows, D))
+        !encode_pool_map<T>(&tk, x.k_pool, rows, D) || !encode_pool_map_3d<T>(&tv, x.v_pool, rows, D))
         return cudaErrorNotSupported;
     auto kernel = chunk_attention_kernel<T, D, SPLIT_P>;
     int dev = 0;
