@@ -1030,9 +1030,11 @@ pkv_status pkv_paged_attention_chunk(const pkv_pool* pool, const void* q, int32_
     p.block_size = pool->block_size;
     p.block_tables = block_tables;
     p.max_blocks_per_seq = max_blocks_per_seq;
-    // the kernel takes maxima before scaling, which a positive scale allows
-    p.scale_log2 = (scale == 0.f ? 1.f : std::fabs(scale)) * 1.4426950408889634f;
-    p.pre_scale = scale > 0.f ? 1.f : scale < 0.f ? -1.f : 0.f;
+    // the kernel takes maxima before scaling, which a positive scale allows: a negative one
+    // negates the product instead, and a zero one becomes so small that every weight is 1
+    const float size = std::fabs(scale) * 1.4426950408889634f;
+    p.scale_log2 = size > 0.f ? size : 1e-30f;
+    p.negate = scale < 0.f;
     p.out = out;
     p.out_dtype = out_dtype;
     p.header = pl.header;

@@ -14,7 +14,7 @@
 // SM, take pieces from that list in order until it is empty.  Twelve warps, fixed roles:
 //   0-3, 4-7  softmax of tile 0 and of tile 1, and their output
 //   8         takes the next piece; tensor copies of K and V pages into a ring of stages
-//   9, 11     one lane each issues the MMAs of tile 0 and of tile 1:
+//   9         one lane issues the MMAs, for the two tiles in turn:
 //               S_t = Q_t . K_j^T            128 x 128 in tensor memory
 //               O_t += P_t . V_j             P_t written over S_t by the softmax
 //             so that one tile's softmax runs while the tensor cores work for the other.
@@ -22,6 +22,7 @@
 //             past the last position the piece may see (they may hold anything; their
 //             weights are zero, and 0 * NaN is not)
 //   10        tensor copies of the query tiles
+//   11        none (fills the warpgroup)
 // The reference maximum of a row is raised only when a step's maximum exceeds it by more
 // than 8 in base 2, so O is rescaled rarely; every term of a row uses the same reference.
 // P enters its product rounded to the pool's type (relative error 2^-9 bf16, 2^-12 fp16 per
@@ -53,7 +54,7 @@ struct ChunkSmem {
     static constexpr int Q_OFF = 0;
     static constexpr int KV_OFF = 2 * TILE;
     static constexpr int BAR_OFF = KV_OFF + STAGES * TILE;
-    static constexpr int NBARS = 2 * STAGES + 16;
+    static constexpr int NBARS = 2 * STAGES + 18;
     static constexpr int PIECE_OFF = BAR_OFF + ((NBARS * 8 + 15) / 16) * 16;
     static constexpr int TMEM_SLOT_OFF = PIECE_OFF + 2 * 32;
     static constexpr int BYTES = TMEM_SLOT_OFF + 16 + 1024;  // + alignment slack
@@ -130,6 +131,95 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return v;
 }
 
+// One step of a row: its 128 scores from tensor memory at s_t, the running reference m_ref and
+// the sum (in four parts), its O at o_t scaled where the reference rose, and its weights
+// written over the scores, the halves handed on at bar_lo and bar_hi.
+template <typename T, int D, bool SPLIT_P, bool EDGE>
+__device__ __forceinline__ void softmax_step(uint32_t s_t, uint32_t o_t, int seen, bool has_o,
+                                             float scale_log2, float& m_ref, uint64_t (&sum2)[2],
+                                             uint32_t bar_lo, uint32_t bar_hi) {
+    constexpr int N = CHUNK_TILE, HALF = N / 2;
+    const int lane = threadIdx.x & 31;
+    uint32_t raw[N];
+    float top[8];  // eight chains of three-input maxima
+    umma::ld32_async(s_t, raw);
+    umma::ld32_async(s_t + 32, raw + 32);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        umma::wait_ld(raw + h * HALF);
+        umma::wait_ld(raw + h * HALF + 32);
+        if (h == 0) {  // the second half arrives while the first is looked at
+            umma::ld32_async(s_t + HALF, raw + HALF);
+            umma::ld32_async(s_t + HALF + 32, raw + HALF + 32);
+        }
+        if (EDGE) {
+#pragma unroll
+            for (int k = h * HALF; k < (h + 1) * HALF; ++k)
+                if (k >= seen) raw[k] = 0xff800000u;  // -inf
+        }
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+            const int k0 = h * HALF + c;
+            if (h == 0) top[c] = __uint_as_float(raw[k0]);
+#pragma unroll
+            for (int k = h == 0 ? k0 + 8 : k0; k + 8 < (h + 1) * HALF; k += 16)
+                top[c] = max3(top[c], __uint_as_float(raw[k]), __uint_as_float(raw[k + 8]));
+            if (h == 0) top[c] = fmaxf(top[c], __uint_as_float(raw[HALF - 8 + c]));
+        }
+    }
+    const float cm = max3(max3(top[0], top[1], top[2]), max3(top[3], top[4], top[5]), fmaxf(top[6], top[7])) *
+                     scale_log2;
+    const bool need = cm > m_ref + CHUNK_RESCALE_LOG2;
+    float alpha = 1.f;
+    if (need) {
+        alpha = fast_exp2(m_ref - cm);
+        m_ref = cm;
+    }
+    const float neg = m_ref == -INFINITY ? 0.f : -m_ref;
+    const uint64_t scale2 = pack2(scale_log2, scale_log2), neg2 = pack2(neg, neg);
+    sum2[0] = mul2(sum2[0], pack2(alpha, alpha));
+    sum2[1] = mul2(sum2[1], pack2(alpha, alpha));
+#pragma unroll
+    for (int c = 0; c < N; c += 32) {
+        uint32_t hi[16], lo[16];
+#pragma unroll
+        for (int k = 0; k < 32; k += 2) {
+            float a, b;
+            unpack2(fma2(pack2(__uint_as_float(raw[c + k]), __uint_as_float(raw[c + k + 1])), scale2, neg2), a, b);
+            a = fast_exp2(a);
+            b = fast_exp2(b);
+            sum2[(k >> 1) & 1] = add2(sum2[(k >> 1) & 1], pack2(a, b));
+            hi[k / 2] = Mma<T>::pack(a, b);
+            if (SPLIT_P) lo[k / 2] = Mma<T>::pack(a - Mma<T>::round_trip(a), b - Mma<T>::round_trip(b));
+        }
+        umma::st16(s_t + c / 2, hi);
+        if (SPLIT_P) umma::st16(s_t + HALF + c / 2, lo);
+        if (c == HALF - 32) {
+            // rows whose reference rose: scale their O (complete through the step before:
+            // this step's S was committed after that P.V)
+            if (has_o && __any_sync(FULL_MASK, need)) {
+#pragma unroll
+                for (int d = 0; d < D; d += 16) {
+                    float o[16];
+                    umma::ld16(o_t + d, o);
+                    uint32_t w[16];
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) w[k] = __float_as_uint(o[k] * alpha);
+                    umma::st16(o_t + d, w);
+                }
+            }
+            umma::wait_st();
+            umma::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar_lo);
+        }
+    }
+    umma::wait_st();
+    umma::fence_before_sync();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar_hi);
+}
+
 template <typename T, int D, bool SPLIT_P>
 __global__ void __launch_bounds__(CHUNK_THREADS, 1)
 chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
@@ -137,10 +227,11 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
                        const __grid_constant__ CUtensorMap tmap_v, const ChunkParams p) {
     using L = ChunkSmem<D>;
     constexpr int NS = L::STAGES, KS = D / 16;
-    constexpr int KV_WARP = 8, MMA_WARP = 9, Q_WARP = 10;  // and the second tile's MMAs: 11
-    constexpr int CONSUMERS = 8 + 3;  // arrivals that free a slot of the piece ring
+    constexpr int KV_WARP = 8, MMA_WARP = 9, Q_WARP = 10, IDLE_WARP = 11;
+    constexpr int CONSUMERS = 8 + 2;  // arrivals that free a slot of the piece ring
     constexpr uint32_t FMT = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
     constexpr uint32_t IDESC_S = umma::idesc_f16(FMT, false, 128, CHUNK_TILE);
+    const uint32_t idesc_s = IDESC_S | (p.negate ? umma::IDESC_NEGATE_A : 0u);
     constexpr uint32_t IDESC_O = umma::idesc_f16(FMT, true, 128, D);
 
     extern __shared__ __align__(128) unsigned char smem_raw[];
@@ -148,19 +239,19 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sbase = smem_addr(smem);
     const uint32_t q_s = sbase + L::Q_OFF, ring = sbase + L::KV_OFF, bar0 = sbase + L::BAR_OFF;
-    // barriers: K / V stage landed and free; Q tile landed and free; S tile ready; P tile
-    // written; a piece's last P.V done; piece published and read; every MMA done
+    // barriers: K / V stage landed and free; Q tile landed and free; S tile ready; a piece's
+    // last P.V done; piece published and read; every MMA done; half of a P tile written
     auto kv_full = [&](int st) { return bar0 + 8 * st; };
     auto kv_empty = [&](int st) { return bar0 + 8 * (NS + st); };
     constexpr int NB = 2 * NS;
     auto q_full = [&](int t) { return bar0 + 8 * (NB + t); };
     auto q_empty = [&](int t) { return bar0 + 8 * (NB + 2 + t); };
     auto s_full = [&](int t) { return bar0 + 8 * (NB + 4 + t); };
-    auto p_full = [&](int t) { return bar0 + 8 * (NB + 6 + t); };
-    auto pv_done = [&](int t) { return bar0 + 8 * (NB + 8 + t); };
-    auto piece_full = [&](int i) { return bar0 + 8 * (NB + 10 + i); };
-    auto piece_empty = [&](int i) { return bar0 + 8 * (NB + 12 + i); };
-    auto all_done = [&](int t) { return bar0 + 8 * (NB + 14 + t); };
+    auto pv_done = [&](int t) { return bar0 + 8 * (NB + 6 + t); };
+    auto piece_full = [&](int i) { return bar0 + 8 * (NB + 8 + i); };
+    auto piece_empty = [&](int i) { return bar0 + 8 * (NB + 10 + i); };
+    const uint32_t all_done = bar0 + 8 * (NB + 12);
+    auto p_full = [&](int t, int h) { return bar0 + 8 * (NB + 14 + 2 * t + h); };
     ChunkPiece* pieces = reinterpret_cast<ChunkPiece*>(smem + L::PIECE_OFF);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::TMEM_SLOT_OFF);
 
@@ -170,18 +261,19 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
     if (threadIdx.x == 0) {
         for (int st = 0; st < NS; ++st) {
             mbar_init(kv_full(st), 1);
-            mbar_init(kv_empty(st), 2);
+            mbar_init(kv_empty(st), 1);
         }
         for (int t = 0; t < 2; ++t) {
             mbar_init(q_full(t), 1);
             mbar_init(q_empty(t), 1);
             mbar_init(s_full(t), 1);
-            mbar_init(p_full(t), 4);
+            mbar_init(p_full(t, 0), 4);
+            mbar_init(p_full(t, 1), 4);
             mbar_init(pv_done(t), 1);
-            mbar_init(all_done(t), 1);
             mbar_init(piece_full(t), 1);
             mbar_init(piece_empty(t), CONSUMERS);
         }
+        mbar_init(all_done, 1);
         mbar_init_fence();
     }
     if (warp == MMA_WARP) umma::alloc(smem_addr(tmem_slot), L::TMEM_COLS);
@@ -307,92 +399,106 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
         }
         for (int t = 0; t < 2; ++t)
             if (used[t] > 0) mbar_wait_short(q_full(t), (used[t] - 1) & 1);
-    } else if (warp == MMA_WARP || warp == MMA_WARP + 2) {
+    } else if (warp == MMA_WARP) {
         regs_dec<CHUNK_REGS_OTHERS>();
-        // ---- MMA issue for tile t.  Every stage is released by both of these warps.
-        const int t = warp == MMA_WARP ? 0 : 1;
-        const uint32_t s_t = tmem + t * CHUNK_TILE, o_t = tmem + L::O_COL + t * D;
-        const uint64_t q_desc = umma::sw128_desc(q_s + t * L::TILE, 16, 1024);
-        int st = 0, used = 0, steps = 0, all_steps = 0;  // next stage; Q tiles and P tiles taken
-        uint32_t total = 0;               // stages of all pieces so far
-        uint32_t phase = 0;               // of that stage
-        auto landed = [&] { return mbar_wait_short(kv_full(st), phase); };
-        auto advance = [&] {
-            if (++st == NS) {
-                st = 0;
-                phase ^= 1;
-            }
-        };
-        auto issue_s = [&] {  // S over the P just read: one thread's MMAs run in issue order
+        // ---- MMA issue, the two tiles in turn: one thread for both, because MMAs issued by
+        // two threads are interleaved, both tiles' scores are then complete at the same time
+        // and their exponentials compete for the same units
+        uint32_t total = 0;               // stages of the pieces so far
+        int used[2] = {0, 0};             // Q tiles taken
+        int steps[2] = {0, 0};            // P tiles taken
+        auto issue_s = [&](int t, int st) {  // S over the P just read: MMAs run in issue order
             const uint64_t k_desc = umma::sw128_desc(ring + st * L::TILE, 16, 1024);
+            const uint64_t q_desc = umma::sw128_desc(q_s + t * L::TILE, 16, 1024);
 #pragma unroll
             for (int kk = 0; kk < KS; ++kk) {
                 const uint32_t off = ((kk >> 2) * L::BOX + (kk & 3) * 32) >> 4;  // start address field
-                umma::mma_f16(s_t, q_desc + off, k_desc + off, IDESC_S, kk > 0 ? 1u : 0u);
+                umma::mma_f16(tmem + t * CHUNK_TILE, q_desc + off, k_desc + off, idesc_s, kk > 0 ? 1u : 0u);
             }
             umma::commit(s_full(t));  // also says that every P.V before is done
         };
-        auto issue_pv = [&](bool first) {
+        auto issue_pv = [&](int t, int st, bool first) -> bool {
             // V is N-major: 64-element columns 2048 apart, 8-token groups 1024, and a K step
-            // is one copy's 16 tokens
+            // is one copy's 16 tokens.  The first half's products run while the softmax still
+            // works on the second half.
             const uint64_t v_desc = umma::sw128_desc(ring + st * L::TILE, CHUNK_TOKENS * 128, 1024);
+            const uint32_t s_t = tmem + t * CHUNK_TILE, o_t = tmem + L::O_COL + t * D;
+            const uint32_t parity = steps[t]++ & 1;
 #pragma unroll
-            for (int kk = 0; kk < CHUNK_TILE / 16; ++kk) {
-                const uint64_t bv = v_desc + (kk * CHUNK_TOKENS * D * 2 >> 4);
-                umma::mma_f16_tmem_a(o_t, s_t + kk * 8, bv, IDESC_O, (!first || kk > 0) ? 1u : 0u);
-                if (SPLIT_P) umma::mma_f16_tmem_a(o_t, s_t + CHUNK_TILE / 2 + kk * 8, bv, IDESC_O, 1u);
+            for (int h = 0; h < 2; ++h) {
+                if (!mbar_wait_short(p_full(t, h), parity)) return false;
+                umma::fence_after_sync();
+#pragma unroll
+                for (int k = 4 * h; k < 4 * h + 4; ++k) {
+                    const uint64_t bv = v_desc + (k * CHUNK_TOKENS * D * 2 >> 4);
+                    umma::mma_f16_tmem_a(o_t, s_t + k * 8, bv, IDESC_O, (!first || k > 0) ? 1u : 0u);
+                    if (SPLIT_P) umma::mma_f16_tmem_a(o_t, s_t + CHUNK_TILE / 2 + k * 8, bv, IDESC_O, 1u);
+                }
             }
+            return true;
         };
         ChunkPiece pc;
         for (int i = 0; next_piece(i, pc); ++i) {
             const int n = pc.kt1 - pc.kt0;
             if (n <= 0) continue;
-            if (t == 1 && pc.queries <= QPT) {  // no second tile: release the stages as they land
-                for (int k = 0; k < 2 * n && ok; ++k) {
-                    ok = __all_sync(FULL_MASK, landed());
-                    if (ok && lane == 0) mbar_arrive(kv_empty(st));
-                    advance();
+            const bool two = pc.queries > QPT;
+            int st = (int)(total % NS);  // next stage and its phase
+            uint32_t phase = (total / NS) & 1;
+            auto landed = [&] { return mbar_wait_short(kv_full(st), phase); };
+            auto advance = [&] {
+                if (++st == NS) {
+                    st = 0;
+                    phase ^= 1;
                 }
-                total += 2 * n;
-                if (!ok) break;
-                continue;
-            }
+            };
             if (umma::elect_one()) {
-                ok = mbar_wait_short(q_full(t), used & 1) && landed();
+                ok = landed();
+                if (ok) ok = mbar_wait_short(q_full(0), used[0] & 1);
                 if (ok) {
                     umma::fence_after_sync();
-                    issue_s();
-                    if (n == 1) umma::commit(q_empty(t));
+                    issue_s(0, st);
+                    if (n == 1) umma::commit(q_empty(0));
+                    if (two) {
+                        ok = mbar_wait_short(q_full(1), used[1] & 1);
+                        umma::fence_after_sync();
+                        if (ok) issue_s(1, st);
+                        if (n == 1) umma::commit(q_empty(1));
+                    }
                     umma::commit(kv_empty(st));
                     advance();
                 }
 #pragma unroll 1
                 for (int j = 0; j < n - 1 && ok; ++j) {
-                    ok = landed() && mbar_wait_short(p_full(t), steps & 1);
-                    if (!ok) break;
-                    ++steps;
-                    umma::fence_after_sync();
-                    issue_pv(j == 0);
                     const int v_st = st;
-                    advance();
                     ok = landed();
                     if (!ok) break;
+                    advance();
+                    ok = issue_pv(0, v_st, j == 0) && landed();
+                    if (!ok) break;
                     umma::fence_after_sync();
-                    issue_s();
-                    if (j == n - 2) umma::commit(q_empty(t));
-                    umma::commit(kv_empty(v_st));
+                    issue_s(0, st);
+                    if (j == n - 2) umma::commit(q_empty(0));
+                    if (two) {
+                        ok = issue_pv(1, v_st, j == 0);
+                        if (!ok) break;
+                        umma::commit(kv_empty(v_st));
+                        issue_s(1, st);
+                        if (j == n - 2) umma::commit(q_empty(1));
+                    } else {
+                        umma::commit(kv_empty(v_st));
+                    }
                     umma::commit(kv_empty(st));
                     advance();
                 }
             }
-            ++used;
+            ++used[0];
+            used[1] += two;
             ok = __all_sync(FULL_MASK, ok);
             if (!ok) break;
-            // every lane's cursor to the piece's last stage, V's
             total += 2 * n;
-            st = (int)((total - 1) % NS);
+            st = (int)((total - 1) % NS);  // every lane: the piece's last stage, V's
             phase = ((total - 1) / NS) & 1;
-            if (chunk_has_tail(pc)) {  // both warps may zero the same rows: the values agree
+            if (chunk_has_tail(pc)) {
                 ok = __all_sync(FULL_MASK, landed());
                 if (!ok) break;
                 const int r0 = pc.lim0 + pc.queries - 1 - (pc.kt1 - 1) * CHUNK_TILE;
@@ -407,25 +513,24 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
                 __syncwarp();
             }
             if (umma::elect_one()) {
-                ok = landed() && mbar_wait_short(p_full(t), (all_steps + n - 1) & 1);
-                if (ok) {
-                    umma::fence_after_sync();
-                    issue_pv(n == 1);
-                    umma::commit(pv_done(t));
-                    umma::commit(kv_empty(st));
+                ok = landed() && issue_pv(0, st, n == 1);
+                if (ok) umma::commit(pv_done(0));
+                if (ok && two) {
+                    ok = issue_pv(1, st, n == 1);
+                    if (ok) umma::commit(pv_done(1));
                 }
+                if (ok) umma::commit(kv_empty(st));
             }
-            all_steps += n;
-            steps = all_steps;
-            advance();
             ok = __all_sync(FULL_MASK, ok);
             if (!ok) break;
         }
         if (umma::elect_one()) {
-            umma::commit(all_done(t));
-            if (!mbar_wait_short(all_done(t), 0)) ok = false;
+            umma::commit(all_done);
+            if (!mbar_wait_short(all_done, 0)) ok = false;
         }
         __syncwarp();
+    } else if (warp == IDLE_WARP) {
+        regs_dec<CHUNK_REGS_OTHERS>();
     } else {
         regs_inc<CHUNK_REGS_SOFTMAX>();
         // ---- softmax and output of tile t: this thread's row is r
@@ -448,77 +553,17 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
                 if (!ok) break;
                 if (busy) {
                     umma::fence_after_sync();
-                    uint32_t raw[CHUNK_TILE];
-#pragma unroll
-                    for (int c = 0; c < CHUNK_TILE; c += 32) umma::ld32_async(s_t + c, raw + c);
-#pragma unroll
-                    for (int c = 0; c < CHUNK_TILE; c += 32) umma::wait_ld(raw + c);
-                    if (p.pre_scale != 1.f) {
-#pragma unroll
-                        for (int k = 0; k < CHUNK_TILE; ++k)
-                            raw[k] = __float_as_uint(__uint_as_float(raw[k]) * p.pre_scale);
-                    }
                     const int seen = lim - (pc.kt0 + j) * CHUNK_TILE;  // columns this row may see
-                    if (__any_sync(FULL_MASK, seen < CHUNK_TILE)) {
-#pragma unroll
-                        for (int k = 0; k < CHUNK_TILE; ++k)
-                            if (k >= seen) raw[k] = 0xff800000u;  // -inf
-                    }
-                    float top[4];  // four chains, three-input maxima
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        top[c] = __uint_as_float(raw[c]);
-#pragma unroll
-                        for (int k = c + 4; k + 4 < CHUNK_TILE; k += 8)
-                            top[c] = max3(top[c], __uint_as_float(raw[k]), __uint_as_float(raw[k + 4]));
-                        top[c] = fmaxf(top[c], __uint_as_float(raw[CHUNK_TILE - 4 + c]));
-                    }
-                    const float cm = max3(top[0], top[1], fmaxf(top[2], top[3])) * p.scale_log2;
-                    const bool need = cm > m_ref + CHUNK_RESCALE_LOG2;
-                    float alpha = 1.f;
-                    if (need) {
-                        alpha = fast_exp2(m_ref - cm);
-                        m_ref = cm;
-                    }
-                    const float neg = m_ref == -INFINITY ? 0.f : -m_ref;
-                    const uint64_t scale2 = pack2(p.scale_log2, p.scale_log2), neg2 = pack2(neg, neg);
-                    sum2[0] = mul2(sum2[0], pack2(alpha, alpha));
-                    sum2[1] = mul2(sum2[1], pack2(alpha, alpha));
-#pragma unroll
-                    for (int c = 0; c < CHUNK_TILE; c += 32) {
-                        uint32_t hi[16], lo[16];
-#pragma unroll
-                        for (int k = 0; k < 32; k += 2) {
-                            float a, b;
-                            unpack2(fma2(pack2(__uint_as_float(raw[c + k]), __uint_as_float(raw[c + k + 1])),
-                                         scale2, neg2), a, b);
-                            a = fast_exp2(a);
-                            b = fast_exp2(b);
-                            sum2[(k >> 1) & 1] = add2(sum2[(k >> 1) & 1], pack2(a, b));
-                            hi[k / 2] = Mma<T>::pack(a, b);
-                            if (SPLIT_P)
-                                lo[k / 2] = Mma<T>::pack(a - Mma<T>::round_trip(a), b - Mma<T>::round_trip(b));
-                        }
-                        umma::st16(s_t + c / 2, hi);
-                        if (SPLIT_P) umma::st16(s_t + CHUNK_TILE / 2 + c / 2, lo);
-                    }
-                    // rows whose reference rose: scale their O (complete through step j - 1: this
-                    // step's S was committed after that P.V)
-                    if (j > 0 && __any_sync(FULL_MASK, need)) {
-#pragma unroll
-                        for (int c = 0; c < D; c += 32) {
-                            float o[32];
-                            umma::ld32(o_t + c, o);
-#pragma unroll
-                            for (int k = 0; k < 32; ++k) o[k] *= alpha;
-                            umma::st32(o_t + c, o);
-                        }
-                    }
-                    umma::wait_st();
+                    if (__any_sync(FULL_MASK, seen < CHUNK_TILE))
+                        softmax_step<T, D, SPLIT_P, true>(s_t, o_t, seen, j > 0, p.scale_log2, m_ref, sum2,
+                                                          p_full(t, 0), p_full(t, 1));
+                    else
+                        softmax_step<T, D, SPLIT_P, false>(s_t, o_t, seen, j > 0, p.scale_log2, m_ref, sum2,
+                                                           p_full(t, 0), p_full(t, 1));
+                } else if (lane == 0) {  // rows of no query: whatever S left there
+                    mbar_arrive(p_full(t, 0));
+                    mbar_arrive(p_full(t, 1));
                 }
-                umma::fence_before_sync();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(p_full(t));
             }
             if (!ok) break;
             if (n > 0) {

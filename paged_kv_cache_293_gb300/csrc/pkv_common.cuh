@@ -183,7 +183,7 @@ struct ChunkParams {
     const int32_t* block_tables;
     int32_t max_blocks_per_seq;
     float scale_log2;   // |scale| * log2(e), positive
-    float pre_scale;    // 1, -1 for a negative scale, 0 for a zero one
+    int32_t negate;     // the scale was negative: the scores are taken negated
     void* out;          // [T][Hq][D]
     int32_t out_dtype;
     int32_t* header;
