@@ -1050,7 +1050,7 @@ pkv_status pkv_paged_attention_chunk(const pkv_pool* pool, const void* q, int32_
     if (e == cudaErrorNotSupported) return PKV_ERR_UNSUPPORTED;
     if (e != cudaSuccess) return PKV_ERR_CUDA;
     if (c.partial_rows == 0) return PKV_OK;
-    const int64_t merge_ctas = std::min<int64_t>(4 * (int64_t)sms, ((int64_t)num_tokens * num_q_heads + 7) / 8);
+    const int64_t merge_ctas = std::min<int64_t>(16 * (int64_t)sms, ((int64_t)num_tokens * num_q_heads + 7) / 8);
     return pkv::launch_chunk_merge(p, (int)merge_ctas, s) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 

@@ -57,37 +57,48 @@ __device__ __forceinline__ int tile_steps(const int4& tile) {
 
 }  // namespace
 
+// One CTA: it is a chain of short dependent steps (load the lengths, sum, search, choose, sum,
+// write), 1024 requests and 1024 tiles at a time, whose arrays stay in shared memory when all
+// of the batch fits into one round and go to the workspace when it does not.
 __global__ void __launch_bounds__(PLAN_THREADS) chunk_plan_kernel(const ChunkPlanParams p) {
     __shared__ int4 warp_sums[32];
     __shared__ int max_steps_s;
     __shared__ float est_s[32];
+    __shared__ int start_s[PLAN_THREADS + 1], tile_start_s[PLAN_THREADS + 1], ctx_s[PLAN_THREADS];
+    __shared__ int4 tiles_s[PLAN_THREADS];  // this round's tiles
+    __shared__ int first_s[PLAN_THREADS];   // pieces up to and with each of them
+    __shared__ int4 base_s[PLAN_THREADS];   // pieces, partial rows, cut items, their rows before it
     // the attention kernel may set itself up meanwhile; it waits for this grid's end
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int QT = 2 * (128 / p.group);  // queries per tile
+    const bool few = p.num_seqs <= PLAN_THREADS;
+    int* tile_start = few ? tile_start_s : p.tile_start;
+    const int* starts = few ? start_s : p.query_start;
+    const int* ctxs = few ? ctx_s : p.context_lens;
     if (tid == 0) {
-        p.tile_start[0] = 0;
+        tile_start[0] = 0;
         max_steps_s = 0;
     }
 
     // ---- tiles of each request
-    bool bad = false;
     int carry = 0;
     for (int s0 = 0; s0 < p.num_seqs; s0 += PLAN_THREADS) {
         const int s = s0 + tid;
         int nt = 0;
+        bool bad = false;
         if (s < p.num_seqs) {
-            const int a = p.query_start[s], b = p.query_start[s + 1];
-            if (a < 0 || b < a || b > p.num_tokens)
-                bad = true;
-            else
-                nt = (int)(((long long)b - a + QT - 1) / QT);
+            const int a = p.query_start[s], b = p.query_start[s + 1], c = p.context_lens[s];
+            if (few) {
+                start_s[s] = a;
+                start_s[s + 1] = b;
+                ctx_s[s] = c;
+            }
+            bad = a < 0 || b < a || b > p.num_tokens;
+            if (!bad) nt = (int)(((long long)b - a + QT - 1) / QT);
         }
-        int4 total;
-        const int4 v = block_scan4(make_int4(nt, 0, 0, 0), warp_sums, &total);
-        // starts that do not ascend could sum past the list: such a batch is refused below
-        if (s < p.num_seqs) p.tile_start[s + 1] = carry + v.x;
-        carry += total.x;
+        // starts that do not ascend could sum past the list: such a batch is refused
         if (__syncthreads_or(bad)) {
             if (tid == 0) {
                 set_error(p.err, PKV_DEVERR_POSITION);
@@ -95,8 +106,14 @@ __global__ void __launch_bounds__(PLAN_THREADS) chunk_plan_kernel(const ChunkPla
             }
             return;
         }
+        int4 total;
+        const int4 v = block_scan4(make_int4(nt, 0, 0, 0), warp_sums, &total);
+        if (s < p.num_seqs) tile_start[s + 1] = carry + v.x;
+        carry += total.x;
     }
     const int num_tiles = carry;
+    int4* tiles = num_tiles <= PLAN_THREADS ? tiles_s : p.tiles;
+    __syncthreads();
 
     // ---- one record per tile, the longest of a request first
     const long long cap = min((long long)p.max_blocks_per_seq * p.block_size, (long long)p.max_context_len);
@@ -105,20 +122,21 @@ __global__ void __launch_bounds__(PLAN_THREADS) chunk_plan_kernel(const ChunkPla
         int lo = 0, hi = p.num_seqs - 1;
         while (lo < hi) {  // first request whose tiles end past ti
             const int mid = (lo + hi) >> 1;
-            if (p.tile_start[mid + 1] > ti) hi = mid; else lo = mid + 1;
+            if (tile_start[mid + 1] > ti) hi = mid; else lo = mid + 1;
         }
-        const int nq = p.query_start[lo + 1] - p.query_start[lo];
-        int ctx = p.context_lens[lo];
+        const int nq = starts[lo + 1] - starts[lo];
+        int ctx = ctxs[lo];
         if (ctx < 0 || ctx > cap) {
             set_error(p.err, PKV_DEVERR_CONTEXT);
             ctx = ctx < 0 ? 0 : (int)cap;
         }
-        const int j0 = (p.tile_start[lo + 1] - 1 - ti) * QT;
+        const int j0 = (tile_start[lo + 1] - 1 - ti) * QT;
         const int4 tile = make_int4(lo, j0, min(QT, nq - j0), ctx - nq + 1 + j0);
-        p.tiles[ti] = tile;
+        tiles[ti] = tile;
         steps = max(steps, tile_steps(tile));
     }
-    atomicMax(&max_steps_s, steps);
+    steps = __reduce_max_sync(FULL_MASK, steps);
+    if (lane == 0) atomicMax(&max_steps_s, steps);
     __syncthreads();
     const int max_steps = max_steps_s;
 
@@ -130,7 +148,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) chunk_plan_kernel(const ChunkPla
         float all = 0.f;
         int n_pieces = 0, rows = 0, cuts = 0;
         for (int ti = lane; ti < num_tiles; ti += 32) {
-            const int4 tile = p.tiles[ti];
+            const int4 tile = tiles[ti];
             const int n = tile_steps(tile), pc = n > c ? (n + c - 1) / c : 1;
             all += (float)n + F * (float)pc;
             n_pieces += pc;
@@ -140,12 +158,10 @@ __global__ void __launch_bounds__(PLAN_THREADS) chunk_plan_kernel(const ChunkPla
             }
         }
 #pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) {
-            all += __shfl_xor_sync(FULL_MASK, all, o);
-            n_pieces += __shfl_xor_sync(FULL_MASK, n_pieces, o);
-            rows += __shfl_xor_sync(FULL_MASK, rows, o);
-            cuts += __shfl_xor_sync(FULL_MASK, cuts, o);
-        }
+        for (int o = 16; o >= 1; o >>= 1) all += __shfl_xor_sync(FULL_MASK, all, o);
+        n_pieces = __reduce_add_sync(FULL_MASK, n_pieces);
+        rows = __reduce_add_sync(FULL_MASK, rows);
+        cuts = __reduce_add_sync(FULL_MASK, cuts);
         if (lane == 0) {
             const float ctas = (float)p.num_sms, H = (float)p.num_kv_heads;
             const float mean = all * H / ctas;
@@ -157,58 +173,69 @@ __global__ void __launch_bounds__(PLAN_THREADS) chunk_plan_kernel(const ChunkPla
             est_s[warp] = est;
         }
         __syncthreads();
-        int best = 0;
-        for (int w = 1; w < 32; ++w)
-            if (est_s[w] < est_s[best]) best = w;
+        // the smallest estimate, the fewest pieces among equals (estimates are not negative, so
+        // their bits order like their values)
+        const unsigned mine = __float_as_uint(est_s[lane]), least = __reduce_min_sync(FULL_MASK, mine);
+        const int best = __ffs(__ballot_sync(FULL_MASK, mine == least)) - 1;
         cut = (max_steps + best) / (best + 1);
     }
 
     // ---- the pieces, tile by tile, the heads of a tile behind one another
+    const int H = p.num_kv_heads;
     int4 base = make_int4(0, 0, 0, 0);  // pieces, partial rows, cut items, their rows
     for (int t0 = 0; t0 < num_tiles; t0 += PLAN_THREADS) {
         const int ti = t0 + tid;
         int4 tile = make_int4(0, 0, 0, 0);
-        int n = 0, pc = 0;
+        int pc = 0;
         if (ti < num_tiles) {
-            tile = p.tiles[ti];
-            n = tile_steps(tile);
+            tile = tiles[ti];
+            const int n = tile_steps(tile);
             pc = n > cut ? (n + cut - 1) / cut : 1;
         }
-        const int H = p.num_kv_heads, R = tile.z * p.group;
+        const int R = tile.z * p.group;
         const int4 mine = make_int4(H * pc, pc > 1 ? H * pc * R : 0, pc > 1 ? H : 0, pc > 1 ? H * R : 0);
         int4 total;
         const int4 v = block_scan4(mine, warp_sums, &total);
-        if (pc > 0) {
-            const int first = base.x + v.x - mine.x, row0 = base.y + v.y - mine.y;
-            const int item0 = base.z + v.z - mine.z, mrow0 = base.w + v.w - mine.w;
-            const int token = p.query_start[tile.x] + tile.y;
-            for (int h = 0; h < H; ++h) {
-                for (int r = 0; r < pc; ++r) {
-                    ChunkPiece x;
-                    x.token = token;
-                    x.kv_head = h;
-                    x.queries = tile.z;
-                    x.lim0 = tile.w;
-                    x.seq = tile.x;
-                    x.kt0 = (int)((long long)n * r / pc);
-                    x.kt1 = (int)((long long)n * (r + 1) / pc);
-                    x.part_row = pc > 1 ? row0 + (h * pc + r) * R : -1;
-                    p.pieces[first + h * pc + r] = x;
-                }
-                if (pc > 1) {
-                    ChunkMerge m;
-                    m.token = token;
-                    m.kv_head = h;
-                    m.rows = R;
-                    m.parts = pc;
-                    m.part_row = row0 + h * pc * R;
-                    m.first = mrow0 + h * R;
-                    m.pad0 = m.pad1 = 0;
-                    p.merges[item0 + h] = m;
-                }
+        if (tiles != tiles_s) tiles_s[tid] = tile;
+        first_s[tid] = v.x;
+        base_s[tid] = make_int4(base.x + v.x - mine.x, base.y + v.y - mine.y, base.z + v.z - mine.z,
+                                base.w + v.w - mine.w);
+        __syncthreads();
+        const int live = min(PLAN_THREADS, num_tiles - t0);
+        for (int e = tid; e < total.x; e += PLAN_THREADS) {
+            int lo = 0, hi = live - 1;
+            while (lo < hi) {  // first tile whose pieces end past e
+                const int mid = (lo + hi) >> 1;
+                if (first_s[mid] > e) hi = mid; else lo = mid + 1;
+            }
+            const int4 x = tiles_s[lo], at = base_s[lo];
+            const int n = tile_steps(x), parts = n > cut ? (n + cut - 1) / cut : 1, rows = x.z * p.group;
+            const int in_tile = base.x + e - at.x, h = in_tile / parts, r = in_tile - h * parts;
+            const int token = starts[x.x] + x.y;
+            ChunkPiece y;
+            y.token = token;
+            y.kv_head = h;
+            y.queries = x.z;
+            y.lim0 = x.w;
+            y.seq = x.x;
+            y.kt0 = (int)((long long)n * r / parts);
+            y.kt1 = (int)((long long)n * (r + 1) / parts);
+            y.part_row = parts > 1 ? at.y + in_tile * rows : -1;
+            p.pieces[base.x + e] = y;
+            if (parts > 1 && r == 0) {
+                ChunkMerge m;
+                m.token = token;
+                m.kv_head = h;
+                m.rows = rows;
+                m.parts = parts;
+                m.part_row = y.part_row;
+                m.first = at.w + h * rows;
+                m.pad0 = m.pad1 = 0;
+                p.merges[at.z + h] = m;
             }
         }
         base = add4(base, total);
+        __syncthreads();
     }
     if (tid == 0) {
         p.header[0] = base.x;
@@ -227,10 +254,14 @@ __global__ void __launch_bounds__(256) chunk_merge_kernel(const ChunkParams p) {
     const int lane = threadIdx.x & 31;
     const int rows = p.header[2], items = p.header[1];
     for (int g = blockIdx.x * 8 + (threadIdx.x >> 5); g < rows; g += gridDim.x * 8) {
-        int lo = 0, hi = items - 1;
-        while (lo < hi) {  // last item starting at or before g
-            const int mid = (lo + hi + 1) >> 1;
-            if (p.merges[mid].first <= g) lo = mid; else hi = mid - 1;
+        int lo = 0, n = items;  // the last item starting at or before g is one of lo .. lo + n - 1
+        while (n > 1) {         // 32 of them at a time, evenly spread
+            const int step = (n + 31) / 32, at = lo + lane * step;
+            const unsigned before = __ballot_sync(FULL_MASK, at < lo + n && p.merges[at].first <= g);
+            const int k = 31 - __clz(before);  // lane 0's always does
+            const int end = lo + n;
+            lo += k * step;
+            n = min(step, end - lo);
         }
         const ChunkMerge m = p.merges[lo];
         const int r = g - m.first;
@@ -275,8 +306,16 @@ __global__ void __launch_bounds__(256) chunk_merge_kernel(const ChunkParams p) {
 }
 
 cudaError_t launch_chunk_plan(const ChunkPlanParams& p, cudaStream_t stream) {
-    chunk_plan_kernel<<<1, PLAN_THREADS, 0, stream>>>(p);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(1);
+    cfg.blockDim = dim3(PLAN_THREADS);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, chunk_plan_kernel, p);
 }
 
 cudaError_t launch_chunk_merge(const ChunkParams& p, int ctas, cudaStream_t stream) {
