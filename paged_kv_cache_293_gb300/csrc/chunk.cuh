@@ -20,7 +20,8 @@
 //             so that one tile's softmax runs while the tensor cores work for the other.
 //             Before a piece's last P.V the warp zeroes the V rows of the last 16-token copy
 //             past the last position the piece may see (they may hold anything; their
-//             weights are zero, and 0 * NaN is not)
+//             weights are zero, and 0 * NaN is not).  Of a piece with one tile of queries
+//             the even and the odd steps' scores take the two tiles' places
 //   10        tensor copies of the query tiles
 //   11        none (fills the warpgroup)
 // The reference maximum of a row is raised only when a step's maximum exceeds it by more
@@ -54,7 +55,7 @@ struct ChunkSmem {
     static constexpr int Q_OFF = 0;
     static constexpr int KV_OFF = 2 * TILE;
     static constexpr int BAR_OFF = KV_OFF + STAGES * TILE;
-    static constexpr int NBARS = 2 * STAGES + 18;
+    static constexpr int NBARS = 2 * STAGES + 25;
     static constexpr int PIECE_OFF = BAR_OFF + ((NBARS * 8 + 15) / 16) * 16;
     static constexpr int TMEM_SLOT_OFF = PIECE_OFF + 2 * 32;
     static constexpr int BYTES = TMEM_SLOT_OFF + 16 + 1024;  // + alignment slack
@@ -132,12 +133,14 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 }
 
 // One step of a row: its 128 scores from tensor memory at s_t, the running reference m_ref and
-// the sum (in four parts), its O at o_t scaled where the reference rose, and its weights
-// written over the scores, the halves handed on at bar_lo and bar_hi.
+// the sum (in four parts), its O at o_t scaled where the reference rose (once phase_o of
+// bar_o says that the products before are done; 0: known), and its weights written over the
+// scores, the halves handed on at bar_lo and bar_hi.
 template <typename T, int D, bool SPLIT_P, bool EDGE>
-__device__ __forceinline__ void softmax_step(uint32_t s_t, uint32_t o_t, int seen, bool has_o,
+__device__ __forceinline__ bool softmax_step(uint32_t s_t, uint32_t o_t, int seen, bool has_o,
                                              float scale_log2, float& m_ref, uint64_t (&sum2)[2],
-                                             uint32_t bar_lo, uint32_t bar_hi) {
+                                             uint32_t bar_lo, uint32_t bar_hi, uint32_t bar_o,
+                                             uint32_t phase_o) {
     constexpr int N = CHUNK_TILE, HALF = N / 2;
     const int lane = threadIdx.x & 31;
     uint32_t raw[N];
@@ -195,9 +198,12 @@ __device__ __forceinline__ void softmax_step(uint32_t s_t, uint32_t o_t, int see
         umma::st16(s_t + c / 2, hi);
         if (SPLIT_P) umma::st16(s_t + HALF + c / 2, lo);
         if (c == HALF - 32) {
-            // rows whose reference rose: scale their O (complete through the step before:
-            // this step's S was committed after that P.V)
+            // rows whose reference rose: scale their O, complete through the step before
             if (has_o && __any_sync(FULL_MASK, need)) {
+                if (bar_o != 0) {
+                    if (!__all_sync(FULL_MASK, mbar_wait_short(bar_o, phase_o & 1))) return false;
+                    umma::fence_after_sync();
+                }
 #pragma unroll
                 for (int d = 0; d < D; d += 16) {
                     float o[16];
@@ -218,6 +224,7 @@ __device__ __forceinline__ void softmax_step(uint32_t s_t, uint32_t o_t, int see
     umma::fence_before_sync();
     __syncwarp();
     if (lane == 0) mbar_arrive(bar_hi);
+    return true;
 }
 
 template <typename T, int D, bool SPLIT_P>
@@ -239,19 +246,26 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sbase = smem_addr(smem);
     const uint32_t q_s = sbase + L::Q_OFF, ring = sbase + L::KV_OFF, bar0 = sbase + L::BAR_OFF;
-    // barriers: K / V stage landed and free; Q tile landed and free; S tile ready; a piece's
-    // last P.V done; piece published and read; every MMA done; half of a P tile written
+    // barriers: K / V stage landed and free; Q tile landed and free; a piece's last P.V
+    // done; piece published and read; every MMA done; the P.V of an even or odd step
+    // of a piece with one tile of queries done (a barrier each: a warp may be a step ahead of
+    // another one, with two products still to come, and one barrier's parity would not tell
+    // them apart)
     auto kv_full = [&](int st) { return bar0 + 8 * st; };
     auto kv_empty = [&](int st) { return bar0 + 8 * (NS + st); };
     constexpr int NB = 2 * NS;
     auto q_full = [&](int t) { return bar0 + 8 * (NB + t); };
     auto q_empty = [&](int t) { return bar0 + 8 * (NB + 2 + t); };
-    auto s_full = [&](int t) { return bar0 + 8 * (NB + 4 + t); };
     auto pv_done = [&](int t) { return bar0 + 8 * (NB + 6 + t); };
     auto piece_full = [&](int i) { return bar0 + 8 * (NB + 8 + i); };
     auto piece_empty = [&](int i) { return bar0 + 8 * (NB + 10 + i); };
     const uint32_t all_done = bar0 + 8 * (NB + 12);
-    auto p_full = [&](int t, int h) { return bar0 + 8 * (NB + 14 + 2 * t + h); };
+    auto pv_step = [&](int b) { return bar0 + 8 * (NB + 4 + b); };
+    // S tile ready and half of a P tile written: i < 2 of tile i, i = 2, 3 of the even and odd
+    // steps of a piece with one tile of queries (barriers of their own, because the second
+    // tile's warps take no part in them)
+    auto s_full = [&](int i) { return bar0 + 8 * (NB + 13 + i); };
+    auto p_full = [&](int i, int h) { return bar0 + 8 * (NB + 17 + 2 * i + h); };
     ChunkPiece* pieces = reinterpret_cast<ChunkPiece*>(smem + L::PIECE_OFF);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::TMEM_SLOT_OFF);
 
@@ -266,10 +280,13 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
         for (int t = 0; t < 2; ++t) {
             mbar_init(q_full(t), 1);
             mbar_init(q_empty(t), 1);
-            mbar_init(s_full(t), 1);
-            mbar_init(p_full(t, 0), 4);
-            mbar_init(p_full(t, 1), 4);
+            for (int i = t; i < 4; i += 2) {
+                mbar_init(s_full(i), 1);
+                mbar_init(p_full(i, 0), 4);
+                mbar_init(p_full(i, 1), 4);
+            }
             mbar_init(pv_done(t), 1);
+            mbar_init(pv_step(t), 1);
             mbar_init(piece_full(t), 1);
             mbar_init(piece_empty(t), CONSUMERS);
         }
@@ -406,27 +423,28 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
         // and their exponentials compete for the same units
         uint32_t total = 0;               // stages of the pieces so far
         int used[2] = {0, 0};             // Q tiles taken
-        int steps[2] = {0, 0};            // P tiles taken
-        auto issue_s = [&](int t, int st) {  // S over the P just read: MMAs run in issue order
+        int steps[4] = {0, 0, 0, 0};      // P tiles taken, as s_full and p_full count them
+        // i: tile 0 or 1, or 2, 3 for an even or odd step of a piece with one tile of queries
+        auto issue_s = [&](int i, int st) {  // S over the P just read: MMAs run in issue order
             const uint64_t k_desc = umma::sw128_desc(ring + st * L::TILE, 16, 1024);
-            const uint64_t q_desc = umma::sw128_desc(q_s + t * L::TILE, 16, 1024);
+            const uint64_t q_desc = umma::sw128_desc(q_s + (i == 1 ? L::TILE : 0), 16, 1024);
 #pragma unroll
             for (int kk = 0; kk < KS; ++kk) {
                 const uint32_t off = ((kk >> 2) * L::BOX + (kk & 3) * 32) >> 4;  // start address field
-                umma::mma_f16(tmem + t * CHUNK_TILE, q_desc + off, k_desc + off, idesc_s, kk > 0 ? 1u : 0u);
+                umma::mma_f16(tmem + (i & 1) * CHUNK_TILE, q_desc + off, k_desc + off, idesc_s, kk > 0 ? 1u : 0u);
             }
-            umma::commit(s_full(t));  // also says that every P.V before is done
+            umma::commit(s_full(i));  // also says that every P.V before is done
         };
-        auto issue_pv = [&](int t, int st, bool first) -> bool {
+        auto issue_pv = [&](int i, int st, bool first) -> bool {
             // V is N-major: 64-element columns 2048 apart, 8-token groups 1024, and a K step
             // is one copy's 16 tokens.  The first half's products run while the softmax still
             // works on the second half.
             const uint64_t v_desc = umma::sw128_desc(ring + st * L::TILE, CHUNK_TOKENS * 128, 1024);
-            const uint32_t s_t = tmem + t * CHUNK_TILE, o_t = tmem + L::O_COL + t * D;
-            const uint32_t parity = steps[t]++ & 1;
+            const uint32_t s_t = tmem + (i & 1) * CHUNK_TILE, o_t = tmem + L::O_COL + (i == 1 ? D : 0);
+            const uint32_t parity = steps[i]++ & 1;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                if (!mbar_wait_short(p_full(t, h), parity)) return false;
+                if (!mbar_wait_short(p_full(i, h), parity)) return false;
                 umma::fence_after_sync();
 #pragma unroll
                 for (int k = 4 * h; k < 4 * h + 4; ++k) {
@@ -451,19 +469,42 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
                     phase ^= 1;
                 }
             };
-            if (umma::elect_one()) {
+            if (!two) {
+                // one tile of queries: the scores of the even and the odd steps take the places
+                // of the two tiles', so that a step's scores are ready when the softmax of the
+                // step before ends
+                if (umma::elect_one()) {
+                    auto stage = [&](int k) { return (int)((total + k) % NS); };
+                    auto in = [&](int k) { return mbar_wait_short(kv_full(stage(k)), ((total + k) / NS) & 1); };
+                    auto scores = [&](int j) -> bool {
+                        if (!in(2 * j)) return false;
+                        umma::fence_after_sync();
+                        issue_s(2 + (j & 1), stage(2 * j));
+                        if (j == n - 1) umma::commit(q_empty(0));
+                        umma::commit(kv_empty(stage(2 * j)));
+                        return true;
+                    };
+                    ok = mbar_wait_short(q_full(0), used[0] & 1) && scores(0) && (n == 1 || scores(1));
+#pragma unroll 1
+                    for (int j = 0; j < n - 1 && ok; ++j) {
+                        ok = in(2 * j + 1) && issue_pv(2 + (j & 1), stage(2 * j + 1), j == 0);
+                        if (!ok) break;
+                        umma::commit(pv_step(j & 1));
+                        umma::commit(kv_empty(stage(2 * j + 1)));
+                        if (j + 2 < n) ok = scores(j + 2);
+                    }
+                }
+            } else if (umma::elect_one()) {
                 ok = landed();
                 if (ok) ok = mbar_wait_short(q_full(0), used[0] & 1);
                 if (ok) {
                     umma::fence_after_sync();
                     issue_s(0, st);
                     if (n == 1) umma::commit(q_empty(0));
-                    if (two) {
-                        ok = mbar_wait_short(q_full(1), used[1] & 1);
-                        umma::fence_after_sync();
-                        if (ok) issue_s(1, st);
-                        if (n == 1) umma::commit(q_empty(1));
-                    }
+                    ok = mbar_wait_short(q_full(1), used[1] & 1);
+                    umma::fence_after_sync();
+                    if (ok) issue_s(1, st);
+                    if (n == 1) umma::commit(q_empty(1));
                     umma::commit(kv_empty(st));
                     advance();
                 }
@@ -478,15 +519,11 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
                     umma::fence_after_sync();
                     issue_s(0, st);
                     if (j == n - 2) umma::commit(q_empty(0));
-                    if (two) {
-                        ok = issue_pv(1, v_st, j == 0);
-                        if (!ok) break;
-                        umma::commit(kv_empty(v_st));
-                        issue_s(1, st);
-                        if (j == n - 2) umma::commit(q_empty(1));
-                    } else {
-                        umma::commit(kv_empty(v_st));
-                    }
+                    ok = issue_pv(1, v_st, j == 0);
+                    if (!ok) break;
+                    umma::commit(kv_empty(v_st));
+                    issue_s(1, st);
+                    if (j == n - 2) umma::commit(q_empty(1));
                     umma::commit(kv_empty(st));
                     advance();
                 }
@@ -512,10 +549,16 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
                 umma::fence_smem_to_async();
                 __syncwarp();
             }
-            if (umma::elect_one()) {
+            if (!two) {
+                if (umma::elect_one()) {
+                    ok = landed() && issue_pv(2 + ((n - 1) & 1), st, n == 1);
+                    if (ok) umma::commit(pv_step((n - 1) & 1));
+                    if (ok) umma::commit(kv_empty(st));
+                }
+            } else if (umma::elect_one()) {
                 ok = landed() && issue_pv(0, st, n == 1);
                 if (ok) umma::commit(pv_done(0));
-                if (ok && two) {
+                if (ok) {
                     ok = issue_pv(1, st, n == 1);
                     if (ok) umma::commit(pv_done(1));
                 }
@@ -536,40 +579,54 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
         // ---- softmax and output of tile t: this thread's row is r
         const int t = warp >> 2, r = threadIdx.x & 127;
         const uint32_t lane_tmem = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-        const uint32_t s_t = lane_tmem + t * CHUNK_TILE, o_t = lane_tmem + L::O_COL + t * D;
+        const uint32_t o_t = lane_tmem + L::O_COL + t * D;
         const int jq = t * QPT + r / G, hg = r % G;  // query within the piece, head of the group
-        int steps = 0, ends = 0;  // S tiles and last P.V's so far: the phases of s_full and pv_done
+        int taken = 0, taken_even = 0, taken_odd = 0;  // S tiles so far: the phases of s_full and pv_step
+        int ends = 0;  // two-tile pieces so far: the phase of pv_done
         ChunkPiece pc;
         for (int i = 0; next_piece(i, pc); ++i) {
-            if (t == 1 && pc.queries <= QPT) continue;
-            const int n = pc.kt1 - pc.kt0;
+            const int n = max(pc.kt1 - pc.kt0, 0);
+            const bool two = pc.queries > QPT;
+            if (t == 1 && !two) continue;  // the other warpgroup takes both S tiles in turn
             const bool valid = r < QPT * G && jq < pc.queries;
             const bool busy = __any_sync(FULL_MASK, valid);
             const int lim = pc.lim0 + jq;
             float m_ref = -INFINITY;
             uint64_t sum2[2] = {0, 0};  // the row's sum, in four parts
-            for (int j = 0; j < n; ++j, ++steps) {
-                ok = __all_sync(FULL_MASK, mbar_wait_short(s_full(t), steps & 1));
+            for (int j = 0; j < n; ++j) {
+                const int b = two ? t : 2 + (j & 1);  // S tile of this step
+                const int phase = two ? taken++ : (j & 1) ? taken_odd++ : taken_even++;
+                ok = __all_sync(FULL_MASK, mbar_wait_short(s_full(b), phase & 1));
                 if (!ok) break;
                 if (busy) {
                     umma::fence_after_sync();
+                    const uint32_t s_t = lane_tmem + (b & 1) * CHUNK_TILE;
                     const int seen = lim - (pc.kt0 + j) * CHUNK_TILE;  // columns this row may see
+                    // with two tiles a step's S was committed after the P.V before, with one not
+                    const uint32_t wait_o = two ? 0u : pv_step((j & 1) ^ 1);
+                    const int phase_o = ((j & 1) ? taken_even : taken_odd) - 1;
                     if (__any_sync(FULL_MASK, seen < CHUNK_TILE))
-                        softmax_step<T, D, SPLIT_P, true>(s_t, o_t, seen, j > 0, p.scale_log2, m_ref, sum2,
-                                                          p_full(t, 0), p_full(t, 1));
+                        ok = softmax_step<T, D, SPLIT_P, true>(s_t, o_t, seen, j > 0, p.scale_log2, m_ref, sum2,
+                                                               p_full(b, 0), p_full(b, 1), wait_o, phase_o);
                     else
-                        softmax_step<T, D, SPLIT_P, false>(s_t, o_t, seen, j > 0, p.scale_log2, m_ref, sum2,
-                                                           p_full(t, 0), p_full(t, 1));
+                        ok = softmax_step<T, D, SPLIT_P, false>(s_t, o_t, seen, j > 0, p.scale_log2, m_ref, sum2,
+                                                                p_full(b, 0), p_full(b, 1), wait_o, phase_o);
+                    if (!ok) break;
                 } else if (lane == 0) {  // rows of no query: whatever S left there
-                    mbar_arrive(p_full(t, 0));
-                    mbar_arrive(p_full(t, 1));
+                    mbar_arrive(p_full(b, 0));
+                    mbar_arrive(p_full(b, 1));
                 }
             }
             if (!ok) break;
             if (n > 0) {
-                ok = __all_sync(FULL_MASK, mbar_wait_short(pv_done(t), ends & 1));
+                if (two) {
+                    ok = __all_sync(FULL_MASK, mbar_wait_short(pv_done(t), ends & 1));
+                    ++ends;
+                } else {
+                    const int last = (n - 1) & 1;
+                    ok = __all_sync(FULL_MASK, mbar_wait_short(pv_step(last), ((last ? taken_odd : taken_even) - 1) & 1));
+                }
                 if (!ok) break;
-                ++ends;
                 umma::fence_after_sync();
             }
             if (busy) {

@@ -386,6 +386,21 @@ def test_chunk_many_requests(P):
     c.check(c.run(P))
 
 
+def test_chunk_pieces_of_all_kinds_one_after_another(P):
+    """Many pieces for each CTA, one and two query tiles and all step counts in turn."""
+    rng = np.random.default_rng(5)
+    ctx, new = [], []
+    for i in range(150):
+        n = int(rng.choice([1, 2, 64, 65, 130, 200, 257]))
+        new.append(n)
+        ctx.append(n + int(rng.integers(0, 700)))
+    c = Chunk("f16", 8, 8, 64, 16, ctx, new, 31, pad=2)
+    out = c.run(P)
+    c.check(out)
+    assert torch.equal(out, c.run(P))
+    assert P.pkv_get_device_error() == 0
+
+
 def test_chunk_agrees_with_decode(P):
     """One query per request: the decode kernel's answer."""
     ctx = [1, 30, 500, 1200, 64]
