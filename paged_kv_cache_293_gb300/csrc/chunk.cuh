@@ -102,30 +102,6 @@ __device__ __forceinline__ void regs_inc() {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-// Two 32-bit values in one 64-bit register: one instruction works on both.
-__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
-    uint64_t v;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi));
-    return v;
-}
-__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t v;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(v) : "l"(a), "l"(b), "l"(c));
-    return v;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-    uint64_t v;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
-    return v;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-    uint64_t v;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
-    return v;
-}
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float v;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(v) : "f"(a), "f"(b), "f"(c));
@@ -638,7 +614,8 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
                 unpack2(sum2[1], part[2], part[3]);
                 const float l = (part[0] + part[1]) + (part[2] + part[3]);
                 const float inv = l > 0.f ? 1.f / l : 0.f;
-#pragma unroll
+                // once per piece: a loop that stays in the instruction cache
+#pragma unroll 1
                 for (int c = 0; c < D; c += 32) {
                     float o[32];
                     if (n > 0) {
