@@ -134,9 +134,10 @@ def _contig(*ts):
 def make_pool(k_pool, v_pool):
     """pkv_pool view of two [N][Hkv][B][D] tensors."""
     _contig(k_pool, v_pool)
-    if k_pool.shape != v_pool.shape or k_pool.dtype != v_pool.dtype or k_pool.dim() != 4:
+    shape = k_pool.shape
+    if shape != v_pool.shape or k_pool.dtype != v_pool.dtype or len(shape) != 4:
         raise ValueError("k_pool and v_pool must be matching [N][Hkv][B][D] tensors")
-    N, Hkv, B, D = k_pool.shape
+    N, Hkv, B, D = shape
     return pkv_pool(k_pool.data_ptr(), v_pool.data_ptr(), N, B, Hkv, D, _DTYPE[k_pool.dtype])
 
 
@@ -396,20 +397,39 @@ def pkv_free_sequences(alloc, block_size, block_tables, seqs, lens, stream=None)
                                   _stream(stream, block_tables)), "pkv_free_sequences")
 
 
-def _expect(t, name, dtype, shape):
-    """A contiguous tensor of this type and shape, or ValueError."""
-    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
-        raise ValueError("%s must be a contiguous %s tensor of shape %s" % (name, dtype, tuple(shape)))
+# The ragged-step calls take many small tensors each and are made once per layer or step by a
+# host loop, so their checks stay short: one pass over a call's tensors, integers for pointers.
+
+def _refuse(t, name, dtype, numel, device):
+    if t.dtype != dtype or t.numel() != numel or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous %s tensor of %d values" % (name, dtype, numel))
+    raise ValueError("%s must be on the current CUDA device (%s)" % (name, device))
 
 
-def _on_current_device(ref, *ts):
-    """All on ref's device, which is the current one (the library launches there)."""
-    d = ref.device
-    for t in ts:
-        if t is not None and t.device != d:
-            raise ValueError("tensors on different devices")
-    if d.type != "cuda" or d.index != torch.cuda.current_device():
-        raise ValueError("the tensors' device must be the current CUDA device")
+def _expect(device, dtype, *specs):
+    """Each (tensor, name, numel): contiguous, of this type and size, on `device`."""
+    for t, name, numel in specs:
+        if (t.dtype is not dtype or t.numel() != numel or not t.is_contiguous()
+                or t.get_device() != device):
+            _refuse(t, name, dtype, numel, device)
+
+
+def _current_device(t, name):
+    """The index of the device the library will launch on, which must hold t."""
+    d = t.get_device()
+    if d < 0 or d != torch.cuda.current_device():
+        raise ValueError("%s must be on the current CUDA device" % name)
+    return d
+
+
+def _raw_stream(stream, device):
+    return torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream)
+
+
+def _pool_of(k_pool, v_pool, device):
+    if k_pool.get_device() != device or v_pool.get_device() != device:
+        raise ValueError("k_pool and v_pool must be on the current CUDA device")
+    return make_pool(k_pool, v_pool)
 
 
 def pkv_build_batch(alloc, block_size, block_tables, past_lens, new_lens, query_start,
@@ -418,31 +438,34 @@ def pkv_build_batch(alloc, block_size, block_tables, past_lens, new_lens, query_
     """Tables, starts, contexts, positions and slots of one ragged step, from past_lens and
     new_lens (int32 [num_seqs]); the token arrays' length is the room for tokens."""
     S, M = block_tables.shape
-    T = positions.numel()
-    i32 = torch.int32
-    _expect(block_tables, "block_tables", i32, (S, M))
-    for t, name, n in ((past_lens, "past_lens", S), (new_lens, "new_lens", S),
-                       (query_start, "query_start", S + 1), (context_lens, "context_lens", S),
-                       (seq_status, "seq_status", S), (positions, "positions", T),
-                       (token_seq, "token_seq", T)):
-        _expect(t, name, i32, (n,))
-    _expect(slot_mapping, "slot_mapping", torch.int64, (T,))
+    T, N = positions.numel(), alloc.num_blocks
+    dev = _current_device(block_tables, "block_tables")
+    _expect(dev, torch.int32, (block_tables, "block_tables", S * M), (past_lens, "past_lens", S),
+            (new_lens, "new_lens", S), (query_start, "query_start", S + 1),
+            (context_lens, "context_lens", S), (positions, "positions", T),
+            (token_seq, "token_seq", T), (seq_status, "seq_status", S),
+            (alloc.free_ids, "free_ids", N), (alloc.free_count, "free_count", 1),
+            (alloc.refcount, "refcount", N))
+    _expect(dev, torch.int64, (slot_mapping, "slot_mapping", T))
+    left = None
     if free_count_out is not None:
-        _expect(free_count_out, "free_count_out", i32, (1,))
-    _on_current_device(block_tables, past_lens, new_lens, query_start, context_lens, positions,
-                       token_seq, slot_mapping, seq_status, free_count_out, alloc.free_ids)
-    a = alloc.struct()
-    _check(lib.pkv_build_batch(ctypes.byref(a), int(block_size), _ptr(block_tables), M,
-                               _ptr(past_lens), _ptr(new_lens), S, T, _ptr(free_count_out),
-                               _ptr(query_start), _ptr(context_lens), _ptr(positions),
-                               _ptr(token_seq), _ptr(slot_mapping), _ptr(seq_status),
-                               _stream(stream, block_tables)), "pkv_build_batch")
+        _expect(dev, torch.int32, (free_count_out, "free_count_out", 1))
+        left = free_count_out.data_ptr()
+    st = lib.pkv_build_batch(alloc.struct(), int(block_size), block_tables.data_ptr(), M,
+                             past_lens.data_ptr(), new_lens.data_ptr(), S, T, left,
+                             query_start.data_ptr(), context_lens.data_ptr(), positions.data_ptr(),
+                             token_seq.data_ptr(), slot_mapping.data_ptr(), seq_status.data_ptr(),
+                             _raw_stream(stream, dev))
+    if st != PKV_OK:
+        raise PagedKVError(st, "pkv_build_batch")
 
 
-def _head_rows(t, name, dtype, T, H, D):
+def _head_rows(t, name, dtype, device, T, H, D):
     """Token stride of a [T][H][D] tensor whose heads are packed."""
-    if t.dtype != dtype or t.shape != (T, H, D) or t.stride(2) != 1 or (H > 1 and t.stride(1) != D):
-        raise ValueError("%s must be a %s tensor of shape %s with packed heads" % (name, dtype, (T, H, D)))
+    if (t.dtype is not dtype or t.shape != (T, H, D) or t.stride(2) != 1
+            or (H > 1 and t.stride(1) != D) or t.get_device() != device):
+        raise ValueError("%s must be a %s tensor of shape %s with packed heads on the current CUDA "
+                         "device" % (name, dtype, (T, H, D)))
     return t.stride(0) if T > 1 else H * D
 
 
@@ -450,29 +473,37 @@ def pkv_qk_norm_rope_write(q, k, v, k_pool, v_pool, positions, slot_mapping, q_o
                            k_weight=None, eps=1e-6, cos_sin=None, interleaved=False, stream=None):
     """Per-head norms (where a weight is given) and rotation (where cos_sin
     [max_position][rotary_dim] is given) of q and k; q to q_out, k and v to their slots."""
-    pool = make_pool(k_pool, v_pool)
     T, Hq, D = q.shape
-    Hkv, dt = pool.num_kv_heads, k_pool.dtype
+    dt = k_pool.dtype
+    dev = _current_device(q, "q")
+    pool = _pool_of(k_pool, v_pool, dev)
+    Hkv = pool.num_kv_heads
     if pool.head_dim != D:
         raise ValueError("q and the pools must have the same head_dim")
-    strides = [_head_rows(t, n, dt, T, h, D) for t, n, h in ((q, "q", Hq), (k, "k", Hkv), (v, "v", Hkv))]
-    _expect(q_out, "q_out", dt, (T, Hq, D))
-    _expect(positions, "positions", torch.int32, (T,))
-    _expect(slot_mapping, "slot_mapping", torch.int64, (T,))
+    qs = _head_rows(q, "q", dt, dev, T, Hq, D)
+    ks = _head_rows(k, "k", dt, dev, T, Hkv, D)
+    vs = _head_rows(v, "v", dt, dev, T, Hkv, D)
+    _expect(dev, dt, (q_out, "q_out", T * Hq * D))
+    _expect(dev, torch.int32, (positions, "positions", T))
+    _expect(dev, torch.int64, (slot_mapping, "slot_mapping", T))
     max_pos = rot = 0
+    table = wq = wk = None
     if cos_sin is not None:
         max_pos, rot = cos_sin.shape
-        _expect(cos_sin, "cos_sin", torch.float32, (max_pos, rot))
-    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None:
-            _expect(w, name, dt, (D,))
-    _on_current_device(q, k, v, k_pool, v_pool, positions, slot_mapping, q_out, q_weight, k_weight,
-                       cos_sin)
-    _check(lib.pkv_qk_norm_rope_write(
-        ctypes.byref(pool), _ptr(q), strides[0], _ptr(k), strides[1], _ptr(v), strides[2], T, Hq,
-        _ptr(q_weight), _ptr(k_weight), float(eps), _ptr(cos_sin), max_pos, rot, int(interleaved),
-        _ptr(positions), _ptr(slot_mapping), _ptr(q_out), _stream(stream, q)),
-        "pkv_qk_norm_rope_write")
+        _expect(dev, torch.float32, (cos_sin, "cos_sin", max_pos * rot))
+        table = cos_sin.data_ptr()
+    if q_weight is not None:
+        _expect(dev, dt, (q_weight, "q_weight", D))
+        wq = q_weight.data_ptr()
+    if k_weight is not None:
+        _expect(dev, dt, (k_weight, "k_weight", D))
+        wk = k_weight.data_ptr()
+    st = lib.pkv_qk_norm_rope_write(pool, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, T, Hq,
+                                    wq, wk, eps, table, max_pos, rot, bool(interleaved),
+                                    positions.data_ptr(), slot_mapping.data_ptr(), q_out.data_ptr(),
+                                    _raw_stream(stream, dev))
+    if st != PKV_OK:
+        raise PagedKVError(st, "pkv_qk_norm_rope_write")
 
 
 def pkv_chunk_workspace_bytes(k_pool, num_tokens, num_seqs, num_q_heads, max_context_len):
@@ -484,21 +515,23 @@ def pkv_chunk_workspace_bytes(k_pool, num_tokens, num_seqs, num_q_heads, max_con
 def pkv_paged_attention_chunk(q, k_pool, v_pool, query_start, block_tables, context_lens, scale,
                               out, max_context_len, workspace, stream=None):
     """q, out: [num_tokens][num_q_heads][head_dim], request s's rows from query_start[s] on."""
-    pool = make_pool(k_pool, v_pool)
     T, Hq, D = q.shape
     S, M = block_tables.shape
-    _expect(q, "q", k_pool.dtype, (T, Hq, pool.head_dim))
-    _expect(out, "out", out.dtype, (T, Hq, D))
-    _expect(query_start, "query_start", torch.int32, (S + 1,))
-    _expect(block_tables, "block_tables", torch.int32, (S, M))
-    _expect(context_lens, "context_lens", torch.int32, (S,))
-    _contig(workspace)
-    _on_current_device(q, k_pool, v_pool, query_start, block_tables, context_lens, out, workspace)
-    _check(lib.pkv_paged_attention_chunk(
-        ctypes.byref(pool), _ptr(q), T, Hq, _ptr(query_start), S, _ptr(block_tables), M,
-        _ptr(context_lens), int(max_context_len), float(scale), _ptr(out), _DTYPE[out.dtype],
-        _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream, q)),
-        "pkv_paged_attention_chunk")
+    dev = _current_device(q, "q")
+    pool = _pool_of(k_pool, v_pool, dev)
+    if pool.head_dim != D:
+        raise ValueError("q and the pools must have the same head_dim")
+    _expect(dev, k_pool.dtype, (q, "q", T * Hq * D))
+    _expect(dev, out.dtype, (out, "out", T * Hq * D))
+    _expect(dev, torch.int32, (query_start, "query_start", S + 1),
+            (block_tables, "block_tables", S * M), (context_lens, "context_lens", S))
+    _expect(dev, workspace.dtype, (workspace, "workspace", workspace.numel()))
+    st = lib.pkv_paged_attention_chunk(
+        pool, q.data_ptr(), T, Hq, query_start.data_ptr(), S, block_tables.data_ptr(), M,
+        context_lens.data_ptr(), int(max_context_len), scale, out.data_ptr(), _DTYPE[out.dtype],
+        workspace.data_ptr(), workspace.nbytes, _raw_stream(stream, dev))
+    if st != PKV_OK:
+        raise PagedKVError(st, "pkv_paged_attention_chunk")
 
 
 def pkv_get_device_error(stream=None, device=None):

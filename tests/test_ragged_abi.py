@@ -122,30 +122,67 @@ def test_chunk_workspace_bytes(P):
 
 
 def test_binding_checks_tensors(P):
+    """Tensors of a wrong kind, or on the host, are refused before the library is called."""
     i = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
+    h = lambda *s: torch.zeros(s, dtype=torch.float16)  # noqa: E731
     alloc = P.BlockAllocator.of_tensors(i(4), i(1), i(4))
-    with pytest.raises(ValueError, match="past_lens"):
-        P.pkv_build_batch(alloc, 16, i(2, 4), i(3), i(2), i(3), i(2), i(8), i(8),
-                          torch.zeros(8, dtype=torch.int64), i(2))
-    with pytest.raises(ValueError, match="slot_mapping"):
-        P.pkv_build_batch(alloc, 16, i(2, 4), i(2), i(2), i(3), i(2), i(8), i(8), i(8), i(2))
-    with pytest.raises(ValueError, match="current CUDA device"):   # host tensors
-        P.pkv_build_batch(alloc, 16, i(2, 4), i(2), i(2), i(3), i(2), i(8), i(8),
-                          torch.zeros(8, dtype=torch.int64), i(2))
+    slots = torch.zeros(8, dtype=torch.int64)
+    pool = h(4, 2, 16, 64)
     with pytest.raises(ValueError):
         P.BlockAllocator.of_tensors(i(4).long(), i(1), i(4))
+    with pytest.raises(ValueError, match="current CUDA device"):
+        P.pkv_build_batch(alloc, 16, i(2, 4), i(2), i(2), i(3), i(2), i(8), i(8), slots, i(2))
+    with pytest.raises(ValueError, match="current CUDA device"):
+        P.pkv_qk_norm_rope_write(h(8, 4, 64), h(8, 2, 64), h(8, 2, 64), pool, pool, i(8), slots, h(8, 4, 64))
+    with pytest.raises(ValueError, match="current CUDA device"):
+        P.pkv_paged_attention_chunk(h(3, 4, 64), pool, pool, i(3), i(2, 4), i(2), 0.1, h(3, 4, 64), 64,
+                                    torch.zeros(64, dtype=torch.uint8))
+
+
+@pytest.mark.parametrize("name,bad", [
+    ("past_lens", lambda t: t[:1]), ("query_start", lambda t: t[:2]), ("positions", lambda t: t[:7]),
+    ("slot_mapping", lambda t: t.int()), ("slot_mapping", lambda t: t[:7]), ("new_lens", lambda t: t.long()),
+    ("context_lens", lambda t: torch.zeros(4, dtype=torch.int32)[::2]), ("seq_status", lambda t: t[:0])])
+def test_build_batch_binding_names_the_bad_tensor(P, monkeypatch, name, bad):
+    monkeypatch.setattr(P, "_current_device", lambda t, n: -1)  # host tensors pass for the device's
+    i = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
+    args = dict(past_lens=i(2), new_lens=i(2), query_start=i(3), context_lens=i(2), positions=i(8),
+                token_seq=i(8), slot_mapping=torch.zeros(8, dtype=torch.int64), seq_status=i(2))
+    args[name] = bad(args[name])
+    if name == "positions":   # the room is its length: the others disagree with it
+        name = "token_seq"
+    with pytest.raises(ValueError, match=name):
+        P.pkv_build_batch(P.BlockAllocator.of_tensors(i(4), i(1), i(4)), 16, i(2, 4), **args)
+
+
+def test_rope_and_chunk_bindings_name_the_bad_tensor(P, monkeypatch):
+    monkeypatch.setattr(P, "_current_device", lambda t, n: -1)
+    i = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
     h = lambda *s: torch.zeros(s, dtype=torch.float16)  # noqa: E731
-    pool = h(4, 2, 16, 64)
-    args = (pool, pool, i(3), torch.zeros(3, dtype=torch.int64), h(3, 4, 64))
-    with pytest.raises(ValueError, match="packed heads"):
-        P.pkv_qk_norm_rope_write(h(4, 3, 64).transpose(0, 1), h(3, 2, 64), h(3, 2, 64), *args)
-    with pytest.raises(ValueError, match="k must"):
-        P.pkv_qk_norm_rope_write(h(3, 4, 64), h(3, 3, 64), h(3, 2, 64), *args)
-    with pytest.raises(ValueError, match="head_dim"):
-        P.pkv_qk_norm_rope_write(h(3, 4, 128), h(3, 2, 128), h(3, 2, 128), *args)
-    with pytest.raises(ValueError, match="query_start"):
-        P.pkv_paged_attention_chunk(h(3, 4, 64), pool, pool, i(2), i(2, 4), i(2), 0.1, h(3, 4, 64), 64,
-                                    torch.zeros(1, dtype=torch.uint8))
-    with pytest.raises(ValueError, match="q must"):
-        P.pkv_paged_attention_chunk(torch.zeros(3, 4, 64), pool, pool, i(3), i(2, 4), i(2), 0.1,
-                                    h(3, 4, 64), 64, torch.zeros(1, dtype=torch.uint8))
+    pool, slots, ws = h(4, 2, 16, 64), torch.zeros(3, dtype=torch.int64), torch.zeros(64, dtype=torch.uint8)
+
+    def rope(match, q=h(3, 4, 64), k=h(3, 2, 64), v=h(3, 2, 64), pos=i(3), sl=slots, out=h(3, 4, 64), **kw):
+        with pytest.raises(ValueError, match=match):
+            P.pkv_qk_norm_rope_write(q, k, v, pool, pool, pos, sl, out, **kw)
+
+    rope("q must", q=h(4, 3, 64).transpose(0, 1))
+    rope("k must", k=h(3, 3, 64))
+    rope("v must", v=h(3, 2, 64).float())
+    rope("head_dim", q=h(3, 4, 128))
+    rope("positions", pos=i(2))
+    rope("slot_mapping", sl=i(3))
+    rope("q_out", out=h(3, 4, 64).float())
+    rope("cos_sin", cos_sin=torch.zeros(8, 64, dtype=torch.float64))
+    rope("q_weight", q_weight=h(32))
+    rope("k_weight", k_weight=torch.ones(64))
+
+    def chunk(match, q=h(3, 4, 64), start=i(3), tables=i(2, 4), ctx=i(2), out=h(3, 4, 64)):
+        with pytest.raises(ValueError, match=match):
+            P.pkv_paged_attention_chunk(q, pool, pool, start, tables, ctx, 0.1, out, 64, ws)
+
+    chunk("query_start", start=i(2))
+    chunk("q must", q=torch.zeros(3, 4, 64))
+    chunk("head_dim", q=h(3, 4, 128))
+    chunk("out must", out=h(3, 4, 32))
+    chunk("block_tables", tables=i(2, 8)[:, :4])
+    chunk("context_lens", ctx=i(2).long())
