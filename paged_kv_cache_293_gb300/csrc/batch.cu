@@ -11,10 +11,11 @@
 // the GPU works in (the growth kernel in allocator.cu pops with atomics instead).
 //
 // The traffic is a few bytes per token and block (4.4 MB = 0.65 us at the measured copy rate
-// for 4096 requests with 260,000 tokens), so launches and memory round trips bound it.  It is
-// one launch of one thread-block cluster: the scan over the requests is split over the
-// cluster's CTAs, which exchange their totals through distributed shared memory, and a
-// cluster barrier stands where a second launch would.
+// for 4096 requests with 260,000 tokens), so launches and memory round trips bound it.  Up to
+// BATCH_ONE_CTA requests and BATCH_FEW_TOKENS tokens it is one launch of one CTA.  More
+// requests are scanned by one thread-block cluster, whose CTAs exchange their totals through
+// distributed shared memory, with a cluster barrier where a launch would stand; more tokens
+// are filled in by a second kernel over the whole GPU, launched early behind the first.
 #include <cooperative_groups.h>
 
 #include "pkv_common.cuh"
@@ -25,8 +26,11 @@ namespace pkv {
 
 namespace {
 
-constexpr int BATCH_CTAS = 8;        // portable cluster size
+constexpr int BATCH_CTAS = 8;          // portable cluster size
 constexpr int BATCH_THREADS = 1024;
+constexpr int BATCH_ONE_CTA = 1024;    // requests: one per thread
+constexpr int BATCH_FEW_TOKENS = 8192; // two rounds of one CTA
+constexpr int TOKENS_THREADS = 256;
 constexpr int BATCH_WARPS = BATCH_THREADS / 32;
 
 struct SeqNeed {
@@ -97,20 +101,77 @@ __device__ __forceinline__ Pair block_inclusive(Pair v, Pair* warp_sums, Pair* t
     return v;
 }
 
+// Four tokens in a row: one search for the request of the first, wide stores.  starts and ctxs
+// are query_start and context_lens or copies of them.
+__device__ __forceinline__ void fill_tokens(const BatchParams& p, long long t0, int real, bool wide,
+                                            const int* starts, const int* ctxs) {
+    const int S = p.num_seqs, M = p.max_blocks_per_seq, B = p.block_size;
+    int s = -1, end = 0, next_pos = 0, ctx = 0;
+    int pos[4], seq[4];
+    long long slot[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const long long t = t0 + i;
+        pos[i] = seq[i] = -1;
+        slot[i] = -1;
+        if (t >= real) continue;
+        if (s < 0 || t >= end) {
+            int lo = s < 0 ? 0 : s + 1, hi = S - 1;  // first request ending past t
+            if (s >= 0 && starts[lo + 1] > t) hi = lo;
+            while (lo < hi) {
+                const int mid = lo + ((hi - lo) >> 1);
+                if (starts[mid + 1] > t) hi = mid; else lo = mid + 1;
+            }
+            s = lo;
+            end = starts[s + 1];
+            ctx = ctxs[s];
+            next_pos = ctx - (end - (int)t);
+        }
+        seq[i] = s;
+        if (ctx > 0) {
+            pos[i] = next_pos;
+            const int id = p.block_tables[(size_t)s * M + next_pos / B];
+            if (id >= 0) slot[i] = (long long)id * B + next_pos % B;
+        }
+        ++next_pos;
+    }
+    if (wide && t0 + 4 <= p.max_tokens) {
+        *reinterpret_cast<int4*>(p.positions + t0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+        *reinterpret_cast<int4*>(p.token_seq + t0) = make_int4(seq[0], seq[1], seq[2], seq[3]);
+        longlong2* out = reinterpret_cast<longlong2*>(p.slot_mapping + t0);
+        out[0] = make_longlong2(slot[0], slot[1]);
+        out[1] = make_longlong2(slot[2], slot[3]);
+    } else {
+        for (int i = 0; i < 4 && t0 + i < p.max_tokens; ++i) {
+            p.positions[t0 + i] = pos[i];
+            p.token_seq[t0 + i] = seq[i];
+            p.slot_mapping[t0 + i] = slot[i];
+        }
+    }
+}
+
+__device__ __forceinline__ bool wide_tokens(const BatchParams& p) {
+    return ((reinterpret_cast<uintptr_t>(p.positions) | reinterpret_cast<uintptr_t>(p.token_seq) |
+             reinterpret_cast<uintptr_t>(p.slot_mapping)) & 15u) == 0;
+}
+
 }  // namespace
 
-__global__ void __cluster_dims__(BATCH_CTAS, 1, 1) __launch_bounds__(BATCH_THREADS)
-build_batch_kernel(const BatchParams p) {
+template <int CTAS>
+__global__ void __launch_bounds__(BATCH_THREADS) build_batch_kernel(const BatchParams p, int fill) {
     static_assert(BATCH_WARPS == 32, "one lane per warp total");
     __shared__ Pair warp_sums[BATCH_WARPS];
     __shared__ Pair cta_total;         // read by the other CTAs of the cluster
     __shared__ long long cta_popped;   // blocks popped up to this CTA's last served request
     __shared__ long long upto_s[BATCH_THREADS];  // inclusive block counts of the tile's requests
     __shared__ int first_s[BATCH_THREADS];       // first fresh logical block, -1: not served
+    __shared__ int start_s[BATCH_THREADS + 1], ctx_s[BATCH_THREADS];  // one CTA: starts and contexts
     cg::cluster_group cluster = cg::this_cluster();
-    const int rank = (int)cluster.block_rank(), tid = threadIdx.x;
+    // the token kernel may be set up meanwhile; it waits for this grid's end
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int rank = CTAS > 1 ? (int)cluster.block_rank() : 0, tid = threadIdx.x;
     const int S = p.num_seqs, M = p.max_blocks_per_seq, B = p.block_size;
-    const int per = (S + BATCH_CTAS - 1) / BATCH_CTAS;
+    const int per = (S + CTAS - 1) / CTAS;
     const int s_lo = min(S, rank * per), s_hi = min(S, s_lo + per);
     long long free_blocks = *p.alloc.free_count;
     free_blocks = free_blocks < 0 ? 0 : min(free_blocks, (long long)p.alloc.num_blocks);
@@ -118,30 +179,32 @@ build_batch_kernel(const BatchParams p) {
     if (rank == 0 && tid == 0) p.query_start[0] = 0;
 
     // ---- this CTA's totals, then the sums of the CTAs before it
-    Pair mine{0, 0}, total;
     SeqNeed held_need{0, 0, 0, 0};
-    for (int s = s_lo + tid; s < s_hi; s += BATCH_THREADS) {
-        held_need = seq_need(p, s, true);
-        mine.tokens += held_need.tokens;
-        mine.need += held_need.need;
-    }
-    block_inclusive(mine, warp_sums, &total);
-    if (tid == 0) {
-        cta_total = total;
-        cta_popped = 0;
-    }
-    cluster.sync();  // also: every CTA has read the free count before it may be rewritten
     Pair base{0, 0};
     long long all_tokens = 0;
-#pragma unroll
-    for (int r = 0; r < BATCH_CTAS; ++r) {
-        const Pair* other = cluster.map_shared_rank(&cta_total, r);
-        const Pair v = *other;
-        all_tokens += v.tokens;
-        if (r < rank) {
-            base.tokens += v.tokens;
-            base.need += v.need;
+    if (tid == 0) cta_popped = 0;
+    if (CTAS > 1) {
+        Pair mine{0, 0}, total;
+        for (int s = s_lo + tid; s < s_hi; s += BATCH_THREADS) {
+            held_need = seq_need(p, s, true);
+            mine.tokens += held_need.tokens;
+            mine.need += held_need.need;
         }
+        block_inclusive(mine, warp_sums, &total);
+        if (tid == 0) cta_total = total;
+        cluster.sync();  // also: every CTA has read the free count before it may be rewritten
+#pragma unroll
+        for (int r = 0; r < CTAS; ++r) {
+            const Pair v = *cluster.map_shared_rank(&cta_total, r);
+            all_tokens += v.tokens;
+            if (r < rank) {
+                base.tokens += v.tokens;
+                base.need += v.need;
+            }
+        }
+    } else {
+        if (s_lo + tid < s_hi) held_need = seq_need(p, s_lo + tid, true);
+        __syncthreads();
     }
 
     // ---- requests in tiles of one per thread: starts, contexts, statuses, table entries
@@ -158,8 +221,14 @@ build_batch_kernel(const BatchParams p) {
         if (live) {
             if (v.tokens > p.max_tokens && n.tokens > 0) n.status = 2;  // its rows are not in the batch
             if (n.status == 0 && n.need > 0 && v.need > free_blocks) n.status = 1;
-            p.query_start[s + 1] = (int)min(v.tokens, (long long)p.max_tokens);
-            p.context_lens[s] = n.status == 0 ? n.past + n.tokens : 0;
+            const int end = (int)min(v.tokens, (long long)p.max_tokens);
+            const int ctx = n.status == 0 ? n.past + n.tokens : 0;
+            p.query_start[s + 1] = end;
+            p.context_lens[s] = ctx;
+            if (CTAS == 1) {
+                start_s[tid + 1] = end;
+                ctx_s[tid] = ctx;
+            }
             p.seq_status[s] = n.status;
             if (n.status == 0 && n.need > 0) atomicMax(&cta_popped, v.need);
         }
@@ -191,70 +260,54 @@ build_batch_kernel(const BatchParams p) {
         base.need += tile.need;
         __syncthreads();
     }
+    if (CTAS == 1) all_tokens = base.tokens;
     if (all_tokens > p.max_tokens && rank == 0 && tid == 0) set_error(p.err, PKV_DEVERR_POSITION);
-    cluster.sync();  // starts, contexts and tables of every CTA are visible
+    if (CTAS > 1) cluster.sync();  // starts, contexts and tables of every CTA are visible
 
     if (rank == 0 && tid == 0) {
-        long long popped = 0;
-        for (int r = 0; r < BATCH_CTAS; ++r) popped = max(popped, *cluster.map_shared_rank(&cta_popped, r));
+        long long popped = cta_popped;
+        if (CTAS > 1)
+            for (int r = 1; r < CTAS; ++r) popped = max(popped, *cluster.map_shared_rank(&cta_popped, r));
         *p.free_count_out = (int)(free_blocks - popped);
     }
-
-    // ---- tokens, four in a row per thread: one search, wide stores
-    const int real = (int)min(all_tokens, (long long)p.max_tokens);
-    const bool wide = ((reinterpret_cast<uintptr_t>(p.positions) | reinterpret_cast<uintptr_t>(p.token_seq) |
-                        reinterpret_cast<uintptr_t>(p.slot_mapping)) & 15u) == 0;
-    for (long long t0 = ((long long)rank * BATCH_THREADS + tid) * 4; t0 < p.max_tokens;
-         t0 += (long long)BATCH_CTAS * BATCH_THREADS * 4) {
-        int s = -1, end = 0, next_pos = 0, ctx = 0;
-        int pos[4], seq[4];
-        long long slot[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const long long t = t0 + i;
-            pos[i] = seq[i] = -1;
-            slot[i] = -1;
-            if (t >= real) continue;
-            if (s < 0 || t >= end) {
-                int lo = s < 0 ? 0 : s + 1, hi = S - 1;  // first request ending past t
-                if (s >= 0 && p.query_start[lo + 1] > t) hi = lo;
-                while (lo < hi) {
-                    const int mid = lo + ((hi - lo) >> 1);
-                    if (p.query_start[mid + 1] > t) hi = mid; else lo = mid + 1;
-                }
-                s = lo;
-                end = p.query_start[s + 1];
-                ctx = p.context_lens[s];
-                next_pos = ctx - (end - (int)t);
-            }
-            seq[i] = s;
-            if (ctx > 0) {
-                pos[i] = next_pos;
-                const int id = p.block_tables[(size_t)s * M + next_pos / B];
-                if (id >= 0) slot[i] = (long long)id * B + next_pos % B;
-            }
-            ++next_pos;
-        }
-        if (wide && t0 + 4 <= p.max_tokens) {
-            *reinterpret_cast<int4*>(p.positions + t0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
-            *reinterpret_cast<int4*>(p.token_seq + t0) = make_int4(seq[0], seq[1], seq[2], seq[3]);
-            longlong2* out = reinterpret_cast<longlong2*>(p.slot_mapping + t0);
-            out[0] = make_longlong2(slot[0], slot[1]);
-            out[1] = make_longlong2(slot[2], slot[3]);
-        } else {
-            for (int i = 0; i < 4 && t0 + i < p.max_tokens; ++i) {
-                p.positions[t0 + i] = pos[i];
-                p.token_seq[t0 + i] = seq[i];
-                p.slot_mapping[t0 + i] = slot[i];
-            }
-        }
+    if (fill) {
+        const int real = (int)min(all_tokens, (long long)p.max_tokens);
+        const bool wide = wide_tokens(p);
+        for (long long t0 = ((long long)rank * BATCH_THREADS + tid) * 4; t0 < p.max_tokens;
+             t0 += (long long)CTAS * BATCH_THREADS * 4)
+            fill_tokens(p, t0, real, wide, CTAS == 1 ? start_s : p.query_start, CTAS == 1 ? ctx_s : p.context_lens);
     }
-    cluster.sync();  // no CTA ends while CTA 0 may still read its shared memory
+    if (CTAS > 1) cluster.sync();  // no CTA ends while CTA 0 may still read its shared memory
+}
+
+__global__ void __launch_bounds__(TOKENS_THREADS) batch_tokens_kernel(const BatchParams p) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const long long t0 = ((long long)blockIdx.x * TOKENS_THREADS + threadIdx.x) * 4;
+    if (t0 < p.max_tokens)
+        fill_tokens(p, t0, p.query_start[p.num_seqs], wide_tokens(p), p.query_start, p.context_lens);
 }
 
 cudaError_t launch_build_batch(const BatchParams& p, cudaStream_t stream) {
-    build_batch_kernel<<<BATCH_CTAS, BATCH_THREADS, 0, stream>>>(p);
-    return cudaGetLastError();
+    const bool one = p.num_seqs <= BATCH_ONE_CTA, fill = p.max_tokens <= BATCH_FEW_TOKENS;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(one ? 1 : BATCH_CTAS);
+    cfg.blockDim = dim3(BATCH_THREADS);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = cfg.gridDim.x;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = one ? 0 : 1;
+    cudaError_t e = one ? cudaLaunchKernelEx(&cfg, build_batch_kernel<1>, p, (int)fill)
+                        : cudaLaunchKernelEx(&cfg, build_batch_kernel<BATCH_CTAS>, p, (int)fill);
+    if (e != cudaSuccess || fill) return e;
+    cfg.gridDim = dim3((unsigned)(((long long)p.max_tokens + 4 * TOKENS_THREADS - 1) / (4 * TOKENS_THREADS)));
+    cfg.blockDim = dim3(TOKENS_THREADS);
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, batch_tokens_kernel, p);
 }
 
 }  // namespace pkv
