@@ -4,13 +4,16 @@
 // A tile is up to 2 * (128 / G) consecutive queries of one request; a tile and a kv head are
 // one item, whose steps are the 128-token stretches of the context its last query may see.
 // An item is cut into several pieces along the context only where that shortens the whole:
-// the cuts are tried for 1 to 32 pieces of the longest item, and the number with the
-// smallest estimate taken, in steps of one CTA,
-//   max(all steps / CTAs, min(rounds of pieces * (piece + F), all steps / CTAs + piece + F)) + merge
-// (the first form in min() when pieces are alike, the second, list scheduling's bound, when
-// they are not; F steps of fixed cost per piece).  Each cut item's pieces leave (m, l, o) per
-// row, merged by log-sum-exp.  Lengths and the number of CTAs decide everything here, so the
-// same batch is always cut, and summed, in the same way.
+// the cuts are tried for 1 to 32 pieces of the longest item, and the number with the smallest
+// estimate taken.  Pieces are handed out longest first, so the end comes close to the larger
+// of two lower bounds, in steps of one CTA with F steps of fixed cost per piece (measured: a
+// piece costs about 6000 cycles beside its steps of 2800):
+//   all steps / CTAs,
+//   ceil(pieces at least x long / CTAs) * x    for x = 4/4, 3/4, 2/4 and 1/4 of the longest
+// plus the merge of the cut rows (a launch, and PARTIAL_ROWS_PER_STEP rows written and read
+// again in the time of a step).  Each cut item's pieces leave (m, l, o) per row, merged by
+// log-sum-exp.  Lengths and the number of CTAs decide everything here, so the same batch is
+// always cut, and summed, in the same way.
 #include <cmath>
 
 #include "pkv_common.cuh"
@@ -20,6 +23,8 @@ namespace pkv {
 namespace {
 
 constexpr int PLAN_THREADS = 1024;
+constexpr float PARTIAL_ROWS_PER_STEP = 7000.f;  // of 128 values: 1 KB each at about 5 TB/s in 1.45 us
+constexpr int LENGTH_CLASSES = 16;
 
 __device__ __forceinline__ int4 add4(int4 a, int4 b) {
     return make_int4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
@@ -62,7 +67,7 @@ __device__ __forceinline__ int tile_steps(const int4& tile) {
 // of the batch fits into one round and go to the workspace when it does not.
 __global__ void __launch_bounds__(PLAN_THREADS) chunk_plan_kernel(const ChunkPlanParams p) {
     __shared__ int4 warp_sums[32];
-    __shared__ int max_steps_s;
+    __shared__ int max_steps_s, pieces_s;  // pieces_s: of the rounds so far
     __shared__ float est_s[32];
     __shared__ int start_s[PLAN_THREADS + 1], tile_start_s[PLAN_THREADS + 1], ctx_s[PLAN_THREADS];
     __shared__ int4 tiles_s[PLAN_THREADS];  // this round's tiles
@@ -79,7 +84,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) chunk_plan_kernel(const ChunkPla
     const int* ctxs = few ? ctx_s : p.context_lens;
     if (tid == 0) {
         tile_start[0] = 0;
-        max_steps_s = 0;
+        max_steps_s = pieces_s = 0;
     }
 
     // ---- tiles of each request
@@ -143,30 +148,36 @@ __global__ void __launch_bounds__(PLAN_THREADS) chunk_plan_kernel(const ChunkPla
     // ---- pieces of the longest item: candidate k = warp + 1
     int cut = max_steps;  // steps per piece at most
     if (p.max_partial_rows > 0 && max_steps >= CHUNK_SPLIT_MIN) {
-        const float F = 2.f, merge = 4.f;
+        const float F = 2.f;
         const int k = warp + 1, c = (max_steps + k - 1) / k;
         float all = 0.f;
-        int n_pieces = 0, rows = 0, cuts = 0;
+        int rows = 0, cuts = 0, longer[4] = {0, 0, 0, 0};
         for (int ti = lane; ti < num_tiles; ti += 32) {
             const int4 tile = tiles[ti];
             const int n = tile_steps(tile), pc = n > c ? (n + c - 1) / c : 1;
+            const int len = pc > 1 ? (n + pc - 1) / pc : n;
             all += (float)n + F * (float)pc;
-            n_pieces += pc;
             if (pc > 1) {
                 rows += pc * tile.z * p.group;
                 cuts += pc;
             }
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+                if (4 * len >= (4 - x) * c) longer[x] += pc;
         }
 #pragma unroll
         for (int o = 16; o >= 1; o >>= 1) all += __shfl_xor_sync(FULL_MASK, all, o);
-        n_pieces = __reduce_add_sync(FULL_MASK, n_pieces);
         rows = __reduce_add_sync(FULL_MASK, rows);
         cuts = __reduce_add_sync(FULL_MASK, cuts);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) longer[x] = __reduce_add_sync(FULL_MASK, longer[x]);
         if (lane == 0) {
             const float ctas = (float)p.num_sms, H = (float)p.num_kv_heads;
-            const float mean = all * H / ctas;
-            const float rounds = ceilf((float)n_pieces * H / ctas) * ((float)c + F);
-            float est = fmaxf(mean, fminf(rounds, mean + (float)c + F)) + (k > 1 ? merge : 0.f);
+            float est = all * H / ctas;
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+                est = fmaxf(est, ceilf((float)longer[x] * H / ctas) * (0.25f * (float)((4 - x) * c) + F));
+            if (k > 1) est += 3.f + (float)rows * H / PARTIAL_ROWS_PER_STEP;
             if (k > 1 && (c < 2 || (long long)rows * p.num_kv_heads > p.max_partial_rows ||
                           (long long)cuts * p.num_kv_heads > p.max_cut_pieces))
                 est = INFINITY;
@@ -180,28 +191,60 @@ __global__ void __launch_bounds__(PLAN_THREADS) chunk_plan_kernel(const ChunkPla
         cut = (max_steps + best) / (best + 1);
     }
 
-    // ---- the pieces, tile by tile, the heads of a tile behind one another
+    // ---- the pieces, the heads of a tile behind one another
     const int H = p.num_kv_heads;
     int4 base = make_int4(0, 0, 0, 0);  // pieces, partial rows, cut items, their rows
     for (int t0 = 0; t0 < num_tiles; t0 += PLAN_THREADS) {
         const int ti = t0 + tid;
+        const int live = min(PLAN_THREADS, num_tiles - t0);
         int4 tile = make_int4(0, 0, 0, 0);
-        int pc = 0;
+        int pc = 0, len = 0;
+        auto parts_of = [&](const int4& x) {
+            const int n = tile_steps(x);
+            return n > cut ? (n + cut - 1) / cut : 1;
+        };
         if (ti < num_tiles) {
             tile = tiles[ti];
-            const int n = tile_steps(tile);
-            pc = n > cut ? (n + cut - 1) / cut : 1;
+            pc = parts_of(tile);
+            len = tile_steps(tile) / pc;
+        }
+        const int round_pieces = H * __reduce_add_sync(FULL_MASK, pc);
+        if (lane == 0) atomicAdd(&pieces_s, round_pieces);
+        __syncthreads();
+        if (pieces_s > p.ctas) {
+            // longest pieces first: a counting sort of the round's tiles by length class, in
+            // tile order within a class
+            const int cls = ti < num_tiles ? min(LENGTH_CLASSES - 1, (cut - len) * LENGTH_CLASSES / max(cut, 1))
+                                           : LENGTH_CLASSES;  // no tile: behind the others
+            const unsigned same = __match_any_sync(FULL_MASK, cls);
+            const int before = __popc(same & ((1u << lane) - 1u));
+            // counts by (class, warp), then their sums: thread c * 32 + w holds class c of warp w
+            if (lane < LENGTH_CLASSES) first_s[lane * 32 + warp] = 0;
+            __syncwarp();
+            if (before == 0 && cls < LENGTH_CLASSES) first_s[cls * 32 + warp] = __popc(same);
+            __syncthreads();
+            const int count = tid < LENGTH_CLASSES * 32 ? first_s[tid] : 0;
+            int4 all_tiles;
+            const int4 upto = block_scan4(make_int4(count, 0, 0, 0), warp_sums, &all_tiles);
+            if (tid < LENGTH_CLASSES * 32) first_s[tid] = upto.x - count;
+            __syncthreads();
+            if (cls < LENGTH_CLASSES) tiles_s[first_s[cls * 32 + warp] + before] = tile;
+            __syncthreads();
+            if (ti < num_tiles) {
+                tile = tiles_s[tid];
+                pc = parts_of(tile);
+            }
+        } else if (ti < num_tiles) {
+            tiles_s[tid] = tile;
         }
         const int R = tile.z * p.group;
         const int4 mine = make_int4(H * pc, pc > 1 ? H * pc * R : 0, pc > 1 ? H : 0, pc > 1 ? H * R : 0);
         int4 total;
         const int4 v = block_scan4(mine, warp_sums, &total);
-        if (tiles != tiles_s) tiles_s[tid] = tile;
         first_s[tid] = v.x;
         base_s[tid] = make_int4(base.x + v.x - mine.x, base.y + v.y - mine.y, base.z + v.z - mine.z,
                                 base.w + v.w - mine.w);
         __syncthreads();
-        const int live = min(PLAN_THREADS, num_tiles - t0);
         for (int e = tid; e < total.x; e += PLAN_THREADS) {
             int lo = 0, hi = live - 1;
             while (lo < hi) {  // first tile whose pieces end past e
@@ -209,7 +252,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) chunk_plan_kernel(const ChunkPla
                 if (first_s[mid] > e) hi = mid; else lo = mid + 1;
             }
             const int4 x = tiles_s[lo], at = base_s[lo];
-            const int n = tile_steps(x), parts = n > cut ? (n + cut - 1) / cut : 1, rows = x.z * p.group;
+            const int n = tile_steps(x), parts = parts_of(x), rows = x.z * p.group;
             const int in_tile = base.x + e - at.x, h = in_tile / parts, r = in_tile - h * parts;
             const int token = starts[x.x] + x.y;
             ChunkPiece y;
