@@ -1044,7 +1044,7 @@ pkv_status pkv_paged_attention_chunk(const pkv_pool* pool, const void* q, int32_
     p.part_l = reinterpret_cast<float*>(ws + c.l);
     p.part_o = reinterpret_cast<float*>(ws + c.o);
     p.err = err;
-    if (pkv::launch_chunk_plan(pl, s) != cudaSuccess) return PKV_ERR_CUDA;
+    if (pkv::launch_chunk_plan(pl, c.tiles, s) != cudaSuccess) return PKV_ERR_CUDA;
     const cudaError_t e = pool->dtype == PKV_F16 ? pkv::launch_chunk<__half>(p, x, s)
                                                  : pkv::launch_chunk<__nv_bfloat16>(p, x, s);
     if (e == cudaErrorNotSupported) return PKV_ERR_UNSUPPORTED;

@@ -22,8 +22,8 @@ namespace pkv {
 
 namespace {
 
-constexpr int PLAN_THREADS = 1024;
 constexpr float PARTIAL_ROWS_PER_STEP = 7000.f;  // of 128 values: 1 KB each at about 5 TB/s in 1.45 us
+constexpr int PIECE_STEPS = 2;       // F above
 constexpr int LENGTH_CLASSES = 16;
 
 __device__ __forceinline__ int4 add4(int4 a, int4 b) {
@@ -40,18 +40,55 @@ __device__ __forceinline__ int4 warp_scan4(int4 v, int lane) {
     return v;
 }
 
-// Inclusive sums over the CTA; `total` gets the sums over all threads.
+__device__ __forceinline__ int warp_scan(int v, int lane) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(FULL_MASK, v, o);
+        if (lane >= o) v += u;
+    }
+    return v;
+}
+
+// Inclusive sums over the CTA's N threads; `total` gets the sums over all of them.
+template <int N>
 __device__ __forceinline__ int4 block_scan4(int4 v, int4* warp_sums, int4* total) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     v = warp_scan4(v, lane);
     if (lane == 31) warp_sums[warp] = v;
     __syncthreads();
-    if (warp == 0) warp_sums[lane] = warp_scan4(warp_sums[lane], lane);
-    __syncthreads();
-    if (warp > 0) v = add4(v, warp_sums[warp - 1]);
-    *total = warp_sums[31];
+    // every warp sums the warps before it itself: one barrier less
+    const int4 w = warp_scan4(lane < N / 32 ? warp_sums[lane] : make_int4(0, 0, 0, 0), lane);
+    const int from = warp > 0 ? warp - 1 : 0;
+    const int4 before = make_int4(__shfl_sync(FULL_MASK, w.x, from), __shfl_sync(FULL_MASK, w.y, from),
+                                  __shfl_sync(FULL_MASK, w.z, from), __shfl_sync(FULL_MASK, w.w, from));
+    if (warp > 0) v = add4(v, before);
+    *total = make_int4(__shfl_sync(FULL_MASK, w.x, 31), __shfl_sync(FULL_MASK, w.y, 31),
+                       __shfl_sync(FULL_MASK, w.z, 31), __shfl_sync(FULL_MASK, w.w, 31));
     __syncthreads();  // warp_sums is free again
     return v;
+}
+
+// The same for one value.
+template <int N>
+__device__ __forceinline__ int block_scan(int v, int4* warp_sums, int* total) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    v = warp_scan(v, lane);
+    if (lane == 31) warp_sums[warp].x = v;
+    __syncthreads();
+    const int w = warp_scan(lane < N / 32 ? warp_sums[lane].x : 0, lane);
+    const int before = __shfl_sync(FULL_MASK, w, warp > 0 ? warp - 1 : 0);
+    if (warp > 0) v += before;
+    *total = __shfl_sync(FULL_MASK, w, 31);
+    __syncthreads();
+    return v;
+}
+
+// ceil(n / c) for 0 <= n < 2^24 steps, 1 <= c: rounded from 32-bit floats, then set right.
+__device__ __forceinline__ int ceil_div_steps(int n, int c, float inv) {
+    const int m = n + c - 1;
+    int q = (int)((float)m * inv);
+    const int r = m - q * c;
+    return r < 0 ? q - 1 : r >= c ? q + 1 : q;
 }
 
 // Steps of a tile: 128-token stretches up to the last position its last query sees.
@@ -62,23 +99,24 @@ __device__ __forceinline__ int tile_steps(const int4& tile) {
 
 }  // namespace
 
-// One CTA: it is a chain of short dependent steps (load the lengths, sum, search, choose, sum,
-// write), 1024 requests and 1024 tiles at a time, whose arrays stay in shared memory when all
+// One CTA: it is a chain of short dependent steps (load the lengths, sum, search, choose, sort,
+// sum, write), N requests and N tiles at a time, whose arrays stay in shared memory when all
 // of the batch fits into one round and go to the workspace when it does not.
-__global__ void __launch_bounds__(PLAN_THREADS) chunk_plan_kernel(const ChunkPlanParams p) {
+template <int N>
+__global__ void __launch_bounds__(N) chunk_plan_kernel(const ChunkPlanParams p) {
     __shared__ int4 warp_sums[32];
     __shared__ int max_steps_s, pieces_s;  // pieces_s: of the rounds so far
-    __shared__ float est_s[32];
-    __shared__ int start_s[PLAN_THREADS + 1], tile_start_s[PLAN_THREADS + 1], ctx_s[PLAN_THREADS];
-    __shared__ int4 tiles_s[PLAN_THREADS];  // this round's tiles
-    __shared__ int first_s[PLAN_THREADS];   // pieces up to and with each of them
-    __shared__ int4 base_s[PLAN_THREADS];   // pieces, partial rows, cut items, their rows before it
+    __shared__ int sums_s[7][32];  // of each candidate
+    __shared__ int start_s[N + 1], tile_start_s[N + 1], ctx_s[N];
+    __shared__ int4 tiles_s[N];  // this round's tiles
+    __shared__ int first_s[N];   // tiles before, by (class, warp)
+    __shared__ int4 base_s[N];   // pieces, partial rows, cut items, their rows before it
     // the attention kernel may set itself up meanwhile; it waits for this grid's end
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int QT = 2 * (128 / p.group);  // queries per tile
-    const bool few = p.num_seqs <= PLAN_THREADS;
+    const bool few = p.num_seqs <= N;
     int* tile_start = few ? tile_start_s : p.tile_start;
     const int* starts = few ? start_s : p.query_start;
     const int* ctxs = few ? ctx_s : p.context_lens;
@@ -86,10 +124,11 @@ __global__ void __launch_bounds__(PLAN_THREADS) chunk_plan_kernel(const ChunkPla
         tile_start[0] = 0;
         max_steps_s = pieces_s = 0;
     }
+    for (int i = tid; i < 7 * 32; i += N) sums_s[i >> 5][i & 31] = 0;
 
     // ---- tiles of each request
     int carry = 0;
-    for (int s0 = 0; s0 < p.num_seqs; s0 += PLAN_THREADS) {
+    for (int s0 = 0; s0 < p.num_seqs; s0 += N) {
         const int s = s0 + tid;
         int nt = 0;
         bool bad = false;
@@ -111,19 +150,19 @@ __global__ void __launch_bounds__(PLAN_THREADS) chunk_plan_kernel(const ChunkPla
             }
             return;
         }
-        int4 total;
-        const int4 v = block_scan4(make_int4(nt, 0, 0, 0), warp_sums, &total);
-        if (s < p.num_seqs) tile_start[s + 1] = carry + v.x;
-        carry += total.x;
+        int total;
+        const int v = block_scan<N>(nt, warp_sums, &total);
+        if (s < p.num_seqs) tile_start[s + 1] = carry + v;
+        carry += total;
     }
     const int num_tiles = carry;
-    int4* tiles = num_tiles <= PLAN_THREADS ? tiles_s : p.tiles;
+    int4* tiles = num_tiles <= N ? tiles_s : p.tiles;
     __syncthreads();
 
     // ---- one record per tile, the longest of a request first
     const long long cap = min((long long)p.max_blocks_per_seq * p.block_size, (long long)p.max_context_len);
     int steps = 0;
-    for (int ti = tid; ti < num_tiles; ti += PLAN_THREADS) {
+    for (int ti = tid; ti < num_tiles; ti += N) {
         int lo = 0, hi = p.num_seqs - 1;
         while (lo < hi) {  // first request whose tiles end past ti
             const int mid = (lo + hi) >> 1;
@@ -145,63 +184,65 @@ __global__ void __launch_bounds__(PLAN_THREADS) chunk_plan_kernel(const ChunkPla
     __syncthreads();
     const int max_steps = max_steps_s;
 
-    // ---- pieces of the longest item: candidate k = warp + 1
-    int cut = max_steps;  // steps per piece at most
+    // ---- pieces of the longest item: 32 candidates, some for each warp
+    int cut = max(max_steps, 1);  // steps per piece at most
     if (p.max_partial_rows > 0 && max_steps >= CHUNK_SPLIT_MIN) {
-        const float F = 2.f;
-        const int k = warp + 1, c = (max_steps + k - 1) / k;
-        float all = 0.f;
-        int rows = 0, cuts = 0, longer[4] = {0, 0, 0, 0};
-        for (int ti = lane; ti < num_tiles; ti += 32) {
+        // lane k - 1 of every warp: candidate k's steps per piece
+        const int my_c = (int)ceilf(__fdividef((float)max_steps, (float)(lane + 1)));
+        const float my_inv = __fdividef(1.f, (float)my_c);
+        int all = 0, rows = 0, cuts = 0, longer[4] = {0, 0, 0, 0};
+        for (int ti = warp; ti < num_tiles; ti += N / 32) {
             const int4 tile = tiles[ti];
-            const int n = tile_steps(tile), pc = n > c ? (n + c - 1) / c : 1;
-            const int len = pc > 1 ? (n + pc - 1) / pc : n;
-            all += (float)n + F * (float)pc;
+            const int n = tile_steps(tile), pc = n > my_c ? ceil_div_steps(n, my_c, my_inv) : 1;
+            all += n + PIECE_STEPS * pc;
             if (pc > 1) {
                 rows += pc * tile.z * p.group;
                 cuts += pc;
             }
+            // the longest of the tile's pieces counts for all of them
 #pragma unroll
             for (int x = 0; x < 4; ++x)
-                if (4 * len >= (4 - x) * c) longer[x] += pc;
+                if (4 * (n + pc - 1) >= (4 - x) * my_c * pc) longer[x] += pc;
         }
+        atomicAdd(&sums_s[0][lane], all);
+        atomicAdd(&sums_s[1][lane], rows);
+        atomicAdd(&sums_s[2][lane], cuts);
 #pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) all += __shfl_xor_sync(FULL_MASK, all, o);
-        rows = __reduce_add_sync(FULL_MASK, rows);
-        cuts = __reduce_add_sync(FULL_MASK, cuts);
-#pragma unroll
-        for (int x = 0; x < 4; ++x) longer[x] = __reduce_add_sync(FULL_MASK, longer[x]);
-        if (lane == 0) {
-            const float ctas = (float)p.num_sms, H = (float)p.num_kv_heads;
-            float est = all * H / ctas;
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-                est = fmaxf(est, ceilf((float)longer[x] * H / ctas) * (0.25f * (float)((4 - x) * c) + F));
-            if (k > 1) est += 3.f + (float)rows * H / PARTIAL_ROWS_PER_STEP;
-            if (k > 1 && (c < 2 || (long long)rows * p.num_kv_heads > p.max_partial_rows ||
-                          (long long)cuts * p.num_kv_heads > p.max_cut_pieces))
-                est = INFINITY;
-            est_s[warp] = est;
-        }
+        for (int x = 0; x < 4; ++x) atomicAdd(&sums_s[3 + x][lane], longer[x]);
         __syncthreads();
+        // lane k - 1 of every warp: candidate k's estimate
+        const float H = (float)p.num_kv_heads, inv_sms = __fdividef(1.f, (float)p.num_sms);
+        rows = sums_s[1][lane];
+        cuts = sums_s[2][lane];
+        float est = (float)sums_s[0][lane] * H * inv_sms;
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+            est = fmaxf(est, ceilf((float)sums_s[3 + x][lane] * H * inv_sms - 1e-4f) *
+                                 (0.25f * (float)((4 - x) * my_c) + (float)PIECE_STEPS));
+        if (lane > 0) {
+            est += 3.f + (float)rows * H * (1.f / PARTIAL_ROWS_PER_STEP);
+            if (my_c < 2 || (long long)rows * p.num_kv_heads > p.max_partial_rows ||
+                (long long)cuts * p.num_kv_heads > p.max_cut_pieces)
+                est = INFINITY;
+        }
         // the smallest estimate, the fewest pieces among equals (estimates are not negative, so
         // their bits order like their values)
-        const unsigned mine = __float_as_uint(est_s[lane]), least = __reduce_min_sync(FULL_MASK, mine);
-        const int best = __ffs(__ballot_sync(FULL_MASK, mine == least)) - 1;
-        cut = (max_steps + best) / (best + 1);
+        const unsigned mine = __float_as_uint(est), least = __reduce_min_sync(FULL_MASK, mine);
+        cut = __shfl_sync(FULL_MASK, my_c, __ffs(__ballot_sync(FULL_MASK, mine == least)) - 1);
     }
 
     // ---- the pieces, the heads of a tile behind one another
+    const float inv_cut = 1.f / (float)cut;
     const int H = p.num_kv_heads;
     int4 base = make_int4(0, 0, 0, 0);  // pieces, partial rows, cut items, their rows
-    for (int t0 = 0; t0 < num_tiles; t0 += PLAN_THREADS) {
+    for (int t0 = 0; t0 < num_tiles; t0 += N) {
         const int ti = t0 + tid;
-        const int live = min(PLAN_THREADS, num_tiles - t0);
+        const int live = min(N, num_tiles - t0);
         int4 tile = make_int4(0, 0, 0, 0);
         int pc = 0, len = 0;
         auto parts_of = [&](const int4& x) {
             const int n = tile_steps(x);
-            return n > cut ? (n + cut - 1) / cut : 1;
+            return n > cut ? ceil_div_steps(n, cut, inv_cut) : 1;
         };
         if (ti < num_tiles) {
             tile = tiles[ti];
@@ -214,21 +255,23 @@ __global__ void __launch_bounds__(PLAN_THREADS) chunk_plan_kernel(const ChunkPla
         if (pieces_s > p.ctas) {
             // longest pieces first: a counting sort of the round's tiles by length class, in
             // tile order within a class
-            const int cls = ti < num_tiles ? min(LENGTH_CLASSES - 1, (cut - len) * LENGTH_CLASSES / max(cut, 1))
+            const int cls = ti < num_tiles ? min(LENGTH_CLASSES - 1, (int)((float)((cut - len) * LENGTH_CLASSES) * inv_cut))
                                            : LENGTH_CLASSES;  // no tile: behind the others
             const unsigned same = __match_any_sync(FULL_MASK, cls);
             const int before = __popc(same & ((1u << lane) - 1u));
-            // counts by (class, warp), then their sums: thread c * 32 + w holds class c of warp w
-            if (lane < LENGTH_CLASSES) first_s[lane * 32 + warp] = 0;
+            // counts by (class, warp), then their sums: entry c * W + w is class c of warp w
+            constexpr int W = N / 32, COUNTS = LENGTH_CLASSES * W;
+            static_assert(COUNTS <= N, "one count per thread");
+            if (lane < LENGTH_CLASSES) first_s[lane * W + warp] = 0;
             __syncwarp();
-            if (before == 0 && cls < LENGTH_CLASSES) first_s[cls * 32 + warp] = __popc(same);
+            if (before == 0 && cls < LENGTH_CLASSES) first_s[cls * W + warp] = __popc(same);
             __syncthreads();
-            const int count = tid < LENGTH_CLASSES * 32 ? first_s[tid] : 0;
-            int4 all_tiles;
-            const int4 upto = block_scan4(make_int4(count, 0, 0, 0), warp_sums, &all_tiles);
-            if (tid < LENGTH_CLASSES * 32) first_s[tid] = upto.x - count;
+            const int count = tid < COUNTS ? first_s[tid] : 0;
+            int all_tiles;
+            const int upto = block_scan<N>(count, warp_sums, &all_tiles);
+            if (tid < COUNTS) first_s[tid] = upto - count;
             __syncthreads();
-            if (cls < LENGTH_CLASSES) tiles_s[first_s[cls * 32 + warp] + before] = tile;
+            if (cls < LENGTH_CLASSES) tiles_s[first_s[cls * W + warp] + before] = tile;
             __syncthreads();
             if (ti < num_tiles) {
                 tile = tiles_s[tid];
@@ -240,41 +283,42 @@ __global__ void __launch_bounds__(PLAN_THREADS) chunk_plan_kernel(const ChunkPla
         const int R = tile.z * p.group;
         const int4 mine = make_int4(H * pc, pc > 1 ? H * pc * R : 0, pc > 1 ? H : 0, pc > 1 ? H * R : 0);
         int4 total;
-        const int4 v = block_scan4(mine, warp_sums, &total);
-        first_s[tid] = v.x;
+        const int4 v = block_scan4<N>(mine, warp_sums, &total);
         base_s[tid] = make_int4(base.x + v.x - mine.x, base.y + v.y - mine.y, base.z + v.z - mine.z,
                                 base.w + v.w - mine.w);
         __syncthreads();
-        for (int e = tid; e < total.x; e += PLAN_THREADS) {
-            int lo = 0, hi = live - 1;
-            while (lo < hi) {  // first tile whose pieces end past e
-                const int mid = (lo + hi) >> 1;
-                if (first_s[mid] > e) hi = mid; else lo = mid + 1;
-            }
-            const int4 x = tiles_s[lo], at = base_s[lo];
+        // `lanes` lanes write a tile's pieces
+        const int lanes = H >= 32 ? 32 : 1 << (32 - __clz(max(H - 1, 0)));  // H rounded up to a power of two
+#pragma unroll 1
+        for (int k = tid / lanes; k < live; k += N / lanes) {
+            const int4 x = tiles_s[k], at = base_s[k];
             const int n = tile_steps(x), parts = parts_of(x), rows = x.z * p.group;
-            const int in_tile = base.x + e - at.x, h = in_tile / parts, r = in_tile - h * parts;
             const int token = starts[x.x] + x.y;
-            ChunkPiece y;
-            y.token = token;
-            y.kv_head = h;
-            y.queries = x.z;
-            y.lim0 = x.w;
-            y.seq = x.x;
-            y.kt0 = (int)((long long)n * r / parts);
-            y.kt1 = (int)((long long)n * (r + 1) / parts);
-            y.part_row = parts > 1 ? at.y + in_tile * rows : -1;
-            p.pieces[base.x + e] = y;
-            if (parts > 1 && r == 0) {
-                ChunkMerge m;
-                m.token = token;
-                m.kv_head = h;
-                m.rows = rows;
-                m.parts = parts;
-                m.part_row = y.part_row;
-                m.first = at.w + h * rows;
-                m.pad0 = m.pad1 = 0;
-                p.merges[at.z + h] = m;
+#pragma unroll 1
+            for (int e = tid & (lanes - 1); e < H * parts; e += lanes) {
+                const int h = parts > 1 ? e / parts : e, r = e - h * parts;
+                ChunkPiece y;
+                y.token = token;
+                y.kv_head = h;
+                y.queries = x.z;
+                y.lim0 = x.w;
+                y.seq = x.x;
+                // (at most 2^24 steps and 32 parts)
+                y.kt0 = parts > 1 ? (int)((unsigned)n * (unsigned)r / (unsigned)parts) : 0;
+                y.kt1 = parts > 1 ? (int)((unsigned)n * (unsigned)(r + 1) / (unsigned)parts) : n;
+                y.part_row = parts > 1 ? at.y + e * rows : -1;
+                p.pieces[at.x + e] = y;
+                if (parts > 1 && r == 0) {
+                    ChunkMerge m;
+                    m.token = token;
+                    m.kv_head = h;
+                    m.rows = rows;
+                    m.parts = parts;
+                    m.part_row = y.part_row;
+                    m.first = at.w + h * rows;
+                    m.pad0 = m.pad1 = 0;
+                    p.merges[at.z + h] = m;
+                }
             }
         }
         base = add4(base, total);
@@ -348,17 +392,20 @@ __global__ void __launch_bounds__(256) chunk_merge_kernel(const ChunkParams p) {
     }
 }
 
-cudaError_t launch_chunk_plan(const ChunkPlanParams& p, cudaStream_t stream) {
+cudaError_t launch_chunk_plan(const ChunkPlanParams& p, int64_t max_tiles, cudaStream_t stream) {
+    // few requests and tiles: fewer warps, whose sums and barriers are shorter
+    const bool few = p.num_seqs <= 256 && max_tiles <= 256;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(1);
-    cfg.blockDim = dim3(PLAN_THREADS);
+    cfg.blockDim = dim3(few ? 256 : 1024);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, chunk_plan_kernel, p);
+    return few ? cudaLaunchKernelEx(&cfg, chunk_plan_kernel<256>, p)
+               : cudaLaunchKernelEx(&cfg, chunk_plan_kernel<1024>, p);
 }
 
 cudaError_t launch_chunk_merge(const ChunkParams& p, int ctas, cudaStream_t stream) {

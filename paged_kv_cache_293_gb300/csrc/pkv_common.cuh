@@ -440,7 +440,7 @@ cudaError_t launch_free_sequences(const AllocatorState& a, int32_t B, int32_t* b
                                   unsigned int* err, cudaStream_t stream);
 cudaError_t launch_build_batch(const BatchParams& p, cudaStream_t stream);
 cudaError_t launch_rope_write(const RopeParams& p, int32_t dtype, cudaStream_t stream);
-cudaError_t launch_chunk_plan(const ChunkPlanParams& p, cudaStream_t stream);
+cudaError_t launch_chunk_plan(const ChunkPlanParams& p, int64_t max_tiles, cudaStream_t stream);
 template <typename T>
 cudaError_t launch_chunk(const ChunkParams& p, const ChunkTensors& x, cudaStream_t stream);
 cudaError_t launch_chunk_merge(const ChunkParams& p, int ctas, cudaStream_t stream);
