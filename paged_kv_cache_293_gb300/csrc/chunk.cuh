@@ -81,18 +81,6 @@ __device__ __forceinline__ uint64_t l2_evict_normal_policy() {
     return pol;
 }
 
-// As mbar_wait, for waits that mostly end within a microsecond: reading the global timer
-// takes about that long itself, so it is first read after WAIT_TRIES tries (each of which the
-// hardware may hold for a while).  With mbar_wait's read after the first try the two tiles'
-// hand-overs took 2800 cycles per step even without any softmax work.
-constexpr int WAIT_TRIES = 256;
-__device__ __forceinline__ bool mbar_wait_short(uint32_t bar, uint32_t parity) {
-#pragma unroll 1
-    for (int i = 0; i < WAIT_TRIES; ++i)
-        if (mbar_try_wait(bar, parity)) return true;
-    return mbar_wait(bar, parity);
-}
-
 template <int N>
 __device__ __forceinline__ void regs_dec() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));

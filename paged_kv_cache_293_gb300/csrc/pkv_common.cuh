@@ -261,6 +261,16 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity,
     }
 }
 
+// As mbar_wait, for waits that mostly end within a microsecond: the global timer, which takes
+// about that long to read, is first read after WAIT_TRIES tries.
+constexpr int WAIT_TRIES = 256;
+__device__ __forceinline__ bool mbar_wait_short(uint32_t bar, uint32_t parity) {
+#pragma unroll 1
+    for (int i = 0; i < WAIT_TRIES; ++i)
+        if (mbar_try_wait(bar, parity)) return true;
+    return mbar_wait(bar, parity);
+}
+
 // L2 policy for data read once per call: evict first, so the block tables,
 // queries and partial results stay resident.
 __device__ __forceinline__ uint64_t l2_evict_first_policy() {

@@ -187,7 +187,12 @@ def _rope_case(T, Hq, Hkv, D, B, dtype, norm, rot, pad, max_pos, seed, packed):
     (9, 12, 6, 128, 32, (1, 0), 48, False, 0, True),
     (64, 3, 3, 64, 16, (1, 1), 0, False, 0, True),
     (1500, 16, 4, 64, 16, (1, 1), 64, True, 2, True),
-    (3, 70, 1, 128, 16, (1, 1), 96, True, 0, True)])
+    (3, 70, 1, 128, 16, (1, 1), 96, True, 0, True),
+    # enough of them to be streamed
+    (2000, 20, 5, 128, 32, (1, 1), 128, False, 5, True),
+    (2101, 33, 9, 64, 16, (0, 1), 32, True, 1, True),
+    (1500, 21, 21, 128, 16, (1, 0), 0, False, 3, False),
+    (900, 52, 3, 128, 16, (1, 1), 128, True, 0, True)])
 def test_norm_rope_write(P, dtype, T, Hq, Hkv, D, B, norm, rot, inter, pad, packed):
     q, k, v, slots, pos, cs, w, kp, vp = _rope_case(T, Hq, Hkv, D, B, dtype, norm, rot, pad, 5000,
                                                     T + D, packed)
@@ -226,10 +231,11 @@ def test_norm_rope_write(P, dtype, T, Hq, Hkv, D, B, norm, rot, inter, pad, pack
     assert torch.equal(got, wk)
 
 
-def test_norm_rope_write_in_place_and_unrotated_infinities(P):
+@pytest.mark.parametrize("T", [33, 2200])
+def test_norm_rope_write_in_place_and_unrotated_infinities(P, T):
     """q_out may be q itself; elements past the rotated ones are not touched by the rotation,
     whatever they hold; a plain copy is exact."""
-    T, Hq, Hkv, D, B = 33, 8, 2, 128, 16
+    Hq, Hkv, D, B = 8, 2, 128, 16
     q, k, v, slots, pos, cs, _, kp, vp = _rope_case(T, Hq, Hkv, D, B, "f16", (0, 0), 64, 0, 300, 3, False)
     q[:, :, 100] = float("inf")
     v[3] = float("nan")
@@ -246,8 +252,9 @@ def test_norm_rope_write_in_place_and_unrotated_infinities(P):
     assert torch.isnan(gvp[s3 // B, :, s3 % B]).all() and torch.isnan(gvp).sum().item() == Hkv * D
 
 
-def test_norm_rope_write_bad_positions_and_slots(P):
-    T, Hq, Hkv, D, B = 6, 4, 2, 64, 16
+@pytest.mark.parametrize("T,Hq", [(6, 4), (2000, 48)])
+def test_norm_rope_write_bad_positions_and_slots(P, T, Hq):
+    Hkv, D, B = 2, 64, 16
     q, k, v, slots, pos, cs, _, kp, vp = _rope_case(T, Hq, Hkv, D, B, "bf16", (0, 0), 64, 0, 50, 4, True)
     pos[2] = 50
     slots[3] = kp.shape[0] * B
@@ -259,7 +266,7 @@ def test_norm_rope_write_bad_positions_and_slots(P):
     assert P.pkv_get_device_error() == P.DEVERR["POSITION"] | P.DEVERR["SLOT"]
     assert (out[2] == 5.0).all() and not (out[3] == 5.0).all()
     changed = (gvp.cpu() != vp).flatten(3).any(-1).transpose(1, 2).reshape(-1, Hkv).any(1).nonzero().flatten()
-    assert sorted(changed.tolist()) == sorted(int(slots[i]) for i in (0, 4, 5))
+    assert sorted(changed.tolist()) == sorted(int(slots[i]) for i in [0] + list(range(4, T)))
 
 
 # ---------------------------------------------------------------- chunk attention
