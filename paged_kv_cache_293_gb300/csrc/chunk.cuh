@@ -42,8 +42,8 @@ namespace pkv {
 
 constexpr int CHUNK_THREADS = 384;
 // Registers per thread: 168 at launch; the softmax warps take what the others give back
-// (256 * 200 + 128 * 104 = 384 * 168).
-constexpr int CHUNK_REGS_SOFTMAX = 200, CHUNK_REGS_OTHERS = 104;
+// (256 * 208 + 128 * 88 = 384 * 168).
+constexpr int CHUNK_REGS_SOFTMAX = 208, CHUNK_REGS_OTHERS = 88;
 constexpr float CHUNK_RESCALE_LOG2 = 8.f;
 
 template <int D>
