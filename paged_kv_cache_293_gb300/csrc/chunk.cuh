@@ -21,7 +21,9 @@
 //             Before a piece's last P.V the warp zeroes the V rows of the last 16-token copy
 //             past the last position the piece may see (they may hold anything; their
 //             weights are zero, and 0 * NaN is not).  Of a piece with one tile of queries
-//             the even and the odd steps' scores take the two tiles' places
+//             the even and the odd steps' scores take the two tiles' places; of one with at
+//             most CHUNK_FEW_ROWS rows each of warps 0-3 has all rows and a quarter of the
+//             tokens
 //   10        tensor copies of the query tiles
 //   11        none (fills the warpgroup)
 // The reference maximum of a row is raised only when a step's maximum exceeds it by more
@@ -45,6 +47,7 @@ constexpr int CHUNK_THREADS = 384;
 // (256 * 208 + 128 * 88 = 384 * 168).
 constexpr int CHUNK_REGS_SOFTMAX = 208, CHUNK_REGS_OTHERS = 88;
 constexpr float CHUNK_RESCALE_LOG2 = 8.f;
+constexpr int CHUNK_FEW_ROWS = 16;  // rows up to which a piece's steps are spread over four warps
 
 template <int D>
 struct ChunkSmem {
@@ -55,14 +58,18 @@ struct ChunkSmem {
     static constexpr int Q_OFF = 0;
     static constexpr int KV_OFF = 2 * TILE;
     static constexpr int BAR_OFF = KV_OFF + STAGES * TILE;
-    static constexpr int NBARS = 2 * STAGES + 25;
+    static constexpr int NBARS = 2 * STAGES + 28;
     static constexpr int PIECE_OFF = BAR_OFF + ((NBARS * 8 + 15) / 16) * 16;
-    static constexpr int TMEM_SLOT_OFF = PIECE_OFF + 2 * 32;
+    static constexpr int FEW_OFF = PIECE_OFF + 2 * 32;  // float [2][4][16]: m and l of the warps' rows
+    static constexpr int TMEM_SLOT_OFF = FEW_OFF + 2 * 4 * CHUNK_FEW_ROWS * 4;
     static constexpr int BYTES = TMEM_SLOT_OFF + 16 + 1024;  // + alignment slack
-    // tensor memory columns: S_0, S_1 (P over them), O_0, O_1
+    // tensor memory columns: S_0, S_1 (P over them), O_0, O_1; of a piece with few rows P has the
+    // last 128 columns
+    static constexpr uint32_t FEW_P_COL = 384;
     static constexpr uint32_t TMEM_COLS = 512;
     static constexpr uint32_t O_COL = 256;
     static_assert(D == 64 || D == 128, "head_dim");
+    static_assert(4 * CHUNK_FEW_ROWS * D * 4 <= TILE, "the warps' rows meet in the second Q tile");
     static_assert(BYTES <= 227 * 1024, "shared memory");
 };
 
@@ -191,9 +198,79 @@ __device__ __forceinline__ bool softmax_step(uint32_t s_t, uint32_t o_t, int see
     return true;
 }
 
+// One step of a row of a piece with few rows: this warp's 32 scores at s_t, the reference, sum
+// and O as in softmax_step, the weights to p_t.  The caller hands them on.
+template <typename T, int D>
+__device__ __forceinline__ bool few_rows_step(uint32_t s_t, uint32_t p_t, uint32_t o_t, int seen, bool has_o,
+                                              float scale_log2, float& m_ref, float& l, uint32_t bar_o,
+                                              uint32_t phase_o) {
+    uint32_t raw[32];
+    umma::ld32_async(s_t, raw);
+    umma::wait_ld(raw);
+    if (__any_sync(FULL_MASK, seen < 32)) {
+#pragma unroll
+        for (int k = 0; k < 32; ++k)
+            if (k >= seen) raw[k] = 0xff800000u;  // -inf
+    }
+    float top[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        top[c] = fmaxf(__uint_as_float(raw[c]), __uint_as_float(raw[c + 28]));
+#pragma unroll
+        for (int k = c + 4; k < 28; k += 8)
+            top[c] = max3(top[c], __uint_as_float(raw[k]), __uint_as_float(raw[k + 4 < 28 ? k + 4 : k]));
+    }
+    const float cm = max3(top[0], top[1], fmaxf(top[2], top[3])) * scale_log2;
+    const bool need = cm > m_ref + CHUNK_RESCALE_LOG2;
+    if (__any_sync(FULL_MASK, need)) {
+        float alpha = 1.f;
+        if (need) {
+            alpha = fast_exp2(m_ref - cm);
+            m_ref = cm;
+        }
+        l *= alpha;
+        if (has_o) {  // rows whose reference rose: scale their O, complete through the step before
+            if (!__all_sync(FULL_MASK, mbar_wait_short(bar_o, phase_o & 1))) return false;
+            umma::fence_after_sync();
+#pragma unroll 1
+            for (int d = 0; d < D; d += 16) {
+                float o[16];
+                umma::ld16(o_t + d, o);
+                uint32_t w[16];
+#pragma unroll
+                for (int k = 0; k < 16; ++k) w[k] = __float_as_uint(o[k] * alpha);
+                umma::st16(o_t + d, w);
+            }
+        }
+    }
+    const float neg = m_ref == -INFINITY ? 0.f : -m_ref;
+    const uint64_t scale2 = pack2(scale_log2, scale_log2), neg2 = pack2(neg, neg);
+    uint64_t sum2[2] = {0, 0};
+    uint32_t hi[16];
+#pragma unroll
+    for (int k = 0; k < 32; k += 2) {
+        float a, b;
+        unpack2(fma2(pack2(__uint_as_float(raw[k]), __uint_as_float(raw[k + 1])), scale2, neg2), a, b);
+        a = fast_exp2(a);
+        b = fast_exp2(b);
+        sum2[(k >> 1) & 1] = add2(sum2[(k >> 1) & 1], pack2(a, b));
+        hi[k / 2] = Mma<T>::pack(a, b);
+    }
+    umma::st16(p_t, hi);
+    float part[4];
+    unpack2(sum2[0], part[0], part[1]);
+    unpack2(sum2[1], part[2], part[3]);
+    l += (part[0] + part[1]) + (part[2] + part[3]);
+    umma::wait_st();
+    umma::fence_before_sync();
+    __syncwarp();
+    return true;
+}
+
 template <typename T, int D, bool SPLIT_P>
 __global__ void __launch_bounds__(CHUNK_THREADS, 1)
 chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
+                       const __grid_constant__ CUtensorMap tmap_q32,
                        const __grid_constant__ CUtensorMap tmap_k,
                        const __grid_constant__ CUtensorMap tmap_v, const ChunkParams p) {
     using L = ChunkSmem<D>;
@@ -210,6 +287,7 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sbase = smem_addr(smem);
     const uint32_t q_s = sbase + L::Q_OFF, ring = sbase + L::KV_OFF, bar0 = sbase + L::BAR_OFF;
+    const int G = p.group, QPT = 128 / G;  // heads per kv head, queries per tile
     // barriers: K / V stage landed and free; Q tile landed and free; a piece's last P.V
     // done; piece published and read; every MMA done; the P.V of an even or odd step
     // of a piece with one tile of queries done (a barrier each: a warp may be a step ahead of
@@ -230,11 +308,16 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
     // tile's warps take no part in them)
     auto s_full = [&](int i) { return bar0 + 8 * (NB + 13 + i); };
     auto p_full = [&](int i, int h) { return bar0 + 8 * (NB + 17 + 2 * i + h); };
+    // the second tile's output has been read; the four warps' rows of a piece with few rows are
+    // in shared memory, and have been read
+    const uint32_t o_read = bar0 + 8 * (NB + 25), few_done = bar0 + 8 * (NB + 26), few_read = bar0 + 8 * (NB + 27);
+    auto is_few = [&](const ChunkPiece& x) {
+        return !SPLIT_P && x.queries * G <= CHUNK_FEW_ROWS && x.kt1 > x.kt0;
+    };
     ChunkPiece* pieces = reinterpret_cast<ChunkPiece*>(smem + L::PIECE_OFF);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::TMEM_SLOT_OFF);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int G = p.group, QPT = 128 / G;  // heads per kv head, queries per tile
 
     if (threadIdx.x == 0) {
         for (int st = 0; st < NS; ++st) {
@@ -255,6 +338,9 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
             mbar_init(piece_empty(t), CONSUMERS);
         }
         mbar_init(all_done, 1);
+        mbar_init(o_read, 4);
+        mbar_init(few_done, 4);
+        mbar_init(few_read, 4);
         mbar_init_fence();
     }
     if (warp == MMA_WARP) umma::alloc(smem_addr(tmem_slot), L::TMEM_COLS);
@@ -360,26 +446,41 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
     } else if (warp == Q_WARP) {
         regs_dec<CHUNK_REGS_OTHERS>();
         // ---- query tiles
-        int used[2] = {0, 0};
+        int loads[2] = {0, 0}, uses[2] = {0, 0};  // of each tile: copies in, and times it was taken
         ChunkPiece pc;
         for (int i = 0; next_piece(i, pc); ++i) {
             if (pc.kt1 <= pc.kt0) continue;
-            for (int t = 0; t < (pc.queries > QPT ? 2 : 1); ++t) {
-                if (used[t] > 0) ok = __all_sync(FULL_MASK, mbar_wait_short(q_empty(t), (used[t] - 1) & 1));
+            // a piece with few rows has them in tile 0 four times, 32 rows apart, and takes tile
+            // 1 for the warps' results
+            const bool few = is_few(pc);
+            for (int t = 0; t < (few || pc.queries > QPT ? 2 : 1); ++t) {
+                if (uses[t] > 0)
+                    ok = __all_sync(FULL_MASK, mbar_wait_short(q_empty(t), (uses[t] - 1) & 1));
                 if (!ok) break;
-                ++used[t];
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(q_full(t), L::BOXES * QPT * G * 128);
-                    for (int x = 0; x < L::BOXES; ++x)
-                        tma_load_4d(q_s + t * L::TILE + x * L::BOX, &tmap_q, 0, x, pc.kv_head * G,
-                                    pc.token + t * QPT, q_full(t));
+                ++uses[t];
+                if (few && t == 1) continue;
+                ++loads[t];
+                if (umma::elect_one()) {
+                    const uint32_t dst = q_s + t * L::TILE;
+                    if (few) {
+                        mbar_arrive_expect_tx(q_full(0), 4 * L::BOXES * (32 / G) * G * 128);
+                        for (int w = 0; w < 4; ++w)
+                            for (int x = 0; x < L::BOXES; ++x)
+                                tma_load_4d(dst + x * L::BOX + w * 32 * 128, &tmap_q32, 0, x, pc.kv_head * G,
+                                            pc.token, q_full(0));
+                    } else {
+                        mbar_arrive_expect_tx(q_full(t), L::BOXES * QPT * G * 128);
+                        for (int x = 0; x < L::BOXES; ++x)
+                            tma_load_4d(dst + x * L::BOX, &tmap_q, 0, x, pc.kv_head * G, pc.token + t * QPT,
+                                        q_full(t));
+                    }
                 }
                 __syncwarp();
             }
             if (!ok) break;
         }
         for (int t = 0; t < 2; ++t)
-            if (used[t] > 0) mbar_wait_short(q_full(t), (used[t] - 1) & 1);
+            if (loads[t] > 0) mbar_wait_short(q_full(t), (loads[t] - 1) & 1);
     } else if (warp == MMA_WARP) {
         regs_dec<CHUNK_REGS_OTHERS>();
         // ---- MMA issue, the two tiles in turn: one thread for both, because MMAs issued by
@@ -399,12 +500,13 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
             }
             umma::commit(s_full(i));  // also says that every P.V before is done
         };
-        auto issue_pv = [&](int i, int st, bool first) -> bool {
+        auto issue_pv = [&](int i, int st, bool first, bool few = false) -> bool {
             // V is N-major: 64-element columns 2048 apart, 8-token groups 1024, and a K step
             // is one copy's 16 tokens.  The first half's products run while the softmax still
             // works on the second half.
             const uint64_t v_desc = umma::sw128_desc(ring + st * L::TILE, CHUNK_TOKENS * 128, 1024);
-            const uint32_t s_t = tmem + (i & 1) * CHUNK_TILE, o_t = tmem + L::O_COL + (i == 1 ? D : 0);
+            const uint32_t o_t = tmem + L::O_COL + (i == 1 ? D : 0);
+            const uint32_t p_t = tmem + (few ? L::FEW_P_COL + (i & 1) * (CHUNK_TILE / 2) : (i & 1) * CHUNK_TILE);
             const uint32_t parity = steps[i]++ & 1;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -413,8 +515,8 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
 #pragma unroll
                 for (int k = 4 * h; k < 4 * h + 4; ++k) {
                     const uint64_t bv = v_desc + (k * CHUNK_TOKENS * D * 2 >> 4);
-                    umma::mma_f16_tmem_a(o_t, s_t + k * 8, bv, IDESC_O, (!first || k > 0) ? 1u : 0u);
-                    if (SPLIT_P) umma::mma_f16_tmem_a(o_t, s_t + CHUNK_TILE / 2 + k * 8, bv, IDESC_O, 1u);
+                    umma::mma_f16_tmem_a(o_t, p_t + k * 8, bv, IDESC_O, (!first || k > 0) ? 1u : 0u);
+                    if (SPLIT_P) umma::mma_f16_tmem_a(o_t, p_t + CHUNK_TILE / 2 + k * 8, bv, IDESC_O, 1u);
                 }
             }
             return true;
@@ -423,7 +525,7 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
         for (int i = 0; next_piece(i, pc); ++i) {
             const int n = pc.kt1 - pc.kt0;
             if (n <= 0) continue;
-            const bool two = pc.queries > QPT;
+            const bool two = pc.queries > QPT, few = is_few(pc);
             int st = (int)(total % NS);  // next stage and its phase
             uint32_t phase = (total / NS) & 1;
             auto landed = [&] { return mbar_wait_short(kv_full(st), phase); };
@@ -451,7 +553,7 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
                     ok = mbar_wait_short(q_full(0), used[0] & 1) && scores(0) && (n == 1 || scores(1));
 #pragma unroll 1
                     for (int j = 0; j < n - 1 && ok; ++j) {
-                        ok = in(2 * j + 1) && issue_pv(2 + (j & 1), stage(2 * j + 1), j == 0);
+                        ok = in(2 * j + 1) && issue_pv(2 + (j & 1), stage(2 * j + 1), j == 0, few);
                         if (!ok) break;
                         umma::commit(pv_step(j & 1));
                         umma::commit(kv_empty(stage(2 * j + 1)));
@@ -515,7 +617,7 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
             }
             if (!two) {
                 if (umma::elect_one()) {
-                    ok = landed() && issue_pv(2 + ((n - 1) & 1), st, n == 1);
+                    ok = landed() && issue_pv(2 + ((n - 1) & 1), st, n == 1, few);
                     if (ok) umma::commit(pv_step((n - 1) & 1));
                     if (ok) umma::commit(kv_empty(st));
                 }
@@ -546,12 +648,130 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
         const uint32_t o_t = lane_tmem + L::O_COL + t * D;
         const int jq = t * QPT + r / G, hg = r % G;  // query within the piece, head of the group
         int taken = 0, taken_even = 0, taken_odd = 0;  // S tiles so far: the phases of s_full and pv_step
-        int ends = 0;  // two-tile pieces so far: the phase of pv_done
+        int ends = 0;  // two-tile pieces so far: the phase of pv_done and o_read
+        int fews = 0;  // pieces with few rows so far: the phase of few_done and few_read
+        bool p_clear = false;  // the P columns of such pieces hold zeros where they should
         ChunkPiece pc;
         for (int i = 0; next_piece(i, pc); ++i) {
             const int n = max(pc.kt1 - pc.kt0, 0);
             const bool two = pc.queries > QPT;
             if (t == 1 && !two) continue;  // the other warpgroup takes both S tiles in turn
+            if (is_few(pc)) {
+                // Few rows: warp w has them all, in its own 32 lanes, and of every step the tokens
+                // 32 w .. 32 w + 31, its own reference, sum and O; its P holds zeros for the other
+                // tokens.  A step's softmax takes a quarter of the time, and the step that of its
+                // copies.
+                const int rows = pc.queries * G, lim_w = pc.lim0 + min(lane, rows - 1) / G - warp * 32;
+                const uint32_t p_t = lane_tmem + L::FEW_P_COL;
+                if (!p_clear) {
+                    // O_1 lies there: the other warps have read it
+                    if (ends > 0) ok = __all_sync(FULL_MASK, mbar_wait_short(o_read, (ends - 1) & 1));
+                    if (!ok) break;
+                    umma::fence_after_sync();
+                    const uint32_t zeros[16] = {0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll 1
+                    for (int c = 0; c < CHUNK_TILE; c += 16) umma::st16(p_t + c, zeros);
+                    umma::wait_st();
+                    p_clear = true;
+                }
+                float m_ref = -INFINITY, l = 0.f;
+                for (int j = 0; j < n; ++j) {
+                    const int b = j & 1, phase = b ? taken_odd++ : taken_even++;
+                    ok = __all_sync(FULL_MASK, mbar_wait_short(s_full(2 + b), phase & 1));
+                    if (!ok) break;
+                    umma::fence_after_sync();
+                    ok = few_rows_step<T, D>(lane_tmem + b * CHUNK_TILE + warp * 32,
+                                             p_t + b * (CHUNK_TILE / 2) + warp * 16, o_t,
+                                             lim_w - (pc.kt0 + j) * CHUNK_TILE, j > 0, p.scale_log2, m_ref, l,
+                                             pv_step(b ^ 1), (b ? taken_even : taken_odd) - 1);
+                    if (!ok) break;
+                    if (lane == 0) {
+                        mbar_arrive(p_full(2 + b, 0));
+                        mbar_arrive(p_full(2 + b, 1));
+                    }
+                }
+                if (!ok) break;
+                const int last = (n - 1) & 1;
+                ok = __all_sync(FULL_MASK,
+                                mbar_wait_short(pv_step(last), ((last ? taken_odd : taken_even) - 1) & 1));
+                if (!ok) break;
+                umma::fence_after_sync();
+                // the four results of each row meet in the second Q tile; row r's 16-byte columns
+                // are turned by r, so that a warp's stores spread over the banks
+                constexpr int COLS = D / 4;
+                float4* rows_s = reinterpret_cast<float4*>(smem + L::Q_OFF + L::TILE);
+                float* m_s = reinterpret_cast<float*>(smem + L::FEW_OFF);
+                float* l_s = m_s + 4 * CHUNK_FEW_ROWS;
+#pragma unroll 1
+                for (int c = 0; c < D; c += 16) {
+                    float o[16];
+                    umma::ld16(o_t + c, o);
+                    if (lane < rows) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            rows_s[(warp * CHUNK_FEW_ROWS + lane) * COLS + (c / 4 + k + lane) % COLS] =
+                                make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                    }
+                    __syncwarp();
+                }
+                if (lane < rows) {
+                    m_s[warp * CHUNK_FEW_ROWS + lane] = m_ref;
+                    l_s[warp * CHUNK_FEW_ROWS + lane] = l;
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(few_done);
+                ok = __all_sync(FULL_MASK, mbar_wait_short(few_done, fews & 1));
+                if (!ok) break;
+                for (int x = warp; x < rows; x += 4) {
+                    float M = -INFINITY, sum = 0.f, f[4];
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) M = fmaxf(M, m_s[w * CHUNK_FEW_ROWS + x]);
+                    const float ref = M == -INFINITY ? 0.f : M;
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+                        f[w] = fast_exp2(m_s[w * CHUNK_FEW_ROWS + x] - ref);
+                        sum = fmaf(f[w], l_s[w * CHUNK_FEW_ROWS + x], sum);
+                    }
+                    const bool direct = pc.part_row < 0;
+                    const float inv = !direct ? 1.f : sum > 0.f ? 1.f / sum : 0.f;
+                    const long long out_row =
+                        ((long long)pc.token + x / G) * p.num_q_heads + pc.kv_head * G + x % G;
+                    const long long part_row = (long long)pc.part_row + x;
+                    if (lane < COLS) {
+                        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                        for (int w = 0; w < 4; ++w) {
+                            const float4 y = rows_s[(w * CHUNK_FEW_ROWS + x) * COLS + (lane + x) % COLS];
+                            const float fw = f[w] * inv;
+                            o.x = fmaf(fw, y.x, o.x);
+                            o.y = fmaf(fw, y.y, o.y);
+                            o.z = fmaf(fw, y.z, o.z);
+                            o.w = fmaf(fw, y.w, o.w);
+                        }
+                        if (direct)
+                            reinterpret_cast<uint2*>(static_cast<T*>(p.out) + out_row * D)[lane] =
+                                make_uint2(Mma<T>::pack(o.x, o.y), Mma<T>::pack(o.z, o.w));
+                        else
+                            reinterpret_cast<float4*>(p.part_o + part_row * D)[lane] = o;
+                    }
+                    if (!direct && lane == 0) {
+                        p.part_m[part_row] = M;  // base 2
+                        p.part_l[part_row] = sum;
+                    }
+                }
+                // the second Q tile goes back when all four have read it
+                fence_proxy_async_shared();
+                umma::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(few_read);
+                if (warp == 0) {
+                    ok = __all_sync(FULL_MASK, mbar_wait_short(few_read, fews & 1));
+                    if (!ok) break;
+                    if (lane == 0) mbar_arrive(q_empty(1));
+                }
+                ++fews;
+                continue;
+            }
             const bool valid = r < QPT * G && jq < pc.queries;
             const bool busy = __any_sync(FULL_MASK, valid);
             const int lim = pc.lim0 + jq;
@@ -585,6 +805,7 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
             if (n > 0) {
                 if (two) {
                     ok = __all_sync(FULL_MASK, mbar_wait_short(pv_done(t), ends & 1));
+                    p_clear = false;
                     ++ends;
                 } else {
                     const int last = (n - 1) & 1;
@@ -638,6 +859,11 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
                     p.part_l[part_row] = l;
                 }
             }
+            if (t == 1 && n > 0) {
+                umma::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(o_read);
+            }
         }
     }
     if (!ok && lane == 0) set_error(p.err, PKV_DEVERR_TIMEOUT);
@@ -651,15 +877,15 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
     }
 }
 
-// q seen as [T][Hq][D / 64][64]: a box is the G heads of one kv head for 128 / G tokens, one
+// q seen as [T][Hq][D / 64][64]: a box is the G heads of one kv head for `tokens` tokens, one
 // 128-byte column, landing as rows (token, head) of 128 bytes with the 128-byte swizzle.
 template <typename T>
-inline bool encode_query_map(CUtensorMap* map, const void* q, int T_, int Hq, int D, int G) {
+inline bool encode_query_map(CUtensorMap* map, const void* q, int T_, int Hq, int D, int G, int tokens) {
     auto enc = tensor_map_encoder();
     if (!enc) return false;
     const cuuint64_t dims[4] = {64, (cuuint64_t)(D / 64), (cuuint64_t)Hq, (cuuint64_t)T_};
     const cuuint64_t strides[3] = {128, (cuuint64_t)D * 2, (cuuint64_t)Hq * D * 2};
-    const cuuint32_t box[4] = {64, 1, (cuuint32_t)G, (cuuint32_t)(128 / G)};
+    const cuuint32_t box[4] = {64, 1, (cuuint32_t)G, (cuuint32_t)tokens};
     const cuuint32_t estr[4] = {1, 1, 1, 1};
     return enc(map, Mma<T>::TMA_TYPE, 4, const_cast<void*>(q), dims, strides, box, estr,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
@@ -670,8 +896,10 @@ template <typename T, int D, bool SPLIT_P>
 cudaError_t launch_chunk_tds(const ChunkParams& p, const ChunkTensors& x, cudaStream_t stream) {
     constexpr int SMEM = ChunkSmem<D>::BYTES;
     const long long rows = (long long)p.num_blocks * p.num_kv_heads * p.block_size;
-    CUtensorMap tq, tk, tv;
-    if (!encode_query_map<T>(&tq, x.q, x.num_tokens, p.num_q_heads, D, p.group) ||
+    const int G = p.group;
+    CUtensorMap tq, tq32, tk, tv;
+    if (!encode_query_map<T>(&tq, x.q, x.num_tokens, p.num_q_heads, D, G, 128 / G) ||
+        !encode_query_map<T>(&tq32, x.q, x.num_tokens, p.num_q_heads, D, G, G <= 32 ? 32 / G : 1) ||
         !encode_pool_map<T>(&tk, x.k_pool, rows, D) || !encode_pool_map_3d<T>(&tv, x.v_pool, rows, D))
         return cudaErrorNotSupported;
     auto kernel = chunk_attention_kernel<T, D, SPLIT_P>;
@@ -694,7 +922,7 @@ cudaError_t launch_chunk_tds(const ChunkParams& p, const ChunkTensors& x, cudaSt
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, tq, tk, tv, p);
+    return cudaLaunchKernelEx(&cfg, kernel, tq, tq32, tk, tv, p);
 }
 
 template <typename T>

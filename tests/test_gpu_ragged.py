@@ -365,6 +365,18 @@ def test_chunk_long_contexts_are_cut(P, dtype, Hq, Hkv, D, ctx, new):
     assert P.pkv_get_device_error() == 0
 
 
+@pytest.mark.parametrize("dtype,D", [("bf16", 128), ("f16", 64)])
+@pytest.mark.parametrize("Hq,Hkv", [(3, 3), (4, 1), (16, 1)])
+def test_chunk_decoding_requests(P, dtype, D, Hq, Hkv):
+    """One query each, contexts around the steps' and their quarters' edges; scores that rise."""
+    ctx = [1, 31, 32, 33, 96, 97, 127, 128, 129, 160, 255, 256, 257, 700, 0, 1500]
+    c = Chunk(dtype, Hq, Hkv, D, 16, ctx, [1] * len(ctx), 7, pad=1)
+    c.check(c.run(P))
+    c = Chunk(dtype, Hq, Hkv, D, 32, [900, 2500, 64], [1, 16 // (Hq // Hkv), 1], 8, sharpen=12.0)
+    c.check(c.run(P))
+    assert P.pkv_get_device_error() == 0
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 @pytest.mark.parametrize("D", [64, 128])
 def test_chunk_f32_output(P, dtype, D):
@@ -393,15 +405,16 @@ def test_chunk_many_requests(P):
     c.check(c.run(P))
 
 
-def test_chunk_pieces_of_all_kinds_one_after_another(P):
+@pytest.mark.parametrize("Hq,Hkv,D", [(8, 8, 64), (6, 6, 128), (15, 5, 128)])
+def test_chunk_pieces_of_all_kinds_one_after_another(P, Hq, Hkv, D):
     """Many pieces for each CTA, one and two query tiles and all step counts in turn."""
     rng = np.random.default_rng(5)
     ctx, new = [], []
     for i in range(150):
-        n = int(rng.choice([1, 2, 64, 65, 130, 200, 257]))
+        n = int(rng.choice([1, 2, 5, 16, 17, 64, 65, 130, 200, 257]))
         new.append(n)
         ctx.append(n + int(rng.integers(0, 700)))
-    c = Chunk("f16", 8, 8, 64, 16, ctx, new, 31, pad=2)
+    c = Chunk("f16", Hq, Hkv, D, 16, ctx, new, 31, pad=2)
     out = c.run(P)
     c.check(out)
     assert torch.equal(out, c.run(P))
