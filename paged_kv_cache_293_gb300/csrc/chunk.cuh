@@ -446,7 +446,8 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
     } else if (warp == Q_WARP) {
         regs_dec<CHUNK_REGS_OTHERS>();
         // ---- query tiles
-        int loads[2] = {0, 0}, uses[2] = {0, 0};  // of each tile: copies in, and times it was taken
+        int loads[2] = {0, 0}, fews = 0;  // copies into each tile, pieces with few rows
+        bool few_last = false;            // tile 1 was taken last by such a piece
         ChunkPiece pc;
         for (int i = 0; next_piece(i, pc); ++i) {
             if (pc.kt1 <= pc.kt0) continue;
@@ -454,11 +455,16 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
             // 1 for the warps' results
             const bool few = is_few(pc);
             for (int t = 0; t < (few || pc.queries > QPT ? 2 : 1); ++t) {
-                if (uses[t] > 0)
-                    ok = __all_sync(FULL_MASK, mbar_wait_short(q_empty(t), (uses[t] - 1) & 1));
+                if (t == 1 && few_last)
+                    ok = __all_sync(FULL_MASK, mbar_wait_short(few_read, (fews - 1) & 1));
+                else if (loads[t] > 0)
+                    ok = __all_sync(FULL_MASK, mbar_wait_short(q_empty(t), (loads[t] - 1) & 1));
                 if (!ok) break;
-                ++uses[t];
-                if (few && t == 1) continue;
+                if (t == 1) few_last = few;
+                if (few && t == 1) {
+                    ++fews;
+                    continue;
+                }
                 ++loads[t];
                 if (umma::elect_one()) {
                     const uint32_t dst = q_s + t * L::TILE;
@@ -702,19 +708,17 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
                 float4* rows_s = reinterpret_cast<float4*>(smem + L::Q_OFF + L::TILE);
                 float* m_s = reinterpret_cast<float*>(smem + L::FEW_OFF);
                 float* l_s = m_s + 4 * CHUNK_FEW_ROWS;
-#pragma unroll 1
-                for (int c = 0; c < D; c += 16) {
-                    float o[16];
-                    umma::ld16(o_t + c, o);
-                    if (lane < rows) {
+                uint32_t o[D];
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            rows_s[(warp * CHUNK_FEW_ROWS + lane) * COLS + (c / 4 + k + lane) % COLS] =
-                                make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
-                    }
-                    __syncwarp();
-                }
+                for (int c = 0; c < D; c += 32) umma::ld32_async(o_t + c, o + c);
+#pragma unroll
+                for (int c = 0; c < D; c += 32) umma::wait_ld(o + c);
                 if (lane < rows) {
+#pragma unroll
+                    for (int k = 0; k < COLS; ++k)
+                        rows_s[(warp * CHUNK_FEW_ROWS + lane) * COLS + (k + lane) % COLS] =
+                            make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]),
+                                        __uint_as_float(o[4 * k + 2]), __uint_as_float(o[4 * k + 3]));
                     m_s[warp * CHUNK_FEW_ROWS + lane] = m_ref;
                     l_s[warp * CHUNK_FEW_ROWS + lane] = l;
                 }
@@ -764,11 +768,6 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
                 umma::fence_before_sync();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(few_read);
-                if (warp == 0) {
-                    ok = __all_sync(FULL_MASK, mbar_wait_short(few_read, fews & 1));
-                    if (!ok) break;
-                    if (lane == 0) mbar_arrive(q_empty(1));
-                }
                 ++fews;
                 continue;
             }
