@@ -45,7 +45,9 @@ __device__ __forceinline__ SeqNeed seq_need(const BatchParams& p, int s, bool re
     r.tokens = nw > 0 ? nw : 0;
     r.need = 0;
     r.status = 0;
-    if (r.past < 0 || nw < 0 || (long long)r.past + nw > (long long)p.max_blocks_per_seq * p.block_size) {
+    // (no context reaches the last block of 2^31 positions: rounding up to blocks stays in range)
+    const long long cap = min((long long)p.max_blocks_per_seq * p.block_size, 0x7fffffffll - p.block_size);
+    if (r.past < 0 || nw < 0 || (long long)r.past + nw > cap) {
         r.status = 2;
         return r;
     }

@@ -369,6 +369,7 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
         regs_dec<CHUNK_REGS_OTHERS>();
         // ---- pieces, and the pages of each: K then V of every 128-token step
         const uint64_t policy = l2_evict_normal_policy();
+        const ChunkPiece first_piece = p.pieces[blockIdx.x];  // the list has a place for each CTA
         const int n_pieces = p.header[0];
         const int B = p.block_size, Hkv = p.num_kv_heads;
         const int far_row = p.num_blocks * Hkv * B;  // past the pools: copies bring zeros
@@ -378,7 +379,7 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
         for (int i = 0;; ++i) {
             ChunkPiece pc;
             pc.kv_head = -1;
-            if (idx < n_pieces) pc = p.pieces[idx];
+            if (idx < n_pieces) pc = i == 0 ? first_piece : p.pieces[idx];
             if (i >= 2) {
                 ok = __all_sync(FULL_MASK, mbar_wait_short(piece_empty(i & 1), ((i >> 1) - 1) & 1));
                 if (!ok) break;

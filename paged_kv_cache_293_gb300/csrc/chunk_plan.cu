@@ -105,7 +105,7 @@ __device__ __forceinline__ int tile_steps(const int4& tile) {
 template <int N>
 __global__ void __launch_bounds__(N) chunk_plan_kernel(const ChunkPlanParams p) {
     __shared__ int4 warp_sums[32];
-    __shared__ int max_steps_s, pieces_s;  // pieces_s: of the rounds so far
+    __shared__ int max_steps_s;
     __shared__ int sums_s[7][32];  // of each candidate
     __shared__ int start_s[N + 1], tile_start_s[N + 1], ctx_s[N];
     __shared__ int4 tiles_s[N];  // this round's tiles
@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(N) chunk_plan_kernel(const ChunkPlanParams p) 
     const int* ctxs = few ? ctx_s : p.context_lens;
     if (tid == 0) {
         tile_start[0] = 0;
-        max_steps_s = pieces_s = 0;
+        max_steps_s = 0;
     }
     for (int i = tid; i < 7 * 32; i += N) sums_s[i >> 5][i & 31] = 0;
 
@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(N) chunk_plan_kernel(const ChunkPlanParams p) 
     int cut = max(max_steps, 1);  // steps per piece at most
     if (p.max_partial_rows > 0 && max_steps >= CHUNK_SPLIT_MIN) {
         // lane k - 1 of every warp: candidate k's steps per piece
-        const int my_c = (int)ceilf(__fdividef((float)max_steps, (float)(lane + 1)));
+        const int my_c = (max_steps + lane) / (lane + 1);
         const float my_inv = __fdividef(1.f, (float)my_c);
         int all = 0, rows = 0, cuts = 0, longer[4] = {0, 0, 0, 0};
         for (int ti = warp; ti < num_tiles; ti += N / 32) {
@@ -249,10 +249,13 @@ __global__ void __launch_bounds__(N) chunk_plan_kernel(const ChunkPlanParams p) 
             pc = parts_of(tile);
             len = tile_steps(tile) / pc;
         }
-        const int round_pieces = H * __reduce_add_sync(FULL_MASK, pc);
-        if (lane == 0) atomicAdd(&pieces_s, round_pieces);
-        __syncthreads();
-        if (pieces_s > p.ctas) {
+        auto amounts = [&] {
+            const int R = tile.z * p.group;
+            return make_int4(H * pc, pc > 1 ? H * pc * R : 0, pc > 1 ? H : 0, pc > 1 ? H * R : 0);
+        };
+        int4 mine = amounts(), total;
+        int4 v = block_scan4<N>(mine, warp_sums, &total);
+        if (total.x > p.ctas) {
             // longest pieces first: a counting sort of the round's tiles by length class, in
             // tile order within a class
             const int cls = ti < num_tiles ? min(LENGTH_CLASSES - 1, (int)((float)((cut - len) * LENGTH_CLASSES) * inv_cut))
@@ -277,13 +280,11 @@ __global__ void __launch_bounds__(N) chunk_plan_kernel(const ChunkPlanParams p) 
                 tile = tiles_s[tid];
                 pc = parts_of(tile);
             }
+            mine = amounts();
+            v = block_scan4<N>(mine, warp_sums, &total);
         } else if (ti < num_tiles) {
             tiles_s[tid] = tile;
         }
-        const int R = tile.z * p.group;
-        const int4 mine = make_int4(H * pc, pc > 1 ? H * pc * R : 0, pc > 1 ? H : 0, pc > 1 ? H * R : 0);
-        int4 total;
-        const int4 v = block_scan4<N>(mine, warp_sums, &total);
         base_s[tid] = make_int4(base.x + v.x - mine.x, base.y + v.y - mine.y, base.z + v.z - mine.z,
                                 base.w + v.w - mine.w);
         __syncthreads();

@@ -397,6 +397,12 @@ def test_chunk_scales(P, scale):
     c.check(c.run(P, scale=scale), scale=scale)
 
 
+@pytest.mark.parametrize("Hq,Hkv", [(64, 1), (128, 1), (66, 2)])
+def test_chunk_large_groups(P, Hq, Hkv):
+    c = Chunk("bf16", Hq, Hkv, 64, 16, [200, 1, 140, 1100], [7, 1, 140, 1], 5, pad=1)
+    c.check(c.run(P))
+
+
 def test_chunk_many_requests(P):
     rng = np.random.default_rng(3)
     ctx = rng.integers(1, 90, 1500)
