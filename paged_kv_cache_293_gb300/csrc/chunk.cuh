@@ -7,12 +7,12 @@
 // zero when lim <= 0.  The G heads of a kv head share its K and V, so the rows of one kv
 // head are (query, head) pairs and a CTA takes two tiles of 128 of them (row r of a tile is
 // query r / G, head r % G) against the pages in steps of 128 tokens: every staged K and V
-// tile serves 256 rows.  One pass, running maximum and sum per row (one thread per row).
+// tile serves 256 rows.  One pass, running maximum and sum per row.
 //
 // A small kernel first lists the pieces of work (chunk_plan.cu): tile pair x kv head, cut
 // along the context where there would be too few of them; the CTAs of this kernel, one per
-// SM, take pieces from that list in order until it is empty.  Twelve warps, fixed roles:
-//   0-3, 4-7  softmax of tile 0 and of tile 1, and their output
+// SM, take pieces from that list in order until it is empty.  Sixteen warps, fixed roles:
+//   0-3, 4-7  softmax of tile 0 and of tile 1
 //   8         takes the next piece; tensor copies of K and V pages into a ring of stages
 //   9         one lane issues the MMAs, for the two tiles in turn:
 //               S_t = Q_t . K_j^T            128 x 128 in tensor memory
@@ -20,17 +20,37 @@
 //             so that one tile's softmax runs while the tensor cores work for the other.
 //             Before a piece's last P.V the warp zeroes the V rows of the last 16-token copy
 //             past the last position the piece may see (they may hold anything; their
-//             weights are zero, and 0 * NaN is not).  Of a piece with one tile of queries
-//             the even and the odd steps' scores take the two tiles' places; of one with at
-//             most CHUNK_FEW_ROWS rows each of warps 0-3 has all rows and a quarter of the
-//             tokens
+//             weights are zero, and 0 * NaN is not)
 //   10        tensor copies of the query tiles
 //   11        none (fills the warpgroup)
+//   12-15     output of a finished piece, while the others are at the next one
+// A piece takes one of three forms by its rows:
+//   more than 128  both tiles;
+//   17 to 128      one tile: the even and the odd steps' scores take the two tiles' places, so
+//                  a step's scores are ready when the softmax of the step before ends;
+//   up to 16       (decoding requests) each of warps 0-3 has all rows and a quarter of the
+//                  tokens of every step, and the four results are joined at the end.
 // The reference maximum of a row is raised only when a step's maximum exceeds it by more
 // than 8 in base 2, so O is rescaled rarely; every term of a row uses the same reference.
-// P enters its product rounded to the pool's type (relative error 2^-9 bf16, 2^-12 fp16 per
-// term at most half a step, like the output's own rounding); with a 32-bit output it enters
-// as a rounded part and the rounded remainder, in two products.
+// P enters its product rounded to the pool's type (at most half a step, 2^-8 of the value in
+// bf16 and 2^-11 in fp16, like the output's own rounding); with a 32-bit output it enters as a
+// rounded part and the rounded remainder, in two products.  Scores, maxima, sums and O are
+// held in 32 bits.
+//
+// What bounds it, measured.  Two full tiles: a step has 2048 cycles of MMAs and takes about
+// 2600, the way of one tile once round: its softmax (1480 cycles: scores from tensor memory 310,
+// 128 exponentials 920), the second half of P.V (256), Q.K^T (512) and three hand-overs.  8192
+// tokens from the first on, 32 / 8 heads of 128, bf16: 352 us, 1.56 PFLOP/s; 500 tokens over
+// 130,500: 700 us, 1.52 PFLOP/s.  What got it there, each for that prompt:
+//   MMAs and copies issued under elect.sync and not under lane == 0 (67 cycles an MMA, 100 a
+//     copy there): 470 -> 411 us, and with V's copies three-dimensional (one for both halves of
+//     16 tokens; K's halves have to lie apart) 394;
+//   one thread issuing both tiles' MMAs and not one each, which run interleaved, so that both
+//     tiles' exponentials compete for the same units at the same time: 394 -> 373;
+//   registers so that the softmax does not spill: 373 -> 364; output by warps of its own: 352.
+// Few rows: 64 KB of K and V a step bound it, 1960 cycles where the HBM's share of an SM is 2790.
+// Tried and slower: 16 softmax warps that share rows and exchange maxima; exponentials begun
+// with the old reference before the maximum is known; merging cut items in this kernel.
 // Every wait is bounded; a CTA that gives up sets PKV_DEVERR_TIMEOUT and returns its tensor
 // memory.
 #pragma once
@@ -42,10 +62,10 @@
 
 namespace pkv {
 
-constexpr int CHUNK_THREADS = 384;
-// Registers per thread: 168 at launch; the softmax warps take what the others give back
-// (256 * 208 + 128 * 88 = 384 * 168).
-constexpr int CHUNK_REGS_SOFTMAX = 208, CHUNK_REGS_OTHERS = 88;
+constexpr int CHUNK_THREADS = 512;
+// Registers per thread: 128 at launch; the softmax warps take what the others give back
+// (256 * 184 + 128 * 72 + 128 * 72 = 512 * 128).
+constexpr int CHUNK_REGS_SOFTMAX = 184, CHUNK_REGS_OTHERS = 72, CHUNK_REGS_OUTPUT = 72;
 constexpr float CHUNK_RESCALE_LOG2 = 8.f;
 constexpr int CHUNK_FEW_ROWS = 16;  // rows up to which a piece's steps are spread over four warps
 
@@ -58,11 +78,11 @@ struct ChunkSmem {
     static constexpr int Q_OFF = 0;
     static constexpr int KV_OFF = 2 * TILE;
     static constexpr int BAR_OFF = KV_OFF + STAGES * TILE;
-    static constexpr int NBARS = 2 * STAGES + 28;
+    static constexpr int NBARS = 2 * STAGES + 31;
     static constexpr int PIECE_OFF = BAR_OFF + ((NBARS * 8 + 15) / 16) * 16;
-    static constexpr int FEW_OFF = PIECE_OFF + 2 * 32;  // float [2][4][16]: m and l of the warps' rows
-    static constexpr int TMEM_SLOT_OFF = FEW_OFF + 2 * 4 * CHUNK_FEW_ROWS * 4;
-    static constexpr int BYTES = TMEM_SLOT_OFF + 16 + 1024;  // + alignment slack
+    static constexpr int STAT_OFF = PIECE_OFF + 2 * 32;  // float [2 tiles][m, l][128 rows]
+    static constexpr int TMEM_SLOT_OFF = STAT_OFF + 2 * 2 * 128 * 4;
+    static constexpr int BYTES = TMEM_SLOT_OFF + 16;
     // tensor memory columns: S_0, S_1 (P over them), O_0, O_1; of a piece with few rows P has the
     // last 128 columns
     static constexpr uint32_t FEW_P_COL = 384;
@@ -275,16 +295,16 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
                        const __grid_constant__ CUtensorMap tmap_v, const ChunkParams p) {
     using L = ChunkSmem<D>;
     constexpr int NS = L::STAGES, KS = D / 16;
-    constexpr int KV_WARP = 8, MMA_WARP = 9, Q_WARP = 10, IDLE_WARP = 11;
-    constexpr int CONSUMERS = 8 + 2;  // arrivals that free a slot of the piece ring
+    constexpr int KV_WARP = 8, MMA_WARP = 9, Q_WARP = 10, IDLE_WARP = 11, OUT_WARP = 12;
+    constexpr int CONSUMERS = 8 + 2 + 4;  // arrivals that free a slot of the piece ring
     constexpr uint32_t FMT = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
     constexpr uint32_t IDESC_S = umma::idesc_f16(FMT, false, 128, CHUNK_TILE);
     const uint32_t idesc_s = IDESC_S | (p.negate ? umma::IDESC_NEGATE_A : 0u);
     constexpr uint32_t IDESC_O = umma::idesc_f16(FMT, true, 128, D);
 
-    extern __shared__ __align__(128) unsigned char smem_raw[];
-    unsigned char* smem = reinterpret_cast<unsigned char*>(
-        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    // the swizzle repeats every 1024 bytes; no static shared memory lies before this array
+    extern __shared__ __align__(1024) unsigned char chunk_smem[];
+    unsigned char* smem = chunk_smem;
     const uint32_t sbase = smem_addr(smem);
     const uint32_t q_s = sbase + L::Q_OFF, ring = sbase + L::KV_OFF, bar0 = sbase + L::BAR_OFF;
     const int G = p.group, QPT = 128 / G;  // heads per kv head, queries per tile
@@ -308,9 +328,12 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
     // tile's warps take no part in them)
     auto s_full = [&](int i) { return bar0 + 8 * (NB + 13 + i); };
     auto p_full = [&](int i, int h) { return bar0 + 8 * (NB + 17 + 2 * i + h); };
-    // the second tile's output has been read; the four warps' rows of a piece with few rows are
-    // in shared memory, and have been read
-    const uint32_t o_read = bar0 + 8 * (NB + 25), few_done = bar0 + 8 * (NB + 26), few_read = bar0 + 8 * (NB + 27);
+    // a tile's m and l are in shared memory; its O (and m and l) have been read; the four warps'
+    // rows of a piece with few rows are in shared memory, and have been read
+    auto stat_full = [&](int t) { return bar0 + 8 * (NB + 25 + t); };
+    auto o_free = [&](int t) { return bar0 + 8 * (NB + 27 + t); };
+    const uint32_t few_done = bar0 + 8 * (NB + 29), few_read = bar0 + 8 * (NB + 30);
+    float* stats = reinterpret_cast<float*>(smem + L::STAT_OFF);  // + 256 t: m, + 128: l
     auto is_few = [&](const ChunkPiece& x) {
         return !SPLIT_P && x.queries * G <= CHUNK_FEW_ROWS && x.kt1 > x.kt0;
     };
@@ -334,11 +357,12 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
             }
             mbar_init(pv_done(t), 1);
             mbar_init(pv_step(t), 1);
+            mbar_init(stat_full(t), 4);
+            mbar_init(o_free(t), 4);
             mbar_init(piece_full(t), 1);
             mbar_init(piece_empty(t), CONSUMERS);
         }
         mbar_init(all_done, 1);
-        mbar_init(o_read, 4);
         mbar_init(few_done, 4);
         mbar_init(few_read, 4);
         mbar_init_fence();
@@ -496,6 +520,7 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
         uint32_t total = 0;               // stages of the pieces so far
         int used[2] = {0, 0};             // Q tiles taken
         int steps[4] = {0, 0, 0, 0};      // P tiles taken, as s_full and p_full count them
+        int outs[2] = {0, 0};             // pieces begun in O_0 and O_1
         // i: tile 0 or 1, or 2, 3 for an even or odd step of a piece with one tile of queries
         auto issue_s = [&](int i, int st) {  // S over the P just read: MMAs run in issue order
             const uint64_t k_desc = umma::sw128_desc(ring + st * L::TILE, 16, 1024);
@@ -515,6 +540,11 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
             const uint32_t o_t = tmem + L::O_COL + (i == 1 ? D : 0);
             const uint32_t p_t = tmem + (few ? L::FEW_P_COL + (i & 1) * (CHUNK_TILE / 2) : (i & 1) * CHUNK_TILE);
             const uint32_t parity = steps[i]++ & 1;
+            if (first) {  // the piece before has been read from O
+                int& o = outs[i == 1];
+                if (o > 0 && !mbar_wait_short(o_free(i == 1), (o - 1) & 1)) return false;
+                ++o;
+            }
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 if (!mbar_wait_short(p_full(i, h), parity)) return false;
@@ -647,22 +677,181 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
         __syncwarp();
     } else if (warp == IDLE_WARP) {
         regs_dec<CHUNK_REGS_OTHERS>();
+    } else if (warp >= OUT_WARP) {
+        regs_dec<CHUNK_REGS_OUTPUT>();
+        // ---- output of both tiles, while the softmax warps are at the next piece: warp w of
+        // these reads the rows that warps w and 4 + w worked on
+        const int w = warp - OUT_WARP, r = w * 32 + lane;
+        const uint32_t lane_tmem = tmem + ((uint32_t)(w * 32) << 16);
+        const int hg = r % G;
+        int even = 0, odd = 0;    // steps of pieces with one tile so far: the phases of pv_step
+        int outs = 0, twos = 0;   // pieces so far, those with two tiles: of stat_full, pv_done
+        int fews = 0;             // pieces with few rows: of few_done
+        ChunkPiece pc;
+        for (int i = 0; next_piece(i, pc); ++i) {
+            const int n = max(pc.kt1 - pc.kt0, 0);
+            const bool two = pc.queries > QPT, direct = pc.part_row < 0, few = is_few(pc);
+            if (!two) {
+                even += (n + 1) / 2;
+                odd += n / 2;
+            }
+            for (int t = 0; t < (two ? 2 : 1); ++t) {
+                const uint32_t o_t = lane_tmem + L::O_COL + t * D;
+                if (n > 0) {
+                    // the sums first: then every product but the last of each barrier is done, and
+                    // the parity tells
+                    ok = __all_sync(FULL_MASK, mbar_wait_short(stat_full(t), (t == 0 ? outs : twos) & 1));
+                    if (!ok) break;
+                    const int last = (n - 1) & 1;
+                    ok = __all_sync(FULL_MASK, two ? mbar_wait_short(pv_done(t), twos & 1)
+                                                   : mbar_wait_short(pv_step(last), ((last ? odd : even) - 1) & 1));
+                    if (!ok) break;
+                    umma::fence_after_sync();
+                }
+                const float m = stats[256 * t + r], l = n > 0 ? stats[256 * t + 128 + r] : 0.f;
+                if (few) {
+                    // the four results of each row meet in the second Q tile; row r's 16-byte
+                    // columns are turned by r, so that a warp's stores spread over the banks
+                    const int rows = pc.queries * G;
+                    constexpr int COLS = D / 4;
+                    float4* rows_s = reinterpret_cast<float4*>(smem + L::Q_OFF + L::TILE);
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 16) {
+                        float o[16];
+                        umma::ld16(o_t + c, o);
+                        if (lane < rows) {
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                rows_s[(w * CHUNK_FEW_ROWS + lane) * COLS + (c / 4 + k + lane) % COLS] =
+                                    make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                        }
+                        __syncwarp();
+                    }
+                    umma::fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(few_done);
+                    ok = __all_sync(FULL_MASK, mbar_wait_short(few_done, fews & 1));
+                    if (!ok) break;
+                    for (int x = w; x < rows; x += 4) {
+                        float M = -INFINITY, sum = 0.f, f[4];
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) M = fmaxf(M, stats[y * 32 + x]);
+                        const float ref = M == -INFINITY ? 0.f : M;
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) {
+                            f[y] = fast_exp2(stats[y * 32 + x] - ref);
+                            sum = fmaf(f[y], stats[128 + y * 32 + x], sum);
+                        }
+                        const float inv = !direct ? 1.f : sum > 0.f ? 1.f / sum : 0.f;
+                        const long long out_row =
+                            ((long long)pc.token + x / G) * p.num_q_heads + pc.kv_head * G + x % G;
+                        const long long part_row = (long long)pc.part_row + x;
+                        if (lane < COLS) {
+                            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                            for (int y = 0; y < 4; ++y) {
+                                const float4 v = rows_s[(y * CHUNK_FEW_ROWS + x) * COLS + (lane + x) % COLS];
+                                const float fw = f[y] * inv;
+                                o.x = fmaf(fw, v.x, o.x);
+                                o.y = fmaf(fw, v.y, o.y);
+                                o.z = fmaf(fw, v.z, o.z);
+                                o.w = fmaf(fw, v.w, o.w);
+                            }
+                            if (direct)
+                                reinterpret_cast<uint2*>(static_cast<T*>(p.out) + out_row * D)[lane] =
+                                    make_uint2(Mma<T>::pack(o.x, o.y), Mma<T>::pack(o.z, o.w));
+                            else
+                                reinterpret_cast<float4*>(p.part_o + part_row * D)[lane] = o;
+                        }
+                        if (!direct && lane == 0) {
+                            p.part_m[part_row] = M;  // base 2
+                            p.part_l[part_row] = sum;
+                        }
+                    }
+                    // the second Q tile, O and the sums go back when all four have read them
+                    fence_proxy_async_shared();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(few_read);
+                        mbar_arrive(o_free(0));
+                    }
+                    ++fews;
+                    break;
+                }
+                const int jq = t * QPT + r / G;  // query within the piece
+                const bool valid = r < QPT * G && jq < pc.queries;
+                if (__any_sync(FULL_MASK, valid)) {
+                    const long long out_row = ((long long)pc.token + jq) * p.num_q_heads + pc.kv_head * G + hg;
+                    const long long part_row = (long long)pc.part_row + (t * QPT * G + r);
+                    const float by = !direct ? 1.f : l > 0.f ? 1.f / l : 0.f;
+                    // once per piece: a loop that stays in the instruction cache
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 16) {
+                        float o[16];
+                        if (n > 0) umma::ld16(o_t + c, o);
+                        // a row that sees nothing is zero, whatever O holds
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) o[k] = l > 0.f ? o[k] * by : 0.f;
+                        if (!valid) {
+                        } else if (direct && !SPLIT_P) {
+                            uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(p.out) + out_row * D + c);
+#pragma unroll
+                            for (int k = 0; k < 16; k += 8)
+                                dst[k / 8] =
+                                    make_uint4(Mma<T>::pack(o[k], o[k + 1]), Mma<T>::pack(o[k + 2], o[k + 3]),
+                                               Mma<T>::pack(o[k + 4], o[k + 5]), Mma<T>::pack(o[k + 6], o[k + 7]));
+                        } else {
+                            float4* dst = reinterpret_cast<float4*>(
+                                direct ? static_cast<float*>(p.out) + out_row * D + c : p.part_o + part_row * D + c);
+#pragma unroll
+                            for (int k = 0; k < 16; k += 4)
+                                dst[k / 4] = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+                        }
+                        __syncwarp();
+                    }
+                    if (valid && !direct) {
+                        p.part_m[part_row] = m;  // base 2
+                        p.part_l[part_row] = l;
+                    }
+                }
+                if (n > 0) {
+                    umma::fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(o_free(t));
+                }
+            }
+            if (!ok) break;
+            if (n > 0) {
+                ++outs;
+                twos += two;
+            }
+        }
     } else {
         regs_inc<CHUNK_REGS_SOFTMAX>();
-        // ---- softmax and output of tile t: this thread's row is r
+        // ---- softmax of tile t: this thread's row is r
         const int t = warp >> 2, r = threadIdx.x & 127;
         const uint32_t lane_tmem = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const uint32_t o_t = lane_tmem + L::O_COL + t * D;
-        const int jq = t * QPT + r / G, hg = r % G;  // query within the piece, head of the group
+        const int jq = t * QPT + r / G;                // query within the piece
         int taken = 0, taken_even = 0, taken_odd = 0;  // S tiles so far: the phases of s_full and pv_step
-        int ends = 0;  // two-tile pieces so far: the phase of pv_done and o_read
-        int fews = 0;  // pieces with few rows so far: the phase of few_done and few_read
-        bool p_clear = false;  // the P columns of such pieces hold zeros where they should
+        int outs = 0, twos = 0;  // pieces handed to the output warps, those with two tiles: of o_free
+        bool p_clear = false;    // the P columns of pieces with few rows hold zeros where they should
+        // this row's m and l to the output warps
+        auto hand_out = [&](float m, float l) -> bool {
+            if (outs > 0) ok = __all_sync(FULL_MASK, mbar_wait_short(o_free(t), (outs - 1) & 1));
+            if (!ok) return false;
+            ++outs;
+            stats[256 * t + r] = m;
+            stats[256 * t + 128 + r] = l;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(stat_full(t));
+            return true;
+        };
         ChunkPiece pc;
         for (int i = 0; next_piece(i, pc); ++i) {
             const int n = max(pc.kt1 - pc.kt0, 0);
             const bool two = pc.queries > QPT;
-            if (t == 1 && !two) continue;  // the other warpgroup takes both S tiles in turn
+            if (n == 0 || (t == 1 && !two)) continue;  // one tile: the other warpgroup takes both S tiles
             if (is_few(pc)) {
                 // Few rows: warp w has them all, in its own 32 lanes, and of every step the tokens
                 // 32 w .. 32 w + 31, its own reference, sum and O; its P holds zeros for the other
@@ -671,8 +860,11 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
                 const int rows = pc.queries * G, lim_w = pc.lim0 + min(lane, rows - 1) / G - warp * 32;
                 const uint32_t p_t = lane_tmem + L::FEW_P_COL;
                 if (!p_clear) {
-                    // O_1 lies there: the other warps have read it
-                    if (ends > 0) ok = __all_sync(FULL_MASK, mbar_wait_short(o_read, (ends - 1) & 1));
+                    // O_1 lies there: wait until it has been read.  (Tile 0 of the piece before
+                    // first, so that at most one reading of O_1 is still to come and the parity
+                    // tells which.)
+                    if (outs > 0) ok = __all_sync(FULL_MASK, mbar_wait_short(o_free(0), (outs - 1) & 1));
+                    if (ok && twos > 0) ok = __all_sync(FULL_MASK, mbar_wait_short(o_free(1), (twos - 1) & 1));
                     if (!ok) break;
                     umma::fence_after_sync();
                     const uint32_t zeros[16] = {0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
@@ -697,83 +889,10 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
                         mbar_arrive(p_full(2 + b, 1));
                     }
                 }
-                if (!ok) break;
-                const int last = (n - 1) & 1;
-                ok = __all_sync(FULL_MASK,
-                                mbar_wait_short(pv_step(last), ((last ? taken_odd : taken_even) - 1) & 1));
-                if (!ok) break;
-                umma::fence_after_sync();
-                // the four results of each row meet in the second Q tile; row r's 16-byte columns
-                // are turned by r, so that a warp's stores spread over the banks
-                constexpr int COLS = D / 4;
-                float4* rows_s = reinterpret_cast<float4*>(smem + L::Q_OFF + L::TILE);
-                float* m_s = reinterpret_cast<float*>(smem + L::FEW_OFF);
-                float* l_s = m_s + 4 * CHUNK_FEW_ROWS;
-                uint32_t o[D];
-#pragma unroll
-                for (int c = 0; c < D; c += 32) umma::ld32_async(o_t + c, o + c);
-#pragma unroll
-                for (int c = 0; c < D; c += 32) umma::wait_ld(o + c);
-                if (lane < rows) {
-#pragma unroll
-                    for (int k = 0; k < COLS; ++k)
-                        rows_s[(warp * CHUNK_FEW_ROWS + lane) * COLS + (k + lane) % COLS] =
-                            make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]),
-                                        __uint_as_float(o[4 * k + 2]), __uint_as_float(o[4 * k + 3]));
-                    m_s[warp * CHUNK_FEW_ROWS + lane] = m_ref;
-                    l_s[warp * CHUNK_FEW_ROWS + lane] = l;
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(few_done);
-                ok = __all_sync(FULL_MASK, mbar_wait_short(few_done, fews & 1));
-                if (!ok) break;
-                for (int x = warp; x < rows; x += 4) {
-                    float M = -INFINITY, sum = 0.f, f[4];
-#pragma unroll
-                    for (int w = 0; w < 4; ++w) M = fmaxf(M, m_s[w * CHUNK_FEW_ROWS + x]);
-                    const float ref = M == -INFINITY ? 0.f : M;
-#pragma unroll
-                    for (int w = 0; w < 4; ++w) {
-                        f[w] = fast_exp2(m_s[w * CHUNK_FEW_ROWS + x] - ref);
-                        sum = fmaf(f[w], l_s[w * CHUNK_FEW_ROWS + x], sum);
-                    }
-                    const bool direct = pc.part_row < 0;
-                    const float inv = !direct ? 1.f : sum > 0.f ? 1.f / sum : 0.f;
-                    const long long out_row =
-                        ((long long)pc.token + x / G) * p.num_q_heads + pc.kv_head * G + x % G;
-                    const long long part_row = (long long)pc.part_row + x;
-                    if (lane < COLS) {
-                        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                        for (int w = 0; w < 4; ++w) {
-                            const float4 y = rows_s[(w * CHUNK_FEW_ROWS + x) * COLS + (lane + x) % COLS];
-                            const float fw = f[w] * inv;
-                            o.x = fmaf(fw, y.x, o.x);
-                            o.y = fmaf(fw, y.y, o.y);
-                            o.z = fmaf(fw, y.z, o.z);
-                            o.w = fmaf(fw, y.w, o.w);
-                        }
-                        if (direct)
-                            reinterpret_cast<uint2*>(static_cast<T*>(p.out) + out_row * D)[lane] =
-                                make_uint2(Mma<T>::pack(o.x, o.y), Mma<T>::pack(o.z, o.w));
-                        else
-                            reinterpret_cast<float4*>(p.part_o + part_row * D)[lane] = o;
-                    }
-                    if (!direct && lane == 0) {
-                        p.part_m[part_row] = M;  // base 2
-                        p.part_l[part_row] = sum;
-                    }
-                }
-                // the second Q tile goes back when all four have read it
-                fence_proxy_async_shared();
-                umma::fence_before_sync();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(few_read);
-                ++fews;
+                if (!ok || !hand_out(m_ref, l)) break;
                 continue;
             }
-            const bool valid = r < QPT * G && jq < pc.queries;
-            const bool busy = __any_sync(FULL_MASK, valid);
+            const bool busy = __any_sync(FULL_MASK, r < QPT * G && jq < pc.queries);
             const int lim = pc.lim0 + jq;
             float m_ref = -INFINITY;
             uint64_t sum2[2] = {0, 0};  // the row's sum, in four parts
@@ -802,68 +921,14 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
                 }
             }
             if (!ok) break;
-            if (n > 0) {
-                if (two) {
-                    ok = __all_sync(FULL_MASK, mbar_wait_short(pv_done(t), ends & 1));
-                    p_clear = false;
-                    ++ends;
-                } else {
-                    const int last = (n - 1) & 1;
-                    ok = __all_sync(FULL_MASK, mbar_wait_short(pv_step(last), ((last ? taken_odd : taken_even) - 1) & 1));
-                }
-                if (!ok) break;
-                umma::fence_after_sync();
+            if (two) {
+                p_clear = false;
+                ++twos;
             }
-            if (busy) {
-                const long long out_row = ((long long)pc.token + jq) * p.num_q_heads + pc.kv_head * G + hg;
-                const long long part_row = (long long)pc.part_row + (t * QPT * G + r);
-                const bool direct = pc.part_row < 0;
-                float part[4];
-                unpack2(sum2[0], part[0], part[1]);
-                unpack2(sum2[1], part[2], part[3]);
-                const float l = (part[0] + part[1]) + (part[2] + part[3]);
-                const float inv = l > 0.f ? 1.f / l : 0.f;
-                // once per piece: a loop that stays in the instruction cache
-#pragma unroll 1
-                for (int c = 0; c < D; c += 32) {
-                    float o[32];
-                    if (n > 0) {
-                        umma::ld32(o_t + c, o);
-                    } else {
-#pragma unroll
-                        for (int k = 0; k < 32; ++k) o[k] = 0.f;
-                    }
-                    if (!valid) {
-                    } else if (direct && !SPLIT_P) {
-                        uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(p.out) + out_row * D + c);
-#pragma unroll
-                        for (int k = 0; k < 32; ++k) o[k] = l > 0.f ? o[k] * inv : 0.f;
-#pragma unroll
-                        for (int k = 0; k < 32; k += 8)
-                            dst[k / 8] = make_uint4(Mma<T>::pack(o[k], o[k + 1]), Mma<T>::pack(o[k + 2], o[k + 3]),
-                                                    Mma<T>::pack(o[k + 4], o[k + 5]), Mma<T>::pack(o[k + 6], o[k + 7]));
-                    } else {
-                        float4* dst = reinterpret_cast<float4*>(
-                            direct ? static_cast<float*>(p.out) + out_row * D + c : p.part_o + part_row * D + c);
-                        if (direct) {
-#pragma unroll
-                            for (int k = 0; k < 32; ++k) o[k] = l > 0.f ? o[k] * inv : 0.f;
-                        }
-#pragma unroll
-                        for (int k = 0; k < 32; k += 4) dst[k / 4] = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
-                    }
-                    __syncwarp();
-                }
-                if (valid && !direct) {
-                    p.part_m[part_row] = m_ref;  // base 2
-                    p.part_l[part_row] = l;
-                }
-            }
-            if (t == 1 && n > 0) {
-                umma::fence_before_sync();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(o_read);
-            }
+            float part[4];
+            unpack2(sum2[0], part[0], part[1]);
+            unpack2(sum2[1], part[2], part[3]);
+            if (!hand_out(m_ref, (part[0] + part[1]) + (part[2] + part[3]))) break;
         }
     }
     if (!ok && lane == 0) set_error(p.err, PKV_DEVERR_TIMEOUT);
