@@ -25,6 +25,7 @@ namespace {
 constexpr float PARTIAL_ROWS_PER_STEP = 7000.f;  // of 128 values: 1 KB each at about 5 TB/s in 1.45 us
 constexpr int PIECE_STEPS = 2;       // F above
 constexpr int LENGTH_CLASSES = 16;
+constexpr int COUNT_MAX = 1 << 25;
 
 __device__ __forceinline__ int4 add4(int4 a, int4 b) {
     return make_int4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
@@ -194,9 +195,11 @@ __global__ void __launch_bounds__(N) chunk_plan_kernel(const ChunkPlanParams p) 
         for (int ti = warp; ti < num_tiles; ti += N / 32) {
             const int4 tile = tiles[ti];
             const int n = tile_steps(tile), pc = n > my_c ? ceil_div_steps(n, my_c, my_inv) : 1;
-            all += n + PIECE_STEPS * pc;
+            // (the largest batches would pass 32 bits; COUNT_MAX is more than any batch may cut,
+            // and 32 warps of it still fit)
+            all = min(all + n + PIECE_STEPS * pc, COUNT_MAX);
             if (pc > 1) {
-                rows += pc * tile.z * p.group;
+                rows = min(rows + pc * tile.z * p.group, COUNT_MAX);
                 cuts += pc;
             }
             // the longest of the tile's pieces counts for all of them

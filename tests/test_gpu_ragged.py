@@ -563,3 +563,193 @@ def test_ragged_steps_end_to_end(P, dtype):
         assert (out[n:] == 33.0).all() and (q_out[n:] == 2.0).all()
         past += np.array(new)
     assert P.pkv_get_device_error() == 0
+
+
+class Engine:
+    """The state of a small engine on the GPU; step() makes the three calls."""
+
+    def __init__(self, P, seed, S=4, T=400, Hq=8, Hkv=2, D=64, B=16, M=40, N=140):
+        self.P, self.D, self.B, self.heads = P, D, B, (Hq, Hkv)
+        g = torch.Generator().manual_seed(seed)
+        dt = torch.bfloat16
+        i32 = lambda *n: torch.zeros(*n, dtype=torch.int32, device=DEV)  # noqa: E731
+        self.alloc = P.BlockAllocator.of_tensors(torch.randperm(N, generator=g).to(torch.int32).to(DEV),
+                                                 _i32([N]), i32(N))
+        self.tables, self.past, self.new, self.start, self.ctx = i32(S, M), i32(S), i32(S), i32(S + 1), i32(S)
+        self.pos, self.seq, self.status = i32(T), i32(T), i32(S)
+        self.slots = torch.zeros(T, dtype=torch.int64, device=DEV)
+        self.x = torch.zeros(T, (Hq + 2 * Hkv) * D, dtype=dt, device=DEV)
+        self.k_pool = torch.full((N, Hkv, B, D), float("nan"), dtype=dt, device=DEV)
+        self.v_pool = self.k_pool.clone()
+        self.cs = torch.rand(M * B, D, generator=g).to(DEV)
+        self.w = (1 + 0.1 * torch.randn(D, generator=g)).to(dt).to(DEV)
+        self.q_out, self.out = (torch.full((T, Hq, D), 7.0, dtype=dt, device=DEV) for _ in range(2))
+        self.ws = P.workspace_tensor(P.pkv_chunk_workspace_bytes(self.k_pool, T, S, Hq, M * B), DEV)
+
+    def step(self, **kw):
+        (Hq, Hkv), D, T = self.heads, self.D, self.x.shape[0]
+        q, k, v = (t.view(T, -1, D) for t in self.x.split([Hq * D, Hkv * D, Hkv * D], 1))
+        self.P.pkv_build_batch(self.alloc, self.B, self.tables, self.past, self.new, self.start, self.ctx,
+                               self.pos, self.seq, self.slots, self.status, **kw)
+        self.P.pkv_qk_norm_rope_write(q, k, v, self.k_pool, self.v_pool, self.pos, self.slots, self.q_out,
+                                      q_weight=self.w, k_weight=self.w, cos_sin=self.cs, **kw)
+        self.P.pkv_paged_attention_chunk(self.q_out, self.k_pool, self.v_pool, self.start, self.tables,
+                                         self.ctx, D ** -0.5, self.out, self.tables.shape[1] * self.B,
+                                         self.ws, **kw)
+
+    def bits(self):
+        """Everything a step leaves behind."""
+        ints = [self.tables, self.start, self.ctx, self.pos, self.seq, self.status, self.slots,
+                self.alloc.free_count, self.alloc.refcount]
+        return [t.clone() for t in ints] + [t.view(torch.int16).clone()
+                                            for t in (self.k_pool, self.v_pool, self.q_out, self.out)]
+
+
+def _steps(seed, T=400, width=768):
+    g = torch.Generator().manual_seed(seed)
+    lens = [[200, 30, 0, 1], [0, 1, 300, 1], [1, 1, 1, 70], [1, 1, 1, 1], [1, 0, 1, 1]]
+    return [(n, torch.randn(T, width, generator=g).to(torch.bfloat16).to(DEV)) for n in lens]
+
+
+def test_captured_step_replays_like_eager_steps(P):
+    """One graph of the whole step, lengths advancing inside it, for prompts and decoding alike."""
+    steps, a, b = _steps(3), Engine(P, 5), Engine(P, 5)
+    want = []
+    for new, x in steps:
+        a.new.copy_(_i32(new))
+        a.x.copy_(x)
+        a.step()
+        a.past += a.new
+        want.append(a.bits())
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        b.step()
+        b.past += b.new
+    for (new, x), w in zip(steps, want):
+        b.new.copy_(_i32(new))
+        b.x.copy_(x)
+        graph.replay()
+        for u, v in zip(w, b.bits()):
+            assert torch.equal(u, v)
+    assert P.pkv_get_device_error() == 0
+
+
+def test_steps_of_two_engines_on_two_streams(P):
+    """Two engines' calls at the same time, each on a stream given by name."""
+    both = [_steps(8), _steps(9)]
+    want = []
+    for i, steps in enumerate(both):
+        e = Engine(P, 20 + i)
+        for new, x in steps:
+            e.new.copy_(_i32(new))
+            e.x.copy_(x)
+            e.step()
+            e.past += e.new
+        want.append(e.bits())
+    engines = [Engine(P, 20 + i) for i in range(2)]
+    news = [[_i32(n) for n, _ in steps] for steps in both]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in engines]
+    for i in range(len(both[0])):
+        for e, steps, new, s in zip(engines, both, news, streams):
+            with torch.cuda.stream(s):
+                e.new.copy_(new[i])
+                e.x.copy_(steps[i][1])
+            e.step(stream=s)
+            with torch.cuda.stream(s):
+                e.past += e.new
+    torch.cuda.synchronize()
+    for e, w in zip(engines, want):
+        for u, v in zip(w, e.bits()):
+            assert torch.equal(u, v)
+    assert P.pkv_get_device_error() == 0
+
+
+def test_steps_at_the_far_end_of_a_large_pool(P):
+    """Blocks whose offsets pass 2^31 elements: 4.6 GB for K and for V."""
+    N, Hq, Hkv, D, B, M = 140000, 32, 4, 128, 32, 50
+    new = [1400, 1, 99]
+    e = Engine(P, 1, S=3, T=sum(new), Hq=Hq, Hkv=Hkv, D=D, B=B, M=M, N=N)
+    e.alloc.free_ids.copy_(torch.arange(N))     # the stack's top is the pool's end
+    e.new.copy_(_i32(new))
+    e.x.copy_(torch.randn(e.x.shape, generator=torch.Generator().manual_seed(4)))
+    e.step()
+    ids = torch.arange(N - 60, N)
+    tables = e.tables.cpu() - (N - 60)
+    used = sum(R.blocks(n, B) for n in new)
+    assert e.alloc.free_count.item() == N - used and int(e.tables[0, 0]) == N - 1
+    kp, vp = e.k_pool[ids.to(DEV)].cpu(), e.v_pool[ids.to(DEV)].cpu()
+    q, k, v = (t.view(sum(new), -1, D) for t in e.x.cpu().split([Hq * D, Hkv * D, Hkv * D], 1))
+    at = e.slots.cpu() - (N - 60) * B
+    eps = torch.finfo(torch.bfloat16).eps
+    for x, got in ((q, e.q_out.cpu()), (k, kp[at // B, :, at % B])):
+        ref, size = R.norm_rope(x, e.w.cpu(), 1e-6, e.cs.cpu(), e.pos.cpu().long(), False)
+        assert ((got.double() - ref).abs() <= eps / 2 * ref.abs() + 24 * 2.0 ** -24 * size + 2.0 ** -25).all()
+    assert torch.equal(vp[at // B, :, at % B], v)
+    ref, size, delta, length = R.chunk_attention(e.q_out.cpu(), kp, vp, e.start.tolist(), tables, new, D ** -0.5)
+    tol = R.chunk_tolerance(ref, size, delta, length, torch.bfloat16, torch.bfloat16)
+    assert ((e.out.cpu().double() - ref).abs() <= tol).all()
+    assert P.pkv_get_device_error() == 0
+
+
+def test_chunk_more_rows_than_32_bits_count(P):
+    """2^20 queries of 128 heads: 17 GB of them, and more rows times pieces than 2^31."""
+    T, S, G, D, B, n, step = 1 << 20, 64, 128, 64, 32, 1 << 14, 4099
+    g = torch.Generator().manual_seed(6)
+    base = torch.randn(step, G, D, generator=g).to(torch.bfloat16)
+    q = torch.empty(T, G, D, dtype=torch.bfloat16, device=DEV)
+    for t in range(0, T, step):
+        q[t:t + step].copy_(base[:min(step, T - t)])
+    kp, vp = (torch.randn(n // B, 1, B, D, generator=g).to(torch.bfloat16) for _ in range(2))
+    tables = torch.randperm(n // B, generator=g).to(torch.int32)[None].repeat(S, 1)  # one context for all
+    out = torch.full_like(q, 33.0)
+    ws = P.workspace_tensor(P.pkv_chunk_workspace_bytes(kp, T, S, G, n), DEV)
+    P.pkv_paged_attention_chunk(q, kp.to(DEV), vp.to(DEV), _i32(np.arange(S + 1) * n), tables.to(DEV),
+                                _i32([n] * S), D ** -0.5, out, n, ws)
+    assert P.pkv_get_device_error() == 0
+    rows = torch.tensor([0, 1, n - 1, n, 7 * n + 130, 40 * n + 9001, T - n, T - 1])
+    ref, size, delta, length = R.chunk_attention(base[rows % step], kp, vp, range(len(rows) + 1), tables,
+                                                 (rows % n + 1).tolist(), D ** -0.5)
+    tol = R.chunk_tolerance(ref, size, delta, length, torch.bfloat16, torch.bfloat16)
+    assert ((out[rows.to(DEV)].cpu().double() - ref).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("new", [[1, 3, 1], [40, 1, 60], [130, 5, 300]])
+def test_chunk_rows_between_requests_may_hold_anything(P, new):
+    """Query rows of no request hold NaN and infinities, next to those of every form of piece;
+    two requests read the same table row."""
+    ctx = [n + 150 for n in new]
+    c = Chunk("bf16", 8, 2, 128, 16, ctx, new, 12, pad=200)
+    want = c.run(P)
+    c.dev[0][sum(new):] = float("nan")
+    c.dev[0][sum(new) + 1] = float("inf")
+    assert torch.equal(c.run(P), want)
+    c.check(want)
+    d = Chunk("bf16", 8, 2, 128, 16, [ctx[0]] * 2, [new[0]] * 2, 13)
+    d.tables[1] = d.tables[0]
+    d.dev[4] = d.tables.to(DEV)
+    d.check(d.run(P))
+    assert P.pkv_get_device_error() == 0
+
+
+def test_norm_rope_write_streamed_in_a_graph(P):
+    """The kernel for many tokens, captured; other positions and slots at the replay."""
+    T, Hq, Hkv, D = 2200, 40, 4, 128
+    q, k, v, slots, pos, cs, w, kp, vp = _rope_case(T, Hq, Hkv, D, 16, "bf16", (True, True), 64, 0, 3000, 3, True)
+    d = [t.to(DEV) for t in (q, k, v, kp, vp, pos, slots)]
+    out, want = (torch.zeros(T, Hq, D, dtype=q.dtype, device=DEV) for _ in range(2))
+    kw = dict(q_weight=w[0].to(DEV), k_weight=w[1].to(DEV), cos_sin=cs.to(DEV))
+    P.pkv_qk_norm_rope_write(*d, out, **kw)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        P.pkv_qk_norm_rope_write(*d, out, **kw)
+    d[5].copy_(pos.flip(0))
+    d[6].copy_(slots.flip(0))
+    eager = [t.clone() for t in d]
+    graph.replay()
+    P.pkv_qk_norm_rope_write(*eager, want, **kw)
+    assert torch.equal(out, want) and not torch.equal(eager[3], kp.to(DEV))
+    assert torch.equal(d[3], eager[3]) and torch.equal(d[4], eager[4])
+    assert P.pkv_get_device_error() == 0
