@@ -515,14 +515,16 @@ pkv_status pkv_qk_norm_rope_write(const pkv_pool* pool, const void* q, int64_t q
  *   context_lens  int32 [num_seqs], each counting the request's new tokens
  *   max_context_len  host-side upper bound of context_lens
  *   out           [num_tokens][num_q_heads][head_dim] of out_dtype (PKV_F32 or the pool
- *                 type), 16-byte aligned; rows outside every request are left as they were
+ *                 type), 16-byte aligned, apart from the inputs; rows outside every request are left as
+ *                 they were
  *   workspace     pkv_chunk_workspace_bytes(...) bytes, always required; its contents need
  *                 no clearing.  Calls that may run at the same time need one each.
  * Cached rows at and past a request's context may hold anything; those below it must be
  * finite.  Any group size num_q_heads / num_kv_heads up to 128.  The probabilities enter
  * the product with V rounded to the pool's type when the output has that type, and with
  * about twice its precision when the output is fp32.  fp16 / bf16 pools of fewer than 2^31
- * (block, kv head, position) rows (else PKV_ERR_UNSUPPORTED).  Device errors: query_start
+ * (block, kv head, position) rows, and tables or max_context_len of at most 2^26 tokens (else
+ * PKV_ERR_UNSUPPORTED).  Device errors: query_start
  * not ascending within [0, num_tokens] (PKV_DEVERR_POSITION, nothing is computed); a
  * context_lens entry negative or past the table row or max_context_len
  * (PKV_DEVERR_CONTEXT, cut to that range); a table entry outside the pool

@@ -986,6 +986,9 @@ pkv_status pkv_paged_attention_chunk(const pkv_pool* pool, const void* q, int32_
     if (pool->dtype == PKV_F32 || G > 128) return PKV_ERR_UNSUPPORTED;
     if ((int64_t)pool->num_blocks * pool->num_kv_heads * pool->block_size >= (1ll << 31))
         return PKV_ERR_UNSUPPORTED;  // tensor-copy rows are int32
+    // one CTA may have a whole context, and the kernel's waits end after about 2 s
+    if (std::min<int64_t>((int64_t)max_blocks_per_seq * pool->block_size, max_context_len) > pkv::CHUNK_MAX_CONTEXT)
+        return PKV_ERR_UNSUPPORTED;
     const ChunkShape c = chunk_shape(pool, num_tokens, num_seqs, num_q_heads, max_context_len);
     if (c.pieces > INT32_MAX) return PKV_ERR_UNSUPPORTED;
     if (num_tokens == 0 || num_seqs == 0) return PKV_OK;
@@ -999,7 +1002,7 @@ pkv_status pkv_paged_attention_chunk(const pkv_pool* pool, const void* q, int32_
     char* ws = static_cast<char*>(workspace);
     const int32_t sms = sm_count();
 
-    pkv::ChunkTensors x{q, pool->k, pool->v, num_tokens, (int32_t)std::min<int64_t>(c.pieces, sms)};
+    pkv::ChunkTensors x{q, pool->k, pool->v, num_tokens, (int32_t)std::min<int64_t>(c.pieces, sms), c.tiles};
     pkv::ChunkPlanParams pl{};
     pl.query_start = query_start;
     pl.context_lens = context_lens;
@@ -1044,9 +1047,8 @@ pkv_status pkv_paged_attention_chunk(const pkv_pool* pool, const void* q, int32_
     p.part_l = reinterpret_cast<float*>(ws + c.l);
     p.part_o = reinterpret_cast<float*>(ws + c.o);
     p.err = err;
-    if (pkv::launch_chunk_plan(pl, c.tiles, s) != cudaSuccess) return PKV_ERR_CUDA;
-    const cudaError_t e = pool->dtype == PKV_F16 ? pkv::launch_chunk<__half>(p, x, s)
-                                                 : pkv::launch_chunk<__nv_bfloat16>(p, x, s);
+    const cudaError_t e = pool->dtype == PKV_F16 ? pkv::launch_chunk<__half>(pl, p, x, s)
+                                                 : pkv::launch_chunk<__nv_bfloat16>(pl, p, x, s);
     if (e == cudaErrorNotSupported) return PKV_ERR_UNSUPPORTED;
     if (e != cudaSuccess) return PKV_ERR_CUDA;
     if (c.partial_rows == 0) return PKV_OK;

@@ -958,7 +958,8 @@ inline bool encode_query_map(CUtensorMap* map, const void* q, int T_, int Hq, in
 }
 
 template <typename T, int D, bool SPLIT_P>
-cudaError_t launch_chunk_tds(const ChunkParams& p, const ChunkTensors& x, cudaStream_t stream) {
+cudaError_t launch_chunk_tds(const ChunkPlanParams& plan, const ChunkParams& p, const ChunkTensors& x,
+                             cudaStream_t stream) {
     constexpr int SMEM = ChunkSmem<D>::BYTES;
     const long long rows = (long long)p.num_blocks * p.num_kv_heads * p.block_size;
     const int G = p.group;
@@ -977,6 +978,9 @@ cudaError_t launch_chunk_tds(const ChunkParams& p, const ChunkTensors& x, cudaSt
         if (e != cudaSuccess) return e;
         if (dev < 64) configured[dev].store(true, std::memory_order_release);
     }
+    // nothing is launched before everything that may be refused
+    e = launch_chunk_plan(plan, x.max_tiles, stream);
+    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)x.ctas);
     cfg.blockDim = dim3(CHUNK_THREADS);
@@ -991,14 +995,15 @@ cudaError_t launch_chunk_tds(const ChunkParams& p, const ChunkTensors& x, cudaSt
 }
 
 template <typename T>
-cudaError_t launch_chunk_impl(const ChunkParams& p, const ChunkTensors& x, cudaStream_t stream) {
+cudaError_t launch_chunk_impl(const ChunkPlanParams& plan, const ChunkParams& p, const ChunkTensors& x,
+                              cudaStream_t stream) {
     const bool f32_out = p.out_dtype == PKV_F32;
     if (p.head_dim == 64)
-        return f32_out ? launch_chunk_tds<T, 64, true>(p, x, stream)
-                       : launch_chunk_tds<T, 64, false>(p, x, stream);
+        return f32_out ? launch_chunk_tds<T, 64, true>(plan, p, x, stream)
+                       : launch_chunk_tds<T, 64, false>(plan, p, x, stream);
     if (p.head_dim == 128)
-        return f32_out ? launch_chunk_tds<T, 128, true>(p, x, stream)
-                       : launch_chunk_tds<T, 128, false>(p, x, stream);
+        return f32_out ? launch_chunk_tds<T, 128, true>(plan, p, x, stream)
+                       : launch_chunk_tds<T, 128, false>(plan, p, x, stream);
     return cudaErrorInvalidValue;
 }
 

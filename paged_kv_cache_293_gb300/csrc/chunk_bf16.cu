@@ -4,8 +4,9 @@
 namespace pkv {
 
 template <>
-cudaError_t launch_chunk<__nv_bfloat16>(const ChunkParams& p, const ChunkTensors& x, cudaStream_t stream) {
-    return launch_chunk_impl<__nv_bfloat16>(p, x, stream);
+cudaError_t launch_chunk<__nv_bfloat16>(const ChunkPlanParams& plan, const ChunkParams& p, const ChunkTensors& x,
+                                        cudaStream_t stream) {
+    return launch_chunk_impl<__nv_bfloat16>(plan, p, x, stream);
 }
 
 }  // namespace pkv

@@ -4,8 +4,9 @@
 namespace pkv {
 
 template <>
-cudaError_t launch_chunk<__half>(const ChunkParams& p, const ChunkTensors& x, cudaStream_t stream) {
-    return launch_chunk_impl<__half>(p, x, stream);
+cudaError_t launch_chunk<__half>(const ChunkPlanParams& plan, const ChunkParams& p, const ChunkTensors& x,
+                                 cudaStream_t stream) {
+    return launch_chunk_impl<__half>(plan, p, x, stream);
 }
 
 }  // namespace pkv

@@ -138,6 +138,7 @@ struct RopeParams {
 // Chunk attention (chunk.cuh, chunk_plan.cu).
 constexpr int CHUNK_TILE = 128;       // cached tokens per step
 constexpr int CHUNK_SPLIT_MIN = 8;    // steps below which no context is cut
+constexpr int64_t CHUNK_MAX_CONTEXT = 1 << 26;  // 2^19 steps: about 1 s of one CTA
 
 // A piece of work: queries [token, token + queries) of the batch for one kv head, over the
 // steps [kt0, kt1) of the request's context.  Query j sees positions below lim0 + j.
@@ -202,6 +203,7 @@ struct ChunkTensors {
     const void* v_pool;
     int32_t num_tokens;
     int32_t ctas;
+    int64_t max_tiles;
 };
 
 // ------------------------------------------------------------------ PTX helpers
@@ -452,7 +454,7 @@ cudaError_t launch_build_batch(const BatchParams& p, cudaStream_t stream);
 cudaError_t launch_rope_write(const RopeParams& p, int32_t dtype, cudaStream_t stream);
 cudaError_t launch_chunk_plan(const ChunkPlanParams& p, int64_t max_tiles, cudaStream_t stream);
 template <typename T>
-cudaError_t launch_chunk(const ChunkParams& p, const ChunkTensors& x, cudaStream_t stream);
+cudaError_t launch_chunk(const ChunkPlanParams& plan, const ChunkParams& p, const ChunkTensors& x, cudaStream_t stream);
 cudaError_t launch_chunk_merge(const ChunkParams& p, int ctas, cudaStream_t stream);
 cudaError_t launch_copy_blocks(const pkv_pool& src, const pkv_pool& dst, const int32_t* pairs,
                                int32_t num_pairs, unsigned int* err, cudaStream_t stream);

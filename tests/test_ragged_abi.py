@@ -102,6 +102,9 @@ def test_chunk_refusals(P):
     assert _chunk(P, pool=_pool(P, num_blocks=1 << 26)) == P.PKV_ERR_UNSUPPORTED     # 2^31 rows
     assert _chunk(P, ws=None) == P.PKV_ERR_WORKSPACE
     assert _chunk(P, ws=ODD) == P.PKV_ERR_WORKSPACE
+    assert _chunk(P, M=1 << 23, max_ctx=(1 << 26) + 1) == P.PKV_ERR_UNSUPPORTED      # longer contexts
+    assert _chunk(P, M=1 << 23, max_ctx=1 << 26, q=None) == P.PKV_ERR_INVALID
+    assert _chunk(P, M=4, max_ctx=(1 << 31) - 1, q=None) == P.PKV_ERR_INVALID        # the table bounds it
     need = P.lib.pkv_chunk_workspace_bytes(ctypes.byref(_pool(P)), 4, 2, 4, 64)
     assert need > 0
     assert _chunk(P, ws_bytes=need - 1) == P.PKV_ERR_WORKSPACE
