@@ -24,7 +24,12 @@ namespace {
 
 constexpr float PARTIAL_ROWS_PER_STEP = 7000.f;  // of 128 values: 1 KB each at about 5 TB/s in 1.45 us
 constexpr int PIECE_STEPS = 2;       // F above
-constexpr int LENGTH_CLASSES = 16;
+constexpr int COST_CLASSES = 16;
+// What a piece costs, for its place in the list, in steps of two query tiles: a step of one tile
+// waits for the HBM alone, and two tiles come with queries and outputs of up to 128 KB.  48
+// requests, 70 % decoding, 40 / 40 heads: 245 us (256 by steps alone); 40 requests, 28 / 4 heads:
+// 48.4 us (49.8); 24 requests of up to 512 queries, 16 / 4 heads of 64: 30.6 us (31.1).
+constexpr float ONE_TILE_STEP = 0.7f, TWO_TILE_EXTRA = 1.5f;
 constexpr int COUNT_MAX = 1 << 25;
 
 __device__ __forceinline__ int4 add4(int4 a, int4 b) {
@@ -259,25 +264,27 @@ __global__ void __launch_bounds__(N) chunk_plan_kernel(const ChunkPlanParams p) 
         int4 mine = amounts(), total;
         int4 v = block_scan4<N>(mine, warp_sums, &total);
         if (total.x > p.ctas) {
-            // longest pieces first: a counting sort of the round's tiles by length class, in
+            // longest pieces first: a counting sort of the round's tiles by classes of cost, in
             // tile order within a class
-            const int cls = ti < num_tiles ? min(LENGTH_CLASSES - 1, (int)((float)((cut - len) * LENGTH_CLASSES) * inv_cut))
-                                           : LENGTH_CLASSES;  // no tile: behind the others
+            const float most = (float)cut + TWO_TILE_EXTRA;
+            const float cost = tile.z > QT / 2 ? (float)len + TWO_TILE_EXTRA : ONE_TILE_STEP * (float)len;
+            const int cls = ti < num_tiles ? min(COST_CLASSES - 1, (int)((most - cost) * (COST_CLASSES / most)))
+                                           : COST_CLASSES;  // no tile: behind the others
             const unsigned same = __match_any_sync(FULL_MASK, cls);
             const int before = __popc(same & ((1u << lane) - 1u));
             // counts by (class, warp), then their sums: entry c * W + w is class c of warp w
-            constexpr int W = N / 32, COUNTS = LENGTH_CLASSES * W;
+            constexpr int W = N / 32, COUNTS = COST_CLASSES * W;
             static_assert(COUNTS <= N, "one count per thread");
-            if (lane < LENGTH_CLASSES) first_s[lane * W + warp] = 0;
+            if (lane < COST_CLASSES) first_s[lane * W + warp] = 0;
             __syncwarp();
-            if (before == 0 && cls < LENGTH_CLASSES) first_s[cls * W + warp] = __popc(same);
+            if (before == 0 && cls < COST_CLASSES) first_s[cls * W + warp] = __popc(same);
             __syncthreads();
             const int count = tid < COUNTS ? first_s[tid] : 0;
             int all_tiles;
             const int upto = block_scan<N>(count, warp_sums, &all_tiles);
             if (tid < COUNTS) first_s[tid] = upto - count;
             __syncthreads();
-            if (cls < LENGTH_CLASSES) tiles_s[first_s[cls * W + warp] + before] = tile;
+            if (cls < COST_CLASSES) tiles_s[first_s[cls * W + warp] + before] = tile;
             __syncthreads();
             if (ti < num_tiles) {
                 tile = tiles_s[tid];
