@@ -31,6 +31,7 @@ constexpr int COST_CLASSES = 16;
 // 48.4 us (49.8); 24 requests of up to 512 queries, 16 / 4 heads of 64: 30.6 us (31.1).
 constexpr float ONE_TILE_STEP = 0.7f, TWO_TILE_EXTRA = 1.5f;
 constexpr int COUNT_MAX = 1 << 25;
+constexpr float MANY_ITEMS = 3.f;
 
 __device__ __forceinline__ int4 add4(int4 a, int4 b) {
     return make_int4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
@@ -111,11 +112,12 @@ __device__ __forceinline__ int tile_steps(const int4& tile) {
 template <int N>
 __global__ void __launch_bounds__(N) chunk_plan_kernel(const ChunkPlanParams p) {
     __shared__ int4 warp_sums[32];
-    __shared__ int max_steps_s;
+    __shared__ int max_steps_s, all_steps_s;
     __shared__ int sums_s[7][32];  // of each candidate
     __shared__ int start_s[N + 1], tile_start_s[N + 1], ctx_s[N];
     __shared__ int4 tiles_s[N];  // this round's tiles
     __shared__ int first_s[N];   // tiles before, by (class, warp)
+    __shared__ int warp_pieces_s[32];
     __shared__ int4 base_s[N];   // pieces, partial rows, cut items, their rows before it
     // the attention kernel may set itself up meanwhile; it waits for this grid's end
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -128,7 +130,7 @@ __global__ void __launch_bounds__(N) chunk_plan_kernel(const ChunkPlanParams p) 
     const int* ctxs = few ? ctx_s : p.context_lens;
     if (tid == 0) {
         tile_start[0] = 0;
-        max_steps_s = 0;
+        max_steps_s = all_steps_s = 0;
     }
     for (int i = tid; i < 7 * 32; i += N) sums_s[i >> 5][i & 31] = 0;
 
@@ -167,7 +169,7 @@ __global__ void __launch_bounds__(N) chunk_plan_kernel(const ChunkPlanParams p) 
 
     // ---- one record per tile, the longest of a request first
     const long long cap = min((long long)p.max_blocks_per_seq * p.block_size, (long long)p.max_context_len);
-    int steps = 0;
+    int steps = 0, all_steps = 0;
     for (int ti = tid; ti < num_tiles; ti += N) {
         int lo = 0, hi = p.num_seqs - 1;
         while (lo < hi) {  // first request whose tiles end past ti
@@ -183,16 +185,25 @@ __global__ void __launch_bounds__(N) chunk_plan_kernel(const ChunkPlanParams p) 
         const int j0 = (tile_start[lo + 1] - 1 - ti) * QT;
         const int4 tile = make_int4(lo, j0, min(QT, nq - j0), ctx - nq + 1 + j0);
         tiles[ti] = tile;
-        steps = max(steps, tile_steps(tile));
+        const int n = tile_steps(tile);
+        steps = max(steps, n);
+        all_steps = min(all_steps + n, COUNT_MAX / 32);
     }
     steps = __reduce_max_sync(FULL_MASK, steps);
-    if (lane == 0) atomicMax(&max_steps_s, steps);
+    all_steps = (int)__reduce_add_sync(FULL_MASK, (unsigned)all_steps);
+    if (lane == 0 && steps > 0) {
+        atomicMax(&max_steps_s, steps);
+        atomicAdd(&all_steps_s, all_steps);
+    }
     __syncthreads();
     const int max_steps = max_steps_s;
+    // each CTA's share of the steps is MANY_ITEMS of the longest item: the pieces handed out last
+    // are short, and cutting could shorten nothing
+    const bool many = (float)all_steps_s * (float)p.num_kv_heads >= MANY_ITEMS * (float)max_steps * (float)p.num_sms;
 
     // ---- pieces of the longest item: 32 candidates, some for each warp
     int cut = max(max_steps, 1);  // steps per piece at most
-    if (p.max_partial_rows > 0 && max_steps >= CHUNK_SPLIT_MIN) {
+    if (p.max_partial_rows > 0 && max_steps >= CHUNK_SPLIT_MIN && !many) {
         // lane k - 1 of every warp: candidate k's steps per piece
         const int my_c = (max_steps + lane) / (lane + 1);
         const float my_inv = __fdividef(1.f, (float)my_c);
@@ -242,6 +253,8 @@ __global__ void __launch_bounds__(N) chunk_plan_kernel(const ChunkPlanParams p) 
     // ---- the pieces, the heads of a tile behind one another
     const float inv_cut = 1.f / (float)cut;
     const int H = p.num_kv_heads;
+    int* parts_s = ctx_s;          // of each tile: its pieces
+    int* token_s = tile_start_s;   // and its first token (both arrays are done with)
     int4 base = make_int4(0, 0, 0, 0);  // pieces, partial rows, cut items, their rows
     for (int t0 = 0; t0 < num_tiles; t0 += N) {
         const int ti = t0 + tid;
@@ -262,8 +275,10 @@ __global__ void __launch_bounds__(N) chunk_plan_kernel(const ChunkPlanParams p) 
             return make_int4(H * pc, pc > 1 ? H * pc * R : 0, pc > 1 ? H : 0, pc > 1 ? H * R : 0);
         };
         int4 mine = amounts(), total;
-        int4 v = block_scan4<N>(mine, warp_sums, &total);
-        if (total.x > p.ctas) {
+        const int warp_pieces = (int)__reduce_add_sync(FULL_MASK, (unsigned)mine.x);
+        if (lane == 0) warp_pieces_s[warp] = warp_pieces;
+        __syncthreads();
+        if (__reduce_add_sync(FULL_MASK, (unsigned)(lane < N / 32 ? warp_pieces_s[lane] : 0)) > (unsigned)p.ctas) {
             // longest pieces first: a counting sort of the round's tiles by classes of cost, in
             // tile order within a class
             const float most = (float)cut + TWO_TILE_EXTRA;
@@ -291,41 +306,46 @@ __global__ void __launch_bounds__(N) chunk_plan_kernel(const ChunkPlanParams p) 
                 pc = parts_of(tile);
             }
             mine = amounts();
-            v = block_scan4<N>(mine, warp_sums, &total);
         } else if (ti < num_tiles) {
             tiles_s[tid] = tile;
         }
+        const int4 v = block_scan4<N>(mine, warp_sums, &total);
+        parts_s[tid] = pc;
+        token_s[tid] = ti < num_tiles ? starts[tile.x] + tile.y : 0;
         base_s[tid] = make_int4(base.x + v.x - mine.x, base.y + v.y - mine.y, base.z + v.z - mine.z,
                                 base.w + v.w - mine.w);
         __syncthreads();
         // `lanes` lanes write a tile's pieces
         const int lanes = H >= 32 ? 32 : 1 << (32 - __clz(max(H - 1, 0)));  // H rounded up to a power of two
-#pragma unroll 1
+#pragma unroll 2
         for (int k = tid / lanes; k < live; k += N / lanes) {
             const int4 x = tiles_s[k], at = base_s[k];
-            const int n = tile_steps(x), parts = parts_of(x), rows = x.z * p.group;
-            const int token = starts[x.x] + x.y;
+            const int n = tile_steps(x), parts = parts_s[k], token = token_s[k], rows = x.z * p.group;
+            int4* out = reinterpret_cast<int4*>(p.pieces + at.x);
+            if (parts == 1) {
+#pragma unroll 2
+                for (int h = tid & (lanes - 1); h < H; h += lanes) {
+                    out[2 * h] = make_int4(token, h, x.z, x.w);
+                    out[2 * h + 1] = make_int4(x.x, 0, n, -1);
+                }
+                continue;
+            }
 #pragma unroll 1
             for (int e = tid & (lanes - 1); e < H * parts; e += lanes) {
-                const int h = parts > 1 ? e / parts : e, r = e - h * parts;
-                ChunkPiece y;
-                y.token = token;
-                y.kv_head = h;
-                y.queries = x.z;
-                y.lim0 = x.w;
-                y.seq = x.x;
+                const int h = e / parts, r = e - h * parts;
                 // (at most 2^24 steps and 32 parts)
-                y.kt0 = parts > 1 ? (int)((unsigned)n * (unsigned)r / (unsigned)parts) : 0;
-                y.kt1 = parts > 1 ? (int)((unsigned)n * (unsigned)(r + 1) / (unsigned)parts) : n;
-                y.part_row = parts > 1 ? at.y + e * rows : -1;
-                p.pieces[at.x + e] = y;
-                if (parts > 1 && r == 0) {
+                const int kt0 = (int)((unsigned)n * (unsigned)r / (unsigned)parts);
+                const int kt1 = (int)((unsigned)n * (unsigned)(r + 1) / (unsigned)parts);
+                const int part_row = at.y + e * rows;
+                out[2 * e] = make_int4(token, h, x.z, x.w);
+                out[2 * e + 1] = make_int4(x.x, kt0, kt1, part_row);
+                if (r == 0) {
                     ChunkMerge m;
                     m.token = token;
                     m.kv_head = h;
                     m.rows = rows;
                     m.parts = parts;
-                    m.part_row = y.part_row;
+                    m.part_row = part_row;
                     m.first = at.w + h * rows;
                     m.pad0 = m.pad1 = 0;
                     p.merges[at.z + h] = m;
