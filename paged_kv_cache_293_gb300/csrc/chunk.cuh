@@ -40,7 +40,7 @@
 // What bounds it, measured.  Two full tiles: a step has 2048 cycles of MMAs and takes about
 // 2600, the way of one tile once round: its softmax (1480 cycles: scores from tensor memory 310,
 // 128 exponentials 920), the second half of P.V (256), Q.K^T (512) and three hand-overs.  8192
-// tokens from the first on, 32 / 8 heads of 128, bf16: 352 us, 1.56 PFLOP/s; 500 tokens over
+// tokens from the first on, 32 / 8 heads of 128, bf16: 350 us, 1.57 PFLOP/s; 500 tokens over
 // 130,500: 700 us, 1.52 PFLOP/s.  What got it there, each for that prompt:
 //   MMAs and copies issued under elect.sync and not under lane == 0 (67 cycles an MMA, 100 a
 //     copy there): 470 -> 411 us, and with V's copies three-dimensional (one for both halves of
@@ -50,7 +50,9 @@
 //   registers so that the softmax does not spill: 373 -> 364; output by warps of its own: 352.
 // Few rows: 64 KB of K and V a step bound it, 1960 cycles where the HBM's share of an SM is 2790.
 // Tried and slower: 16 softmax warps that share rows and exchange maxima; exponentials begun
-// with the old reference before the maximum is known; merging cut items in this kernel.
+// with the old reference before the maximum is known; merging cut items in this kernel; the first
+// scores of the next piece issued before the last products of this one (48 requests, 70 % decoding,
+// 40 / 40 heads: 268 us, 256 without), and its record and first block fetched early (260).
 // Every wait is bounded; a CTA that gives up sets PKV_DEVERR_TIMEOUT and returns its tensor
 // memory.
 #pragma once
@@ -67,7 +69,9 @@ constexpr int CHUNK_THREADS = 512;
 // (256 * 184 + 128 * 72 + 128 * 72 = 512 * 128).
 constexpr int CHUNK_REGS_SOFTMAX = 184, CHUNK_REGS_OTHERS = 72, CHUNK_REGS_OUTPUT = 72;
 constexpr float CHUNK_RESCALE_LOG2 = 8.f;
-constexpr int CHUNK_FEW_ROWS = 16;  // rows up to which a piece's steps are spread over four warps
+// Rows up to which a piece's steps are spread over four warps: 200 requests with 1-5 queries, 32 / 8
+// heads, contexts about 300: 70 us (85 with 4 rows).
+constexpr int CHUNK_FEW_ROWS = 16;
 
 template <int D>
 struct ChunkSmem {

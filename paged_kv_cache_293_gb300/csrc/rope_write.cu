@@ -276,7 +276,7 @@ __global__ void __launch_bounds__(ROPE_MAX_THREADS) rope_write_kernel(const Rope
 }
 
 // Many tokens: CTAs that stay and stream them.  A token's q, k and v rows and its table row are
-// each contiguous, so one thread brings them into a ring of stages by bulk copies; eight warps
+// each contiguous, so one thread brings them into a ring of stages by bulk copies; four warps
 // turn the q and k rows in place, and the same thread sends q out by one bulk copy and every
 // head of k and v to its cache row by one each.  The copies keep running whatever the
 // arithmetic does, which loads held in registers (rope_write_kernel) do not: 16384 tokens of
