@@ -1055,7 +1055,8 @@ pkv_status pkv_paged_attention_chunk(const pkv_pool* pool, const void* q, int32_
     // half of what the GPU holds at a time: few to set up where nothing was cut (24 requests of up to
     // 512 queries 30.6 -> 29.8 us against 16 per SM; with 1 per SM 500 tokens over 130,500 take 735
     // us and not 700)
-    const int64_t merge_ctas = std::min<int64_t>(4 * (int64_t)sms, ((int64_t)num_tokens * num_q_heads + 7) / 8);
+    const int64_t merge_ctas = std::min<int64_t>(
+        4 * (int64_t)sms, std::max(c.tiles * pool->num_kv_heads, ((int64_t)num_tokens * num_q_heads + 7) / 8));
     return pkv::launch_chunk_merge(p, (int)merge_ctas, s) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 

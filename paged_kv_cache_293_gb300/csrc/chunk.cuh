@@ -418,7 +418,7 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
             }
             if (pc.kv_head < 0) break;
             int next = 0;
-            if (lane == 0) next = atomicAdd(p.header + 3, 1);
+            if (lane == 0) next = atomicAdd(p.header + 2, 1);
             const int32_t* bt_row = p.block_tables + (size_t)pc.seq * p.max_blocks_per_seq;
             const int tok_end = pc.lim0 + pc.queries - 1;
             auto row_of = [&](int kt) -> int {  // pool row of this lane's copy in step kt

@@ -35,16 +35,19 @@ constexpr int COUNT_MAX = 1 << 25;
 // mixed batch of 51 tiles and 40 heads.
 constexpr float MANY_ITEMS = 3.f;
 
-__device__ __forceinline__ int4 add4(int4 a, int4 b) {
-    return make_int4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
+__device__ __forceinline__ int3 add3(int3 a, int3 b) { return make_int3(a.x + b.x, a.y + b.y, a.z + b.z); }
+
+__device__ __forceinline__ int3 shfl3(int3 v, int from) {
+    return make_int3(__shfl_sync(FULL_MASK, v.x, from), __shfl_sync(FULL_MASK, v.y, from),
+                     __shfl_sync(FULL_MASK, v.z, from));
 }
 
-__device__ __forceinline__ int4 warp_scan4(int4 v, int lane) {
+__device__ __forceinline__ int3 warp_scan3(int3 v, int lane) {
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int4 u = make_int4(__shfl_up_sync(FULL_MASK, v.x, o), __shfl_up_sync(FULL_MASK, v.y, o),
-                                 __shfl_up_sync(FULL_MASK, v.z, o), __shfl_up_sync(FULL_MASK, v.w, o));
-        if (lane >= o) v = add4(v, u);
+        const int3 u = make_int3(__shfl_up_sync(FULL_MASK, v.x, o), __shfl_up_sync(FULL_MASK, v.y, o),
+                                 __shfl_up_sync(FULL_MASK, v.z, o));
+        if (lane >= o) v = add3(v, u);
     }
     return v;
 }
@@ -60,26 +63,23 @@ __device__ __forceinline__ int warp_scan(int v, int lane) {
 
 // Inclusive sums over the CTA's N threads; `total` gets the sums over all of them.
 template <int N>
-__device__ __forceinline__ int4 block_scan4(int4 v, int4* warp_sums, int4* total) {
+__device__ __forceinline__ int3 block_scan3(int3 v, int3* warp_sums, int3* total) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    v = warp_scan4(v, lane);
+    v = warp_scan3(v, lane);
     if (lane == 31) warp_sums[warp] = v;
     __syncthreads();
     // every warp sums the warps before it itself: one barrier less
-    const int4 w = warp_scan4(lane < N / 32 ? warp_sums[lane] : make_int4(0, 0, 0, 0), lane);
-    const int from = warp > 0 ? warp - 1 : 0;
-    const int4 before = make_int4(__shfl_sync(FULL_MASK, w.x, from), __shfl_sync(FULL_MASK, w.y, from),
-                                  __shfl_sync(FULL_MASK, w.z, from), __shfl_sync(FULL_MASK, w.w, from));
-    if (warp > 0) v = add4(v, before);
-    *total = make_int4(__shfl_sync(FULL_MASK, w.x, 31), __shfl_sync(FULL_MASK, w.y, 31),
-                       __shfl_sync(FULL_MASK, w.z, 31), __shfl_sync(FULL_MASK, w.w, 31));
+    const int3 w = warp_scan3(lane < N / 32 ? warp_sums[lane] : make_int3(0, 0, 0), lane);
+    const int3 before = shfl3(w, warp > 0 ? warp - 1 : 0);
+    if (warp > 0) v = add3(v, before);
+    *total = shfl3(w, 31);
     __syncthreads();  // warp_sums is free again
     return v;
 }
 
 // The same for one value.
 template <int N>
-__device__ __forceinline__ int block_scan(int v, int4* warp_sums, int* total) {
+__device__ __forceinline__ int block_scan(int v, int3* warp_sums, int* total) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     v = warp_scan(v, lane);
     if (lane == 31) warp_sums[warp].x = v;
@@ -113,14 +113,14 @@ __device__ __forceinline__ int tile_steps(const int4& tile) {
 // of the batch fits into one round and go to the workspace when it does not.
 template <int N>
 __global__ void __launch_bounds__(N) chunk_plan_kernel(const ChunkPlanParams p) {
-    __shared__ int4 warp_sums[32];
+    __shared__ int3 warp_sums[32];
     __shared__ int max_steps_s, all_steps_s;
     __shared__ int sums_s[7][32];  // of each candidate
     __shared__ int start_s[N + 1], tile_start_s[N + 1], ctx_s[N];
     __shared__ int4 tiles_s[N];  // this round's tiles
     __shared__ int first_s[N];   // tiles before, by (class, warp)
     __shared__ int warp_pieces_s[32];
-    __shared__ int4 base_s[N];   // pieces, partial rows, cut items, their rows before it
+    __shared__ int3 base_s[N];   // pieces, partial rows, cut items before it
     // the attention kernel may set itself up meanwhile; it waits for this grid's end
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -156,7 +156,7 @@ __global__ void __launch_bounds__(N) chunk_plan_kernel(const ChunkPlanParams p) 
         if (__syncthreads_or(bad)) {
             if (tid == 0) {
                 set_error(p.err, PKV_DEVERR_POSITION);
-                p.header[0] = p.header[1] = p.header[2] = p.header[3] = 0;
+                p.header[0] = p.header[1] = p.header[2] = 0;
             }
             return;
         }
@@ -257,7 +257,7 @@ __global__ void __launch_bounds__(N) chunk_plan_kernel(const ChunkPlanParams p) 
     const int H = p.num_kv_heads;
     int* parts_s = ctx_s;          // of each tile: its pieces
     int* token_s = tile_start_s;   // and its first token (both arrays are done with)
-    int4 base = make_int4(0, 0, 0, 0);  // pieces, partial rows, cut items, their rows
+    int3 base = make_int3(0, 0, 0);  // pieces, partial rows, cut items
     for (int t0 = 0; t0 < num_tiles; t0 += N) {
         const int ti = t0 + tid;
         const int live = min(N, num_tiles - t0);
@@ -273,10 +273,9 @@ __global__ void __launch_bounds__(N) chunk_plan_kernel(const ChunkPlanParams p) 
             len = tile_steps(tile) / pc;
         }
         auto amounts = [&] {
-            const int R = tile.z * p.group;
-            return make_int4(H * pc, pc > 1 ? H * pc * R : 0, pc > 1 ? H : 0, pc > 1 ? H * R : 0);
+            return make_int3(H * pc, pc > 1 ? H * pc * tile.z * p.group : 0, pc > 1 ? H : 0);
         };
-        int4 mine = amounts(), total;
+        int3 mine = amounts(), total;
         const int warp_pieces = (int)__reduce_add_sync(FULL_MASK, (unsigned)mine.x);
         if (lane == 0) warp_pieces_s[warp] = warp_pieces;
         __syncthreads();
@@ -311,17 +310,17 @@ __global__ void __launch_bounds__(N) chunk_plan_kernel(const ChunkPlanParams p) 
         } else if (ti < num_tiles) {
             tiles_s[tid] = tile;
         }
-        const int4 v = block_scan4<N>(mine, warp_sums, &total);
+        const int3 v = block_scan3<N>(mine, warp_sums, &total);
         parts_s[tid] = pc;
         token_s[tid] = ti < num_tiles ? starts[tile.x] + tile.y : 0;
-        base_s[tid] = make_int4(base.x + v.x - mine.x, base.y + v.y - mine.y, base.z + v.z - mine.z,
-                                base.w + v.w - mine.w);
+        base_s[tid] = make_int3(base.x + v.x - mine.x, base.y + v.y - mine.y, base.z + v.z - mine.z);
         __syncthreads();
         // `lanes` lanes write a tile's pieces
         const int lanes = H >= 32 ? 32 : 1 << (32 - __clz(max(H - 1, 0)));  // H rounded up to a power of two
 #pragma unroll 1
         for (int k = tid / lanes; k < live; k += N / lanes) {
-            const int4 x = tiles_s[k], at = base_s[k];
+            const int4 x = tiles_s[k];
+            const int3 at = base_s[k];
             const int n = tile_steps(x), parts = parts_s[k], token = token_s[k], rows = x.z * p.group;
             int4* out = reinterpret_cast<int4*>(p.pieces + at.x);
             if (parts == 1) {
@@ -348,80 +347,91 @@ __global__ void __launch_bounds__(N) chunk_plan_kernel(const ChunkPlanParams p) 
                     m.rows = rows;
                     m.parts = parts;
                     m.part_row = part_row;
-                    m.first = at.w + h * rows;
-                    m.pad0 = m.pad1 = 0;
+                    m.pad0 = m.pad1 = m.pad2 = 0;
                     p.merges[at.z + h] = m;
                 }
             }
         }
-        base = add4(base, total);
+        base = add3(base, total);
         __syncthreads();
     }
     if (tid == 0) {
         p.header[0] = base.x;
         p.header[1] = base.z;
-        p.header[2] = base.w;
-        p.header[3] = p.ctas;  // pieces handed out: CTA i starts with piece i
+        p.header[2] = p.ctas;  // pieces handed out: CTA i starts with piece i
     }
 }
 
 // One warp per row of a cut item: out = sum_k 2^(m_k - M) o_k / sum_k 2^(m_k - M) l_k over
-// its pieces (at most 32: lane k holds piece k's weight).
+// its pieces (at most 32: lane k holds piece k's weight).  A CTA takes every n-th group of eight
+// rows of one item, where n CTAs share it, so that a row's way is three loads behind one another:
+// counts, item, results.
 template <int D>
 __global__ void __launch_bounds__(256) chunk_merge_kernel(const ChunkParams p) {
-    constexpr int V = D / 32;
+    constexpr int V = D / 32, AHEAD = 4;  // results loaded before their weights are known
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int lane = threadIdx.x & 31;
-    const int rows = p.header[2], items = p.header[1];
-    for (int g = blockIdx.x * 8 + (threadIdx.x >> 5); g < rows; g += gridDim.x * 8) {
-        int lo = 0, n = items;  // the last item starting at or before g is one of lo .. lo + n - 1
-        while (n > 1) {         // 32 of them at a time, evenly spread
-            const int step = (n + 31) / 32, at = lo + lane * step;
-            const unsigned before = __ballot_sync(FULL_MASK, at < lo + n && p.merges[at].first <= g);
-            const int k = 31 - __clz(before);  // lane 0's always does
-            const int end = lo + n;
-            lo += k * step;
-            n = min(step, end - lo);
-        }
-        const ChunkMerge m = p.merges[lo];
-        const int r = g - m.first;
-        const long long row0 = (long long)m.part_row + r;
-        float mk = -INFINITY, lk = 0.f;
-        if (lane < m.parts) {
-            mk = p.part_m[row0 + (long long)lane * m.rows];
-            lk = p.part_l[row0 + (long long)lane * m.rows];
-        }
-        if (!(lk > 0.f)) mk = -INFINITY;
-        float M = mk;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int items = p.header[1];
+    if (items == 0) return;
+    const int share = max(1, (int)gridDim.x / items);  // CTAs of an item
+    if ((int)blockIdx.x >= items * share) return;
+    for (int item = (int)blockIdx.x % items; item < items; item += (int)gridDim.x) {
+        const ChunkMerge m = p.merges[item];
+        for (int r = (int)blockIdx.x / items * 8 + warp; r < m.rows; r += share * 8) {
+            const long long row0 = (long long)m.part_row + r;
+            const float* src = p.part_o + row0 * D + lane * V;
+            const long long apart = (long long)m.rows * D;
+            auto load = [&](float (&v)[V], int k) {
+                if constexpr (V == 4) {
+                    const float4 x = *reinterpret_cast<const float4*>(src + k * apart);
+                    v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+                } else {
+                    const float2 x = *reinterpret_cast<const float2*>(src + k * apart);
+                    v[0] = x.x; v[1] = x.y;
+                }
+            };
+            float v[AHEAD][V];
 #pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(FULL_MASK, M, o));
-        const float w = lk > 0.f ? fast_exp2(mk - M) : 0.f;
-        float l = w * lk;
-#pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) l += __shfl_xor_sync(FULL_MASK, l, o);
-        float acc[V];
-#pragma unroll
-        for (int i = 0; i < V; ++i) acc[i] = 0.f;
-#pragma unroll 4
-        for (int k = 0; k < m.parts; ++k) {
-            const float wk = __shfl_sync(FULL_MASK, w, k);
-            const float* src = p.part_o + (row0 + (long long)k * m.rows) * D + lane * V;
-            float v[V];
-            if constexpr (V == 4) {
-                const float4 x = *reinterpret_cast<const float4*>(src);
-                v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
-            } else {
-                const float2 x = *reinterpret_cast<const float2*>(src);
-                v[0] = x.x; v[1] = x.y;
+            for (int k = 0; k < AHEAD; ++k)
+                if (k < m.parts) load(v[k], k);
+            float mk = -INFINITY, lk = 0.f;
+            if (lane < m.parts) {
+                mk = p.part_m[row0 + (long long)lane * m.rows];
+                lk = p.part_l[row0 + (long long)lane * m.rows];
             }
-            // a piece that saw nothing for this row has weight 0 and zeros
+            if (!(lk > 0.f)) mk = -INFINITY;
+            float M = mk;
 #pragma unroll
-            for (int i = 0; i < V; ++i) acc[i] = fmaf(wk, v[i], acc[i]);
+            for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(FULL_MASK, M, o));
+            const float w = lk > 0.f ? fast_exp2(mk - M) : 0.f;
+            float l = w * lk;
+#pragma unroll
+            for (int o = 16; o >= 1; o >>= 1) l += __shfl_xor_sync(FULL_MASK, l, o);
+            float acc[V];
+#pragma unroll
+            for (int i = 0; i < V; ++i) acc[i] = 0.f;
+            // (a piece that saw nothing for this row has weight 0 and zeros)
+#pragma unroll
+            for (int k = 0; k < AHEAD; ++k) {
+                const float wk = __shfl_sync(FULL_MASK, w, k);
+                if (k < m.parts) {
+#pragma unroll
+                    for (int i = 0; i < V; ++i) acc[i] = fmaf(wk, v[k][i], acc[i]);
+                }
+            }
+#pragma unroll 4
+            for (int k = AHEAD; k < m.parts; ++k) {
+                const float wk = __shfl_sync(FULL_MASK, w, k);
+                float x[V];
+                load(x, k);
+#pragma unroll
+                for (int i = 0; i < V; ++i) acc[i] = fmaf(wk, x[i], acc[i]);
+            }
+            const size_t out =
+                (((size_t)m.token + r / p.group) * p.num_q_heads + m.kv_head * p.group + r % p.group) * D + lane * V;
+#pragma unroll
+            for (int i = 0; i < V; ++i) store_out(p.out, p.out_dtype, out + i, l > 0.f ? acc[i] / l : 0.f);
         }
-        const size_t out = (((size_t)m.token + r / p.group) * p.num_q_heads + m.kv_head * p.group + r % p.group) * D +
-                           lane * V;
-#pragma unroll
-        for (int i = 0; i < V; ++i) store_out(p.out, p.out_dtype, out + i, l > 0.f ? acc[i] / l : 0.f);
     }
 }
 

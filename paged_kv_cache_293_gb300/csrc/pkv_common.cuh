@@ -151,10 +151,10 @@ struct __align__(16) ChunkPiece {
 };
 
 // A cut item: `rows` (query, head) rows whose `parts` pieces left partial results, piece k's
-// at part_row + k * rows; `first` counts the rows of the cut items before it.
+// at part_row + k * rows.
 struct __align__(16) ChunkMerge {
     int32_t token, kv_head, rows, parts;
-    int32_t part_row, first, pad0, pad1;
+    int32_t part_row, pad0, pad1, pad2;
 };
 
 // Whether the piece's last copy holds positions no query of it sees.
@@ -172,7 +172,7 @@ struct ChunkPlanParams {
     int32_t num_sms, ctas;
     int64_t max_partial_rows;     // 0: no context may be cut
     int64_t max_cut_pieces;
-    int32_t* header;              // pieces, cut items, their rows, next piece
+    int32_t* header;              // pieces, cut items, next piece
     int32_t* tile_start;          // [S + 1]
     int4* tiles;                  // (request, first query, queries, limit of the first)
     ChunkPiece* pieces;
