@@ -30,8 +30,12 @@ namespace {
 constexpr int ROPE_FEW_ROWS = 2, ROPE_ROWS = 8;
 constexpr int ROPE_FEW_TOKENS = 512;
 constexpr int ROPE_MAX_THREADS = 512;
-constexpr int STREAM_WARPS = 4, STREAM_THREADS = (STREAM_WARPS + 1) * 32, STREAM_MAX_STAGES = 4;
-constexpr int STREAM_BYTES = 54 * 1024;  // of stages per CTA: four CTAs on an SM
+constexpr int STREAM_MAX_STAGES = 4;
+// Of stages per SM, at least three for each of four, two or one CTAs with four, eight or sixteen
+// warps that turn rows; measured for the rows too wide for four CTAs, 4000 tokens: 40 + 2 * 40
+// heads of 128, fp32 83.5 us (136 without streaming), 32 + 2 * 32 65.7 (86.3); 32 + 2 * 8, fp32
+// 34.6 (36.4 with four warps in each of two CTAs), 64 + 2 * 8, bf16 35.1 (37.6).
+constexpr int STREAM_BYTES = 216 * 1024;
 // Streaming pays for its set-up and for its few instructions per copy from about this many
 // values in all and bytes per token on; measured with head_dim 128, streaming against not:
 // 32 + 2 * 8 heads, bf16: 512 tokens 4.9 / 5.0 us, 1024 7.0 / 9.2, 8192 36.1 / 58.0;
@@ -276,7 +280,7 @@ __global__ void __launch_bounds__(ROPE_MAX_THREADS) rope_write_kernel(const Rope
 }
 
 // Many tokens: CTAs that stay and stream them.  A token's q, k and v rows and its table row are
-// each contiguous, so one thread brings them into a ring of stages by bulk copies; four warps
+// each contiguous, so one thread brings them into a ring of stages by bulk copies; the other warps
 // turn the q and k rows in place, and the same thread sends q out by one bulk copy and every
 // head of k and v to its cache row by one each.  The copies keep running whatever the
 // arithmetic does, which loads held in registers (rope_write_kernel) do not: 16384 tokens of
@@ -291,11 +295,11 @@ __device__ __forceinline__ void bulk_wait_read() {
     asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
 }
 
-template <typename T, int D, bool INTERLEAVED, bool FULL>
-__global__ void __launch_bounds__(STREAM_THREADS) rope_stream_kernel(const RopeParams p, int stages,
+template <typename T, int D, bool INTERLEAVED, bool FULL, int WARPS>
+__global__ void __launch_bounds__((WARPS + 1) * 32) rope_stream_kernel(const RopeParams p, int stages,
                                                                      uint32_t stage_bytes) {
     constexpr int V = 16 / (int)sizeof(T), LPR = D / V, P = Chunk8<T>::PAIRS;
-    constexpr int GROUPS = STREAM_WARPS * 32 / LPR;
+    constexpr int GROUPS = WARPS * 32 / LPR;
     extern __shared__ __align__(128) unsigned char ring[];
     __shared__ __align__(8) uint64_t bars[2 * STREAM_MAX_STAGES];
     __shared__ int live[STREAM_MAX_STAGES];  // the stage holds a token
@@ -309,13 +313,13 @@ __global__ void __launch_bounds__(STREAM_THREADS) rope_stream_kernel(const RopeP
     if (threadIdx.x == 0) {
         for (int st = 0; st < stages; ++st) {
             mbar_init(full(st), 1);
-            mbar_init(done(st), STREAM_WARPS);
+            mbar_init(done(st), WARPS);
         }
         mbar_init_fence();
     }
     __syncthreads();
     bool ok = true;
-    if (warp == STREAM_WARPS) {
+    if (warp == WARPS) {
         if (umma::elect_one()) {  // one thread as the compiler sees it: copies are issued faster
             const uint64_t policy = l2_evict_first_policy();  // the projections are not read again
             auto token = [&](int i) { return (int)blockIdx.x + i * (int)gridDim.x; };
@@ -381,6 +385,8 @@ __global__ void __launch_bounds__(STREAM_THREADS) rope_stream_kernel(const RopeP
         const int lo = INTERLEAVED || !turns ? l * V : l * (V / 2);
         const int hi = INTERLEAVED || !turns ? lo + V / 2 : lo + half;
         const bool norm_q = p.q_weight != nullptr, norm_k = p.k_weight != nullptr;
+        // the groups with the fewest q rows take the first k rows
+        const int first = (group + GROUPS - Hq % GROUPS) % GROUPS;
         for (int i = 0; i < n; ++i) {
             const int st = i % stages;
             ok = __all_sync(FULL_MASK, mbar_wait_short(full(st), (i / stages) & 1));
@@ -412,8 +418,6 @@ __global__ void __launch_bounds__(STREAM_THREADS) rope_stream_kernel(const RopeP
                     }
                 }
                 make_turn<T, INTERLEAVED, P>(m, p.k_weight, lo, hi, turns, c, s);
-                // the groups with the fewest q rows take the first k rows
-                const int first = (group + GROUPS - Hq % GROUPS) % GROUPS;
                 for (int h0 = 0; h0 < Hkv; h0 += GROUPS) {
                     const int h = h0 + first;
                     if (!__any_sync(FULL_MASK, h < Hkv)) break;
@@ -460,21 +464,25 @@ template <typename T, int D, bool INTERLEAVED>
 cudaError_t launch_rope_tdi(const RopeParams& p, cudaStream_t stream) {
     const int H = p.num_q_heads + 2 * p.num_kv_heads;
     const long long stage = ((long long)H * D * (int)sizeof(T) + 4ll * p.rotary_dim + 127) / 128 * 128;
-    if (stage >= STREAM_MIN_ROW && 3 * stage <= 2 * STREAM_BYTES &&
+    if (stage >= STREAM_MIN_ROW && 3 * stage <= STREAM_BYTES &&
         p.num_tokens * (stage / (int)sizeof(T)) >= STREAM_MIN_VALUES) {
-        auto kernel = p.rotary_dim == D ? rope_stream_kernel<T, D, INTERLEAVED, true>
-                                        : rope_stream_kernel<T, D, INTERLEAVED, false>;
-        const int per_sm = 3 * stage <= STREAM_BYTES ? 4 : 2;
-        const long long room = (long long)STREAM_BYTES * 4 / per_sm;
+        // (the wider ones ask for the rotated elements' number as they run)
+        const int per_sm = 12 * stage <= STREAM_BYTES ? 4 : 6 * stage <= STREAM_BYTES ? 2 : 1;
+        auto kernel = per_sm == 1   ? rope_stream_kernel<T, D, INTERLEAVED, false, 16>
+                      : per_sm == 2 ? rope_stream_kernel<T, D, INTERLEAVED, false, 8>
+                      : p.rotary_dim == D ? rope_stream_kernel<T, D, INTERLEAVED, true, 4>
+                                          : rope_stream_kernel<T, D, INTERLEAVED, false, 4>;
+        const int threads = (16 / per_sm + 1) * 32;
+        const long long room = STREAM_BYTES / per_sm;
         const int stages = (int)(room / stage < STREAM_MAX_STAGES ? room / stage : STREAM_MAX_STAGES);
         int dev = 0, sms = 0;
         cudaError_t e = cudaGetDevice(&dev);
         if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
         if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 2 * STREAM_BYTES);
+            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, STREAM_BYTES);
         if (e != cudaSuccess) return e;
         const int ctas = p.num_tokens < sms * per_sm ? p.num_tokens : sms * per_sm;
-        kernel<<<ctas, STREAM_THREADS, (size_t)stages * stage, stream>>>(p, stages, (uint32_t)stage);
+        kernel<<<ctas, threads, (size_t)stages * stage, stream>>>(p, stages, (uint32_t)stage);
         return cudaGetLastError();
     }
     return p.num_tokens < ROPE_FEW_TOKENS ? launch_rope_rows<T, D, INTERLEAVED, ROPE_FEW_ROWS>(p, stream)

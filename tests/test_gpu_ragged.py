@@ -231,6 +231,14 @@ def test_norm_rope_write(P, dtype, T, Hq, Hkv, D, B, norm, rot, inter, pad, pack
     assert torch.equal(got, wk)
 
 
+@pytest.mark.parametrize("dtype,T,Hq,Hkv,D,rot", [
+    ("f32", 700, 40, 40, 128, 128), ("bf16", 500, 100, 30, 128, 96), ("f16", 1200, 130, 7, 64, 64),
+    ("f32", 600, 90, 30, 128, 0), ("bf16", 300, 300, 20, 128, 128)])
+def test_norm_rope_write_wide_rows(P, dtype, T, Hq, Hkv, D, rot):
+    """Tokens so wide that one or two CTAs' stages fill an SM, or none do."""
+    test_norm_rope_write(P, dtype, T, Hq, Hkv, D, 16, (1, rot != 96), rot, rot == 64, 3, True)
+
+
 @pytest.mark.parametrize("T", [33, 2200])
 def test_norm_rope_write_in_place_and_unrotated_infinities(P, T):
     """q_out may be q itself; elements past the rotated ones are not touched by the rotation,
