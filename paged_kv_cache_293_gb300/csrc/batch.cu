@@ -108,12 +108,22 @@ __device__ __forceinline__ Pair block_inclusive(Pair v, Pair* warp_sums, Pair* t
     return v;
 }
 
-// Four tokens in a row: one search for the request of the first, wide stores.  starts and ctxs
-// are query_start and context_lens or copies of them.
-__device__ __forceinline__ void fill_tokens(const BatchParams& p, long long t0, int real, bool wide,
+// The first of requests lo .. num_seqs - 1 that ends past token t (there is one).
+__device__ __forceinline__ int request_of(const int* starts, int lo, int num_seqs, long long t) {
+    int hi = num_seqs - 1;
+    while (lo < hi) {
+        const int mid = lo + ((hi - lo) >> 1);
+        if (starts[mid + 1] > t) hi = mid; else lo = mid + 1;
+    }
+    return lo;
+}
+
+// Four tokens in a row, the first of request s (when it is one of the `real` ones), with wide
+// stores.  starts and ctxs are query_start and context_lens or copies of them.
+__device__ __forceinline__ void fill_tokens(const BatchParams& p, long long t0, int real, int s, bool wide,
                                             const int* starts, const int* ctxs) {
     const int S = p.num_seqs, M = p.max_blocks_per_seq, B = p.block_size;
-    int s = -1, end = 0, next_pos = 0, ctx = 0;
+    int end = 0, next_pos = 0, ctx = 0;
     int pos[4], seq[4];
     long long slot[4];
 #pragma unroll
@@ -122,14 +132,8 @@ __device__ __forceinline__ void fill_tokens(const BatchParams& p, long long t0, 
         pos[i] = seq[i] = -1;
         slot[i] = -1;
         if (t >= real) continue;
-        if (s < 0 || t >= end) {
-            int lo = s < 0 ? 0 : s + 1, hi = S - 1;  // first request ending past t
-            if (s >= 0 && starts[lo + 1] > t) hi = lo;
-            while (lo < hi) {
-                const int mid = lo + ((hi - lo) >> 1);
-                if (starts[mid + 1] > t) hi = mid; else lo = mid + 1;
-            }
-            s = lo;
+        if (i == 0 || t >= end) {
+            if (i > 0 && starts[++s + 1] <= t) s = request_of(starts, s + 1, S, t);
             end = starts[s + 1];
             ctx = ctxs[s];
             next_pos = ctx - (end - (int)t);
@@ -168,14 +172,16 @@ template <int CTAS>
 __global__ void __launch_bounds__(BATCH_THREADS) build_batch_kernel(const BatchParams p, int fill) {
     static_assert(BATCH_WARPS == 32, "one lane per warp total");
     __shared__ Pair warp_sums[BATCH_WARPS];
-    __shared__ Pair cta_total;         // read by the other CTAs of the cluster
-    __shared__ long long cta_popped;   // blocks popped up to this CTA's last served request
+    __shared__ Pair totals_s[CTAS];       // of every CTA, written by each into all
+    __shared__ long long popped_s[CTAS];  // blocks popped up to each CTA's last served request: of rank 0
+    __shared__ long long cta_popped;      // this CTA's
     __shared__ long long upto_s[BATCH_THREADS];  // inclusive block counts of the tile's requests
     __shared__ int first_s[BATCH_THREADS];       // first fresh logical block, -1: not served
     __shared__ int start_s[BATCH_THREADS + 1], ctx_s[BATCH_THREADS];  // one CTA: starts and contexts
     cg::cluster_group cluster = cg::this_cluster();
     // the token kernel may be set up meanwhile; it waits for this grid's end
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (CTAS > 1) cluster.barrier_arrive();  // running: its shared memory may be written to
     const int rank = CTAS > 1 ? (int)cluster.block_rank() : 0, tid = threadIdx.x;
     const int S = p.num_seqs, M = p.max_blocks_per_seq, B = p.block_size;
     const int per = (S + CTAS - 1) / CTAS;
@@ -198,11 +204,12 @@ __global__ void __launch_bounds__(BATCH_THREADS) build_batch_kernel(const BatchP
             mine.need += held_need.need;
         }
         block_inclusive(mine, warp_sums, &total);
-        if (tid == 0) cta_total = total;
+        cluster.barrier_wait();
+        if (tid < CTAS) *cluster.map_shared_rank(&totals_s[rank], tid) = total;
         cluster.sync();  // also: every CTA has read the free count before it may be rewritten
 #pragma unroll
         for (int r = 0; r < CTAS; ++r) {
-            const Pair v = *cluster.map_shared_rank(&cta_total, r);
+            const Pair v = totals_s[r];
             all_tokens += v.tokens;
             if (r < rank) {
                 base.tokens += v.tokens;
@@ -246,6 +253,7 @@ __global__ void __launch_bounds__(BATCH_THREADS) build_batch_kernel(const BatchP
         for (long long k = tid; k < tile.need; k += BATCH_THREADS) {
             const long long at = base.need + k;
             if (at >= free_blocks) break;  // past the stack: its request is not served
+            const int id = p.alloc.free_ids[free_blocks - 1 - at];
             int lo = 0, hi = min(BATCH_THREADS, s_hi - s0) - 1;
             while (lo < hi) {
                 const int mid = (lo + hi) >> 1;
@@ -253,7 +261,6 @@ __global__ void __launch_bounds__(BATCH_THREADS) build_batch_kernel(const BatchP
             }
             if (first_s[lo] < 0) continue;
             const long long before = lo > 0 ? upto_s[lo - 1] : base.need;
-            const int id = p.alloc.free_ids[free_blocks - 1 - at];
             int32_t* entry = p.block_tables + (size_t)(s0 + lo) * M + first_s[lo] + (at - before);
             if ((unsigned)id >= (unsigned)p.alloc.num_blocks) {
                 set_error(p.err, PKV_DEVERR_BLOCK_ID);  // not a free stack: no block is taken
@@ -269,29 +276,55 @@ __global__ void __launch_bounds__(BATCH_THREADS) build_batch_kernel(const BatchP
     }
     if (CTAS == 1) all_tokens = base.tokens;
     if (all_tokens > p.max_tokens && rank == 0 && tid == 0) set_error(p.err, PKV_DEVERR_POSITION);
-    if (CTAS > 1) cluster.sync();  // starts, contexts and tables of every CTA are visible
-
+    if (CTAS > 1) {
+        if (tid == 0) *cluster.map_shared_rank(&popped_s[rank], 0) = cta_popped;
+        cluster.sync();  // and starts, contexts and tables of every CTA are visible
+    }
     if (rank == 0 && tid == 0) {
         long long popped = cta_popped;
-        if (CTAS > 1)
-            for (int r = 1; r < CTAS; ++r) popped = max(popped, *cluster.map_shared_rank(&cta_popped, r));
+#pragma unroll
+        for (int r = 1; r < CTAS; ++r) popped = max(popped, popped_s[r]);
         *p.free_count_out = (int)(free_blocks - popped);
     }
     if (fill) {
         const int real = (int)min(all_tokens, (long long)p.max_tokens);
         const bool wide = wide_tokens(p);
+        const int* starts = CTAS == 1 ? start_s : p.query_start;
         for (long long t0 = ((long long)rank * BATCH_THREADS + tid) * 4; t0 < p.max_tokens;
              t0 += (long long)CTAS * BATCH_THREADS * 4)
-            fill_tokens(p, t0, real, wide, CTAS == 1 ? start_s : p.query_start, CTAS == 1 ? ctx_s : p.context_lens);
+            fill_tokens(p, t0, real, t0 < real ? request_of(starts, 0, S, t0) : 0, wide, starts,
+                        CTAS == 1 ? ctx_s : p.context_lens);
     }
-    if (CTAS > 1) cluster.sync();  // no CTA ends while CTA 0 may still read its shared memory
 }
 
 __global__ void __launch_bounds__(TOKENS_THREADS) batch_tokens_kernel(const BatchParams p) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const long long t0 = ((long long)blockIdx.x * TOKENS_THREADS + threadIdx.x) * 4;
-    if (t0 < p.max_tokens)
-        fill_tokens(p, t0, p.query_start[p.num_seqs], wide_tokens(p), p.query_start, p.context_lens);
+    const int S = p.num_seqs, lane = threadIdx.x & 31;
+    const int* starts = p.query_start;
+    const long long t0 = ((long long)blockIdx.x * TOKENS_THREADS + threadIdx.x) * 4, w0 = t0 - 4 * lane;
+    const int real = starts[S];
+    int s = 0;
+    if (w0 < real) {
+        // the request of the warp's first token, 32 groups of requests at a time: two or three loads
+        // behind one another where one lane's search would take twelve
+        int lo = 0, n = S;
+        while (n > 1) {
+            const int step = (n + 31) / 32, first = lane * step;
+            const bool past = first < n && starts[lo + min(first + step, n)] > w0;  // the group's last ends past it
+            const int k = __ffs(__ballot_sync(FULL_MASK, past)) - 1;
+            lo += k * step;
+            n = min(step, n - k * step);
+        }
+        // that of each lane's: among the next 32, whose ends the lanes hold, or searched for
+        const int end = starts[min(lo + lane, S - 1) + 1];
+        int k = 0;
+#pragma unroll
+        for (int b = 16; b >= 1; b >>= 1)
+            if (__shfl_sync(FULL_MASK, end, k + b - 1) <= t0) k += b;
+        s = min(lo + k, S - 1);
+        if (t0 < real && k == 31 && starts[s + 1] <= t0) s = request_of(starts, s, S, t0);
+    }
+    if (t0 < p.max_tokens) fill_tokens(p, t0, real, s, wide_tokens(p), starts, p.context_lens);
 }
 
 cudaError_t launch_build_batch(const BatchParams& p, cudaStream_t stream) {
