@@ -28,12 +28,12 @@ namespace {
 
 constexpr int BATCH_CTAS = 8;          // portable cluster size
 constexpr int BATCH_THREADS = 1024;
-// Requests of one CTA, one per thread: 100 requests 6.4 us (the cluster 10.7), 1000 with one token
-// each 8.2 (12.9).
+// Requests of one CTA, one per thread: 100 requests 6.0 us (the cluster 9.2), 1000 with one token
+// each 7.7 (10.5).
 constexpr int BATCH_ONE_CTA = 1024;
 // Tokens up to which the first kernel fills them in itself, one round of one CTA: 300 requests with
-// 3400 tokens 8.2 us (8.8 with the second kernel), 2 with 5600 7.5 (6.3 with it), 1000 with 15000
-// 17.9 (11.2 with it).
+// 3400 tokens 7.8 us (8.6 with the second kernel), 2 with 5600 7.5 (6.4 with it), 1000 with 15000
+// 17.2 (10.0 with it).
 constexpr int BATCH_FEW_TOKENS = 4096;
 constexpr int TOKENS_THREADS = 256;
 constexpr int BATCH_WARPS = BATCH_THREADS / 32;
