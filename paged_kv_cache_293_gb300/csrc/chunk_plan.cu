@@ -5,7 +5,7 @@
 // one item, whose steps are the 128-token stretches of the context its last query may see.
 // An item is cut into several pieces along the context only where that shortens the whole:
 // the cuts are tried for 1 to 32 pieces of the longest item, and the number with the smallest
-// estimate taken.  Pieces are handed out longest first, so the end comes close to the larger
+// estimate taken.  Pieces are handed out costliest first, so the end comes close to the larger
 // of two lower bounds, in steps of one CTA with F steps of fixed cost per piece (a piece costs
 // up to 6000 cycles beside its steps of 2400 to 2800):
 //   all steps / CTAs,
