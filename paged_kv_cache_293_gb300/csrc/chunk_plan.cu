@@ -280,7 +280,7 @@ __global__ void __launch_bounds__(N) chunk_plan_kernel(const ChunkPlanParams p) 
         if (lane == 0) warp_pieces_s[warp] = warp_pieces;
         __syncthreads();
         if (__reduce_add_sync(FULL_MASK, (unsigned)(lane < N / 32 ? warp_pieces_s[lane] : 0)) > (unsigned)p.ctas) {
-            // longest pieces first: a counting sort of the round's tiles by classes of cost, in
+            // costliest pieces first: a counting sort of the round's tiles by classes of cost, in
             // tile order within a class
             const float most = (float)cut + TWO_TILE_EXTRA;
             const float cost = tile.z > QT / 2 ? (float)len + TWO_TILE_EXTRA : ONE_TILE_STEP * (float)len;
