@@ -112,6 +112,14 @@ __device__ __forceinline__ uint64_t l2_evict_normal_policy() {
     return pol;
 }
 
+// x, as a value made here: addresses derived from it are made where they are used.  Kept in
+// registers across the loops, those of all the products took the MMA warp 192 bytes past its
+// registers, and an 8192-token prompt 402 us and not 357.
+__device__ __forceinline__ uint32_t made_here(uint32_t x) {
+    asm volatile("" : "+r"(x));
+    return x;
+}
+
 template <int N>
 __device__ __forceinline__ void regs_dec() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
@@ -299,7 +307,7 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
                        const __grid_constant__ CUtensorMap tmap_v, const ChunkParams p) {
     using L = ChunkSmem<D>;
     constexpr int NS = L::STAGES, KS = D / 16;
-    constexpr int KV_WARP = 8, MMA_WARP = 9, Q_WARP = 10, IDLE_WARP = 11, OUT_WARP = 12;
+    constexpr int KV_WARP = 8, MMA_WARP = 9, Q_WARP = 10, OUT_WARP = 12;
     constexpr int CONSUMERS = 8 + 2 + 4;  // arrivals that free a slot of the piece ring
     constexpr uint32_t FMT = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
     constexpr uint32_t IDESC_S = umma::idesc_f16(FMT, false, 128, CHUNK_TILE);
@@ -391,296 +399,297 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
         return pc.kv_head >= 0;
     };
 
-    // each role sets its registers inside its own branch: where branches meet again, the
-    // compiler would hold both to the smaller number
-    if (warp == KV_WARP) {
+    // Each warpgroup sets its registers once, all four warps at the same place (setmaxnreg is
+    // undefined where a warpgroup's warps do not take it alike), and inside its own branch: where
+    // branches meet again, the compiler would hold both to the smaller number.
+    if (warp >= KV_WARP && warp < OUT_WARP) {
         regs_dec<CHUNK_REGS_OTHERS>();
-        // ---- pieces, and the pages of each: K then V of every 128-token step
-        const uint64_t policy = l2_evict_normal_policy();
-        const ChunkPiece first_piece = p.pieces[blockIdx.x];  // the list has a place for each CTA
-        const int n_pieces = p.header[0];
-        const int B = p.block_size, Hkv = p.num_kv_heads;
-        const int far_row = p.num_blocks * Hkv * B;  // past the pools: copies bring zeros
-        constexpr int NBOX = CHUNK_TILE / CHUNK_TOKENS;  // 16-token copies of a step; lane b finds b's block
-        uint32_t it = 0;  // stages filled so far
-        int idx = blockIdx.x;
-        for (int i = 0;; ++i) {
-            ChunkPiece pc;
-            pc.kv_head = -1;
-            if (idx < n_pieces) pc = i == 0 ? first_piece : p.pieces[idx];
-            if (i >= 2) {
-                ok = __all_sync(FULL_MASK, mbar_wait_short(piece_empty(i & 1), ((i >> 1) - 1) & 1));
-                if (!ok) break;
-            }
-            if (lane == 0) {
-                pieces[i & 1] = pc;
-                mbar_arrive(piece_full(i & 1));  // release: the record is visible to its waiters
-            }
-            if (pc.kv_head < 0) break;
-            int next = 0;
-            if (lane == 0) next = atomicAdd(p.header + 2, 1);
-            const int32_t* bt_row = p.block_tables + (size_t)pc.seq * p.max_blocks_per_seq;
-            const int tok_end = pc.lim0 + pc.queries - 1;
-            auto row_of = [&](int kt) -> int {  // pool row of this lane's copy in step kt
-                const int t = kt * CHUNK_TILE + lane * CHUNK_TOKENS;
-                if (kt >= pc.kt1 || t >= tok_end || lane >= NBOX) return far_row;
-                const int phys = __ldg(bt_row + t / B);
-                if ((unsigned)phys >= (unsigned)p.num_blocks) {
-                    set_error(p.err, PKV_DEVERR_BLOCK_ID);
-                    return far_row;
+        if (warp == KV_WARP) {
+            // ---- pieces, and the pages of each: K then V of every 128-token step
+            const uint64_t policy = l2_evict_normal_policy();
+            const ChunkPiece first_piece = p.pieces[blockIdx.x];  // the list has a place for each CTA
+            const int n_pieces = p.header[0];
+            const int B = p.block_size, Hkv = p.num_kv_heads;
+            const int far_row = p.num_blocks * Hkv * B;  // past the pools: copies bring zeros
+            constexpr int NBOX = CHUNK_TILE / CHUNK_TOKENS;  // 16-token copies of a step; lane b finds b's block
+            uint32_t it = 0;  // stages filled so far
+            int idx = blockIdx.x;
+            for (int i = 0;; ++i) {
+                ChunkPiece pc;
+                pc.kv_head = -1;
+                if (idx < n_pieces) pc = i == 0 ? first_piece : p.pieces[idx];
+                if (i >= 2) {
+                    ok = __all_sync(FULL_MASK, mbar_wait_short(piece_empty(i & 1), ((i >> 1) - 1) & 1));
+                    if (!ok) break;
                 }
-                return (phys * Hkv + pc.kv_head) * B + t % B;
-            };
-            int row = row_of(pc.kt0);
-            for (int kt = pc.kt0; kt < pc.kt1 && ok; ++kt) {
-                const int row_next = row_of(kt + 1);
-                int rows[NBOX];
-#pragma unroll
-                for (int b = 0; b < NBOX; ++b) rows[b] = __shfl_sync(FULL_MASK, row, b);
-#pragma unroll
-                for (int kv = 0; kv < 2; ++kv, ++it) {
-                    const int st = it % NS;
-                    if (it >= NS) {
-                        ok = __all_sync(FULL_MASK, mbar_wait_short(kv_empty(st), ((it / NS) - 1) & 1));
-                        if (!ok) break;
+                if (lane == 0) {
+                    pieces[i & 1] = pc;
+                    mbar_arrive(piece_full(i & 1));  // release: the record is visible to its waiters
+                }
+                if (pc.kv_head < 0) break;
+                int next = 0;
+                if (lane == 0) next = atomicAdd(p.header + 2, 1);
+                const int32_t* bt_row = p.block_tables + (size_t)pc.seq * p.max_blocks_per_seq;
+                const int tok_end = pc.lim0 + pc.queries - 1;
+                auto row_of = [&](int kt) -> int {  // pool row of this lane's copy in step kt
+                    const int t = kt * CHUNK_TILE + lane * CHUNK_TOKENS;
+                    if (kt >= pc.kt1 || t >= tok_end || lane >= NBOX) return far_row;
+                    const int phys = __ldg(bt_row + t / B);
+                    if ((unsigned)phys >= (unsigned)p.num_blocks) {
+                        set_error(p.err, PKV_DEVERR_BLOCK_ID);
+                        return far_row;
                     }
-                    // from one elected thread: copies issued by 16 lanes at once took about
-                    // 100 cycles each, and the whole kernel the time of its copies
-                    if (umma::elect_one()) {
-                        const uint32_t full = kv_full(st), dst = ring + st * L::TILE;
-                        mbar_arrive_expect_tx(full, L::TILE);
+                    return (phys * Hkv + pc.kv_head) * B + t % B;
+                };
+                int row = row_of(pc.kt0);
+                for (int kt = pc.kt0; kt < pc.kt1 && ok; ++kt) {
+                    const int row_next = row_of(kt + 1);
+                    int rows[NBOX];
 #pragma unroll
-                        for (int b = 0; b < NBOX; ++b) {
-                            if (kv == 0) {
-                                // K tile: 128-byte columns of 128 rows
+                    for (int b = 0; b < NBOX; ++b) rows[b] = __shfl_sync(FULL_MASK, row, b);
 #pragma unroll
-                                for (int x = 0; x < L::BOXES; ++x)
-                                    tma_load_2d(dst + x * L::BOX + b * CHUNK_TOKENS * 128, &tmap_k, x * 64, rows[b],
-                                                full, policy);
-                            } else {
-                                // V tile: a copy's columns behind one another (one K step of P.V)
-                                tma_load_3d(dst + b * CHUNK_TOKENS * D * 2, &tmap_v, 0, rows[b], 0, full, policy);
+                    for (int kv = 0; kv < 2; ++kv, ++it) {
+                        const int st = it % NS;
+                        if (it >= NS) {
+                            ok = __all_sync(FULL_MASK, mbar_wait_short(kv_empty(st), ((it / NS) - 1) & 1));
+                            if (!ok) break;
+                        }
+                        // from one elected thread: copies issued by 16 lanes at once took about
+                        // 100 cycles each, and the whole kernel the time of its copies
+                        if (umma::elect_one()) {
+                            const uint32_t full = kv_full(st), dst = ring + st * L::TILE;
+                            mbar_arrive_expect_tx(full, L::TILE);
+#pragma unroll
+                            for (int b = 0; b < NBOX; ++b) {
+                                if (kv == 0) {
+                                    // K tile: 128-byte columns of 128 rows
+#pragma unroll
+                                    for (int x = 0; x < L::BOXES; ++x)
+                                        tma_load_2d(dst + x * L::BOX + b * CHUNK_TOKENS * 128, &tmap_k, x * 64,
+                                                    rows[b], full, policy);
+                                } else {
+                                    // V tile: a copy's columns behind one another (one K step of P.V)
+                                    tma_load_3d(dst + b * CHUNK_TOKENS * D * 2, &tmap_v, 0, rows[b], 0, full, policy);
+                                }
                             }
+                        }
+                        __syncwarp();
+                    }
+                    row = row_next;
+                }
+                if (!ok) break;
+                idx = __shfl_sync(FULL_MASK, next, 0);
+            }
+            // the CTA must not end with copies still landing in its shared memory
+            for (uint32_t k = it > NS ? it - NS : 0; k < it; ++k) mbar_wait_short(kv_full(k % NS), (k / NS) & 1);
+        } else if (warp == Q_WARP) {
+            // ---- query tiles
+            int loads[2] = {0, 0}, fews = 0;  // copies into each tile, pieces with few rows
+            bool few_last = false;            // tile 1 was taken last by such a piece
+            ChunkPiece pc;
+            for (int i = 0; next_piece(i, pc); ++i) {
+                if (pc.kt1 <= pc.kt0) continue;
+                // a piece with few rows has them in tile 0 four times, 32 rows apart, and takes tile
+                // 1 for the warps' results
+                const bool few = is_few(pc);
+                for (int t = 0; t < (few || pc.queries > QPT ? 2 : 1); ++t) {
+                    if (t == 1 && few_last)
+                        ok = __all_sync(FULL_MASK, mbar_wait_short(few_read, (fews - 1) & 1));
+                    else if (loads[t] > 0)
+                        ok = __all_sync(FULL_MASK, mbar_wait_short(q_empty(t), (loads[t] - 1) & 1));
+                    if (!ok) break;
+                    if (t == 1) few_last = few;
+                    if (few && t == 1) {
+                        ++fews;
+                        continue;
+                    }
+                    ++loads[t];
+                    if (umma::elect_one()) {
+                        const uint32_t dst = q_s + t * L::TILE;
+                        if (few) {
+                            mbar_arrive_expect_tx(q_full(0), 4 * L::BOXES * (32 / G) * G * 128);
+                            for (int w = 0; w < 4; ++w)
+                                for (int x = 0; x < L::BOXES; ++x)
+                                    tma_load_4d(dst + x * L::BOX + w * 32 * 128, &tmap_q32, 0, x, pc.kv_head * G,
+                                                pc.token, q_full(0));
+                        } else {
+                            mbar_arrive_expect_tx(q_full(t), L::BOXES * QPT * G * 128);
+                            for (int x = 0; x < L::BOXES; ++x)
+                                tma_load_4d(dst + x * L::BOX, &tmap_q, 0, x, pc.kv_head * G, pc.token + t * QPT,
+                                            q_full(t));
                         }
                     }
                     __syncwarp();
                 }
-                row = row_next;
-            }
-            if (!ok) break;
-            idx = __shfl_sync(FULL_MASK, next, 0);
-        }
-        // the CTA must not end with copies still landing in its shared memory
-        for (uint32_t k = it > NS ? it - NS : 0; k < it; ++k) mbar_wait_short(kv_full(k % NS), (k / NS) & 1);
-    } else if (warp == Q_WARP) {
-        regs_dec<CHUNK_REGS_OTHERS>();
-        // ---- query tiles
-        int loads[2] = {0, 0}, fews = 0;  // copies into each tile, pieces with few rows
-        bool few_last = false;            // tile 1 was taken last by such a piece
-        ChunkPiece pc;
-        for (int i = 0; next_piece(i, pc); ++i) {
-            if (pc.kt1 <= pc.kt0) continue;
-            // a piece with few rows has them in tile 0 four times, 32 rows apart, and takes tile
-            // 1 for the warps' results
-            const bool few = is_few(pc);
-            for (int t = 0; t < (few || pc.queries > QPT ? 2 : 1); ++t) {
-                if (t == 1 && few_last)
-                    ok = __all_sync(FULL_MASK, mbar_wait_short(few_read, (fews - 1) & 1));
-                else if (loads[t] > 0)
-                    ok = __all_sync(FULL_MASK, mbar_wait_short(q_empty(t), (loads[t] - 1) & 1));
                 if (!ok) break;
-                if (t == 1) few_last = few;
-                if (few && t == 1) {
-                    ++fews;
-                    continue;
+            }
+            for (int t = 0; t < 2; ++t)
+                if (loads[t] > 0) mbar_wait_short(q_full(t), (loads[t] - 1) & 1);
+        } else if (warp == MMA_WARP) {
+            // ---- MMA issue, the two tiles in turn: one thread for both, because MMAs issued by
+            // two threads are interleaved, both tiles' scores are then complete at the same time
+            // and their exponentials compete for the same units
+            uint32_t total = 0;               // stages of the pieces so far
+            int used[2] = {0, 0};             // Q tiles taken
+            int steps[4] = {0, 0, 0, 0};      // P tiles taken, as s_full and p_full count them
+            int outs[2] = {0, 0};             // pieces begun in O_0 and O_1
+            // i: tile 0 or 1, or 2, 3 for an even or odd step of a piece with one tile of queries
+            auto issue_s = [&](int i, int st) {  // S over the P just read: MMAs run in issue order
+                const uint64_t k_desc = umma::sw128_desc(ring + st * L::TILE, 16, 1024);
+                const uint64_t q_desc = umma::sw128_desc(made_here(q_s + (i == 1 ? L::TILE : 0)), 16, 1024);
+#pragma unroll
+                for (int kk = 0; kk < KS; ++kk) {
+                    const uint32_t off = ((kk >> 2) * L::BOX + (kk & 3) * 32) >> 4;  // start address field
+                    umma::mma_f16(tmem + (i & 1) * CHUNK_TILE, q_desc + off, k_desc + off, idesc_s, kk > 0 ? 1u : 0u);
                 }
-                ++loads[t];
-                if (umma::elect_one()) {
-                    const uint32_t dst = q_s + t * L::TILE;
-                    if (few) {
-                        mbar_arrive_expect_tx(q_full(0), 4 * L::BOXES * (32 / G) * G * 128);
-                        for (int w = 0; w < 4; ++w)
-                            for (int x = 0; x < L::BOXES; ++x)
-                                tma_load_4d(dst + x * L::BOX + w * 32 * 128, &tmap_q32, 0, x, pc.kv_head * G,
-                                            pc.token, q_full(0));
-                    } else {
-                        mbar_arrive_expect_tx(q_full(t), L::BOXES * QPT * G * 128);
-                        for (int x = 0; x < L::BOXES; ++x)
-                            tma_load_4d(dst + x * L::BOX, &tmap_q, 0, x, pc.kv_head * G, pc.token + t * QPT,
-                                        q_full(t));
+                umma::commit(s_full(i));  // also says that every P.V before is done
+            };
+            auto issue_pv = [&](int i, int st, bool first, bool few = false) -> bool {
+                // V is N-major: 64-element columns 2048 apart, 8-token groups 1024, and a K step
+                // is one copy's 16 tokens.  The first half's products run while the softmax still
+                // works on the second half.
+                const uint64_t v_desc = umma::sw128_desc(ring + st * L::TILE, CHUNK_TOKENS * 128, 1024);
+                const uint32_t cols = made_here(tmem), o_t = cols + L::O_COL + (i == 1 ? D : 0);
+                const uint32_t p_t =
+                    cols + (few ? L::FEW_P_COL + (i & 1) * (CHUNK_TILE / 2) : (i & 1) * CHUNK_TILE);
+                const uint32_t parity = steps[i]++ & 1;
+                if (first) {  // the piece before has been read from O
+                    int& o = outs[i == 1];
+                    if (o > 0 && !mbar_wait_short(o_free(i == 1), (o - 1) & 1)) return false;
+                    ++o;
+                }
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    if (!mbar_wait_short(p_full(i, h), parity)) return false;
+                    umma::fence_after_sync();
+#pragma unroll
+                    for (int k = 4 * h; k < 4 * h + 4; ++k) {
+                        const uint64_t bv = v_desc + (k * CHUNK_TOKENS * D * 2 >> 4);
+                        umma::mma_f16_tmem_a(o_t, p_t + k * 8, bv, IDESC_O, (!first || k > 0) ? 1u : 0u);
+                        if (SPLIT_P) umma::mma_f16_tmem_a(o_t, p_t + CHUNK_TILE / 2 + k * 8, bv, IDESC_O, 1u);
                     }
                 }
-                __syncwarp();
-            }
-            if (!ok) break;
-        }
-        for (int t = 0; t < 2; ++t)
-            if (loads[t] > 0) mbar_wait_short(q_full(t), (loads[t] - 1) & 1);
-    } else if (warp == MMA_WARP) {
-        regs_dec<CHUNK_REGS_OTHERS>();
-        // ---- MMA issue, the two tiles in turn: one thread for both, because MMAs issued by
-        // two threads are interleaved, both tiles' scores are then complete at the same time
-        // and their exponentials compete for the same units
-        uint32_t total = 0;               // stages of the pieces so far
-        int used[2] = {0, 0};             // Q tiles taken
-        int steps[4] = {0, 0, 0, 0};      // P tiles taken, as s_full and p_full count them
-        int outs[2] = {0, 0};             // pieces begun in O_0 and O_1
-        // i: tile 0 or 1, or 2, 3 for an even or odd step of a piece with one tile of queries
-        auto issue_s = [&](int i, int st) {  // S over the P just read: MMAs run in issue order
-            const uint64_t k_desc = umma::sw128_desc(ring + st * L::TILE, 16, 1024);
-            const uint64_t q_desc = umma::sw128_desc(q_s + (i == 1 ? L::TILE : 0), 16, 1024);
-#pragma unroll
-            for (int kk = 0; kk < KS; ++kk) {
-                const uint32_t off = ((kk >> 2) * L::BOX + (kk & 3) * 32) >> 4;  // start address field
-                umma::mma_f16(tmem + (i & 1) * CHUNK_TILE, q_desc + off, k_desc + off, idesc_s, kk > 0 ? 1u : 0u);
-            }
-            umma::commit(s_full(i));  // also says that every P.V before is done
-        };
-        auto issue_pv = [&](int i, int st, bool first, bool few = false) -> bool {
-            // V is N-major: 64-element columns 2048 apart, 8-token groups 1024, and a K step
-            // is one copy's 16 tokens.  The first half's products run while the softmax still
-            // works on the second half.
-            const uint64_t v_desc = umma::sw128_desc(ring + st * L::TILE, CHUNK_TOKENS * 128, 1024);
-            const uint32_t o_t = tmem + L::O_COL + (i == 1 ? D : 0);
-            const uint32_t p_t = tmem + (few ? L::FEW_P_COL + (i & 1) * (CHUNK_TILE / 2) : (i & 1) * CHUNK_TILE);
-            const uint32_t parity = steps[i]++ & 1;
-            if (first) {  // the piece before has been read from O
-                int& o = outs[i == 1];
-                if (o > 0 && !mbar_wait_short(o_free(i == 1), (o - 1) & 1)) return false;
-                ++o;
-            }
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                if (!mbar_wait_short(p_full(i, h), parity)) return false;
-                umma::fence_after_sync();
-#pragma unroll
-                for (int k = 4 * h; k < 4 * h + 4; ++k) {
-                    const uint64_t bv = v_desc + (k * CHUNK_TOKENS * D * 2 >> 4);
-                    umma::mma_f16_tmem_a(o_t, p_t + k * 8, bv, IDESC_O, (!first || k > 0) ? 1u : 0u);
-                    if (SPLIT_P) umma::mma_f16_tmem_a(o_t, p_t + CHUNK_TILE / 2 + k * 8, bv, IDESC_O, 1u);
-                }
-            }
-            return true;
-        };
-        ChunkPiece pc;
-        for (int i = 0; next_piece(i, pc); ++i) {
-            const int n = pc.kt1 - pc.kt0;
-            if (n <= 0) continue;
-            const bool two = pc.queries > QPT, few = is_few(pc);
-            int st = (int)(total % NS);  // next stage and its phase
-            uint32_t phase = (total / NS) & 1;
-            auto landed = [&] { return mbar_wait_short(kv_full(st), phase); };
-            auto advance = [&] {
-                if (++st == NS) {
-                    st = 0;
-                    phase ^= 1;
-                }
+                return true;
             };
-            if (!two) {
-                // one tile of queries: the scores of the even and the odd steps take the places
-                // of the two tiles', so that a step's scores are ready when the softmax of the
-                // step before ends
-                if (umma::elect_one()) {
-                    auto stage = [&](int k) { return (int)((total + k) % NS); };
-                    auto in = [&](int k) { return mbar_wait_short(kv_full(stage(k)), ((total + k) / NS) & 1); };
-                    auto scores = [&](int j) -> bool {
-                        if (!in(2 * j)) return false;
+            ChunkPiece pc;
+            for (int i = 0; next_piece(i, pc); ++i) {
+                const int n = pc.kt1 - pc.kt0;
+                if (n <= 0) continue;
+                const bool two = pc.queries > QPT, few = is_few(pc);
+                int st = (int)(total % NS);  // next stage and its phase
+                uint32_t phase = (total / NS) & 1;
+                auto landed = [&] { return mbar_wait_short(kv_full(st), phase); };
+                auto advance = [&] {
+                    if (++st == NS) {
+                        st = 0;
+                        phase ^= 1;
+                    }
+                };
+                if (!two) {
+                    // one tile of queries: the scores of the even and the odd steps take the places
+                    // of the two tiles', so that a step's scores are ready when the softmax of the
+                    // step before ends
+                    if (umma::elect_one()) {
+                        auto stage = [&](int k) { return (int)((total + k) % NS); };
+                        auto in = [&](int k) { return mbar_wait_short(kv_full(stage(k)), ((total + k) / NS) & 1); };
+                        auto scores = [&](int j) -> bool {
+                            if (!in(2 * j)) return false;
+                            umma::fence_after_sync();
+                            issue_s(2 + (j & 1), stage(2 * j));
+                            if (j == n - 1) umma::commit(q_empty(0));
+                            umma::commit(kv_empty(stage(2 * j)));
+                            return true;
+                        };
+                        ok = mbar_wait_short(q_full(0), used[0] & 1) && scores(0) && (n == 1 || scores(1));
+#pragma unroll 1
+                        for (int j = 0; j < n - 1 && ok; ++j) {
+                            ok = in(2 * j + 1) && issue_pv(2 + (j & 1), stage(2 * j + 1), j == 0, few);
+                            if (!ok) break;
+                            umma::commit(pv_step(j & 1));
+                            umma::commit(kv_empty(stage(2 * j + 1)));
+                            if (j + 2 < n) ok = scores(j + 2);
+                        }
+                    }
+                } else if (umma::elect_one()) {
+                    ok = landed();
+                    if (ok) ok = mbar_wait_short(q_full(0), used[0] & 1);
+                    if (ok) {
                         umma::fence_after_sync();
-                        issue_s(2 + (j & 1), stage(2 * j));
-                        if (j == n - 1) umma::commit(q_empty(0));
-                        umma::commit(kv_empty(stage(2 * j)));
-                        return true;
-                    };
-                    ok = mbar_wait_short(q_full(0), used[0] & 1) && scores(0) && (n == 1 || scores(1));
+                        issue_s(0, st);
+                        if (n == 1) umma::commit(q_empty(0));
+                        ok = mbar_wait_short(q_full(1), used[1] & 1);
+                        umma::fence_after_sync();
+                        if (ok) issue_s(1, st);
+                        if (n == 1) umma::commit(q_empty(1));
+                        umma::commit(kv_empty(st));
+                        advance();
+                    }
 #pragma unroll 1
                     for (int j = 0; j < n - 1 && ok; ++j) {
-                        ok = in(2 * j + 1) && issue_pv(2 + (j & 1), stage(2 * j + 1), j == 0, few);
+                        const int v_st = st;
+                        ok = landed();
                         if (!ok) break;
-                        umma::commit(pv_step(j & 1));
-                        umma::commit(kv_empty(stage(2 * j + 1)));
-                        if (j + 2 < n) ok = scores(j + 2);
+                        advance();
+                        ok = issue_pv(0, v_st, j == 0) && landed();
+                        if (!ok) break;
+                        umma::fence_after_sync();
+                        issue_s(0, st);
+                        if (j == n - 2) umma::commit(q_empty(0));
+                        ok = issue_pv(1, v_st, j == 0);
+                        if (!ok) break;
+                        umma::commit(kv_empty(v_st));
+                        issue_s(1, st);
+                        if (j == n - 2) umma::commit(q_empty(1));
+                        umma::commit(kv_empty(st));
+                        advance();
                     }
                 }
-            } else if (umma::elect_one()) {
-                ok = landed();
-                if (ok) ok = mbar_wait_short(q_full(0), used[0] & 1);
-                if (ok) {
-                    umma::fence_after_sync();
-                    issue_s(0, st);
-                    if (n == 1) umma::commit(q_empty(0));
-                    ok = mbar_wait_short(q_full(1), used[1] & 1);
-                    umma::fence_after_sync();
-                    if (ok) issue_s(1, st);
-                    if (n == 1) umma::commit(q_empty(1));
-                    umma::commit(kv_empty(st));
-                    advance();
-                }
-#pragma unroll 1
-                for (int j = 0; j < n - 1 && ok; ++j) {
-                    const int v_st = st;
-                    ok = landed();
-                    if (!ok) break;
-                    advance();
-                    ok = issue_pv(0, v_st, j == 0) && landed();
-                    if (!ok) break;
-                    umma::fence_after_sync();
-                    issue_s(0, st);
-                    if (j == n - 2) umma::commit(q_empty(0));
-                    ok = issue_pv(1, v_st, j == 0);
-                    if (!ok) break;
-                    umma::commit(kv_empty(v_st));
-                    issue_s(1, st);
-                    if (j == n - 2) umma::commit(q_empty(1));
-                    umma::commit(kv_empty(st));
-                    advance();
-                }
-            }
-            ++used[0];
-            used[1] += two;
-            ok = __all_sync(FULL_MASK, ok);
-            if (!ok) break;
-            total += 2 * n;
-            st = (int)((total - 1) % NS);  // every lane: the piece's last stage, V's
-            phase = ((total - 1) / NS) & 1;
-            if (chunk_has_tail(pc)) {
-                ok = __all_sync(FULL_MASK, landed());
+                ++used[0];
+                used[1] += two;
+                ok = __all_sync(FULL_MASK, ok);
                 if (!ok) break;
-                const int r0 = pc.lim0 + pc.queries - 1 - (pc.kt1 - 1) * CHUNK_TILE;
-                const int rows = CHUNK_TOKENS - r0 % CHUNK_TOKENS;
-                unsigned char* tile = smem + L::KV_OFF + st * L::TILE + r0 / CHUNK_TOKENS * (CHUNK_TOKENS * D * 2);
-                for (int v = lane; v < rows * L::BOXES * 8; v += 32) {
-                    const int r = r0 % CHUNK_TOKENS + v / (L::BOXES * 8), c = v % (L::BOXES * 8);
-                    *reinterpret_cast<uint4*>(tile + (c / 8) * (CHUNK_TOKENS * 128) + r * 128 + (c % 8) * 16) =
-                        make_uint4(0u, 0u, 0u, 0u);
+                total += 2 * n;
+                st = (int)((total - 1) % NS);  // every lane: the piece's last stage, V's
+                phase = ((total - 1) / NS) & 1;
+                if (chunk_has_tail(pc)) {
+                    ok = __all_sync(FULL_MASK, landed());
+                    if (!ok) break;
+                    const int r0 = pc.lim0 + pc.queries - 1 - (pc.kt1 - 1) * CHUNK_TILE;
+                    const int rows = CHUNK_TOKENS - r0 % CHUNK_TOKENS;
+                    unsigned char* tile =
+                        smem + L::KV_OFF + st * L::TILE + r0 / CHUNK_TOKENS * (CHUNK_TOKENS * D * 2);
+                    for (int v = lane; v < rows * L::BOXES * 8; v += 32) {
+                        const int r = r0 % CHUNK_TOKENS + v / (L::BOXES * 8), c = v % (L::BOXES * 8);
+                        *reinterpret_cast<uint4*>(tile + (c / 8) * (CHUNK_TOKENS * 128) + r * 128 + (c % 8) * 16) =
+                            make_uint4(0u, 0u, 0u, 0u);
+                    }
+                    umma::fence_smem_to_async();
+                    __syncwarp();
                 }
-                umma::fence_smem_to_async();
-                __syncwarp();
-            }
-            if (!two) {
-                if (umma::elect_one()) {
-                    ok = landed() && issue_pv(2 + ((n - 1) & 1), st, n == 1, few);
-                    if (ok) umma::commit(pv_step((n - 1) & 1));
+                if (!two) {
+                    if (umma::elect_one()) {
+                        ok = landed() && issue_pv(2 + ((n - 1) & 1), st, n == 1, few);
+                        if (ok) umma::commit(pv_step((n - 1) & 1));
+                        if (ok) umma::commit(kv_empty(st));
+                    }
+                } else if (umma::elect_one()) {
+                    ok = landed() && issue_pv(0, st, n == 1);
+                    if (ok) umma::commit(pv_done(0));
+                    if (ok) {
+                        ok = issue_pv(1, st, n == 1);
+                        if (ok) umma::commit(pv_done(1));
+                    }
                     if (ok) umma::commit(kv_empty(st));
                 }
-            } else if (umma::elect_one()) {
-                ok = landed() && issue_pv(0, st, n == 1);
-                if (ok) umma::commit(pv_done(0));
-                if (ok) {
-                    ok = issue_pv(1, st, n == 1);
-                    if (ok) umma::commit(pv_done(1));
-                }
-                if (ok) umma::commit(kv_empty(st));
+                ok = __all_sync(FULL_MASK, ok);
+                if (!ok) break;
             }
-            ok = __all_sync(FULL_MASK, ok);
-            if (!ok) break;
+            if (umma::elect_one()) {
+                umma::commit(all_done);
+                if (!mbar_wait_short(all_done, 0)) ok = false;
+            }
+            __syncwarp();
         }
-        if (umma::elect_one()) {
-            umma::commit(all_done);
-            if (!mbar_wait_short(all_done, 0)) ok = false;
-        }
-        __syncwarp();
-    } else if (warp == IDLE_WARP) {
-        regs_dec<CHUNK_REGS_OTHERS>();
     } else if (warp >= OUT_WARP) {
         regs_dec<CHUNK_REGS_OUTPUT>();
         // ---- output of both tiles, while the softmax warps are at the next piece: warp w of
