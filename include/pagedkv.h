@@ -520,7 +520,9 @@ pkv_status pkv_qk_norm_rope_write(const pkv_pool* pool, const void* q, int64_t q
  *   workspace     pkv_chunk_workspace_bytes(...) bytes, always required; its contents need
  *                 no clearing.  Calls that may run at the same time need one each.
  * Cached rows at and past a request's context may hold anything; those below it must be
- * finite.  Any group size num_q_heads / num_kv_heads up to 128.  The probabilities enter
+ * finite.  A query row that sees tokens and holds a NaN or an infinity, or whose scores pass
+ * fp32's range, is NaN; the other rows do not notice.  Any group size num_q_heads /
+ * num_kv_heads up to 128.  The probabilities enter
  * the product with V rounded to the pool's type when the output has that type, and with
  * about twice its precision when the output is fp32.  fp16 / bf16 pools of fewer than 2^31
  * (block, kv head, position) rows, and tables or max_context_len of at most 2^26 tokens (else

@@ -4,7 +4,7 @@
 //
 // For query j of request s (n_s queries, context c_s counting them), head h:
 //   out = softmax(scale q . K_s[0..lim)^T) V_s[0..lim),   lim = c_s - n_s + 1 + j,
-// zero when lim <= 0.  The G heads of a kv head share its K and V, so the rows of one kv
+// zero when lim <= 0; a NaN or infinite score makes its row NaN.  The G heads of a kv head share its K and V, so the rows of one kv
 // head are (query, head) pairs and a CTA takes two tiles of 128 of them (row r of a tile is
 // query r / G, head r % G) against the pages in steps of 128 tokens: every staged K and V
 // tile serves 256 rows.  One pass, running maximum and sum per row.
@@ -755,7 +755,8 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
                             f[y] = fast_exp2(stats[y * 32 + x] - ref);
                             sum = fmaf(f[y], stats[128 + y * 32 + x], sum);
                         }
-                        const float inv = !direct ? 1.f : sum > 0.f ? 1.f / sum : 0.f;
+                        // zero for a row that sees nothing; a NaN or a sum of no weight is the result
+                        const float inv = !direct ? 1.f : pc.lim0 + x / G > 0 ? 1.f / sum : 0.f;
                         const long long out_row =
                             ((long long)pc.token + x / G) * p.num_q_heads + pc.kv_head * G + x % G;
                         const long long part_row = (long long)pc.part_row + x;
@@ -796,15 +797,17 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
                 if (__any_sync(FULL_MASK, valid)) {
                     const long long out_row = ((long long)pc.token + jq) * p.num_q_heads + pc.kv_head * G + hg;
                     const long long part_row = (long long)pc.part_row + (t * QPT * G + r);
-                    const float by = !direct ? 1.f : l > 0.f ? 1.f / l : 0.f;
+                    // a row that sees nothing is zero, whatever O holds; a NaN in its sum, or no weight
+                    // in it although it sees tokens (scores of -inf), is the result
+                    const bool nothing = direct ? pc.lim0 + jq <= 0 : l == 0.f;
+                    const float by = direct ? 1.f / l : 1.f;
                     // once per piece: a loop that stays in the instruction cache
 #pragma unroll 1
                     for (int c = 0; c < D; c += 16) {
                         float o[16];
                         if (n > 0) umma::ld16(o_t + c, o);
-                        // a row that sees nothing is zero, whatever O holds
 #pragma unroll
-                        for (int k = 0; k < 16; ++k) o[k] = l > 0.f ? o[k] * by : 0.f;
+                        for (int k = 0; k < 16; ++k) o[k] = nothing ? 0.f : o[k] * by;
                         if (!valid) {
                         } else if (direct && !SPLIT_P) {
                             uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(p.out) + out_row * D + c);

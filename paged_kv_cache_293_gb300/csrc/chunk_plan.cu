@@ -347,7 +347,8 @@ __global__ void __launch_bounds__(N) chunk_plan_kernel(const ChunkPlanParams p) 
                     m.rows = rows;
                     m.parts = parts;
                     m.part_row = part_row;
-                    m.pad0 = m.pad1 = m.pad2 = 0;
+                    m.lim0 = x.w;
+                    m.pad0 = m.pad1 = 0;
                     p.merges[at.z + h] = m;
                 }
             }
@@ -399,11 +400,11 @@ __global__ void __launch_bounds__(256) chunk_merge_kernel(const ChunkParams p) {
                 mk = p.part_m[row0 + (long long)lane * m.rows];
                 lk = p.part_l[row0 + (long long)lane * m.rows];
             }
-            if (!(lk > 0.f)) mk = -INFINITY;
+            if (lk == 0.f) mk = -INFINITY;  // (a NaN goes on)
             float M = mk;
 #pragma unroll
             for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(FULL_MASK, M, o));
-            const float w = lk > 0.f ? fast_exp2(mk - M) : 0.f;
+            const float w = lk == 0.f ? 0.f : fast_exp2(mk - M);
             float l = w * lk;
 #pragma unroll
             for (int o = 16; o >= 1; o >>= 1) l += __shfl_xor_sync(FULL_MASK, l, o);
@@ -430,7 +431,8 @@ __global__ void __launch_bounds__(256) chunk_merge_kernel(const ChunkParams p) {
             const size_t out =
                 (((size_t)m.token + r / p.group) * p.num_q_heads + m.kv_head * p.group + r % p.group) * D + lane * V;
 #pragma unroll
-            for (int i = 0; i < V; ++i) store_out(p.out, p.out_dtype, out + i, l > 0.f ? acc[i] / l : 0.f);
+            for (int i = 0; i < V; ++i)
+                store_out(p.out, p.out_dtype, out + i, m.lim0 + r / p.group > 0 ? acc[i] / l : 0.f);
         }
     }
 }

@@ -151,10 +151,10 @@ struct __align__(16) ChunkPiece {
 };
 
 // A cut item: `rows` (query, head) rows whose `parts` pieces left partial results, piece k's
-// at part_row + k * rows.
+// at part_row + k * rows; lim0 as in ChunkPiece.
 struct __align__(16) ChunkMerge {
     int32_t token, kv_head, rows, parts;
-    int32_t part_row, pad0, pad1, pad2;
+    int32_t part_row, lim0, pad0, pad1;
 };
 
 // Whether the piece's last copy holds positions no query of it sees.
