@@ -487,8 +487,9 @@ pkv_status pkv_build_batch(const pkv_block_allocator* alloc, int32_t block_size,
  *   interleaved   0: element i pairs with i + rotary_dim / 2; otherwise 2 i with 2 i + 1
  *   positions     int32 [T]; negative: the row holds no token and nothing is written
  *   slot_mapping  int64 [T]; negative: k and v of that token are not written
- *   q_out         [T][num_q_heads][D]; may be q itself when q_stride = num_q_heads * D,
- *                 but must not overlap the inputs in another way
+ *   q_out         [T][num_q_heads][D]; may be q itself when q_stride = num_q_heads * D
+ *                 (or T = 1); shares no memory with the inputs or pools in another way
+ *                 (PKV_ERR_INVALID)
  * All pointers but positions and slot_mapping 16-byte aligned.  Slots within one call
  * must be distinct.  A position at or past max_position skips its token and sets
  * PKV_DEVERR_POSITION; a slot past the pool skips its k and v and sets PKV_DEVERR_SLOT.

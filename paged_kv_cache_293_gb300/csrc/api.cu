@@ -865,6 +865,21 @@ pkv_status pkv_build_batch(const pkv_block_allocator* alloc, int32_t block_size,
                : PKV_ERR_CUDA;
 }
 
+namespace {
+
+// Whether any of n rows of `width` bytes, `stride` >= width apart from a on, shares a byte with
+// the `bytes` from b on.
+bool rows_overlap(const void* a, int64_t stride, int64_t width, int64_t n, const void* b, int64_t bytes) {
+    if (!a || !b || n <= 0 || width <= 0 || bytes <= 0) return false;
+    if (n == 1) stride = width;
+    // the first row that ends past b
+    const int64_t to_b = static_cast<const char*>(b) - static_cast<const char*>(a);
+    const int64_t t = to_b < width ? 0 : (to_b - width) / stride + 1;
+    return t < n && t * stride < to_b + bytes;
+}
+
+}  // namespace
+
 pkv_status pkv_qk_norm_rope_write(const pkv_pool* pool, const void* q, int64_t q_stride,
                                   const void* k, int64_t k_stride, const void* v, int64_t v_stride,
                                   int32_t num_tokens, int32_t num_q_heads, const void* q_weight,
@@ -891,6 +906,18 @@ pkv_status pkv_qk_norm_rope_write(const pkv_pool* pool, const void* q, int64_t q
     const int64_t need_q = num_q_heads * D, need_kv = pool->num_kv_heads * D;
     if (q_stride % vec != 0 || k_stride % vec != 0 || v_stride % vec != 0) return PKV_ERR_INVALID;
     if (num_tokens > 1 && (q_stride < need_q || k_stride < need_kv || v_stride < need_kv))
+        return PKV_ERR_INVALID;
+    // q_out may be q, row for row; otherwise tokens are read after others have been written
+    const int64_t size = pool->dtype == PKV_F32 ? 4 : 2, T = num_tokens, out_bytes = T * need_q * size;
+    const int64_t pool_bytes = (int64_t)pool->num_blocks * pool->block_size * need_kv * size;
+    auto apart = [&](const void* in, int64_t bytes) { return !rows_overlap(in, bytes, bytes, 1, q_out, out_bytes); };
+    const bool in_place = q_out == q && (T == 1 || q_stride == need_q);
+    if ((!in_place && rows_overlap(q, q_stride * size, need_q * size, T, q_out, out_bytes)) ||
+        rows_overlap(k, k_stride * size, need_kv * size, T, q_out, out_bytes) ||
+        rows_overlap(v, v_stride * size, need_kv * size, T, q_out, out_bytes) ||
+        !apart(pool->k, pool_bytes) || !apart(pool->v, pool_bytes) || !apart(q_weight, D * size) ||
+        !apart(k_weight, D * size) || !apart(cos_sin, (int64_t)max_position * rotary_dim * 4) ||
+        !apart(positions, T * 4) || !apart(slot_mapping, T * 8))
         return PKV_ERR_INVALID;
     pkv::RopeParams p{};
     st = error_word(&p.err);

@@ -57,3 +57,28 @@ def test_queries_that_are_not_finite(P, form, f32_out, value):
     assert torch.isnan(got[hit & sees[:, None]]).all()
     assert (got[:-1][~sees[:-1]] == 0).all()
     assert P.pkv_get_device_error() == 0
+
+
+# ---------------------------------------------------------------- where the write's output may lie
+
+@pytest.mark.parametrize("place", ["before", "behind", "in a gap", "one token in place"])
+def test_write_output_next_to_its_inputs(P, place):
+    """Outputs that touch the packed rows, lie between two rows or are one token's own row: allowed."""
+    Hq, Hkv, D, B, T = 4, 2, 64, 16, 1 if place == "one token in place" else 3
+    row, n = (Hq + 2 * Hkv) * D, T * Hq * D
+    stride = row + n if place == "in a gap" else row
+    g = torch.Generator().manual_seed(3)
+    buf = torch.randn(2 * n + T * stride, generator=g).to(torch.bfloat16).to(DEV)
+    x = buf[n:n + T * stride].view(T, stride)
+    q, k, v = (x[:, a * D:b * D].view(T, b - a, D) for a, b in ((0, Hq), (Hq, Hq + Hkv), (Hq + Hkv, Hq + 2 * Hkv)))
+    at = {"before": 0, "behind": n + T * stride, "in a gap": n + row, "one token in place": n}[place]
+    cs = torch.rand(8, D, generator=g).to(DEV)
+    pos = torch.arange(T, dtype=torch.int32, device=DEV)
+    slots = torch.arange(T, device=DEV)
+    pools = [torch.zeros(1, Hkv, B, D, dtype=torch.bfloat16, device=DEV) for _ in range(4)]
+    want = torch.empty(T, Hq, D, dtype=torch.bfloat16, device=DEV)
+    P.pkv_qk_norm_rope_write(q, k, v, *pools[:2], pos, slots, want, cos_sin=cs)
+    out = buf[at:at + n].view(T, Hq, D)
+    P.pkv_qk_norm_rope_write(q, k, v, *pools[2:], pos, slots, out, cos_sin=cs)
+    assert torch.equal(out, want) and torch.equal(pools[0], pools[2]) and torch.equal(pools[1], pools[3])
+    assert P.pkv_get_device_error() == 0
