@@ -524,8 +524,10 @@ pkv_status pkv_qk_norm_rope_write(const pkv_pool* pool, const void* q, int64_t q
  * finite.  A query row that sees tokens and holds a NaN or an infinity, or whose scores pass
  * fp32's range, is NaN; the other rows do not notice.  Any group size num_q_heads /
  * num_kv_heads up to 128.  The probabilities enter
- * the product with V rounded to the pool's type when the output has that type, and with
- * about twice its precision when the output is fp32.  fp16 / bf16 pools of fewer than 2^31
+ * the product with V rounded to the pool's type when the output has that type (off by at
+ * most 2^-8 of their value in bf16, 2^-11 in fp16), and with about twice its precision when
+ * the output is fp32; in fp16, by at most 2^-32 of the row's largest where that is more.
+ * fp16 / bf16 pools of fewer than 2^31
  * (block, kv head, position) rows, and tables or max_context_len of at most 2^26 tokens (else
  * PKV_ERR_UNSUPPORTED).  Device errors: query_start
  * not ascending within [0, num_tokens] (PKV_DEVERR_POSITION, nothing is computed); a

@@ -30,12 +30,14 @@
 //                  a step's scores are ready when the softmax of the step before ends;
 //   up to 16       (decoding requests) each of warps 0-3 has all rows and a quarter of the
 //                  tokens of every step, and the four results are joined at the end.
-// The reference maximum of a row is raised only when a step's maximum exceeds it by more
-// than 8 in base 2, so O is rescaled rarely; every term of a row uses the same reference.
-// P enters its product rounded to the pool's type (at most half a step, 2^-8 of the value in
-// bf16 and 2^-11 in fp16, like the output's own rounding); with a 32-bit output it enters as a
-// rounded part and the rounded remainder, in two products.  Scores, maxima, sums and O are
-// held in 32 bits.
+// The reference of a row follows its maximum, and is raised only when a step's maximum exceeds
+// the one it was set by by more than 8 in base 2, so O is rescaled rarely; every term of a row uses
+// the same reference.  P enters its product rounded to the pool's type (at most half a step,
+// 2^-8 of the value in bf16 and 2^-11 in fp16, like the output's own rounding); with a 32-bit
+// output it enters as a rounded part and the rounded remainder, in two products.  fp16 has full
+// steps from 2^-14 on and half a step of 2^-25 below, so there the reference lies 7 below the
+// maximum: weights go up to 2^15, those from 2^-21 of the largest on keep their 11 bits, and no
+// weight is off by more than 2^-32 of the largest.  Scores, maxima, sums and O are held in 32 bits.
 //
 // What bounds it, measured.  Two full tiles: a step has 2048 cycles of MMAs and takes about
 // 2600, the way of one tile once round: its softmax (1480 cycles: scores from tensor memory 310,
@@ -68,7 +70,20 @@ constexpr int CHUNK_THREADS = 512;
 // Registers per thread: 128 at launch; the softmax warps take what the others give back
 // (256 * 184 + 128 * 72 + 128 * 72 = 512 * 128).
 constexpr int CHUNK_REGS_SOFTMAX = 184, CHUNK_REGS_OTHERS = 72, CHUNK_REGS_OUTPUT = 72;
-constexpr float CHUNK_RESCALE_LOG2 = 8.f;
+// The maximum of a row, in base 2, that a step's weights are judged by, how far below it the
+// reference is set, and how far it may exceed the reference.  The largest weight of fp16 has to stay
+// below 2^16: its maximum is rounded up, so that the one product and sum of a weight's exponent,
+// which leaves out the maximum's rounding, cannot exceed what was judged.
+template <typename T>
+struct ChunkReference {
+    static constexpr float BELOW = 0.f, RAISE = 8.f;
+    __device__ __forceinline__ static float scaled(float x, float scale_log2) { return x * scale_log2; }
+};
+template <>
+struct ChunkReference<__half> {
+    static constexpr float BELOW = 7.f, RAISE = 15.f;
+    __device__ __forceinline__ static float scaled(float x, float scale_log2) { return __fmul_ru(x, scale_log2); }
+};
 // Rows up to which a piece's steps are spread over four warps: 200 requests with 1-5 queries, 32 / 8
 // heads, contexts about 300: 70 us (85 with 4 rows).
 constexpr int CHUNK_FEW_ROWS = 16;
@@ -173,13 +188,14 @@ __device__ __forceinline__ bool softmax_step(uint32_t s_t, uint32_t o_t, int see
             if (h == 0) top[c] = fmaxf(top[c], __uint_as_float(raw[HALF - 8 + c]));
         }
     }
-    const float cm = max3(max3(top[0], top[1], top[2]), max3(top[3], top[4], top[5]), fmaxf(top[6], top[7])) *
-                     scale_log2;
-    const bool need = cm > m_ref + CHUNK_RESCALE_LOG2;
+    using Ref = ChunkReference<T>;
+    const float cm = Ref::scaled(
+        max3(max3(top[0], top[1], top[2]), max3(top[3], top[4], top[5]), fmaxf(top[6], top[7])), scale_log2);
+    const bool need = cm - m_ref > Ref::RAISE;
     float alpha = 1.f;
     if (need) {
-        alpha = fast_exp2(m_ref - cm);
-        m_ref = cm;
+        alpha = fast_exp2(m_ref - (cm - Ref::BELOW));
+        m_ref = cm - Ref::BELOW;
     }
     const float neg = m_ref == -INFINITY ? 0.f : -m_ref;
     const uint64_t scale2 = pack2(scale_log2, scale_log2), neg2 = pack2(neg, neg);
@@ -252,13 +268,14 @@ __device__ __forceinline__ bool few_rows_step(uint32_t s_t, uint32_t p_t, uint32
         for (int k = c + 4; k < 28; k += 8)
             top[c] = max3(top[c], __uint_as_float(raw[k]), __uint_as_float(raw[k + 4 < 28 ? k + 4 : k]));
     }
-    const float cm = max3(top[0], top[1], fmaxf(top[2], top[3])) * scale_log2;
-    const bool need = cm > m_ref + CHUNK_RESCALE_LOG2;
+    using Ref = ChunkReference<T>;
+    const float cm = Ref::scaled(max3(top[0], top[1], fmaxf(top[2], top[3])), scale_log2);
+    const bool need = cm - m_ref > Ref::RAISE;
     if (__any_sync(FULL_MASK, need)) {
         float alpha = 1.f;
         if (need) {
-            alpha = fast_exp2(m_ref - cm);
-            m_ref = cm;
+            alpha = fast_exp2(m_ref - (cm - Ref::BELOW));
+            m_ref = cm - Ref::BELOW;
         }
         l *= alpha;
         if (has_o) {  // rows whose reference rose: scale their O, complete through the step before

@@ -59,6 +59,82 @@ def test_queries_that_are_not_finite(P, form, f32_out, value):
     assert P.pkv_get_device_error() == 0
 
 
+# ---------------------------------------------------------------- weights far below the largest
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("f32_out", [False, True])
+@pytest.mark.parametrize("new,cut", [(1, False), (17, False), (140, False), (1, True)])
+@pytest.mark.parametrize("bits", [13.4, 17.6, 21.3, 25.1, 27.8])
+def test_small_weights_beside_a_large_one(P, dtype, f32_out, new, cut, bits):
+    """One key whose value is zero and whose score lies `bits` (in base 2) above all others, which
+    share the value 30: out = 30 (n - 1) w / (1 + (n - 1) w) with w = 2^-bits.
+
+    What may be lost: a weight is held relative to 2^7 times the row's largest (fp16), so it is off
+    by half a step of 2^-24, 2^-25 2^-7 of the largest, besides 2^-11 of itself (2^-8 in bf16; u^2
+    with a 32-bit output, where its remainder is held too).  Scores: one product and one rounding
+    of the scaled score, base 2, at most 4 * 2^-24 * bits, and the exponential's 2^-20.  Sums of n
+    terms, 2^-23 each, for numerator and sum.  Half a step of the output (fp16: at least 2^-25)."""
+    D, B, n = 64, 16, 4000 if cut else 880
+    dt = R.DTYPE[dtype]
+    N = R.blocks(n, B)
+    k, v = torch.zeros(N, 1, B, D), torch.full((N, 1, B, D), 30.0)
+    k[..., 0] = -1.0
+    k[0, 0, 0, 0], v[0, 0, 0] = 0.0, 0.0
+    q = torch.zeros(new, 1, D)
+    q[..., 0] = 1.0
+    k, v, q = (x.to(dt).to(DEV) for x in (k, v, q))
+    out = torch.zeros(new, 1, D, dtype=torch.float32 if f32_out else dt, device=DEV)
+    i32 = lambda *a: torch.tensor(a, dtype=torch.int32, device=DEV)  # noqa: E731
+    scale = torch.tensor(bits * 0.6931471805599453).float().item()
+    ws = P.workspace_tensor(P.pkv_chunk_workspace_bytes(k, new, 1, 1, n), DEV)
+    P.pkv_paged_attention_chunk(q, k, v, i32(0, new), torch.arange(N, dtype=torch.int32, device=DEV)[None],
+                                i32(n), scale, out, n, ws)
+    others = (n - new + torch.arange(new, dtype=torch.float64))[:, None, None]
+    w = torch.exp(torch.tensor(-scale, dtype=torch.float64))
+    ref = 30 * others * w / (1 + others * w)
+    u = torch.finfo(dt).eps / 2
+    tol = ref * ((u * u if f32_out else u) + 4 * 2.0 ** -24 * bits + 2.0 ** -20 + 2 * n * 2.0 ** -23)
+    if dtype == "f16":
+        tol = tol + 30 * others * 2.0 ** -32
+        if not f32_out:
+            tol = tol + 2.0 ** -25
+    tol = tol + torch.finfo(out.dtype).eps / 2 * (ref + tol)
+    err = (out.cpu().double() - ref).abs()
+    assert (err <= tol).all(), (float(err.max()), float(tol.min()))
+    assert P.pkv_get_device_error() == 0
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("new,rising", [(1, True), (1, False), (17, True), (140, True), (140, False)])
+def test_scores_of_many_millions(P, dtype, new, rising):
+    """Scores up to 2^26 (base 2), 4e4 apart, where 32 bits hold them to 8: each row's largest has all the
+    weight, rising along the context or falling, and the output is its value (half a step, and
+    half a step of the weight)."""
+    D, B, n = 64, 16, 600
+    dt = R.DTYPE[dtype]
+    N = R.blocks(n, B)
+    g = torch.Generator().manual_seed(5)
+    k, v = torch.zeros(N, 1, B, D), torch.randn(N, 1, B, D, generator=g).to(dt)
+    a = 16384 + 64.0 * torch.arange(n)             # (bf16 holds every fourth or so: ties share)
+    a = a if rising else a.flip(0)
+    k[..., 0] = torch.cat([a, a.new_zeros(N * B - n)]).view(N, 1, B)
+    k, q = k.to(dt), torch.zeros(new, 1, D)
+    q[..., 0] = 49152.0
+    q = q.to(dt)
+    out = torch.zeros(new, 1, D, dtype=dt, device=DEV)
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device=DEV)  # noqa: E731
+    ws = P.workspace_tensor(P.pkv_chunk_workspace_bytes(k, new, 1, 1, n), DEV)
+    P.pkv_paged_attention_chunk(q.to(DEV), k.to(DEV), v.to(DEV), i32(0, new),
+                                torch.arange(N, dtype=torch.int32, device=DEV)[None], i32(n), 2.0 ** -6, out, n, ws)
+    held, flat = k.reshape(-1, D)[:, 0].double(), v.reshape(-1, D).double()
+    for t in range(new):
+        seen = held[:n - new + 1 + t]
+        ref = flat[:len(seen)][seen == seen.max()]
+        tol = torch.finfo(dt).eps * ref.abs().mean(0) + 2.0 ** -24
+        assert ((out[t, 0].cpu().double() - ref.mean(0)).abs() <= tol).all(), t
+    assert P.pkv_get_device_error() == 0
+
+
 # ---------------------------------------------------------------- where the write's output may lie
 
 @pytest.mark.parametrize("place", ["before", "behind", "in a gap", "one token in place"])
