@@ -527,6 +527,8 @@ pkv_status pkv_qk_norm_rope_write(const pkv_pool* pool, const void* q, int64_t q
  * the product with V rounded to the pool's type when the output has that type (off by at
  * most 2^-8 of their value in bf16, 2^-11 in fp16), and with about twice its precision when
  * the output is fp32; in fp16, by at most 2^-32 of the row's largest where that is more.
+ * Products are summed on the tensor cores over at most 2^15 tokens of a row, which may lose 2^-12
+ * of the sum (2^-11 for an fp32 output), and in fp32 beyond.
  * fp16 / bf16 pools of fewer than 2^31
  * (block, kv head, position) rows, and tables or max_context_len of at most 2^26 tokens (else
  * PKV_ERR_UNSUPPORTED).  Device errors: query_start

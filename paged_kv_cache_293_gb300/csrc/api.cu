@@ -956,7 +956,7 @@ namespace {
 // Sizes of a chunk attention call and where its workspace's parts lie.
 struct ChunkShape {
     int64_t tiles, pieces, cut_pieces, partial_rows;
-    size_t tile_start, tile, piece, merge, m, l, o, bytes;
+    size_t tile_start, tile, piece, merge, m, l, o, totals, bytes;
 };
 
 ChunkShape chunk_shape(const pkv_pool* pool, int32_t T, int32_t S, int32_t Hq, int32_t max_ctx) {
@@ -964,7 +964,8 @@ ChunkShape chunk_shape(const pkv_pool* pool, int32_t T, int32_t S, int32_t Hq, i
     const int64_t QT = 2 * (128 / G);  // queries per tile
     ChunkShape c{};
     c.tiles = std::min<int64_t>(T, T / QT + S);
-    const bool cuts = (max_ctx + (int64_t)pkv::CHUNK_TILE - 1) / pkv::CHUNK_TILE >= pkv::CHUNK_SPLIT_MIN;
+    const int64_t steps = (max_ctx + (int64_t)pkv::CHUNK_TILE - 1) / pkv::CHUNK_TILE;
+    const bool cuts = steps >= pkv::CHUNK_SPLIT_MIN;
     c.cut_pieces = cuts ? std::min<int64_t>(8 * sms, c.tiles * Hkv * 32) : 0;
     c.partial_rows = cuts ? std::min<int64_t>(3 * sms * 256, (int64_t)T * Hq * 32) : 0;
     c.pieces = c.tiles * Hkv + c.cut_pieces;
@@ -981,6 +982,9 @@ ChunkShape chunk_shape(const pkv_pool* pool, int32_t T, int32_t S, int32_t Hq, i
     c.m = take((size_t)c.partial_rows * 4);
     c.l = take((size_t)c.partial_rows * 4);
     c.o = take((size_t)c.partial_rows * pool->head_dim * 4);
+    // two tiles of 128 rows per CTA
+    const int64_t totals = std::min(c.pieces, sms) * 256 * (pool->head_dim + 4);
+    c.totals = take(steps > pkv::CHUNK_SUM_STEPS ? (size_t)totals * 4 : 0);
     c.bytes = at;
     return c;
 }
@@ -1073,6 +1077,7 @@ pkv_status pkv_paged_attention_chunk(const pkv_pool* pool, const void* q, int32_
     p.part_m = reinterpret_cast<float*>(ws + c.m);
     p.part_l = reinterpret_cast<float*>(ws + c.l);
     p.part_o = reinterpret_cast<float*>(ws + c.o);
+    p.totals = reinterpret_cast<float*>(ws + c.totals);
     p.err = err;
     const cudaError_t e = pool->dtype == PKV_F16 ? pkv::launch_chunk<__half>(pl, p, x, s)
                                                  : pkv::launch_chunk<__nv_bfloat16>(pl, p, x, s);

@@ -4,10 +4,10 @@
 //
 // For query j of request s (n_s queries, context c_s counting them), head h:
 //   out = softmax(scale q . K_s[0..lim)^T) V_s[0..lim),   lim = c_s - n_s + 1 + j,
-// zero when lim <= 0; a NaN or infinite score makes its row NaN.  The G heads of a kv head share its K and V, so the rows of one kv
-// head are (query, head) pairs and a CTA takes two tiles of 128 of them (row r of a tile is
-// query r / G, head r % G) against the pages in steps of 128 tokens: every staged K and V
-// tile serves 256 rows.  One pass, running maximum and sum per row.
+// zero when lim <= 0; a NaN or infinite score makes its row NaN.  The G heads of a kv head share
+// its K and V, so the rows of one kv head are (query, head) pairs and a CTA takes two tiles of 128
+// of them (row r of a tile is query r / G, head r % G) against the pages in steps of 128 tokens:
+// every staged K and V tile serves 256 rows.  One pass, running maximum and sum per row.
 //
 // A small kernel first lists the pieces of work (chunk_plan.cu): tile pair x kv head, cut
 // along the context where there would be too few of them; the CTAs of this kernel, one per
@@ -38,6 +38,12 @@
 // steps from 2^-14 on and half a step of 2^-25 below, so there the reference lies 7 below the
 // maximum: weights go up to 2^15, those from 2^-21 of the largest on keep their 11 bits, and no
 // weight is off by more than 2^-32 of the largest.  Scores, maxima, sums and O are held in 32 bits.
+// The tensor cores cut a sum's low bits off, always towards zero, so a row's O in tensor memory
+// falls behind its sum by up to 2^-23 a product of 16 tokens (weights alike over 2^20 tokens: by
+// 1 %).  So after every CHUNK_SUM_STEPS steps of a piece O and the sum are added to 32-bit totals in
+// the workspace and begin at zero again: off by 8 * 256 * 2^-23 = 2^-12 at most, whatever the
+// length (2^-11 with a 32-bit output, whose weights take two products; measured, weights and values
+// alike over 2^20 tokens: 2^-14).  A row's sum is one of sums of steps.
 //
 // What bounds it, measured.  Two full tiles: a step has 2048 cycles of MMAs and takes about
 // 2600, the way of one tile once round: its softmax (1480 cycles: scores from tensor memory 310,
@@ -150,13 +156,49 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return v;
 }
 
+// Adds the row's total, kept at `kept` (its 16-byte columns 128 apart) and scaled by f, to its O at
+// o_t.  TO_TOTAL: the sum becomes the total (the `first` one is O alone), and O zero.  Out of line:
+// inlined, it cost steps that never come here (8192-token prompt 365 us, 360 so).
+template <int D, bool TO_TOTAL>
+__device__ __noinline__ void add_total(uint32_t o_t, float4* kept, float f, bool first) {
+    const uint32_t zeros[16] = {0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll 1
+    for (int d = 0; d < D; d += 16) {
+        float4 v[4];
+        float o[16];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] = first ? make_float4(0.f, 0.f, 0.f, 0.f) : kept[(d / 4 + k) * 128];
+        umma::ld16(o_t + d, o);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            o[4 * k] = fmaf(v[k].x, f, o[4 * k]);
+            o[4 * k + 1] = fmaf(v[k].y, f, o[4 * k + 1]);
+            o[4 * k + 2] = fmaf(v[k].z, f, o[4 * k + 2]);
+            o[4 * k + 3] = fmaf(v[k].w, f, o[4 * k + 3]);
+        }
+        if (TO_TOTAL) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                kept[(d / 4 + k) * 128] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+            umma::st16(o_t + d, zeros);
+        } else {
+            uint32_t w[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) w[k] = __float_as_uint(o[k]);
+            umma::st16(o_t + d, w);
+        }
+    }
+    umma::wait_st();
+    umma::fence_before_sync();
+}
+
 // One step of a row: its 128 scores from tensor memory at s_t, the running reference m_ref and
-// the sum (in four parts), its O at o_t scaled where the reference rose (once phase_o of
+// the sum (in two parts), its O at o_t scaled where the reference rose (once phase_o of
 // bar_o says that the products before are done; 0: known), and its weights written over the
 // scores, the halves handed on at bar_lo and bar_hi.
 template <typename T, int D, bool SPLIT_P, bool EDGE>
 __device__ __forceinline__ bool softmax_step(uint32_t s_t, uint32_t o_t, int seen, bool has_o,
-                                             float scale_log2, float& m_ref, uint64_t (&sum2)[2],
+                                             float scale_log2, float& m_ref, uint64_t& sum2,
                                              uint32_t bar_lo, uint32_t bar_hi, uint32_t bar_o,
                                              uint32_t phase_o) {
     constexpr int N = CHUNK_TILE, HALF = N / 2;
@@ -199,8 +241,8 @@ __device__ __forceinline__ bool softmax_step(uint32_t s_t, uint32_t o_t, int see
     }
     const float neg = m_ref == -INFINITY ? 0.f : -m_ref;
     const uint64_t scale2 = pack2(scale_log2, scale_log2), neg2 = pack2(neg, neg);
-    sum2[0] = mul2(sum2[0], pack2(alpha, alpha));
-    sum2[1] = mul2(sum2[1], pack2(alpha, alpha));
+    sum2 = mul2(sum2, pack2(alpha, alpha));
+    uint64_t step2[2] = {0, 0};
 #pragma unroll
     for (int c = 0; c < N; c += 32) {
         uint32_t hi[16], lo[16];
@@ -210,7 +252,7 @@ __device__ __forceinline__ bool softmax_step(uint32_t s_t, uint32_t o_t, int see
             unpack2(fma2(pack2(__uint_as_float(raw[c + k]), __uint_as_float(raw[c + k + 1])), scale2, neg2), a, b);
             a = fast_exp2(a);
             b = fast_exp2(b);
-            sum2[(k >> 1) & 1] = add2(sum2[(k >> 1) & 1], pack2(a, b));
+            step2[(k >> 1) & 1] = add2(step2[(k >> 1) & 1], pack2(a, b));
             hi[k / 2] = Mma<T>::pack(a, b);
             if (SPLIT_P) lo[k / 2] = Mma<T>::pack(a - Mma<T>::round_trip(a), b - Mma<T>::round_trip(b));
         }
@@ -239,6 +281,7 @@ __device__ __forceinline__ bool softmax_step(uint32_t s_t, uint32_t o_t, int see
             if (lane == 0) mbar_arrive(bar_lo);
         }
     }
+    sum2 = add2(sum2, add2(step2[0], step2[1]));
     umma::wait_st();
     umma::fence_before_sync();
     __syncwarp();
@@ -869,6 +912,37 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
         int taken = 0, taken_even = 0, taken_odd = 0;  // S tiles so far: the phases of s_full and pv_step
         int outs = 0, twos = 0;  // pieces handed to the output warps, those with two tiles: of o_free
         bool p_clear = false;    // the P columns of pieces with few rows hold zeros where they should
+        // The row's totals of the steps before, in the workspace: O's, then the sum and their
+        // reference (not in registers, which the steps need).
+        auto kept = [&]() -> float4* {
+            return reinterpret_cast<float4*>(p.totals) + (blockIdx.x * 2 + t) * (128 * (D / 4 + 1)) + r;
+        };
+        auto to_now = [](float m_kept, float m_ref) { return m_kept == m_ref ? 1.f : fast_exp2(m_kept - m_ref); };
+        // before step j's softmax, its products so far done: O and the sum into the totals
+        auto keep = [&](int j, float m_ref, float l) {
+            float2* const sum_and_ref = reinterpret_cast<float2*>(kept() + D / 4 * 128);
+            const bool first = j == CHUNK_SUM_STEPS;
+            const float2 before = first ? make_float2(0.f, m_ref) : *sum_and_ref;
+            const float f = to_now(before.y, m_ref);
+            add_total<D, true>(o_t, kept(), f, first);
+            *sum_and_ref = make_float2(fmaf(before.x, f, l), m_ref);
+        };
+        // at the end, all products done: the totals into O and the sum
+        auto total = [&](float m_ref, float l) -> float {
+            const float2 before = *reinterpret_cast<const float2*>(kept() + D / 4 * 128);
+            const float f = to_now(before.y, m_ref);
+            add_total<D, false>(o_t, kept(), f, false);
+            return fmaf(before.x, f, l);
+        };
+        // waits for the products of the steps before step j (not yet taken), or of all of a piece
+        auto products_before = [&](int j, bool two, bool all = false) -> bool {
+            // (two tiles: the next scores are committed behind the products before them)
+            const uint32_t bar = !two ? pv_step((j - 1) & 1) : all ? pv_done(t) : s_full(t);
+            const int phase = !two ? ((j & 1) ? taken_even : taken_odd) - 1 : all ? twos : taken;
+            if (!__all_sync(FULL_MASK, mbar_wait_short(bar, phase & 1))) return false;
+            umma::fence_after_sync();
+            return true;
+        };
         // this row's m and l to the output warps
         auto hand_out = [&](float m, float l) -> bool {
             if (outs > 0) ok = __all_sync(FULL_MASK, mbar_wait_short(o_free(t), (outs - 1) & 1));
@@ -907,20 +981,32 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
                     p_clear = true;
                 }
                 float m_ref = -INFINITY, l = 0.f;
-                for (int j = 0; j < n; ++j) {
-                    const int b = j & 1, phase = b ? taken_odd++ : taken_even++;
-                    ok = __all_sync(FULL_MASK, mbar_wait_short(s_full(2 + b), phase & 1));
-                    if (!ok) break;
-                    umma::fence_after_sync();
-                    ok = few_rows_step<T, D>(lane_tmem + b * CHUNK_TILE + warp * 32,
-                                             p_t + b * (CHUNK_TILE / 2) + warp * 16, o_t,
-                                             lim_w - (pc.kt0 + j) * CHUNK_TILE, j > 0, p.scale_log2, m_ref, l,
-                                             pv_step(b ^ 1), (b ? taken_even : taken_odd) - 1);
-                    if (!ok) break;
-                    if (lane == 0) {
-                        mbar_arrive(p_full(2 + b, 0));
-                        mbar_arrive(p_full(2 + b, 1));
+                for (int j = 0; j < n && ok;) {
+                    if (j > 0) {
+                        ok = products_before(j, false);
+                        if (!ok) break;
+                        keep(j, m_ref, l);
+                        l = 0.f;
                     }
+                    for (const int end = min(n, j + CHUNK_SUM_STEPS); j < end; ++j) {
+                        const int b = j & 1, phase = b ? taken_odd++ : taken_even++;
+                        ok = __all_sync(FULL_MASK, mbar_wait_short(s_full(2 + b), phase & 1));
+                        if (!ok) break;
+                        umma::fence_after_sync();
+                        ok = few_rows_step<T, D>(lane_tmem + b * CHUNK_TILE + warp * 32,
+                                                 p_t + b * (CHUNK_TILE / 2) + warp * 16, o_t,
+                                                 lim_w - (pc.kt0 + j) * CHUNK_TILE, j > 0, p.scale_log2, m_ref, l,
+                                                 pv_step(b ^ 1), (b ? taken_even : taken_odd) - 1);
+                        if (!ok) break;
+                        if (lane == 0) {
+                            mbar_arrive(p_full(2 + b, 0));
+                            mbar_arrive(p_full(2 + b, 1));
+                        }
+                    }
+                }
+                if (ok && n > CHUNK_SUM_STEPS) {
+                    ok = products_before(n, false, true);
+                    if (ok) l = total(m_ref, l);
                 }
                 if (!ok || !hand_out(m_ref, l)) break;
                 continue;
@@ -928,40 +1014,56 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
             const bool busy = __any_sync(FULL_MASK, r < QPT * G && jq < pc.queries);
             const int lim = pc.lim0 + jq;
             float m_ref = -INFINITY;
-            uint64_t sum2[2] = {0, 0};  // the row's sum, in four parts
-            for (int j = 0; j < n; ++j) {
-                const int b = two ? t : 2 + (j & 1);  // S tile of this step
-                const int phase = two ? taken++ : (j & 1) ? taken_odd++ : taken_even++;
-                ok = __all_sync(FULL_MASK, mbar_wait_short(s_full(b), phase & 1));
-                if (!ok) break;
-                if (busy) {
-                    umma::fence_after_sync();
-                    const uint32_t s_t = lane_tmem + (b & 1) * CHUNK_TILE;
-                    const int seen = lim - (pc.kt0 + j) * CHUNK_TILE;  // columns this row may see
-                    // with two tiles a step's S was committed after the P.V before, with one not
-                    const uint32_t wait_o = two ? 0u : pv_step((j & 1) ^ 1);
-                    const int phase_o = ((j & 1) ? taken_even : taken_odd) - 1;
-                    if (__any_sync(FULL_MASK, seen < CHUNK_TILE))
-                        ok = softmax_step<T, D, SPLIT_P, true>(s_t, o_t, seen, j > 0, p.scale_log2, m_ref, sum2,
-                                                               p_full(b, 0), p_full(b, 1), wait_o, phase_o);
-                    else
-                        ok = softmax_step<T, D, SPLIT_P, false>(s_t, o_t, seen, j > 0, p.scale_log2, m_ref, sum2,
-                                                                p_full(b, 0), p_full(b, 1), wait_o, phase_o);
+            uint64_t sum2 = 0;  // the row's sum, in two parts
+            auto sum = [&] {
+                float a, b;
+                unpack2(sum2, a, b);
+                return a + b;
+            };
+            for (int j = 0; j < n && ok;) {
+                if (j > 0) {
+                    ok = products_before(j, two);
                     if (!ok) break;
-                } else if (lane == 0) {  // rows of no query: whatever S left there
-                    mbar_arrive(p_full(b, 0));
-                    mbar_arrive(p_full(b, 1));
+                    if (busy) keep(j, m_ref, sum());
+                    sum2 = 0;
+                }
+                for (const int end = min(n, j + CHUNK_SUM_STEPS); j < end; ++j) {
+                    const int b = two ? t : 2 + (j & 1);  // S tile of this step
+                    const int phase = two ? taken++ : (j & 1) ? taken_odd++ : taken_even++;
+                    ok = __all_sync(FULL_MASK, mbar_wait_short(s_full(b), phase & 1));
+                    if (!ok) break;
+                    if (busy) {
+                        umma::fence_after_sync();
+                        const uint32_t s_t = lane_tmem + (b & 1) * CHUNK_TILE;
+                        const int seen = lim - (pc.kt0 + j) * CHUNK_TILE;  // columns this row may see
+                        // with two tiles a step's S was committed after the P.V before, with one not
+                        const uint32_t wait_o = two ? 0u : pv_step((j & 1) ^ 1);
+                        const int phase_o = ((j & 1) ? taken_even : taken_odd) - 1;
+                        if (__any_sync(FULL_MASK, seen < CHUNK_TILE))
+                            ok = softmax_step<T, D, SPLIT_P, true>(s_t, o_t, seen, j > 0, p.scale_log2, m_ref, sum2,
+                                                                   p_full(b, 0), p_full(b, 1), wait_o, phase_o);
+                        else
+                            ok = softmax_step<T, D, SPLIT_P, false>(s_t, o_t, seen, j > 0, p.scale_log2, m_ref, sum2,
+                                                                    p_full(b, 0), p_full(b, 1), wait_o, phase_o);
+                        if (!ok) break;
+                    } else if (lane == 0) {  // rows of no query: whatever S left there
+                        mbar_arrive(p_full(b, 0));
+                        mbar_arrive(p_full(b, 1));
+                    }
                 }
             }
             if (!ok) break;
+            float l = sum();
+            if (busy && n > CHUNK_SUM_STEPS) {
+                ok = products_before(n, two, true);
+                if (!ok) break;
+                l = total(m_ref, l);
+            }
             if (two) {
                 p_clear = false;
                 ++twos;
             }
-            float part[4];
-            unpack2(sum2[0], part[0], part[1]);
-            unpack2(sum2[1], part[2], part[3]);
-            if (!hand_out(m_ref, (part[0] + part[1]) + (part[2] + part[3]))) break;
+            if (!hand_out(m_ref, l)) break;
         }
     }
     if (!ok && lane == 0) set_error(p.err, PKV_DEVERR_TIMEOUT);

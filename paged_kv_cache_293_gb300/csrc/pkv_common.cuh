@@ -141,6 +141,8 @@ constexpr int CHUNK_TILE = 128;       // cached tokens per step
 // heads, 18.8 us (23.3 with 16); 200 over 600 19.9 us (23.5 with 4).
 constexpr int CHUNK_SPLIT_MIN = 8;
 constexpr int64_t CHUNK_MAX_CONTEXT = 1 << 26;  // 2^19 steps: about 1 s of one CTA
+// Steps over which results are summed in tensor memory before they go into totals.
+constexpr int CHUNK_SUM_STEPS = 256;
 
 // A piece of work: queries [token, token + queries) of the batch for one kv head, over the
 // steps [kt0, kt1) of the request's context.  Query j sees positions below lim0 + j.
@@ -195,6 +197,7 @@ struct ChunkParams {
     float* part_m;      // base 2
     float* part_l;
     float* part_o;
+    float* totals;      // [ctas][2 tiles][D / 4 + 1][128 rows][4], where a piece may pass CHUNK_SUM_STEPS
     unsigned int* err;
 };
 

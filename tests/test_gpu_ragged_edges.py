@@ -1,5 +1,7 @@
 """The ragged-step operators on the GPU where values, lengths or sizes are extreme, against the
 plain models of ragged_helpers.py or results known from the formulas."""
+import math
+
 import pytest
 import torch
 
@@ -133,6 +135,82 @@ def test_scores_of_many_millions(P, dtype, new, rising):
         tol = torch.finfo(dt).eps * ref.abs().mean(0) + 2.0 ** -24
         assert ((out[t, 0].cpu().double() - ref.mean(0)).abs() <= tol).all(), t
     assert P.pkv_get_device_error() == 0
+
+
+# ---------------------------------------------------------------- long sums
+
+def _same_context(P, S, new, k, v, q, n, scale, out_dtype):
+    """S requests of `new` queries each, which all read one context of n tokens; also the number of cut items."""
+    T, i32 = S * new, dict(dtype=torch.int32, device=DEV)
+    tables = torch.arange(k.shape[0], **i32)[None].repeat(S, 1)
+    out = torch.zeros(T, q.shape[1], q.shape[2], dtype=out_dtype, device=DEV)
+    ws = P.workspace_tensor(P.pkv_chunk_workspace_bytes(k, T, S, q.shape[1], n), DEV)
+    start, ctx = torch.arange(0, T + 1, new, **i32), torch.full((S,), n, **i32)
+    P.pkv_paged_attention_chunk(q, k, v, start, tables, ctx, scale, out, n, ws)
+    assert P.pkv_get_device_error() == 0
+    return out, ws[:8].view(torch.int32)[1].item()
+
+
+@pytest.mark.parametrize("dtype,D", [("f16", 64), ("bf16", 128)])
+@pytest.mark.parametrize("f32_out", [False, True])
+@pytest.mark.parametrize("new,cut", [(1, False), (17, False), (140, False), (1, True)])
+@pytest.mark.parametrize("n", [1 << 17, 1 << 20])
+def test_long_sums_of_like_weights(P, dtype, D, f32_out, new, cut, n):
+    """A first key with weight 1, n - 1 others with one weight below it, and the same value everywhere: the
+    output is that value.  Weight and value have as many bits as the type holds, so that every product
+    and sum is rounded, all of them the same way.
+
+    The tensor cores cut off, 2^-23 at most a product of 16 tokens, over 256 steps of 8 products
+    until results go into totals: 2^-12; 16 products with a 32-bit output, whose weights have
+    remainders: 2^-11.  The sum: 32 terms a part of a step, 256 steps, and the n / 2^15 totals of
+    it and of the output, 2^-24 each.  The weights themselves: equal but for 2^-20, whose rounding
+    to the type gives the weight meant.  Pieces of a cut context: 32 terms.  Half a step of the output."""
+    dt, B = R.DTYPE[dtype], 32
+    bits = 10 if dtype == "f16" else 7
+    w, value = (2 ** bits + 15) * 2.0 ** (-bits - 3), 1 + 1 / 2.0 ** bits
+    n = 2 * n if cut else n          # (at most 32 pieces: of up to 512 steps)
+    S = 1 if cut else 3 * torch.cuda.get_device_properties(0).multi_processor_count + 14
+    k = torch.zeros(n // B, 1, B, D, dtype=dt, device=DEV)
+    k[..., 0] = -1
+    k[0, 0, 0, 0] = 0
+    q = torch.zeros(S * new, 1, D, dtype=dt, device=DEV)
+    q[..., 0] = 1
+    out, cuts = _same_context(P, S, new, k, torch.full_like(k, value), q, n, -math.log(w),
+                              torch.float32 if f32_out else dt)
+    assert (cuts > 0) == cut
+    tol = (2.0 ** -11 if f32_out else 2.0 ** -12) + (32 + 256 + 2 * n / 2 ** 15 + 2 * 32) * 2.0 ** -24 + 2.0 ** -20
+    tol = tol + torch.finfo(out.dtype).eps / 2 * (1 + tol)
+    err = out.double() / value - 1
+    assert err.abs().max().item() <= tol, (err.min().item(), err.max().item(), tol)
+
+
+@pytest.mark.parametrize("dtype,D,f32_out", [("f16", 128, False), ("bf16", 64, True), ("bf16", 128, False)])
+@pytest.mark.parametrize("new", [1, 20, 140])
+@pytest.mark.parametrize("sharpen", [0.0, 10.0])
+def test_long_pieces(P, dtype, D, f32_out, new, sharpen):
+    """Contexts of 70000 tokens in one piece each, so that totals are kept twice, with references that
+    stay and that rise along the context."""
+    dt, n, B = R.DTYPE[dtype], 70000, 16
+    S = 3 * torch.cuda.get_device_properties(0).multi_processor_count + 14
+    g = torch.Generator().manual_seed(new + D)
+    rising = sharpen * torch.arange(n).view(n // B, 1, B, 1) / n
+    k = (torch.randn(n // B, 1, B, D, generator=g) + rising).to(dt)
+    v = torch.randn(n // B, 1, B, D, generator=g).to(dt)
+    q = (torch.randn(S * new, 1, D, generator=g) + (0.5 if sharpen else 0.0)).to(dt)
+    out, cuts = _same_context(P, S, new, k.to(DEV), v.to(DEV), q.to(DEV), n, D ** -0.5,
+                              torch.float32 if f32_out else dt)
+    assert cuts == 0
+    some = [0, 151, S // 2, S - 1]
+    rows = torch.cat([torch.arange(s * new, (s + 1) * new) for s in some])
+    table = torch.arange(n // B)[None].repeat(len(some), 1)
+    ref, size, delta, length = R.chunk_attention(q[rows], k, v, range(0, len(rows) + 1, new), table, [n] * len(some),
+                                                 D ** -0.5)
+    # as the tolerance of one piece, whose sums count 2^-23 a token, but with 2^15 tokens and 3 totals
+    tol = R.chunk_tolerance(ref, size, delta, length.clamp(max=2 ** 15 + 3), dt, out.dtype)
+    if dtype == "f16":
+        tol = tol + n * 2.0 ** -32 * 8
+    err = (out[rows.to(DEV)].cpu().double() - ref).abs()
+    assert (err <= tol).all(), (float(err.max()), float((err / tol).max()))
 
 
 # ---------------------------------------------------------------- where the write's output may lie
