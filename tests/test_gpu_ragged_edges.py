@@ -2,12 +2,13 @@
 plain models of ragged_helpers.py or results known from the formulas."""
 import math
 
+import numpy as np
 import pytest
 import torch
 
 import ragged_helpers as R
 from gpu_helpers import pkv
-from test_gpu_ragged import DEV, Chunk
+from test_gpu_ragged import DEV, Chunk, GpuBatch, _host_batch
 
 pytestmark = pytest.mark.gpu
 
@@ -235,4 +236,71 @@ def test_write_output_next_to_its_inputs(P, place):
     out = buf[at:at + n].view(T, Hq, D)
     P.pkv_qk_norm_rope_write(q, k, v, *pools[2:], pos, slots, out, cos_sin=cs)
     assert torch.equal(out, want) and torch.equal(pools[0], pools[2]) and torch.equal(pools[1], pools[3])
+    assert P.pkv_get_device_error() == 0
+
+
+# ---------------------------------------------------------------- batches of more than one CTA or round
+
+def _mixed_batch(S, B, seed, spare):
+    """Lengths of S requests with invalid, too long, waiting and shared ones strewn in, and a free stack
+    that holds `spare` of the blocks they need."""
+    rng = np.random.default_rng(seed)
+    past, new = rng.integers(0, 3 * B, S), rng.integers(0, 2 * B, S)
+    M = 6
+    kind = rng.choice(["plain", "waits", "past < 0", "new < 0", "too long", "shared", "bad entry"], S,
+                      p=[0.76, 0.06, 0.03, 0.03, 0.04, 0.05, 0.03])
+    new[kind == "waits"] = 0
+    past[kind == "past < 0"] = -3
+    new[kind == "new < 0"] = -1
+    new[kind == "too long"] = M * B
+    h = _host_batch(S, past, B, M, spare=0, seed=seed)
+    for s in np.flatnonzero((kind == "shared") | (kind == "bad entry")):
+        if past[s] > 0 and past[s] % B:
+            if kind[s] == "shared":
+                h.refs[h.tables[s, past[s] // B]] = 2
+            else:
+                h.tables[s, past[s] // B] = -1
+    need = sum(R.blocks(max(p + n, 0), B) - R.blocks(max(p, 0), B) for p, n in zip(past, new) if n > 0)
+    first = h.N
+    h.N += int(need * spare)
+    h.free = [int(b) for b in rng.permutation(np.arange(first, h.N))]
+    h.refs = np.concatenate([h.refs, np.zeros(h.N - first, np.int32)])
+    return h, past, new
+
+
+@pytest.mark.parametrize("S,B", [(700, 16), (1500, 16), (1500, 32), (9000, 16), (20000, 16)])
+@pytest.mark.parametrize("spare", [0.45, 2.0])
+@pytest.mark.parametrize("room", [0.3, 0.8, 1.1])
+def test_large_batches_where_things_go_wrong(P, S, B, spare, room):
+    """Blocks or token rows that run out in a middle CTA or tile, requests of every status between
+    the served ones, and the kernel that fills in many tokens over all of them."""
+    h, past, new = _mixed_batch(S, B, S + B, spare)
+    T = int(np.maximum(new, 0).sum() * room)     # (past 4096, a second kernel's, but for 700 with 0.3)
+    g = GpuBatch(P, h, T)
+    g.build(past, new)
+    bad_entries = any(n > 0 and p > 0 and p % B and h.tables[s, p // B] < 0 and p + n <= h.M * B
+                      for s, (p, n) in enumerate(zip(past, new)))
+    want = h.build(past, new, T)
+    g.check(h, want)
+    counts = np.bincount(want["status"], minlength=4)
+    assert (counts[1] > 0) == (spare < 1 and room > 0.45) and counts[0] > 0 and counts[2] > 0 and counts[3] > 0
+    assert P.pkv_get_device_error() == ((P.DEVERR["POSITION"] if room < 1 else 0) |
+                                        (P.DEVERR["BLOCK_ID"] if bad_entries else 0))
+
+
+@pytest.mark.parametrize("Hq,Hkv,D", [(4, 1, 64), (4, 4, 128)])
+@pytest.mark.parametrize("places", [(3, 1101), (1060, 1070)])
+def test_chunk_cuts_in_a_list_of_many_tiles(P, Hq, Hkv, D, places):
+    """More tiles than one round of the list holds, with contexts to cut in the first and the last round."""
+    rng = np.random.default_rng(17)
+    ctx = rng.integers(1, 60, 1102).tolist()
+    new = [1] * len(ctx)
+    for s, (c, n) in zip(places, ((31000, 3), (36000, 260))):
+        ctx[s], new[s] = c, n
+    c = Chunk("bf16", Hq, Hkv, D, 16, ctx, new, 9, pad=2)
+    ws = c.workspace(P)
+    out = c.run(P, ws=ws)
+    assert ws[:8].view(torch.int32)[1].item() > 0    # items that were cut
+    c.check(out)
+    assert torch.equal(out, c.run(P))
     assert P.pkv_get_device_error() == 0
