@@ -430,11 +430,12 @@ pkv_status pkv_free_sequences(const pkv_block_allocator* alloc, int32_t block_si
 /*
  * One ragged step from the request lengths alone: request s holds past_lens[s]
  * cached tokens and brings new_lens[s] (any number, one for a decoding request,
- * none for one that waits); the step's tokens are packed request by request.  In
- * one launch: the blocks the new tokens need go from the free stack into the
- * tables, and every token gets its request, position and slot ("What Is vLLM",
- * section "How does PagedAttention work?": blocks are allocated on demand;
- * "Serving models with vLLM", section "How it works: continuous batching").
+ * none for one that waits); the step's tokens are packed request by request.  One
+ * call (one launch, or two above 4096 token rows): the blocks the new tokens need
+ * go from the free stack into the tables, and every token gets its request,
+ * position and slot ("What Is vLLM", section "How does PagedAttention work?":
+ * blocks are allocated on demand; "Serving models with vLLM", section "How it
+ * works: continuous batching").
  *   past_lens, new_lens  int32 [num_seqs]
  *   max_tokens      rows of the token arrays; the entries past the step's last
  *                   token are set to -1 (room for a captured step)
@@ -523,16 +524,14 @@ pkv_status pkv_qk_norm_rope_write(const pkv_pool* pool, const void* q, int64_t q
  * Cached rows at and past a request's context may hold anything; those below it must be
  * finite.  A query row that sees tokens and holds a NaN or an infinity, or whose scores pass
  * fp32's range, is NaN; the other rows do not notice.  Any group size num_q_heads /
- * num_kv_heads up to 128.  The probabilities enter
- * the product with V rounded to the pool's type when the output has that type (off by at
- * most 2^-8 of their value in bf16, 2^-11 in fp16), and with about twice its precision when
- * the output is fp32; in fp16, by at most 2^-32 of the row's largest where that is more.
- * Products are summed on the tensor cores over at most 2^15 tokens of a row, which may lose 2^-12
- * of the sum (2^-11 for an fp32 output), and in fp32 beyond.
- * fp16 / bf16 pools of fewer than 2^31
- * (block, kv head, position) rows, and tables or max_context_len of at most 2^26 tokens (else
- * PKV_ERR_UNSUPPORTED).  Device errors: query_start
- * not ascending within [0, num_tokens] (PKV_DEVERR_POSITION, nothing is computed); a
+ * num_kv_heads up to 128.  The probabilities enter the product with V rounded to the pool's
+ * type when the output has that type (off by at most 2^-8 of their value in bf16, 2^-11 in
+ * fp16), and with about twice its precision when the output is fp32; in fp16, by at most
+ * 2^-32 of the row's largest where that is more.  Products are summed on the tensor cores over
+ * at most 2^15 tokens of a row, which may lose 2^-12 of the sum (2^-11 for an fp32 output),
+ * and in fp32 beyond.  fp16 / bf16 pools of fewer than 2^31 (block, kv head, position) rows,
+ * and tables or max_context_len of at most 2^26 tokens (else PKV_ERR_UNSUPPORTED).
+ * Device errors: query_start not ascending within [0, num_tokens] (PKV_DEVERR_POSITION, nothing is computed); a
  * context_lens entry negative or past the table row or max_context_len
  * (PKV_DEVERR_CONTEXT, cut to that range); a table entry outside the pool
  * (PKV_DEVERR_BLOCK_ID, its positions count as zeros).

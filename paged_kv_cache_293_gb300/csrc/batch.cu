@@ -225,7 +225,8 @@ __global__ void __launch_bounds__(BATCH_THREADS) build_batch_kernel(const BatchP
     for (int s0 = s_lo; s0 < s_hi; s0 += BATCH_THREADS) {
         const int s = s0 + tid;
         const bool live = s < s_hi;
-        // one tile per CTA in all but the largest batches: the first pass's values serve
+        // one tile per CTA in all but the largest batches: the first pass's values serve (their sums
+        // within the CTA are made again)
         SeqNeed n{0, 0, 0, 0};
         if (live) n = (s_hi - s_lo <= BATCH_THREADS) ? held_need : seq_need(p, s, false);
         Pair tile;

@@ -42,21 +42,27 @@
 // falls behind its sum by up to 2^-23 a product of 16 tokens (weights alike over 2^20 tokens: by
 // 1 %).  So after every CHUNK_SUM_STEPS steps of a piece O and the sum are added to 32-bit totals in
 // the workspace and begin at zero again: off by 8 * 256 * 2^-23 = 2^-12 at most, whatever the
-// length (2^-11 with a 32-bit output, whose weights take two products; measured, weights and values
-// alike over 2^20 tokens: 2^-14).  A row's sum is one of sums of steps.
+// length (2^-11 with a 32-bit output, whose weights take two products; measured there, weights and
+// values alike over 2^20 tokens: 2^-12.7).  A row's sum is one of sums of steps.
 //
 // What bounds it, measured.  Two full tiles: a step has 2048 cycles of MMAs and takes about
-// 2600, the way of one tile once round: its softmax (1480 cycles: scores from tensor memory 310,
+// 2650, the way of one tile once round: its softmax (1500 cycles: scores from tensor memory 310,
 // 128 exponentials 920), the second half of P.V (256), Q.K^T (512) and three hand-overs.  8192
-// tokens from the first on, 32 / 8 heads of 128, bf16: 350 us, 1.57 PFLOP/s; 500 tokens over
-// 130,500: 700 us, 1.52 PFLOP/s.  What got it there, each for that prompt:
+// tokens from the first on, 32 / 8 heads of 128, bf16: 360 us, 1.53 PFLOP/s (0.80 of cuBLAS);
+// 500 tokens over 130,500: 712 to 745 us at the power cap, about 1.47 PFLOP/s.  What got it there,
+// each for that prompt:
 //   MMAs and copies issued under elect.sync and not under lane == 0 (67 cycles an MMA, 100 a
 //     copy there): 470 -> 411 us, and with V's copies three-dimensional (one for both halves of
 //     16 tokens; K's halves have to lie apart) 394;
 //   one thread issuing both tiles' MMAs and not one each, which run interleaved, so that both
 //     tiles' exponentials compete for the same units at the same time: 394 -> 373;
 //   registers so that the softmax does not spill: 373 -> 364; output by warps of its own: 352.
-// Few rows: 64 KB of K and V a step bound it, 1960 cycles where the HBM's share of an SM is 2790.
+// (One setmaxnreg for warps 8 to 11 and sums of steps brought it to 360.)  With a 32-bit output, whose
+// P.V is twice as long, the prompt takes 624 us.
+// Few rows over long contexts: 64 KB of K and V a step bound it, 1960 cycles where the HBM's share of
+// an SM is 2790 (32 requests over 60,000 tokens, 64 / 8 heads: 1135 us, 6.9 TB/s).  Over short ones
+// a piece's fixed cycles do, because copies run at most two pieces ahead of the output: 200 requests of
+// one query over 300 tokens, 32 / 8 heads 61.5 us, 1.7 times their bytes; 16 over 1500 24 us, 1.7.
 // Tried and slower: 16 softmax warps that share rows and exchange maxima; exponentials begun
 // with the old reference before the maximum is known; merging cut items in this kernel; the first
 // scores of the next piece issued before the last products of this one (48 requests, 70 % decoding,
@@ -91,7 +97,7 @@ struct ChunkReference<__half> {
     __device__ __forceinline__ static float scaled(float x, float scale_log2) { return __fmul_ru(x, scale_log2); }
 };
 // Rows up to which a piece's steps are spread over four warps: 200 requests with 1-5 queries, 32 / 8
-// heads, contexts about 300: 70 us (85 with 4 rows).
+// heads, contexts about 300: 79 us (93 with 4 rows).
 constexpr int CHUNK_FEW_ROWS = 16;
 
 template <int D>
