@@ -154,7 +154,7 @@ def _same_context(P, S, new, k, v, q, n, scale, out_dtype):
 
 @pytest.mark.parametrize("dtype,D", [("f16", 64), ("bf16", 128)])
 @pytest.mark.parametrize("f32_out", [False, True])
-@pytest.mark.parametrize("new,cut", [(1, False), (17, False), (140, False), (1, True)])
+@pytest.mark.parametrize("new,cut", [(1, False), (17, False), (140, False), (1, True), (17, True), (140, True)])
 @pytest.mark.parametrize("n", [1 << 17, 1 << 20])
 def test_long_sums_of_like_weights(P, dtype, D, f32_out, new, cut, n):
     """A first key with weight 1, n - 1 others with one weight below it, and the same value everywhere: the
