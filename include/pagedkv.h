@@ -23,7 +23,8 @@
  *    device error word that pkv_get_device_error() reads back; kernels never
  *    trap, assert or wait without a limit.
  *  - Element types: PKV_F32, PKV_F16, PKV_BF16.  q, k_new and v_new have the
- *    pool's element type.  Decode output is fp32 or the pool's type.
+ *    pool's element type.  Decode output is fp32 or the pool's type.  (The calls on
+ *    a pool of 8-bit values, pkv_q8_pool, name the type of the rest.)
  */
 #ifndef PAGEDKV_H
 #define PAGEDKV_H
@@ -545,6 +546,92 @@ pkv_status pkv_paged_attention_chunk(const pkv_pool* pool, const void* q, int32_
                                      int32_t max_context_len, float scale, void* out,
                                      int32_t out_dtype, void* workspace, size_t workspace_bytes,
                                      void* stream);
+
+/*
+ * A pool held in 8 bits: two arrays of e4m3 values (1 sign, 4 exponent and 3 fraction
+ * bits, largest 448, no infinities), each laid out [num_blocks][num_kv_heads]
+ * [block_size][head_dim] as in pkv_pool, and for each a 32-bit scale per page, that is
+ * per block and kv head: float [num_blocks][num_kv_heads].  A cached number is its e4m3
+ * value times its page's scale.  k and v 16-byte aligned, the scales 4-byte aligned;
+ * block_size in {16, 32}, head_dim in {64, 128}.  Half the bytes of a 16-bit pool, and
+ * 8 / (block_size * head_dim) more for the scales (0.4 % with 16 and 128).
+ */
+typedef struct pkv_q8_pool {
+    void* k;
+    void* v;
+    float* k_scale;
+    float* v_scale;
+    int32_t num_blocks;
+    int32_t block_size;
+    int32_t num_kv_heads;
+    int32_t head_dim;
+} pkv_q8_pool;
+
+/*
+ * pkv_qk_norm_rope_write into a pool held in 8 bits: the same norms and rotation, q rounded
+ * once to dtype (PKV_F16 or PKV_BF16, the type of q, k, v, the weights and q_out), and k and
+ * v rounded once to their pages' e4m3 values.  The tokens of one block stand behind one
+ * another in the call, their slots advancing as their rows do, as pkv_build_batch leaves them
+ * (rows between them may hold no token); each such run of tokens sets its page's scale, for
+ * keys and for values apart:
+ *   need   the least power of two, 2^-100 at least, whose 448 times reach the largest |x|
+ *          of the run's finite numbers
+ *   scale  need, where the run begins with the block's first slot (the block begins anew,
+ *          and what its other rows hold has no meaning any more); otherwise the larger of
+ *          need and the scale that the page has.  Where that is more than the page had, the
+ *          page's other rows are rounded again to the new scale.  (Old and new scales that
+ *          are powers of two, as this call makes them, leave a row's values as they were, but
+ *          for those that fall below 2^-6 of the new scale.)
+ *   value  x / scale to the nearest e4m3 value, even at ties; NaN where x is not finite
+ * Arguments and errors as pkv_qk_norm_rope_write's.  A run whose block the token before
+ * it has too, but not as the slot before (a slot twice, or slots in falling order), is not
+ * written and sets PKV_DEVERR_SLOT.  A block that comes at two separate places of a call has
+ * no defined contents; where the two are seen to meet, PKV_DEVERR_SLOT is set and one of them is
+ * left out.
+ */
+pkv_status pkv_qk_norm_rope_write_q8(const pkv_q8_pool* pool, int32_t dtype, const void* q,
+                                     int64_t q_stride, const void* k, int64_t k_stride,
+                                     const void* v, int64_t v_stride, int32_t num_tokens,
+                                     int32_t num_q_heads, const void* q_weight,
+                                     const void* k_weight, float eps, const float* cos_sin,
+                                     int32_t max_position, int32_t rotary_dim, int32_t interleaved,
+                                     const int32_t* positions, const int64_t* slot_mapping,
+                                     void* q_out, void* stream);
+
+/*
+ * Decode attention over a pool held in 8 bits, one or several query rows per sequence (as
+ * pkv_paged_attention_decode_multi: the queries of sequence s are those of its last
+ * num_queries positions, whose K and V are in the cache):
+ *   out[s][j][h] = softmax(scale * q[s][j][h] . K_s[0..c_j)^T) V_s[0..c_j),
+ *   c_j = context_lens[s] - num_queries + 1 + j     (a row with c_j <= 0 is zero).
+ *   q             [num_seqs][num_queries][num_q_heads][head_dim] of dtype (PKV_F16 or
+ *                 PKV_BF16), 16-byte aligned
+ *   block_tables  int32 [num_seqs][max_blocks_per_seq]; context_lens int32 [num_seqs]
+ *   out           as q, of out_dtype (PKV_F32 or dtype), 16-byte aligned
+ *   partition_size  tokens a piece of a context, a multiple of block_size; 0: chosen for
+ *                 the batch
+ *   workspace     pkv_decode_q8_workspace_bytes(...) bytes (0: none needed), 16-byte aligned;
+ *                 calls that may run at the same time need one each
+ * Any group size num_q_heads / num_kv_heads.  num_seqs and the number of pieces of a context
+ * up to 65535 each.  The queries enter their products exactly (in bf16, but for elements below 2^-30
+ * of their row's largest), the probabilities rounded to fp16 (off by at most 2^-11 of their value,
+ * and 2^-32 of the row's largest), with a remainder of another 11 bits when out is fp32.
+ * Cached rows past a query's last position may hold anything.  A row that sees tokens is NaN
+ * where its scores hold a NaN or pass fp32's range, or a seen value is NaN.  Scales are finite.
+ * Device errors: a context_lens entry negative or past the table row or max_context_len
+ * (PKV_DEVERR_CONTEXT, cut to that range); a table entry outside the pool
+ * (PKV_DEVERR_BLOCK_ID, its positions are left out).
+ */
+size_t pkv_decode_q8_workspace_bytes(const pkv_q8_pool* pool, int32_t num_seqs,
+                                     int32_t num_queries, int32_t num_q_heads,
+                                     int32_t max_context_len, int32_t partition_size);
+pkv_status pkv_paged_attention_decode_q8(const pkv_q8_pool* pool, int32_t dtype, const void* q,
+                                         int32_t num_queries, int32_t num_seqs,
+                                         int32_t num_q_heads, const int32_t* block_tables,
+                                         int32_t max_blocks_per_seq, const int32_t* context_lens,
+                                         int32_t max_context_len, float scale, void* out,
+                                         int32_t out_dtype, int32_t partition_size,
+                                         void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * Synchronises stream, then reads and clears the current device's error word

@@ -12,6 +12,7 @@
 
 #include "pkv_common.cuh"
 #include "prefix.cuh"
+#include "q8.cuh"
 
 namespace {
 
@@ -880,48 +881,45 @@ bool rows_overlap(const void* a, int64_t stride, int64_t width, int64_t n, const
 
 }  // namespace
 
-pkv_status pkv_qk_norm_rope_write(const pkv_pool* pool, const void* q, int64_t q_stride,
-                                  const void* k, int64_t k_stride, const void* v, int64_t v_stride,
-                                  int32_t num_tokens, int32_t num_q_heads, const void* q_weight,
-                                  const void* k_weight, float eps, const float* cos_sin,
-                                  int32_t max_position, int32_t rotary_dim, int32_t interleaved,
-                                  const int32_t* positions, const int64_t* slot_mapping,
-                                  void* q_out, void* stream) {
-    pkv_status st = check_pool(pool);
-    if (st != PKV_OK) return st;
-    if (num_tokens < 0 || num_q_heads <= 0 || rotary_dim < 0 || rotary_dim > pool->head_dim)
+namespace {
+
+// The arguments that both writes of turned rows take, checked and as their kernels want them; the
+// pools are checked before, `size` is an element of q's, k's and v's, `cache_bytes` those of a pool.
+pkv_status rope_params(pkv::RopeParams& p, int64_t size, void* k_pool, void* v_pool, int64_t cache_bytes,
+                       const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                       int64_t v_stride, int32_t num_tokens, int32_t num_q_heads, const void* q_weight,
+                       const void* k_weight, float eps, const float* cos_sin, int32_t max_position,
+                       int32_t rotary_dim, int32_t interleaved, const int32_t* positions,
+                       const int64_t* slot_mapping, void* q_out) {
+    if (num_tokens < 0 || num_q_heads <= 0 || rotary_dim < 0 || rotary_dim > p.head_dim)
         return PKV_ERR_INVALID;
     if (!std::isfinite(eps) || eps < 0.f) return PKV_ERR_INVALID;
     if ((rotary_dim > 0) != (cos_sin != nullptr) || (rotary_dim > 0 && max_position <= 0))
         return PKV_ERR_INVALID;
     if (rotary_dim % 16 != 0) return PKV_ERR_UNSUPPORTED;
-    if (num_q_heads > INT32_MAX - 2 * (int64_t)pool->num_kv_heads) return PKV_ERR_UNSUPPORTED;
+    if (num_q_heads > INT32_MAX - 2 * (int64_t)p.num_kv_heads) return PKV_ERR_UNSUPPORTED;
     if (num_tokens == 0) return PKV_OK;
     if (!q || !k || !v || !q_out || !positions || !slot_mapping) return PKV_ERR_INVALID;
     if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out) ||
         !aligned16(q_weight) || !aligned16(k_weight) || !aligned16(cos_sin))
         return PKV_ERR_INVALID;
     // a row of heads is packed; rows may be further apart, by whole 16-byte vectors
-    const int64_t vec = pool->dtype == PKV_F32 ? 4 : 8, D = pool->head_dim;
-    const int64_t need_q = num_q_heads * D, need_kv = pool->num_kv_heads * D;
+    const int64_t vec = 16 / size, D = p.head_dim;
+    const int64_t need_q = num_q_heads * D, need_kv = p.num_kv_heads * D;
     if (q_stride % vec != 0 || k_stride % vec != 0 || v_stride % vec != 0) return PKV_ERR_INVALID;
     if (num_tokens > 1 && (q_stride < need_q || k_stride < need_kv || v_stride < need_kv))
         return PKV_ERR_INVALID;
     // q_out may be q, row for row; otherwise tokens are read after others have been written
-    const int64_t size = pool->dtype == PKV_F32 ? 4 : 2, T = num_tokens, out_bytes = T * need_q * size;
-    const int64_t pool_bytes = (int64_t)pool->num_blocks * pool->block_size * need_kv * size;
+    const int64_t T = num_tokens, out_bytes = T * need_q * size;
     auto apart = [&](const void* in, int64_t bytes) { return !rows_overlap(in, bytes, bytes, 1, q_out, out_bytes); };
     const bool in_place = q_out == q && (T == 1 || q_stride == need_q);
     if ((!in_place && rows_overlap(q, q_stride * size, need_q * size, T, q_out, out_bytes)) ||
         rows_overlap(k, k_stride * size, need_kv * size, T, q_out, out_bytes) ||
         rows_overlap(v, v_stride * size, need_kv * size, T, q_out, out_bytes) ||
-        !apart(pool->k, pool_bytes) || !apart(pool->v, pool_bytes) || !apart(q_weight, D * size) ||
+        !apart(k_pool, cache_bytes) || !apart(v_pool, cache_bytes) || !apart(q_weight, D * size) ||
         !apart(k_weight, D * size) || !apart(cos_sin, (int64_t)max_position * rotary_dim * 4) ||
         !apart(positions, T * 4) || !apart(slot_mapping, T * 8))
         return PKV_ERR_INVALID;
-    pkv::RopeParams p{};
-    st = error_word(&p.err);
-    if (st != PKV_OK) return st;
     p.q = q;
     p.k = k;
     p.v = v;
@@ -940,12 +938,35 @@ pkv_status pkv_qk_norm_rope_write(const pkv_pool* pool, const void* q, int64_t q
     p.positions = positions;
     p.slot_mapping = slot_mapping;
     p.q_out = q_out;
-    p.k_pool = pool->k;
-    p.v_pool = pool->v;
+    p.k_pool = k_pool;
+    p.v_pool = v_pool;
+    return PKV_OK;
+}
+
+}  // namespace
+
+pkv_status pkv_qk_norm_rope_write(const pkv_pool* pool, const void* q, int64_t q_stride,
+                                  const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                                  int32_t num_tokens, int32_t num_q_heads, const void* q_weight,
+                                  const void* k_weight, float eps, const float* cos_sin,
+                                  int32_t max_position, int32_t rotary_dim, int32_t interleaved,
+                                  const int32_t* positions, const int64_t* slot_mapping,
+                                  void* q_out, void* stream) {
+    pkv_status st = check_pool(pool);
+    if (st != PKV_OK) return st;
+    const int64_t size = pool->dtype == PKV_F32 ? 4 : 2;
+    pkv::RopeParams p{};
     p.num_blocks = pool->num_blocks;
     p.block_size = pool->block_size;
     p.num_kv_heads = pool->num_kv_heads;
     p.head_dim = pool->head_dim;
+    st = rope_params(p, size, pool->k, pool->v,
+                     (int64_t)pool->num_blocks * pool->block_size * pool->num_kv_heads * pool->head_dim * size, q,
+                     q_stride, k, k_stride, v, v_stride, num_tokens, num_q_heads, q_weight, k_weight, eps, cos_sin,
+                     max_position, rotary_dim, interleaved, positions, slot_mapping, q_out);
+    if (st != PKV_OK || num_tokens == 0) return st;
+    st = error_word(&p.err);
+    if (st != PKV_OK) return st;
     return pkv::launch_rope_write(p, pool->dtype, static_cast<cudaStream_t>(stream)) == cudaSuccess
                ? PKV_OK
                : PKV_ERR_CUDA;
@@ -1090,6 +1111,156 @@ pkv_status pkv_paged_attention_chunk(const pkv_pool* pool, const void* q, int32_
     const int64_t merge_ctas = std::min<int64_t>(
         4 * (int64_t)sms, std::max(c.tiles * pool->num_kv_heads, ((int64_t)num_tokens * num_q_heads + 7) / 8));
     return pkv::launch_chunk_merge(p, (int)merge_ctas, s) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+namespace {
+
+pkv_status check_q8(const pkv_q8_pool* pool, int32_t dtype) {
+    if (!pool || !pool->k || !pool->v || !pool->k_scale || !pool->v_scale) return PKV_ERR_INVALID;
+    if (!aligned16(pool->k) || !aligned16(pool->v) ||
+        ((reinterpret_cast<uintptr_t>(pool->k_scale) | reinterpret_cast<uintptr_t>(pool->v_scale)) & 3u) != 0)
+        return PKV_ERR_INVALID;
+    if (pool->num_blocks <= 0 || pool->block_size <= 0 || pool->num_kv_heads <= 0 || pool->head_dim <= 0)
+        return PKV_ERR_INVALID;
+    if (dtype != PKV_F32 && dtype != PKV_F16 && dtype != PKV_BF16) return PKV_ERR_INVALID;
+    if (dtype == PKV_F32) return PKV_ERR_UNSUPPORTED;
+    if (pool->block_size != 16 && pool->block_size != 32) return PKV_ERR_UNSUPPORTED;
+    if (pool->head_dim != 64 && pool->head_dim != 128) return PKV_ERR_UNSUPPORTED;
+    return PKV_OK;
+}
+
+}  // namespace
+
+pkv_status pkv_qk_norm_rope_write_q8(const pkv_q8_pool* pool, int32_t dtype, const void* q,
+                                     int64_t q_stride, const void* k, int64_t k_stride,
+                                     const void* v, int64_t v_stride, int32_t num_tokens,
+                                     int32_t num_q_heads, const void* q_weight,
+                                     const void* k_weight, float eps, const float* cos_sin,
+                                     int32_t max_position, int32_t rotary_dim, int32_t interleaved,
+                                     const int32_t* positions, const int64_t* slot_mapping,
+                                     void* q_out, void* stream) {
+    pkv_status st = check_q8(pool, dtype);
+    if (st != PKV_OK) return st;
+    const int64_t pages = (int64_t)pool->num_blocks * pool->num_kv_heads;
+    pkv::RopeParams p{};
+    p.num_blocks = pool->num_blocks;
+    p.block_size = pool->block_size;
+    p.num_kv_heads = pool->num_kv_heads;
+    p.head_dim = pool->head_dim;
+    st = rope_params(p, 2, pool->k, pool->v, pages * pool->block_size * pool->head_dim, q, q_stride, k, k_stride, v,
+                     v_stride, num_tokens, num_q_heads, q_weight, k_weight, eps, cos_sin, max_position, rotary_dim,
+                     interleaved, positions, slot_mapping, q_out);
+    if (st != PKV_OK || num_tokens == 0) return st;
+    const int64_t out_bytes = (int64_t)num_tokens * num_q_heads * pool->head_dim * 2;
+    if (rows_overlap(pool->k_scale, pages * 4, pages * 4, 1, q_out, out_bytes) ||
+        rows_overlap(pool->v_scale, pages * 4, pages * 4, 1, q_out, out_bytes))
+        return PKV_ERR_INVALID;
+    st = error_word(&p.err);
+    if (st != PKV_OK) return st;
+    return pkv::launch_q8_write(p, pool->k_scale, pool->v_scale, dtype, static_cast<cudaStream_t>(stream)) ==
+                   cudaSuccess
+               ? PKV_OK
+               : PKV_ERR_CUDA;
+}
+
+namespace {
+
+// Tokens a piece: enough pieces for the SMs to be full twice over (three CTAs each), of 256 tokens
+// or more, and of 1024 at most where contexts are long, so that those of unequal length end together.
+int32_t q8_partition(const pkv_q8_pool* pool, int32_t S, int32_t NQ, int32_t Hq, int32_t max_ctx) {
+    const int32_t B = pool->block_size;
+    const int64_t cols = (int64_t)NQ * (Hq / pool->num_kv_heads);
+    const int64_t ctas = std::max<int64_t>(1, (int64_t)S * pool->num_kv_heads * ((cols + 7) / 8));
+    const int64_t parts = std::max<int64_t>(1, (6 * (int64_t)sm_count() + ctas - 1) / ctas);
+    int64_t P = std::max<int64_t>(256, ceil_div(max_ctx, parts));
+    if (max_ctx > 3072) P = std::min<int64_t>(P, 1024);
+    return (int32_t)(ceil_div(P, B) * B);
+}
+
+struct Q8Layout {
+    int32_t P, parts;
+    size_t l_off, o_off, bytes;
+};
+
+Q8Layout q8_layout(const pkv_q8_pool* pool, int32_t S, int32_t NQ, int32_t Hq, int32_t max_ctx, int32_t P) {
+    Q8Layout w{};
+    w.P = P > 0 ? P : q8_partition(pool, S, NQ, Hq, max_ctx);
+    w.parts = max_ctx > 0 ? ceil_div(max_ctx, w.P) : 1;
+    if (w.parts <= 1) return w;
+    const size_t rows = (size_t)S * NQ * Hq * w.parts;
+    w.l_off = (rows * 4 + 15) & ~size_t(15);
+    w.o_off = 2 * w.l_off;
+    w.bytes = w.o_off + rows * pool->head_dim * 4;
+    return w;
+}
+
+}  // namespace
+
+size_t pkv_decode_q8_workspace_bytes(const pkv_q8_pool* pool, int32_t num_seqs, int32_t num_queries,
+                                     int32_t num_q_heads, int32_t max_context_len,
+                                     int32_t partition_size) {
+    if (!pool || pool->num_kv_heads <= 0 || pool->head_dim <= 0 || pool->block_size <= 0 || num_seqs < 0 ||
+        num_queries <= 0 || num_q_heads <= 0 || max_context_len < 0 || partition_size < 0 ||
+        num_q_heads % pool->num_kv_heads != 0)
+        return 0;
+    return q8_layout(pool, num_seqs, num_queries, num_q_heads, max_context_len, partition_size).bytes;
+}
+
+pkv_status pkv_paged_attention_decode_q8(const pkv_q8_pool* pool, int32_t dtype, const void* q,
+                                         int32_t num_queries, int32_t num_seqs,
+                                         int32_t num_q_heads, const int32_t* block_tables,
+                                         int32_t max_blocks_per_seq, const int32_t* context_lens,
+                                         int32_t max_context_len, float scale, void* out,
+                                         int32_t out_dtype, int32_t partition_size,
+                                         void* workspace, size_t workspace_bytes, void* stream) {
+    pkv_status st = check_q8(pool, dtype);
+    if (st != PKV_OK) return st;
+    if (num_seqs < 0 || num_queries <= 0 || num_q_heads <= 0 || max_blocks_per_seq <= 0 || max_context_len < 0 ||
+        num_q_heads % pool->num_kv_heads != 0 || !std::isfinite(scale) || partition_size < 0 ||
+        partition_size % pool->block_size != 0)
+        return PKV_ERR_INVALID;
+    if (out_dtype != PKV_F32 && out_dtype != dtype) return PKV_ERR_UNSUPPORTED;
+    const Q8Layout w = q8_layout(pool, num_seqs, num_queries, num_q_heads, max_context_len, partition_size);
+    const int64_t cols = (int64_t)num_queries * (num_q_heads / pool->num_kv_heads);
+    if (num_seqs > 65535 || w.parts > 65535 || cols > INT32_MAX - 8 ||
+        pool->num_kv_heads * ((cols + 7) / 8) > INT32_MAX ||
+        (int64_t)num_seqs * num_queries * num_q_heads > INT32_MAX)
+        return PKV_ERR_UNSUPPORTED;
+    if (num_seqs == 0) return PKV_OK;
+    if (!q || !block_tables || !context_lens || !out || !aligned16(q) || !aligned16(out)) return PKV_ERR_INVALID;
+    if (w.bytes > 0 && (!workspace || !aligned16(workspace) || workspace_bytes < w.bytes)) return PKV_ERR_WORKSPACE;
+    pkv::Q8DecodeParams p{};
+    st = error_word(&p.err);
+    if (st != PKV_OK) return st;
+    p.k_pool = static_cast<const uint8_t*>(pool->k);
+    p.v_pool = static_cast<const uint8_t*>(pool->v);
+    p.k_scale = pool->k_scale;
+    p.v_scale = pool->v_scale;
+    p.num_blocks = pool->num_blocks;
+    p.block_size = pool->block_size;
+    p.num_kv_heads = pool->num_kv_heads;
+    p.q = q;
+    p.num_seqs = num_seqs;
+    p.num_queries = num_queries;
+    p.num_q_heads = num_q_heads;
+    p.block_tables = block_tables;
+    p.max_blocks_per_seq = max_blocks_per_seq;
+    p.context_lens = context_lens;
+    p.max_context_len = max_context_len;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    p.partition_size = w.P;
+    p.max_parts = w.parts;
+    p.out = out;
+    p.out_dtype = out_dtype;
+    char* const ws = static_cast<char*>(workspace);
+    p.part_m = reinterpret_cast<float*>(ws);
+    p.part_l = reinterpret_cast<float*>(ws + w.l_off);
+    p.part_o = reinterpret_cast<float*>(ws + w.o_off);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t e = dtype == PKV_F16 ? pkv::launch_q8_decode<__half>(p, pool->head_dim, s)
+                                     : pkv::launch_q8_decode<__nv_bfloat16>(p, pool->head_dim, s);
+    if (e == cudaSuccess && w.parts > 1) e = pkv::launch_q8_merge(p, pool->head_dim, s);
+    return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
 pkv_status pkv_get_device_error(uint32_t* flags, void* stream) {

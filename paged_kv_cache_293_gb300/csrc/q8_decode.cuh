@@ -1,0 +1,363 @@
+// q8_decode.cuh -- decode attention over a paged cache held in 8 bits ("What Is vLLM", section
+// "How does PagedAttention work?": every cached position is found through the block table and
+// read from the physical block holding it).
+//
+// For a query row q, pages b with scales a_b (keys) and c_b (values) and e4m3 values K, V:
+//   s_t = scale a_b (q . K_t),   out = sum_b c_b sum_t e^(s_t - m) V_t / sum_t e^(s_t - m)
+// HBM bound: a token of a kv head is 2 D bytes, read once for the G heads that share it, so the
+// work per byte is twice that of a 16-bit cache and the kernel is laid out to need few
+// instructions a byte.  Both products run on mma.sync.m16n8k16 in fp16, which holds every e4m3
+// value: scores^T [16 tokens x 8] = K . Q^T and O^T [D x 8] = V^T . P^T, the 8 columns being the
+// (query, head) pairs of one kv head, and the operands go from global memory to registers:
+//   K  lane (g, c) = (lane / 4, lane % 4) reads 16 bytes of tokens g and g + 8; the order of a
+//      product's D terms is free, so the 4 values of a word are a lane's terms of one k step
+//      (and Q is laid out alike);
+//   V  lane (g, c) reads the D / 8 bytes from g D / 8 on of tokens 2c, 2c + 1, 2c + 8, 2c + 9: the
+//      four tokens that its part of a k step takes, whose bytes one prmt a pair brings together.
+// No shared memory, no barrier in the loop, and the pages of a warp's next 16 tokens are on their
+// way while it works on these.  A page's scale a_b goes into the factor that its scores are
+// multiplied with anyway, and c_b into the sum of its O into the row's, in 32 bits.
+// Each row's reference follows its maximum and is raised only where a score exceeds it by more
+// than 15 in base 2 (it is set 7 below the maximum), so no lane asks the others for theirs but then.
+// P enters its product in fp16 (weights from 2^-21 of the largest on with 11 bits, none off by more
+// than 2^-32 of it), and with a 32-bit output in two parts.
+#pragma once
+
+#include "decode_mma.cuh"
+#include "q8.cuh"
+
+namespace pkv {
+
+constexpr int Q8_WARPS = 4;
+constexpr float Q8_BELOW = 7.f, Q8_RAISE = 15.f;
+
+__device__ __forceinline__ uint4 ldg_stream(const void* p) {
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
+__device__ __forceinline__ uint2 ldg_stream8(const void* p) {
+    uint2 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+    return v;
+}
+
+// The 8 x 8 matrix of 16-bit values whose row lane / 4 this lane has a pair of, transposed.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+template <typename T> __device__ __forceinline__ float2 pair_to_floats(uint32_t w);
+template <> __device__ __forceinline__ float2 pair_to_floats<__half>(uint32_t w) { return float2_of_f16x2(w); }
+template <> __device__ __forceinline__ float2 pair_to_floats<__nv_bfloat16>(uint32_t w) {
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+
+// The words of 16 tokens that a lane holds.
+template <int D>
+struct Q8Tokens {
+    static constexpr int KW = D / 16;  // words of a token's key: 16 bytes per 64 elements
+    static constexpr int VW = D / 32;  // words of a token's value
+    uint32_t k[2][KW];
+    uint32_t v[4][VW];
+    __device__ __forceinline__ void load_k(const uint8_t* page, int g, int c) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+            for (int i = 0; i < D / 64; ++i) {
+                const uint4 w = ldg_stream(page + (g + 8 * r) * D + 64 * i + 16 * c);
+                k[r][4 * i] = w.x; k[r][4 * i + 1] = w.y; k[r][4 * i + 2] = w.z; k[r][4 * i + 3] = w.w;
+            }
+    }
+    __device__ __forceinline__ void load_v(const uint8_t* page, int g, int c) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const uint8_t* at = page + (2 * c + (r & 1) + 8 * (r >> 1)) * D + g * (D / 8);
+            if constexpr (D == 128) {
+                const uint4 w = ldg_stream(at);
+                v[r][0] = w.x; v[r][1] = w.y; v[r][2] = w.z; v[r][3] = w.w;
+            } else {
+                const uint2 w = ldg_stream8(at);
+                v[r][0] = w.x; v[r][1] = w.y;
+            }
+        }
+    }
+};
+
+template <typename T, int D, bool SPLIT_P>
+__global__ void __launch_bounds__(Q8_WARPS * 32) q8_decode_kernel(const Q8DecodeParams p) {
+    constexpr int KS = D / 16, NW = Q8_WARPS;
+    __shared__ float red[NW][8][D + 2];
+    const int Hkv = p.num_kv_heads, Hq = p.num_q_heads, G = Hq / Hkv, NQ = p.num_queries, B = p.block_size;
+    const int kvh = blockIdx.x % Hkv, col0 = (blockIdx.x / Hkv) * 8, s = blockIdx.y;
+    const int part = gridDim.z - 1 - blockIdx.z;  // the last pieces, which few contexts reach, first
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+    const int ncols = min(8, NQ * G - col0);
+    // column n: query (col0 + n) / G, head (col0 + n) % G of the kv head
+    auto row_of = [&](int n) -> size_t {
+        return ((size_t)s * NQ + (col0 + n) / G) * Hq + kvh * G + (col0 + n) % G;
+    };
+
+    int ctx = p.context_lens[s];
+    const long long table = (long long)p.max_blocks_per_seq * B;
+    const int cap = (int)(table < p.max_context_len ? table : p.max_context_len);
+    if (ctx < 0 || ctx > cap) {
+        if (threadIdx.x == 0 && part == 0 && blockIdx.x == 0) set_error(p.err, PKV_DEVERR_CONTEXT);
+        ctx = ctx < 0 ? 0 : cap;
+    }
+    const int P = p.partition_size, n_parts = (ctx + P - 1) / P, tok0 = part * P;
+    if (part > 0 && tok0 >= ctx) return;
+    const bool direct = n_parts <= 1;
+    const int tok_end = min(ctx, tok0 + P);
+    const int n_chunks = (tok_end - tok0 + CHUNK_TOKENS - 1) / CHUNK_TOKENS;
+    const int n_my = warp < n_chunks ? (n_chunks - warp + NW - 1) / NW : 0;
+
+    // this warp's pages, 32 steps at a time: lane i has the page of step i, and its scales
+    const int32_t* bt_row = p.block_tables + (size_t)s * p.max_blocks_per_seq;
+    int page = -1;
+    float ka = 0.f, va = 0.f;
+    auto look_up = [&](int i) {
+        page = -1;
+        if (i >= n_my) return;
+        const int phys = __ldg(bt_row + (tok0 + (warp + NW * i) * CHUNK_TOKENS) / B);
+        if ((unsigned)phys >= (unsigned)p.num_blocks) {
+            set_error(p.err, PKV_DEVERR_BLOCK_ID);
+            return;
+        }
+        page = phys;
+        const size_t at = (size_t)phys * Hkv + kvh;
+        ka = __ldg(p.k_scale + at);
+        va = __ldg(p.v_scale + at);
+    };
+    // where step i's 16 tokens lie in the pools (the first block where there is none: read, not used)
+    auto place = [&](int i) -> size_t {
+        const int phys = max(__shfl_sync(FULL_MASK, page, i & 31), 0);
+        return (((size_t)phys * Hkv + kvh) * B + (warp + NW * i) * CHUNK_TOKENS % B) * D;
+    };
+    look_up(lane);
+    Q8Tokens<D> x;
+    size_t at = 0;
+    if (n_my > 0) {
+        at = place(0);
+        x.load_k(p.k_pool + at, g, c);
+        x.load_v(p.v_pool + at, g, c);
+    }
+
+    // Q^T: column g's terms 64 i + 16 c + 4 w .. + 3 for k step 4 i + w, in fp16.  bf16 rows are
+    // scaled by the power of two that brings their largest below 2^14, which keeps their bits.
+    uint32_t qb[KS][2];
+    float q_inv = 1.f;  // of column g
+    {
+        const T* src = static_cast<const T*>(p.q) + row_of(g < ncols ? g : 0) * D;
+        uint32_t w[D / 8];
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint4 v = __ldg(reinterpret_cast<const uint4*>(src + 64 * i + 16 * c + 8 * h));
+                w[8 * i + 4 * h] = v.x; w[8 * i + 4 * h + 1] = v.y; w[8 * i + 4 * h + 2] = v.z; w[8 * i + 4 * h + 3] = v.w;
+            }
+        if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+            float top = 0.f;
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) {
+                const float2 v = pair_to_floats<T>(w[i]);
+                top = fmaxf(top, fmaxf(fabsf(v.x), fabsf(v.y)));
+            }
+            top = fmaxf(top, __shfl_xor_sync(FULL_MASK, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(FULL_MASK, top, 2));
+            // top < 2^(e + 1): times 2^(13 - e); rows below 2^-80 keep that factor
+            const int e = max((__float_as_int(top) >> 23) - 127, -80);
+            const float mul = __int_as_float((13 - e + 127) << 23);
+            q_inv = __int_as_float((e - 13 + 127) << 23);
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) {
+                const float2 v = pair_to_floats<T>(w[i]);
+                w[i] = Mma<__half>::pack(v.x * mul, v.y * mul);
+            }
+        }
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) qb[ks][h] = g < ncols ? w[2 * ks + h] : 0u;
+    }
+    // this lane's columns from here on: 2 c and 2 c + 1, of tokens g and g + 8
+    float f[2], m_ref[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    int lim[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int n = 2 * c + h;
+        f[h] = p.scale_log2 * __shfl_sync(FULL_MASK, q_inv, 4 * n);
+        lim[h] = n < ncols ? ctx - NQ + 1 + (col0 + n) / G : ctx;  // positions below are seen
+    }
+    const int lim_all = min(lim[0], lim[1]);
+    float o[KS][4];
+#pragma unroll
+    for (int i = 0; i < KS; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+
+    for (int i = 0; i < n_my; ++i) {
+        const int t0 = tok0 + (warp + NW * i) * CHUNK_TOKENS;
+        const bool there = __shfl_sync(FULL_MASK, page, i & 31) >= 0;
+        const float a_b = __shfl_sync(FULL_MASK, ka, i & 31), c_b = __shfl_sync(FULL_MASK, va, i & 31);
+        if ((i & 31) == 31) look_up(i + 1 + lane);
+        const bool more = i + 1 < n_my;
+        if (more) at = place(i + 1);
+
+        float sc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+            uint32_t a0, a1, a2, a3;
+            f16x4_of_e4m3x4(x.k[0][ks], a0, a2);
+            f16x4_of_e4m3x4(x.k[1][ks], a1, a3);
+            Mma<__half>::run(sc, a0, a1, a2, a3, qb[ks][0], qb[ks][1]);
+        }
+        if (more) x.load_k(p.k_pool + at, g, c);
+
+        float pr[4];  // scores in base 2: token g + 8 (j / 2), column 2 c + j % 2
+        float over = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) pr[j] = sc[j] * (f[j & 1] * a_b);
+        if (!there || t0 + CHUNK_TOKENS > tok_end || __any_sync(FULL_MASK, t0 + CHUNK_TOKENS > lim_all)) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int t = t0 + g + 8 * (j >> 1);
+                if (!there || t >= tok_end || t >= lim[j & 1]) pr[j] = -INFINITY;
+            }
+            // values of tokens that no row sees may be anything, and 0 * NaN is not 0
+            const int seen = there ? tok_end - t0 : 0;
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                if (2 * c + (r & 1) + 8 * (r >> 1) >= seen) {
+#pragma unroll
+                    for (int w = 0; w < Q8Tokens<D>::VW; ++w) x.v[r][w] = 0u;
+                }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) over = fmaxf(over, pr[j] - m_ref[j & 1]);
+        if (__any_sync(FULL_MASK, over > Q8_RAISE)) {
+            float alpha[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float top = fmaxf(pr[h], pr[h + 2]);
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(FULL_MASK, top, d));
+                const float ref = top - m_ref[h] > Q8_RAISE ? top - Q8_BELOW : m_ref[h];
+                alpha[h] = ref == m_ref[h] ? 1.f : fast_exp2(m_ref[h] - ref);
+                m_ref[h] = ref;
+                l[h] *= alpha[h];
+            }
+#pragma unroll
+            for (int d = 0; d < KS; ++d) {
+                o[d][0] *= alpha[0]; o[d][1] *= alpha[1];
+                o[d][2] *= alpha[0]; o[d][3] *= alpha[1];
+            }
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const float ref = m_ref[h] == -INFINITY ? 0.f : m_ref[h];
+            pr[h] = fast_exp2(pr[h] - ref);
+            pr[h + 2] = fast_exp2(pr[h + 2] - ref);
+            l[h] += pr[h] + pr[h + 2];
+        }
+        const uint32_t b0 = transpose8x8(Mma<__half>::pack(pr[0], pr[1]));
+        const uint32_t b1 = transpose8x8(Mma<__half>::pack(pr[2], pr[3]));
+        uint32_t r0 = 0, r1 = 0;
+        if (SPLIT_P) {
+            float rem[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) rem[j] = pr[j] - Mma<__half>::round_trip(pr[j]);
+            r0 = transpose8x8(Mma<__half>::pack(rem[0], rem[1]));
+            r1 = transpose8x8(Mma<__half>::pack(rem[2], rem[3]));
+        }
+        // rows of O^T's tile 2 w + h: elements g D / 8 + 4 w + 2 h and the next one
+#pragma unroll
+        for (int w = 0; w < Q8Tokens<D>::VW; ++w)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint32_t a0, a1, a2, a3;
+                f16x4_of_e4m3x4(__byte_perm(x.v[0][w], x.v[1][w], h == 0 ? 0x5140 : 0x7362), a0, a1);
+                f16x4_of_e4m3x4(__byte_perm(x.v[2][w], x.v[3][w], h == 0 ? 0x5140 : 0x7362), a2, a3);
+                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                Mma<__half>::run(sum, a0, a1, a2, a3, b0, b1);
+                if (SPLIT_P) Mma<__half>::run(sum, a0, a1, a2, a3, r0, r1);
+                float(&od)[4] = o[2 * w + h];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) od[j] = fmaf(sum[j], c_b, od[j]);
+            }
+        if (more) x.load_v(p.v_pool + at, g, c);
+    }
+
+    // ---- the warps' results together
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) l[h] += __shfl_xor_sync(FULL_MASK, l[h], d);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        float* r = red[warp][2 * c + h];
+#pragma unroll
+        for (int i = 0; i < KS; ++i) {
+            r[g * (D / 8) + 2 * i] = o[i][h];
+            r[g * (D / 8) + 2 * i + 1] = o[i][h + 2];
+        }
+        if (g == 0) {
+            r[D] = m_ref[h];
+            r[D + 1] = l[h];
+        }
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < ncols * D; i += NW * 32) {
+        const int n = i / D, d = i % D;
+        float M = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) M = fmaxf(M, red[w][n][D]);
+        const float ref = M == -INFINITY ? 0.f : M;
+        float L = 0.f, O = 0.f;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+            const float by = fast_exp2(red[w][n][D] - ref);
+            L = fmaf(red[w][n][D + 1], by, L);
+            O = fmaf(red[w][n][d], by, O);
+        }
+        const size_t row = row_of(n);
+        if (direct) {
+            // zero for a row that sees nothing; a NaN or a sum of no weight is the result
+            const bool nothing = ctx - NQ + 1 + (col0 + n) / G <= 0;
+            store_out(p.out, p.out_dtype, row * D + d, nothing ? 0.f : O / L);
+        } else {
+            const size_t at_part = row * p.max_parts + part;
+            p.part_o[at_part * D + d] = O;
+            if (d == 0) {
+                p.part_m[at_part] = M;
+                p.part_l[at_part] = L;
+            }
+        }
+    }
+}
+
+template <typename T>
+cudaError_t launch_q8_decode_impl(const Q8DecodeParams& p, int head_dim, cudaStream_t stream) {
+    const int cols = p.num_queries * (p.num_q_heads / p.num_kv_heads);
+    const dim3 grid((unsigned)(p.num_kv_heads * ((cols + 7) / 8)), (unsigned)p.num_seqs, (unsigned)p.max_parts);
+    const bool split = p.out_dtype == PKV_F32;
+    if (head_dim == 64) {
+        if (split)
+            q8_decode_kernel<T, 64, true><<<grid, Q8_WARPS * 32, 0, stream>>>(p);
+        else
+            q8_decode_kernel<T, 64, false><<<grid, Q8_WARPS * 32, 0, stream>>>(p);
+    } else if (head_dim == 128) {
+        if (split)
+            q8_decode_kernel<T, 128, true><<<grid, Q8_WARPS * 32, 0, stream>>>(p);
+        else
+            q8_decode_kernel<T, 128, false><<<grid, Q8_WARPS * 32, 0, stream>>>(p);
+    } else {
+        return cudaErrorInvalidValue;
+    }
+    return cudaGetLastError();
+}
+
+}  // namespace pkv

@@ -36,6 +36,13 @@ class pkv_pool(ctypes.Structure):
                 ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int32)]
 
 
+class pkv_q8_pool(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("num_blocks", ctypes.c_int32),
+                ("block_size", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32)]
+
+
 class pkv_block_allocator(ctypes.Structure):
     _fields_ = [("free_ids", ctypes.c_void_p), ("free_count", ctypes.c_void_p),
                 ("refcount", ctypes.c_void_p), ("num_blocks", ctypes.c_int32)]
@@ -44,6 +51,7 @@ class pkv_block_allocator(ctypes.Structure):
 _P, _i32, _i64, _sz, _f32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
 _PP = ctypes.POINTER(pkv_pool)
 _PA = ctypes.POINTER(pkv_block_allocator)
+_PQ = ctypes.POINTER(pkv_q8_pool)
 _SIGS = {
     "pkv_slot_mapping": (_i32, [_P, _i32, _i32, _P, _P, _i32, _i32, _P, _P]),
     "pkv_kv_cache_write": (_i32, [_PP, _P, _P, _P, _i32, _P]),
@@ -81,6 +89,11 @@ _SIGS = {
     "pkv_chunk_workspace_bytes": (_sz, [_PP, _i32, _i32, _i32, _i32]),
     "pkv_paged_attention_chunk": (_i32, [_PP, _P, _i32, _i32, _P, _i32, _P, _i32, _P, _i32, _f32,
                                          _P, _i32, _P, _sz, _P]),
+    "pkv_qk_norm_rope_write_q8": (_i32, [_PQ, _i32, _P, _i64, _P, _i64, _P, _i64, _i32, _i32, _P, _P,
+                                         _f32, _P, _i32, _i32, _i32, _P, _P, _P, _P]),
+    "pkv_decode_q8_workspace_bytes": (_sz, [_PQ, _i32, _i32, _i32, _i32, _i32]),
+    "pkv_paged_attention_decode_q8": (_i32, [_PQ, _i32, _P, _i32, _i32, _i32, _P, _i32, _P, _i32,
+                                             _f32, _P, _i32, _i32, _P, _sz, _P]),
     "pkv_status_str": (ctypes.c_char_p, [_i32]),
     "pkv_version": (_i32, []),
     "pkv_set_decode_engine": (_i32, [_i32]),
@@ -469,17 +482,10 @@ def _head_rows(t, name, dtype, device, T, H, D):
     return t.stride(0) if T > 1 else H * D
 
 
-def pkv_qk_norm_rope_write(q, k, v, k_pool, v_pool, positions, slot_mapping, q_out, q_weight=None,
-                           k_weight=None, eps=1e-6, cos_sin=None, interleaved=False, stream=None):
-    """Per-head norms (where a weight is given) and rotation (where cos_sin
-    [max_position][rotary_dim] is given) of q and k; q to q_out, k and v to their slots."""
+def _rope_arguments(q, k, v, dt, dev, Hkv, positions, slot_mapping, q_out, q_weight, k_weight, eps, cos_sin,
+                    interleaved):
+    """What both writes of turned rows pass on after their pool, checked."""
     T, Hq, D = q.shape
-    dt = k_pool.dtype
-    dev = _current_device(q, "q")
-    pool = _pool_of(k_pool, v_pool, dev)
-    Hkv = pool.num_kv_heads
-    if pool.head_dim != D:
-        raise ValueError("q and the pools must have the same head_dim")
     qs = _head_rows(q, "q", dt, dev, T, Hq, D)
     ks = _head_rows(k, "k", dt, dev, T, Hkv, D)
     vs = _head_rows(v, "v", dt, dev, T, Hkv, D)
@@ -498,10 +504,21 @@ def pkv_qk_norm_rope_write(q, k, v, k_pool, v_pool, positions, slot_mapping, q_o
     if k_weight is not None:
         _expect(dev, dt, (k_weight, "k_weight", D))
         wk = k_weight.data_ptr()
-    st = lib.pkv_qk_norm_rope_write(pool, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, T, Hq,
-                                    wq, wk, eps, table, max_pos, rot, bool(interleaved),
-                                    positions.data_ptr(), slot_mapping.data_ptr(), q_out.data_ptr(),
-                                    _raw_stream(stream, dev))
+    return (q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, T, Hq, wq, wk, eps, table, max_pos, rot,
+            bool(interleaved), positions.data_ptr(), slot_mapping.data_ptr(), q_out.data_ptr())
+
+
+def pkv_qk_norm_rope_write(q, k, v, k_pool, v_pool, positions, slot_mapping, q_out, q_weight=None,
+                           k_weight=None, eps=1e-6, cos_sin=None, interleaved=False, stream=None):
+    """Per-head norms (where a weight is given) and rotation (where cos_sin
+    [max_position][rotary_dim] is given) of q and k; q to q_out, k and v to their slots."""
+    dev = _current_device(q, "q")
+    pool = _pool_of(k_pool, v_pool, dev)
+    if pool.head_dim != q.shape[2]:
+        raise ValueError("q and the pools must have the same head_dim")
+    st = lib.pkv_qk_norm_rope_write(
+        pool, *_rope_arguments(q, k, v, k_pool.dtype, dev, pool.num_kv_heads, positions, slot_mapping, q_out,
+                               q_weight, k_weight, eps, cos_sin, interleaved), _raw_stream(stream, dev))
     if st != PKV_OK:
         raise PagedKVError(st, "pkv_qk_norm_rope_write")
 
@@ -532,6 +549,88 @@ def pkv_paged_attention_chunk(q, k_pool, v_pool, query_start, block_tables, cont
         workspace.data_ptr(), workspace.nbytes, _raw_stream(stream, dev))
     if st != PKV_OK:
         raise PagedKVError(st, "pkv_paged_attention_chunk")
+
+
+def make_q8_pool(k_pool, v_pool, k_scale, v_scale):
+    """pkv_q8_pool view of two float8_e4m3fn [N][Hkv][B][D] tensors and their float32 [N][Hkv] scales."""
+    _contig(k_pool, v_pool, k_scale, v_scale)
+    shape = k_pool.shape
+    if len(shape) != 4 or v_pool.shape != shape or k_scale.shape != shape[:2] or v_scale.shape != shape[:2]:
+        raise ValueError("k_pool and v_pool must be matching [N][Hkv][B][D] tensors, the scales [N][Hkv]")
+    if k_pool.dtype is not torch.float8_e4m3fn or v_pool.dtype is not torch.float8_e4m3fn:
+        raise ValueError("k_pool and v_pool must be float8_e4m3fn")
+    if k_scale.dtype is not torch.float32 or v_scale.dtype is not torch.float32:
+        raise ValueError("k_scale and v_scale must be float32")
+    return pkv_q8_pool(k_pool.data_ptr(), v_pool.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                       shape[0], shape[2], shape[1], shape[3])
+
+
+def _q8_pool_of(k_pool, v_pool, k_scale, v_scale, device):
+    for t in (k_pool, v_pool, k_scale, v_scale):
+        if t.get_device() != device:
+            raise ValueError("the pools and their scales must be on the current CUDA device")
+    return make_q8_pool(k_pool, v_pool, k_scale, v_scale)
+
+
+_HALVES = {torch.float16: PKV_F16, torch.bfloat16: PKV_BF16}
+
+
+def _half_type(t, name):
+    code = _HALVES.get(t.dtype)
+    if code is None:
+        raise ValueError("%s must be float16 or bfloat16" % name)
+    return code
+
+
+def pkv_qk_norm_rope_write_q8(q, k, v, k_pool, v_pool, k_scale, v_scale, positions, slot_mapping, q_out,
+                              q_weight=None, k_weight=None, eps=1e-6, cos_sin=None, interleaved=False,
+                              stream=None):
+    """pkv_qk_norm_rope_write into float8_e4m3fn pools whose pages (block, kv head) have a float32
+    scale each; the tokens of a block stand behind one another, in the order of their slots."""
+    dev = _current_device(q, "q")
+    pool = _q8_pool_of(k_pool, v_pool, k_scale, v_scale, dev)
+    if pool.head_dim != q.shape[2]:
+        raise ValueError("q and the pools must have the same head_dim")
+    st = lib.pkv_qk_norm_rope_write_q8(
+        pool, _half_type(q, "q"),
+        *_rope_arguments(q, k, v, q.dtype, dev, pool.num_kv_heads, positions, slot_mapping, q_out, q_weight,
+                         k_weight, eps, cos_sin, interleaved), _raw_stream(stream, dev))
+    if st != PKV_OK:
+        raise PagedKVError(st, "pkv_qk_norm_rope_write_q8")
+
+
+def pkv_decode_q8_workspace_bytes(k_pool, num_seqs, num_queries, num_q_heads, max_context_len,
+                                  partition_size=0):
+    N, Hkv, B, D = k_pool.shape
+    return lib.pkv_decode_q8_workspace_bytes(pkv_q8_pool(None, None, None, None, N, B, Hkv, D), num_seqs,
+                                             num_queries, num_q_heads, int(max_context_len),
+                                             int(partition_size))
+
+
+def pkv_paged_attention_decode_q8(q, k_pool, v_pool, k_scale, v_scale, block_tables, context_lens, scale,
+                                  out, max_context_len, partition_size=0, workspace=None, stream=None):
+    """Decode over float8_e4m3fn pools; q, out: [num_seqs][num_q_heads][head_dim], or
+    [num_seqs][num_queries][num_q_heads][head_dim] for the last num_queries positions."""
+    S, NQ, Hq, D = q.shape if q.dim() == 4 else (q.shape[0], 1, q.shape[1], q.shape[2])
+    M = block_tables.shape[1]
+    dev = _current_device(q, "q")
+    pool = _q8_pool_of(k_pool, v_pool, k_scale, v_scale, dev)
+    if pool.head_dim != D:
+        raise ValueError("q and the pools must have the same head_dim")
+    dt = _half_type(q, "q")
+    _expect(dev, q.dtype, (q, "q", S * NQ * Hq * D))
+    _expect(dev, out.dtype, (out, "out", S * NQ * Hq * D))
+    _expect(dev, torch.int32, (block_tables, "block_tables", S * M), (context_lens, "context_lens", S))
+    ws = ws_bytes = 0
+    if workspace is not None:
+        _expect(dev, workspace.dtype, (workspace, "workspace", workspace.numel()))
+        ws, ws_bytes = workspace.data_ptr(), workspace.nbytes
+    st = lib.pkv_paged_attention_decode_q8(
+        pool, dt, q.data_ptr(), NQ, S, Hq, block_tables.data_ptr(), M, context_lens.data_ptr(),
+        int(max_context_len), scale, out.data_ptr(), _DTYPE[out.dtype], int(partition_size), ws or None,
+        ws_bytes, _raw_stream(stream, dev))
+    if st != PKV_OK:
+        raise PagedKVError(st, "pkv_paged_attention_decode_q8")
 
 
 def pkv_get_device_error(stream=None, device=None):
