@@ -634,6 +634,23 @@ pkv_status pkv_paged_attention_decode_q8(const pkv_q8_pool* pool, int32_t dtype,
                                          void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * pkv_paged_attention_chunk over a pool held in 8 bits: arguments, limits and errors as there
+ * with dtype (PKV_F16 or PKV_BF16) for the type of q and of the products.  A cached number, its
+ * e4m3 value times its page's scale, enters the products rounded once to dtype: exactly, where
+ * the scale is a power of two (as pkv_qk_norm_rope_write_q8 makes them) and the number in the
+ * type's range of full steps.  The workspace is pkv_chunk_q8_workspace_bytes(...) bytes.
+ */
+size_t pkv_chunk_q8_workspace_bytes(const pkv_q8_pool* pool, int32_t num_tokens, int32_t num_seqs,
+                                    int32_t num_q_heads, int32_t max_context_len);
+pkv_status pkv_paged_attention_chunk_q8(const pkv_q8_pool* pool, int32_t dtype, const void* q,
+                                        int32_t num_tokens, int32_t num_q_heads,
+                                        const int32_t* query_start, int32_t num_seqs,
+                                        const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                        const int32_t* context_lens, int32_t max_context_len,
+                                        float scale, void* out, int32_t out_dtype, void* workspace,
+                                        size_t workspace_bytes, void* stream);
+
+/*
  * Synchronises stream, then reads and clears the current device's error word
  * into *flags (host pointer).  Returns PKV_ERR_DEVICE when any bit was set.
  */

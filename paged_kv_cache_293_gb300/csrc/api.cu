@@ -980,8 +980,8 @@ struct ChunkShape {
     size_t tile_start, tile, piece, merge, m, l, o, totals, bytes;
 };
 
-ChunkShape chunk_shape(const pkv_pool* pool, int32_t T, int32_t S, int32_t Hq, int32_t max_ctx) {
-    const int64_t Hkv = pool->num_kv_heads, G = Hq / Hkv, sms = sm_count();
+ChunkShape chunk_shape(int64_t Hkv, int32_t D, int32_t T, int32_t S, int32_t Hq, int32_t max_ctx) {
+    const int64_t G = Hq / Hkv, sms = sm_count();
     const int64_t QT = 2 * (128 / G);  // queries per tile
     ChunkShape c{};
     c.tiles = std::min<int64_t>(T, T / QT + S);
@@ -1002,9 +1002,9 @@ ChunkShape chunk_shape(const pkv_pool* pool, int32_t T, int32_t S, int32_t Hq, i
     c.merge = take((size_t)(c.cut_pieces / 2) * sizeof(pkv::ChunkMerge));
     c.m = take((size_t)c.partial_rows * 4);
     c.l = take((size_t)c.partial_rows * 4);
-    c.o = take((size_t)c.partial_rows * pool->head_dim * 4);
+    c.o = take((size_t)c.partial_rows * D * 4);
     // two tiles of 128 rows per CTA
-    const int64_t totals = std::min(c.pieces, sms) * 256 * (pool->head_dim + 4);
+    const int64_t totals = std::min(c.pieces, sms) * 256 * (D + 4);
     c.totals = take(steps > pkv::CHUNK_SUM_STEPS ? (size_t)totals * 4 : 0);
     c.bytes = at;
     return c;
@@ -1012,58 +1012,62 @@ ChunkShape chunk_shape(const pkv_pool* pool, int32_t T, int32_t S, int32_t Hq, i
 
 }  // namespace
 
-size_t pkv_chunk_workspace_bytes(const pkv_pool* pool, int32_t num_tokens, int32_t num_seqs,
-                                 int32_t num_q_heads, int32_t max_context_len) {
-    if (!pool || pool->num_kv_heads <= 0 || pool->head_dim <= 0 || num_tokens < 0 || num_seqs < 0 ||
-        num_q_heads <= 0 || max_context_len < 0 || num_q_heads % pool->num_kv_heads != 0 ||
-        num_q_heads / pool->num_kv_heads > 128)
+namespace {
+
+// The pool of a chunk attention call: 16-bit, or 8-bit with its scales.
+struct ChunkPool {
+    const void *k, *v;
+    const float *k_scale, *v_scale;  // null: 16-bit
+    int32_t num_blocks, block_size, num_kv_heads, head_dim, dtype;
+};
+
+size_t chunk_workspace(const ChunkPool& pool, int32_t num_tokens, int32_t num_seqs, int32_t num_q_heads,
+                       int32_t max_context_len) {
+    if (pool.num_kv_heads <= 0 || pool.head_dim <= 0 || num_tokens < 0 || num_seqs < 0 ||
+        num_q_heads <= 0 || max_context_len < 0 || num_q_heads % pool.num_kv_heads != 0 ||
+        num_q_heads / pool.num_kv_heads > 128)
         return 0;
-    return chunk_shape(pool, num_tokens, num_seqs, num_q_heads, max_context_len).bytes;
+    return chunk_shape(pool.num_kv_heads, pool.head_dim, num_tokens, num_seqs, num_q_heads, max_context_len).bytes;
 }
 
-pkv_status pkv_paged_attention_chunk(const pkv_pool* pool, const void* q, int32_t num_tokens,
-                                     int32_t num_q_heads, const int32_t* query_start,
-                                     int32_t num_seqs, const int32_t* block_tables,
-                                     int32_t max_blocks_per_seq, const int32_t* context_lens,
-                                     int32_t max_context_len, float scale, void* out,
-                                     int32_t out_dtype, void* workspace, size_t workspace_bytes,
-                                     void* stream) {
-    pkv_status st = check_pool(pool);
-    if (st != PKV_OK) return st;
+pkv_status run_chunk(const ChunkPool& pool, const void* q, int32_t num_tokens, int32_t num_q_heads,
+                     const int32_t* query_start, int32_t num_seqs, const int32_t* block_tables,
+                     int32_t max_blocks_per_seq, const int32_t* context_lens, int32_t max_context_len, float scale,
+                     void* out, int32_t out_dtype, void* workspace, size_t workspace_bytes, void* stream) {
     if (num_tokens < 0 || num_seqs < 0 || num_q_heads <= 0 || max_blocks_per_seq <= 0 ||
-        max_context_len < 0 || num_q_heads % pool->num_kv_heads != 0 || !std::isfinite(scale))
+        max_context_len < 0 || num_q_heads % pool.num_kv_heads != 0 || !std::isfinite(scale))
         return PKV_ERR_INVALID;
-    if (out_dtype != PKV_F32 && out_dtype != pool->dtype) return PKV_ERR_UNSUPPORTED;
-    const int32_t G = num_q_heads / pool->num_kv_heads;
-    if (pool->dtype == PKV_F32 || G > 128) return PKV_ERR_UNSUPPORTED;
-    if ((int64_t)pool->num_blocks * pool->num_kv_heads * pool->block_size >= (1ll << 31))
+    if (out_dtype != PKV_F32 && out_dtype != pool.dtype) return PKV_ERR_UNSUPPORTED;
+    const int32_t G = num_q_heads / pool.num_kv_heads;
+    if (pool.dtype == PKV_F32 || G > 128) return PKV_ERR_UNSUPPORTED;
+    if ((int64_t)pool.num_blocks * pool.num_kv_heads * pool.block_size >= (1ll << 31))
         return PKV_ERR_UNSUPPORTED;  // tensor-copy rows are int32
     // one CTA may have a whole context, and the kernel's waits end after about 2 s
-    if (std::min<int64_t>((int64_t)max_blocks_per_seq * pool->block_size, max_context_len) > pkv::CHUNK_MAX_CONTEXT)
+    if (std::min<int64_t>((int64_t)max_blocks_per_seq * pool.block_size, max_context_len) > pkv::CHUNK_MAX_CONTEXT)
         return PKV_ERR_UNSUPPORTED;
-    const ChunkShape c = chunk_shape(pool, num_tokens, num_seqs, num_q_heads, max_context_len);
+    const ChunkShape c = chunk_shape(pool.num_kv_heads, pool.head_dim, num_tokens, num_seqs, num_q_heads, max_context_len);
     if (c.pieces > INT32_MAX) return PKV_ERR_UNSUPPORTED;
     if (num_tokens == 0 || num_seqs == 0) return PKV_OK;
     if (!q || !query_start || !block_tables || !context_lens || !out || !aligned16(q) || !aligned16(out))
         return PKV_ERR_INVALID;
     if (!workspace || !aligned16(workspace) || workspace_bytes < c.bytes) return PKV_ERR_WORKSPACE;
     unsigned int* err = nullptr;
-    st = error_word(&err);
+    const pkv_status st = error_word(&err);
     if (st != PKV_OK) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     char* ws = static_cast<char*>(workspace);
     const int32_t sms = sm_count();
 
-    pkv::ChunkTensors x{q, pool->k, pool->v, num_tokens, (int32_t)std::min<int64_t>(c.pieces, sms), c.tiles};
+    pkv::ChunkTensors x{q, pool.k, pool.v, num_tokens, (int32_t)std::min<int64_t>(c.pieces, sms), c.tiles};
     pkv::ChunkPlanParams pl{};
     pl.query_start = query_start;
     pl.context_lens = context_lens;
     pl.num_seqs = num_seqs;
     pl.num_tokens = num_tokens;
     pl.max_blocks_per_seq = max_blocks_per_seq;
-    pl.block_size = pool->block_size;
+    pl.block_size = pool.block_size;
     pl.max_context_len = max_context_len;
-    pl.num_kv_heads = pool->num_kv_heads;
+    pl.num_kv_heads = pool.num_kv_heads;
     pl.group = G;
     pl.num_sms = sms;
     pl.ctas = x.ctas;
@@ -1078,11 +1082,11 @@ pkv_status pkv_paged_attention_chunk(const pkv_pool* pool, const void* q, int32_
 
     pkv::ChunkParams p{};
     p.num_q_heads = num_q_heads;
-    p.num_kv_heads = pool->num_kv_heads;
+    p.num_kv_heads = pool.num_kv_heads;
     p.group = G;
-    p.head_dim = pool->head_dim;
-    p.num_blocks = pool->num_blocks;
-    p.block_size = pool->block_size;
+    p.head_dim = pool.head_dim;
+    p.num_blocks = pool.num_blocks;
+    p.block_size = pool.block_size;
     p.block_tables = block_tables;
     p.max_blocks_per_seq = max_blocks_per_seq;
     // the kernel takes maxima before scaling, which a positive scale allows: a negative one
@@ -1099,9 +1103,14 @@ pkv_status pkv_paged_attention_chunk(const pkv_pool* pool, const void* q, int32_
     p.part_l = reinterpret_cast<float*>(ws + c.l);
     p.part_o = reinterpret_cast<float*>(ws + c.o);
     p.totals = reinterpret_cast<float*>(ws + c.totals);
+    p.k_scale = pool.k_scale;
+    p.v_scale = pool.v_scale;
     p.err = err;
-    const cudaError_t e = pool->dtype == PKV_F16 ? pkv::launch_chunk<__half>(pl, p, x, s)
-                                                 : pkv::launch_chunk<__nv_bfloat16>(pl, p, x, s);
+    const bool f16 = pool.dtype == PKV_F16;
+    const cudaError_t e = pool.k_scale ? (f16 ? pkv::launch_chunk_q8<__half>(pl, p, x, s)
+                                              : pkv::launch_chunk_q8<__nv_bfloat16>(pl, p, x, s))
+                                       : (f16 ? pkv::launch_chunk<__half>(pl, p, x, s)
+                                              : pkv::launch_chunk<__nv_bfloat16>(pl, p, x, s));
     if (e == cudaErrorNotSupported) return PKV_ERR_UNSUPPORTED;
     if (e != cudaSuccess) return PKV_ERR_CUDA;
     if (c.partial_rows == 0) return PKV_OK;
@@ -1109,8 +1118,37 @@ pkv_status pkv_paged_attention_chunk(const pkv_pool* pool, const void* q, int32_
     // 512 queries 30.6 -> 29.8 us against 16 per SM; with 1 per SM 500 tokens over 130,500 take 735
     // us and not 700)
     const int64_t merge_ctas = std::min<int64_t>(
-        4 * (int64_t)sms, std::max(c.tiles * pool->num_kv_heads, ((int64_t)num_tokens * num_q_heads + 7) / 8));
+        4 * (int64_t)sms, std::max(c.tiles * pool.num_kv_heads, ((int64_t)num_tokens * num_q_heads + 7) / 8));
     return pkv::launch_chunk_merge(p, (int)merge_ctas, s) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+ChunkPool chunk_pool(const pkv_pool* p) {
+    return {p->k, p->v, nullptr, nullptr, p->num_blocks, p->block_size, p->num_kv_heads, p->head_dim, p->dtype};
+}
+
+ChunkPool chunk_pool_q8(const pkv_q8_pool* p, int32_t dtype) {
+    return {p->k, p->v, p->k_scale, p->v_scale, p->num_blocks, p->block_size, p->num_kv_heads, p->head_dim, dtype};
+}
+
+}  // namespace
+
+size_t pkv_chunk_workspace_bytes(const pkv_pool* pool, int32_t num_tokens, int32_t num_seqs,
+                                 int32_t num_q_heads, int32_t max_context_len) {
+    return pool ? chunk_workspace(chunk_pool(pool), num_tokens, num_seqs, num_q_heads, max_context_len) : 0;
+}
+
+pkv_status pkv_paged_attention_chunk(const pkv_pool* pool, const void* q, int32_t num_tokens,
+                                     int32_t num_q_heads, const int32_t* query_start,
+                                     int32_t num_seqs, const int32_t* block_tables,
+                                     int32_t max_blocks_per_seq, const int32_t* context_lens,
+                                     int32_t max_context_len, float scale, void* out,
+                                     int32_t out_dtype, void* workspace, size_t workspace_bytes,
+                                     void* stream) {
+    const pkv_status st = check_pool(pool);
+    if (st != PKV_OK) return st;
+    return run_chunk(chunk_pool(pool), q, num_tokens, num_q_heads, query_start, num_seqs, block_tables,
+                     max_blocks_per_seq, context_lens, max_context_len, scale, out, out_dtype, workspace,
+                     workspace_bytes, stream);
 }
 
 namespace {
@@ -1261,6 +1299,25 @@ pkv_status pkv_paged_attention_decode_q8(const pkv_q8_pool* pool, int32_t dtype,
                                      : pkv::launch_q8_decode<__nv_bfloat16>(p, pool->head_dim, s);
     if (e == cudaSuccess && w.parts > 1) e = pkv::launch_q8_merge(p, pool->head_dim, s);
     return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+size_t pkv_chunk_q8_workspace_bytes(const pkv_q8_pool* pool, int32_t num_tokens, int32_t num_seqs,
+                                    int32_t num_q_heads, int32_t max_context_len) {
+    return pool ? chunk_workspace(chunk_pool_q8(pool, PKV_F16), num_tokens, num_seqs, num_q_heads, max_context_len) : 0;
+}
+
+pkv_status pkv_paged_attention_chunk_q8(const pkv_q8_pool* pool, int32_t dtype, const void* q,
+                                        int32_t num_tokens, int32_t num_q_heads,
+                                        const int32_t* query_start, int32_t num_seqs,
+                                        const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                        const int32_t* context_lens, int32_t max_context_len,
+                                        float scale, void* out, int32_t out_dtype, void* workspace,
+                                        size_t workspace_bytes, void* stream) {
+    const pkv_status st = check_q8(pool, dtype);
+    if (st != PKV_OK) return st;
+    return run_chunk(chunk_pool_q8(pool, dtype), q, num_tokens, num_q_heads, query_start, num_seqs, block_tables,
+                     max_blocks_per_seq, context_lens, max_context_len, scale, out, out_dtype, workspace,
+                     workspace_bytes, stream);
 }
 
 pkv_status pkv_get_device_error(uint32_t* flags, void* stream) {

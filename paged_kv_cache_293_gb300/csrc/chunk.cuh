@@ -74,6 +74,7 @@
 #include <type_traits>
 
 #include "decode_mma.cuh"
+#include "q8.cuh"
 #include "umma.cuh"
 
 namespace pkv {
@@ -100,16 +101,21 @@ struct ChunkReference<__half> {
 // heads, contexts about 300: 79 us (93 with 4 rows).
 constexpr int CHUNK_FEW_ROWS = 16;
 
-template <int D>
+// Q8: pages of e4m3 values arrive in a ring of their own, and the stages hold them as numbers.
+template <int D, bool Q8>
 struct ChunkSmem {
     static constexpr int BOXES = D / 64;                  // 128-byte columns of a row
     static constexpr int BOX = 128 * 128;                 // one of a 128-row tile
     static constexpr int TILE = BOXES * BOX;              // a tile of Q, K or V
-    static constexpr int STAGES = D == 128 ? 5 : 8;
+    static constexpr int STAGES = Q8 ? (D == 128 ? 3 : 6) : (D == 128 ? 5 : 8);
+    static constexpr int RAW_STAGES = Q8 ? (D == 128 ? 4 : 8) : 0;
+    static constexpr int RAW_TILE = 128 * D;
     static constexpr int Q_OFF = 0;
     static constexpr int KV_OFF = 2 * TILE;
-    static constexpr int BAR_OFF = KV_OFF + STAGES * TILE;
-    static constexpr int NBARS = 2 * STAGES + 31;
+    static constexpr int RAW_OFF = KV_OFF + STAGES * TILE;
+    static constexpr int SCALE_OFF = RAW_OFF + RAW_STAGES * RAW_TILE;  // float [RAW_STAGES][8 copies]
+    static constexpr int BAR_OFF = SCALE_OFF + RAW_STAGES * 32;
+    static constexpr int NBARS = 2 * STAGES + 31 + 2 * RAW_STAGES;
     static constexpr int PIECE_OFF = BAR_OFF + ((NBARS * 8 + 15) / 16) * 16;
     static constexpr int STAT_OFF = PIECE_OFF + 2 * 32;  // float [2 tiles][m, l][128 rows]
     static constexpr int TMEM_SLOT_OFF = STAT_OFF + 2 * 2 * 128 * 4;
@@ -365,13 +371,58 @@ __device__ __forceinline__ bool few_rows_step(uint32_t s_t, uint32_t p_t, uint32
     return true;
 }
 
-template <typename T, int D, bool SPLIT_P>
+// Two fp16 values as 32-bit ones, times s, rounded to two of the type of the products.
+template <typename T>
+__device__ __forceinline__ uint32_t scaled_pair(uint32_t h, uint64_t s2) {
+    const float2 v = float2_of_f16x2(h);
+    float a, b;
+    unpack2(mul2(pack2(v.x, v.y), s2), a, b);
+    return Mma<T>::pack(a, b);
+}
+
+// A raw tile (128 tokens of D e4m3 values, rows behind one another) into a stage's K or V tile, by
+// four warps: 16 values a lane at a time, which become two 16-byte columns.  Eight lanes read 128
+// bytes in a row, and write eight different columns of the 128-byte swizzle (with D = 128 the lanes of
+// the second half store their odd column first).
+template <typename T, int D>
+__device__ __forceinline__ void numbers_of_tile(const unsigned char* raw, const float* scale, unsigned char* tile,
+                                                bool is_v, int w, int lane) {
+    constexpr int LANES = D / 16, ROWS = 32 / LANES;    // lanes a row, rows a warp at a time
+    constexpr int STEPS = 128 / (4 * ROWS);
+    const int m = lane % LANES, box = m / 4, col = 2 * (m % 4);
+#pragma unroll 2
+    for (int i = 0; i < STEPS; ++i) {
+        const int row = (i * 4 + w) * ROWS + lane / LANES, b = row / CHUNK_TOKENS, r = row % CHUNK_TOKENS;
+        const uint4 x = *reinterpret_cast<const uint4*>(raw + row * D + m * 16);
+        const float s = scale[b];
+        const uint64_t s2 = pack2(s, s);
+        const uint32_t in[4] = {x.x, x.y, x.z, x.w};
+        uint32_t out[8];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            uint32_t lo, hi;
+            f16x4_of_e4m3x4(in[k], lo, hi);
+            out[2 * k] = scaled_pair<T>(lo, s2);
+            out[2 * k + 1] = scaled_pair<T>(hi, s2);
+        }
+        unsigned char* const at = is_v ? tile + b * (CHUNK_TOKENS * D * 2) + box * (CHUNK_TOKENS * 128) + r * 128
+                                       : tile + box * (128 * 128) + row * 128;
+        uint4* const even = reinterpret_cast<uint4*>(at + ((col ^ (r & 7)) << 4));
+        uint4* const odd = reinterpret_cast<uint4*>(at + (((col + 1) ^ (r & 7)) << 4));
+        const uint4 lo4 = make_uint4(out[0], out[1], out[2], out[3]), hi4 = make_uint4(out[4], out[5], out[6], out[7]);
+        const bool swap = box == 1;
+        *(swap ? odd : even) = swap ? hi4 : lo4;
+        *(swap ? even : odd) = swap ? lo4 : hi4;
+    }
+}
+
+template <typename T, int D, bool SPLIT_P, bool Q8>
 __global__ void __launch_bounds__(CHUNK_THREADS, 1)
 chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
                        const __grid_constant__ CUtensorMap tmap_q32,
                        const __grid_constant__ CUtensorMap tmap_k,
                        const __grid_constant__ CUtensorMap tmap_v, const ChunkParams p) {
-    using L = ChunkSmem<D>;
+    using L = ChunkSmem<D, Q8>;
     constexpr int NS = L::STAGES, KS = D / 16;
     constexpr int KV_WARP = 8, MMA_WARP = 9, Q_WARP = 10, OUT_WARP = 12;
     constexpr int CONSUMERS = 8 + 2 + 4;  // arrivals that free a slot of the piece ring
@@ -411,6 +462,11 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
     auto stat_full = [&](int t) { return bar0 + 8 * (NB + 25 + t); };
     auto o_free = [&](int t) { return bar0 + 8 * (NB + 27 + t); };
     const uint32_t few_done = bar0 + 8 * (NB + 29), few_read = bar0 + 8 * (NB + 30);
+    // Q8: a tile of e4m3 values landed, and read
+    constexpr int NR = L::RAW_STAGES;
+    auto raw_full = [&](int st) { return bar0 + 8 * (NB + 31 + st); };
+    auto raw_empty = [&](int st) { return bar0 + 8 * (NB + 31 + NR + st); };
+    float* raw_scale = reinterpret_cast<float*>(smem + L::SCALE_OFF);
     float* stats = reinterpret_cast<float*>(smem + L::STAT_OFF);  // + 256 t: m, + 128: l
     auto is_few = [&](const ChunkPiece& x) {
         return !SPLIT_P && x.queries * G <= CHUNK_FEW_ROWS && x.kt1 > x.kt0;
@@ -422,8 +478,12 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
 
     if (threadIdx.x == 0) {
         for (int st = 0; st < NS; ++st) {
-            mbar_init(kv_full(st), 1);
+            mbar_init(kv_full(st), Q8 ? 4 : 1);
             mbar_init(kv_empty(st), 1);
+        }
+        for (int st = 0; st < NR; ++st) {
+            mbar_init(raw_full(st), 1);
+            mbar_init(raw_empty(st), 4);
         }
         for (int t = 0; t < 2; ++t) {
             mbar_init(q_full(t), 1);
@@ -508,13 +568,44 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
                     return (phys * Hkv + pc.kv_head) * B + t % B;
                 };
                 int row = row_of(pc.kt0);
+                // Q8: the scales of this lane's copy (far_row: a multiple of B, past the last page)
+                float k_scale = 0.f, v_scale = 0.f;
+                auto scales_of = [&](int row) {
+                    k_scale = v_scale = 0.f;
+                    if (row != far_row) {
+                        k_scale = __ldg(p.k_scale + row / B);
+                        v_scale = __ldg(p.v_scale + row / B);
+                    }
+                };
+                if constexpr (Q8) scales_of(row);
                 for (int kt = pc.kt0; kt < pc.kt1 && ok; ++kt) {
                     const int row_next = row_of(kt + 1);
+                    const float scale_now[2] = {k_scale, v_scale};
+                    if constexpr (Q8) scales_of(row_next);
                     int rows[NBOX];
 #pragma unroll
                     for (int b = 0; b < NBOX; ++b) rows[b] = __shfl_sync(FULL_MASK, row, b);
 #pragma unroll
                     for (int kv = 0; kv < 2; ++kv, ++it) {
+                        if constexpr (Q8) {
+                            const int st = it % NR;
+                            if (it >= NR) {
+                                ok = __all_sync(FULL_MASK, mbar_wait_short(raw_empty(st), ((it / NR) - 1) & 1));
+                                if (!ok) break;
+                            }
+                            if (lane < NBOX) raw_scale[st * NBOX + lane] = scale_now[kv];
+                            __syncwarp();  // the scales are there before the arrival that tells of the tile
+                            if (umma::elect_one()) {
+                                const uint32_t full = raw_full(st), dst = sbase + L::RAW_OFF + st * L::RAW_TILE;
+                                mbar_arrive_expect_tx(full, L::RAW_TILE);
+#pragma unroll
+                                for (int b = 0; b < NBOX; ++b)
+                                    tma_load_2d(dst + b * CHUNK_TOKENS * D, kv == 0 ? &tmap_k : &tmap_v, 0, rows[b],
+                                                full, policy);
+                            }
+                            __syncwarp();
+                            continue;
+                        }
                         const int st = it % NS;
                         if (it >= NS) {
                             ok = __all_sync(FULL_MASK, mbar_wait_short(kv_empty(st), ((it / NS) - 1) & 1));
@@ -547,7 +638,11 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
                 idx = __shfl_sync(FULL_MASK, next, 0);
             }
             // the CTA must not end with copies still landing in its shared memory
-            for (uint32_t k = it > NS ? it - NS : 0; k < it; ++k) mbar_wait_short(kv_full(k % NS), (k / NS) & 1);
+            if constexpr (Q8) {
+                for (uint32_t k = it > NR ? it - NR : 0; k < it; ++k) mbar_wait_short(raw_full(k % NR), (k / NR) & 1);
+            } else {
+                for (uint32_t k = it > NS ? it - NS : 0; k < it; ++k) mbar_wait_short(kv_full(k % NS), (k / NS) & 1);
+            }
         } else if (warp == Q_WARP) {
             // ---- query tiles
             int loads[2] = {0, 0}, fews = 0;  // copies into each tile, pieces with few rows
@@ -766,8 +861,46 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
         int even = 0, odd = 0;    // steps of pieces with one tile so far: the phases of pv_step
         int outs = 0, twos = 0;   // pieces so far, those with two tiles: of stat_full, pv_done
         int fews = 0;             // pieces with few rows: of few_done
-        ChunkPiece pc;
-        for (int i = 0; next_piece(i, pc); ++i) {
+        // Q8: these warps also make the stages' numbers, of a piece before its output and of the next
+        // piece's first step too, so that its scores need not wait for that output.  (A stage that is
+        // waited for here becomes free by products that no output is needed for.)
+        uint32_t made = 0;  // stages so far
+        auto make_stages = [&](int count) -> bool {
+            for (int k = 0; k < count; ++k, ++made) {
+                const int from = made % (NR > 0 ? NR : 1), st = made % NS;
+                if (!__all_sync(FULL_MASK, mbar_wait_short(raw_full(from), (made / (NR > 0 ? NR : 1)) & 1))) return false;
+                if (made >= NS && !__all_sync(FULL_MASK, mbar_wait_short(kv_empty(st), (made / NS - 1) & 1)))
+                    return false;
+                // (even ones are K's)
+                numbers_of_tile<T, D>(smem + L::RAW_OFF + from * L::RAW_TILE, raw_scale + from * 8,
+                                      smem + L::KV_OFF + st * L::TILE, made & 1, w, lane);
+                umma::fence_smem_to_async();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(kv_full(st));
+                    mbar_arrive(raw_empty(from));
+                }
+            }
+            return true;
+        };
+        constexpr int AHEAD = 2;
+        ChunkPiece pc, following;
+        bool any = Q8 && next_piece(0, following);
+        int ahead = 0;  // stages of the next piece that are made already
+        for (int i = 0;; ++i) {
+            if constexpr (Q8) {
+                if (!any) break;
+                pc = following;
+                ok = make_stages(2 * max(pc.kt1 - pc.kt0, 0) - ahead);
+                if (!ok) break;
+                any = next_piece(i + 1, following);
+                if (!ok) break;
+                ahead = any ? min(AHEAD, 2 * max(following.kt1 - following.kt0, 0)) : 0;
+                ok = make_stages(ahead);
+                if (!ok) break;
+            } else if (!next_piece(i, pc)) {
+                break;
+            }
             const int n = max(pc.kt1 - pc.kt0, 0);
             const bool two = pc.queries > QPT, direct = pc.part_row < 0, few = is_few(pc);
             if (!two) {
@@ -1098,18 +1231,32 @@ inline bool encode_query_map(CUtensorMap* map, const void* q, int T_, int Hq, in
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <typename T, int D, bool SPLIT_P>
+// An 8-bit pool seen as [N * Hkv * B rows][D bytes]: boxes of 16 rows, as they lie.
+inline bool encode_q8_map(CUtensorMap* map, const void* base, long long rows, int D) {
+    auto enc = tensor_map_encoder();
+    if (!enc) return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)D, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)D};
+    const cuuint32_t box[2] = {(cuuint32_t)D, (cuuint32_t)CHUNK_TOKENS};
+    const cuuint32_t estr[2] = {1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename T, int D, bool SPLIT_P, bool Q8>
 cudaError_t launch_chunk_tds(const ChunkPlanParams& plan, const ChunkParams& p, const ChunkTensors& x,
                              cudaStream_t stream) {
-    constexpr int SMEM = ChunkSmem<D>::BYTES;
+    constexpr int SMEM = ChunkSmem<D, Q8>::BYTES;
     const long long rows = (long long)p.num_blocks * p.num_kv_heads * p.block_size;
     const int G = p.group;
     CUtensorMap tq, tq32, tk, tv;
     if (!encode_query_map<T>(&tq, x.q, x.num_tokens, p.num_q_heads, D, G, 128 / G) ||
         !encode_query_map<T>(&tq32, x.q, x.num_tokens, p.num_q_heads, D, G, G <= 32 ? 32 / G : 1) ||
-        !encode_pool_map<T>(&tk, x.k_pool, rows, D) || !encode_pool_map_3d<T>(&tv, x.v_pool, rows, D))
+        !(Q8 ? encode_q8_map(&tk, x.k_pool, rows, D) : encode_pool_map<T>(&tk, x.k_pool, rows, D)) ||
+        !(Q8 ? encode_q8_map(&tv, x.v_pool, rows, D) : encode_pool_map_3d<T>(&tv, x.v_pool, rows, D)))
         return cudaErrorNotSupported;
-    auto kernel = chunk_attention_kernel<T, D, SPLIT_P>;
+    auto kernel = chunk_attention_kernel<T, D, SPLIT_P, Q8>;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
@@ -1135,16 +1282,16 @@ cudaError_t launch_chunk_tds(const ChunkPlanParams& plan, const ChunkParams& p, 
     return cudaLaunchKernelEx(&cfg, kernel, tq, tq32, tk, tv, p);
 }
 
-template <typename T>
+template <typename T, bool Q8>
 cudaError_t launch_chunk_impl(const ChunkPlanParams& plan, const ChunkParams& p, const ChunkTensors& x,
                               cudaStream_t stream) {
     const bool f32_out = p.out_dtype == PKV_F32;
     if (p.head_dim == 64)
-        return f32_out ? launch_chunk_tds<T, 64, true>(plan, p, x, stream)
-                       : launch_chunk_tds<T, 64, false>(plan, p, x, stream);
+        return f32_out ? launch_chunk_tds<T, 64, true, Q8>(plan, p, x, stream)
+                       : launch_chunk_tds<T, 64, false, Q8>(plan, p, x, stream);
     if (p.head_dim == 128)
-        return f32_out ? launch_chunk_tds<T, 128, true>(plan, p, x, stream)
-                       : launch_chunk_tds<T, 128, false>(plan, p, x, stream);
+        return f32_out ? launch_chunk_tds<T, 128, true, Q8>(plan, p, x, stream)
+                       : launch_chunk_tds<T, 128, false, Q8>(plan, p, x, stream);
     return cudaErrorInvalidValue;
 }
 

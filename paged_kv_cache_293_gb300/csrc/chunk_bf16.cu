@@ -6,7 +6,7 @@ namespace pkv {
 template <>
 cudaError_t launch_chunk<__nv_bfloat16>(const ChunkPlanParams& plan, const ChunkParams& p, const ChunkTensors& x,
                                         cudaStream_t stream) {
-    return launch_chunk_impl<__nv_bfloat16>(plan, p, x, stream);
+    return launch_chunk_impl<__nv_bfloat16, false>(plan, p, x, stream);
 }
 
 }  // namespace pkv

@@ -6,7 +6,7 @@ namespace pkv {
 template <>
 cudaError_t launch_chunk<__half>(const ChunkPlanParams& plan, const ChunkParams& p, const ChunkTensors& x,
                                  cudaStream_t stream) {
-    return launch_chunk_impl<__half>(plan, p, x, stream);
+    return launch_chunk_impl<__half, false>(plan, p, x, stream);
 }
 
 }  // namespace pkv

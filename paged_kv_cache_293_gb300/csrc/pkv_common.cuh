@@ -198,6 +198,8 @@ struct ChunkParams {
     float* part_l;
     float* part_o;
     float* totals;      // [ctas][2 tiles][D / 4 + 1][128 rows][4], where a piece may pass CHUNK_SUM_STEPS
+    const float* k_scale;  // 8-bit pools: [num_blocks][num_kv_heads]
+    const float* v_scale;
     unsigned int* err;
 };
 
@@ -460,6 +462,9 @@ cudaError_t launch_rope_write(const RopeParams& p, int32_t dtype, cudaStream_t s
 cudaError_t launch_chunk_plan(const ChunkPlanParams& p, int64_t max_tiles, cudaStream_t stream);
 template <typename T>
 cudaError_t launch_chunk(const ChunkPlanParams& plan, const ChunkParams& p, const ChunkTensors& x, cudaStream_t stream);
+// the same over pools held in 8 bits
+template <typename T>
+cudaError_t launch_chunk_q8(const ChunkPlanParams& plan, const ChunkParams& p, const ChunkTensors& x, cudaStream_t stream);
 cudaError_t launch_chunk_merge(const ChunkParams& p, int ctas, cudaStream_t stream);
 cudaError_t launch_copy_blocks(const pkv_pool& src, const pkv_pool& dst, const int32_t* pairs,
                                int32_t num_pairs, unsigned int* err, cudaStream_t stream);

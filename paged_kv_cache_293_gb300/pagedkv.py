@@ -94,6 +94,9 @@ _SIGS = {
     "pkv_decode_q8_workspace_bytes": (_sz, [_PQ, _i32, _i32, _i32, _i32, _i32]),
     "pkv_paged_attention_decode_q8": (_i32, [_PQ, _i32, _P, _i32, _i32, _i32, _P, _i32, _P, _i32,
                                              _f32, _P, _i32, _i32, _P, _sz, _P]),
+    "pkv_chunk_q8_workspace_bytes": (_sz, [_PQ, _i32, _i32, _i32, _i32]),
+    "pkv_paged_attention_chunk_q8": (_i32, [_PQ, _i32, _P, _i32, _i32, _P, _i32, _P, _i32, _P, _i32,
+                                            _f32, _P, _i32, _P, _sz, _P]),
     "pkv_status_str": (ctypes.c_char_p, [_i32]),
     "pkv_version": (_i32, []),
     "pkv_set_decode_engine": (_i32, [_i32]),
@@ -565,6 +568,11 @@ def make_q8_pool(k_pool, v_pool, k_scale, v_scale):
                        shape[0], shape[2], shape[1], shape[3])
 
 
+def _q8_shape(k_pool):
+    N, Hkv, B, D = k_pool.shape
+    return pkv_q8_pool(None, None, None, None, N, B, Hkv, D)
+
+
 def _q8_pool_of(k_pool, v_pool, k_scale, v_scale, device):
     for t in (k_pool, v_pool, k_scale, v_scale):
         if t.get_device() != device:
@@ -601,10 +609,8 @@ def pkv_qk_norm_rope_write_q8(q, k, v, k_pool, v_pool, k_scale, v_scale, positio
 
 def pkv_decode_q8_workspace_bytes(k_pool, num_seqs, num_queries, num_q_heads, max_context_len,
                                   partition_size=0):
-    N, Hkv, B, D = k_pool.shape
-    return lib.pkv_decode_q8_workspace_bytes(pkv_q8_pool(None, None, None, None, N, B, Hkv, D), num_seqs,
-                                             num_queries, num_q_heads, int(max_context_len),
-                                             int(partition_size))
+    return lib.pkv_decode_q8_workspace_bytes(_q8_shape(k_pool), num_seqs, num_queries, num_q_heads,
+                                             int(max_context_len), int(partition_size))
 
 
 def pkv_paged_attention_decode_q8(q, k_pool, v_pool, k_scale, v_scale, block_tables, context_lens, scale,
@@ -631,6 +637,34 @@ def pkv_paged_attention_decode_q8(q, k_pool, v_pool, k_scale, v_scale, block_tab
         ws_bytes, _raw_stream(stream, dev))
     if st != PKV_OK:
         raise PagedKVError(st, "pkv_paged_attention_decode_q8")
+
+
+def pkv_chunk_q8_workspace_bytes(k_pool, num_tokens, num_seqs, num_q_heads, max_context_len):
+    return lib.pkv_chunk_q8_workspace_bytes(_q8_shape(k_pool), num_tokens, num_seqs, num_q_heads,
+                                            int(max_context_len))
+
+
+def pkv_paged_attention_chunk_q8(q, k_pool, v_pool, k_scale, v_scale, query_start, block_tables,
+                                 context_lens, scale, out, max_context_len, workspace, stream=None):
+    """pkv_paged_attention_chunk over float8_e4m3fn pools with a float32 scale a page."""
+    T, Hq, D = q.shape
+    S, M = block_tables.shape
+    dev = _current_device(q, "q")
+    pool = _q8_pool_of(k_pool, v_pool, k_scale, v_scale, dev)
+    if pool.head_dim != D:
+        raise ValueError("q and the pools must have the same head_dim")
+    dt = _half_type(q, "q")
+    _expect(dev, q.dtype, (q, "q", T * Hq * D))
+    _expect(dev, out.dtype, (out, "out", T * Hq * D))
+    _expect(dev, torch.int32, (query_start, "query_start", S + 1),
+            (block_tables, "block_tables", S * M), (context_lens, "context_lens", S))
+    _expect(dev, workspace.dtype, (workspace, "workspace", workspace.numel()))
+    st = lib.pkv_paged_attention_chunk_q8(
+        pool, dt, q.data_ptr(), T, Hq, query_start.data_ptr(), S, block_tables.data_ptr(), M,
+        context_lens.data_ptr(), int(max_context_len), scale, out.data_ptr(), _DTYPE[out.dtype],
+        workspace.data_ptr(), workspace.nbytes, _raw_stream(stream, dev))
+    if st != PKV_OK:
+        raise PagedKVError(st, "pkv_paged_attention_chunk_q8")
 
 
 def pkv_get_device_error(stream=None, device=None):
