@@ -8,15 +8,17 @@
 // work per byte is twice that of a 16-bit cache and the kernel is laid out to need few
 // instructions a byte.  Both products run on mma.sync.m16n8k16 in fp16, which holds every e4m3
 // value: scores^T [16 tokens x 8] = K . Q^T and O^T [D x 8] = V^T . P^T, the 8 columns being the
-// (query, head) pairs of one kv head, and the operands go from global memory to registers:
-//   K  lane (g, c) = (lane / 4, lane % 4) reads 16 bytes of tokens g and g + 8; the order of a
-//      product's D terms is free, so the 4 values of a word are a lane's terms of one k step
+// (query, head) pairs of one kv head.  Each warp brings 16 tokens at a time into a ring of its own by
+// cp.async (a page's 16 tokens are D / 8 rows of 128 bytes, their 16-byte columns turned so that
+// the reads below meet no bank twice) and takes the operands from there as they lie:
+//   K  lane (g, c) = (lane / 4, lane % 4) reads D / 4 bytes in a row of tokens g and g + 8; the order of
+//      a product's D terms is free, so the 4 values of a word are a lane's terms of one k step
 //      (and Q is laid out alike);
 //   V  lane (g, c) reads the D / 8 bytes from g D / 8 on of tokens 2c, 2c + 1, 2c + 8, 2c + 9: the
 //      four tokens that its part of a k step takes, whose bytes one prmt a pair brings together.
-// No shared memory, no barrier in the loop, and the pages of a warp's next 16 tokens are on their
-// way while it works on these.  A page's scale a_b goes into the factor that its scores are
-// multiplied with anyway, and c_b into the sum of its O into the row's, in 32 bits.
+// No barrier in the loop: a warp's lanes wait for their own copies, then for one another.  A page's
+// scale a_b goes into the factor that its scores are multiplied with anyway, and c_b into the sum of its
+// O into the row's, in 32 bits.
 // Each row's reference follows its maximum and is raised only where a score exceeds it by more
 // than 15 in base 2 (it is set 7 below the maximum), so no lane asks the others for theirs but then.
 // P enters its product in fp16 (weights from 2^-21 of the largest on with 11 bits, none off by more
@@ -31,17 +33,14 @@ namespace pkv {
 constexpr int Q8_WARPS = 4;
 constexpr float Q8_BELOW = 7.f, Q8_RAISE = 15.f;
 
-__device__ __forceinline__ uint4 ldg_stream(const void* p) {
-    uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
-    return v;
+// 16 bytes global -> shared past L1, asynchronously; groups of copies and the wait for all but N.
+__device__ __forceinline__ void cp_async16_stream(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
-__device__ __forceinline__ uint2 ldg_stream8(const void* p) {
-    uint2 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
-    return v;
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait_but() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 // The 8 x 8 matrix of 16-bit values whose row lane / 4 this lane has a pair of, transposed.
@@ -57,41 +56,50 @@ template <> __device__ __forceinline__ float2 pair_to_floats<__nv_bfloat16>(uint
     return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
 }
 
-// The words of 16 tokens that a lane holds.
+// 16 tokens of one pool in shared memory: rows of 128 bytes, one token (D = 128) or two (D = 64), the
+// 16-byte column j of row r at column j ^ turn(r).
 template <int D>
-struct Q8Tokens {
-    static constexpr int KW = D / 16;  // words of a token's key: 16 bytes per 64 elements
-    static constexpr int VW = D / 32;  // words of a token's value
-    uint32_t k[2][KW];
-    uint32_t v[4][VW];
-    __device__ __forceinline__ void load_k(const uint8_t* page, int g, int c) {
-#pragma unroll
-        for (int r = 0; r < 2; ++r)
-#pragma unroll
-            for (int i = 0; i < D / 64; ++i) {
-                const uint4 w = ldg_stream(page + (g + 8 * r) * D + 64 * i + 16 * c);
-                k[r][4 * i] = w.x; k[r][4 * i + 1] = w.y; k[r][4 * i + 2] = w.z; k[r][4 * i + 3] = w.w;
-            }
+struct Q8Tile {
+    static constexpr int BYTES = CHUNK_TOKENS * D, COLUMNS = BYTES / 16;
+    __device__ __forceinline__ static int at(int row, int col) {
+        return row * 128 + ((col ^ (D == 128 ? row & 7 : 2 * (row & 3))) << 4);
     }
-    __device__ __forceinline__ void load_v(const uint8_t* page, int g, int c) {
+    // word w of a lane's part of token t: of a key, bytes c D / 4 + 4 w .. + 3
+    __device__ __forceinline__ static void key(const unsigned char* tile, int t, int c, uint32_t (&k)[D / 16]) {
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const uint8_t* at = page + (2 * c + (r & 1) + 8 * (r >> 1)) * D + g * (D / 8);
-            if constexpr (D == 128) {
-                const uint4 w = ldg_stream(at);
-                v[r][0] = w.x; v[r][1] = w.y; v[r][2] = w.z; v[r][3] = w.w;
-            } else {
-                const uint2 w = ldg_stream8(at);
-                v[r][0] = w.x; v[r][1] = w.y;
-            }
+        for (int i = 0; i < D / 64; ++i) {
+            const int col = D == 128 ? 2 * c + i : 4 * (t & 1) + c;
+            const uint4 w = *reinterpret_cast<const uint4*>(tile + at(D == 128 ? t : t >> 1, col));
+            k[4 * i] = w.x; k[4 * i + 1] = w.y; k[4 * i + 2] = w.z; k[4 * i + 3] = w.w;
+        }
+    }
+    // of a value, bytes g D / 8 + 4 w .. + 3
+    __device__ __forceinline__ static void value(const unsigned char* tile, int t, int g, uint32_t (&v)[D / 32]) {
+        if constexpr (D == 128) {
+            const uint4 w = *reinterpret_cast<const uint4*>(tile + at(t, g));
+            v[0] = w.x; v[1] = w.y; v[2] = w.z; v[3] = w.w;
+        } else {
+            const uint2 w = *reinterpret_cast<const uint2*>(tile + at(t >> 1, 4 * (t & 1) + (g >> 1)) + 8 * (g & 1));
+            v[0] = w.x; v[1] = w.y;
         }
     }
 };
 
+// Stages of a warp's ring, and CTAs per SM that the registers are held to.
+constexpr int Q8_STAGES = 3, Q8_CTAS = 4;
+template <int D>
+constexpr int q8_smem_bytes() {
+    return Q8_WARPS * Q8_STAGES * 2 * Q8Tile<D>::BYTES;
+}
+
 template <typename T, int D, bool SPLIT_P>
-__global__ void __launch_bounds__(Q8_WARPS * 32) q8_decode_kernel(const Q8DecodeParams p) {
-    constexpr int KS = D / 16, NW = Q8_WARPS;
-    __shared__ float red[NW][8][D + 2];
+__global__ void __launch_bounds__(Q8_WARPS * 32, Q8_CTAS) q8_decode_kernel(const Q8DecodeParams p) {
+    constexpr int KS = D / 16, NW = Q8_WARPS, NS = Q8_STAGES;
+    using Tile = Q8Tile<D>;
+    extern __shared__ __align__(128) unsigned char q8_smem[];
+    __shared__ float2 stage_scale[NW][NS];
+    float(*red)[8][D + 2] = reinterpret_cast<float(*)[8][D + 2]>(q8_smem);  // [NW], once the rings are done with
+    static_assert(NW * 8 * (D + 2) * 4 <= q8_smem_bytes<D>(), "the warps' results fit into the rings");
     const int Hkv = p.num_kv_heads, Hq = p.num_q_heads, G = Hq / Hkv, NQ = p.num_queries, B = p.block_size;
     const int kvh = blockIdx.x % Hkv, col0 = (blockIdx.x / Hkv) * 8, s = blockIdx.y;
     const int part = gridDim.z - 1 - blockIdx.z;  // the last pieces, which few contexts reach, first
@@ -118,12 +126,14 @@ __global__ void __launch_bounds__(Q8_WARPS * 32) q8_decode_kernel(const Q8Decode
 
     // this warp's pages, 32 steps at a time: lane i has the page of step i, and its scales
     const int32_t* bt_row = p.block_tables + (size_t)s * p.max_blocks_per_seq;
+    const int shift = B == 32 ? 5 : 4;  // B is 16 or 32
+    auto token_of = [&](int i) { return tok0 + (warp + NW * i) * CHUNK_TOKENS; };
     int page = -1;
     float ka = 0.f, va = 0.f;
     auto look_up = [&](int i) {
         page = -1;
         if (i >= n_my) return;
-        const int phys = __ldg(bt_row + (tok0 + (warp + NW * i) * CHUNK_TOKENS) / B);
+        const int phys = __ldg(bt_row + (token_of(i) >> shift));
         if ((unsigned)phys >= (unsigned)p.num_blocks) {
             set_error(p.err, PKV_DEVERR_BLOCK_ID);
             return;
@@ -133,21 +143,32 @@ __global__ void __launch_bounds__(Q8_WARPS * 32) q8_decode_kernel(const Q8Decode
         ka = __ldg(p.k_scale + at);
         va = __ldg(p.v_scale + at);
     };
-    // where step i's 16 tokens lie in the pools (the first block where there is none: read, not used)
-    auto place = [&](int i) -> size_t {
-        const int phys = max(__shfl_sync(FULL_MASK, page, i & 31), 0);
-        return (((size_t)phys * Hkv + kvh) * B + (warp + NW * i) * CHUNK_TOKENS % B) * D;
+    unsigned char* const ring = q8_smem + warp * NS * 2 * Tile::BYTES;
+    unsigned there = 0;  // stages that hold a page
+    auto issue = [&](int i) {
+        if (i < n_my) {
+            if ((i & 31) == 0) look_up(i + lane);
+            const int phys = __shfl_sync(FULL_MASK, page, i & 31), st = i % NS;
+            const float a_b = __shfl_sync(FULL_MASK, ka, i & 31), c_b = __shfl_sync(FULL_MASK, va, i & 31);
+            there = phys >= 0 ? there | (1u << st) : there & ~(1u << st);
+            if (lane == 0) stage_scale[warp][st] = make_float2(a_b, c_b);
+            if (phys >= 0) {
+                const size_t at = ((((size_t)phys * Hkv + kvh) << shift) + (token_of(i) & (B - 1))) * D;
+                const uint32_t dst = smem_addr(ring + st * 2 * Tile::BYTES);
+#pragma unroll
+                for (int j = lane; j < Tile::COLUMNS; j += 32) {
+                    const uint32_t to = dst + Tile::at(j >> 3, j & 7);
+                    cp_async16_stream(to, p.k_pool + at + 16 * j);
+                    cp_async16_stream(to + Tile::BYTES, p.v_pool + at + 16 * j);
+                }
+            }
+        }
+        cp_async_commit();
     };
-    look_up(lane);
-    Q8Tokens<D> x;
-    size_t at = 0;
-    if (n_my > 0) {
-        at = place(0);
-        x.load_k(p.k_pool + at, g, c);
-        x.load_v(p.v_pool + at, g, c);
-    }
+#pragma unroll
+    for (int i = 0; i < NS - 1; ++i) issue(i);
 
-    // Q^T: column g's terms 64 i + 16 c + 4 w .. + 3 for k step 4 i + w, in fp16.  bf16 rows are
+    // Q^T: column g's terms c D / 4 + 4 w .. + 3 for k step w, in fp16.  bf16 rows are
     // scaled by the power of two that brings their largest below 2^14, which keeps their bits.
     uint32_t qb[KS][2];
     float q_inv = 1.f;  // of column g
@@ -155,12 +176,10 @@ __global__ void __launch_bounds__(Q8_WARPS * 32) q8_decode_kernel(const Q8Decode
         const T* src = static_cast<const T*>(p.q) + row_of(g < ncols ? g : 0) * D;
         uint32_t w[D / 8];
 #pragma unroll
-        for (int i = 0; i < D / 64; ++i)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const uint4 v = __ldg(reinterpret_cast<const uint4*>(src + 64 * i + 16 * c + 8 * h));
-                w[8 * i + 4 * h] = v.x; w[8 * i + 4 * h + 1] = v.y; w[8 * i + 4 * h + 2] = v.z; w[8 * i + 4 * h + 3] = v.w;
-            }
+        for (int i = 0; i < D / 32; ++i) {
+            const uint4 v = __ldg(reinterpret_cast<const uint4*>(src + c * (D / 4)) + i);
+            w[4 * i] = v.x; w[4 * i + 1] = v.y; w[4 * i + 2] = v.z; w[4 * i + 3] = v.w;
+        }
         if constexpr (std::is_same<T, __nv_bfloat16>::value) {
             float top = 0.f;
 #pragma unroll
@@ -200,40 +219,49 @@ __global__ void __launch_bounds__(Q8_WARPS * 32) q8_decode_kernel(const Q8Decode
     for (int i = 0; i < KS; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
 
     for (int i = 0; i < n_my; ++i) {
-        const int t0 = tok0 + (warp + NW * i) * CHUNK_TOKENS;
-        const bool there = __shfl_sync(FULL_MASK, page, i & 31) >= 0;
-        const float a_b = __shfl_sync(FULL_MASK, ka, i & 31), c_b = __shfl_sync(FULL_MASK, va, i & 31);
-        if ((i & 31) == 31) look_up(i + 1 + lane);
-        const bool more = i + 1 < n_my;
-        if (more) at = place(i + 1);
+        const int t0 = token_of(i), st = i % NS;
+        cp_async_wait_but<NS - 2>();
+        __syncwarp();  // every lane's copies of this stage are there, and all are done with the stage before
+        issue(i + NS - 1);
+        const unsigned char* const k_tile = ring + st * 2 * Tile::BYTES;
+        const float2 scales = stage_scale[warp][st];
+        const float a_b = scales.x, c_b = scales.y;
+        const bool here = (there >> st) & 1;
 
         float sc[4] = {0.f, 0.f, 0.f, 0.f};
+        {
+            uint32_t k0[KS], k1[KS];
+            Tile::key(k_tile, g, c, k0);
+            Tile::key(k_tile, g + 8, c, k1);
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-            uint32_t a0, a1, a2, a3;
-            f16x4_of_e4m3x4(x.k[0][ks], a0, a2);
-            f16x4_of_e4m3x4(x.k[1][ks], a1, a3);
-            Mma<__half>::run(sc, a0, a1, a2, a3, qb[ks][0], qb[ks][1]);
+            for (int ks = 0; ks < KS; ++ks) {
+                uint32_t a0, a1, a2, a3;
+                f16x4_of_e4m3x4(k0[ks], a0, a2);
+                f16x4_of_e4m3x4(k1[ks], a1, a3);
+                Mma<__half>::run(sc, a0, a1, a2, a3, qb[ks][0], qb[ks][1]);
+            }
         }
-        if (more) x.load_k(p.k_pool + at, g, c);
+        uint32_t v[4][D / 32];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) Tile::value(k_tile + Tile::BYTES, 2 * c + (r & 1) + 8 * (r >> 1), g, v[r]);
 
         float pr[4];  // scores in base 2: token g + 8 (j / 2), column 2 c + j % 2
         float over = -INFINITY;
 #pragma unroll
         for (int j = 0; j < 4; ++j) pr[j] = sc[j] * (f[j & 1] * a_b);
-        if (!there || t0 + CHUNK_TOKENS > tok_end || __any_sync(FULL_MASK, t0 + CHUNK_TOKENS > lim_all)) {
+        if (!here || t0 + CHUNK_TOKENS > tok_end || __any_sync(FULL_MASK, t0 + CHUNK_TOKENS > lim_all)) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int t = t0 + g + 8 * (j >> 1);
-                if (!there || t >= tok_end || t >= lim[j & 1]) pr[j] = -INFINITY;
+                if (!here || t >= tok_end || t >= lim[j & 1]) pr[j] = -INFINITY;
             }
             // values of tokens that no row sees may be anything, and 0 * NaN is not 0
-            const int seen = there ? tok_end - t0 : 0;
+            const int seen = here ? tok_end - t0 : 0;
 #pragma unroll
             for (int r = 0; r < 4; ++r)
                 if (2 * c + (r & 1) + 8 * (r >> 1) >= seen) {
 #pragma unroll
-                    for (int w = 0; w < Q8Tokens<D>::VW; ++w) x.v[r][w] = 0u;
+                    for (int w = 0; w < D / 32; ++w) v[r][w] = 0u;
                 }
         }
 #pragma unroll
@@ -275,12 +303,12 @@ __global__ void __launch_bounds__(Q8_WARPS * 32) q8_decode_kernel(const Q8Decode
         }
         // rows of O^T's tile 2 w + h: elements g D / 8 + 4 w + 2 h and the next one
 #pragma unroll
-        for (int w = 0; w < Q8Tokens<D>::VW; ++w)
+        for (int w = 0; w < D / 32; ++w)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 uint32_t a0, a1, a2, a3;
-                f16x4_of_e4m3x4(__byte_perm(x.v[0][w], x.v[1][w], h == 0 ? 0x5140 : 0x7362), a0, a1);
-                f16x4_of_e4m3x4(__byte_perm(x.v[2][w], x.v[3][w], h == 0 ? 0x5140 : 0x7362), a2, a3);
+                f16x4_of_e4m3x4(__byte_perm(v[0][w], v[1][w], h == 0 ? 0x5140 : 0x7362), a0, a1);
+                f16x4_of_e4m3x4(__byte_perm(v[2][w], v[3][w], h == 0 ? 0x5140 : 0x7362), a2, a3);
                 float sum[4] = {0.f, 0.f, 0.f, 0.f};
                 Mma<__half>::run(sum, a0, a1, a2, a3, b0, b1);
                 if (SPLIT_P) Mma<__half>::run(sum, a0, a1, a2, a3, r0, r1);
@@ -288,8 +316,8 @@ __global__ void __launch_bounds__(Q8_WARPS * 32) q8_decode_kernel(const Q8Decode
 #pragma unroll
                 for (int j = 0; j < 4; ++j) od[j] = fmaf(sum[j], c_b, od[j]);
             }
-        if (more) x.load_v(p.v_pool + at, g, c);
     }
+    __syncthreads();  // the rings are done with (no copy is in flight: the last waits were for all that were issued)
 
     // ---- the warps' results together
 #pragma unroll
@@ -339,25 +367,33 @@ __global__ void __launch_bounds__(Q8_WARPS * 32) q8_decode_kernel(const Q8Decode
     }
 }
 
-template <typename T>
-cudaError_t launch_q8_decode_impl(const Q8DecodeParams& p, int head_dim, cudaStream_t stream) {
+template <typename T, int D, bool SPLIT_P>
+cudaError_t launch_q8_decode_tds(const Q8DecodeParams& p, cudaStream_t stream) {
+    constexpr int SMEM = q8_smem_bytes<D>();
+    auto kernel = q8_decode_kernel<T, D, SPLIT_P>;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    static std::atomic<bool> configured[64];  // per device; setting it twice is harmless
+    if (dev >= 64 || !configured[dev].load(std::memory_order_acquire)) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+        if (e != cudaSuccess) return e;
+        if (dev < 64) configured[dev].store(true, std::memory_order_release);
+    }
     const int cols = p.num_queries * (p.num_q_heads / p.num_kv_heads);
     const dim3 grid((unsigned)(p.num_kv_heads * ((cols + 7) / 8)), (unsigned)p.num_seqs, (unsigned)p.max_parts);
-    const bool split = p.out_dtype == PKV_F32;
-    if (head_dim == 64) {
-        if (split)
-            q8_decode_kernel<T, 64, true><<<grid, Q8_WARPS * 32, 0, stream>>>(p);
-        else
-            q8_decode_kernel<T, 64, false><<<grid, Q8_WARPS * 32, 0, stream>>>(p);
-    } else if (head_dim == 128) {
-        if (split)
-            q8_decode_kernel<T, 128, true><<<grid, Q8_WARPS * 32, 0, stream>>>(p);
-        else
-            q8_decode_kernel<T, 128, false><<<grid, Q8_WARPS * 32, 0, stream>>>(p);
-    } else {
-        return cudaErrorInvalidValue;
-    }
+    kernel<<<grid, Q8_WARPS * 32, SMEM, stream>>>(p);
     return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_q8_decode_impl(const Q8DecodeParams& p, int head_dim, cudaStream_t stream) {
+    const bool split = p.out_dtype == PKV_F32;
+    if (head_dim == 64)
+        return split ? launch_q8_decode_tds<T, 64, true>(p, stream) : launch_q8_decode_tds<T, 64, false>(p, stream);
+    if (head_dim == 128)
+        return split ? launch_q8_decode_tds<T, 128, true>(p, stream) : launch_q8_decode_tds<T, 128, false>(p, stream);
+    return cudaErrorInvalidValue;
 }
 
 }  // namespace pkv
