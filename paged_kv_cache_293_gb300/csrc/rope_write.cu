@@ -196,9 +196,11 @@ __global__ void __launch_bounds__((WARPS + 1) * 32) rope_stream_kernel(const Rop
                 const uint32_t dst = ring0 + st * stage_bytes;
                 mbar_arrive_expect_tx(full(st), q_bytes + 2 * kv_bytes + 4 * R);
                 bulk_g2s(dst, static_cast<const T*>(p.q) + t * p.q_stride, q_bytes, full(st), policy);
-                bulk_g2s(dst + q_bytes, static_cast<const T*>(p.k) + t * p.k_stride, kv_bytes, full(st), policy);
-                bulk_g2s(dst + q_bytes + kv_bytes, static_cast<const T*>(p.v) + t * p.v_stride, kv_bytes, full(st),
-                         policy);
+                if (kv_bytes > 0) {  // (none: q alone, beside q8_write.cu's keys and values)
+                    bulk_g2s(dst + q_bytes, static_cast<const T*>(p.k) + t * p.k_stride, kv_bytes, full(st), policy);
+                    bulk_g2s(dst + q_bytes + kv_bytes, static_cast<const T*>(p.v) + t * p.v_stride, kv_bytes,
+                             full(st), policy);
+                }
                 if (R > 0)
                     bulk_g2s(dst + q_bytes + 2 * kv_bytes, p.cos_sin + (size_t)pos * R, 4 * R, full(st), policy);
             };
