@@ -8,12 +8,11 @@
 // any other scale but where numbers are 2^-15 of the page's largest; and when a page that is
 // partly filled needs a larger scale, its rows only change their exponents.
 //
-// The tokens of one block stand behind one another in a call: a run, at most a block long.  A CTA
-// has some heads of the runs that begin in a few rows of the call, a warp (two for pages of 32 x 128)
-// the keys or values of one head: as many rows as a block has tokens are whole in its registers, 64
-// numbers a lane at most, be they one run or many short ones.  It takes each run's largest |x|, then
-// rounds.  Lane j looks after row j of that window: its slot, its run and that run's scale.  The warps of
-// a CTA share the window's rows of the rotation table in shared memory.
+// The tokens of one block stand behind one another in a call: a run, at most a block long.  A window is
+// as many rows of the call as a block has tokens: one run or several short ones, whole.  A warp (two
+// for pages of 32 x 128) has the keys or values of one head of a window in its registers, 64 numbers a
+// lane at most: it takes each run's largest |x|, then rounds.  Lane j looks after row j: its slot, its
+// run and that run's scale.
 #include <cfloat>
 #include <type_traits>
 
@@ -26,9 +25,11 @@ namespace {
 
 constexpr int Q8_Q_ROWS = 2;      // rows of q per group of lanes, in flight together
 constexpr int Q8_KV_WARPS = 8;
-// From this many tokens on q goes through rope_write.cu's kernels, a launch more.
+// From this many tokens on q goes through rope_write.cu's kernels and k and v are streamed, a launch
+// more.
 constexpr int Q8_MANY_TOKENS = 512;
-// Rows whose runs a CTA looks for.
+// Rows whose runs a CTA looks for: few while that does not make more CTAs than fit the SMs.
+constexpr int Q8_CTAS = 456;
 constexpr int Q8_FEW_ROWS = 4, Q8_GROUP_ROWS = 16;
 // What a scale reads as while the run that changes it is at work: a NaN that nothing else makes.
 constexpr uint32_t Q8_LOCKED = 0xffc5a5c5u;
@@ -39,22 +40,16 @@ struct LanePart {
     bool turns;
 };
 
-template <int P>
-__device__ __forceinline__ void load_angles(const float* row, int R, int l, int V, float (&c)[2 * P], float (&s)[2 * P]) {
-    row += l * (V / 2);
-#pragma unroll
-    for (int i = 0; i < 2 * P; i += 2) {
-        const float2 x = *reinterpret_cast<const float2*>(row + i);
-        const float2 y = *reinterpret_cast<const float2*>(row + R / 2 + i);
-        c[i] = x.x; c[i + 1] = x.y;
-        s[i] = y.x; s[i + 1] = y.y;
-    }
+__device__ __forceinline__ void load_angles(const float* row, int R, int l, float (&c)[4], float (&s)[4]) {
+    const float4 x = *reinterpret_cast<const float4*>(row + l * 4), y = *reinterpret_cast<const float4*>(row + R / 2 + l * 4);
+    c[0] = x.x; c[1] = x.y; c[2] = x.z; c[3] = x.w;
+    s[0] = y.x; s[1] = y.y; s[2] = y.z; s[3] = y.w;
 }
 
 // The q rows of token t, by the whole CTA.
 template <typename T, int D, bool INTERLEAVED>
 __device__ __forceinline__ void turn_queries(const RopeParams& p, const LanePart& at, int t) {
-    constexpr int V = 8, LPR = D / V, P = 2;
+    constexpr int LPR = D / 8, P = 2;
     const int groups = blockDim.x / LPR, group = threadIdx.x / LPR, Hq = p.num_q_heads, R = p.rotary_dim;
     const int pos = p.positions[t];
     const long long slot = p.slot_mapping[t];
@@ -65,7 +60,7 @@ __device__ __forceinline__ void turn_queries(const RopeParams& p, const LanePart
     }
     if (threadIdx.x == 0 && slot >= (long long)p.num_blocks * p.block_size) set_error(p.err, PKV_DEVERR_SLOT);
     float c[2 * P], s[2 * P];
-    if (at.turns) load_angles<P>(p.cos_sin + (size_t)pos * R, R, at.l, V, c, s);
+    if (at.turns) load_angles(p.cos_sin + (size_t)pos * R, R, at.l, c, s);
     Turn<P> m;
     make_turn<T, INTERLEAVED, P>(m, p.q_weight, at.lo, at.hi, at.turns, c, s);
     const T* src = static_cast<const T*>(p.q) + t * p.q_stride;
@@ -90,6 +85,45 @@ __device__ __forceinline__ void turn_queries(const RopeParams& p, const LanePart
     }
 }
 
+// A lane's chunks a and b of a key, times the weights wa and wb (none: without a norm) and turned by c and
+// s; the factor that the norm asks for besides.  The sum of squares takes all lanes of the warp.
+template <typename T, int D, bool INTERLEAVED>
+__device__ __forceinline__ float turn_key(const uint2& a2, const uint2& b2, bool norm, const uint64_t (&wa)[2],
+                                          const uint64_t (&wb)[2], bool turns, const float (&c)[4], const float (&s)[4],
+                                          float eps, uint64_t (&x)[2], uint64_t (&y)[2]) {
+    Chunk8<T>::unpack(a2, x);
+    Chunk8<T>::unpack(b2, y);
+    float r = 1.f;
+    if (norm) {
+        float u, v;
+        unpack2(fma2(y[1], y[1], fma2(x[1], x[1], fma2(y[0], y[0], mul2(x[0], x[0])))), u, v);
+        float ss = u + v;
+#pragma unroll
+        for (int o = D / 16; o >= 1; o >>= 1) ss += __shfl_xor_sync(FULL_MASK, ss, o);
+        r = rsqrtf(ss * (1.f / D) + eps);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            x[i] = mul2(x[i], wa[i]);
+            y[i] = mul2(y[i], wb[i]);
+        }
+    }
+    if (turns) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint64_t u = x[i], v = y[i];
+            if (INTERLEAVED) {  // pair i of a turns by c[i], pair i of b by c[2 + i]
+                x[i] = fma2(swap2(u), pack2(-s[i], s[i]), mul2(u, pack2(c[i], c[i])));
+                y[i] = fma2(swap2(v), pack2(-s[2 + i], s[2 + i]), mul2(v, pack2(c[2 + i], c[2 + i])));
+            } else {
+                const uint64_t cc = pack2(c[2 * i], c[2 * i + 1]);
+                x[i] = fma2(v, pack2(-s[2 * i], -s[2 * i + 1]), mul2(u, cc));
+                y[i] = fma2(u, pack2(s[2 * i], s[2 * i + 1]), mul2(v, cc));
+            }
+        }
+    }
+    return r;
+}
+
 // Rounds a row of a page to a larger scale, a lane's 8 values.
 __device__ __forceinline__ void round_again(uint2* at, float ratio) {
     const uint2 w = *at;
@@ -106,233 +140,457 @@ __device__ __forceinline__ void round_again(uint2* at, float ratio) {
     *at = make_uint2(e4m3x4_of_floats(x[0], x[1], x[2], x[3]), e4m3x4_of_floats(x[4], x[5], x[6], x[7]));
 }
 
+// What lane j knows of row j of a window that begins at row t of the call.
+struct Window {
+    int blk, row, pos;    // block (-1: no key and value there), place in it, position
+    int lead, last;       // the first and the last row of its run
+    int lead_row;         // the first one's place in the block
+    unsigned run;         // all lanes: the rows that are written, and those that begin a run
+    unsigned leaders;
+};
+
+// The runs that begin in rows [t, t_end) and are whole in the B rows from t on; t moves to the first that
+// is not.  A run: tokens whose slots advance as their rows do, in one block.  `first`: what lies before
+// t is not known yet.  Whole warps.
+template <int B>
+__device__ __forceinline__ Window find_window(const RopeParams& p, int& t, int t_end, bool first, bool reports) {
+    const int lane = threadIdx.x & 31;
+    const long long num_slots = (long long)p.num_blocks * B;
+    auto look = [&](int i, int& row, int& pos) -> int {
+        pos = row = -1;
+        if (i < 0 || i >= p.num_tokens) return -1;
+        pos = p.positions[i];
+        const long long slot = p.slot_mapping[i];
+        if (pos < 0 || (p.rotary_dim > 0 && pos >= p.max_position) || slot < 0 || slot >= num_slots) return -1;
+        row = (int)(slot & (B - 1));
+        return (int)(slot / B);
+    };
+    Window w;
+    w.blk = look(t + lane, w.row, w.pos);
+    const unsigned below = (1u << lane) - 1, here = 1u << lane;
+    const unsigned there = __ballot_sync(FULL_MASK, w.blk >= 0);
+    // the nearest row before that holds a token: in the window, or (for its first token) before it
+    int d = (there & below) != 0 ? lane - (31 - __clz(there & below)) : 0;
+    int blk_d = __shfl_sync(FULL_MASK, w.blk, lane - d), row_d = __shfl_sync(FULL_MASK, w.row, lane - d);
+    if (first && there != 0) {
+        int unused, row_b;
+        const int blk_b = look(t - 1 - lane, row_b, unused);
+        const unsigned near = __ballot_sync(FULL_MASK, blk_b >= 0);
+        const int k = near != 0 ? __ffs(near) - 1 : 0, j = __ffs(there) - 1;
+        const int blk_k = __shfl_sync(FULL_MASK, blk_b, k), row_k = __shfl_sync(FULL_MASK, row_b, k);
+        if (lane == j && near != 0) {
+            d = j + k + 1;
+            blk_d = blk_k;
+            row_d = row_k;
+        }
+    }
+    const bool same = w.blk >= 0 && d > 0 && d <= max(w.row, 1) && blk_d == w.blk;
+    const bool follows = same && row_d == w.row - d;
+    w.leaders = __ballot_sync(FULL_MASK, w.blk >= 0 && !follows);
+    const unsigned refused = __ballot_sync(FULL_MASK, same && !follows);  // a slot twice, or in falling order
+    // (rows before the first leader are of a run that began before t, another CTA's)
+    const unsigned upto = w.leaders & (below | here), later = w.leaders & ~(below | here);
+    const int lead = upto != 0 ? 31 - __clz(upto) : -1;
+    w.lead = max(lead, 0);
+    w.last = later != 0 ? __ffs(later) - 2 : 31;
+    w.lead_row = __shfl_sync(FULL_MASK, w.row, w.lead);
+    // where the row's run is known to end: before the next one, or with its block
+    const bool known = later != 0 || lead + B - w.lead_row <= 32;
+    const bool member = w.blk >= 0 && lead >= 0;
+    // runs that have a row past those held here, or may go on past the window, wait for the next one
+    // (a run that begins at row 0 is always whole)
+    const unsigned over = __ballot_sync(FULL_MASK, member && (lane >= B || !known));
+    const unsigned late = __ballot_sync(FULL_MASK, lead >= 0 && t + lead >= t_end);
+    const int stop_over = over != 0 ? __shfl_sync(FULL_MASK, lead, __ffs(over) - 1) : 32;
+    const int stop = min(stop_over, late != 0 ? __ffs(late) - 1 : 32);
+    w.run = __ballot_sync(FULL_MASK, member && lead < stop && !((refused >> w.lead) & 1));
+    if (reports && (refused & ((stop < 32 ? 1u << stop : 0u) - 1)) != 0) set_error(p.err, PKV_DEVERR_SLOT);
+    t = stop < 32 ? t + stop : min(t + 32, t_end);
+    return w;
+}
+
+// How a window's rows lie in a warp.
+template <int D, int B>
+struct Rows {
+    static constexpr int V = 8, LPR = D / V;    // elements per lane, lanes per row
+    static constexpr int GPW = 32 / LPR;        // rows a warp at a time
+    static constexpr int W = B * D > 16 * 128 ? (B * D) / (16 * 128) : 1;  // warps a page
+    static constexpr int IT = B / (GPW * W);    // rows a lane
+    static_assert(IT * 8 <= 64, "numbers a lane");
+};
+
+// One row of a head's keys or values: by times f are its numbers.
+template <typename T, int D, bool INTERLEAVED>
+__device__ __forceinline__ void make_row(bool is_k, const uint2& a, const uint2& b, const float* angles, int R, bool norm,
+                                         const uint64_t (&wa)[2], const uint64_t (&wb)[2], const LanePart& at, float eps,
+                                         uint64_t (&f)[4], float& by) {
+    uint64_t x[2], y[2];
+    by = 1.f;
+    if (is_k) {
+        float c[4], s[4];
+        if (at.turns) load_angles(angles, R, at.l, c, s);
+        by = turn_key<T, D, INTERLEAVED>(a, b, norm, wa, wb, at.turns, c, s, eps, x, y);
+    } else {
+        Chunk8<T>::unpack(a, x);
+        Chunk8<T>::unpack(b, y);
+    }
+    f[0] = x[0];
+    f[1] = x[1];
+    f[2] = y[0];
+    f[3] = y[1];
+}
+
+// The largest of m and the sizes of a lane's eight numbers of a row (a NaN is left out).
+__device__ __forceinline__ float largest(const uint64_t (&f)[4], float m = 0.f) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        float a, b;
+        unpack2(f[k], a, b);
+        asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(m), "f"(a), "f"(b));
+    }
+    return m;
+}
+
+// A lane's eight numbers of a row, times x, into its places of the row.
+__device__ __forceinline__ void store_row(uint8_t* out, const LanePart& at, const uint64_t (&f)[4], float x) {
+    const uint64_t x2 = pack2(x, x);
+    float v[8];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) unpack2(mul2(f[k], x2), v[2 * k], v[2 * k + 1]);
+    *reinterpret_cast<uint32_t*>(out + at.lo) = e4m3x4_of_floats(v[0], v[1], v[2], v[3]);
+    *reinterpret_cast<uint32_t*>(out + at.hi) = e4m3x4_of_floats(v[4], v[5], v[6], v[7]);
+}
+
+// The scales of a window's pages and their values, from the rows' numbers by[i] f[i] of one head.  `had`:
+// lane j's page's scale before, where row j begins a run; tops and hads: this page's, in shared memory,
+// which two warps of a page share behind barrier `bar`.
+template <int D, int B>
+__device__ __forceinline__ void store_window(const Window& w, uint64_t (&f)[Rows<D, B>::IT][4],
+                                             float (&by)[Rows<D, B>::IT], int part, const LanePart& at, bool real,
+                                             uint8_t* pool, float* scales, unsigned page, uint32_t had, float* tops,
+                                             uint32_t* hads, int bar, unsigned int* err) {
+    using L = Rows<D, B>;
+    constexpr int IT = L::IT, GPW = L::GPW, W = L::W, LPR = L::LPR;
+    const int lane = threadIdx.x & 31, sub = lane / LPR, l = at.l;
+    auto none = [&](int i) { return ((w.run >> ((part * IT + i) * GPW)) & ((1u << GPW) - 1)) == 0; };
+    auto mine = [&](int i) { return ((w.run >> ((part * IT + i) * GPW + sub)) & 1) != 0; };
+    const bool single = __popc(w.leaders & w.run) == 1;  // one run: nothing differs from row to row
+    const bool in_run = (w.run >> lane) & 1, leads = in_run && w.lead == lane;
+    float most = 0.f;
+#pragma unroll
+    for (int i = 0; i < IT; ++i) {
+        const float m = by[i] * largest(f[i]);
+        if (mine(i)) most = fmaxf(most, m);
+    }
+    if (__any_sync(FULL_MASK, most > FLT_MAX)) {  // infinities are left out too, and become NaN
+        most = 0.f;
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                float a, b;
+                unpack2(f[i][k], a, b);
+                if (!(fabsf(a) * by[i] <= FLT_MAX)) a = __int_as_float(0x7fffffff);
+                if (!(fabsf(b) * by[i] <= FLT_MAX)) b = __int_as_float(0x7fffffff);
+                f[i][k] = pack2(a, b);
+            }
+            if (mine(i)) most = fmaxf(most, by[i] * largest(f[i]));
+        }
+    }
+    float top = most;
+    if (single) {
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(FULL_MASK, top, o));
+        if (W > 1 && lane == 0) tops[part] = top;
+    } else {
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+            if (none(i)) continue;
+            float m = fmaxf(by[i] * largest(f[i]), 0.f);
+#pragma unroll
+            for (int o = LPR / 2; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(FULL_MASK, m, o));
+            if (l == 0) tops[(part * IT + i) * GPW + sub] = m;
+        }
+    }
+    if constexpr (W > 1) {
+        if (part == 0) hads[lane] = had;
+        asm volatile("bar.sync %0, %1;" ::"r"(bar), "n"(32 * W) : "memory");
+        had = hads[lane];
+    } else {
+        __syncwarp();
+    }
+    if (single) {
+#pragma unroll
+        for (int k = 0; k < W; ++k)
+            if (W > 1) top = fmaxf(top, tops[k]);
+    } else {
+        top = in_run ? tops[lane] : 0.f;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const float x = __shfl_up_sync(FULL_MASK, top, o);
+            if (lane - o >= w.lead) top = fmaxf(top, x);
+        }
+        top = __shfl_sync(FULL_MASK, top, w.last);
+    }
+    had = __shfl_sync(FULL_MASK, had, w.lead);
+    const bool ok = real && in_run && had != Q8_LOCKED;
+    if (real && leads && !ok) set_error(err, PKV_DEVERR_SLOT);
+    const float old = __uint_as_float(had), need = q8_scale_for(top);
+    const float s = w.lead_row > 0 ? fmaxf(old, need) : need;  // (a scale that is NaN counts as none)
+    const float inv = 1.f / s;
+    unsigned grown = __ballot_sync(FULL_MASK, ok && leads && w.lead_row > 0 && s > old);
+    for (; grown != 0; grown &= grown - 1) {
+        const int j = __ffs(grown) - 1, row0 = __shfl_sync(FULL_MASK, w.row, j);
+        const unsigned rows_j = __ballot_sync(FULL_MASK, in_run && w.lead == j);
+        const float ratio = __shfl_sync(FULL_MASK, old / s, j);
+        uint8_t* const codes = pool + (size_t)__shfl_sync(FULL_MASK, page, j) * (B * D);
+        for (int r = part * GPW + sub; r < B; r += W * GPW) {
+            const int k = j + r - row0;
+            if (k < j || k > 31 || !((rows_j >> k) & 1)) round_again(reinterpret_cast<uint2*>(codes + r * D) + l, ratio);
+        }
+    }
+    const unsigned stored = __ballot_sync(FULL_MASK, ok);
+    if (single) {  // rows behind one another in one page
+        const int j = __ffs(w.run & w.leaders) - 1;
+        const float x = __shfl_sync(FULL_MASK, inv, j);
+        uint8_t* const out = pool + (size_t)__shfl_sync(FULL_MASK, page, j) * (B * D) +
+                             (__shfl_sync(FULL_MASK, w.row, j) - j + part * IT * GPW + sub) * D;
+#pragma unroll
+        for (int i = 0; i < IT; ++i)
+            if ((stored >> ((part * IT + i) * GPW + sub)) & 1) store_row(out + i * GPW * D, at, f[i], x * by[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+            const int r0 = (part * IT + i) * GPW, r = r0 + sub;
+            if (((stored >> r0) & ((1u << GPW) - 1)) == 0) continue;
+            const float x = __shfl_sync(FULL_MASK, inv, r) * by[i];
+            uint8_t* const out =
+                pool + (size_t)__shfl_sync(FULL_MASK, page, r) * (B * D) + __shfl_sync(FULL_MASK, w.row, r) * D;
+            if ((stored >> r) & 1) store_row(out, at, f[i], x);
+        }
+    }
+    if (ok && leads && part == 0) atomicExch(reinterpret_cast<unsigned int*>(scales + page), __float_as_uint(s));
+}
+
+template <typename T, bool INTERLEAVED>
+__device__ __forceinline__ LanePart lane_part(int l, int R) {
+    LanePart at;
+    at.l = l;
+    at.turns = l * 8 < R;
+    at.lo = INTERLEAVED || !at.turns ? l * 8 : l * 4;
+    at.hi = INTERLEAVED || !at.turns ? at.lo + 4 : at.lo + R / 2;
+    return at;
+}
+
+template <typename T>
+__device__ __forceinline__ void load_weights(const void* w, const LanePart& at, uint64_t (&wa)[2], uint64_t (&wb)[2]) {
+    wa[0] = wa[1] = wb[0] = wb[1] = 0;
+    if (w == nullptr) return;
+    Chunk8<T>::unpack(__ldg(reinterpret_cast<const uint2*>(static_cast<const T*>(w) + at.lo)), wa);
+    Chunk8<T>::unpack(__ldg(reinterpret_cast<const uint2*>(static_cast<const T*>(w) + at.hi)), wb);
+}
+
 }  // namespace
 
-// The first q_ctas CTAs have the q rows of a token each; of the others, every `heads` have the runs that
-// begin in `rows` rows.
+// Few tokens, whose time is one row's way through the kernel: the first q_ctas CTAs have the q rows of a
+// token each; of the others, every `heads` have the runs that begin in `rows` rows, and a warp one page's
+// rows, all in flight.  The warps share the window's rows of the rotation table in shared memory.
 template <typename T, int D, int B, bool INTERLEAVED>
 __global__ void __launch_bounds__(Q8_KV_WARPS * 32, 2)
 q8_write_kernel(const RopeParams p, float* k_scale, float* v_scale, int q_ctas, int heads, int rows) {
-    constexpr int V = 8, LPR = D / V, P = 2;    // elements per lane, lanes per row
-    constexpr int GPW = 32 / LPR;               // rows a warp at a time
-    constexpr int W = B * D > 32 * 64 ? (B * D) / (16 * 128) : 1;  // warps a page
-    constexpr int IT = B / (GPW * W);           // rows a lane
-    static_assert(IT * 8 <= 64 && Q8_KV_WARPS % W == 0, "numbers a lane");
+    using L = Rows<D, B>;
+    constexpr int IT = L::IT, GPW = L::GPW, W = L::W;
     __shared__ __align__(16) float angles[B * D];
     __shared__ float tops[Q8_KV_WARPS / W][32];
     __shared__ uint32_t hads[Q8_KV_WARPS / W][32];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane / LPR, l = lane % LPR;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane / L::LPR;
     const int Hkv = p.num_kv_heads, R = p.rotary_dim;
-    LanePart at;
-    at.l = l;
-    at.turns = l * V < R;
-    at.lo = INTERLEAVED || !at.turns ? l * V : l * (V / 2);
-    at.hi = INTERLEAVED || !at.turns ? at.lo + V / 2 : at.lo + R / 2;
+    const LanePart at = lane_part<T, INTERLEAVED>(lane % L::LPR, R);
     if ((int)blockIdx.x < q_ctas) {
         turn_queries<T, D, INTERLEAVED>(p, at, blockIdx.x);
         return;
     }
-    const int cta = (int)blockIdx.x - q_ctas;
-    const int u = cta % heads * (Q8_KV_WARPS / W) + warp / W, part = warp % W;
-    const int first_u = u - warp / W;
+    const int cta = (int)blockIdx.x - q_ctas, part = warp % W, unit = warp / W;
+    const int first_u = cta % heads * (Q8_KV_WARPS / W), u = first_u + unit;
     const bool real = u < 2 * Hkv, is_k = u < Hkv;
     const int head = real ? (is_k ? u : u - Hkv) : 0;
-    const long long num_slots = (long long)p.num_blocks * B;
-    const bool norm = p.k_weight != nullptr;
     float* const scales = is_k ? k_scale : v_scale;
     uint8_t* const pool = static_cast<uint8_t*>(is_k ? p.k_pool : p.v_pool);
-
-    // slot and position of a row; slot -1: no key and value there
-    auto look = [&](int i, int& pos) -> long long {
-        pos = -1;
-        if (i < 0 || i >= p.num_tokens) return -1;
-        pos = p.positions[i];
-        const long long slot = p.slot_mapping[i];
-        return pos < 0 || (R > 0 && pos >= p.max_position) || slot < 0 || slot >= num_slots ? -1 : slot;
-    };
-    // A run: tokens whose slots advance as their rows do, in one block.  Row 0 of the window is t, lane j
-    // has row j.
-    const int t_end = min(cta / heads * rows + rows, p.num_tokens);
-    bool first = true;
-    for (int t = cta / heads * rows; t < t_end;) {
-        int pos, unused;
-        const long long slot = look(t + lane, pos);
-        const long long blk = slot >= 0 ? slot / B : -1;
-        const int row = (int)(slot - blk * B);
-        const unsigned below = (1u << lane) - 1;
-        const unsigned there = __ballot_sync(FULL_MASK, slot >= 0);
-        // the nearest row before that holds a token: in the window, or (for its first token) before it
-        int d = (there & below) != 0 ? lane - (31 - __clz(there & below)) : 0;
-        long long other = __shfl_sync(FULL_MASK, slot, lane - d);
-        if (first && there != 0) {
-            const int j = __ffs(there) - 1;
-            const long long before = look(t - 1 - lane, unused);
-            const unsigned near = __ballot_sync(FULL_MASK, before >= 0);
-            const long long nearest = __shfl_sync(FULL_MASK, before, near != 0 ? __ffs(near) - 1 : 0);
-            if (lane == j && near != 0) {
-                d = j + __ffs(near);
-                other = nearest;
-            }
-        }
-        const bool same = slot >= 0 && d > 0 && d <= max(row, 1) && other / B == blk;
-        const bool follows = same && other == slot - d;
-        const unsigned leaders = __ballot_sync(FULL_MASK, slot >= 0 && !follows);
-        const unsigned refused = __ballot_sync(FULL_MASK, same && !follows);  // a slot twice, or in falling order
-        // rows from the first leader on; those of a run that began before t are another CTA's
-        const unsigned upto = leaders & (below | (1u << lane));
-        const int lead = upto != 0 ? 31 - __clz(upto) : -1;
-        const unsigned later = leaders & ~(below | (1u << lane));
-        // where the row's run is known to end: before the next one, or with its block
-        const int lead_row = __shfl_sync(FULL_MASK, row, max(lead, 0));
-        const bool known = later != 0 || lead + B - lead_row <= 32;
-        const bool member = slot >= 0 && lead >= 0;
-        // runs that have a row past those held here, or may go on past the window, wait for the next one
-        const unsigned over = __ballot_sync(FULL_MASK, member && (lane >= B || !known));
-        const unsigned late = __ballot_sync(FULL_MASK, lead >= 0 && t + lead >= t_end);
-        const int stop_over = over != 0 ? __shfl_sync(FULL_MASK, lead, __ffs(over) - 1) : 32;
-        const int stop_late = late != 0 ? __ffs(late) - 1 : 32;
-        const int stop = min(stop_over, stop_late);  // (a run that begins at row 0 is always whole)
-        const unsigned run = __ballot_sync(FULL_MASK, member && lead < stop && !((refused >> max(lead, 0)) & 1));
-        if (refused & ((stop < 32 ? 1u << stop : 0u) - 1) && threadIdx.x == 0) set_error(p.err, PKV_DEVERR_SLOT);
+    const long long stride = is_k ? p.k_stride : p.v_stride;
+    uint64_t wa[2], wb[2];
+    load_weights<T>(p.k_weight, at, wa, wb);
+    const int t_begin = cta / heads * rows, t_end = min(t_begin + rows, p.num_tokens);
+    for (int t = t_begin; t < t_end;) {
         const int t_now = t;
-        t = stop < 32 ? t + stop : t + 32 > t_end ? t_end : t + 32;
-        first = false;
-        if (run == 0) continue;
-        const int n = 32 - __clz(run);  // at most B
-        const bool in_run = (run >> lane) & 1, leads = in_run && lead == lane;
-
+        const Window w = find_window<B>(p, t, t_end, t_now == t_begin, threadIdx.x == 0);
+        if (w.run == 0) continue;
         // the scale of each run's page, and no other run at that page from here on
-        const size_t page = (size_t)max(blk, 0ll) * Hkv + head;
+        const unsigned page = (unsigned)max(w.blk, 0) * Hkv + head;  // (pages are 1 KB or more)
         uint32_t had = 0;
-        if (real && leads && part == 0) had = atomicExch(reinterpret_cast<unsigned int*>(scales + page), Q8_LOCKED);
-
+        if (real && part == 0 && (w.run & w.leaders) >> lane & 1)
+            had = atomicExch(reinterpret_cast<unsigned int*>(scales + page), Q8_LOCKED);
         // this lane's chunks of rows (part * IT + i) * GPW + sub
         uint2 a[IT], b[IT];
-        const T* const base = (is_k ? static_cast<const T*>(p.k) + t_now * p.k_stride
-                                    : static_cast<const T*>(p.v) + t_now * p.v_stride) + (size_t)head * D;
-        const long long stride = is_k ? p.k_stride : p.v_stride;
+        const T* const base = static_cast<const T*>(is_k ? p.k : p.v) + (t_now + part * IT * GPW + sub) * stride + head * D;
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
-            const int r = (part * IT + i) * GPW + sub;
             a[i] = b[i] = make_uint2(0u, 0u);
-            if ((run >> r) & 1) {
-                a[i] = __ldcs(reinterpret_cast<const uint2*>(base + r * stride + at.lo));
-                b[i] = __ldcs(reinterpret_cast<const uint2*>(base + r * stride + at.hi));
+            if ((w.run >> ((part * IT + i) * GPW + sub)) & 1) {
+                a[i] = __ldcs(reinterpret_cast<const uint2*>(base + i * GPW * stride + at.lo));
+                b[i] = __ldcs(reinterpret_cast<const uint2*>(base + i * GPW * stride + at.hi));
             }
         }
-        // the rows of the rotation table, for all warps
         if (R > 0 && first_u < Hkv) {
-            for (int r = warp; r < n; r += Q8_KV_WARPS) {
-                const int pr = __shfl_sync(FULL_MASK, pos, r);
-                if ((run >> r) & 1)
+            for (int r = warp; r < B; r += Q8_KV_WARPS) {
+                const int pr = __shfl_sync(FULL_MASK, w.pos, r);
+                if ((w.run >> r) & 1)
                     for (int i = lane * 4; i < R; i += 128)
                         *reinterpret_cast<float4*>(angles + r * D + i) =
                             __ldg(reinterpret_cast<const float4*>(p.cos_sin + (size_t)pr * R + i));
             }
         }
         __syncthreads();
-
-        float f[IT][8], most = 0.f;
-#pragma unroll
-        for (int i = 0; i < IT; ++i) {
-            const int r0 = (part * IT + i) * GPW, r = r0 + sub;
-            if (((run >> r0) & ((1u << GPW) - 1)) == 0) {  // the whole warp
-#pragma unroll
-                for (int k = 0; k < 8; ++k) f[i][k] = 0.f;
-                continue;
-            }
-            uint64_t x[P], y[P];
-            if (is_k) {
-                float c[2 * P], s[2 * P];
-                if (at.turns) load_angles<P>(angles + r * D, R, l, V, c, s);
-                Turn<P> m;
-                make_turn<T, INTERLEAVED, P>(m, p.k_weight, at.lo, at.hi, at.turns, c, s);
-                turn_values<T, D, INTERLEAVED, P>(m, norm, at.turns, p.eps, a[i], b[i], x, y);
-            } else {
-                Chunk8<T>::unpack(a[i], x);
-                Chunk8<T>::unpack(b[i], y);
-            }
-            unpack2(x[0], f[i][0], f[i][1]);
-            unpack2(x[1], f[i][2], f[i][3]);
-            unpack2(y[0], f[i][4], f[i][5]);
-            unpack2(y[1], f[i][6], f[i][7]);
-            if (!((run >> r) & 1)) {  // made from no angles
-#pragma unroll
-                for (int k = 0; k < 8; ++k) f[i][k] = 0.f;
-            }
-#pragma unroll
-            for (int k = 0; k < 8; ++k) most = fmaxf(most, fabsf(f[i][k]));  // (a NaN is left out)
-        }
-        if (__any_sync(FULL_MASK, most > FLT_MAX)) {  // infinities are left out too, and become NaN
-#pragma unroll
-            for (int i = 0; i < IT; ++i)
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    if (!(fabsf(f[i][k]) <= FLT_MAX)) f[i][k] = __int_as_float(0x7fffffff);
-        }
-        // each row's largest, then each run's
-        float top = 0.f;
+        uint64_t f[IT][4];
+        float by[IT];
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
             const int r0 = (part * IT + i) * GPW;
-            if (((run >> r0) & ((1u << GPW) - 1)) == 0) continue;
-            float m = 0.f;
-#pragma unroll
-            for (int k = 0; k < 8; ++k) m = fmaxf(m, fabsf(f[i][k]));
-#pragma unroll
-            for (int o = LPR / 2; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(FULL_MASK, m, o));
-            if (l == 0) tops[warp / W][r0 + sub] = m;
-        }
-        if constexpr (W > 1) {
-            if (part == 0) hads[warp / W][lane] = had;
-            __syncthreads();
-            had = hads[warp / W][lane];
-        } else {
-            __syncwarp();
-        }
-        if (in_run) top = tops[warp / W][lane];
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const float m = __shfl_up_sync(FULL_MASK, top, o);
-            if (lane - o >= lead) top = fmaxf(top, m);  // (lead >= 0 where it matters)
-        }
-        top = __shfl_sync(FULL_MASK, top, later != 0 ? __ffs(later) - 2 : 31);
-        had = __shfl_sync(FULL_MASK, had, max(lead, 0));
-        const bool ok = real && in_run && had != Q8_LOCKED;
-        if (real && in_run && !ok && leads) set_error(p.err, PKV_DEVERR_SLOT);
-        const float old = __uint_as_float(had), need = q8_scale_for(top);
-        const float s = lead_row > 0 ? fmaxf(old, need) : need;  // (a scale that is NaN counts as none)
-        const float inv = 1.f / s, ratio = old / s;
-        unsigned grown = __ballot_sync(FULL_MASK, ok && leads && lead_row > 0 && s > old);
-        for (; grown != 0; grown &= grown - 1) {
-            const int j = __ffs(grown) - 1, row0 = __shfl_sync(FULL_MASK, row, j);
-            const unsigned rows_j = __ballot_sync(FULL_MASK, in_run && lead == j);
-            const float ratio_j = __shfl_sync(FULL_MASK, ratio, j);
-            uint8_t* const codes = pool + __shfl_sync(FULL_MASK, (unsigned long long)page, j) * (B * D);
-            for (int r = part * GPW + sub; r < B; r += W * GPW) {
-                const int k = j + r - row0;
-                if (k < j || k > 31 || !((rows_j >> k) & 1))
-                    round_again(reinterpret_cast<uint2*>(codes + r * D) + l, ratio_j);
+            if (((w.run >> r0) & ((1u << GPW) - 1)) != 0) {  // (rows that are not of a run: made from anything, not used)
+                make_row<T, D, INTERLEAVED>(is_k, a[i], b[i], angles + (r0 + sub) * D, R, p.k_weight != nullptr, wa, wb, at,
+                                            p.eps, f[i], by[i]);
+            } else {
+                by[i] = 0.f;
+                f[i][0] = f[i][1] = f[i][2] = f[i][3] = 0;
             }
         }
-        const unsigned stored = __ballot_sync(FULL_MASK, ok);
-        const unsigned long long place = ((unsigned long long)page * B + row) * D;
-#pragma unroll
-        for (int i = 0; i < IT; ++i) {
-            const int r0 = (part * IT + i) * GPW, r = r0 + sub;
-            if (((stored >> r0) & ((1u << GPW) - 1)) == 0) continue;
-            const float by = __shfl_sync(FULL_MASK, inv, r);
-            uint8_t* const out = pool + __shfl_sync(FULL_MASK, place, r);
-            if ((stored >> r) & 1) {
-                *reinterpret_cast<uint32_t*>(out + at.lo) =
-                    e4m3x4_of_floats(f[i][0] * by, f[i][1] * by, f[i][2] * by, f[i][3] * by);
-                *reinterpret_cast<uint32_t*>(out + at.hi) =
-                    e4m3x4_of_floats(f[i][4] * by, f[i][5] * by, f[i][6] * by, f[i][7] * by);
-            }
-        }
-        if (ok && leads && part == 0)
-            atomicExch(reinterpret_cast<unsigned int*>(scales + page), __float_as_uint(s));
+        store_window<D, B>(w, f, by, part, at, real, pool, scales, page, had, tops[unit], hads[unit], 1 + unit, p.err);
         __syncthreads();  // before the next window's rows of the table and maxima
+    }
+}
+
+// Many tokens: CTAs that stay.  Up to 16 warps have a page each, window by window, and their next rows
+// and the table's are on their way while they are at these.  The last warp, whose values take less work
+// than keys, also finds the windows, two ahead.
+constexpr int Q8_STREAM_WARPS = 16, Q8_FOUND = 4;
+
+template <int D, int B>
+struct StreamSmem {
+    static constexpr int ROWS = B / Rows<D, B>::W * D * 2;   // a warp's rows of a window
+    static constexpr int ANGLES = B * D * 4;
+    __host__ __device__ static constexpr int bytes(int warps) { return 2 * (warps * ROWS + ANGLES); }
+};
+
+template <typename T, int D, int B, bool INTERLEAVED>
+__global__ void __launch_bounds__(Q8_STREAM_WARPS * 32, 1)
+q8_stream_kernel(const RopeParams p, float* k_scale, float* v_scale, int warps, int slices, int rows) {
+    using L = Rows<D, B>;
+    using S = StreamSmem<D, B>;
+    constexpr int IT = L::IT, GPW = L::GPW, W = L::W, CH = D / 8;  // 16-byte columns of a row
+    extern __shared__ __align__(128) unsigned char stream_smem[];
+    struct Found {
+        int t;
+        unsigned run, leaders;
+        int blk[32], row[32], pos[32], lead[32], last[32], lead_row[32];
+    };
+    __shared__ Found found[Q8_FOUND];
+    __shared__ float tops[Q8_STREAM_WARPS / W][32];
+    __shared__ uint32_t hads[Q8_STREAM_WARPS / W][32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane / L::LPR;
+    const int Hkv = p.num_kv_heads, R = p.rotary_dim;
+    const int t_begin = (int)blockIdx.x / slices * rows, t_end = min(t_begin + rows, p.num_tokens);
+    const int first_u = (int)blockIdx.x % slices * (warps / W);
+    float* const angles = reinterpret_cast<float*>(stream_smem + 2 * warps * S::ROWS);
+
+    int t = t_begin;
+    auto find = [&](int i) {
+        Found& x = found[i % Q8_FOUND];
+        Window w;
+        w.run = 0;
+        int t_now = t;
+        while (t < t_end && w.run == 0) {
+            t_now = t;
+            w = find_window<B>(p, t, t_end, t_now == t_begin, lane == 0);
+        }
+        if (w.run != 0) {
+            x.blk[lane] = w.blk; x.row[lane] = w.row; x.pos[lane] = w.pos;
+            x.lead[lane] = w.lead; x.last[lane] = w.last; x.lead_row[lane] = w.lead_row;
+        }
+        if (lane == 0) {
+            x.t = t_now;
+            x.run = w.run;
+            x.leaders = w.leaders;
+        }
+        __syncwarp();
+    };
+    const LanePart at = lane_part<T, INTERLEAVED>(lane % L::LPR, R);
+    const int part = warp % W, unit = warp / W, u = first_u + unit;
+    const bool real = u < 2 * Hkv, is_k = u < Hkv;
+    const int head = real ? (is_k ? u : u - Hkv) : 0;
+    float* const scales = is_k ? k_scale : v_scale;
+    uint8_t* const pool = static_cast<uint8_t*>(is_k ? p.k_pool : p.v_pool);
+    const long long stride = is_k ? p.k_stride : p.v_stride;
+    const T* const rows_in = static_cast<const T*>(is_k ? p.k : p.v) + head * D;
+    uint64_t wa[2], wb[2];
+    load_weights<T>(p.k_weight, at, wa, wb);
+    unsigned char* const stages = stream_smem + warp * 2 * S::ROWS;
+    auto bring = [&](int i) {  // of window i, this warp's rows and its share of the table's
+        const Found& x = found[i % Q8_FOUND];
+        const unsigned run = x.run;
+        const T* const from = rows_in + x.t * stride;
+#pragma unroll
+        for (int k = 0; k < IT; ++k) {
+            const int r0 = k * GPW + sub, r = part * IT * GPW + r0;
+            if (real && ((run >> r) & 1))
+                cp_async16(smem_addr(stages + (i & 1) * S::ROWS + (r0 * CH + at.l) * 16), from + r * stride + at.l * 8);
+        }
+        if (R > 0 && first_u < Hkv)
+            for (int r = warp; r < B; r += warps)
+                if ((run >> r) & 1)
+                    for (int c = lane * 4; c < R; c += 128)
+                        cp_async16(smem_addr(angles + (i & 1) * (B * D) + r * D + c),
+                                   p.cos_sin + (size_t)x.pos[r] * R + c);
+    };
+    const bool finds = warp == warps - 1;
+    if (finds) {
+        find(0);
+        find(1);
+    }
+    __syncthreads();
+    if (found[0].run != 0) bring(0);
+    cp_async_wait_all();
+    __syncthreads();
+    for (int i = 0; found[i % Q8_FOUND].run != 0; ++i) {
+        const Found& x = found[i % Q8_FOUND];
+        if (found[(i + 1) % Q8_FOUND].run != 0) bring(i + 1);
+        Window w;
+        w.run = x.run; w.leaders = x.leaders;
+        w.blk = x.blk[lane]; w.row = x.row[lane]; w.lead = x.lead[lane]; w.last = x.last[lane]; w.lead_row = x.lead_row[lane];
+        // the scale of each run's page, and no other run at that page from here on
+        const unsigned page = (unsigned)max(w.blk, 0) * Hkv + head;
+        uint32_t had = 0;
+        if (real && part == 0 && (w.run & w.leaders) >> lane & 1)
+            had = atomicExch(reinterpret_cast<unsigned int*>(scales + page), Q8_LOCKED);
+        const unsigned char* const stage = stages + (i & 1) * S::ROWS;
+        const float* const turn = angles + (i & 1) * (B * D);
+        uint64_t f[IT][4];
+        float by[IT];
+#pragma unroll
+        for (int k = 0; k < IT; ++k) {
+            const int r0 = (part * IT + k) * GPW;
+            if (((w.run >> r0) & ((1u << GPW) - 1)) != 0) {  // (rows that are not of a run: made from anything, not used)
+                const T* const row = reinterpret_cast<const T*>(stage) + (k * GPW + sub) * D;
+                make_row<T, D, INTERLEAVED>(is_k, *reinterpret_cast<const uint2*>(row + at.lo),
+                                            *reinterpret_cast<const uint2*>(row + at.hi), turn + (r0 + sub) * D, R,
+                                            p.k_weight != nullptr, wa, wb, at, p.eps, f[k], by[k]);
+            } else {
+                by[k] = 0.f;
+                f[k][0] = f[k][1] = f[k][2] = f[k][3] = 0;
+            }
+        }
+        store_window<D, B>(w, f, by, part, at, real, pool, scales, page, had, tops[unit], hads[unit], 1 + unit, p.err);
+        if (finds) find(i + 2);
+        cp_async_wait_all();  // this warp's part of window i + 1
+        __syncthreads();
     }
 }
 
@@ -340,16 +598,37 @@ namespace {
 
 template <typename T, int D, int B, bool INTERLEAVED>
 cudaError_t launch_q8_write_tdbi(const RopeParams& p, float* k_scale, float* v_scale, cudaStream_t stream) {
-    constexpr int W = B * D > 32 * 64 ? (B * D) / (16 * 128) : 1, UNITS = Q8_KV_WARPS / W;
-    const long long heads = (2ll * p.num_kv_heads + UNITS - 1) / UNITS;
-    const bool few = p.num_tokens < Q8_MANY_TOKENS;
-    const int rows = few ? Q8_FEW_ROWS : Q8_GROUP_ROWS, q_ctas = few ? p.num_tokens : 0;
-    const long long ctas = q_ctas + ((long long)p.num_tokens + rows - 1) / rows * heads;
+    constexpr int W = Rows<D, B>::W, UNITS = Q8_KV_WARPS / W;
+    if (p.num_tokens < Q8_MANY_TOKENS) {
+        const long long heads = (2ll * p.num_kv_heads + UNITS - 1) / UNITS;
+        const int rows = (p.num_tokens + Q8_FEW_ROWS - 1) / Q8_FEW_ROWS * heads <= Q8_CTAS ? Q8_FEW_ROWS : Q8_GROUP_ROWS;
+        const long long ctas = p.num_tokens + ((long long)p.num_tokens + rows - 1) / rows * heads;
+        if (ctas > 0x7fffffff) return cudaErrorInvalidConfiguration;
+        q8_write_kernel<T, D, B, INTERLEAVED>
+            <<<(unsigned)ctas, Q8_KV_WARPS * 32, 0, stream>>>(p, k_scale, v_scale, p.num_tokens, (int)heads, rows);
+        return cudaGetLastError();
+    }
+    // a CTA per SM (two of few warps), each with a stretch of the rows and up to 16 warps' heads
+    const long long units = 2ll * p.num_kv_heads * W;
+    const int warps = units < Q8_STREAM_WARPS ? (int)units : Q8_STREAM_WARPS;
+    const long long slices = (units + warps - 1) / warps;
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    auto kernel = q8_stream_kernel<T, D, B, INTERLEAVED>;
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 StreamSmem<D, B>::bytes(Q8_STREAM_WARPS));
+    if (e != cudaSuccess) return e;
+    const long long want = (long long)sms * (warps <= Q8_STREAM_WARPS / 2 ? 2 : 1);
+    long long rows = (p.num_tokens * slices + want - 1) / want;
+    rows = (rows + B - 1) / B * B;
+    const long long ctas = (p.num_tokens + rows - 1) / rows * slices;
     if (ctas > 0x7fffffff) return cudaErrorInvalidConfiguration;
-    q8_write_kernel<T, D, B, INTERLEAVED>
-        <<<(unsigned)ctas, Q8_KV_WARPS * 32, 0, stream>>>(p, k_scale, v_scale, q_ctas, (int)heads, rows);
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess || few) return e;
+    kernel<<<(unsigned)ctas, warps * 32, StreamSmem<D, B>::bytes(warps), stream>>>(p, k_scale, v_scale, warps,
+                                                                                        (int)slices, (int)rows);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
     RopeParams q = p;  // the q rows alone
     q.num_kv_heads = 0;
     return launch_rope_write(q, std::is_same<T, __half>::value ? PKV_F16 : PKV_BF16, stream);
