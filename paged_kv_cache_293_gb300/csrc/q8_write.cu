@@ -85,43 +85,53 @@ __device__ __forceinline__ void turn_queries(const RopeParams& p, const LanePart
     }
 }
 
-// A lane's chunks a and b of a key, times the weights wa and wb (none: without a norm) and turned by c and
-// s; the factor that the norm asks for besides.  The sum of squares takes all lanes of the warp.
-template <typename T, int D, bool INTERLEAVED>
-__device__ __forceinline__ float turn_key(const uint2& a2, const uint2& b2, bool norm, const uint64_t (&wa)[2],
-                                          const uint64_t (&wb)[2], bool turns, const float (&c)[4], const float (&s)[4],
-                                          float eps, uint64_t (&x)[2], uint64_t (&y)[2]) {
+// Which lanes rotate their part of a row.
+enum class Turning { NONE, SOME, ALL };
+
+// A lane's chunks a and b of a key, times the weights wa and wb (ones: without a norm) and turned by the
+// table's row; by: the factor that the norm asks for besides.  No branches, so that several rows' chains
+// run side by side.  All lanes of the warp.
+template <typename T, int D, bool INTERLEAVED, Turning TURN>
+__device__ __forceinline__ void make_key(const uint2& a2, const uint2& b2, const float* angles, int R, bool norm,
+                                         const uint64_t (&wa)[2], const uint64_t (&wb)[2], const LanePart& at, float eps,
+                                         uint64_t (&f)[4], float& by) {
+    uint64_t x[2], y[2];
     Chunk8<T>::unpack(a2, x);
     Chunk8<T>::unpack(b2, y);
-    float r = 1.f;
-    if (norm) {
-        float u, v;
-        unpack2(fma2(y[1], y[1], fma2(x[1], x[1], fma2(y[0], y[0], mul2(x[0], x[0])))), u, v);
-        float ss = u + v;
+    float u, v;
+    unpack2(fma2(y[1], y[1], fma2(x[1], x[1], fma2(y[0], y[0], mul2(x[0], x[0])))), u, v);
+    float ss = u + v;
 #pragma unroll
-        for (int o = D / 16; o >= 1; o >>= 1) ss += __shfl_xor_sync(FULL_MASK, ss, o);
-        r = rsqrtf(ss * (1.f / D) + eps);
+    for (int o = D / 16; o >= 1; o >>= 1) ss += __shfl_xor_sync(FULL_MASK, ss, o);
+    const float r = rsqrtf(ss * (1.f / D) + eps);
+    by = norm ? r : 1.f;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            x[i] = mul2(x[i], wa[i]);
-            y[i] = mul2(y[i], wb[i]);
-        }
+    for (int i = 0; i < 2; ++i) {
+        x[i] = mul2(x[i], wa[i]);
+        y[i] = mul2(y[i], wb[i]);
     }
-    if (turns) {
+    f[0] = x[0];
+    f[1] = x[1];
+    f[2] = y[0];
+    f[3] = y[1];
+    if constexpr (TURN != Turning::NONE) {
+        float c[4], s[4];
+        load_angles(angles, R, at.l, c, s);  // (a lane that does not turn: its share of whatever lies there)
+        uint64_t g[4];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const uint64_t u = x[i], v = y[i];
             if (INTERLEAVED) {  // pair i of a turns by c[i], pair i of b by c[2 + i]
-                x[i] = fma2(swap2(u), pack2(-s[i], s[i]), mul2(u, pack2(c[i], c[i])));
-                y[i] = fma2(swap2(v), pack2(-s[2 + i], s[2 + i]), mul2(v, pack2(c[2 + i], c[2 + i])));
+                g[i] = fma2(swap2(x[i]), pack2(-s[i], s[i]), mul2(x[i], pack2(c[i], c[i])));
+                g[2 + i] = fma2(swap2(y[i]), pack2(-s[2 + i], s[2 + i]), mul2(y[i], pack2(c[2 + i], c[2 + i])));
             } else {
                 const uint64_t cc = pack2(c[2 * i], c[2 * i + 1]);
-                x[i] = fma2(v, pack2(-s[2 * i], -s[2 * i + 1]), mul2(u, cc));
-                y[i] = fma2(u, pack2(s[2 * i], s[2 * i + 1]), mul2(v, cc));
+                g[i] = fma2(y[i], pack2(-s[2 * i], -s[2 * i + 1]), mul2(x[i], cc));
+                g[2 + i] = fma2(x[i], pack2(s[2 * i], s[2 * i + 1]), mul2(y[i], cc));
             }
         }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] = TURN == Turning::ALL || at.turns ? g[i] : f[i];
     }
-    return r;
 }
 
 // Rounds a row of a page to a larger scale, a lane's 8 values.
@@ -219,25 +229,51 @@ struct Rows {
     static_assert(IT * 8 <= 64, "numbers a lane");
 };
 
-// One row of a head's keys or values: by times f are its numbers.
-template <typename T, int D, bool INTERLEAVED>
-__device__ __forceinline__ void make_row(bool is_k, const uint2& a, const uint2& b, const float* angles, int R, bool norm,
-                                         const uint64_t (&wa)[2], const uint64_t (&wb)[2], const LanePart& at, float eps,
-                                         uint64_t (&f)[4], float& by) {
-    uint64_t x[2], y[2];
-    by = 1.f;
-    if (is_k) {
-        float c[4], s[4];
-        if (at.turns) load_angles(angles, R, at.l, c, s);
-        by = turn_key<T, D, INTERLEAVED>(a, b, norm, wa, wb, at.turns, c, s, eps, x, y);
+// The first n of a lane's IT rows of a head's keys or values (n uniform; the others zero): by times f are
+// their numbers.  in(i, a, b) gives row i's chunks, angles its place in the rows of the table.
+template <typename T, int D, int B, bool INTERLEAVED, bool ONE, typename In>
+__device__ __forceinline__ void make_rows(bool is_k, const In& in, const float* angles, int R, bool norm,
+                                          const uint64_t (&wa)[2], const uint64_t (&wb)[2], const LanePart& at, float eps,
+                                          uint64_t (&f)[Rows<D, B>::IT][4], float (&by)[Rows<D, B>::IT]) {
+    constexpr int IT = Rows<D, B>::IT, N = ONE ? 1 : IT, STEP = Rows<D, B>::GPW * D;
+    uint2 a, b;
+    if (!is_k) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            uint64_t x[2], y[2];
+            in(i, a, b);
+            Chunk8<T>::unpack(a, x);
+            Chunk8<T>::unpack(b, y);
+            f[i][0] = x[0];
+            f[i][1] = x[1];
+            f[i][2] = y[0];
+            f[i][3] = y[1];
+            by[i] = 1.f;
+        }
+    } else if (R == D) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            in(i, a, b);
+            make_key<T, D, INTERLEAVED, Turning::ALL>(a, b, angles + i * STEP, R, norm, wa, wb, at, eps, f[i], by[i]);
+        }
+    } else if (R > 0) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            in(i, a, b);
+            make_key<T, D, INTERLEAVED, Turning::SOME>(a, b, angles + i * STEP, R, norm, wa, wb, at, eps, f[i], by[i]);
+        }
     } else {
-        Chunk8<T>::unpack(a, x);
-        Chunk8<T>::unpack(b, y);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            in(i, a, b);
+            make_key<T, D, INTERLEAVED, Turning::NONE>(a, b, angles + i * STEP, R, norm, wa, wb, at, eps, f[i], by[i]);
+        }
     }
-    f[0] = x[0];
-    f[1] = x[1];
-    f[2] = y[0];
-    f[3] = y[1];
+#pragma unroll
+    for (int i = N; i < IT; ++i) {
+        by[i] = 0.f;
+        f[i][0] = f[i][1] = f[i][2] = f[i][3] = 0;
+    }
 }
 
 // The largest of m and the sizes of a lane's eight numbers of a row (a NaN is left out).
@@ -252,13 +288,16 @@ __device__ __forceinline__ float largest(const uint64_t (&f)[4], float m = 0.f) 
 }
 
 // A lane's eight numbers of a row, times x, into its places of the row.
-__device__ __forceinline__ void store_row(uint8_t* out, const LanePart& at, const uint64_t (&f)[4], float x) {
+__device__ __forceinline__ void store_row(uint8_t* out, const LanePart& at, const uint64_t (&f)[4], float x, bool real) {
     const uint64_t x2 = pack2(x, x);
     float v[8];
 #pragma unroll
     for (int k = 0; k < 4; ++k) unpack2(mul2(f[k], x2), v[2 * k], v[2 * k + 1]);
-    *reinterpret_cast<uint32_t*>(out + at.lo) = e4m3x4_of_floats(v[0], v[1], v[2], v[3]);
-    *reinterpret_cast<uint32_t*>(out + at.hi) = e4m3x4_of_floats(v[4], v[5], v[6], v[7]);
+    const uint32_t lo = e4m3x4_of_floats(v[0], v[1], v[2], v[3]), hi = e4m3x4_of_floats(v[4], v[5], v[6], v[7]);
+    if (real) {
+        *reinterpret_cast<uint32_t*>(out + at.lo) = lo;
+        *reinterpret_cast<uint32_t*>(out + at.hi) = hi;
+    }
 }
 
 // The scales of a window's pages and their values, from the rows' numbers by[i] f[i] of one head.  `had`:
@@ -357,7 +396,7 @@ __device__ __forceinline__ void store_window(const Window& w, uint64_t (&f)[Rows
                              (__shfl_sync(FULL_MASK, w.row, j) - j + part * IT * GPW + sub) * D;
 #pragma unroll
         for (int i = 0; i < IT; ++i)
-            if ((stored >> ((part * IT + i) * GPW + sub)) & 1) store_row(out + i * GPW * D, at, f[i], x * by[i]);
+            store_row(out + i * GPW * D, at, f[i], x * by[i], (stored >> ((part * IT + i) * GPW + sub)) & 1);
     } else {
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
@@ -366,7 +405,7 @@ __device__ __forceinline__ void store_window(const Window& w, uint64_t (&f)[Rows
             const float x = __shfl_sync(FULL_MASK, inv, r) * by[i];
             uint8_t* const out =
                 pool + (size_t)__shfl_sync(FULL_MASK, page, r) * (B * D) + __shfl_sync(FULL_MASK, w.row, r) * D;
-            if ((stored >> r) & 1) store_row(out, at, f[i], x);
+            store_row(out, at, f[i], x, (stored >> r) & 1);
         }
     }
     if (ok && leads && part == 0) atomicExch(reinterpret_cast<unsigned int*>(scales + page), __float_as_uint(s));
@@ -384,7 +423,7 @@ __device__ __forceinline__ LanePart lane_part(int l, int R) {
 
 template <typename T>
 __device__ __forceinline__ void load_weights(const void* w, const LanePart& at, uint64_t (&wa)[2], uint64_t (&wb)[2]) {
-    wa[0] = wa[1] = wb[0] = wb[1] = 0;
+    wa[0] = wa[1] = wb[0] = wb[1] = pack2(1.f, 1.f);
     if (w == nullptr) return;
     Chunk8<T>::unpack(__ldg(reinterpret_cast<const uint2*>(static_cast<const T*>(w) + at.lo)), wa);
     Chunk8<T>::unpack(__ldg(reinterpret_cast<const uint2*>(static_cast<const T*>(w) + at.hi)), wb);
@@ -450,19 +489,19 @@ q8_write_kernel(const RopeParams p, float* k_scale, float* v_scale, int q_ctas, 
             }
         }
         __syncthreads();
+        const bool several = (w.run >> GPW) != 0;
         uint64_t f[IT][4];
         float by[IT];
-#pragma unroll
-        for (int i = 0; i < IT; ++i) {
-            const int r0 = (part * IT + i) * GPW;
-            if (((w.run >> r0) & ((1u << GPW) - 1)) != 0) {  // (rows that are not of a run: made from anything, not used)
-                make_row<T, D, INTERLEAVED>(is_k, a[i], b[i], angles + (r0 + sub) * D, R, p.k_weight != nullptr, wa, wb, at,
-                                            p.eps, f[i], by[i]);
-            } else {
-                by[i] = 0.f;
-                f[i][0] = f[i][1] = f[i][2] = f[i][3] = 0;
-            }
-        }
+        // (rows that are not of a run are made from anything, and not used)
+        const float* const turn = angles + (part * IT * GPW + sub) * D;
+        auto in = [&](int i, uint2& x, uint2& y) {
+            x = a[i];
+            y = b[i];
+        };
+        if (several)
+            make_rows<T, D, B, INTERLEAVED, false>(is_k, in, turn, R, p.k_weight != nullptr, wa, wb, at, p.eps, f, by);
+        else
+            make_rows<T, D, B, INTERLEAVED, true>(is_k, in, turn, R, p.k_weight != nullptr, wa, wb, at, p.eps, f, by);
         store_window<D, B>(w, f, by, part, at, real, pool, scales, page, had, tops[unit], hads[unit], 1 + unit, p.err);
         __syncthreads();  // before the next window's rows of the table and maxima
     }
@@ -570,23 +609,16 @@ q8_stream_kernel(const RopeParams p, float* k_scale, float* v_scale, int warps, 
         uint32_t had = 0;
         if (real && part == 0 && (w.run & w.leaders) >> lane & 1)
             had = atomicExch(reinterpret_cast<unsigned int*>(scales + page), Q8_LOCKED);
-        const unsigned char* const stage = stages + (i & 1) * S::ROWS;
-        const float* const turn = angles + (i & 1) * (B * D);
+        // (rows that are not of a run are made from anything, and not used)
+        const T* const row = reinterpret_cast<const T*>(stages + (i & 1) * S::ROWS) + sub * D;
+        auto in = [&](int k, uint2& x, uint2& y) {
+            x = *reinterpret_cast<const uint2*>(row + k * GPW * D + at.lo);
+            y = *reinterpret_cast<const uint2*>(row + k * GPW * D + at.hi);
+        };
         uint64_t f[IT][4];
         float by[IT];
-#pragma unroll
-        for (int k = 0; k < IT; ++k) {
-            const int r0 = (part * IT + k) * GPW;
-            if (((w.run >> r0) & ((1u << GPW) - 1)) != 0) {  // (rows that are not of a run: made from anything, not used)
-                const T* const row = reinterpret_cast<const T*>(stage) + (k * GPW + sub) * D;
-                make_row<T, D, INTERLEAVED>(is_k, *reinterpret_cast<const uint2*>(row + at.lo),
-                                            *reinterpret_cast<const uint2*>(row + at.hi), turn + (r0 + sub) * D, R,
-                                            p.k_weight != nullptr, wa, wb, at, p.eps, f[k], by[k]);
-            } else {
-                by[k] = 0.f;
-                f[k][0] = f[k][1] = f[k][2] = f[k][3] = 0;
-            }
-        }
+        make_rows<T, D, B, INTERLEAVED, false>(is_k, in, angles + (i & 1) * (B * D) + (part * IT * GPW + sub) * D, R,
+                                               p.k_weight != nullptr, wa, wb, at, p.eps, f, by);
         store_window<D, B>(w, f, by, part, at, real, pool, scales, page, had, tops[unit], hads[unit], 1 + unit, p.err);
         if (finds) find(i + 2);
         cp_async_wait_all();  // this warp's part of window i + 1
