@@ -16,8 +16,10 @@
 #include <cfloat>
 #include <type_traits>
 
+#include "decode_mma.cuh"
 #include "q8.cuh"
 #include "rope.cuh"
+#include "umma.cuh"
 
 namespace pkv {
 
@@ -159,32 +161,41 @@ struct Window {
     unsigned leaders;
 };
 
+// A row's slot and position as the call has them (none past its rows).
+struct RawRow {
+    long long slot;
+    int pos;
+};
+__device__ __forceinline__ RawRow load_row(const RopeParams& p, int i) {
+    if (i < 0 || i >= p.num_tokens) return RawRow{-1, -1};
+    return RawRow{p.slot_mapping[i], p.positions[i]};
+}
+
 // The runs that begin in rows [t, t_end) and are whole in the B rows from t on; t moves to the first that
 // is not.  A run: tokens whose slots advance as their rows do, in one block.  `first`: what lies before
-// t is not known yet.  Whole warps.
+// t is not known yet; raw: lane j's row t + j.  Whole warps.
 template <int B>
-__device__ __forceinline__ Window find_window(const RopeParams& p, int& t, int t_end, bool first, bool reports) {
+__device__ __forceinline__ Window find_window(const RopeParams& p, const RawRow& raw, int& t, int t_end, bool first,
+                                              bool reports) {
     const int lane = threadIdx.x & 31;
     const long long num_slots = (long long)p.num_blocks * B;
-    auto look = [&](int i, int& row, int& pos) -> int {
-        pos = row = -1;
-        if (i < 0 || i >= p.num_tokens) return -1;
-        pos = p.positions[i];
-        const long long slot = p.slot_mapping[i];
-        if (pos < 0 || (p.rotary_dim > 0 && pos >= p.max_position) || slot < 0 || slot >= num_slots) return -1;
-        row = (int)(slot & (B - 1));
-        return (int)(slot / B);
+    auto look = [&](const RawRow& x, int& row) -> int {
+        row = -1;
+        if (x.pos < 0 || (p.rotary_dim > 0 && x.pos >= p.max_position) || x.slot < 0 || x.slot >= num_slots) return -1;
+        row = (int)(x.slot & (B - 1));
+        return (int)(x.slot / B);
     };
     Window w;
-    w.blk = look(t + lane, w.row, w.pos);
+    w.pos = raw.pos;
+    w.blk = look(raw, w.row);
     const unsigned below = (1u << lane) - 1, here = 1u << lane;
     const unsigned there = __ballot_sync(FULL_MASK, w.blk >= 0);
     // the nearest row before that holds a token: in the window, or (for its first token) before it
     int d = (there & below) != 0 ? lane - (31 - __clz(there & below)) : 0;
     int blk_d = __shfl_sync(FULL_MASK, w.blk, lane - d), row_d = __shfl_sync(FULL_MASK, w.row, lane - d);
     if (first && there != 0) {
-        int unused, row_b;
-        const int blk_b = look(t - 1 - lane, row_b, unused);
+        int row_b;
+        const int blk_b = look(load_row(p, t - 1 - lane), row_b);
         const unsigned near = __ballot_sync(FULL_MASK, blk_b >= 0);
         const int k = near != 0 ? __ffs(near) - 1 : 0, j = __ffs(there) - 1;
         const int blk_k = __shfl_sync(FULL_MASK, blk_b, k), row_k = __shfl_sync(FULL_MASK, row_b, k);
@@ -288,26 +299,28 @@ __device__ __forceinline__ float largest(const uint64_t (&f)[4], float m = 0.f) 
 }
 
 // A lane's eight numbers of a row, times x, into its places of the row.
-__device__ __forceinline__ void store_row(uint8_t* out, const LanePart& at, const uint64_t (&f)[4], float x, bool real) {
+__device__ __forceinline__ void store_row(uint8_t* out, int lo_at, int hi_at, const uint64_t (&f)[4], float x, bool real) {
     const uint64_t x2 = pack2(x, x);
     float v[8];
 #pragma unroll
     for (int k = 0; k < 4; ++k) unpack2(mul2(f[k], x2), v[2 * k], v[2 * k + 1]);
     const uint32_t lo = e4m3x4_of_floats(v[0], v[1], v[2], v[3]), hi = e4m3x4_of_floats(v[4], v[5], v[6], v[7]);
     if (real) {
-        *reinterpret_cast<uint32_t*>(out + at.lo) = lo;
-        *reinterpret_cast<uint32_t*>(out + at.hi) = hi;
+        *reinterpret_cast<uint32_t*>(out + lo_at) = lo;
+        *reinterpret_cast<uint32_t*>(out + hi_at) = hi;
     }
 }
 
 // The scales of a window's pages and their values, from the rows' numbers by[i] f[i] of one head.  `had`:
 // lane j's page's scale before, where row j begins a run; tops and hads: this page's, in shared memory,
-// which two warps of a page share behind barrier `bar`.
+// which two warps of a page share behind barrier `bar`; staged: room for the warp's rows of values, from
+// where a bulk copy brings a run of neighbouring rows to its page (none: stored directly).
 template <int D, int B>
 __device__ __forceinline__ void store_window(const Window& w, uint64_t (&f)[Rows<D, B>::IT][4],
                                              float (&by)[Rows<D, B>::IT], int part, const LanePart& at, bool real,
                                              uint8_t* pool, float* scales, unsigned page, uint32_t had, float* tops,
-                                             uint32_t* hads, int bar, unsigned int* err) {
+                                             uint32_t* hads, int bar, unsigned int* err,
+                                             unsigned char* staged = nullptr) {
     using L = Rows<D, B>;
     constexpr int IT = L::IT, GPW = L::GPW, W = L::W, LPR = L::LPR;
     const int lane = threadIdx.x & 31, sub = lane / LPR, l = at.l;
@@ -376,7 +389,9 @@ __device__ __forceinline__ void store_window(const Window& w, uint64_t (&f)[Rows
     if (real && leads && !ok) set_error(err, PKV_DEVERR_SLOT);
     const float old = __uint_as_float(had), need = q8_scale_for(top);
     const float s = w.lead_row > 0 ? fmaxf(old, need) : need;  // (a scale that is NaN counts as none)
-    const float inv = 1.f / s;
+    // (of a power of two exactly, and without a division)
+    const int bits = __float_as_int(s);
+    const float inv = (bits & 0x7fffff) == 0 ? __int_as_float(0x7f000000 - bits) : 1.f / s;
     unsigned grown = __ballot_sync(FULL_MASK, ok && leads && w.lead_row > 0 && s > old);
     for (; grown != 0; grown &= grown - 1) {
         const int j = __ffs(grown) - 1, row0 = __shfl_sync(FULL_MASK, w.row, j);
@@ -390,13 +405,38 @@ __device__ __forceinline__ void store_window(const Window& w, uint64_t (&f)[Rows
     }
     const unsigned stored = __ballot_sync(FULL_MASK, ok);
     if (single) {  // rows behind one another in one page
-        const int j = __ffs(w.run & w.leaders) - 1;
+        const int j = __ffs(w.run & w.leaders) - 1, r0 = part * IT * GPW;
         const float x = __shfl_sync(FULL_MASK, inv, j);
         uint8_t* const out = pool + (size_t)__shfl_sync(FULL_MASK, page, j) * (B * D) +
-                             (__shfl_sync(FULL_MASK, w.row, j) - j + part * IT * GPW + sub) * D;
+                             (__shfl_sync(FULL_MASK, w.row, j) - j + r0) * D;
+        if (staged != nullptr && stored == w.run && j == 0 && (w.run & (w.run + 1)) == 0) {
+            if (lane == 0) bulk_wait_read<0>();  // the copy before has read its rows
+            __syncwarp();
+            const bool swap = sub & 1;  // (so that the rows of a warp meet in no bank)
 #pragma unroll
-        for (int i = 0; i < IT; ++i)
-            store_row(out + i * GPW * D, at, f[i], x * by[i], (stored >> ((part * IT + i) * GPW + sub)) & 1);
+            for (int i = 0; i < IT; ++i) {
+                const uint64_t x2 = pack2(x * by[i], x * by[i]);
+                float v[8];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) unpack2(mul2(f[i][k], x2), v[2 * k], v[2 * k + 1]);
+                const uint32_t lo = e4m3x4_of_floats(v[0], v[1], v[2], v[3]), hi = e4m3x4_of_floats(v[4], v[5], v[6], v[7]);
+                unsigned char* const row = staged + (i * GPW + sub) * D;
+                *reinterpret_cast<uint32_t*>(row + (swap ? at.hi : at.lo)) = swap ? hi : lo;
+                *reinterpret_cast<uint32_t*>(row + (swap ? at.lo : at.hi)) = swap ? lo : hi;
+            }
+            fence_proxy_async_shared();
+            __syncwarp();
+            const int rows = min(__popc(w.run) - r0, IT * GPW);
+            if (lane == 0) {
+                if (rows > 0) bulk_s2g(out, smem_addr(staged), rows * D);
+                bulk_commit();
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < IT; ++i)
+                store_row(out + (i * GPW + sub) * D, at.lo, at.hi, f[i], x * by[i],
+                          (stored >> ((part * IT + i) * GPW + sub)) & 1);
+        }
     } else {
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
@@ -405,7 +445,7 @@ __device__ __forceinline__ void store_window(const Window& w, uint64_t (&f)[Rows
             const float x = __shfl_sync(FULL_MASK, inv, r) * by[i];
             uint8_t* const out =
                 pool + (size_t)__shfl_sync(FULL_MASK, page, r) * (B * D) + __shfl_sync(FULL_MASK, w.row, r) * D;
-            store_row(out, at, f[i], x, (stored >> r) & 1);
+            store_row(out, at.lo, at.hi, f[i], x, (stored >> r) & 1);
         }
     }
     if (ok && leads && part == 0) atomicExch(reinterpret_cast<unsigned int*>(scales + page), __float_as_uint(s));
@@ -461,7 +501,7 @@ q8_write_kernel(const RopeParams p, float* k_scale, float* v_scale, int q_ctas, 
     const int t_begin = cta / heads * rows, t_end = min(t_begin + rows, p.num_tokens);
     for (int t = t_begin; t < t_end;) {
         const int t_now = t;
-        const Window w = find_window<B>(p, t, t_end, t_now == t_begin, threadIdx.x == 0);
+        const Window w = find_window<B>(p, load_row(p, t + lane), t, t_end, t_now == t_begin, threadIdx.x == 0);
         if (w.run == 0) continue;
         // the scale of each run's page, and no other run at that page from here on
         const unsigned page = (unsigned)max(w.blk, 0) * Hkv + head;  // (pages are 1 KB or more)
@@ -507,24 +547,31 @@ q8_write_kernel(const RopeParams p, float* k_scale, float* v_scale, int q_ctas, 
     }
 }
 
-// Many tokens: CTAs that stay.  Up to 16 warps have a page each, window by window, and their next rows
-// and the table's are on their way while they are at these.  The last warp, whose values take less work
-// than keys, also finds the windows, two ahead.
+// Many tokens: CTAs that stay, with the keys and values of up to 8 heads, a page a warp (or two), window by
+// window.  A window's rows come by one tensor copy each for k and v, a window ahead like its rows of the
+// table and the pages' scales, and a run's values go out by one copy a page.  All this is with the warps
+// of values, which take less work than keys; the last one also finds the windows, two ahead, from slots
+// that it loads before its own window.
 constexpr int Q8_STREAM_WARPS = 16, Q8_FOUND = 4;
 
 template <int D, int B>
 struct StreamSmem {
-    static constexpr int ROWS = B / Rows<D, B>::W * D * 2;   // a warp's rows of a window
-    static constexpr int ANGLES = B * D * 4;
-    __host__ __device__ static constexpr int bytes(int warps) { return 2 * (warps * ROWS + ANGLES); }
+    static constexpr int OUT = B * D / Rows<D, B>::W;  // a warp's values of a window
+    // two stages of k and v rows of `heads` heads and of table rows, and the values
+    __host__ __device__ static constexpr int rows(int heads) { return B * heads * D * 2; }
+    __host__ __device__ static constexpr int stage(int heads) { return 2 * rows(heads) + B * D * 4; }
+    __host__ __device__ static constexpr int bytes(int heads) {
+        return 2 * stage(heads) + 2 * heads * Rows<D, B>::W * OUT;
+    }
 };
 
 template <typename T, int D, int B, bool INTERLEAVED>
 __global__ void __launch_bounds__(Q8_STREAM_WARPS * 32, 1)
-q8_stream_kernel(const RopeParams p, float* k_scale, float* v_scale, int warps, int slices, int rows) {
+q8_stream_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
+                 const RopeParams p, float* k_scale, float* v_scale, int heads, int slices, int rows) {
     using L = Rows<D, B>;
     using S = StreamSmem<D, B>;
-    constexpr int IT = L::IT, GPW = L::GPW, W = L::W, CH = D / 8;  // 16-byte columns of a row
+    constexpr int IT = L::IT, GPW = L::GPW, W = L::W;
     extern __shared__ __align__(128) unsigned char stream_smem[];
     struct Found {
         int t;
@@ -534,13 +581,31 @@ q8_stream_kernel(const RopeParams p, float* k_scale, float* v_scale, int warps, 
     __shared__ Found found[Q8_FOUND];
     __shared__ float tops[Q8_STREAM_WARPS / W][32];
     __shared__ uint32_t hads[Q8_STREAM_WARPS / W][32];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane / L::LPR;
+    __shared__ __align__(8) uint64_t bars[2];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane / L::LPR, warps = 2 * heads * W;
     const int Hkv = p.num_kv_heads, R = p.rotary_dim;
     const int t_begin = (int)blockIdx.x / slices * rows, t_end = min(t_begin + rows, p.num_tokens);
-    const int first_u = (int)blockIdx.x % slices * (warps / W);
-    float* const angles = reinterpret_cast<float*>(stream_smem + 2 * warps * S::ROWS);
+    const int head0 = (int)blockIdx.x % slices * heads, n_heads = min(heads, Hkv - head0);
+    const uint32_t bar0 = smem_addr(bars);
+    if (threadIdx.x == 0) {
+        mbar_init(bar0, 1);
+        mbar_init(bar0 + 8, 1);
+        mbar_init_fence();
+    }
+    const LanePart at = lane_part<T, INTERLEAVED>(lane % L::LPR, R);
+    const int part = warp % W, unit = warp / W;
+    const bool is_k = unit < heads;
+    const int h = is_k ? unit : unit - heads;   // of this slice
+    const bool real = h < n_heads;
+    float* const scales = is_k ? k_scale : v_scale;
+    uint8_t* const pool = static_cast<uint8_t*>(is_k ? p.k_pool : p.v_pool);
+    uint64_t wa[2], wb[2];
+    load_weights<T>(p.k_weight, at, wa, wb);
+    unsigned char* const out = stream_smem + 2 * S::stage(heads) + warp * S::OUT;
+    const uint64_t policy = l2_evict_first_policy();  // the projections are not read again
 
     int t = t_begin;
+    RawRow raw = load_row(p, t + lane);
     auto find = [&](int i) {
         Found& x = found[i % Q8_FOUND];
         Window w;
@@ -548,7 +613,8 @@ q8_stream_kernel(const RopeParams p, float* k_scale, float* v_scale, int warps, 
         int t_now = t;
         while (t < t_end && w.run == 0) {
             t_now = t;
-            w = find_window<B>(p, t, t_end, t_now == t_begin, lane == 0);
+            w = find_window<B>(p, raw, t, t_end, t_now == t_begin, lane == 0);
+            if (w.run == 0) raw = load_row(p, t + lane);
         }
         if (w.run != 0) {
             x.blk[lane] = w.blk; x.row[lane] = w.row; x.pos[lane] = w.pos;
@@ -561,72 +627,86 @@ q8_stream_kernel(const RopeParams p, float* k_scale, float* v_scale, int warps, 
         }
         __syncwarp();
     };
-    const LanePart at = lane_part<T, INTERLEAVED>(lane % L::LPR, R);
-    const int part = warp % W, unit = warp / W, u = first_u + unit;
-    const bool real = u < 2 * Hkv, is_k = u < Hkv;
-    const int head = real ? (is_k ? u : u - Hkv) : 0;
-    float* const scales = is_k ? k_scale : v_scale;
-    uint8_t* const pool = static_cast<uint8_t*>(is_k ? p.k_pool : p.v_pool);
-    const long long stride = is_k ? p.k_stride : p.v_stride;
-    const T* const rows_in = static_cast<const T*>(is_k ? p.k : p.v) + head * D;
-    uint64_t wa[2], wb[2];
-    load_weights<T>(p.k_weight, at, wa, wb);
-    unsigned char* const stages = stream_smem + warp * 2 * S::ROWS;
-    auto bring = [&](int i) {  // of window i, this warp's rows and its share of the table's
+    auto bring = [&](int i) {  // this warp's share of window i's rows
         const Found& x = found[i % Q8_FOUND];
         const unsigned run = x.run;
-        const T* const from = rows_in + x.t * stride;
-#pragma unroll
-        for (int k = 0; k < IT; ++k) {
-            const int r0 = k * GPW + sub, r = part * IT * GPW + r0;
-            if (real && ((run >> r) & 1))
-                cp_async16(smem_addr(stages + (i & 1) * S::ROWS + (r0 * CH + at.l) * 16), from + r * stride + at.l * 8);
+        if (is_k || run == 0) return;
+        const uint32_t bar = bar0 + 8 * (i & 1), stage = smem_addr(stream_smem + (i & 1) * S::stage(heads));
+        if (warp == heads * W && umma::elect_one()) {
+            mbar_arrive_expect_tx(bar, 2 * S::rows(heads));
+            tma_load_3d(stage, &tmap_k, 0, head0, x.t, bar, policy);
+            tma_load_3d(stage + S::rows(heads), &tmap_v, 0, head0, x.t, bar, policy);
         }
-        if (R > 0 && first_u < Hkv)
-            for (int r = warp; r < B; r += warps)
-                if ((run >> r) & 1)
-                    for (int c = lane * 4; c < R; c += 128)
-                        cp_async16(smem_addr(angles + (i & 1) * (B * D) + r * D + c),
-                                   p.cos_sin + (size_t)x.pos[r] * R + c);
+        for (int r = warp - heads * W; r < B; r += heads * W)
+            if (((run >> r) & 1) && 4 * lane < R)
+                cp_async16(stage + 2 * S::rows(heads) + (r * D + 4 * lane) * 4, p.cos_sin + (size_t)x.pos[r] * R + 4 * lane);
+    };
+    // the scale of each run's page, and no other run at that page from here on
+    auto lock = [&](int i) -> uint32_t {
+        const Found& x = found[i % Q8_FOUND];
+        if (!real || part != 0 || !((x.run & x.leaders) >> lane & 1)) return 0u;
+        return atomicExch(reinterpret_cast<unsigned int*>(scales + ((unsigned)x.blk[lane] * Hkv + head0 + h)), Q8_LOCKED);
     };
     const bool finds = warp == warps - 1;
+    if (finds) find(0);
+    __syncthreads();
+    bring(0);
+    __syncwarp();
+    uint32_t had = lock(0);
     if (finds) {
-        find(0);
+        raw = load_row(p, t + lane);
         find(1);
     }
-    __syncthreads();
-    if (found[0].run != 0) bring(0);
     cp_async_wait_all();
     __syncthreads();
     for (int i = 0; found[i % Q8_FOUND].run != 0; ++i) {
         const Found& x = found[i % Q8_FOUND];
-        if (found[(i + 1) % Q8_FOUND].run != 0) bring(i + 1);
+        bring(i + 1);
+        __syncwarp();
+        if (finds) raw = load_row(p, t + lane);
         Window w;
         w.run = x.run; w.leaders = x.leaders;
         w.blk = x.blk[lane]; w.row = x.row[lane]; w.lead = x.lead[lane]; w.last = x.last[lane]; w.lead_row = x.lead_row[lane];
-        // the scale of each run's page, and no other run at that page from here on
-        const unsigned page = (unsigned)max(w.blk, 0) * Hkv + head;
-        uint32_t had = 0;
-        if (real && part == 0 && (w.run & w.leaders) >> lane & 1)
-            had = atomicExch(reinterpret_cast<unsigned int*>(scales + page), Q8_LOCKED);
+        const unsigned page = (unsigned)max(w.blk, 0) * Hkv + head0 + (real ? h : 0);
+        if (!mbar_wait_short(bar0 + 8 * (i & 1), (i >> 1) & 1)) set_error(p.err, PKV_DEVERR_TIMEOUT);
+        __syncwarp();
         // (rows that are not of a run are made from anything, and not used)
-        const T* const row = reinterpret_cast<const T*>(stages + (i & 1) * S::ROWS) + sub * D;
-        auto in = [&](int k, uint2& x, uint2& y) {
-            x = *reinterpret_cast<const uint2*>(row + k * GPW * D + at.lo);
-            y = *reinterpret_cast<const uint2*>(row + k * GPW * D + at.hi);
+        const unsigned char* const stage = stream_smem + (i & 1) * S::stage(heads);
+        const T* const row = reinterpret_cast<const T*>(stage + (is_k ? 0 : S::rows(heads))) +
+                             ((part * IT * GPW + sub) * heads + h) * D;
+        auto in = [&](int k, uint2& a, uint2& b) {
+            a = *reinterpret_cast<const uint2*>(row + k * GPW * heads * D + at.lo);
+            b = *reinterpret_cast<const uint2*>(row + k * GPW * heads * D + at.hi);
         };
         uint64_t f[IT][4];
         float by[IT];
-        make_rows<T, D, B, INTERLEAVED, false>(is_k, in, angles + (i & 1) * (B * D) + (part * IT * GPW + sub) * D, R,
-                                               p.k_weight != nullptr, wa, wb, at, p.eps, f, by);
-        store_window<D, B>(w, f, by, part, at, real, pool, scales, page, had, tops[unit], hads[unit], 1 + unit, p.err);
+        make_rows<T, D, B, INTERLEAVED, false>(
+            is_k, in, reinterpret_cast<const float*>(stage + 2 * S::rows(heads)) + (part * IT * GPW + sub) * D, R,
+            p.k_weight != nullptr, wa, wb, at, p.eps, f, by);
+        store_window<D, B>(w, f, by, part, at, real, pool, scales, page, had, tops[unit], hads[unit], 1 + unit, p.err, out);
+        had = lock(i + 1);  // (not before: the fence in there would wait for it)
         if (finds) find(i + 2);
-        cp_async_wait_all();  // this warp's part of window i + 1
+        cp_async_wait_all();  // this warp's rows of the next window's table
         __syncthreads();
     }
+    if (lane == 0) bulk_wait_read<0>();  // the CTA must not end with copies still reading its shared memory
 }
 
 namespace {
+
+// k or v seen as [tokens][heads][D]: a box is `heads` heads of `rows` tokens, as they lie.
+template <typename T>
+bool encode_rows_map(CUtensorMap* map, const void* base, long long stride, const RopeParams& p, int heads, int rows) {
+    auto enc = tensor_map_encoder();
+    if (!enc) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)p.head_dim, (cuuint64_t)p.num_kv_heads, (cuuint64_t)p.num_tokens};
+    const cuuint64_t strides[2] = {(cuuint64_t)p.head_dim * 2, (cuuint64_t)stride * 2};
+    const cuuint32_t box[3] = {(cuuint32_t)p.head_dim, (cuuint32_t)heads, (cuuint32_t)rows};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return enc(map, Mma<T>::TMA_TYPE, 3, const_cast<void*>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 template <typename T, int D, int B, bool INTERLEAVED>
 cudaError_t launch_q8_write_tdbi(const RopeParams& p, float* k_scale, float* v_scale, cudaStream_t stream) {
@@ -640,25 +720,27 @@ cudaError_t launch_q8_write_tdbi(const RopeParams& p, float* k_scale, float* v_s
             <<<(unsigned)ctas, Q8_KV_WARPS * 32, 0, stream>>>(p, k_scale, v_scale, p.num_tokens, (int)heads, rows);
         return cudaGetLastError();
     }
-    // a CTA per SM (two of few warps), each with a stretch of the rows and up to 16 warps' heads
-    const long long units = 2ll * p.num_kv_heads * W;
-    const int warps = units < Q8_STREAM_WARPS ? (int)units : Q8_STREAM_WARPS;
-    const long long slices = (units + warps - 1) / warps;
+    // a CTA per SM (two of few warps), each with a stretch of the rows and an even share of the heads
+    constexpr int MOST = Q8_STREAM_WARPS / (2 * W);
+    const int slices = (p.num_kv_heads + MOST - 1) / MOST, heads = (p.num_kv_heads + slices - 1) / slices;
+    const int warps = 2 * heads * W;
     int dev = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     auto kernel = q8_stream_kernel<T, D, B, INTERLEAVED>;
     if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 StreamSmem<D, B>::bytes(Q8_STREAM_WARPS));
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, StreamSmem<D, B>::bytes(MOST));
     if (e != cudaSuccess) return e;
     const long long want = (long long)sms * (warps <= Q8_STREAM_WARPS / 2 ? 2 : 1);
-    long long rows = (p.num_tokens * slices + want - 1) / want;
+    long long rows = ((long long)p.num_tokens * slices + want - 1) / want;
     rows = (rows + B - 1) / B * B;
     const long long ctas = (p.num_tokens + rows - 1) / rows * slices;
     if (ctas > 0x7fffffff) return cudaErrorInvalidConfiguration;
-    kernel<<<(unsigned)ctas, warps * 32, StreamSmem<D, B>::bytes(warps), stream>>>(p, k_scale, v_scale, warps,
-                                                                                        (int)slices, (int)rows);
+    CUtensorMap tk, tv;
+    if (!encode_rows_map<T>(&tk, p.k, p.k_stride, p, heads, B) || !encode_rows_map<T>(&tv, p.v, p.v_stride, p, heads, B))
+        return cudaErrorNotSupported;
+    kernel<<<(unsigned)ctas, warps * 32, StreamSmem<D, B>::bytes(heads), stream>>>(tk, tv, p, k_scale, v_scale, heads,
+                                                                                  slices, (int)rows);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     RopeParams q = p;  // the q rows alone

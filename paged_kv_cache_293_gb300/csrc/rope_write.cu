@@ -145,16 +145,6 @@ __global__ void __launch_bounds__(ROPE_MAX_THREADS) rope_write_kernel(const Rope
 // head of k and v to its cache row by one each.  The copies keep running whatever the
 // arithmetic does, which loads held in registers (rope_write_kernel) do not: 16384 tokens of
 // 32 + 2 * 8 heads of 128 take 67 us here (411 MB, 6.1 TB/s) and 114 us there.
-__device__ __forceinline__ void bulk_s2g(void* dst, uint32_t src, uint32_t bytes) {
-    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes)
-                 : "memory");
-}
-__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void bulk_wait_read() {
-    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
-}
-
 template <typename T, int D, bool INTERLEAVED, bool FULL, int WARPS>
 __global__ void __launch_bounds__((WARPS + 1) * 32) rope_stream_kernel(const RopeParams p, int stages,
                                                                      uint32_t stage_bytes) {
