@@ -53,6 +53,8 @@ struct Q8DecodeParams {
     int32_t max_context_len;
     float scale_log2;           // scale * log2(e)
     int32_t partition_size, max_parts;
+    int32_t column_tiles;       // columns (query, head) a CTA has, in tiles of 8: 1 or 2
+    int32_t clustered;          // a context's pieces meet in a cluster's shared memory and not in the workspace
     void* out;
     int32_t out_dtype;
     float* part_m;              // base 2; [row][part], then sums, then [row][part][D]
@@ -61,6 +63,8 @@ struct Q8DecodeParams {
     unsigned int* err;
 };
 
+// Pieces of a context up to which they are one cluster.
+constexpr int Q8_CLUSTER = 8;
 cudaError_t launch_q8_write(const RopeParams& p, float* k_scale, float* v_scale, int32_t dtype, cudaStream_t stream);
 template <typename T>
 cudaError_t launch_q8_decode(const Q8DecodeParams& p, int head_dim, cudaStream_t stream);

@@ -87,24 +87,40 @@ struct Q8Tile {
 
 // Stages of a warp's ring, and CTAs per SM that the registers are held to.
 constexpr int Q8_STAGES = 3, Q8_CTAS = 4;
-template <int D>
+template <int D, int NT>
 constexpr int q8_smem_bytes() {
-    return Q8_WARPS * Q8_STAGES * 2 * Q8Tile<D>::BYTES;
+    const int rings = Q8_WARPS * Q8_STAGES * 2 * Q8Tile<D>::BYTES, results = (Q8_WARPS + 1) * 8 * NT * (D + 2) * 4;
+    return rings > results ? rings : results;
 }
 
-template <typename T, int D, bool SPLIT_P>
-__global__ void __launch_bounds__(Q8_WARPS * 32, Q8_CTAS) q8_decode_kernel(const Q8DecodeParams p) {
-    constexpr int KS = D / 16, NW = Q8_WARPS, NS = Q8_STAGES;
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The 32-bit value that CTA `rank` of the cluster has at this CTA's shared-memory address a.
+__device__ __forceinline__ float load_from_cta(uint32_t a, uint32_t rank) {
+    uint32_t there;
+    float v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(a), "r"(rank));
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(there) : "memory");
+    return v;
+}
+
+// NT: 8-column tiles of the products, 1 or 2.
+template <typename T, int D, int NT, bool SPLIT_P>
+__global__ void __launch_bounds__(Q8_WARPS * 32, NT * D > 128 ? Q8_CTAS - 1 : Q8_CTAS)
+q8_decode_kernel(const Q8DecodeParams p) {
+    constexpr int KS = D / 16, NW = Q8_WARPS, NS = Q8_STAGES, COLS = 8 * NT;
     using Tile = Q8Tile<D>;
     extern __shared__ __align__(128) unsigned char q8_smem[];
     __shared__ float2 stage_scale[NW][NS];
-    float(*red)[8][D + 2] = reinterpret_cast<float(*)[8][D + 2]>(q8_smem);  // [NW], once the rings are done with
-    static_assert(NW * 8 * (D + 2) * 4 <= q8_smem_bytes<D>(), "the warps' results fit into the rings");
+    // [NW], and one for the CTA's result in a cluster, once the rings are done with
+    float(*red)[COLS][D + 2] = reinterpret_cast<float(*)[COLS][D + 2]>(q8_smem);
+    static_assert((NW + 1) * COLS * (D + 2) * 4 <= q8_smem_bytes<D, NT>(), "the warps' results fit into the rings");
     const int Hkv = p.num_kv_heads, Hq = p.num_q_heads, G = Hq / Hkv, NQ = p.num_queries, B = p.block_size;
-    const int kvh = blockIdx.x % Hkv, col0 = (blockIdx.x / Hkv) * 8, s = blockIdx.y;
+    const int kvh = blockIdx.x % Hkv, col0 = (blockIdx.x / Hkv) * COLS, s = blockIdx.y;
     const int part = gridDim.z - 1 - blockIdx.z;  // the last pieces, which few contexts reach, first
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-    const int ncols = min(8, NQ * G - col0);
+    const int ncols = min(COLS, NQ * G - col0);
     // column n: query (col0 + n) / G, head (col0 + n) % G of the kv head
     auto row_of = [&](int n) -> size_t {
         return ((size_t)s * NQ + (col0 + n) / G) * Hq + kvh * G + (col0 + n) % G;
@@ -118,10 +134,10 @@ __global__ void __launch_bounds__(Q8_WARPS * 32, Q8_CTAS) q8_decode_kernel(const
         ctx = ctx < 0 ? 0 : cap;
     }
     const int P = p.partition_size, n_parts = (ctx + P - 1) / P, tok0 = part * P;
-    if (part > 0 && tok0 >= ctx) return;
+    if (!p.clustered && part > 0 && tok0 >= ctx) return;
     const bool direct = n_parts <= 1;
     const int tok_end = min(ctx, tok0 + P);
-    const int n_chunks = (tok_end - tok0 + CHUNK_TOKENS - 1) / CHUNK_TOKENS;
+    const int n_chunks = max(tok_end - tok0 + CHUNK_TOKENS - 1, 0) / CHUNK_TOKENS;
     const int n_my = warp < n_chunks ? (n_chunks - warp + NW - 1) / NW : 0;
 
     // this warp's pages, 32 steps at a time: lane i has the page of step i, and its scales
@@ -170,10 +186,15 @@ __global__ void __launch_bounds__(Q8_WARPS * 32, Q8_CTAS) q8_decode_kernel(const
 
     // Q^T: column g's terms c D / 4 + 4 w .. + 3 for k step w, in fp16.  bf16 rows are
     // scaled by the power of two that brings their largest below 2^14, which keeps their bits.
-    uint32_t qb[KS][2];
-    float q_inv = 1.f;  // of column g
-    {
-        const T* src = static_cast<const T*>(p.q) + row_of(g < ncols ? g : 0) * D;
+    uint32_t qb[NT][KS][2];
+    // this lane's columns of the scores on: 8 nt + 2 c and the next one, of tokens g and g + 8
+    float f[NT][2], m_ref[NT][2], l[NT][2];
+    int lim[NT][2], lim_all = ctx;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        const int col = 8 * nt + g;
+        float q_inv = 1.f;  // of column g
+        const T* src = static_cast<const T*>(p.q) + row_of(col < ncols ? col : 0) * D;
         uint32_t w[D / 8];
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) {
@@ -202,21 +223,22 @@ __global__ void __launch_bounds__(Q8_WARPS * 32, Q8_CTAS) q8_decode_kernel(const
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) qb[ks][h] = g < ncols ? w[2 * ks + h] : 0u;
-    }
-    // this lane's columns from here on: 2 c and 2 c + 1, of tokens g and g + 8
-    float f[2], m_ref[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-    int lim[2];
+            for (int h = 0; h < 2; ++h) qb[nt][ks][h] = col < ncols ? w[2 * ks + h] : 0u;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const int n = 2 * c + h;
-        f[h] = p.scale_log2 * __shfl_sync(FULL_MASK, q_inv, 4 * n);
-        lim[h] = n < ncols ? ctx - NQ + 1 + (col0 + n) / G : ctx;  // positions below are seen
+        for (int h = 0; h < 2; ++h) {
+            const int n = 8 * nt + 2 * c + h;
+            f[nt][h] = p.scale_log2 * __shfl_sync(FULL_MASK, q_inv, 4 * (2 * c + h));
+            m_ref[nt][h] = -INFINITY;
+            l[nt][h] = 0.f;
+            lim[nt][h] = n < ncols ? ctx - NQ + 1 + (col0 + n) / G : ctx;  // positions below are seen
+            lim_all = min(lim_all, lim[nt][h]);
+        }
     }
-    const int lim_all = min(lim[0], lim[1]);
-    float o[KS][4];
+    float o[NT][KS][4];
 #pragma unroll
-    for (int i = 0; i < KS; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < KS; ++i) o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.f;
 
     for (int i = 0; i < n_my; ++i) {
         const int t0 = token_of(i), st = i % NS;
@@ -228,33 +250,48 @@ __global__ void __launch_bounds__(Q8_WARPS * 32, Q8_CTAS) q8_decode_kernel(const
         const float a_b = scales.x, c_b = scales.y;
         const bool here = (there >> st) & 1;
 
-        float sc[4] = {0.f, 0.f, 0.f, 0.f};
+        float pr[NT][4];  // scores, then weights: token g + 8 (j / 2), column 8 nt + 2 c + j % 2
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) pr[nt][0] = pr[nt][1] = pr[nt][2] = pr[nt][3] = 0.f;
         {
             uint32_t k0[KS], k1[KS];
             Tile::key(k_tile, g, c, k0);
             Tile::key(k_tile, g + 8, c, k1);
+            float odd[NT][4];  // two sums side by side: a product waits for the one before the last
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) odd[nt][0] = odd[nt][1] = odd[nt][2] = odd[nt][3] = 0.f;
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) {
                 uint32_t a0, a1, a2, a3;
                 f16x4_of_e4m3x4(k0[ks], a0, a2);
                 f16x4_of_e4m3x4(k1[ks], a1, a3);
-                Mma<__half>::run(sc, a0, a1, a2, a3, qb[ks][0], qb[ks][1]);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+                    Mma<__half>::run(ks & 1 ? odd[nt] : pr[nt], a0, a1, a2, a3, qb[nt][ks][0], qb[nt][ks][1]);
             }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) pr[nt][j] += odd[nt][j];
         }
         uint32_t v[4][D / 32];
 #pragma unroll
         for (int r = 0; r < 4; ++r) Tile::value(k_tile + Tile::BYTES, 2 * c + (r & 1) + 8 * (r >> 1), g, v[r]);
 
-        float pr[4];  // scores in base 2: token g + 8 (j / 2), column 2 c + j % 2
+        // in base 2
         float over = -INFINITY;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) pr[j] = sc[j] * (f[j & 1] * a_b);
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) pr[nt][j] *= f[nt][j & 1] * a_b;
         if (!here || t0 + CHUNK_TOKENS > tok_end || __any_sync(FULL_MASK, t0 + CHUNK_TOKENS > lim_all)) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int t = t0 + g + 8 * (j >> 1);
-                if (!here || t >= tok_end || t >= lim[j & 1]) pr[j] = -INFINITY;
-            }
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int t = t0 + g + 8 * (j >> 1);
+                    if (!here || t >= tok_end || t >= lim[nt][j & 1]) pr[nt][j] = -INFINITY;
+                }
             // values of tokens that no row sees may be anything, and 0 * NaN is not 0
             const int seen = here ? tok_end - t0 : 0;
 #pragma unroll
@@ -265,41 +302,50 @@ __global__ void __launch_bounds__(Q8_WARPS * 32, Q8_CTAS) q8_decode_kernel(const
                 }
         }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) over = fmaxf(over, pr[j] - m_ref[j & 1]);
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) over = fmaxf(over, pr[nt][j] - m_ref[nt][j & 1]);
         if (__any_sync(FULL_MASK, over > Q8_RAISE)) {
-            float alpha[2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                float alpha[2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float top = fmaxf(pr[nt][h], pr[nt][h + 2]);
+#pragma unroll
+                    for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(FULL_MASK, top, d));
+                    const float ref = top - m_ref[nt][h] > Q8_RAISE ? top - Q8_BELOW : m_ref[nt][h];
+                    alpha[h] = ref == m_ref[nt][h] ? 1.f : fast_exp2(m_ref[nt][h] - ref);
+                    m_ref[nt][h] = ref;
+                    l[nt][h] *= alpha[h];
+                }
+#pragma unroll
+                for (int d = 0; d < KS; ++d) {
+                    o[nt][d][0] *= alpha[0]; o[nt][d][1] *= alpha[1];
+                    o[nt][d][2] *= alpha[0]; o[nt][d][3] *= alpha[1];
+                }
+            }
+        }
+        uint32_t pb[NT][2], rb[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            float(&x)[4] = pr[nt];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                float top = fmaxf(pr[h], pr[h + 2]);
-#pragma unroll
-                for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(FULL_MASK, top, d));
-                const float ref = top - m_ref[h] > Q8_RAISE ? top - Q8_BELOW : m_ref[h];
-                alpha[h] = ref == m_ref[h] ? 1.f : fast_exp2(m_ref[h] - ref);
-                m_ref[h] = ref;
-                l[h] *= alpha[h];
+                const float ref = m_ref[nt][h] == -INFINITY ? 0.f : m_ref[nt][h];
+                x[h] = fast_exp2(x[h] - ref);
+                x[h + 2] = fast_exp2(x[h + 2] - ref);
+                l[nt][h] += x[h] + x[h + 2];
             }
+            pb[nt][0] = transpose8x8(Mma<__half>::pack(x[0], x[1]));
+            pb[nt][1] = transpose8x8(Mma<__half>::pack(x[2], x[3]));
+            if (SPLIT_P) {
+                float rem[4];
 #pragma unroll
-            for (int d = 0; d < KS; ++d) {
-                o[d][0] *= alpha[0]; o[d][1] *= alpha[1];
-                o[d][2] *= alpha[0]; o[d][3] *= alpha[1];
+                for (int j = 0; j < 4; ++j) rem[j] = x[j] - Mma<__half>::round_trip(x[j]);
+                rb[nt][0] = transpose8x8(Mma<__half>::pack(rem[0], rem[1]));
+                rb[nt][1] = transpose8x8(Mma<__half>::pack(rem[2], rem[3]));
             }
-        }
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const float ref = m_ref[h] == -INFINITY ? 0.f : m_ref[h];
-            pr[h] = fast_exp2(pr[h] - ref);
-            pr[h + 2] = fast_exp2(pr[h + 2] - ref);
-            l[h] += pr[h] + pr[h + 2];
-        }
-        const uint32_t b0 = transpose8x8(Mma<__half>::pack(pr[0], pr[1]));
-        const uint32_t b1 = transpose8x8(Mma<__half>::pack(pr[2], pr[3]));
-        uint32_t r0 = 0, r1 = 0;
-        if (SPLIT_P) {
-            float rem[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) rem[j] = pr[j] - Mma<__half>::round_trip(pr[j]);
-            r0 = transpose8x8(Mma<__half>::pack(rem[0], rem[1]));
-            r1 = transpose8x8(Mma<__half>::pack(rem[2], rem[3]));
         }
         // rows of O^T's tile 2 w + h: elements g D / 8 + 4 w + 2 h and the next one
 #pragma unroll
@@ -309,35 +355,44 @@ __global__ void __launch_bounds__(Q8_WARPS * 32, Q8_CTAS) q8_decode_kernel(const
                 uint32_t a0, a1, a2, a3;
                 f16x4_of_e4m3x4(__byte_perm(v[0][w], v[1][w], h == 0 ? 0x5140 : 0x7362), a0, a1);
                 f16x4_of_e4m3x4(__byte_perm(v[2][w], v[3][w], h == 0 ? 0x5140 : 0x7362), a2, a3);
-                float sum[4] = {0.f, 0.f, 0.f, 0.f};
-                Mma<__half>::run(sum, a0, a1, a2, a3, b0, b1);
-                if (SPLIT_P) Mma<__half>::run(sum, a0, a1, a2, a3, r0, r1);
-                float(&od)[4] = o[2 * w + h];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) od[j] = fmaf(sum[j], c_b, od[j]);
+                for (int nt = 0; nt < NT; ++nt) {
+                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                    Mma<__half>::run(sum, a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
+                    if (SPLIT_P) Mma<__half>::run(sum, a0, a1, a2, a3, rb[nt][0], rb[nt][1]);
+                    float(&od)[4] = o[nt][2 * w + h];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) od[j] = fmaf(sum[j], c_b, od[j]);
+                }
             }
     }
     __syncthreads();  // the rings are done with (no copy is in flight: the last waits were for all that were issued)
 
     // ---- the warps' results together
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int d = 4; d < 32; d <<= 1) l[h] += __shfl_xor_sync(FULL_MASK, l[h], d);
+        for (int h = 0; h < 2; ++h) {
+            float sum = l[nt][h];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        float* r = red[warp][2 * c + h];
+            for (int d = 4; d < 32; d <<= 1) sum += __shfl_xor_sync(FULL_MASK, sum, d);
+            float* r = red[warp][8 * nt + 2 * c + h];
 #pragma unroll
-        for (int i = 0; i < KS; ++i) {
-            r[g * (D / 8) + 2 * i] = o[i][h];
-            r[g * (D / 8) + 2 * i + 1] = o[i][h + 2];
+            for (int i = 0; i < KS; ++i) {
+                r[g * (D / 8) + 2 * i] = o[nt][i][h];
+                r[g * (D / 8) + 2 * i + 1] = o[nt][i][h + 2];
+            }
+            if (g == 0) {
+                r[D] = m_ref[nt][h];
+                r[D + 1] = sum;
+            }
         }
-        if (g == 0) {
-            r[D] = m_ref[h];
-            r[D + 1] = l[h];
-        }
-    }
     __syncthreads();
+    // zero for a row that sees nothing; a NaN or a sum of no weight is the result
+    auto finish = [&](int n, int d, float O, float L) {
+        const bool nothing = ctx - NQ + 1 + (col0 + n) / G <= 0;
+        store_out(p.out, p.out_dtype, row_of(n) * D + d, nothing ? 0.f : O / L);
+    };
     for (int i = threadIdx.x; i < ncols * D; i += NW * 32) {
         const int n = i / D, d = i % D;
         float M = -INFINITY;
@@ -351,13 +406,16 @@ __global__ void __launch_bounds__(Q8_WARPS * 32, Q8_CTAS) q8_decode_kernel(const
             L = fmaf(red[w][n][D + 1], by, L);
             O = fmaf(red[w][n][d], by, O);
         }
-        const size_t row = row_of(n);
-        if (direct) {
-            // zero for a row that sees nothing; a NaN or a sum of no weight is the result
-            const bool nothing = ctx - NQ + 1 + (col0 + n) / G <= 0;
-            store_out(p.out, p.out_dtype, row * D + d, nothing ? 0.f : O / L);
+        if (p.clustered) {
+            red[NW][n][d] = O;
+            if (d == 0) {
+                red[NW][n][D] = M;
+                red[NW][n][D + 1] = L;
+            }
+        } else if (direct) {
+            finish(n, d, O, L);
         } else {
-            const size_t at_part = row * p.max_parts + part;
+            const size_t at_part = row_of(n) * p.max_parts + part;
             p.part_o[at_part * D + d] = O;
             if (d == 0) {
                 p.part_m[at_part] = M;
@@ -365,12 +423,38 @@ __global__ void __launch_bounds__(Q8_WARPS * 32, Q8_CTAS) q8_decode_kernel(const
             }
         }
     }
+    if (p.clustered) {
+        // the pieces of a context, a CTA each, from one another's shared memory: CTA r takes every
+        // gridDim.z-th of the rows' elements
+        cluster_sync();
+        const int parts = gridDim.z;
+        for (int i = blockIdx.z * (NW * 32) + threadIdx.x; i < ncols * D; i += parts * (NW * 32)) {
+            const int n = i / D, d = i % D;
+            const uint32_t at = smem_addr(&red[NW][n][0]);
+            float m[Q8_CLUSTER], M = -INFINITY, L = 0.f, O = 0.f;
+#pragma unroll
+            for (int k = 0; k < Q8_CLUSTER; ++k) {
+                m[k] = k < parts ? load_from_cta(at + D * 4, k) : -INFINITY;
+                M = fmaxf(M, m[k]);
+            }
+            const float ref = M == -INFINITY ? 0.f : M;
+#pragma unroll
+            for (int k = 0; k < Q8_CLUSTER; ++k)
+                if (k < parts) {
+                    const float by = fast_exp2(m[k] - ref);
+                    L = fmaf(load_from_cta(at + (D + 1) * 4, k), by, L);
+                    O = fmaf(load_from_cta(at + d * 4, k), by, O);
+                }
+            finish(n, d, O, L);
+        }
+        cluster_sync();  // no CTA ends while others read its shared memory
+    }
 }
 
-template <typename T, int D, bool SPLIT_P>
-cudaError_t launch_q8_decode_tds(const Q8DecodeParams& p, cudaStream_t stream) {
-    constexpr int SMEM = q8_smem_bytes<D>();
-    auto kernel = q8_decode_kernel<T, D, SPLIT_P>;
+template <typename T, int D, int NT, bool SPLIT_P>
+cudaError_t launch_q8_decode_tdns(const Q8DecodeParams& p, cudaStream_t stream) {
+    constexpr int SMEM = q8_smem_bytes<D, NT>();
+    auto kernel = q8_decode_kernel<T, D, NT, SPLIT_P>;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
@@ -381,18 +465,33 @@ cudaError_t launch_q8_decode_tds(const Q8DecodeParams& p, cudaStream_t stream) {
         if (dev < 64) configured[dev].store(true, std::memory_order_release);
     }
     const int cols = p.num_queries * (p.num_q_heads / p.num_kv_heads);
-    const dim3 grid((unsigned)(p.num_kv_heads * ((cols + 7) / 8)), (unsigned)p.num_seqs, (unsigned)p.max_parts);
-    kernel<<<grid, Q8_WARPS * 32, SMEM, stream>>>(p);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(p.num_kv_heads * ((cols + 8 * NT - 1) / (8 * NT))), (unsigned)p.num_seqs,
+                       (unsigned)p.max_parts);
+    cfg.blockDim = dim3(Q8_WARPS * 32);
+    cfg.dynamicSmemBytes = SMEM;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = (unsigned)p.max_parts;
+    cfg.attrs = attr;
+    cfg.numAttrs = p.clustered ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+template <typename T, int D>
+cudaError_t launch_q8_decode_td(const Q8DecodeParams& p, cudaStream_t stream) {
+    const bool split = p.out_dtype == PKV_F32;
+    if (p.column_tiles == 1)
+        return split ? launch_q8_decode_tdns<T, D, 1, true>(p, stream) : launch_q8_decode_tdns<T, D, 1, false>(p, stream);
+    return split ? launch_q8_decode_tdns<T, D, 2, true>(p, stream) : launch_q8_decode_tdns<T, D, 2, false>(p, stream);
 }
 
 template <typename T>
 cudaError_t launch_q8_decode_impl(const Q8DecodeParams& p, int head_dim, cudaStream_t stream) {
-    const bool split = p.out_dtype == PKV_F32;
-    if (head_dim == 64)
-        return split ? launch_q8_decode_tds<T, 64, true>(p, stream) : launch_q8_decode_tds<T, 64, false>(p, stream);
-    if (head_dim == 128)
-        return split ? launch_q8_decode_tds<T, 128, true>(p, stream) : launch_q8_decode_tds<T, 128, false>(p, stream);
+    if (head_dim == 64) return launch_q8_decode_td<T, 64>(p, stream);
+    if (head_dim == 128) return launch_q8_decode_td<T, 128>(p, stream);
     return cudaErrorInvalidValue;
 }
 

@@ -28,8 +28,10 @@ namespace {
 constexpr int Q8_Q_ROWS = 2;      // rows of q per group of lanes, in flight together
 constexpr int Q8_KV_WARPS = 8;
 // From this many tokens on q goes through rope_write.cu's kernels and k and v are streamed, a launch
-// more.
-constexpr int Q8_MANY_TOKENS = 512;
+// more; measured, one launch against two, bf16: 32 + 2 * 8 heads of 128, 1024 tokens 12.3 / 13.0 us, 2048
+// 20.4 / 18.6; 40 + 2 * 40, 1024 23.2 / 24.6, 1536 33.6 / 28.7; 16 + 2 * 4 of 64, 1024 10.8 / 10.9, 2048
+// 15.0 / 10.9.
+constexpr int Q8_MANY_TOKENS = 1025;
 // Rows whose runs a CTA looks for: few while that does not make more CTAs than fit the SMs.
 constexpr int Q8_CTAS = 456;
 constexpr int Q8_FEW_ROWS = 4, Q8_GROUP_ROWS = 16;
@@ -173,10 +175,10 @@ __device__ __forceinline__ RawRow load_row(const RopeParams& p, int i) {
 
 // The runs that begin in rows [t, t_end) and are whole in the B rows from t on; t moves to the first that
 // is not.  A run: tokens whose slots advance as their rows do, in one block.  `first`: what lies before
-// t is not known yet; raw: lane j's row t + j.  Whole warps.
+// t is not known yet, and lane j has row t - 1 - j in `back`; raw: lane j's row t + j.  Whole warps.
 template <int B>
-__device__ __forceinline__ Window find_window(const RopeParams& p, const RawRow& raw, int& t, int t_end, bool first,
-                                              bool reports) {
+__device__ __forceinline__ Window find_window(const RopeParams& p, const RawRow& raw, const RawRow& back, int& t,
+                                              int t_end, bool first, bool reports) {
     const int lane = threadIdx.x & 31;
     const long long num_slots = (long long)p.num_blocks * B;
     auto look = [&](const RawRow& x, int& row) -> int {
@@ -195,7 +197,7 @@ __device__ __forceinline__ Window find_window(const RopeParams& p, const RawRow&
     int blk_d = __shfl_sync(FULL_MASK, w.blk, lane - d), row_d = __shfl_sync(FULL_MASK, w.row, lane - d);
     if (first && there != 0) {
         int row_b;
-        const int blk_b = look(load_row(p, t - 1 - lane), row_b);
+        const int blk_b = look(back, row_b);
         const unsigned near = __ballot_sync(FULL_MASK, blk_b >= 0);
         const int k = near != 0 ? __ffs(near) - 1 : 0, j = __ffs(there) - 1;
         const int blk_k = __shfl_sync(FULL_MASK, blk_b, k), row_k = __shfl_sync(FULL_MASK, row_b, k);
@@ -499,9 +501,10 @@ q8_write_kernel(const RopeParams p, float* k_scale, float* v_scale, int q_ctas, 
     uint64_t wa[2], wb[2];
     load_weights<T>(p.k_weight, at, wa, wb);
     const int t_begin = cta / heads * rows, t_end = min(t_begin + rows, p.num_tokens);
+    const RawRow back = load_row(p, t_begin - 1 - lane);
     for (int t = t_begin; t < t_end;) {
         const int t_now = t;
-        const Window w = find_window<B>(p, load_row(p, t + lane), t, t_end, t_now == t_begin, threadIdx.x == 0);
+        const Window w = find_window<B>(p, load_row(p, t + lane), back, t, t_end, t_now == t_begin, threadIdx.x == 0);
         if (w.run == 0) continue;
         // the scale of each run's page, and no other run at that page from here on
         const unsigned page = (unsigned)max(w.blk, 0) * Hkv + head;  // (pages are 1 KB or more)
@@ -606,6 +609,7 @@ q8_stream_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
 
     int t = t_begin;
     RawRow raw = load_row(p, t + lane);
+    const RawRow back = load_row(p, t - 1 - lane);
     auto find = [&](int i) {
         Found& x = found[i % Q8_FOUND];
         Window w;
@@ -613,7 +617,7 @@ q8_stream_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
         int t_now = t;
         while (t < t_end && w.run == 0) {
             t_now = t;
-            w = find_window<B>(p, raw, t, t_end, t_now == t_begin, lane == 0);
+            w = find_window<B>(p, raw, back, t, t_end, t_now == t_begin, lane == 0);
             if (w.run == 0) raw = load_row(p, t + lane);
         }
         if (w.run != 0) {

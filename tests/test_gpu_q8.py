@@ -132,6 +132,50 @@ def test_write_of_many_tokens(P, T):
     assert P.pkv_get_device_error() == 0
 
 
+@pytest.mark.parametrize("Hq,Hkv,D,B", [(4, 2, 64, 16), (4, 2, 64, 32), (8, 2, 128, 16), (5, 5, 128, 32), (12, 12, 64, 16),
+                                        (9, 9, 128, 16)])
+@pytest.mark.parametrize("dt,norm,rot,interleaved", [("bf16", True, None, False), ("f16", False, 32, True),
+                                                     ("bf16", True, 0, False)])
+def test_write_of_streamed_tokens(P, Hq, Hkv, D, B, dt, norm, rot, interleaved):
+    # whole prompts, parts that begin and end inside blocks, short runs side by side, rows without a token
+    spans = [(0, 500), (13, 300), (7, 1), (40, 2), (16, 16), (0, 0), (3, 60)] + [(i % 50, 1 + i % 3) for i in range(120)]
+    w = Write(spans, Hq, Hkv, D, B, DTYPE[dt], seed=D + B, norm=norm, rot=rot, interleaved=interleaved, pad=40)
+    assert w.T > 1024
+    w.run(P)
+    w.check()
+    assert P.pkv_get_device_error() == 0
+
+
+def test_write_of_streamed_decoding_requests(P):
+    w = Write([(i % 70, 1) for i in range(1100)], 2, 2, 128, 16, torch.bfloat16, seed=1)
+    w.run(P)
+    w.check()
+    assert P.pkv_get_device_error() == 0
+
+
+def test_write_of_streamed_numbers_that_are_not_finite_and_bad_rows(P):
+    w = Write([(0, 700), (5, 400)], 2, 2, 64, 16, torch.float16, seed=2, norm=False, rot=0, size=4.0)
+    _, k, v = w.rows(w.x)
+    k[3, 0, 5], v[40, 1, 7], v[719, 0, 0] = float("inf"), float("nan"), float("-inf")
+    k[64:80, 1] = float("nan")     # a page with nothing finite
+    w.run(P)
+    w.check()
+    assert P.pkv_get_device_error() == 0
+    w = Write([(0, 700), (5, 400)], 2, 2, 64, 16, torch.float16, seed=2)
+    w.pos[30], w.slots[705] = w.cos_sin.shape[0], w.N * 16
+    w.run(P)
+    assert P.pkv_get_device_error() == P.DEVERR["POSITION"] | P.DEVERR["SLOT"]
+    w.pos[30], w.slots[30], w.slots[705] = -1, -1, -1   # as if there were no token, and no key and value
+    w.q_out[30] = 7
+    w.check()
+    w = Write([(0, 16), (0, 1100)], 2, 1, 64, 16, torch.float16, seed=3)
+    w.slots[8:16] = w.slots[0:8].clone()              # a block's first slots a second time
+    w.run(P)
+    assert P.pkv_get_device_error() == P.DEVERR["SLOT"]
+    w.slots[8:16] = -1
+    w.check()
+
+
 @pytest.mark.parametrize("size", [1e-4, 30.0, 300.0])
 def test_write_grows_a_page_and_keeps_its_scale(P, size):
     # a page's scale rises with larger numbers, its rows rounded again, and never falls
@@ -305,6 +349,17 @@ def test_decode_equals_the_plain_model(P, D, B, Hq, Hkv, NQ):
         d = Decode(lens, NQ, Hq, Hkv, D, B, dt, seed=D + Hq)
         for out_dtype in (dt, torch.float32):
             d.check(d.run(P, out_dtype))
+    assert P.pkv_get_device_error() == 0
+
+
+@pytest.mark.parametrize("Hq,Hkv,NQ,D", [(32, 2, 1, 128), (16, 2, 3, 64), (20, 1, 1, 64)])
+def test_decode_of_large_batches_of_many_columns(P, Hq, Hkv, NQ, D):
+    # 16 columns a CTA; contexts of one and of several pieces
+    lens = [1 + (i * 389) % 700 for i in range(1000)] + [1500]
+    d = Decode(lens, NQ, Hq, Hkv, D, 16, torch.bfloat16, seed=Hq)
+    d.check(d.run(P))
+    d.check(d.run(P, torch.float32, 512))
+    d.check(d.run(P, torch.float32, 128))
     assert P.pkv_get_device_error() == 0
 
 

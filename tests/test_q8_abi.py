@@ -111,11 +111,12 @@ def test_decode_refusals(P):
 def test_decode_workspace(P):
     size = lambda *a: P.lib.pkv_decode_q8_workspace_bytes(ctypes.byref(_pool(P)), *a)  # noqa: E731
     assert size(2, 1, 4, 64, 64) == 0                         # one piece
-    n = size(2, 1, 4, 64, 16)                                 # four: m, l and 128 numbers a row and piece
-    assert n == 2 * 1 * 4 * 4 * (2 + 128) * 4
-    assert _decode(P, part=16) == P.PKV_ERR_WORKSPACE
-    assert _decode(P, part=16, ws=D16, wsb=n - 1) == P.PKV_ERR_WORKSPACE
-    assert _decode(P, part=16, ws=ODD, wsb=n) == P.PKV_ERR_WORKSPACE
+    assert size(2, 1, 4, 128, 16) == 0                        # eight, which meet in a cluster
+    n = size(2, 1, 4, 129, 16)                                # nine: m, l and 128 numbers a row and piece
+    assert n == 2 * 1 * 4 * 9 * (2 + 128) * 4
+    assert _decode(P, ctx=129, part=16) == P.PKV_ERR_WORKSPACE
+    assert _decode(P, ctx=129, part=16, ws=D16, wsb=n - 1) == P.PKV_ERR_WORKSPACE
+    assert _decode(P, ctx=129, part=16, ws=ODD, wsb=n) == P.PKV_ERR_WORKSPACE
     for bad in ((-1, 1, 4, 64, 16), (2, 0, 4, 64, 16), (2, 1, 3, 64, 16), (2, 1, 0, 64, 16), (2, 1, 4, -1, 16),
                 (2, 1, 4, 64, -16)):
         assert size(*bad) == 0, bad
