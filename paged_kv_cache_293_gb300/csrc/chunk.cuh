@@ -101,7 +101,10 @@ struct ChunkReference<__half> {
 // heads, contexts about 300: 79 us (93 with 4 rows).
 constexpr int CHUNK_FEW_ROWS = 16;
 
-// Q8: pages of e4m3 values arrive in a ring of their own, and the stages hold them as numbers.
+// Q8: pages of e4m3 values arrive in a ring of their own, and the stages hold them as numbers of the products' types.
+// Steps whose references (below) are kept: a step's are written when its copies are issued, at most
+// RAW_STAGES + STAGES stages before its products, and read by the softmax, at most two steps later.
+constexpr int Q8_STEP_RING = 16;
 template <int D, bool Q8>
 struct ChunkSmem {
     static constexpr int BOXES = D / 64;                  // 128-byte columns of a row
@@ -114,7 +117,8 @@ struct ChunkSmem {
     static constexpr int KV_OFF = 2 * TILE;
     static constexpr int RAW_OFF = KV_OFF + STAGES * TILE;
     static constexpr int SCALE_OFF = RAW_OFF + RAW_STAGES * RAW_TILE;  // float [RAW_STAGES][8 copies]
-    static constexpr int BAR_OFF = SCALE_OFF + RAW_STAGES * 32;
+    static constexpr int STEP_OFF = SCALE_OFF + RAW_STAGES * 32;       // float2 [Q8_STEP_RING]
+    static constexpr int BAR_OFF = STEP_OFF + (Q8 ? Q8_STEP_RING * 8 : 0);
     static constexpr int NBARS = 2 * STAGES + 31 + 2 * RAW_STAGES;
     static constexpr int PIECE_OFF = BAR_OFF + ((NBARS * 8 + 15) / 16) * 16;
     static constexpr int STAT_OFF = PIECE_OFF + 2 * 32;  // float [2 tiles][m, l][128 rows]
@@ -204,13 +208,21 @@ __device__ __noinline__ void add_total(uint32_t o_t, float4* kept, float f, bool
     umma::fence_before_sync();
 }
 
+// 2 to a whole number from -126 to 127.  (The sum holds it in its last bits.)
+__device__ __forceinline__ float two_to(float x) {
+    return __int_as_float((__float_as_int(x + 12582912.f) - 0x4b400000 + 127) << 23);
+}
+
 // One step of a row: its 128 scores from tensor memory at s_t, the running reference m_ref and
 // the sum (in two parts), its O at o_t scaled where the reference rose (once phase_o of
 // bar_o says that the products before are done; 0: known), and its weights written over the
 // scores, the halves handed on at bar_lo and bar_hi.
-template <typename T, int D, bool SPLIT_P, bool EDGE>
+// Q8: the values of this step are 2^lv smaller than they should be, so its weights are taken 2^lv
+// times as large, the reference with them, and count for that much less in the sum.
+// (exponent() reads lv from shared memory: a second time at the end, so that no register keeps it.)
+template <typename T, int D, bool SPLIT_P, bool EDGE, bool Q8, typename Exponent>
 __device__ __forceinline__ bool softmax_step(uint32_t s_t, uint32_t o_t, int seen, bool has_o,
-                                             float scale_log2, float& m_ref, uint64_t& sum2,
+                                             float scale_log2, const Exponent& exponent, float& m_ref, uint64_t& sum2,
                                              uint32_t bar_lo, uint32_t bar_hi, uint32_t bar_o,
                                              uint32_t phase_o) {
     constexpr int N = CHUNK_TILE, HALF = N / 2;
@@ -243,15 +255,16 @@ __device__ __forceinline__ bool softmax_step(uint32_t s_t, uint32_t o_t, int see
         }
     }
     using Ref = ChunkReference<T>;
-    const float cm = Ref::scaled(
-        max3(max3(top[0], top[1], top[2]), max3(top[3], top[4], top[5]), fmaxf(top[6], top[7])), scale_log2);
+    const float most = max3(max3(top[0], top[1], top[2]), max3(top[3], top[4], top[5]), fmaxf(top[6], top[7]));
+    const float lv = exponent();
+    const float cm = Q8 ? __fmaf_ru(most, scale_log2, lv) : Ref::scaled(most, scale_log2);
     const bool need = cm - m_ref > Ref::RAISE;
     float alpha = 1.f;
     if (need) {
         alpha = fast_exp2(m_ref - (cm - Ref::BELOW));
         m_ref = cm - Ref::BELOW;
     }
-    const float neg = m_ref == -INFINITY ? 0.f : -m_ref;
+    const float neg = m_ref == -INFINITY ? 0.f : Q8 ? lv - m_ref : -m_ref;
     const uint64_t scale2 = pack2(scale_log2, scale_log2), neg2 = pack2(neg, neg);
     sum2 = mul2(sum2, pack2(alpha, alpha));
     uint64_t step2[2] = {0, 0};
@@ -293,7 +306,12 @@ __device__ __forceinline__ bool softmax_step(uint32_t s_t, uint32_t o_t, int see
             if (lane == 0) mbar_arrive(bar_lo);
         }
     }
-    sum2 = add2(sum2, add2(step2[0], step2[1]));
+    if (Q8) {
+        const float by = two_to(-exponent());
+        sum2 = fma2(add2(step2[0], step2[1]), pack2(by, by), sum2);
+    } else {
+        sum2 = add2(sum2, add2(step2[0], step2[1]));
+    }
     umma::wait_st();
     umma::fence_before_sync();
     __syncwarp();
@@ -303,9 +321,9 @@ __device__ __forceinline__ bool softmax_step(uint32_t s_t, uint32_t o_t, int see
 
 // One step of a row of a piece with few rows: this warp's 32 scores at s_t, the reference, sum
 // and O as in softmax_step, the weights to p_t.  The caller hands them on.
-template <typename T, int D>
+template <typename T, int D, bool Q8>
 __device__ __forceinline__ bool few_rows_step(uint32_t s_t, uint32_t p_t, uint32_t o_t, int seen, bool has_o,
-                                              float scale_log2, float& m_ref, float& l, uint32_t bar_o,
+                                              float scale_log2, float lv, float& m_ref, float& l, uint32_t bar_o,
                                               uint32_t phase_o) {
     uint32_t raw[32];
     umma::ld32_async(s_t, raw);
@@ -324,7 +342,8 @@ __device__ __forceinline__ bool few_rows_step(uint32_t s_t, uint32_t p_t, uint32
             top[c] = max3(top[c], __uint_as_float(raw[k]), __uint_as_float(raw[k + 4 < 28 ? k + 4 : k]));
     }
     using Ref = ChunkReference<T>;
-    const float cm = Ref::scaled(max3(top[0], top[1], fmaxf(top[2], top[3])), scale_log2);
+    const float most = max3(top[0], top[1], fmaxf(top[2], top[3]));
+    const float cm = Q8 ? __fmaf_ru(most, scale_log2, lv) : Ref::scaled(most, scale_log2);
     const bool need = cm - m_ref > Ref::RAISE;
     if (__any_sync(FULL_MASK, need)) {
         float alpha = 1.f;
@@ -347,7 +366,7 @@ __device__ __forceinline__ bool few_rows_step(uint32_t s_t, uint32_t p_t, uint32
             }
         }
     }
-    const float neg = m_ref == -INFINITY ? 0.f : -m_ref;
+    const float neg = m_ref == -INFINITY ? 0.f : Q8 ? lv - m_ref : -m_ref;
     const uint64_t scale2 = pack2(scale_log2, scale_log2), neg2 = pack2(neg, neg);
     uint64_t sum2[2] = {0, 0};
     uint32_t hi[16];
@@ -364,56 +383,79 @@ __device__ __forceinline__ bool few_rows_step(uint32_t s_t, uint32_t p_t, uint32
     float part[4];
     unpack2(sum2[0], part[0], part[1]);
     unpack2(sum2[1], part[2], part[3]);
-    l += (part[0] + part[1]) + (part[2] + part[3]);
+    const float sum = (part[0] + part[1]) + (part[2] + part[3]);
+    l = Q8 ? fmaf(sum, two_to(-lv), l) : l + sum;
     umma::wait_st();
     umma::fence_before_sync();
     __syncwarp();
     return true;
 }
 
-// Two fp16 values as 32-bit ones, times s, rounded to two of the type of the products.
-template <typename T>
-__device__ __forceinline__ uint32_t scaled_pair(uint32_t h, uint64_t s2) {
-    const float2 v = float2_of_f16x2(h);
-    float a, b;
-    unpack2(mul2(pack2(v.x, v.y), s2), a, b);
-    return Mma<T>::pack(a, b);
-}
+// A raw tile (128 tokens of D e4m3 values, rows behind one another) into a stage's K or V tile of 16-bit
+// numbers, times a factor per copy of 16 tokens, by four warps: 16 values a lane at a time, which become
+// two 16-byte columns.  Eight lanes read 128 bytes in a row, and write eight different columns of the
+// 128-byte swizzle (with D = 128 the lanes of the second half store their odd column first).  To fp16,
+// factors that it holds, as those between powers of two are, multiply in fp16, and factors of 1 not at
+// all; others, and all to bf16, in 32 bits, so that each number is rounded once.
+enum class Factor { ONE, HALF, SINGLE };
 
-// A raw tile (128 tokens of D e4m3 values, rows behind one another) into a stage's K or V tile, by
-// four warps: 16 values a lane at a time, which become two 16-byte columns.  Eight lanes read 128
-// bytes in a row, and write eight different columns of the 128-byte swizzle (with D = 128 the lanes of
-// the second half store their odd column first).
-template <typename T, int D>
-__device__ __forceinline__ void numbers_of_tile(const unsigned char* raw, const float* scale, unsigned char* tile,
-                                                bool is_v, int w, int lane) {
+template <typename M, int D, Factor BY, int UNROLL>
+__device__ __forceinline__ void numbers_by(const unsigned char* raw, const float* factor, unsigned char* tile,
+                                           bool is_v, int w, int lane) {
     constexpr int LANES = D / 16, ROWS = 32 / LANES;    // lanes a row, rows a warp at a time
     constexpr int STEPS = 128 / (4 * ROWS);
     const int m = lane % LANES, box = m / 4, col = 2 * (m % 4);
-#pragma unroll 2
+    const bool swap = box == 1;
+    // rows (i * 4 + w) * ROWS + lane / LANES: whole copies of 16 rows a step apart
+    const int row0 = w * ROWS + lane / LANES, r = row0 % CHUNK_TOKENS, b0 = row0 / CHUNK_TOKENS;
+    constexpr int COPIES = 4 * ROWS / CHUNK_TOKENS;     // copies a step
+    unsigned char* at = is_v ? tile + b0 * (CHUNK_TOKENS * D * 2) + box * (CHUNK_TOKENS * 128) + r * 128
+                             : tile + box * (128 * 128) + row0 * 128;
+    const int stride = is_v ? COPIES * CHUNK_TOKENS * D * 2 : 4 * ROWS * 128;
+    at += ((col + swap) ^ (r & 7)) << 4;
+    const int other = ((((col + swap) ^ 1) ^ (r & 7)) << 4) - (((col + swap) ^ (r & 7)) << 4);
+    raw += row0 * D + m * 16;
+    // (short loops: the code of all roles shares the instruction cache; whole, they cost a prompt 10 %)
+#pragma unroll(UNROLL)
     for (int i = 0; i < STEPS; ++i) {
-        const int row = (i * 4 + w) * ROWS + lane / LANES, b = row / CHUNK_TOKENS, r = row % CHUNK_TOKENS;
-        const uint4 x = *reinterpret_cast<const uint4*>(raw + row * D + m * 16);
-        const float s = scale[b];
-        const uint64_t s2 = pack2(s, s);
+        const uint4 x = *reinterpret_cast<const uint4*>(raw + i * 4 * ROWS * D);
         const uint32_t in[4] = {x.x, x.y, x.z, x.w};
         uint32_t out[8];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            uint32_t lo, hi;
-            f16x4_of_e4m3x4(in[k], lo, hi);
-            out[2 * k] = scaled_pair<T>(lo, s2);
-            out[2 * k + 1] = scaled_pair<T>(hi, s2);
+        for (int k = 0; k < 4; ++k) f16x4_of_e4m3x4(in[k], out[2 * k], out[2 * k + 1]);
+        if (BY != Factor::ONE) {
+            const float s = factor[b0 + i * COPIES];
+            const __half2 h2 = __half2half2(__float2half_rn(s));
+            const uint64_t s2 = pack2(s, s);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                if (BY == Factor::HALF) {
+                    const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&out[k]), h2);
+                    out[k] = *reinterpret_cast<const uint32_t*>(&v);
+                } else {
+                    const float2 v = float2_of_f16x2(out[k]);
+                    float a, c;
+                    unpack2(mul2(pack2(v.x, v.y), s2), a, c);
+                    out[k] = Mma<M>::pack(a, c);
+                }
+            }
         }
-        unsigned char* const at = is_v ? tile + b * (CHUNK_TOKENS * D * 2) + box * (CHUNK_TOKENS * 128) + r * 128
-                                       : tile + box * (128 * 128) + row * 128;
-        uint4* const even = reinterpret_cast<uint4*>(at + ((col ^ (r & 7)) << 4));
-        uint4* const odd = reinterpret_cast<uint4*>(at + (((col + 1) ^ (r & 7)) << 4));
         const uint4 lo4 = make_uint4(out[0], out[1], out[2], out[3]), hi4 = make_uint4(out[4], out[5], out[6], out[7]);
-        const bool swap = box == 1;
-        *(swap ? odd : even) = swap ? hi4 : lo4;
-        *(swap ? even : odd) = swap ? lo4 : hi4;
+        *reinterpret_cast<uint4*>(at + i * stride) = swap ? hi4 : lo4;
+        *reinterpret_cast<uint4*>(at + i * stride + other) = swap ? lo4 : hi4;
     }
+}
+
+template <typename M, int D>
+__device__ __forceinline__ void numbers_of_tile(const unsigned char* raw, const float* factor, unsigned char* tile,
+                                                bool is_v, int w, int lane) {
+    const float mine = factor[lane % 8];
+    if (!std::is_same<M, __half>::value)
+        numbers_by<M, D, Factor::SINGLE, 2>(raw, factor, tile, is_v, w, lane);
+    else if (__all_sync(FULL_MASK, __half2float(__float2half_rn(mine)) == mine))
+        numbers_by<__half, D, Factor::HALF, 2>(raw, factor, tile, is_v, w, lane);
+    else
+        numbers_by<__half, D, Factor::SINGLE, 1>(raw, factor, tile, is_v, w, lane);
 }
 
 template <typename T, int D, bool SPLIT_P, bool Q8>
@@ -426,10 +468,15 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
     constexpr int NS = L::STAGES, KS = D / 16;
     constexpr int KV_WARP = 8, MMA_WARP = 9, Q_WARP = 10, OUT_WARP = 12;
     constexpr int CONSUMERS = 8 + 2 + 4;  // arrivals that free a slot of the piece ring
+    // The type of the weights and values: over 8-bit pools fp16, which holds every e4m3 value and takes
+    // fewest instructions to reach.  Keys have the queries' type.
+    using M = typename std::conditional<Q8, __half, T>::type;
+    constexpr bool KEYS_F16 = std::is_same<T, __half>::value;
     constexpr uint32_t FMT = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
+    constexpr uint32_t FMT_O = std::is_same<M, __nv_bfloat16>::value ? 1u : 0u;
     constexpr uint32_t IDESC_S = umma::idesc_f16(FMT, false, 128, CHUNK_TILE);
     const uint32_t idesc_s = IDESC_S | (p.negate ? umma::IDESC_NEGATE_A : 0u);
-    constexpr uint32_t IDESC_O = umma::idesc_f16(FMT, true, 128, D);
+    constexpr uint32_t IDESC_O = umma::idesc_f16(FMT_O, true, 128, D);
 
     // the swizzle repeats every 1024 bytes; no static shared memory lies before this array
     extern __shared__ __align__(1024) unsigned char chunk_smem[];
@@ -467,6 +514,8 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
     auto raw_full = [&](int st) { return bar0 + 8 * (NB + 31 + st); };
     auto raw_empty = [&](int st) { return bar0 + 8 * (NB + 31 + NR + st); };
     float* raw_scale = reinterpret_cast<float*>(smem + L::SCALE_OFF);
+    // of the n-th step of this CTA: what its keys are smaller by (fp16 ones), and its values (in base 2)
+    float2* step_ref = reinterpret_cast<float2*>(smem + L::STEP_OFF);
     float* stats = reinterpret_cast<float*>(smem + L::STAT_OFF);  // + 256 t: m, + 128: l
     auto is_few = [&](const ChunkPiece& x) {
         return !SPLIT_P && x.queries * G <= CHUNK_FEW_ROWS && x.kt1 > x.kt0;
@@ -569,19 +618,37 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
                 };
                 int row = row_of(pc.kt0);
                 // Q8: the scales of this lane's copy (far_row: a multiple of B, past the last page)
-                float k_scale = 0.f, v_scale = 0.f;
+                float scale_next[2] = {0.f, 0.f};
                 auto scales_of = [&](int row) {
-                    k_scale = v_scale = 0.f;
+                    scale_next[0] = scale_next[1] = 0.f;
                     if (row != far_row) {
-                        k_scale = __ldg(p.k_scale + row / B);
-                        v_scale = __ldg(p.v_scale + row / B);
+                        scale_next[0] = __ldg(p.k_scale + row / B);
+                        scale_next[1] = __ldg(p.v_scale + row / B);
                     }
                 };
                 if constexpr (Q8) scales_of(row);
                 for (int kt = pc.kt0; kt < pc.kt1 && ok; ++kt) {
                     const int row_next = row_of(kt + 1);
-                    const float scale_now[2] = {k_scale, v_scale};
-                    if constexpr (Q8) scales_of(row_next);
+                    // Q8: in fp16 a step's pages enter the products relative to the largest scale among them,
+                    // of values to the power of two that reaches it, which goes into the exponents; numbers of
+                    // pages far smaller than that lose bits in fp16's last steps, 2^-33 of the step's largest
+                    float factor[2] = {0.f, 0.f};
+                    if constexpr (Q8) {
+                        float most[2];
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            most[k] = fabsf(scale_next[k]);
+#pragma unroll
+                            for (int o = 4; o >= 1; o >>= 1) most[k] = fmaxf(most[k], __shfl_xor_sync(FULL_MASK, most[k], o));
+                        }
+                        // (values below 2^-69 of numbers that 8 bits hold at a scale of 1 fade out)
+                        const int bits = __float_as_int(most[1]);
+                        const int lv = max((bits >> 23) - 127 + ((bits & 0x7fffff) != 0), -60);
+                        factor[0] = !KEYS_F16 ? scale_next[0] : most[0] > 0.f ? scale_next[0] / most[0] : 0.f;
+                        factor[1] = scale_next[1] * __int_as_float((127 - min(lv, 126)) << 23);
+                        if (lane == 0) step_ref[(it / 2) % Q8_STEP_RING] = make_float2(most[0], (float)min(lv, 126));
+                        scales_of(row_next);
+                    }
                     int rows[NBOX];
 #pragma unroll
                     for (int b = 0; b < NBOX; ++b) rows[b] = __shfl_sync(FULL_MASK, row, b);
@@ -593,7 +660,7 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
                                 ok = __all_sync(FULL_MASK, mbar_wait_short(raw_empty(st), ((it / NR) - 1) & 1));
                                 if (!ok) break;
                             }
-                            if (lane < NBOX) raw_scale[st * NBOX + lane] = scale_now[kv];
+                            if (lane < NBOX) raw_scale[st * NBOX + lane] = factor[kv];
                             __syncwarp();  // the scales are there before the arrival that tells of the tile
                             if (umma::elect_one()) {
                                 const uint32_t full = raw_full(st), dst = sbase + L::RAW_OFF + st * L::RAW_TILE;
@@ -872,8 +939,12 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
                 if (made >= NS && !__all_sync(FULL_MASK, mbar_wait_short(kv_empty(st), (made / NS - 1) & 1)))
                     return false;
                 // (even ones are K's)
-                numbers_of_tile<T, D>(smem + L::RAW_OFF + from * L::RAW_TILE, raw_scale + from * 8,
-                                      smem + L::KV_OFF + st * L::TILE, made & 1, w, lane);
+                const unsigned char* const raw = smem + L::RAW_OFF + from * L::RAW_TILE;
+                unsigned char* const tile = smem + L::KV_OFF + st * L::TILE;
+                if (KEYS_F16 || (made & 1))
+                    numbers_of_tile<M, D>(raw, raw_scale + from * 8, tile, made & 1, w, lane);
+                else
+                    numbers_of_tile<T, D>(raw, raw_scale + from * 8, tile, false, w, lane);
                 umma::fence_smem_to_async();
                 __syncwarp();
                 if (lane == 0) {
@@ -883,21 +954,33 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
             }
             return true;
         };
+        // Of the piece at work and the next one only their steps are needed here, so that the registers are
+        // free for the numbers: the record stays where it is until the output.
         constexpr int AHEAD = 2;
-        ChunkPiece pc, following;
-        bool any = Q8 && next_piece(0, following);
+        int steps_next = 0;
+        auto look_at = [&](int i) -> bool {
+            ok = __all_sync(FULL_MASK, mbar_wait_short(piece_full(i & 1), (i >> 1) & 1));
+            if (!ok) return false;
+            const ChunkPiece& x = pieces[i & 1];
+            steps_next = max(x.kt1 - x.kt0, 0);
+            return x.kv_head >= 0;
+        };
+        ChunkPiece pc;
+        bool any = Q8 && look_at(0);
         int ahead = 0;  // stages of the next piece that are made already
         for (int i = 0;; ++i) {
             if constexpr (Q8) {
                 if (!any) break;
-                pc = following;
-                ok = make_stages(2 * max(pc.kt1 - pc.kt0, 0) - ahead);
+                ok = make_stages(2 * steps_next - ahead);
                 if (!ok) break;
-                any = next_piece(i + 1, following);
+                any = look_at(i + 1);
                 if (!ok) break;
-                ahead = any ? min(AHEAD, 2 * max(following.kt1 - following.kt0, 0)) : 0;
+                ahead = any ? min(AHEAD, 2 * steps_next) : 0;
                 ok = make_stages(ahead);
                 if (!ok) break;
+                pc = pieces[i & 1];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(piece_empty(i & 1));
             } else if (!next_piece(i, pc)) {
                 break;
             }
@@ -1050,6 +1133,14 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
         const int jq = t * QPT + r / G;                // query within the piece
         int taken = 0, taken_even = 0, taken_odd = 0;  // S tiles so far: the phases of s_full and pv_step
         int outs = 0, twos = 0;  // pieces handed to the output warps, those with two tiles: of o_free
+        uint32_t steps = 0;      // Q8: of the pieces before, as step_ref counts them
+        // what the scores of step j of the piece are multiplied with (positive, though nothing be left of it:
+        // hidden scores are -inf), and the exponent that its weights are larger by
+        auto step_scale = [&](int j) -> float {
+            if constexpr (!Q8 || !KEYS_F16) return p.scale_log2;
+            return fmaxf(p.scale_log2 * step_ref[(steps + j) % Q8_STEP_RING].x, 1.2e-38f);
+        };
+        auto step_exponent = [&](int j) -> float { return Q8 ? step_ref[(steps + j) % Q8_STEP_RING].y : 0.f; };
         bool p_clear = false;    // the P columns of pieces with few rows hold zeros where they should
         // The row's totals of the steps before, in the workspace: O's, then the sum and their
         // reference (not in registers, which the steps need).
@@ -1097,7 +1188,10 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
         for (int i = 0; next_piece(i, pc); ++i) {
             const int n = max(pc.kt1 - pc.kt0, 0);
             const bool two = pc.queries > QPT;
-            if (n == 0 || (t == 1 && !two)) continue;  // one tile: the other warpgroup takes both S tiles
+            if (n == 0 || (t == 1 && !two)) {  // one tile: the other warpgroup takes both S tiles
+                steps += n;
+                continue;
+            }
             if (is_few(pc)) {
                 // Few rows: warp w has them all, in its own 32 lanes, and of every step the tokens
                 // 32 w .. 32 w + 31, its own reference, sum and O; its P holds zeros for the other
@@ -1132,10 +1226,11 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
                         ok = __all_sync(FULL_MASK, mbar_wait_short(s_full(2 + b), phase & 1));
                         if (!ok) break;
                         umma::fence_after_sync();
-                        ok = few_rows_step<T, D>(lane_tmem + b * CHUNK_TILE + warp * 32,
-                                                 p_t + b * (CHUNK_TILE / 2) + warp * 16, o_t,
-                                                 lim_w - (pc.kt0 + j) * CHUNK_TILE, j > 0, p.scale_log2, m_ref, l,
-                                                 pv_step(b ^ 1), (b ? taken_even : taken_odd) - 1);
+                        const float by = step_scale(j), lv = step_exponent(j);
+                        ok = few_rows_step<M, D, Q8>(lane_tmem + b * CHUNK_TILE + warp * 32,
+                                                     p_t + b * (CHUNK_TILE / 2) + warp * 16, o_t,
+                                                     lim_w - (pc.kt0 + j) * CHUNK_TILE, j > 0, by, lv, m_ref, l,
+                                                     pv_step(b ^ 1), (b ? taken_even : taken_odd) - 1);
                         if (!ok) break;
                         if (lane == 0) {
                             mbar_arrive(p_full(2 + b, 0));
@@ -1147,6 +1242,7 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
                     ok = products_before(n, false, true);
                     if (ok) l = total(m_ref, l);
                 }
+                steps += n;
                 if (!ok || !hand_out(m_ref, l)) break;
                 continue;
             }
@@ -1173,17 +1269,19 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
                     if (!ok) break;
                     if (busy) {
                         umma::fence_after_sync();
+                        const float by = step_scale(j);
+                        auto lv = [&] { return step_exponent(j); };
                         const uint32_t s_t = lane_tmem + (b & 1) * CHUNK_TILE;
                         const int seen = lim - (pc.kt0 + j) * CHUNK_TILE;  // columns this row may see
                         // with two tiles a step's S was committed after the P.V before, with one not
                         const uint32_t wait_o = two ? 0u : pv_step((j & 1) ^ 1);
                         const int phase_o = ((j & 1) ? taken_even : taken_odd) - 1;
                         if (__any_sync(FULL_MASK, seen < CHUNK_TILE))
-                            ok = softmax_step<T, D, SPLIT_P, true>(s_t, o_t, seen, j > 0, p.scale_log2, m_ref, sum2,
-                                                                   p_full(b, 0), p_full(b, 1), wait_o, phase_o);
+                            ok = softmax_step<M, D, SPLIT_P, true, Q8>(s_t, o_t, seen, j > 0, by, lv, m_ref, sum2,
+                                                                       p_full(b, 0), p_full(b, 1), wait_o, phase_o);
                         else
-                            ok = softmax_step<T, D, SPLIT_P, false>(s_t, o_t, seen, j > 0, p.scale_log2, m_ref, sum2,
-                                                                    p_full(b, 0), p_full(b, 1), wait_o, phase_o);
+                            ok = softmax_step<M, D, SPLIT_P, false, Q8>(s_t, o_t, seen, j > 0, by, lv, m_ref, sum2,
+                                                                        p_full(b, 0), p_full(b, 1), wait_o, phase_o);
                         if (!ok) break;
                     } else if (lane == 0) {  // rows of no query: whatever S left there
                         mbar_arrive(p_full(b, 0));
@@ -1192,6 +1290,7 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
                 }
             }
             if (!ok) break;
+            steps += n;
             float l = sum();
             if (busy && n > CHUNK_SUM_STEPS) {
                 ok = products_before(n, two, true);
