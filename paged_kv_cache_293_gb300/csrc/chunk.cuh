@@ -220,8 +220,9 @@ __device__ __forceinline__ float two_to(float x) {
 // Q8: the values of this step are 2^lv smaller than they should be, so its weights are taken 2^lv
 // times as large, the reference with them, and count for that much less in the sum.
 // (exponent() reads lv from shared memory: a second time at the end, so that no register keeps it.)
-template <typename T, int D, bool SPLIT_P, bool EDGE, bool Q8, typename Exponent>
-__device__ __forceinline__ bool softmax_step(uint32_t s_t, uint32_t o_t, int seen, bool has_o,
+// edge: the warp has scores that their rows do not see.
+template <typename T, int D, bool SPLIT_P, bool Q8, typename Edge, typename Exponent>
+__device__ __forceinline__ bool softmax_step(uint32_t s_t, uint32_t o_t, int seen, const Edge edge, bool has_o,
                                              float scale_log2, const Exponent& exponent, float& m_ref, uint64_t& sum2,
                                              uint32_t bar_lo, uint32_t bar_hi, uint32_t bar_o,
                                              uint32_t phase_o) {
@@ -239,7 +240,7 @@ __device__ __forceinline__ bool softmax_step(uint32_t s_t, uint32_t o_t, int see
             umma::ld32_async(s_t + HALF, raw + HALF);
             umma::ld32_async(s_t + HALF + 32, raw + HALF + 32);
         }
-        if (EDGE) {
+        if (edge) {
 #pragma unroll
             for (int k = h * HALF; k < (h + 1) * HALF; ++k)
                 if (k >= seen) raw[k] = 0xff800000u;  // -inf
@@ -627,28 +628,27 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
                     }
                 };
                 if constexpr (Q8) scales_of(row);
+                // In fp16 a step's pages enter the products relative to the largest scale among them, of values
+                // to the power of two that reaches it, which goes into the exponents; numbers of pages far
+                // smaller than that lose bits in fp16's last steps, 2^-33 of the step's largest.
+                float factor[2] = {0.f, 0.f};
+                auto make_factors = [&] {
+                    float most[2];
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        most[k] = fabsf(scale_next[k]);
+#pragma unroll
+                        for (int o = 4; o >= 1; o >>= 1) most[k] = fmaxf(most[k], __shfl_xor_sync(FULL_MASK, most[k], o));
+                    }
+                    // (values below 2^-69 of numbers that 8 bits hold at a scale of 1 fade out)
+                    const int bits = __float_as_int(most[1]);
+                    const int lv = min(max((bits >> 23) - 127 + ((bits & 0x7fffff) != 0), -60), 126);
+                    factor[0] = !KEYS_F16 ? scale_next[0] : most[0] > 0.f ? scale_next[0] / most[0] : 0.f;
+                    factor[1] = scale_next[1] * __int_as_float((127 - lv) << 23);
+                    if (lane == 0) step_ref[(it / 2) % Q8_STEP_RING] = make_float2(most[0], (float)lv);
+                };
                 for (int kt = pc.kt0; kt < pc.kt1 && ok; ++kt) {
                     const int row_next = row_of(kt + 1);
-                    // Q8: in fp16 a step's pages enter the products relative to the largest scale among them,
-                    // of values to the power of two that reaches it, which goes into the exponents; numbers of
-                    // pages far smaller than that lose bits in fp16's last steps, 2^-33 of the step's largest
-                    float factor[2] = {0.f, 0.f};
-                    if constexpr (Q8) {
-                        float most[2];
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            most[k] = fabsf(scale_next[k]);
-#pragma unroll
-                            for (int o = 4; o >= 1; o >>= 1) most[k] = fmaxf(most[k], __shfl_xor_sync(FULL_MASK, most[k], o));
-                        }
-                        // (values below 2^-69 of numbers that 8 bits hold at a scale of 1 fade out)
-                        const int bits = __float_as_int(most[1]);
-                        const int lv = max((bits >> 23) - 127 + ((bits & 0x7fffff) != 0), -60);
-                        factor[0] = !KEYS_F16 ? scale_next[0] : most[0] > 0.f ? scale_next[0] / most[0] : 0.f;
-                        factor[1] = scale_next[1] * __int_as_float((127 - min(lv, 126)) << 23);
-                        if (lane == 0) step_ref[(it / 2) % Q8_STEP_RING] = make_float2(most[0], (float)min(lv, 126));
-                        scales_of(row_next);
-                    }
                     int rows[NBOX];
 #pragma unroll
                     for (int b = 0; b < NBOX; ++b) rows[b] = __shfl_sync(FULL_MASK, row, b);
@@ -660,16 +660,20 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
                                 ok = __all_sync(FULL_MASK, mbar_wait_short(raw_empty(st), ((it / NR) - 1) & 1));
                                 if (!ok) break;
                             }
-                            if (lane < NBOX) raw_scale[st * NBOX + lane] = factor[kv];
-                            __syncwarp();  // the scales are there before the arrival that tells of the tile
+                            // the copies first, while the scales are on their way, and the arrival that tells of
+                            // both when these are there
                             if (umma::elect_one()) {
                                 const uint32_t full = raw_full(st), dst = sbase + L::RAW_OFF + st * L::RAW_TILE;
-                                mbar_arrive_expect_tx(full, L::RAW_TILE);
 #pragma unroll
                                 for (int b = 0; b < NBOX; ++b)
                                     tma_load_2d(dst + b * CHUNK_TOKENS * D, kv == 0 ? &tmap_k : &tmap_v, 0, rows[b],
                                                 full, policy);
                             }
+                            __syncwarp();
+                            if (kv == 0) make_factors();
+                            if (lane < NBOX) raw_scale[st * NBOX + lane] = factor[kv];
+                            __syncwarp();
+                            if (umma::elect_one()) mbar_arrive_expect_tx(raw_full(st), L::RAW_TILE);
                             __syncwarp();
                             continue;
                         }
@@ -700,6 +704,7 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
                         __syncwarp();
                     }
                     row = row_next;
+                    if constexpr (Q8) scales_of(row);  // (the table's entry has been on its way since the step began)
                 }
                 if (!ok) break;
                 idx = __shfl_sync(FULL_MASK, next, 0);
@@ -1276,12 +1281,20 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
                         // with two tiles a step's S was committed after the P.V before, with one not
                         const uint32_t wait_o = two ? 0u : pv_step((j & 1) ^ 1);
                         const int phase_o = ((j & 1) ? taken_even : taken_odd) - 1;
-                        if (__any_sync(FULL_MASK, seen < CHUNK_TILE))
-                            ok = softmax_step<M, D, SPLIT_P, true, Q8>(s_t, o_t, seen, j > 0, by, lv, m_ref, sum2,
-                                                                       p_full(b, 0), p_full(b, 1), wait_o, phase_o);
+                        const bool edge = __any_sync(FULL_MASK, seen < CHUNK_TILE);
+                        // Two copies of the code, or one where the conversion's is there too, for the sake of the
+                        // instruction cache: 24 requests of up to 512 queries, heads of 64, 48 us (52 with two);
+                        // prompts and 48 mixed requests, heads of 128, bf16, 487 and 317 us (491 and 336), but
+                        // fp16 508 (456 with two).
+                        if (Q8 && (D == 64 || !KEYS_F16))
+                            ok = softmax_step<M, D, SPLIT_P, Q8>(s_t, o_t, seen, edge, j > 0, by, lv, m_ref, sum2,
+                                                                 p_full(b, 0), p_full(b, 1), wait_o, phase_o);
+                        else if (edge)
+                            ok = softmax_step<M, D, SPLIT_P, Q8>(s_t, o_t, seen, std::true_type(), j > 0, by, lv, m_ref,
+                                                                 sum2, p_full(b, 0), p_full(b, 1), wait_o, phase_o);
                         else
-                            ok = softmax_step<M, D, SPLIT_P, false, Q8>(s_t, o_t, seen, j > 0, by, lv, m_ref, sum2,
-                                                                        p_full(b, 0), p_full(b, 1), wait_o, phase_o);
+                            ok = softmax_step<M, D, SPLIT_P, Q8>(s_t, o_t, seen, std::false_type(), j > 0, by, lv, m_ref,
+                                                                 sum2, p_full(b, 0), p_full(b, 1), wait_o, phase_o);
                         if (!ok) break;
                     } else if (lane == 0) {  // rows of no query: whatever S left there
                         mbar_arrive(p_full(b, 0));
