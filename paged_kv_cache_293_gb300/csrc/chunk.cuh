@@ -67,6 +67,17 @@
 // with the old reference before the maximum is known; merging cut items in this kernel; the first
 // scores of the next piece issued before the last products of this one (48 requests, 70 % decoding,
 // 40 / 40 heads: 268 us, 256 without), and its record and first block fetched early (260).
+// Over a pool held in 8 bits (Q8) the pages come in as e4m3 values, and warps 12-15 turn each tile into the
+// 16-bit numbers of the products between its copy and them, ahead of the MMAs by as many stages as there
+// are, and the next piece's first tiles before they put out this one's results.  Keys become the queries'
+// type, values fp16: an e4m3 value times a power of two is exact in either.  fp16 has no room for a
+// page's scale, so a step's pages enter relative to the largest scale among them; of the keys it goes into
+// the factor of the scores, of the values into the exponents of the weights, which are 2^lv times as
+// large, the reference with them, and count for that much less in the row's sum.  What bounds it: shared
+// memory, which the products read at 128 bytes a cycle while scores are made (1540 of a step's cycles), the
+// copies, reads and stores of the conversion take 1020 more of, and the conversion's issue slots beside
+// the softmax's.  A step takes about 3500 cycles: the prompt 465 us (360 from 16 bits), 500 tokens over
+// 130,500 857 us (700), 48 requests, 70 % decoding, 302 us (250); fp16 454 and 843 us.
 // Every wait is bounded; a CTA that gives up sets PKV_DEVERR_TIMEOUT and returns its tensor
 // memory.
 #pragma once
@@ -110,13 +121,18 @@ struct ChunkSmem {
     static constexpr int BOXES = D / 64;                  // 128-byte columns of a row
     static constexpr int BOX = 128 * 128;                 // one of a 128-row tile
     static constexpr int TILE = BOXES * BOX;              // a tile of Q, K or V
-    static constexpr int STAGES = Q8 ? (D == 128 ? 3 : 6) : (D == 128 ? 5 : 8);
-    static constexpr int RAW_STAGES = Q8 ? (D == 128 ? 4 : 8) : 0;
+    // Q8, D = 128: a tile's e4m3 rows land where the second half of its numbers will be, and become
+    // numbers there, row by row.  (With a ring of their own and three stages of numbers, a step's keys had
+    // no room until the values before the last were done with: a prompt took 489 us and not 465.)
+    // D = 64: rows of half a line, in a ring of their own.
+    static constexpr bool IN_PLACE = Q8 && D == 128;
+    static constexpr int STAGES = D == 128 ? 5 : Q8 ? 6 : 8;
+    static constexpr int RAW_STAGES = Q8 ? (IN_PLACE ? STAGES : 8) : 0;  // tiles of e4m3 values, as their barriers count
     static constexpr int RAW_TILE = 128 * D;
     static constexpr int Q_OFF = 0;
     static constexpr int KV_OFF = 2 * TILE;
     static constexpr int RAW_OFF = KV_OFF + STAGES * TILE;
-    static constexpr int SCALE_OFF = RAW_OFF + RAW_STAGES * RAW_TILE;  // float [RAW_STAGES][8 copies]
+    static constexpr int SCALE_OFF = RAW_OFF + (IN_PLACE ? 0 : RAW_STAGES * RAW_TILE);  // float [RAW_STAGES][8 copies]
     static constexpr int STEP_OFF = SCALE_OFF + RAW_STAGES * 32;       // float2 [Q8_STEP_RING]
     static constexpr int BAR_OFF = STEP_OFF + (Q8 ? Q8_STEP_RING * 8 : 0);
     static constexpr int NBARS = 2 * STAGES + 31 + 2 * RAW_STAGES;
@@ -396,11 +412,11 @@ __device__ __forceinline__ bool few_rows_step(uint32_t s_t, uint32_t p_t, uint32
 // numbers, times a factor per copy of 16 tokens, by four warps: 16 values a lane at a time, which become
 // two 16-byte columns.  Eight lanes read 128 bytes in a row, and write eight different columns of the
 // 128-byte swizzle (with D = 128 the lanes of the second half store their odd column first).  To fp16,
-// factors that it holds, as those between powers of two are, multiply in fp16, and factors of 1 not at
-// all; others, and all to bf16, in 32 bits, so that each number is rounded once.
-enum class Factor { ONE, HALF, SINGLE };
+// factors that it holds, as those between powers of two are, multiply in fp16; others, and all to bf16, in
+// 32 bits, so that each number is rounded once.
+enum class Factor { HALF, SINGLE };
 
-template <typename M, int D, Factor BY, int UNROLL>
+template <typename M, int D, Factor BY, int UNROLL, bool IN_PLACE>
 __device__ __forceinline__ void numbers_by(const unsigned char* raw, const float* factor, unsigned char* tile,
                                            bool is_v, int w, int lane) {
     constexpr int LANES = D / 16, ROWS = 32 / LANES;    // lanes a row, rows a warp at a time
@@ -410,22 +426,28 @@ __device__ __forceinline__ void numbers_by(const unsigned char* raw, const float
     // rows (i * 4 + w) * ROWS + lane / LANES: whole copies of 16 rows a step apart
     const int row0 = w * ROWS + lane / LANES, r = row0 % CHUNK_TOKENS, b0 = row0 / CHUNK_TOKENS;
     constexpr int COPIES = 4 * ROWS / CHUNK_TOKENS;     // copies a step
-    unsigned char* at = is_v ? tile + b0 * (CHUNK_TOKENS * D * 2) + box * (CHUNK_TOKENS * 128) + r * 128
-                             : tile + box * (128 * 128) + row0 * 128;
-    const int stride = is_v ? COPIES * CHUNK_TOKENS * D * 2 : 4 * ROWS * 128;
+    const int copy = is_v ? CHUNK_TOKENS * D * 2 : CHUNK_TOKENS * 128;
+    unsigned char* at = tile + b0 * copy + box * (is_v ? CHUNK_TOKENS * 128 : 128 * 128) + r * 128;
+    const int stride = COPIES * copy;
     at += ((col + swap) ^ (r & 7)) << 4;
     const int other = ((((col + swap) ^ 1) ^ (r & 7)) << 4) - (((col + swap) ^ (r & 7)) << 4);
-    raw += row0 * D + m * 16;
+    // (in place: the row's place in the second half of the numbers)
+    raw = IN_PLACE ? tile + b0 * copy + (is_v ? CHUNK_TOKENS * 128 : 128 * 128) + r * 128 + m * 16 : raw + row0 * D + m * 16;
+    const int raw_stride = IN_PLACE ? stride : 4 * ROWS * D;
     // (short loops: the code of all roles shares the instruction cache; whole, they cost a prompt 10 %)
-#pragma unroll(UNROLL)
-    for (int i = 0; i < STEPS; ++i) {
-        const uint4 x = *reinterpret_cast<const uint4*>(raw + i * 4 * ROWS * D);
-        const uint32_t in[4] = {x.x, x.y, x.z, x.w};
-        uint32_t out[8];
+#pragma unroll 1
+    for (int i = 0; i < STEPS; i += UNROLL) {
+        uint4 x[UNROLL];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) f16x4_of_e4m3x4(in[k], out[2 * k], out[2 * k + 1]);
-        if (BY != Factor::ONE) {
-            const float s = factor[b0 + i * COPIES];
+        for (int u = 0; u < UNROLL; ++u) x[u] = *reinterpret_cast<const uint4*>(raw + (i + u) * raw_stride);
+        if (IN_PLACE) __syncwarp();  // a row is read by the lanes that write over it, before they do
+#pragma unroll
+        for (int u = 0; u < UNROLL; ++u) {
+            const uint32_t in[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+            uint32_t out[8];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) f16x4_of_e4m3x4(in[k], out[2 * k], out[2 * k + 1]);
+            const float s = factor[b0 + (i + u) * COPIES];
             const __half2 h2 = __half2half2(__float2half_rn(s));
             const uint64_t s2 = pack2(s, s);
 #pragma unroll
@@ -440,23 +462,23 @@ __device__ __forceinline__ void numbers_by(const unsigned char* raw, const float
                     out[k] = Mma<M>::pack(a, c);
                 }
             }
+            const uint4 lo4 = make_uint4(out[0], out[1], out[2], out[3]), hi4 = make_uint4(out[4], out[5], out[6], out[7]);
+            *reinterpret_cast<uint4*>(at + (i + u) * stride) = swap ? hi4 : lo4;
+            *reinterpret_cast<uint4*>(at + (i + u) * stride + other) = swap ? lo4 : hi4;
         }
-        const uint4 lo4 = make_uint4(out[0], out[1], out[2], out[3]), hi4 = make_uint4(out[4], out[5], out[6], out[7]);
-        *reinterpret_cast<uint4*>(at + i * stride) = swap ? hi4 : lo4;
-        *reinterpret_cast<uint4*>(at + i * stride + other) = swap ? lo4 : hi4;
     }
 }
 
-template <typename M, int D>
+template <typename M, int D, bool IN_PLACE>
 __device__ __forceinline__ void numbers_of_tile(const unsigned char* raw, const float* factor, unsigned char* tile,
                                                 bool is_v, int w, int lane) {
     const float mine = factor[lane % 8];
     if (!std::is_same<M, __half>::value)
-        numbers_by<M, D, Factor::SINGLE, 2>(raw, factor, tile, is_v, w, lane);
+        numbers_by<M, D, Factor::SINGLE, 2, IN_PLACE>(raw, factor, tile, is_v, w, lane);
     else if (__all_sync(FULL_MASK, __half2float(__float2half_rn(mine)) == mine))
-        numbers_by<__half, D, Factor::HALF, 2>(raw, factor, tile, is_v, w, lane);
+        numbers_by<__half, D, Factor::HALF, 2, IN_PLACE>(raw, factor, tile, is_v, w, lane);
     else
-        numbers_by<__half, D, Factor::SINGLE, 1>(raw, factor, tile, is_v, w, lane);
+        numbers_by<__half, D, Factor::SINGLE, 1, IN_PLACE>(raw, factor, tile, is_v, w, lane);
 }
 
 template <typename T, int D, bool SPLIT_P, bool Q8>
@@ -657,17 +679,22 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
                         if constexpr (Q8) {
                             const int st = it % NR;
                             if (it >= NR) {
-                                ok = __all_sync(FULL_MASK, mbar_wait_short(raw_empty(st), ((it / NR) - 1) & 1));
+                                ok = __all_sync(FULL_MASK, mbar_wait_short(L::IN_PLACE ? kv_empty(st) : raw_empty(st),
+                                                                           ((it / NR) - 1) & 1));
                                 if (!ok) break;
                             }
                             // the copies first, while the scales are on their way, and the arrival that tells of
                             // both when these are there
                             if (umma::elect_one()) {
-                                const uint32_t full = raw_full(st), dst = sbase + L::RAW_OFF + st * L::RAW_TILE;
+                                const uint32_t full = raw_full(st);
+                                uint32_t dst = sbase + L::RAW_OFF + st * L::RAW_TILE, copy = CHUNK_TOKENS * D;
+                                if (L::IN_PLACE) {  // into the second half of each row's numbers
+                                    dst = ring + st * L::TILE + (kv == 0 ? L::BOX : CHUNK_TOKENS * 128);
+                                    copy = kv == 0 ? CHUNK_TOKENS * 128 : CHUNK_TOKENS * D * 2;
+                                }
 #pragma unroll
                                 for (int b = 0; b < NBOX; ++b)
-                                    tma_load_2d(dst + b * CHUNK_TOKENS * D, kv == 0 ? &tmap_k : &tmap_v, 0, rows[b],
-                                                full, policy);
+                                    tma_load_2d(dst + b * copy, kv == 0 ? &tmap_k : &tmap_v, 0, rows[b], full, policy);
                             }
                             __syncwarp();
                             if (kv == 0) make_factors();
@@ -941,27 +968,28 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
             for (int k = 0; k < count; ++k, ++made) {
                 const int from = made % (NR > 0 ? NR : 1), st = made % NS;
                 if (!__all_sync(FULL_MASK, mbar_wait_short(raw_full(from), (made / (NR > 0 ? NR : 1)) & 1))) return false;
-                if (made >= NS && !__all_sync(FULL_MASK, mbar_wait_short(kv_empty(st), (made / NS - 1) & 1)))
+                if (!L::IN_PLACE && made >= NS &&
+                    !__all_sync(FULL_MASK, mbar_wait_short(kv_empty(st), (made / NS - 1) & 1)))
                     return false;
                 // (even ones are K's)
                 const unsigned char* const raw = smem + L::RAW_OFF + from * L::RAW_TILE;
                 unsigned char* const tile = smem + L::KV_OFF + st * L::TILE;
                 if (KEYS_F16 || (made & 1))
-                    numbers_of_tile<M, D>(raw, raw_scale + from * 8, tile, made & 1, w, lane);
+                    numbers_of_tile<M, D, L::IN_PLACE>(raw, raw_scale + from * 8, tile, made & 1, w, lane);
                 else
-                    numbers_of_tile<T, D>(raw, raw_scale + from * 8, tile, false, w, lane);
+                    numbers_of_tile<T, D, L::IN_PLACE>(raw, raw_scale + from * 8, tile, false, w, lane);
                 umma::fence_smem_to_async();
                 __syncwarp();
                 if (lane == 0) {
                     mbar_arrive(kv_full(st));
-                    mbar_arrive(raw_empty(from));
+                    if (!L::IN_PLACE) mbar_arrive(raw_empty(from));
                 }
             }
             return true;
         };
         // Of the piece at work and the next one only their steps are needed here, so that the registers are
         // free for the numbers: the record stays where it is until the output.
-        constexpr int AHEAD = 2;
+        constexpr int AHEAD = NS - 1;
         int steps_next = 0;
         auto look_at = [&](int i) -> bool {
             ok = __all_sync(FULL_MASK, mbar_wait_short(piece_full(i & 1), (i >> 1) & 1));
@@ -1284,9 +1312,9 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
                         const bool edge = __any_sync(FULL_MASK, seen < CHUNK_TILE);
                         // Two copies of the code, or one where the conversion's is there too, for the sake of the
                         // instruction cache: 24 requests of up to 512 queries, heads of 64, 48 us (52 with two);
-                        // prompts and 48 mixed requests, heads of 128, bf16, 487 and 317 us (491 and 336), but
-                        // fp16 508 (456 with two).
-                        if (Q8 && (D == 64 || !KEYS_F16))
+                        // 500 queries over 130,500 tokens, heads of 128, fp16, 847 us (885 with two), but bf16
+                        // 912 (861 with two).
+                        if (Q8 && (D == 64 || KEYS_F16))
                             ok = softmax_step<M, D, SPLIT_P, Q8>(s_t, o_t, seen, edge, j > 0, by, lv, m_ref, sum2,
                                                                  p_full(b, 0), p_full(b, 1), wait_o, phase_o);
                         else if (edge)

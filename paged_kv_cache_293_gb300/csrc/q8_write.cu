@@ -13,6 +13,11 @@
 // for pages of 32 x 128) has the keys or values of one head of a window in its registers, 64 numbers a
 // lane at most: it takes each run's largest |x|, then rounds.  Lane j looks after row j: its slot, its
 // run and that run's scale.
+// Measured: one token of 32 + 2 * 8 heads of 128 4.9 us (two dependent round trips to memory, the slots and
+// then rows, scales and table), 128 of 40 + 2 * 40 9.7; 16384 of 32 + 2 * 8, bf16, 78 us (378 MB, 4.8 TB/s), of
+// which q alone, through rope_write.cu, takes 50, and the keys and values 28: about 6000 cycles a window
+// of 16 tokens and CTA, bound by instructions (46 % of the issue slots) at 16 warps per SM, whose numbers
+// take all registers.
 #include <cfloat>
 #include <type_traits>
 
@@ -473,6 +478,7 @@ __device__ __forceinline__ void load_weights(const void* w, const LanePart& at, 
 
 }  // namespace
 
+// (Runs one after another in a CTA took 44 us for 512 decoding requests, windows of many runs 13.)
 // Few tokens, whose time is one row's way through the kernel: the first q_ctas CTAs have the q rows of a
 // token each; of the others, every `heads` have the runs that begin in `rows` rows, and a warp one page's
 // rows, all in flight.  The warps share the window's rows of the rotation table in shared memory.
