@@ -76,8 +76,8 @@
 // large, the reference with them, and count for that much less in the row's sum.  What bounds it: shared
 // memory, which the products read at 128 bytes a cycle while scores are made (1540 of a step's cycles), the
 // copies, reads and stores of the conversion take 1020 more of, and the conversion's issue slots beside
-// the softmax's.  A step takes about 3500 cycles: the prompt 465 us (360 from 16 bits), 500 tokens over
-// 130,500 857 us (700), 48 requests, 70 % decoding, 302 us (250); fp16 454 and 843 us.
+// the softmax's.  (Both figures from the bytes.)  The prompt takes 465 us (359 from 16 bits), 863,000 cycles
+// an SM for 219 steps, pieces' beginnings and ends among them; 500 tokens over 130,500 858 us (689 to 703), 48 requests, 70 % decoding, 302 us (250); fp16 454 and 843 us.
 // Every wait is bounded; a CTA that gives up sets PKV_DEVERR_TIMEOUT and returns its tensor
 // memory.
 #pragma once
