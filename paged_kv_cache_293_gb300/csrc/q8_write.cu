@@ -178,41 +178,51 @@ __device__ __forceinline__ RawRow load_row(const RopeParams& p, int i) {
     return RawRow{p.slot_mapping[i], p.positions[i]};
 }
 
-// The runs that begin in rows [t, t_end) and are whole in the B rows from t on; t moves to the first that
-// is not.  A run: tokens whose slots advance as their rows do, in one block.  `first`: what lies before
-// t is not known yet, and lane j has row t - 1 - j in `back`; raw: lane j's row t + j.  Whole warps.
+// The block that a row's token lies in (-1: there is none) and its place there.
 template <int B>
-__device__ __forceinline__ Window find_window(const RopeParams& p, const RawRow& raw, const RawRow& back, int& t,
-                                              int t_end, bool first, bool reports) {
+__device__ __forceinline__ int block_of(const RopeParams& p, const RawRow& x, int& row) {
+    row = -1;
+    if (x.pos < 0 || (p.rotary_dim > 0 && x.pos >= p.max_position) || x.slot < 0 ||
+        x.slot >= (long long)p.num_blocks * B)
+        return -1;
+    row = (int)(x.slot & (B - 1));
+    return (int)(x.slot / B);
+}
+
+// The nearest row with a token before a window (blk: -1 where none of the 32 rows before has one).
+struct Before {
+    int blk, row, at;
+};
+template <int B>
+__device__ __forceinline__ Before before_row(const RopeParams& p, int t) {
+    int row;
+    const int blk = block_of<B>(p, load_row(p, t - 1 - (int)(threadIdx.x & 31)), row);
+    const unsigned near = __ballot_sync(FULL_MASK, blk >= 0);
+    const int k = near != 0 ? __ffs(near) - 1 : 0;
+    return Before{__shfl_sync(FULL_MASK, blk, k), __shfl_sync(FULL_MASK, row, k), t - 1 - k};
+}
+
+// The runs that begin in rows [t, t_end) and are whole in the B rows from t on; t moves to the first that
+// is not, and `before` with it.  A run: tokens whose slots advance as their rows do, in one block.  raw:
+// lane j's row t + j.  Whole warps.
+template <int B>
+__device__ __forceinline__ Window find_window(const RopeParams& p, const RawRow& raw, Before& before, int& t,
+                                              int t_end, bool reports) {
     const int lane = threadIdx.x & 31;
-    const long long num_slots = (long long)p.num_blocks * B;
-    auto look = [&](const RawRow& x, int& row) -> int {
-        row = -1;
-        if (x.pos < 0 || (p.rotary_dim > 0 && x.pos >= p.max_position) || x.slot < 0 || x.slot >= num_slots) return -1;
-        row = (int)(x.slot & (B - 1));
-        return (int)(x.slot / B);
-    };
     Window w;
     w.pos = raw.pos;
-    w.blk = look(raw, w.row);
+    w.blk = block_of<B>(p, raw, w.row);
     const unsigned below = (1u << lane) - 1, here = 1u << lane;
     const unsigned there = __ballot_sync(FULL_MASK, w.blk >= 0);
     // the nearest row before that holds a token: in the window, or (for its first token) before it
     int d = (there & below) != 0 ? lane - (31 - __clz(there & below)) : 0;
     int blk_d = __shfl_sync(FULL_MASK, w.blk, lane - d), row_d = __shfl_sync(FULL_MASK, w.row, lane - d);
-    if (first && there != 0) {
-        int row_b;
-        const int blk_b = look(back, row_b);
-        const unsigned near = __ballot_sync(FULL_MASK, blk_b >= 0);
-        const int k = near != 0 ? __ffs(near) - 1 : 0, j = __ffs(there) - 1;
-        const int blk_k = __shfl_sync(FULL_MASK, blk_b, k), row_k = __shfl_sync(FULL_MASK, row_b, k);
-        if (lane == j && near != 0) {
-            d = j + k + 1;
-            blk_d = blk_k;
-            row_d = row_k;
-        }
+    if (lane == __ffs(there) - 1 && before.blk >= 0) {
+        d = t + lane - before.at;
+        blk_d = before.blk;
+        row_d = before.row;
     }
-    const bool same = w.blk >= 0 && d > 0 && d <= max(w.row, 1) && blk_d == w.blk;
+    const bool same = w.blk >= 0 && d > 0 && d <= 32 && blk_d == w.blk;
     const bool follows = same && row_d == w.row - d;
     w.leaders = __ballot_sync(FULL_MASK, w.blk >= 0 && !follows);
     const unsigned refused = __ballot_sync(FULL_MASK, same && !follows);  // a slot twice, or in falling order
@@ -233,6 +243,11 @@ __device__ __forceinline__ Window find_window(const RopeParams& p, const RawRow&
     const int stop = min(stop_over, late != 0 ? __ffs(late) - 1 : 32);
     w.run = __ballot_sync(FULL_MASK, member && lead < stop && !((refused >> w.lead) & 1));
     if (reports && (refused & ((stop < 32 ? 1u << stop : 0u) - 1)) != 0) set_error(p.err, PKV_DEVERR_SLOT);
+    const unsigned passed = there & (stop < 32 ? (1u << stop) - 1 : FULL_MASK);
+    if (passed != 0) {
+        const int k = 31 - __clz(passed);
+        before = Before{__shfl_sync(FULL_MASK, w.blk, k), __shfl_sync(FULL_MASK, w.row, k), t + k};
+    }
     t = stop < 32 ? t + stop : min(t + 32, t_end);
     return w;
 }
@@ -507,10 +522,10 @@ q8_write_kernel(const RopeParams p, float* k_scale, float* v_scale, int q_ctas, 
     uint64_t wa[2], wb[2];
     load_weights<T>(p.k_weight, at, wa, wb);
     const int t_begin = cta / heads * rows, t_end = min(t_begin + rows, p.num_tokens);
-    const RawRow back = load_row(p, t_begin - 1 - lane);
+    Before before = before_row<B>(p, t_begin);
     for (int t = t_begin; t < t_end;) {
         const int t_now = t;
-        const Window w = find_window<B>(p, load_row(p, t + lane), back, t, t_end, t_now == t_begin, threadIdx.x == 0);
+        const Window w = find_window<B>(p, load_row(p, t + lane), before, t, t_end, threadIdx.x == 0);
         if (w.run == 0) continue;
         // the scale of each run's page, and no other run at that page from here on
         const unsigned page = (unsigned)max(w.blk, 0) * Hkv + head;  // (pages are 1 KB or more)
@@ -615,7 +630,7 @@ q8_stream_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
 
     int t = t_begin;
     RawRow raw = load_row(p, t + lane);
-    const RawRow back = load_row(p, t - 1 - lane);
+    Before before = before_row<B>(p, t);
     auto find = [&](int i) {
         Found& x = found[i % Q8_FOUND];
         Window w;
@@ -623,7 +638,7 @@ q8_stream_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
         int t_now = t;
         while (t < t_end && w.run == 0) {
             t_now = t;
-            w = find_window<B>(p, raw, back, t, t_end, t_now == t_begin, lane == 0);
+            w = find_window<B>(p, raw, before, t, t_end, lane == 0);
             if (w.run == 0) raw = load_row(p, t + lane);
         }
         if (w.run != 0) {

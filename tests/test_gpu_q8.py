@@ -273,6 +273,24 @@ def test_write_refuses_a_block_twice_in_a_row(P):
     w.check()
 
 
+@pytest.mark.parametrize("T", [60, 900, 1100])
+@pytest.mark.parametrize("B,first,again", [(16, 11, 11), (16, 16, 9), (32, 20, 20), (32, 32, 12)])
+@pytest.mark.parametrize("gap", [0, 3])
+def test_write_refuses_a_block_that_comes_again_at_once(P, T, B, first, again, gap):
+    # a block's first rows, then the same rows again, perhaps behind rows without a token: wherever the
+    # rows that are looked at together end, the second run is left out, and what follows is written
+    w = Write([(0, T)], 24, 24, 64, B, torch.bfloat16, seed=T + B, norm=False, rot=0)
+    base = int(w.slots[0])
+    at = first + gap
+    w.slots[first:at] = -1
+    w.slots[at:at + again] = base + torch.arange(again)
+    w.slots[at + again:2 * B + 4] = -1
+    w.run(P)
+    assert P.pkv_get_device_error() == P.DEVERR["SLOT"]
+    w.slots[at:at + again] = -1
+    w.check()
+
+
 def test_write_to_far_blocks_and_on_another_stream(P):
     # places past 2^32 bytes of each pool
     N, Hkv, B, D = 300000, 8, 16, 128
