@@ -583,7 +583,7 @@ typedef struct pkv_q8_pool {
  *          are powers of two, as this call makes them, leave a row's values as they were, but
  *          for those that fall below 2^-6 of the new scale.)
  *   value  x / scale to the nearest e4m3 value, even at ties; NaN where x is not finite
- * Arguments and errors as pkv_qk_norm_rope_write's.  A run whose block the token before
+ * Arguments and errors as pkv_qk_norm_rope_write's; the pool's four arrays share no byte.  A run whose block the token before
  * it (of the 32 rows before) has too, but not as the slot before (a slot twice, or slots in
  * falling order), is not written and sets PKV_DEVERR_SLOT.  A block that comes at two separate places of a call has
  * no defined contents; where the two are seen to meet, PKV_DEVERR_SLOT is set and one of them is

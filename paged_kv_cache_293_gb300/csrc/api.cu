@@ -1193,6 +1193,13 @@ pkv_status pkv_qk_norm_rope_write_q8(const pkv_q8_pool* pool, int32_t dtype, con
     if (rows_overlap(pool->k_scale, pages * 4, pages * 4, 1, q_out, out_bytes) ||
         rows_overlap(pool->v_scale, pages * 4, pages * 4, 1, q_out, out_bytes))
         return PKV_ERR_INVALID;
+    // what is written is written by many CTAs: no two of the four arrays share a byte
+    const int64_t code_bytes = pages * pool->block_size * pool->head_dim;
+    const void* const arrays[4] = {pool->k, pool->v, pool->k_scale, pool->v_scale};
+    const int64_t bytes[4] = {code_bytes, code_bytes, pages * 4, pages * 4};
+    for (int i = 0; i < 4; ++i)
+        for (int j = 0; j < i; ++j)
+            if (rows_overlap(arrays[i], bytes[i], bytes[i], 1, arrays[j], bytes[j])) return PKV_ERR_INVALID;
     st = error_word(&p.err);
     if (st != PKV_OK) return st;
     return pkv::launch_q8_write(p, pool->k_scale, pool->v_scale, dtype, static_cast<cudaStream_t>(stream)) ==

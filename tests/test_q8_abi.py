@@ -87,6 +87,13 @@ def _decode(P, pool=None, dtype=1, NQ=1, S=2, Hq=4, M=4, ctx=64, scale=0.1, out_
                                                ctx, scale, g("out"), out_dtype, part, ws, wsb, None)
 
 
+def test_write_refuses_arrays_over_one_another(P):
+    # the pools end at 256 + 16384 and 65536 + 16384, the scales are 32 bytes each
+    for bad in (dict(v=256), dict(v=256 + 16368), dict(k=65536 + 16368), dict(v_scale=131072),
+                dict(v_scale=131072 + 28), dict(k_scale=131972), dict(k_scale=256), dict(v_scale=65536 + 16380)):
+        assert _write(P, pool=_pool(P, **bad)) == P.PKV_ERR_INVALID, bad
+
+
 def test_decode_refusals(P):
     assert _decode(P, S=0) == P.PKV_OK
     for bad in BAD_POOLS:
