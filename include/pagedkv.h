@@ -613,7 +613,7 @@ pkv_status pkv_qk_norm_rope_write_q8(const pkv_q8_pool* pool, int32_t dtype, con
  *   workspace     pkv_decode_q8_workspace_bytes(...) bytes (0: none needed), 16-byte aligned;
  *                 calls that may run at the same time need one each
  * Any group size num_q_heads / num_kv_heads.  num_seqs and the number of pieces of a context
- * up to 65535 each.  The queries enter their products exactly (in bf16, but for elements below 2^-30
+ * up to 65535 each, max_context_len up to 2^30.  The queries enter their products exactly (in bf16, but for elements below 2^-30
  * of their row's largest), the probabilities rounded to fp16 (off by at most 2^-11 of their value,
  * and 2^-32 of the row's largest), with a remainder of another 11 bits when out is fp32.
  * Cached rows past a query's last position may hold anything.  A row that sees tokens is NaN

@@ -1224,8 +1224,9 @@ Q8Layout q8_layout(const pkv_q8_pool* pool, int32_t S, int32_t NQ, int32_t Hq, i
     const int64_t cols = (int64_t)NQ * (Hq / pool->num_kv_heads), rows = (int64_t)S * pool->num_kv_heads;
     Q8Layout w{};
     w.column_tiles = cols > 8 && rows * ((cols + 15) / 16) >= (1 << 20) / std::max(max_ctx, 1) ? 2 : 1;
-    if (P > 0) {
-        w.P = P;
+    if (P > 0) {  // no more than the whole context
+        const int64_t B = pool->block_size;
+        w.P = (int32_t)std::min<int64_t>(P, (std::max<int64_t>(max_ctx, 1) + B - 1) / B * B);
     } else {
         const int64_t tile = 8 * w.column_tiles, ctas = std::max<int64_t>(1, rows * ((cols + tile - 1) / tile));
         const int64_t parts = std::max<int64_t>(1, 4 * (int64_t)sm_count() / ctas);
@@ -1274,7 +1275,8 @@ pkv_status pkv_paged_attention_decode_q8(const pkv_q8_pool* pool, int32_t dtype,
     if (out_dtype != PKV_F32 && out_dtype != dtype) return PKV_ERR_UNSUPPORTED;
     const Q8Layout w = q8_layout(pool, num_seqs, num_queries, num_q_heads, max_context_len, partition_size);
     const int64_t cols = (int64_t)num_queries * (num_q_heads / pool->num_kv_heads);
-    if (num_seqs > 65535 || w.parts > 65535 || cols > INT32_MAX - 8 ||
+    // (positions, with a piece added, are 32-bit numbers in the kernels)
+    if (max_context_len > (1 << 30) || num_seqs > 65535 || w.parts > 65535 || cols > INT32_MAX - 8 ||
         pool->num_kv_heads * ((cols + 7) / 8) > INT32_MAX ||
         (int64_t)num_seqs * num_queries * num_q_heads > INT32_MAX)
         return PKV_ERR_UNSUPPORTED;

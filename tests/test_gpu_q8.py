@@ -389,6 +389,15 @@ def test_decode_in_pieces(P, part):
     assert P.pkv_get_device_error() == 0
 
 
+@pytest.mark.parametrize("part", [2 ** 31 - 16, 2 ** 30, 2 ** 28])
+@pytest.mark.parametrize("max_ctx", [900, 2 ** 30])
+def test_decode_in_pieces_of_any_size(P, part, max_ctx):
+    # sums of a position and a piece stay within 32 bits
+    d = Decode([900, 1, 0, 333], 2, 8, 2, 128, 16, torch.bfloat16, seed=5)
+    d.check(d.run(P, part=part, max_ctx=max_ctx))
+    assert P.pkv_get_device_error() == 0
+
+
 @pytest.mark.parametrize("scale", [-0.1, 0.0, 3.0])
 def test_decode_of_other_scales(P, scale):
     d = Decode([40, 300], 1, 4, 2, 64, 16, torch.float16, seed=2)

@@ -107,6 +107,8 @@ def test_decode_refusals(P):
                 dict(part=24)):
         assert _decode(P, **bad) == P.PKV_ERR_INVALID, bad
     assert _decode(P, S=65536) == P.PKV_ERR_UNSUPPORTED
+    assert _decode(P, ctx=2 ** 30 + 1, part=2 ** 30) == P.PKV_ERR_UNSUPPORTED    # a piece's end passes 32 bits
+    assert _decode(P, ctx=2 ** 31 - 1, part=2 ** 20) == P.PKV_ERR_UNSUPPORTED
     assert _decode(P, ctx=16 * 65536, part=16) == P.PKV_ERR_UNSUPPORTED
     assert _decode(P, NQ=2 ** 30, S=2, Hq=4) == P.PKV_ERR_UNSUPPORTED
     for name in ("q", "tables", "lens", "out"):
