@@ -596,17 +596,26 @@ paged_decode_mma_kernel(const __grid_constant__ CUtensorMap tmap_k,
 
 // ------------------------------------------------------------------ host side
 
-// cuTensorMapEncodeTiled, looked up once through the runtime (no libcuda link).
+// A driver function, looked up through the runtime (no libcuda link).
+inline void* driver_entry_point(const char* name) {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    return cudaGetDriverEntryPointByVersion(name, &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+                   q == cudaDriverEntryPointSuccess
+               ? f
+               : nullptr;
+}
+
+// cuTensorMapEncodeTiled, looked up once.  It asks for a context, which the runtime gives a thread with
+// its first call that needs one: a thread whose first call this is has none yet.
 inline PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
-        void* f = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
-                                             &q) != cudaSuccess ||
-            q != cudaDriverEntryPointSuccess)
-            f = nullptr;
-        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-    }();
+    static const auto fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(driver_entry_point("cuTensorMapEncodeTiled"));
+    static const auto current = reinterpret_cast<CUresult (*)(CUcontext*)>(driver_entry_point("cuCtxGetCurrent"));
+    CUcontext ctx = nullptr;
+    int dev = 0;
+    if (fn && current && current(&ctx) == CUDA_SUCCESS && !ctx &&
+        (cudaGetDevice(&dev) != cudaSuccess || cudaSetDevice(dev) != cudaSuccess))
+        return nullptr;
     return fn;
 }
 

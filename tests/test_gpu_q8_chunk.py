@@ -208,3 +208,128 @@ def test_prompts_as_they_are_used(P):
         assert bool(((out.cpu().double() - ref).abs() <= tol)[:n].all())
         past += new
     assert P.pkv_get_device_error() == 0
+
+
+@pytest.mark.parametrize("which", ["chunk_q8", "decode_q8", "write_q8", "many_write_q8", "chunk"])
+def test_a_call_from_a_thread_that_made_none_before(P, which):
+    # once everything that is asked for once is known, a new thread's first call has no context yet
+    import threading
+    c = Chunk([(0, 1100), (40, 3)], 4, 2, 64, 16, torch.float16, seed=3)
+    T, S, mc = c.q.shape[0], 2, max(c.lens)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=DEV)  # noqa: E731
+    q, tables, starts, lens = c.q.to(DEV), c.tables.to(DEV), i32(c.starts), i32(c.lens)
+    pools = [t.to(DEV) for t in (c.kc, c.vc, c.ks, c.vs)]
+    half = [torch.nan_to_num(Q.numbers(a, b)).half().to(DEV) for a, b in ((c.kc, c.ks), (c.vc, c.vs))]
+    out, dec = torch.zeros_like(q), torch.zeros_like(q[:2])
+    ws = P.workspace_tensor(max(P.pkv_chunk_q8_workspace_bytes(pools[0], T, S, 4, mc),
+                                P.pkv_chunk_workspace_bytes(half[0], T, S, 4, mc)), DEV)
+    spare = [torch.zeros_like(t.view(torch.uint8)).view(t.dtype) for t in pools]
+    slots = torch.arange(1100, dtype=torch.int64, device=DEV)
+    pos, kv, q_out = slots.int(), q[:1100, :2].contiguous(), torch.zeros_like(q[:1100])
+    write = lambda n, s: P.pkv_qk_norm_rope_write_q8(q[:n], kv[:n], kv[:n], *spare, pos[:n], slots[:n],  # noqa: E731
+                                                     q_out[:n], stream=s)
+    call = {"chunk_q8": lambda s: P.pkv_paged_attention_chunk_q8(q, *pools, starts, tables, lens, c.scale, out, mc, ws,
+                                                                 stream=s),
+            "decode_q8": lambda s: P.pkv_paged_attention_decode_q8(q[:2], *pools, tables, lens, c.scale, dec, mc, 512,
+                                                                   None, stream=s),
+            "write_q8": lambda s: write(9, s), "many_write_q8": lambda s: write(1100, s),
+            "chunk": lambda s: P.pkv_paged_attention_chunk(q, *half, starts, tables, lens, c.scale, out, mc, ws,
+                                                           stream=s)}[which]
+    stream = torch.cuda.current_stream()
+    results = (out, dec, q_out, *spare)
+    call(stream)
+    want = [t.view(torch.uint8).clone() for t in results]
+    assert any(bool(t.any()) for t in want)
+    for t in results:
+        t.view(torch.uint8).zero_()
+    torch.cuda.synchronize()
+    failed = []
+
+    def first():
+        try:
+            call(stream)
+        except Exception as e:  # noqa: BLE001
+            failed.append(e)
+
+    t = threading.Thread(target=first)
+    t.start()
+    t.join()
+    torch.cuda.synchronize()
+    assert not failed
+    assert all(torch.equal(a.view(torch.uint8), b) for a, b in zip(results, want))
+    assert P.pkv_get_device_error() == 0
+
+
+def test_calls_from_several_threads_and_a_graph_beside_them(P):
+    # the same calls one after another, from four threads on streams of their own, and replayed from a
+    # graph while those run: the same bits each time
+    import threading
+
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=DEV)  # noqa: E731
+
+    class Work:
+        def __init__(self, seed, D, dt):
+            c = self.c = Chunk([(0, 150), (700, 1), (33, 40), (1200, 9)], 8, 2, D, 16, dt, seed=seed)
+            T, self.S, self.mc = c.q.shape[0], len(c.lens), max(c.lens)
+            self.q, self.tables, self.starts, self.lens = c.q.to(DEV), c.tables.to(DEV), i32(c.starts), i32(c.lens)
+            self.pools = [t.to(DEV) for t in (c.kc, c.vc, c.ks, c.vs)]
+            self.out, self.dec = torch.zeros_like(self.q), torch.zeros_like(self.q[:self.S])
+            ws = lambda n: P.workspace_tensor(max(n, 16), DEV)  # noqa: E731
+            self.ws = ws(P.pkv_chunk_q8_workspace_bytes(self.pools[0], T, self.S, 8, self.mc))
+            self.wd = ws(P.pkv_decode_q8_workspace_bytes(self.pools[0], self.S, 1, 8, self.mc, 64))
+            # a write of its own: rows of one request into the first blocks of spare pools
+            self.spare = [torch.zeros_like(t.view(torch.uint8)).view(t.dtype) for t in self.pools]
+            self.slots = torch.arange(64, dtype=torch.int64, device=DEV)
+            self.kv = self.q[:64, :2].contiguous()
+            self.q_out = torch.zeros_like(self.q[:64])
+
+        def run(self, stream=None):
+            P.pkv_paged_attention_chunk_q8(self.q, *self.pools, self.starts, self.tables, self.lens, self.c.scale,
+                                           self.out, self.mc, self.ws, stream=stream)
+            P.pkv_paged_attention_decode_q8(self.q[:self.S], *self.pools, self.tables, self.lens, self.c.scale, self.dec,
+                                            self.mc, 64, self.wd, stream=stream)
+            P.pkv_qk_norm_rope_write_q8(self.q[:64], self.kv, self.kv, *self.spare, self.slots.int(), self.slots,
+                                        self.q_out, stream=stream)
+
+        def results(self):
+            return [t.view(torch.uint8).clone() for t in (self.out, self.dec, self.q_out, *self.spare)]
+
+        def clear(self):
+            for t in (self.out, self.dec, self.q_out, *self.spare):
+                t.view(torch.uint8).zero_()
+
+    work = [Work(n, (64, 128)[n % 2], (torch.float16, torch.bfloat16)[n // 2 % 2]) for n in range(5)]
+    want = []
+    for w in work:
+        w.run()
+        w.c.check(w.out.cpu())
+        want.append(w.results())
+        w.clear()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        work[4].run()
+    torch.cuda.synchronize()
+    failed = []
+
+    def loop(w):
+        try:
+            s = torch.cuda.Stream()
+            with torch.cuda.stream(s):
+                for _ in range(20):
+                    w.run()
+            s.synchronize()
+        except Exception as e:  # noqa: BLE001
+            failed.append(e)
+
+    threads = [threading.Thread(target=loop, args=(w,)) for w in work[:4]]
+    for t in threads:
+        t.start()
+    for _ in range(20):
+        graph.replay()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not failed
+    for w, x in zip(work, want):
+        assert all(torch.equal(a, b) for a, b in zip(w.results(), x))
+    assert P.pkv_get_device_error() == 0
