@@ -14,8 +14,8 @@
 // lane at most: it takes each run's largest |x|, then rounds.  Lane j looks after row j: its slot, its
 // run and that run's scale.
 // Measured: one token of 32 + 2 * 8 heads of 128 4.9 us (two dependent round trips to memory, the slots and
-// then rows, scales and table), 128 of 40 + 2 * 40 9.7; 16384 of 32 + 2 * 8, bf16, 78 us (378 MB, 4.8 TB/s), of
-// which q alone, through rope_write.cu, takes 50, and the keys and values 28: about 6000 cycles a window
+// then rows, scales and table), 128 of 40 + 2 * 40 9.9; 16384 of 32 + 2 * 8, bf16, 76 us (378 MB, 5.0 TB/s);
+// q alone, through rope_write.cu, takes 50 of them, and the keys and values 28: about 6000 cycles a window
 // of 16 tokens and CTA, bound by instructions (46 % of the issue slots) at 16 warps per SM, whose numbers
 // take all registers.
 #include <cfloat>
@@ -33,7 +33,8 @@ namespace {
 constexpr int Q8_Q_ROWS = 2;      // rows of q per group of lanes, in flight together
 constexpr int Q8_KV_WARPS = 8;
 // From this many tokens on q goes through rope_write.cu's kernels and k and v are streamed, a launch
-// more; measured, one launch against two, bf16: 32 + 2 * 8 heads of 128, 1024 tokens 12.3 / 13.0 us, 2048
+// more, which begins where the first leaves room (16384 tokens 76 us, 79.5 one after the other; 2048 of
+// 32 + 2 * 8 heads 17.1 / 18.8); measured, one launch against two one after the other, bf16: 32 + 2 * 8 heads of 128, 1024 tokens 12.3 / 13.0 us, 2048
 // 20.4 / 18.6; 40 + 2 * 40, 1024 23.2 / 24.6, 1536 33.6 / 28.7; 16 + 2 * 4 of 64, 1024 10.8 / 10.9, 2048
 // 15.0 / 10.9.
 constexpr int Q8_MANY_TOKENS = 1025;
@@ -715,6 +716,8 @@ q8_stream_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
         __syncthreads();
     }
     if (lane == 0) bulk_wait_read<0>();  // the CTA must not end with copies still reading its shared memory
+    // q's kernel, beside which this one may run and of which it needs nothing, is done when this one is
+    asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 namespace {
@@ -764,13 +767,21 @@ cudaError_t launch_q8_write_tdbi(const RopeParams& p, float* k_scale, float* v_s
     CUtensorMap tk, tv;
     if (!encode_rows_map<T>(&tk, p.k, p.k_stride, p, heads, B) || !encode_rows_map<T>(&tv, p.v, p.v_stride, p, heads, B))
         return cudaErrorNotSupported;
-    kernel<<<(unsigned)ctas, warps * 32, StreamSmem<D, B>::bytes(heads), stream>>>(tk, tv, p, k_scale, v_scale, heads,
-                                                                                  slices, (int)rows);
-    e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
     RopeParams q = p;  // the q rows alone
     q.num_kv_heads = 0;
-    return launch_rope_write(q, std::is_same<T, __half>::value ? PKV_F16 : PKV_BF16, stream);
+    e = launch_rope_write(q, std::is_same<T, __half>::value ? PKV_F16 : PKV_BF16, stream);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)ctas);
+    cfg.blockDim = dim3(warps * 32);
+    cfg.dynamicSmemBytes = StreamSmem<D, B>::bytes(heads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, tk, tv, p, k_scale, v_scale, heads, slices, (int)rows);
 }
 
 template <typename T, int D>

@@ -51,6 +51,8 @@ constexpr long long STREAM_MIN_ROW = 6000;
 // FULL: every lane's elements are rotated (rotary_dim = D).
 template <typename T, int D, bool INTERLEAVED, bool FULL, int ROWS>
 __global__ void __launch_bounds__(ROPE_MAX_THREADS) rope_write_kernel(const RopeParams p) {
+    // (q alone: q8_write.cu's keys and values may begin wherever an SM has room)
+    if (p.num_kv_heads == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     constexpr int V = 16 / (int)sizeof(T);      // elements per lane
     constexpr int LPR = D / V;                  // lanes per row
     constexpr int P = Chunk8<T>::PAIRS;
@@ -153,6 +155,8 @@ __global__ void __launch_bounds__((WARPS + 1) * 32) rope_stream_kernel(const Rop
     extern __shared__ __align__(128) unsigned char ring[];
     __shared__ __align__(8) uint64_t bars[2 * STREAM_MAX_STAGES];
     __shared__ int live[STREAM_MAX_STAGES];  // the stage holds a token
+    // (as above)
+    if (p.num_kv_heads == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int Hq = p.num_q_heads, Hkv = p.num_kv_heads, R = FULL ? D : p.rotary_dim, half = R / 2;
     const uint32_t q_bytes = (uint32_t)(Hq * D * (int)sizeof(T)), kv_bytes = (uint32_t)(Hkv * D * (int)sizeof(T));
