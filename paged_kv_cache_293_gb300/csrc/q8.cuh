@@ -27,7 +27,6 @@ __device__ __forceinline__ uint32_t e4m3x4_of_floats(float a, float b, float c, 
     return (uint32_t)lo | ((uint32_t)hi << 16);
 }
 
-constexpr float Q8_LARGEST = 448.f;
 constexpr int Q8_LEAST_POWER = -100;
 
 // The least power of two, 2^-100 at least, whose 448 times reach x (finite, not negative): with

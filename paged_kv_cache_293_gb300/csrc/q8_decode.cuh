@@ -28,7 +28,7 @@
 // operands loaded straight to registers 162 us, too few bytes on their way at 12 warps of 158 registers;
 // this ring with three stages and four CTAs per SM 122 us (two stages 128, three CTAs with four 127, eight
 // warps a CTA 136).  Few requests (4 of ~700 tokens: 7.1 us) are a chain of dependent loads (length,
-// table, scale and page: 2.5 us), three or four steps of about 0.5 us and the cluster's meeting, which
+// table, scale and page), three or four steps and the cluster's meeting, which
 // replaced a merge kernel (9.7 us).
 #pragma once
 
