@@ -57,6 +57,9 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
     return y;
 }
 
+// All ones in the bytes of four e4m3 values that are NaN.
+__device__ __forceinline__ uint32_t nan_codes(uint32_t w) { return __vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu); }
+
 template <typename T> __device__ __forceinline__ float2 pair_to_floats(uint32_t w);
 template <> __device__ __forceinline__ float2 pair_to_floats<__half>(uint32_t w) { return float2_of_f16x2(w); }
 template <> __device__ __forceinline__ float2 pair_to_floats<__nv_bfloat16>(uint32_t w) {
@@ -70,6 +73,10 @@ struct Q8Tile {
     static constexpr int BYTES = CHUNK_TOKENS * D, COLUMNS = BYTES / 16;
     __device__ __forceinline__ static int at(int row, int col) {
         return row * 128 + ((col ^ (D == 128 ? row & 7 : 2 * (row & 3))) << 4);
+    }
+    // elements 4 w .. 4 w + 3 of token t
+    __device__ __forceinline__ static int at_word(int t, int w) {
+        return (D == 128 ? at(t, w >> 2) : at(t >> 1, 4 * (t & 1) + (w >> 2))) + 4 * (w & 3);
     }
     // word w of a lane's part of token t: of a key, bytes c D / 4 + 4 w .. + 3
     __device__ __forceinline__ static void key(const unsigned char* tile, int t, int c, uint32_t (&k)[D / 16]) {
@@ -112,14 +119,18 @@ __device__ __forceinline__ float load_from_cta(uint32_t a, uint32_t rank) {
     return v;
 }
 
-// NT: 8-column tiles of the products, 1 or 2.
-template <typename T, int D, int NT, bool SPLIT_P>
+// NT: 8-column tiles of the products, 1 or 2.  SEVERAL: queries a sequence, which do not see the same tokens
+// (an instance of its own: the code for values that some of them see, in a kernel of one query, cost 128 requests
+// of ~600 tokens 2 % and 64 of ~500 7 %).
+template <typename T, int D, int NT, bool SPLIT_P, bool SEVERAL>
 __global__ void __launch_bounds__(Q8_WARPS * 32, NT * D > 128 ? Q8_CTAS - 1 : Q8_CTAS)
 q8_decode_kernel(const Q8DecodeParams p) {
     constexpr int KS = D / 16, NW = Q8_WARPS, NS = Q8_STAGES, COLS = 8 * NT;
     using Tile = Q8Tile<D>;
     extern __shared__ __align__(128) unsigned char q8_smem[];
     __shared__ float2 stage_scale[NW][NS];
+    __shared__ uint32_t nan_marks[SEVERAL ? NW : 1][COLS][D / 32];  // elements that are NaN besides, a bit each
+    bool marked = false;                                           // this warp has made some
     // [NW], and one for the CTA's result in a cluster, once the rings are done with
     float(*red)[COLS][D + 2] = reinterpret_cast<float(*)[COLS][D + 2]>(q8_smem);
     static_assert((NW + 1) * COLS * (D + 2) * 4 <= q8_smem_bytes<D, NT>(), "the warps' results fit into the rings");
@@ -307,6 +318,37 @@ q8_decode_kernel(const Q8DecodeParams p) {
 #pragma unroll
                     for (int w = 0; w < D / 32; ++w) v[r][w] = 0u;
                 }
+            if constexpr (SEVERAL) {
+                // nor is it for a query that does not see a token which later ones do
+                uint32_t nan = 0u;
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+#pragma unroll
+                    for (int w = 0; w < D / 32; ++w) nan |= nan_codes(v[r][w]);
+                if (__any_sync(FULL_MASK, nan != 0u)) {
+                    // NaN values become zeros, noted for the columns that see them
+                    if (!marked)
+                        for (int x = lane; x < COLS * (D / 32); x += 32) (&nan_marks[warp][0][0])[x] = 0u;
+                    marked = true;
+                    __syncwarp();
+                    unsigned char* const v_tile = ring + st * 2 * Tile::BYTES + Tile::BYTES;
+#pragma unroll 1
+                    for (int x = lane; x < CHUNK_TOKENS * (D / 4); x += 32) {
+                        const int t = x / (D / 4), w = x % (D / 4);
+                        uint32_t* const at = reinterpret_cast<uint32_t*>(v_tile + Tile::at_word(t, w));
+                        const uint32_t codes = t < seen ? nan_codes(*at) : 0xffffffffu;
+                        *at &= ~codes;
+                        if (codes == 0u || t >= seen) continue;
+                        const uint32_t bits = (codes & 0x08040201u) * 0x01010101u >> 24;  // one a byte
+                        for (int n = 0; n < ncols; ++n)
+                            if (t0 + t < ctx - NQ + 1 + (col0 + n) / G)
+                                atomicOr(&nan_marks[warp][n][w / 8], bits << (4 * w % 32));
+                    }
+                    __syncwarp();
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) Tile::value(v_tile, 2 * c + (r & 1) + 8 * (r >> 1), g, v[r]);
+                }
+            }
         }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -393,6 +435,12 @@ q8_decode_kernel(const Q8DecodeParams p) {
                 r[D] = m_ref[nt][h];
                 r[D + 1] = sum;
             }
+            if (SEVERAL && marked) {
+                constexpr int EACH = D / 8;  // of this lane's elements
+                uint32_t nan = nan_marks[warp][8 * nt + 2 * c + h][g * EACH / 32] >> (g * EACH % 32);
+                for (nan &= (1u << EACH) - 1; nan != 0u; nan &= nan - 1)
+                    r[g * EACH + __ffs(nan) - 1] = __int_as_float(0x7fffffff);
+            }
         }
     __syncthreads();
     // zero for a row that sees nothing; a NaN or a sum of no weight is the result
@@ -458,10 +506,10 @@ q8_decode_kernel(const Q8DecodeParams p) {
     }
 }
 
-template <typename T, int D, int NT, bool SPLIT_P>
-cudaError_t launch_q8_decode_tdns(const Q8DecodeParams& p, cudaStream_t stream) {
+template <typename T, int D, int NT, bool SPLIT_P, bool SEVERAL>
+cudaError_t launch_q8_decode_tdnsq(const Q8DecodeParams& p, cudaStream_t stream) {
     constexpr int SMEM = q8_smem_bytes<D, NT>();
-    auto kernel = q8_decode_kernel<T, D, NT, SPLIT_P>;
+    auto kernel = q8_decode_kernel<T, D, NT, SPLIT_P, SEVERAL>;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
@@ -485,6 +533,12 @@ cudaError_t launch_q8_decode_tdns(const Q8DecodeParams& p, cudaStream_t stream) 
     cfg.attrs = attr;
     cfg.numAttrs = p.clustered ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+template <typename T, int D, int NT, bool SPLIT_P>
+cudaError_t launch_q8_decode_tdns(const Q8DecodeParams& p, cudaStream_t stream) {
+    return p.num_queries > 1 ? launch_q8_decode_tdnsq<T, D, NT, SPLIT_P, true>(p, stream)
+                             : launch_q8_decode_tdnsq<T, D, NT, SPLIT_P, false>(p, stream);
 }
 
 template <typename T, int D>
