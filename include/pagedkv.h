@@ -637,14 +637,14 @@ pkv_status pkv_paged_attention_decode_q8(const pkv_q8_pool* pool, int32_t dtype,
  * pkv_paged_attention_chunk over a pool held in 8 bits: arguments, limits and errors as there,
  * with dtype (PKV_F16 or PKV_BF16) for the type of q and out_dtype of PKV_F32 or dtype.  A cached
  * number is its e4m3 value times its page's scale, rounded once: a key's to dtype, a value's to
- * fp16 relative to the largest scale among the pages of its 128 positions.  Where scales are
- * powers of two, as pkv_qk_norm_rope_write_q8 makes them, that is exact, but for numbers of pages
- * whose scale is less than 2^-15 of the largest there (values, and fp16's keys: off by at most
- * 2^-25 of that scale) and values of pages of a scale below 2^-75.  The weights are rounded to
- * fp16 (2^-11 of their value, and 2^-32 of the row's largest; with a remainder of another 11
- * bits when out is fp32).  Scales are finite; those of a context's values, where they are not
- * pages of zeros, lie within a factor of 2^60 of one another.  The workspace is
- * pkv_chunk_q8_workspace_bytes(...) bytes.
+ * fp16, with steps no coarser than it has relative to the largest scale among the pages of its 128
+ * positions.  Where scales are powers of two, as pkv_qk_norm_rope_write_q8 makes them, that is
+ * exact, but for numbers of pages whose scale is less than 2^-15 of the largest there (values, and
+ * fp16's keys: off by at most 2^-25 of that scale) and values of pages of a scale below 2^-75.  The
+ * weights are rounded to fp16 (2^-11 of their value, and 2^-32 of the row's largest, whatever the
+ * scales; with a remainder of another 11 bits when out is fp32).  Scales are finite; those of a
+ * context's values, where they are not pages of zeros, lie within a factor of 2^60 of one another.
+ * The workspace is pkv_chunk_q8_workspace_bytes(...) bytes.
  */
 size_t pkv_chunk_q8_workspace_bytes(const pkv_q8_pool* pool, int32_t num_tokens, int32_t num_seqs,
                                     int32_t num_q_heads, int32_t max_context_len);

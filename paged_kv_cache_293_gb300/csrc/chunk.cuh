@@ -70,18 +70,22 @@
 // Over a pool held in 8 bits (Q8) the pages come in as e4m3 values, and warps 12-15 turn each tile into the
 // 16-bit numbers of the products between its copy and them, ahead of the MMAs by as many stages as there
 // are, and the next piece's first tiles before they put out this one's results.  Keys become the queries'
-// type, values fp16: an e4m3 value times a power of two is exact in either.  fp16 has no room for a
-// page's scale, so a step's pages enter relative to the largest scale among them; of the keys it goes into
-// the factor of the scores, of the values into the exponents of the weights, which are 2^lv times as
-// large, the reference with them, and count for that much less in the row's sum.  What bounds it: shared
-// memory, which the products read at 128 bytes a cycle while scores are made (1540 of a step's cycles), the
-// copies, reads and stores of the conversion take 1020 more of, and the conversion's issue slots beside
-// the softmax's.  (Both figures from the bytes.)  The prompt takes 465 us (359 from 16 bits), 863,000 cycles
-// an SM for 219 steps, pieces' beginnings and ends among them; 500 tokens over 130,500 858 us (689 to 703), 48 requests, 70 % decoding, 302 us (250); fp16 454 and 843 us.
+// type, values fp16: an e4m3 value times a power of two is exact in either.  fp16 has no room for any
+// page's scale, so keys enter relative to the largest scale of their step, which goes into the factor of the
+// scores, and values relative to a power of two, the base, by which O is held until its output.  The base
+// moves only where fp16 would not hold a step's values by it, and O is scaled with it, in 32 bits; so the
+// weights are the same whatever the scales are.  What bounds it: shared memory, which the products read at
+// 128 bytes a cycle while scores are made (1540 of a step's cycles), the copies, reads and stores of the
+// conversion take 1020 more of, and the conversion's issue slots beside the softmax's.  (Both figures from
+// the bytes.)  Besides, the code of all roles together passes what an SM keeps of it: code that is never run
+// cost up to 10 % by where it put the rest (500 tokens over 130,500, with 64 more instructions there 960 us).
+// The prompt takes 465 us (359 from 16 bits), 863,000 cycles an SM for 219 steps, pieces' beginnings and ends
+// among them; 500 tokens over 130,500 855 us (689 to 703); fp16 455 and 850 us.
 // Every wait is bounded; a CTA that gives up sets PKV_DEVERR_TIMEOUT and returns its tensor
 // memory.
 #pragma once
 
+#include <climits>
 #include <type_traits>
 
 #include "decode_mma.cuh"
@@ -112,10 +116,14 @@ struct ChunkReference<__half> {
 // heads, contexts about 300: 79 us (93 with 4 rows).
 constexpr int CHUNK_FEW_ROWS = 16;
 
-// Q8: pages of e4m3 values arrive in a ring of their own, and the stages hold them as numbers of the products' types.
+// Q8: pages arrive as e4m3 values, and the stages hold them as numbers of the products' types.
 // Steps whose references (below) are kept: a step's are written when its copies are issued, at most
 // RAW_STAGES + STAGES stages before its products, and read by the softmax, at most two steps later.
 constexpr int Q8_STEP_RING = 16;
+// Bases of values, as powers of two: what a piece begins with (pages whose largest number lies between 2^-14 and
+// 448 * 2^-1 need no other), and the least one, also relative to the largest so far: O is scaled up by no more.
+constexpr int Q8_FIRST_BASE = -8, Q8_LEAST_BASE = -60;
+constexpr int Q8_PART_POWER = 40;
 template <int D, bool Q8>
 struct ChunkSmem {
     static constexpr int BOXES = D / 64;                  // 128-byte columns of a row
@@ -127,18 +135,19 @@ struct ChunkSmem {
     // D = 64: rows of half a line, in a ring of their own.
     static constexpr bool IN_PLACE = Q8 && D == 128;
     static constexpr int STAGES = D == 128 ? 5 : Q8 ? 6 : 8;
-    static constexpr int RAW_STAGES = Q8 ? (IN_PLACE ? STAGES : 8) : 0;  // tiles of e4m3 values, as their barriers count
+    static constexpr int RAW_STAGES = Q8 ? (IN_PLACE ? STAGES : 8) : 0;  // of e4m3 values, as their barriers count
     static constexpr int RAW_TILE = 128 * D;
     static constexpr int Q_OFF = 0;
     static constexpr int KV_OFF = 2 * TILE;
     static constexpr int RAW_OFF = KV_OFF + STAGES * TILE;
     static constexpr int SCALE_OFF = RAW_OFF + (IN_PLACE ? 0 : RAW_STAGES * RAW_TILE);  // float [RAW_STAGES][8 copies]
-    static constexpr int STEP_OFF = SCALE_OFF + RAW_STAGES * 32;       // float2 [Q8_STEP_RING]
-    static constexpr int BAR_OFF = STEP_OFF + (Q8 ? Q8_STEP_RING * 8 : 0);
+    static constexpr int STEP_OFF = SCALE_OFF + RAW_STAGES * 32;       // float4 [Q8_STEP_RING]
+    static constexpr int BAR_OFF = STEP_OFF + (Q8 ? Q8_STEP_RING * 16 : 0);
     static constexpr int NBARS = 2 * STAGES + 31 + 2 * RAW_STAGES;
     static constexpr int PIECE_OFF = BAR_OFF + ((NBARS * 8 + 15) / 16) * 16;
     static constexpr int STAT_OFF = PIECE_OFF + 2 * 32;  // float [2 tiles][m, l][128 rows]
-    static constexpr int TMEM_SLOT_OFF = STAT_OFF + 2 * 2 * 128 * 4;
+    static constexpr int BASE_OFF = STAT_OFF + 2 * 2 * 128 * 4;  // Q8: int [4], the bases that pieces end with
+    static constexpr int TMEM_SLOT_OFF = BASE_OFF + 16;
     static constexpr int BYTES = TMEM_SLOT_OFF + 16;
     // tensor memory columns: S_0, S_1 (P over them), O_0, O_1; of a piece with few rows P has the
     // last 128 columns
@@ -188,12 +197,24 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return v;
 }
 
-// Adds the row's total, kept at `kept` (its 16-byte columns 128 apart) and scaled by f, to its O at
-// o_t.  TO_TOTAL: the sum becomes the total (the `first` one is O alone), and O zero.  Out of line:
-// inlined, it cost steps that never come here (8192-token prompt 365 us, 360 so).
-template <int D, bool TO_TOTAL>
-__device__ __noinline__ void add_total(uint32_t o_t, float4* kept, float f, bool first) {
+// 2 to a whole number from -126 to 127.
+__device__ __forceinline__ float two_to(int x) { return __int_as_float((x + 127) << 23); }
+
+// Adds the row's total, kept at `kept` (its 16-byte columns 128 apart; O's, then the sum and their
+// reference), to its O at o_t and its sum l.  TO_TOTAL: the sums become the total (the `first` ones are O and
+// l alone), and O zero.  Q8: the total is held by a base of 2^40, O by base[0]'s.  Returns the sum.  Out of
+// line: inlined, it cost steps that never come here (8192-token prompt 365 us, 360 so).
+template <int D, bool TO_TOTAL, bool Q8>
+__device__ __noinline__ float add_total(uint32_t o_t, float4* kept, float m_ref, float l, const int* base,
+                                        bool first) {
     const uint32_t zeros[16] = {0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
+    float2* const sum_and_ref = reinterpret_cast<float2*>(kept + D / 4 * 128);
+    const float2 before = first ? make_float2(0.f, m_ref) : *sum_and_ref;
+    float f = before.y == m_ref ? 1.f : fast_exp2(before.y - m_ref);
+    l = fmaf(before.x, f, l);
+    if (TO_TOTAL) *sum_and_ref = make_float2(l, m_ref);
+    const float unit = Q8 && TO_TOTAL ? two_to(*base - Q8_PART_POWER) : 1.f;
+    if (Q8 && !TO_TOTAL) f *= two_to(Q8_PART_POWER - *base);
 #pragma unroll 1
     for (int d = 0; d < D; d += 16) {
         float4 v[4];
@@ -201,6 +222,10 @@ __device__ __noinline__ void add_total(uint32_t o_t, float4* kept, float f, bool
 #pragma unroll
         for (int k = 0; k < 4; ++k) v[k] = first ? make_float4(0.f, 0.f, 0.f, 0.f) : kept[(d / 4 + k) * 128];
         umma::ld16(o_t + d, o);
+        if (Q8 && TO_TOTAL) {
+#pragma unroll
+            for (int k = 0; k < 16; ++k) o[k] *= unit;
+        }
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             o[4 * k] = fmaf(v[k].x, f, o[4 * k]);
@@ -222,24 +247,28 @@ __device__ __noinline__ void add_total(uint32_t o_t, float4* kept, float f, bool
     }
     umma::wait_st();
     umma::fence_before_sync();
+    return l;
 }
 
-// 2 to a whole number from -126 to 127.  (The sum holds it in its last bits.)
-__device__ __forceinline__ float two_to(float x) {
-    return __int_as_float((__float_as_int(x + 12582912.f) - 0x4b400000 + 127) << 23);
+// The base of a step's values, from their pages' scales (a lane each; 0: none), the base of the steps before
+// and the largest one so far.  Whole warps.  Out of line: seldom called.
+static __device__ __noinline__ int moved_base(int scale, int base, int base_top) {
+    const int most = __reduce_max_sync(FULL_MASK, scale);
+    const int least = __reduce_min_sync(FULL_MASK, scale == 0 ? INT_MAX : (scale & 0x7fffff) == 0 ? scale : 0);
+    const int power = (most >> 23) - 127 + ((most & 0x7fffff) != 0);  // of two, that reaches the largest
+    if (power <= base + 7 && base <= max((least >> 23) - 127 + 15, power)) return base;
+    return min(max(power - 4, max(base_top, 0) + Q8_LEAST_BASE), 126);
 }
 
 // One step of a row: its 128 scores from tensor memory at s_t, the running reference m_ref and
 // the sum (in two parts), its O at o_t scaled where the reference rose (once phase_o of
 // bar_o says that the products before are done; 0: known), and its weights written over the
 // scores, the halves handed on at bar_lo and bar_hi.
-// Q8: the values of this step are 2^lv smaller than they should be, so its weights are taken 2^lv
-// times as large, the reference with them, and count for that much less in the sum.
-// (exponent() reads lv from shared memory: a second time at the end, so that no register keeps it.)
+// Q8: moved is what O is multiplied with besides, where the base of the values moves with this step.
 // edge: the warp has scores that their rows do not see.
-template <typename T, int D, bool SPLIT_P, bool Q8, typename Edge, typename Exponent>
+template <typename T, int D, bool SPLIT_P, bool Q8, typename Edge>
 __device__ __forceinline__ bool softmax_step(uint32_t s_t, uint32_t o_t, int seen, const Edge edge, bool has_o,
-                                             float scale_log2, const Exponent& exponent, float& m_ref, uint64_t& sum2,
+                                             float scale_log2, float moved, float& m_ref, uint64_t& sum2,
                                              uint32_t bar_lo, uint32_t bar_hi, uint32_t bar_o,
                                              uint32_t phase_o) {
     constexpr int N = CHUNK_TILE, HALF = N / 2;
@@ -273,15 +302,14 @@ __device__ __forceinline__ bool softmax_step(uint32_t s_t, uint32_t o_t, int see
     }
     using Ref = ChunkReference<T>;
     const float most = max3(max3(top[0], top[1], top[2]), max3(top[3], top[4], top[5]), fmaxf(top[6], top[7]));
-    const float lv = exponent();
-    const float cm = Q8 ? __fmaf_ru(most, scale_log2, lv) : Ref::scaled(most, scale_log2);
+    const float cm = Ref::scaled(most, scale_log2);
     const bool need = cm - m_ref > Ref::RAISE;
     float alpha = 1.f;
     if (need) {
         alpha = fast_exp2(m_ref - (cm - Ref::BELOW));
         m_ref = cm - Ref::BELOW;
     }
-    const float neg = m_ref == -INFINITY ? 0.f : Q8 ? lv - m_ref : -m_ref;
+    const float neg = m_ref == -INFINITY ? 0.f : -m_ref;
     const uint64_t scale2 = pack2(scale_log2, scale_log2), neg2 = pack2(neg, neg);
     sum2 = mul2(sum2, pack2(alpha, alpha));
     uint64_t step2[2] = {0, 0};
@@ -301,8 +329,10 @@ __device__ __forceinline__ bool softmax_step(uint32_t s_t, uint32_t o_t, int see
         umma::st16(s_t + c / 2, hi);
         if (SPLIT_P) umma::st16(s_t + HALF + c / 2, lo);
         if (c == HALF - 32) {
-            // rows whose reference rose: scale their O, complete through the step before
-            if (has_o && __any_sync(FULL_MASK, need)) {
+            // rows whose reference rose, or all where the base moves: scale their O, complete through the
+            // step before
+            if (has_o && (__any_sync(FULL_MASK, need) || (Q8 && moved != 1.f))) {
+                if (Q8) alpha *= moved;
                 if (bar_o != 0) {
                     if (!__all_sync(FULL_MASK, mbar_wait_short(bar_o, phase_o & 1))) return false;
                     umma::fence_after_sync();
@@ -323,12 +353,7 @@ __device__ __forceinline__ bool softmax_step(uint32_t s_t, uint32_t o_t, int see
             if (lane == 0) mbar_arrive(bar_lo);
         }
     }
-    if (Q8) {
-        const float by = two_to(-exponent());
-        sum2 = fma2(add2(step2[0], step2[1]), pack2(by, by), sum2);
-    } else {
-        sum2 = add2(sum2, add2(step2[0], step2[1]));
-    }
+    sum2 = add2(sum2, add2(step2[0], step2[1]));
     umma::wait_st();
     umma::fence_before_sync();
     __syncwarp();
@@ -340,7 +365,7 @@ __device__ __forceinline__ bool softmax_step(uint32_t s_t, uint32_t o_t, int see
 // and O as in softmax_step, the weights to p_t.  The caller hands them on.
 template <typename T, int D, bool Q8>
 __device__ __forceinline__ bool few_rows_step(uint32_t s_t, uint32_t p_t, uint32_t o_t, int seen, bool has_o,
-                                              float scale_log2, float lv, float& m_ref, float& l, uint32_t bar_o,
+                                              float scale_log2, float moved, float& m_ref, float& l, uint32_t bar_o,
                                               uint32_t phase_o) {
     uint32_t raw[32];
     umma::ld32_async(s_t, raw);
@@ -360,16 +385,17 @@ __device__ __forceinline__ bool few_rows_step(uint32_t s_t, uint32_t p_t, uint32
     }
     using Ref = ChunkReference<T>;
     const float most = max3(top[0], top[1], fmaxf(top[2], top[3]));
-    const float cm = Q8 ? __fmaf_ru(most, scale_log2, lv) : Ref::scaled(most, scale_log2);
+    const float cm = Ref::scaled(most, scale_log2);
     const bool need = cm - m_ref > Ref::RAISE;
-    if (__any_sync(FULL_MASK, need)) {
+    if (__any_sync(FULL_MASK, need) || (Q8 && moved != 1.f)) {
         float alpha = 1.f;
         if (need) {
             alpha = fast_exp2(m_ref - (cm - Ref::BELOW));
             m_ref = cm - Ref::BELOW;
         }
         l *= alpha;
-        if (has_o) {  // rows whose reference rose: scale their O, complete through the step before
+        if (Q8) alpha *= moved;
+        if (has_o) {  // rows whose reference rose (all, where the base moves): O is complete through the step before
             if (!__all_sync(FULL_MASK, mbar_wait_short(bar_o, phase_o & 1))) return false;
             umma::fence_after_sync();
 #pragma unroll 1
@@ -383,7 +409,7 @@ __device__ __forceinline__ bool few_rows_step(uint32_t s_t, uint32_t p_t, uint32
             }
         }
     }
-    const float neg = m_ref == -INFINITY ? 0.f : Q8 ? lv - m_ref : -m_ref;
+    const float neg = m_ref == -INFINITY ? 0.f : -m_ref;
     const uint64_t scale2 = pack2(scale_log2, scale_log2), neg2 = pack2(neg, neg);
     uint64_t sum2[2] = {0, 0};
     uint32_t hi[16];
@@ -401,7 +427,7 @@ __device__ __forceinline__ bool few_rows_step(uint32_t s_t, uint32_t p_t, uint32
     unpack2(sum2[0], part[0], part[1]);
     unpack2(sum2[1], part[2], part[3]);
     const float sum = (part[0] + part[1]) + (part[2] + part[3]);
-    l = Q8 ? fmaf(sum, two_to(-lv), l) : l + sum;
+    l += sum;
     umma::wait_st();
     umma::fence_before_sync();
     __syncwarp();
@@ -432,7 +458,8 @@ __device__ __forceinline__ void numbers_by(const unsigned char* raw, const float
     at += ((col + swap) ^ (r & 7)) << 4;
     const int other = ((((col + swap) ^ 1) ^ (r & 7)) << 4) - (((col + swap) ^ (r & 7)) << 4);
     // (in place: the row's place in the second half of the numbers)
-    raw = IN_PLACE ? tile + b0 * copy + (is_v ? CHUNK_TOKENS * 128 : 128 * 128) + r * 128 + m * 16 : raw + row0 * D + m * 16;
+    raw = IN_PLACE ? tile + b0 * copy + (is_v ? CHUNK_TOKENS * 128 : 128 * 128) + r * 128 + m * 16
+                   : raw + row0 * D + m * 16;
     const int raw_stride = IN_PLACE ? stride : 4 * ROWS * D;
     // (short loops: the code of all roles shares the instruction cache; whole, they cost a prompt 10 %)
 #pragma unroll 1
@@ -462,7 +489,8 @@ __device__ __forceinline__ void numbers_by(const unsigned char* raw, const float
                     out[k] = Mma<M>::pack(a, c);
                 }
             }
-            const uint4 lo4 = make_uint4(out[0], out[1], out[2], out[3]), hi4 = make_uint4(out[4], out[5], out[6], out[7]);
+            const uint4 lo4 = make_uint4(out[0], out[1], out[2], out[3]);
+            const uint4 hi4 = make_uint4(out[4], out[5], out[6], out[7]);
             *reinterpret_cast<uint4*>(at + (i + u) * stride) = swap ? hi4 : lo4;
             *reinterpret_cast<uint4*>(at + (i + u) * stride + other) = swap ? lo4 : hi4;
         }
@@ -537,9 +565,13 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
     auto raw_full = [&](int st) { return bar0 + 8 * (NB + 31 + st); };
     auto raw_empty = [&](int st) { return bar0 + 8 * (NB + 31 + NR + st); };
     float* raw_scale = reinterpret_cast<float*>(smem + L::SCALE_OFF);
-    // of the n-th step of this CTA: what its keys are smaller by (fp16 ones), and its values (in base 2)
-    float2* step_ref = reinterpret_cast<float2*>(smem + L::STEP_OFF);
+    // of the n-th step of this CTA: what its keys are smaller by (fp16 ones), what O is multiplied with where the
+    // base of its values is another than that of the step before (1 otherwise), and that base
+    float4* step_ref = reinterpret_cast<float4*>(smem + L::STEP_OFF);
     float* stats = reinterpret_cast<float*>(smem + L::STAT_OFF);  // + 256 t: m, + 128: l
+    // Q8: the base that the n-th piece of this CTA ends with (whoever takes a piece is done with the one before the
+    // last, and pieces are published two ahead: four places)
+    int* piece_base = reinterpret_cast<int*>(smem + L::BASE_OFF);
     auto is_few = [&](const ChunkPiece& x) {
         return !SPLIT_P && x.queries * G <= CHUNK_FEW_ROWS && x.kt1 > x.kt0;
     };
@@ -641,36 +673,50 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
                 };
                 int row = row_of(pc.kt0);
                 // Q8: the scales of this lane's copy (far_row: a multiple of B, past the last page)
-                float scale_next[2] = {0.f, 0.f};
-                auto scales_of = [&](int row) {
-                    scale_next[0] = scale_next[1] = 0.f;
+                float scale_now[2] = {0.f, 0.f}, scale_next[2] = {0.f, 0.f};
+                auto scales_of = [&](int row, float (&s)[2]) {
+                    s[0] = s[1] = 0.f;
                     if (row != far_row) {
-                        scale_next[0] = __ldg(p.k_scale + row / B);
-                        scale_next[1] = __ldg(p.v_scale + row / B);
+                        s[0] = __ldg(p.k_scale + row / B);
+                        s[1] = __ldg(p.v_scale + row / B);
                     }
                 };
-                if constexpr (Q8) scales_of(row);
-                // In fp16 a step's pages enter the products relative to the largest scale among them, of values
-                // to the power of two that reaches it, which goes into the exponents; numbers of pages far
-                // smaller than that lose bits in fp16's last steps, 2^-33 of the step's largest.
+                int row_then = 0;
+                if constexpr (Q8) {
+                    scales_of(row, scale_now);
+                    row_then = row_of(pc.kt0 + 1);
+                }
+                // In fp16 a step's keys enter the products relative to the largest scale among their pages, which
+                // goes into the scores' factor: numbers of pages far smaller than that lose bits in fp16's last
+                // steps, 2^-33 of the step's largest.  Values enter relative to 2^base, and O is a sum of such.
+                // The base stays while fp16 holds the step's values by it: up to 2^7 times the base in scale, and
+                // down to 2^-15 of it where scales are powers of two (e4m3's steps of 2^-9 times that are 2^-24),
+                // otherwise no less than it; pages smaller than 2^-15 of the step's largest do not count.  So it
+                // moves seldom, and then to 2^-4 of the largest.
                 float factor[2] = {0.f, 0.f};
+                int base = Q8_FIRST_BASE, base_top = Q8_FIRST_BASE;
                 auto make_factors = [&] {
-                    float most[2];
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        most[k] = fabsf(scale_next[k]);
-#pragma unroll
-                        for (int o = 4; o >= 1; o >>= 1) most[k] = fmaxf(most[k], __shfl_xor_sync(FULL_MASK, most[k], o));
+                    // (sizes as whole numbers, which are ordered alike; lanes without a page have zeros)
+                    const int own = __float_as_int(fabsf(scale_now[1])), before = base;
+                    const bool fits = (own & 0x7fffff) == 0 && (unsigned)own - ((base - 15 + 127) << 23) <= 22u << 23;
+                    if (!__all_sync(FULL_MASK, fits || own == 0)) {
+                        base = moved_base(own, base, base_top);
+                        base_top = max(base_top, base);
                     }
-                    // (values below 2^-69 of numbers that 8 bits hold at a scale of 1 fade out)
-                    const int bits = __float_as_int(most[1]);
-                    const int lv = min(max((bits >> 23) - 127 + ((bits & 0x7fffff) != 0), -60), 126);
-                    factor[0] = !KEYS_F16 ? scale_next[0] : most[0] > 0.f ? scale_next[0] / most[0] : 0.f;
-                    factor[1] = scale_next[1] * __int_as_float((127 - lv) << 23);
-                    if (lane == 0) step_ref[(it / 2) % Q8_STEP_RING] = make_float2(most[0], (float)lv);
+                    const float moved = two_to(max(before - base, -126));
+                    float keys = 0.f;
+                    if (KEYS_F16)
+                        keys = __int_as_float(__reduce_max_sync(FULL_MASK, __float_as_int(fabsf(scale_now[0]))));
+                    factor[0] = !KEYS_F16 ? scale_now[0] : keys > 0.f ? scale_now[0] / keys : 0.f;
+                    factor[1] = scale_now[1] * two_to(-base);
+                    if (lane == 0) {
+                        step_ref[(it / 2) % Q8_STEP_RING] = make_float4(keys, moved, __int_as_float(base), 0.f);
+                        piece_base[i & 3] = base;
+                    }
                 };
                 for (int kt = pc.kt0; kt < pc.kt1 && ok; ++kt) {
-                    const int row_next = row_of(kt + 1);
+                    const int row_next = row_of(Q8 ? kt + 2 : kt + 1);
+                    if constexpr (Q8) scales_of(row_then, scale_next);
                     int rows[NBOX];
 #pragma unroll
                     for (int b = 0; b < NBOX; ++b) rows[b] = __shfl_sync(FULL_MASK, row, b);
@@ -730,8 +776,14 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
                         }
                         __syncwarp();
                     }
-                    row = row_next;
-                    if constexpr (Q8) scales_of(row);  // (the table's entry has been on its way since the step began)
+                    if constexpr (Q8) {
+                        row = row_then;
+                        row_then = row_next;
+                        scale_now[0] = scale_next[0];
+                        scale_now[1] = scale_next[1];
+                    } else {
+                        row = row_next;
+                    }
                 }
                 if (!ok) break;
                 idx = __shfl_sync(FULL_MASK, next, 0);
@@ -967,7 +1019,8 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
         auto make_stages = [&](int count) -> bool {
             for (int k = 0; k < count; ++k, ++made) {
                 const int from = made % (NR > 0 ? NR : 1), st = made % NS;
-                if (!__all_sync(FULL_MASK, mbar_wait_short(raw_full(from), (made / (NR > 0 ? NR : 1)) & 1))) return false;
+                if (!__all_sync(FULL_MASK, mbar_wait_short(raw_full(from), (made / (NR > 0 ? NR : 1)) & 1)))
+                    return false;
                 if (!L::IN_PLACE && made >= NS &&
                     !__all_sync(FULL_MASK, mbar_wait_short(kv_empty(st), (made / NS - 1) & 1)))
                     return false;
@@ -1036,7 +1089,16 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
                     if (!ok) break;
                     umma::fence_after_sync();
                 }
-                const float m = stats[256 * t + r], l = n > 0 ? stats[256 * t + 128 + r] : 0.f;
+                const float m = stats[256 * t + r];
+                float l = n > 0 ? stats[256 * t + 128 + r] : 0.f;
+                // Q8: O times its base; of a part of a row 2^-40 of that and of the sum, whose weights go up to
+                // 2^15, so that values at the end of the range leave room for them
+                float unit = 1.f, sum_unit = 1.f;
+                if (Q8 && n > 0) {
+                    sum_unit = direct ? 1.f : two_to(-Q8_PART_POWER);
+                    unit = two_to(piece_base[i & 3]) * sum_unit;
+                    l *= sum_unit;
+                }
                 if (few) {
                     // the four results of each row meet in the second Q tile; row r's 16-byte
                     // columns are turned by r, so that a warp's stores spread over the banks
@@ -1068,7 +1130,7 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
 #pragma unroll
                         for (int y = 0; y < 4; ++y) {
                             f[y] = fast_exp2(stats[y * 32 + x] - ref);
-                            sum = fmaf(f[y], stats[128 + y * 32 + x], sum);
+                            sum = fmaf(f[y], stats[128 + y * 32 + x] * sum_unit, sum);
                         }
                         // zero for a row that sees nothing; a NaN or a sum of no weight is the result
                         const float inv = !direct ? 1.f : pc.lim0 + x / G > 0 ? 1.f / sum : 0.f;
@@ -1080,7 +1142,7 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
 #pragma unroll
                             for (int y = 0; y < 4; ++y) {
                                 const float4 v = rows_s[(y * CHUNK_FEW_ROWS + x) * COLS + (lane + x) % COLS];
-                                const float fw = f[y] * inv;
+                                const float fw = f[y] * (inv * unit);
                                 o.x = fmaf(fw, v.x, o.x);
                                 o.y = fmaf(fw, v.y, o.y);
                                 o.z = fmaf(fw, v.z, o.z);
@@ -1115,7 +1177,7 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
                     // a row that sees nothing is zero, whatever O holds; a NaN in its sum, or no weight
                     // in it although it sees tokens (scores of -inf), is the result
                     const bool nothing = direct ? pc.lim0 + jq <= 0 : l == 0.f;
-                    const float by = direct ? 1.f / l : 1.f;
+                    const float by = (direct ? 1.f / l : 1.f) * unit;
                     // once per piece: a loop that stays in the instruction cache
 #pragma unroll 1
                     for (int c = 0; c < D; c += 16) {
@@ -1168,34 +1230,29 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
         int outs = 0, twos = 0;  // pieces handed to the output warps, those with two tiles: of o_free
         uint32_t steps = 0;      // Q8: of the pieces before, as step_ref counts them
         // what the scores of step j of the piece are multiplied with (positive, though nothing be left of it:
-        // hidden scores are -inf), and the exponent that its weights are larger by
-        auto step_scale = [&](int j) -> float {
+        // hidden scores are -inf), what O is where the base of the values moves, and that base
+        auto step_scale = [&](const float2& ref) -> float {
             if constexpr (!Q8 || !KEYS_F16) return p.scale_log2;
-            return fmaxf(p.scale_log2 * step_ref[(steps + j) % Q8_STEP_RING].x, 1.2e-38f);
+            return fmaxf(p.scale_log2 * ref.x, 1.2e-38f);
         };
-        auto step_exponent = [&](int j) -> float { return Q8 ? step_ref[(steps + j) % Q8_STEP_RING].y : 0.f; };
+        auto step_at = [&](int j) -> float2 {
+            return Q8 ? *reinterpret_cast<const float2*>(step_ref + (steps + j) % Q8_STEP_RING) : make_float2(1.f, 1.f);
+        };
         bool p_clear = false;    // the P columns of pieces with few rows hold zeros where they should
-        // The row's totals of the steps before, in the workspace: O's, then the sum and their
-        // reference (not in registers, which the steps need).
+        // The row's totals of the steps before, in the workspace: O's, then the sum and their reference (not in
+        // registers, which the steps need).
         auto kept = [&]() -> float4* {
             return reinterpret_cast<float4*>(p.totals) + (blockIdx.x * 2 + t) * (128 * (D / 4 + 1)) + r;
         };
-        auto to_now = [](float m_kept, float m_ref) { return m_kept == m_ref ? 1.f : fast_exp2(m_kept - m_ref); };
         // before step j's softmax, its products so far done: O and the sum into the totals
         auto keep = [&](int j, float m_ref, float l) {
-            float2* const sum_and_ref = reinterpret_cast<float2*>(kept() + D / 4 * 128);
-            const bool first = j == CHUNK_SUM_STEPS;
-            const float2 before = first ? make_float2(0.f, m_ref) : *sum_and_ref;
-            const float f = to_now(before.y, m_ref);
-            add_total<D, true>(o_t, kept(), f, first);
-            *sum_and_ref = make_float2(fmaf(before.x, f, l), m_ref);
+            const float4* const ref = step_ref + (steps + j - 1) % Q8_STEP_RING;
+            add_total<D, true, Q8>(o_t, kept(), m_ref, l, Q8 ? reinterpret_cast<const int*>(ref) + 2 : nullptr,
+                                   j == CHUNK_SUM_STEPS);
         };
-        // at the end, all products done: the totals into O and the sum
-        auto total = [&](float m_ref, float l) -> float {
-            const float2 before = *reinterpret_cast<const float2*>(kept() + D / 4 * 128);
-            const float f = to_now(before.y, m_ref);
-            add_total<D, false>(o_t, kept(), f, false);
-            return fmaf(before.x, f, l);
+        // at the end of piece i, all products done: the totals into O and the sum
+        auto total = [&](int i, float m_ref, float l) -> float {
+            return add_total<D, false, Q8>(o_t, kept(), m_ref, l, Q8 ? piece_base + (i & 3) : nullptr, false);
         };
         // waits for the products of the steps before step j (not yet taken), or of all of a piece
         auto products_before = [&](int j, bool two, bool all = false) -> bool {
@@ -1259,10 +1316,11 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
                         ok = __all_sync(FULL_MASK, mbar_wait_short(s_full(2 + b), phase & 1));
                         if (!ok) break;
                         umma::fence_after_sync();
-                        const float by = step_scale(j), lv = step_exponent(j);
+                        const float2 ref = step_at(j);
+                        const float by = step_scale(ref), moved = ref.y;
                         ok = few_rows_step<M, D, Q8>(lane_tmem + b * CHUNK_TILE + warp * 32,
                                                      p_t + b * (CHUNK_TILE / 2) + warp * 16, o_t,
-                                                     lim_w - (pc.kt0 + j) * CHUNK_TILE, j > 0, by, lv, m_ref, l,
+                                                     lim_w - (pc.kt0 + j) * CHUNK_TILE, j > 0, by, moved, m_ref, l,
                                                      pv_step(b ^ 1), (b ? taken_even : taken_odd) - 1);
                         if (!ok) break;
                         if (lane == 0) {
@@ -1273,7 +1331,7 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
                 }
                 if (ok && n > CHUNK_SUM_STEPS) {
                     ok = products_before(n, false, true);
-                    if (ok) l = total(m_ref, l);
+                    if (ok) l = total(i, m_ref, l);
                 }
                 steps += n;
                 if (!ok || !hand_out(m_ref, l)) break;
@@ -1302,8 +1360,8 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
                     if (!ok) break;
                     if (busy) {
                         umma::fence_after_sync();
-                        const float by = step_scale(j);
-                        auto lv = [&] { return step_exponent(j); };
+                        const float2 ref = step_at(j);
+                        const float by = step_scale(ref), moved = ref.y;
                         const uint32_t s_t = lane_tmem + (b & 1) * CHUNK_TILE;
                         const int seen = lim - (pc.kt0 + j) * CHUNK_TILE;  // columns this row may see
                         // with two tiles a step's S was committed after the P.V before, with one not
@@ -1315,14 +1373,16 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
                         // 500 queries over 130,500 tokens, heads of 128, fp16, 847 us (885 with two), but bf16
                         // 912 (861 with two).
                         if (Q8 && (D == 64 || KEYS_F16))
-                            ok = softmax_step<M, D, SPLIT_P, Q8>(s_t, o_t, seen, edge, j > 0, by, lv, m_ref, sum2,
+                            ok = softmax_step<M, D, SPLIT_P, Q8>(s_t, o_t, seen, edge, j > 0, by, moved, m_ref, sum2,
                                                                  p_full(b, 0), p_full(b, 1), wait_o, phase_o);
                         else if (edge)
-                            ok = softmax_step<M, D, SPLIT_P, Q8>(s_t, o_t, seen, std::true_type(), j > 0, by, lv, m_ref,
-                                                                 sum2, p_full(b, 0), p_full(b, 1), wait_o, phase_o);
+                            ok = softmax_step<M, D, SPLIT_P, Q8>(s_t, o_t, seen, std::true_type(), j > 0, by, moved,
+                                                                 m_ref, sum2, p_full(b, 0), p_full(b, 1), wait_o,
+                                                                 phase_o);
                         else
-                            ok = softmax_step<M, D, SPLIT_P, Q8>(s_t, o_t, seen, std::false_type(), j > 0, by, lv, m_ref,
-                                                                 sum2, p_full(b, 0), p_full(b, 1), wait_o, phase_o);
+                            ok = softmax_step<M, D, SPLIT_P, Q8>(s_t, o_t, seen, std::false_type(), j > 0, by, moved,
+                                                                 m_ref, sum2, p_full(b, 0), p_full(b, 1), wait_o,
+                                                                 phase_o);
                         if (!ok) break;
                     } else if (lane == 0) {  // rows of no query: whatever S left there
                         mbar_arrive(p_full(b, 0));
@@ -1336,7 +1396,7 @@ chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
             if (busy && n > CHUNK_SUM_STEPS) {
                 ok = products_before(n, two, true);
                 if (!ok) break;
-                l = total(m_ref, l);
+                l = total(i, m_ref, l);
             }
             if (two) {
                 p_clear = false;
