@@ -613,14 +613,16 @@ pkv_status pkv_qk_norm_rope_write_q8(const pkv_q8_pool* pool, int32_t dtype, con
  *   workspace     pkv_decode_q8_workspace_bytes(...) bytes (0: none needed), 16-byte aligned;
  *                 calls that may run at the same time need one each
  * Any group size num_q_heads / num_kv_heads.  num_seqs and the number of pieces of a context
- * up to 65535 each, max_context_len up to 2^30.  The queries enter their products exactly (in bf16, but for elements below 2^-30
- * of their row's largest), the probabilities rounded to fp16 (off by at most 2^-11 of their value,
- * and 2^-32 of the row's largest), with a remainder of another 11 bits when out is fp32.
+ * up to 65535 each, max_context_len up to 2^30.  The queries enter their products exactly (in
+ * bf16, but for elements below 2^-30 of their row's largest), the probabilities rounded to fp16
+ * (off by at most 2^-11 of their value, and 2^-32 of the row's largest), with a remainder of
+ * another 11 bits when out is fp32.
  * Cached rows past a query's last position may hold anything.  A row that sees tokens is NaN
- * where its scores hold a NaN or pass fp32's range, or a seen value is NaN.  Scales are finite.
+ * where its scores hold a NaN or pass fp32's range (downwards: where all do), or a seen value is
+ * NaN.  Scales are finite.
  * Device errors: a context_lens entry negative or past the table row or max_context_len
  * (PKV_DEVERR_CONTEXT, cut to that range); a table entry outside the pool
- * (PKV_DEVERR_BLOCK_ID, its positions are left out).
+ * (PKV_DEVERR_BLOCK_ID, its positions are left out: a row that has no other is zero).
  */
 size_t pkv_decode_q8_workspace_bytes(const pkv_q8_pool* pool, int32_t num_seqs,
                                      int32_t num_queries, int32_t num_q_heads,

@@ -32,6 +32,9 @@
 // replaced a merge kernel (9.7 us).
 #pragma once
 
+#include <cfloat>
+#include <climits>
+
 #include "decode_mma.cuh"
 #include "q8.cuh"
 
@@ -178,13 +181,15 @@ q8_decode_kernel(const Q8DecodeParams p) {
         va = __ldg(p.v_scale + at);
     };
     unsigned char* const ring = q8_smem + warp * NS * 2 * Tile::BYTES;
-    unsigned there = 0;  // stages that hold a page
+    unsigned there = 0;  // stages that hold a page; bit 31: one did
+    int first = INT_MAX;  // (several queries) from where on
     auto issue = [&](int i) {
         if (i < n_my) {
             if ((i & 31) == 0) look_up(i + lane);
             const int phys = __shfl_sync(FULL_MASK, page, i & 31), st = i % NS;
             const float a_b = __shfl_sync(FULL_MASK, ka, i & 31), c_b = __shfl_sync(FULL_MASK, va, i & 31);
-            there = phys >= 0 ? there | (1u << st) : there & ~(1u << st);
+            there = phys >= 0 ? there | (1u << st | 1u << 31) : there & ~(1u << st);
+            if (SEVERAL && phys >= 0) first = min(first, token_of(i));
             if (lane == 0) stage_scale[warp][st] = make_float2(a_b, c_b);
             if (phys >= 0) {
                 const size_t at = ((((size_t)phys * Hkv + kvh) << shift) + (token_of(i) & (B - 1))) * D;
@@ -339,10 +344,11 @@ q8_decode_kernel(const Q8DecodeParams p) {
                         const uint32_t codes = t < seen ? nan_codes(*at) : 0xffffffffu;
                         *at &= ~codes;
                         if (codes == 0u || t >= seen) continue;
-                        const uint32_t bits = (codes & 0x08040201u) * 0x01010101u >> 24;  // one a byte
+                        // (a bit a byte)
+                        const uint32_t bits = ((codes & 0x08040201u) * 0x01010101u >> 24) << (4 * w % 32);
                         for (int n = 0; n < ncols; ++n)
                             if (t0 + t < ctx - NQ + 1 + (col0 + n) / G)
-                                atomicOr(&nan_marks[warp][n][w / 8], bits << (4 * w % 32));
+                                atomicOr(&nan_marks[warp][n][w / 8], bits);
                     }
                     __syncwarp();
 #pragma unroll
@@ -432,7 +438,9 @@ q8_decode_kernel(const Q8DecodeParams p) {
                 r[g * (D / 8) + 2 * i + 1] = o[nt][i][h + 2];
             }
             if (g == 0) {
-                r[D] = m_ref[nt][h];
+                // (-inf: a row that sees no page; one whose scores are all -inf does)
+                const bool sees = SEVERAL ? first < lim[nt][h] : there >> 31 != 0u;
+                r[D] = sees ? fmaxf(m_ref[nt][h], -FLT_MAX) : m_ref[nt][h];
                 r[D + 1] = sum;
             }
             if (SEVERAL && marked) {
@@ -444,9 +452,8 @@ q8_decode_kernel(const Q8DecodeParams p) {
         }
     __syncthreads();
     // zero for a row that sees nothing; a NaN or a sum of no weight is the result
-    auto finish = [&](int n, int d, float O, float L) {
-        const bool nothing = ctx - NQ + 1 + (col0 + n) / G <= 0;
-        store_out(p.out, p.out_dtype, row_of(n) * D + d, nothing ? 0.f : O / L);
+    auto finish = [&](int n, int d, float M, float O, float L) {
+        store_out(p.out, p.out_dtype, row_of(n) * D + d, M == -INFINITY ? 0.f : O / L);
     };
     for (int i = threadIdx.x; i < ncols * D; i += NW * 32) {
         const int n = i / D, d = i % D;
@@ -468,7 +475,7 @@ q8_decode_kernel(const Q8DecodeParams p) {
                 red[NW][n][D + 1] = L;
             }
         } else if (direct) {
-            finish(n, d, O, L);
+            finish(n, d, M, O, L);
         } else {
             const size_t at_part = row_of(n) * p.max_parts + part;
             p.part_o[at_part * D + d] = O;
@@ -500,7 +507,7 @@ q8_decode_kernel(const Q8DecodeParams p) {
                     L = fmaf(load_from_cta(at + (D + 1) * 4, k), by, L);
                     O = fmaf(load_from_cta(at + d * 4, k), by, O);
                 }
-            finish(n, d, O, L);
+            finish(n, d, M, O, L);
         }
         cluster_sync();  // no CTA ends while others read its shared memory
     }

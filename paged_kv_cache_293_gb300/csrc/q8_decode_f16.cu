@@ -21,7 +21,6 @@ __global__ void __launch_bounds__(Q8_MERGE_WARPS * 32) q8_merge_kernel(const Q8D
     const long long row = blockIdx.x;
     const int warps = blockDim.x / 32, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int s = (int)(row / ((long long)p.num_q_heads * p.num_queries));
-    const int j = (int)(row / p.num_q_heads % p.num_queries);
     const long long table = (long long)p.max_blocks_per_seq * p.block_size;
     const int cap = (int)(table < p.max_context_len ? table : p.max_context_len);
     const int ctx = min(max(p.context_lens[s], 0), cap);
@@ -47,14 +46,14 @@ __global__ void __launch_bounds__(Q8_MERGE_WARPS * 32) q8_merge_kernel(const Q8D
     for (int i = 0; i < V; ++i) red[warp][lane * V + i] = acc[i];
     if (lane == 0) red[warp][D] = L;
     __syncthreads();
-    const bool nothing = ctx - p.num_queries + 1 + j <= 0;
     for (int d = threadIdx.x; d < D; d += blockDim.x) {
         float num = 0.f, den = 0.f;
         for (int w = 0; w < warps; ++w) {
             num += red[w][d];
             den += red[w][D];
         }
-        store_out(p.out, p.out_dtype, (size_t)row * D + d, nothing ? 0.f : num / den);
+        // (-inf: a row that sees nothing)
+        store_out(p.out, p.out_dtype, (size_t)row * D + d, M == -INFINITY ? 0.f : num / den);
     }
 }
 
