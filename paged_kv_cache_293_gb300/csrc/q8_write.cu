@@ -412,9 +412,11 @@ __device__ __forceinline__ void store_window(const Window& w, uint64_t (&f)[Rows
     if (real && leads && !ok) set_error(err, PKV_DEVERR_SLOT);
     const float old = __uint_as_float(had), need = q8_scale_for(top);
     const float s = w.lead_row > 0 ? fmaxf(old, need) : need;  // (a scale that is NaN counts as none)
-    // (of a power of two exactly, and without a division)
+    // (of a power of two exactly, and without a division: but for 2^127, whose reciprocal has no place among the
+    // normal numbers)
     const int bits = __float_as_int(s);
-    const float inv = (bits & 0x7fffff) == 0 ? __int_as_float(0x7f000000 - bits) : 1.f / s;
+    const bool simple = (bits & 0x7fffff) == 0 && bits != 0x7f000000;
+    const float inv = simple ? __int_as_float(0x7f000000 - bits) : 1.f / s;
     unsigned grown = __ballot_sync(FULL_MASK, ok && leads && w.lead_row > 0 && s > old);
     for (; grown != 0; grown &= grown - 1) {
         const int j = __ffs(grown) - 1, row0 = __shfl_sync(FULL_MASK, w.row, j);
