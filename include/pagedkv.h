@@ -555,6 +555,10 @@ pkv_status pkv_paged_attention_chunk(const pkv_pool* pool, const void* q, int32_
  * value times its page's scale.  k and v 16-byte aligned, the scales 4-byte aligned;
  * block_size in {16, 32}, head_dim in {64, 128}.  Half the bytes of a 16-bit pool, and
  * 8 / (block_size * head_dim) more for the scales (0.4 % with 16 and 128).
+ *
+ * pkv_copy_blocks and the other calls that take a pkv_pool do not take these pools.  A block to be
+ * copied (one that pkv_build_batch answers status 3 for, say) is four stretches of memory, its
+ * num_kv_heads pages of keys and of values and their scales, which the caller copies.
  */
 typedef struct pkv_q8_pool {
     void* k;
@@ -582,12 +586,14 @@ typedef struct pkv_q8_pool {
  *          page's other rows are rounded again to the new scale.  (Old and new scales that
  *          are powers of two, as this call makes them, leave a row's values as they were, but
  *          for those that fall below 2^-6 of the new scale.)
- *   value  x / scale to the nearest e4m3 value, even at ties; NaN where x is not finite
- * Arguments and errors as pkv_qk_norm_rope_write's; the pool's four arrays share no byte.  A run whose block the token before
- * it (of the 32 rows before) has too, but not as the slot before (a slot twice, or slots in
- * falling order), is not written and sets PKV_DEVERR_SLOT.  A block that comes at two separate places of a call has
- * no defined contents; where the two are seen to meet, PKV_DEVERR_SLOT is set and one of them is
- * left out.
+ *   value  x / scale to the nearest e4m3 value, even at ties; NaN where x is not finite.  (Where
+ *          the page keeps a scale that is no power of two, of the quotient that 32 bits have,
+ *          2^-21 of it off at most.)
+ * Arguments and errors as pkv_qk_norm_rope_write's; the pool's four arrays share no byte.  A run
+ * whose block the token before it (of the 32 rows before) has too, but not as the slot before (a
+ * slot twice, or slots in falling order), is not written and sets PKV_DEVERR_SLOT.  A block that
+ * comes at two separate places of a call has no defined contents; where the two are seen to meet,
+ * PKV_DEVERR_SLOT is set and one of them is left out.
  */
 pkv_status pkv_qk_norm_rope_write_q8(const pkv_q8_pool* pool, int32_t dtype, const void* q,
                                      int64_t q_stride, const void* k, int64_t k_stride,
