@@ -617,7 +617,9 @@ pkv_status pkv_qk_norm_rope_write_q8(const pkv_q8_pool* pool, int32_t dtype, con
  *   partition_size  tokens a piece of a context, a multiple of block_size; 0: chosen for
  *                 the batch
  *   workspace     pkv_decode_q8_workspace_bytes(...) bytes (0: none needed), 16-byte aligned;
- *                 calls that may run at the same time need one each
+ *                 calls that may run at the same time need one each.  With the same
+ *                 partition_size, what is asked for grows with the batch, the queries and the
+ *                 context: a workspace for the largest call serves the smaller ones
  * Any group size num_q_heads / num_kv_heads.  num_seqs and the number of pieces of a context
  * up to 65535 each, max_context_len up to 2^30.  The queries enter their products exactly (in
  * bf16, but for elements below 2^-30 of their row's largest), the probabilities rounded to fp16

@@ -1215,6 +1215,13 @@ struct Q8Layout {
     size_t l_off, o_off, bytes;
 };
 
+// Maxima, sums and unscaled outputs of that many pieces' rows.
+void q8_place(Q8Layout& w, size_t results, int32_t D) {
+    w.l_off = (results * 4 + 15) & ~size_t(15);
+    w.o_off = 2 * w.l_off;
+    w.bytes = w.o_off + results * D * 4;
+}
+
 // How a decode call is cut.  A CTA has 8 columns (query, head) of a kv head, or 16 of a large batch: these
 // share what is read and converted, but three fit an SM where four of the others do (32 heads of 128 on 4,
 // 64 requests of ~4000 tokens: 62.8 us with 16, 71.7 with 8; of ~500: 32.7 and 25.3).  Where that leaves
@@ -1240,11 +1247,23 @@ Q8Layout q8_layout(const pkv_q8_pool* pool, int32_t S, int32_t NQ, int32_t Hq, i
     w.parts = max_ctx > 0 ? ceil_div(max_ctx, w.P) : 1;
     w.clustered = w.parts > 1 && w.parts <= pkv::Q8_CLUSTER;
     if (w.parts <= 1 || w.clustered) return w;
-    const size_t results = (size_t)S * NQ * Hq * w.parts;
-    w.l_off = (results * 4 + 15) & ~size_t(15);
-    w.o_off = 2 * w.l_off;
-    w.bytes = w.o_off + results * pool->head_dim * 4;
+    q8_place(w, (size_t)S * NQ * Hq * w.parts, pool->head_dim);
     return w;
+}
+
+// What a workspace has to hold for all calls up to this size whose pieces are chosen: contexts of more than
+// 4096 tokens are cut into no more pieces than fill the SMs, 4 CTAs of at most 16 columns each (of which every
+// one of their results is a row), or into pieces of 1024 tokens; and none is shorter than 128.
+size_t q8_workspace(const pkv_q8_pool* pool, int32_t S, int32_t NQ, int32_t Hq, int32_t max_ctx) {
+    if (max_ctx <= 4096) return 0;
+    const size_t rows = (size_t)S * NQ * Hq;
+    const int64_t cols = (int64_t)NQ * (Hq / pool->num_kv_heads);
+    const size_t filling = (size_t)(4 * (int64_t)sm_count() * std::min<int64_t>(cols, 16));
+    size_t results = std::min(rows * ceil_div(max_ctx, 128), filling);
+    if (ceil_div(max_ctx, 1024) > pkv::Q8_CLUSTER) results = std::max(results, rows * ceil_div(max_ctx, 1024));
+    Q8Layout w{};
+    q8_place(w, results, pool->head_dim);
+    return w.bytes;
 }
 
 }  // namespace
@@ -1256,7 +1275,9 @@ size_t pkv_decode_q8_workspace_bytes(const pkv_q8_pool* pool, int32_t num_seqs, 
         num_queries <= 0 || num_q_heads <= 0 || max_context_len < 0 || partition_size < 0 ||
         num_q_heads % pool->num_kv_heads != 0)
         return 0;
-    return q8_layout(pool, num_seqs, num_queries, num_q_heads, max_context_len, partition_size).bytes;
+    return partition_size > 0
+               ? q8_layout(pool, num_seqs, num_queries, num_q_heads, max_context_len, partition_size).bytes
+               : q8_workspace(pool, num_seqs, num_queries, num_q_heads, max_context_len);
 }
 
 pkv_status pkv_paged_attention_decode_q8(const pkv_q8_pool* pool, int32_t dtype, const void* q,
