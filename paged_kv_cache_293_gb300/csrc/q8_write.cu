@@ -14,7 +14,7 @@
 // lane at most: it takes each run's largest |x|, then rounds.  Lane j looks after row j: its slot, its
 // run and that run's scale.
 // Measured: one token of 32 + 2 * 8 heads of 128 4.9 us (two dependent round trips to memory, the slots and
-// then rows, scales and table), 128 of 40 + 2 * 40 9.9; 16384 of 32 + 2 * 8, bf16, 76 us (378 MB, 5.0 TB/s);
+// then rows, scales and table), 128 of 40 + 2 * 40 7.7; 16384 of 32 + 2 * 8, bf16, 76 us (378 MB, 5.0 TB/s);
 // q alone, through rope_write.cu, takes 50 of them, and the keys and values 28: about 6000 cycles a window
 // of 16 tokens and CTA, bound by instructions (46 % of the issue slots) at 16 warps per SM, whose numbers
 // take all registers.
@@ -32,14 +32,20 @@ namespace {
 
 constexpr int Q8_Q_ROWS = 2;      // rows of q per group of lanes, in flight together
 constexpr int Q8_KV_WARPS = 8;
-// From this many tokens on q goes through rope_write.cu's kernels and k and v are streamed, a launch
-// more, which begins where the first leaves room (16384 tokens 76 us, 79.5 one after the other; 2048 of
-// 32 + 2 * 8 heads 17.1 / 18.8); measured, one launch against two one after the other, bf16: 32 + 2 * 8 heads of 128, 1024 tokens 12.3 / 13.0 us, 2048
-// 20.4 / 18.6; 40 + 2 * 40, 1024 23.2 / 24.6, 1536 33.6 / 28.7; 16 + 2 * 4 of 64, 1024 10.8 / 10.9, 2048
-// 15.0 / 10.9.
+// From this many tokens on q goes through rope_write.cu's kernels and k and v are streamed by a second launch.
+// One launch against these two, one after the other, bf16:
+//   32 + 2 * 8 heads of 128    1024 tokens 12.3 / 13.0 us    2048 tokens 20.4 / 18.6
+//   40 + 2 * 40 heads of 128   1024 tokens 23.2 / 24.6       1536 tokens 33.6 / 28.7
+//   16 + 2 * 4 heads of 64     1024 tokens 10.8 / 10.9       2048 tokens 15.0 / 10.9
+// The second launch begins where the first leaves room: 2048 tokens of 32 + 2 * 8 heads 17.1 us (18.8 one after
+// the other), 16384 76 (79.5); 2048 decoding requests of 40 + 2 * 40 heads 43.5 (42.4).
 constexpr int Q8_MANY_TOKENS = 1025;
-// Rows whose runs a CTA looks for: few while that does not make more CTAs than fit the SMs.
-constexpr int Q8_CTAS = 456;
+// Rows whose runs a CTA looks for: few while that makes no more CTAs of keys and values than fit the SMs at a
+// time, two each.  Decoding requests, 4 rows / 16 rows:
+//   32 + 2 * 8 heads of 128    16 requests 5.3 / 6.2 us    256 requests 7.6 / 6.9    384 8.5 / 9.6 (4 rows taken)
+//   40 + 2 * 40 heads of 128   64 requests 6.7 / 6.9       128 requests 9.9 / 8.0    512 28.0 / 15.7 (16 from 122 on)
+// (Counted with q's CTAs, it would gain 0.7 us at the 256 and lose 1.1 at the 384.)
+constexpr int Q8_CTAS_PER_SM = 2;
 constexpr int Q8_FEW_ROWS = 4, Q8_GROUP_ROWS = 16;
 // What a scale reads as while the run that changes it is at work: a NaN that nothing else makes.
 constexpr uint32_t Q8_LOCKED = 0xffc5a5c5u;
@@ -51,7 +57,8 @@ struct LanePart {
 };
 
 __device__ __forceinline__ void load_angles(const float* row, int R, int l, float (&c)[4], float (&s)[4]) {
-    const float4 x = *reinterpret_cast<const float4*>(row + l * 4), y = *reinterpret_cast<const float4*>(row + R / 2 + l * 4);
+    const float4 x = *reinterpret_cast<const float4*>(row + l * 4);
+    const float4 y = *reinterpret_cast<const float4*>(row + R / 2 + l * 4);
     c[0] = x.x; c[1] = x.y; c[2] = x.z; c[3] = x.w;
     s[0] = y.x; s[1] = y.y; s[2] = y.z; s[3] = y.w;
 }
@@ -322,7 +329,8 @@ __device__ __forceinline__ float largest(const uint64_t (&f)[4], float m = 0.f) 
 }
 
 // A lane's eight numbers of a row, times x, into its places of the row.
-__device__ __forceinline__ void store_row(uint8_t* out, int lo_at, int hi_at, const uint64_t (&f)[4], float x, bool real) {
+__device__ __forceinline__ void store_row(uint8_t* out, int lo_at, int hi_at, const uint64_t (&f)[4], float x,
+                                          bool real) {
     const uint64_t x2 = pack2(x, x);
     float v[8];
 #pragma unroll
@@ -425,7 +433,8 @@ __device__ __forceinline__ void store_window(const Window& w, uint64_t (&f)[Rows
         uint8_t* const codes = pool + (size_t)__shfl_sync(FULL_MASK, page, j) * (B * D);
         for (int r = part * GPW + sub; r < B; r += W * GPW) {
             const int k = j + r - row0;
-            if (k < j || k > 31 || !((rows_j >> k) & 1)) round_again(reinterpret_cast<uint2*>(codes + r * D) + l, ratio);
+            if (k < j || k > 31 || !((rows_j >> k) & 1))
+                round_again(reinterpret_cast<uint2*>(codes + r * D) + l, ratio);
         }
     }
     const unsigned stored = __ballot_sync(FULL_MASK, ok);
@@ -444,7 +453,8 @@ __device__ __forceinline__ void store_window(const Window& w, uint64_t (&f)[Rows
                 float v[8];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) unpack2(mul2(f[i][k], x2), v[2 * k], v[2 * k + 1]);
-                const uint32_t lo = e4m3x4_of_floats(v[0], v[1], v[2], v[3]), hi = e4m3x4_of_floats(v[4], v[5], v[6], v[7]);
+                const uint32_t lo = e4m3x4_of_floats(v[0], v[1], v[2], v[3]);
+                const uint32_t hi = e4m3x4_of_floats(v[4], v[5], v[6], v[7]);
                 unsigned char* const row = staged + (i * GPW + sub) * D;
                 *reinterpret_cast<uint32_t*>(row + (swap ? at.hi : at.lo)) = swap ? hi : lo;
                 *reinterpret_cast<uint32_t*>(row + (swap ? at.lo : at.hi)) = swap ? lo : hi;
@@ -501,7 +511,7 @@ __device__ __forceinline__ void load_weights(const void* w, const LanePart& at, 
 // token each; of the others, every `heads` have the runs that begin in `rows` rows, and a warp one page's
 // rows, all in flight.  The warps share the window's rows of the rotation table in shared memory.
 template <typename T, int D, int B, bool INTERLEAVED>
-__global__ void __launch_bounds__(Q8_KV_WARPS * 32, 2)
+__global__ void __launch_bounds__(Q8_KV_WARPS * 32, Q8_CTAS_PER_SM)
 q8_write_kernel(const RopeParams p, float* k_scale, float* v_scale, int q_ctas, int heads, int rows) {
     using L = Rows<D, B>;
     constexpr int IT = L::IT, GPW = L::GPW, W = L::W;
@@ -537,7 +547,8 @@ q8_write_kernel(const RopeParams p, float* k_scale, float* v_scale, int q_ctas, 
             had = atomicExch(reinterpret_cast<unsigned int*>(scales + page), Q8_LOCKED);
         // this lane's chunks of rows (part * IT + i) * GPW + sub
         uint2 a[IT], b[IT];
-        const T* const base = static_cast<const T*>(is_k ? p.k : p.v) + (t_now + part * IT * GPW + sub) * stride + head * D;
+        const T* const base =
+            static_cast<const T*>(is_k ? p.k : p.v) + (t_now + part * IT * GPW + sub) * stride + head * D;
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
             a[i] = b[i] = make_uint2(0u, 0u);
@@ -667,13 +678,15 @@ q8_stream_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
         }
         for (int r = warp - heads * W; r < B; r += heads * W)
             if (((run >> r) & 1) && 4 * lane < R)
-                cp_async16(stage + 2 * S::rows(heads) + (r * D + 4 * lane) * 4, p.cos_sin + (size_t)x.pos[r] * R + 4 * lane);
+                cp_async16(stage + 2 * S::rows(heads) + (r * D + 4 * lane) * 4,
+                           p.cos_sin + (size_t)x.pos[r] * R + 4 * lane);
     };
     // the scale of each run's page, and no other run at that page from here on
     auto lock = [&](int i) -> uint32_t {
         const Found& x = found[i % Q8_FOUND];
         if (!real || part != 0 || !((x.run & x.leaders) >> lane & 1)) return 0u;
-        return atomicExch(reinterpret_cast<unsigned int*>(scales + ((unsigned)x.blk[lane] * Hkv + head0 + h)), Q8_LOCKED);
+        float* const at = scales + ((unsigned)x.blk[lane] * Hkv + head0 + h);
+        return atomicExch(reinterpret_cast<unsigned int*>(at), Q8_LOCKED);
     };
     const bool finds = warp == warps - 1;
     if (finds) find(0);
@@ -694,7 +707,8 @@ q8_stream_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
         if (finds) raw = load_row(p, t + lane);
         Window w;
         w.run = x.run; w.leaders = x.leaders;
-        w.blk = x.blk[lane]; w.row = x.row[lane]; w.lead = x.lead[lane]; w.last = x.last[lane]; w.lead_row = x.lead_row[lane];
+        w.blk = x.blk[lane]; w.row = x.row[lane]; w.lead_row = x.lead_row[lane];
+        w.lead = x.lead[lane]; w.last = x.last[lane];
         const unsigned page = (unsigned)max(w.blk, 0) * Hkv + head0 + (real ? h : 0);
         if (!mbar_wait_short(bar0 + 8 * (i & 1), (i >> 1) & 1)) set_error(p.err, PKV_DEVERR_TIMEOUT);
         __syncwarp();
@@ -711,7 +725,8 @@ q8_stream_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
         make_rows<T, D, B, INTERLEAVED, false>(
             is_k, in, reinterpret_cast<const float*>(stage + 2 * S::rows(heads)) + (part * IT * GPW + sub) * D, R,
             p.k_weight != nullptr, wa, wb, at, p.eps, f, by);
-        store_window<D, B>(w, f, by, part, at, real, pool, scales, page, had, tops[unit], hads[unit], 1 + unit, p.err, out);
+        store_window<D, B>(w, f, by, part, at, real, pool, scales, page, had, tops[unit], hads[unit], 1 + unit, p.err,
+                           out);
         had = lock(i + 1);  // (not before: the fence in there would wait for it)
         if (finds) find(i + 2);
         cp_async_wait_all();  // this warp's rows of the next window's table
@@ -741,9 +756,14 @@ bool encode_rows_map(CUtensorMap* map, const void* base, long long stride, const
 template <typename T, int D, int B, bool INTERLEAVED>
 cudaError_t launch_q8_write_tdbi(const RopeParams& p, float* k_scale, float* v_scale, cudaStream_t stream) {
     constexpr int W = Rows<D, B>::W, UNITS = Q8_KV_WARPS / W;
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
     if (p.num_tokens < Q8_MANY_TOKENS) {
         const long long heads = (2ll * p.num_kv_heads + UNITS - 1) / UNITS;
-        const int rows = (p.num_tokens + Q8_FEW_ROWS - 1) / Q8_FEW_ROWS * heads <= Q8_CTAS ? Q8_FEW_ROWS : Q8_GROUP_ROWS;
+        const long long few = (p.num_tokens + Q8_FEW_ROWS - 1) / Q8_FEW_ROWS * heads;
+        const int rows = few <= (long long)Q8_CTAS_PER_SM * sms ? Q8_FEW_ROWS : Q8_GROUP_ROWS;
         const long long ctas = p.num_tokens + ((long long)p.num_tokens + rows - 1) / rows * heads;
         if (ctas > 0x7fffffff) return cudaErrorInvalidConfiguration;
         q8_write_kernel<T, D, B, INTERLEAVED>
@@ -754,12 +774,8 @@ cudaError_t launch_q8_write_tdbi(const RopeParams& p, float* k_scale, float* v_s
     constexpr int MOST = Q8_STREAM_WARPS / (2 * W);
     const int slices = (p.num_kv_heads + MOST - 1) / MOST, heads = (p.num_kv_heads + slices - 1) / slices;
     const int warps = 2 * heads * W;
-    int dev = 0, sms = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     auto kernel = q8_stream_kernel<T, D, B, INTERLEAVED>;
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, StreamSmem<D, B>::bytes(MOST));
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, StreamSmem<D, B>::bytes(MOST));
     if (e != cudaSuccess) return e;
     const long long want = (long long)sms * (warps <= Q8_STREAM_WARPS / 2 ? 2 : 1);
     long long rows = ((long long)p.num_tokens * slices + want - 1) / want;
@@ -767,7 +783,8 @@ cudaError_t launch_q8_write_tdbi(const RopeParams& p, float* k_scale, float* v_s
     const long long ctas = (p.num_tokens + rows - 1) / rows * slices;
     if (ctas > 0x7fffffff) return cudaErrorInvalidConfiguration;
     CUtensorMap tk, tv;
-    if (!encode_rows_map<T>(&tk, p.k, p.k_stride, p, heads, B) || !encode_rows_map<T>(&tv, p.v, p.v_stride, p, heads, B))
+    if (!encode_rows_map<T>(&tk, p.k, p.k_stride, p, heads, B) ||
+        !encode_rows_map<T>(&tv, p.v, p.v_stride, p, heads, B))
         return cudaErrorNotSupported;
     RopeParams q = p;  // the q rows alone
     q.num_kv_heads = 0;
