@@ -654,6 +654,8 @@ pkv_status pkv_paged_attention_decode_q8(const pkv_q8_pool* pool, int32_t dtype,
  * weights are rounded to fp16 (2^-11 of their value, and 2^-32 of the row's largest, whatever the
  * scales; with a remainder of another 11 bits when out is fp32).  Scales are finite; those of a
  * context's values, where they are not pages of zeros, lie within a factor of 2^60 of one another.
+ * Cached rows below a context are finite: pkv_qk_norm_rope_write_q8 stores NaN for what is not, and a
+ * NaN value may make its element NaN in earlier queries of the request, too.
  * The workspace is pkv_chunk_q8_workspace_bytes(...) bytes.
  */
 size_t pkv_chunk_q8_workspace_bytes(const pkv_q8_pool* pool, int32_t num_tokens, int32_t num_seqs,

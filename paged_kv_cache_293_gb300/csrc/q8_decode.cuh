@@ -23,7 +23,7 @@
 // than 15 in base 2 (it is set 7 below the maximum), so no lane asks the others for theirs but then.
 // P enters its product in fp16 (weights from 2^-21 of the largest on with 11 bits, none off by more
 // than 2^-32 of it), and with a 32-bit output in two parts.
-// Measured: 128 requests of ~600 tokens, 40 heads, fp16: 125 us, 6.1 TB/s (233 from 16 bits); 8 contexts of
+// Measured: 128 requests of ~600 tokens, 40 heads, fp16: 123 us, 6.2 TB/s (233 from 16 bits); 8 contexts of
 // ~80000 tokens, 32 / 8 heads, bf16: 250 us with the merge, 6.4 TB/s (457).  What got it there, for the first:
 // operands loaded straight to registers 162 us, too few bytes on their way at 12 warps of 158 registers;
 // this ring with three stages and four CTAs per SM 122 us (two stages 128, three CTAs with four 127, eight
