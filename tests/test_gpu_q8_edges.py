@@ -81,3 +81,12 @@ def test_decode_in_pieces_beside_rows_that_nobody_sees(P, part):
         d.kc[b], d.vc[b], d.ks[b], d.vs[b] = NAN[0], NAN[0], float("nan"), float("nan")
     assert torch.equal(d.run(P, torch.float32, part), clean)
     assert P.pkv_get_device_error() == 0
+
+
+def test_decode_of_scales_below_zero(P):
+    d = Decode([70, 300, 16], 2, 8, 2, 128, 16, torch.bfloat16, seed=12)
+    d.ks[::3] *= -1.0
+    d.vs[1::3] *= -1.0
+    for out_dtype in (torch.bfloat16, torch.float32):
+        d.check(d.run(P, out_dtype))
+    assert P.pkv_get_device_error() == 0

@@ -121,3 +121,37 @@ def test_chunk_of_long_pieces_of_two_sizes(P, new, down):
         tol = tol + n * 2.0 ** -32 * _largest(c, v, e)
         off = (out[rows.to(DEV)].cpu().double() - ref)[..., e].abs()
         assert bool((off <= tol).all()), float((off / tol).max())
+
+
+@pytest.mark.parametrize("dt", [torch.float16, torch.bfloat16])
+def test_chunk_of_scales_of_zero_and_below(P, dt):
+    # pages of scale zero alone in a step and beside others, and scales that turn the sign
+    c = Chunk([(0, 300), (700, 3), (130, 40), (513, 1)], 8, 2, 128, 16, dt, seed=9)
+    for s, n in enumerate(c.lens):
+        for b in range(R.blocks(n, c.B)):
+            blk = int(c.tables[s, b])
+            if b // 8 % 3 == 1 or b % 5 == 2:
+                c.vs[blk] = 0.0
+            if b % 7 == 3:
+                c.ks[blk] = 0.0
+            if b % 4 == 1:
+                c.vs[blk, 0] *= -1.0
+                c.ks[blk, 1] *= -1.0
+    for out_dtype in (dt, torch.float32):
+        c.check(c.run(P, out_dtype))
+    assert P.pkv_get_device_error() == 0
+
+
+def test_chunk_of_values_of_many_sizes_gives_the_same_bits(P):
+    # whichever CTA takes a piece, and whatever it had before: also with scales that are no powers of two
+    spans = [(i * 97 % 900, 1 + i % 3) for i in range(300)] + [(i * 331 % 2000, 20 + i * 7 % 200) for i in range(12)]
+    for dt, odd in ((torch.float16, False), (torch.bfloat16, True)):
+        c = Chunk(spans, 8, 2, 64, 16, dt, seed=11)
+        power = torch.randint(-30, 20, (c.vs.shape[0], 1), generator=c.g)
+        c.vs *= torch.pow(2.0, power.float())
+        if odd:
+            c.vs *= 0.5 + torch.rand(c.vs.shape, generator=c.g)
+        want = c.run(P)
+        for _ in range(5):
+            assert torch.equal(c.run(P), want)
+    assert P.pkv_get_device_error() == 0
